@@ -1,0 +1,44 @@
+// Private declarations of the operators beside the swap-in path
+// (hs_latent_attend, hs_latent_prefill, hs_rms_norm).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "hs.h"
+
+// hs_ops.cpp has checked the arguments; these launch.
+cudaError_t hs_launch_attend(const hs_attend_t& a, cudaStream_t s);
+cudaError_t hs_launch_prefill(const hs_prefill_t& a, cudaStream_t s);
+cudaError_t hs_launch_norm(const hs_norm_t& a, cudaStream_t s);
+size_t hs_attend_workspace_bytes(int batch, int positions, int heads, int64_t rows);
+size_t hs_prefill_workspace_bytes(int64_t k_tokens, int heads);
+
+constexpr float HS_E4M3_MAX = 448.0f;
+
+template <typename T> struct HsType;
+template <> struct HsType<__nv_bfloat16> {
+    using Pair = __nv_bfloat162;
+    static __device__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+    static __device__ __nv_bfloat16 from_float(float v) { return __float2bfloat16_rn(v); }
+};
+template <> struct HsType<__half> {
+    using Pair = __half2;
+    static __device__ float to_float(__half v) { return __half2float(v); }
+    static __device__ __half from_float(float v) { return __float2half_rn(v); }
+};
+template <> struct HsType<float> {
+    static __device__ float to_float(float v) { return v; }
+    static __device__ float from_float(float v) { return v; }
+};
+
+__device__ inline float hs_e4m3_to_float(uint8_t v)
+{
+    __nv_fp8_e4m3 x;
+    x.__x = v;
+    return static_cast<float>(x);
+}

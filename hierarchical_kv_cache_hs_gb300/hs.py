@@ -60,6 +60,22 @@ HS_MAX_BATCH = 4096
 HS_MAX_ROW_BYTES = 65536
 HS_MAX_LAYERS = 16
 
+HS_LATENT_DIM = 512
+HS_ROPE_DIM = 64
+HS_ROW_DIM = 576
+HS_HEAD_DIM = 128
+HS_ROW8_SCALE = 576
+HS_ROW8_BYTES = 592
+HS_TYPE_BF16 = 0
+HS_TYPE_FP16 = 1
+HS_TYPE_FP32 = 2
+HS_ROWS_16BIT = 0
+HS_ROWS_E4M3 = 1
+HS_MAX_HEADS = 1024
+HS_MAX_POSITIONS = 1024
+HS_MAX_TOKENS = 1 << 24
+HS_MAX_NORM_DIM = 16384
+
 
 class HsError(RuntimeError):
     def __init__(self, code: int, where: str):
@@ -76,6 +92,79 @@ class hs_stats_t(ctypes.Structure):
         ("bytes_copied", ctypes.c_int64),
         ("err_bits", ctypes.c_int32),
         ("reserved", ctypes.c_int32),
+    ]
+
+
+class hs_attend_t(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32),
+        ("row_format", ctypes.c_int32),
+        ("batch", ctypes.c_int32),
+        ("positions", ctypes.c_int32),
+        ("heads", ctypes.c_int32),
+        ("entries", ctypes.c_int32),
+        ("n_rows", ctypes.c_int64),
+        ("q", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64 * 3),
+        ("rows", ctypes.c_void_p),
+        ("row_stride", ctypes.c_int64),
+        ("request_stride", ctypes.c_int64),
+        ("slots", ctypes.c_void_p),
+        ("slots_stride", ctypes.c_int64 * 2),
+        ("lengths", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("out_stride", ctypes.c_int64 * 3),
+        ("lse", ctypes.c_void_p),
+        ("scale", ctypes.c_float),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class hs_prefill_t(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32),
+        ("row_format", ctypes.c_int32),
+        ("batch", ctypes.c_int32),
+        ("heads", ctypes.c_int32),
+        ("q_tokens", ctypes.c_int64),
+        ("k_tokens", ctypes.c_int64),
+        ("q", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64 * 2),
+        ("rows", ctypes.c_void_p),
+        ("row_stride", ctypes.c_int64),
+        ("w_uk", ctypes.c_void_p),
+        ("w_uv", ctypes.c_void_p),
+        ("q_start", ctypes.c_void_p),
+        ("k_start", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("out_stride", ctypes.c_int64 * 2),
+        ("lse", ctypes.c_void_p),
+        ("scale", ctypes.c_float),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class hs_norm_t(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32),
+        ("dim", ctypes.c_int32),
+        ("carry", ctypes.c_int32),
+        ("group", ctypes.c_int32),
+        ("tokens", ctypes.c_int64),
+        ("x", ctypes.c_void_p),
+        ("x_stride", ctypes.c_int64),
+        ("residual", ctypes.c_void_p),
+        ("residual_stride", ctypes.c_int64),
+        ("residual_out", ctypes.c_void_p),
+        ("residual_out_stride", ctypes.c_int64),
+        ("weight", ctypes.c_void_p),
+        ("eps", ctypes.c_float),
+        ("out", ctypes.c_void_p),
+        ("out_stride", ctypes.c_int64),
+        ("scales", ctypes.c_void_p),
+        ("scales_stride", ctypes.c_int64),
     ]
 
 
@@ -122,6 +211,11 @@ def _load():
         "hs_set_eviction_seed": ([P, ctypes.c_uint64], I),
         "hs_set_tail_mode": ([P, I], I),
         "hs_resolve_noalloc": ([I, I, I, I, I, I, P, I, P, P, P, P, P, P, P, P, P], I),
+        "hs_latent_attend_workspace": ([I, I, I, ctypes.c_int64], Z),
+        "hs_latent_attend": ([P, P], I),
+        "hs_latent_prefill_workspace": ([ctypes.c_int64, I], Z),
+        "hs_latent_prefill": ([P, P], I),
+        "hs_rms_norm": ([P, P], I),
         "hs_error_string": ([I], ctypes.c_char_p),
     }
     for name, (args, res) in sig.items():
@@ -453,6 +547,212 @@ def hs_profile_events(h: int, before_copy=None, after_copy=None) -> None:
     _check(lib.hs_profile_events(h, ev(before_copy), ev(after_copy)), "hs_profile_events")
 
 
+# ---- Operators beside the swap-in path -------------------------------------
+# These take torch tensors and check them (type, shape, layout, device) before
+# the call; a mismatch raises ValueError.  What the library itself refuses
+# (alignments, limits, a workspace that is too small) raises HsError.
+
+def _type_of(x, name, fp32=False):
+    import torch
+    if x.dtype == torch.bfloat16:
+        return HS_TYPE_BF16
+    if x.dtype == torch.float16:
+        return HS_TYPE_FP16
+    if fp32 and x.dtype == torch.float32:
+        return HS_TYPE_FP32
+    raise ValueError("%s: type %s is not taken" % (name, x.dtype))
+
+
+def _want(x, name, shape, dtype, device):
+    """One tensor of a call: its shape, type, contiguous last axis and device."""
+    if tuple(x.shape) != shape:
+        raise ValueError("%s must have shape %s, has %s" % (name, shape, tuple(x.shape)))
+    if x.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, x.dtype))
+    if shape and shape[-1] > 1 and x.stride(-1) != 1:
+        raise ValueError("the last axis of %s must be contiguous" % name)
+    if x.device != device:
+        raise ValueError("%s must be on %s, is on %s" % (name, device, x.device))
+
+
+def _on_current_device(device):
+    import torch
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError("tensors must be on the current CUDA device, are on %s" % device)
+
+
+def _rows_of(rows, row_format, q, lead):
+    """(address, rows a request, row stride, request stride) in bytes of a row array
+    [*lead, n, channels or bytes], or of a handle's device buffer."""
+    import torch
+    width = {HS_ROWS_16BIT: 2 * HS_ROW_DIM, HS_ROWS_E4M3: HS_ROW8_BYTES}.get(row_format)
+    if width is None:
+        raise ValueError("unknown row_format %r" % (row_format,))
+    if isinstance(rows, Handle):
+        if (rows.B,) != lead or rows.R < width:
+            raise ValueError("the handle has %d requests of %d-byte rows" % (rows.B, rows.R))
+        n = rows.S + rows.T
+        return hs_device_buffer(rows.h), n, rows.R, n * rows.R
+    if rows.dim() != len(lead) + 2 or tuple(rows.shape[:-2]) != lead:
+        raise ValueError("rows must have shape %s + (rows, channels), has %s" % (lead, tuple(rows.shape)))
+    if rows.dtype == torch.uint8:
+        wide = rows.shape[-1] >= width
+    else:
+        wide = row_format == HS_ROWS_16BIT and rows.dtype == q.dtype and rows.shape[-1] == HS_ROW_DIM
+    if not wide:
+        raise ValueError("rows: %s of %s are not rows of this format" % (rows.dtype, tuple(rows.shape)))
+    if rows.stride(-1) != 1 or rows.device != q.device:
+        raise ValueError("rows must be contiguous in the last axis and on %s" % q.device)
+    e = rows.element_size()
+    return (rows.data_ptr(), rows.shape[-2], rows.stride(-2) * e,
+            rows.stride(0) * e if lead else 0)
+
+
+def _workspace_of(workspace, device):
+    if workspace is None:
+        return None, 0
+    if not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError("workspace must be contiguous and on %s" % device)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def hs_latent_attend_workspace(batch: int, positions: int, heads: int, rows: int) -> int:
+    """Bytes of workspace of hs_latent_attend; `rows`: entries of a slot list, or rows a request."""
+    n = int(lib.hs_latent_attend_workspace(int(batch), int(positions), int(heads), int(rows)))
+    if n == 0:
+        raise HsError(HS_ERR_ARG, "hs_latent_attend_workspace")
+    return n
+
+
+def hs_latent_attend(q, rows, out, scale: float, slots=None, lengths=None,
+                     row_format: int = HS_ROWS_16BIT, lse=None, workspace=None,
+                     stream=None) -> None:
+    """Absorbed latent attention of q [B][P][H][576] into out [B][P][H][512].
+
+    rows: a tensor [B][N][576] of q's type, a uint8 tensor [B][N][bytes] of rows in
+    `row_format`, or a Handle (its device buffer).  Give either slots (int32
+    [B][P][K], from hs_resolve; entries outside [0, N) are absent) or lengths
+    (int32 [B], the P positions being the last).  lse: fp32 [B][P][H] or None.
+    """
+    import torch
+    kind = _type_of(q, "q")
+    if q.dim() != 4:
+        raise ValueError("q must have 4 axes, has %d" % q.dim())
+    B, P, H, _ = q.shape
+    device = q.device
+    _want(q, "q", (B, P, H, HS_ROW_DIM), q.dtype, device)
+    _want(out, "out", (B, P, H, HS_LATENT_DIM), q.dtype, device)
+    address, n_rows, row_stride, request_stride = _rows_of(rows, row_format, q, (B,))
+    if (slots is None) == (lengths is None):
+        raise ValueError("give slots or lengths, and not both")
+    entries, slots_stride = 0, (0, 0, 1)
+    if slots is not None:
+        entries = slots.shape[-1] if slots.dim() else 0
+        _want(slots, "slots", (B, P, entries), torch.int32, device)
+        slots_stride = slots.stride()
+    else:
+        _want(lengths, "lengths", (B,), torch.int32, device)
+    if lse is not None:
+        _want(lse, "lse", (B, P, H), torch.float32, device)
+        if not lse.is_contiguous():
+            raise ValueError("lse must be contiguous")
+    space, space_bytes = _workspace_of(workspace, device)
+    _on_current_device(device)
+    qs, os_ = q.stride(), out.stride()
+    args = hs_attend_t(kind, row_format, B, P, H, entries, n_rows, q.data_ptr(), qs[:3], address,
+                       row_stride, request_stride, None if slots is None else slots.data_ptr() or 16,
+                       slots_stride[:2], None if lengths is None else lengths.data_ptr(),
+                       out.data_ptr(), os_[:3], None if lse is None else lse.data_ptr(), scale,
+                       space, space_bytes)
+    _check(lib.hs_latent_attend(ctypes.byref(args), _stream(stream)), "hs_latent_attend")
+
+
+def hs_latent_prefill_workspace(k_tokens: int, heads: int) -> int:
+    """Bytes of workspace of hs_latent_prefill over k_tokens rows."""
+    n = int(lib.hs_latent_prefill_workspace(int(k_tokens), int(heads)))
+    if n == 0:
+        raise HsError(HS_ERR_ARG, "hs_latent_prefill_workspace")
+    return n
+
+
+def hs_latent_prefill(q, rows, w_uk, w_uv, q_start, k_start, out, scale: float,
+                      row_format: int = HS_ROWS_16BIT, lse=None, workspace=None,
+                      stream=None) -> None:
+    """Expanded latent attention of ragged prompts, causal: q [Tq][H][192] over rows
+    [Tk] into out [Tq][H][128]; request b has queries q_start[b]..q_start[b + 1] and
+    rows k_start[b]..k_start[b + 1] (int32 [B + 1]), its queries being its last tokens.
+    """
+    import torch
+    kind = _type_of(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must have 3 axes, has %d" % q.dim())
+    Tq, H, _ = q.shape
+    device, B = q.device, q_start.numel() - 1
+    _want(q, "q", (Tq, H, HS_HEAD_DIM + HS_ROPE_DIM), q.dtype, device)
+    _want(out, "out", (Tq, H, HS_HEAD_DIM), q.dtype, device)
+    for w, name in ((w_uk, "w_uk"), (w_uv, "w_uv")):
+        _want(w, name, (H, HS_HEAD_DIM, HS_LATENT_DIM), q.dtype, device)
+        if not w.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+    for x, name in ((q_start, "q_start"), (k_start, "k_start")):
+        _want(x, name, (B + 1,), torch.int32, device)
+    address, k_tokens, row_stride, _ = _rows_of(rows, row_format, q, ())
+    if lse is not None:
+        _want(lse, "lse", (Tq, H), torch.float32, device)
+        if not lse.is_contiguous():
+            raise ValueError("lse must be contiguous")
+    space, space_bytes = _workspace_of(workspace, device)
+    _on_current_device(device)
+    args = hs_prefill_t(kind, row_format, B, H, Tq, k_tokens, q.data_ptr(), q.stride()[:2], address,
+                        row_stride, w_uk.data_ptr(), w_uv.data_ptr(), q_start.data_ptr(),
+                        k_start.data_ptr(), out.data_ptr(), out.stride()[:2],
+                        None if lse is None else lse.data_ptr(), scale, space, space_bytes)
+    _check(lib.hs_latent_prefill(ctypes.byref(args), _stream(stream)), "hs_latent_prefill")
+
+
+def hs_rms_norm(x, weight, out, eps: float, residual=None, residual_out=None, carry: int = 0,
+                scales=None, group: int = 0, stream=None) -> None:
+    """Root-mean-square norm of x[:, :dim] (+ residual), the last `carry` channels of x
+    passed on as they are.  x [N][dim + carry] bf16, fp16 or fp32; residual and
+    residual_out [N][dim] (both or neither; they may be one tensor); weight [dim].
+    out: [N][dim + carry] of x's type, or float8_e4m3fn (or uint8) with scales fp32
+    [N][groups], one for each `group` channels (0: one for the row).
+    """
+    import torch
+    kind = _type_of(x, "x", fp32=True)
+    if x.dim() != 2 or not 0 <= carry < max(x.shape[1], 1):
+        raise ValueError("x must be [tokens][dim + carry] with dim > 0")
+    n, width = x.shape
+    dim, device = width - carry, x.device
+    _want(x, "x", (n, width), x.dtype, device)
+    _want(weight, "weight", (dim,), x.dtype, device)
+    if (residual is None) != (residual_out is None):
+        raise ValueError("give both residual and residual_out, or neither")
+    r = ro = s = (None, 0)
+    if residual is not None:
+        _want(residual, "residual", (n, dim), x.dtype, device)
+        _want(residual_out, "residual_out", (n, dim), x.dtype, device)
+        r = residual.data_ptr(), residual.stride(0)
+        ro = residual_out.data_ptr(), residual_out.stride(0)
+    if scales is None:
+        if group:
+            raise ValueError("group needs scales")
+        _want(out, "out", (n, width), x.dtype, device)
+    else:
+        if group < 0:
+            raise ValueError("group must not be negative")
+        if out.dtype != torch.uint8:
+            _want(out, "out", (n, width), torch.float8_e4m3fn, device)
+        else:
+            _want(out, "out", (n, width), torch.uint8, device)
+        _want(scales, "scales", (n, -(-width // group) if group else 1), torch.float32, device)
+        s = scales.data_ptr(), scales.stride(0)
+    _on_current_device(device)
+    args = hs_norm_t(kind, dim, carry, group, n, x.data_ptr(), x.stride(0), r[0], r[1], ro[0], ro[1],
+                     weight.data_ptr(), eps, out.data_ptr(), out.stride(0), s[0], s[1])
+    _check(lib.hs_rms_norm(ctypes.byref(args), _stream(stream)), "hs_rms_norm")
+
+
 class Handle:
     """Owning wrapper: one swap-in state (one layer, B requests)."""
 
@@ -487,6 +787,12 @@ class Handle:
 
     def resolve(self, topk_idx, K, out_slot, stream=None):
         hs_resolve(self.h, topk_idx, K, out_slot, stream)
+
+    def attend(self, q, slots, out, scale, row_format=HS_ROWS_16BIT, lse=None, workspace=None,
+               stream=None):
+        """Latent attention over the buffer rows that a resolve step returned."""
+        hs_latent_attend(q, self, out, scale, slots=slots, row_format=row_format, lse=lse,
+                         workspace=workspace, stream=stream)
 
     def stats(self, last_miss=None):
         return hs_stats(self.h, last_miss)

@@ -586,6 +586,180 @@ int hs_resolve_noalloc(int batch, int ctx_len, int row_bytes, int buffer_slots, 
                        const int32_t* lengths, const uint8_t* host_pool, uint8_t* device_buffer,
                        hs_control_t* control, hs_stream_t stream);
 
+/*
+ * ---- Operators beside the swap-in path -----------------------------------
+ * What produces and reads the rows that the path moves, on caller-owned
+ * device memory.  A token's row has 576 channels: HS_LATENT_DIM latent
+ * channels, then HS_ROPE_DIM rotary channels (already rotated); all attention
+ * heads share it.  It is held in one of two forms:
+ *   HS_ROWS_16BIT  576 values of the call's type (bf16 or fp16), 1152 bytes
+ *   HS_ROWS_E4M3   HS_ROW8_BYTES = 592 bytes: 576 e4m3 values, at byte
+ *                  HS_ROW8_SCALE the row's fp32 scale (a value is its e4m3
+ *                  times the scale), then 12 bytes that are never read
+ * so a handle created with row_bytes 1152 or 592 can move either.
+ *
+ * The calls only enqueue work: no allocation, no host synchronisation, no
+ * state kept between calls; they can be captured in a CUDA graph.  They run
+ * on the device that is current.  Sums, softmax statistics and accumulators
+ * are fp32; results do not depend on timing (no atomics).  Workspaces are
+ * the caller's, 16-byte aligned device memory of at least the bytes that the
+ * matching _workspace call returns (0 when its sizes are out of range);
+ * their contents need not survive a call, and calls that overlap on the GPU
+ * need one each.  Errors: HS_ERR_ARG (a NULL or misaligned pointer, a size,
+ * type or stride that the call does not take, a workspace that is too small),
+ * HS_ERR_LIMIT, HS_ERR_CUDA; nothing is enqueued then.
+ */
+#define HS_LATENT_DIM  512
+#define HS_ROPE_DIM    64
+#define HS_ROW_DIM     576
+#define HS_HEAD_DIM    128  /* channels of an expanded key (without the rotary ones) or value */
+#define HS_ROW8_SCALE  576
+#define HS_ROW8_BYTES  592
+#define HS_TYPE_BF16   0
+#define HS_TYPE_FP16   1
+#define HS_TYPE_FP32   2    /* hs_rms_norm only */
+#define HS_ROWS_16BIT  0
+#define HS_ROWS_E4M3   1
+#define HS_MAX_HEADS   1024
+#define HS_MAX_POSITIONS 1024
+#define HS_MAX_TOKENS  (1 << 24)  /* tokens of one hs_latent_prefill or hs_rms_norm call */
+#define HS_MAX_NORM_DIM 16384     /* channels of one normed row, the carried ones included */
+
+/*
+ * Latent attention, absorbed form: for each request b, position p and head h
+ *   s_i = scale * <q, row_i>        over the allowed rows i
+ *   out = sum_i softmax(s)_i * row_i[0 : HS_LATENT_DIM]
+ *   lse = log sum_i exp(s_i)
+ * q is the query with the key projection absorbed (its latent part, then its
+ * rotary part); the value projection is the caller's to apply to out.  The
+ * allowed rows are given in one of two ways:
+ *   slots    device int32 [batch][positions][entries], strides in entries: the
+ *            rows of the request to read, as hs_resolve and hs_resolve_multi
+ *            return them.  An entry < 0 or >= n_rows is absent (its row is not
+ *            read); a row listed twice counts twice.
+ *   lengths  device int32 [batch]: the request's first lengths[b] rows in
+ *            order, the last `positions` of them being the call's own tokens:
+ *            position p reads rows t < lengths[b] - positions + 1 + p.  A
+ *            length is clamped to [0, n_rows]; `entries` is ignored.
+ * Exactly one of the two is not NULL.  With no allowed row, out is 0 and lse
+ * -inf; rows that are not allowed may hold anything, NaN included.
+ *   q    [batch][positions][heads][576], out [batch][positions][heads][512]
+ *        of `dtype`; channels contiguous, other strides in elements, multiples
+ *        of 8; both 16-byte aligned
+ *   rows n_rows rows a request, row_stride and request_stride in bytes,
+ *        multiples of 16; 16-byte aligned (a handle's hs_device_buffer:
+ *        n_rows = S + T, row_stride = R, request_stride = (S + T) * R)
+ *   lse  fp32 [batch][positions][heads], contiguous, or NULL
+ * Softmax weights are rounded to `dtype` before the product with the rows.
+ * The workspace call takes `rows` = entries (slots) or n_rows (lengths).
+ * Source: no passage (the pages name the sparse attention that reads the
+ * resolved rows as the path's consumer and do not define it).
+ */
+typedef struct {
+    int32_t dtype;        /* HS_TYPE_BF16 or HS_TYPE_FP16 */
+    int32_t row_format;   /* HS_ROWS_* */
+    int32_t batch, positions, heads, entries;
+    int64_t n_rows;
+    const void* q;
+    int64_t q_stride[3];  /* batch, position, head */
+    const void* rows;
+    int64_t row_stride, request_stride;
+    const int32_t* slots;
+    int64_t slots_stride[2];  /* batch, position */
+    const int32_t* lengths;
+    void* out;
+    int64_t out_stride[3];
+    float* lse;
+    float scale;
+    void* workspace;
+    size_t workspace_bytes;
+} hs_attend_t;
+
+size_t hs_latent_attend_workspace(int batch, int positions, int heads, int64_t rows);
+int hs_latent_attend(const hs_attend_t* args, hs_stream_t stream);
+
+/*
+ * Latent attention, expanded form, of ragged prompts: for each request b and
+ * head h, keys k_j = [w_uk[h] latent_j ; rotary_j] and values v_j = w_uv[h]
+ * latent_j of the request's rows, and
+ *   out_i = sum_j softmax_j(scale * <q_i, k_j>) v_j
+ * over the keys that query i sees: of n queries and m rows, those with
+ * j <= i + m - n (the queries are the last n of the m tokens; where m < n the
+ * first queries see nothing and their out is 0).  Request b has queries
+ * [q_start[b], q_start[b+1]) and rows [k_start[b], k_start[b+1]) (device int32
+ * [batch + 1], non-decreasing from 0; clamped to q_tokens and k_tokens).
+ * Tokens outside every request are not written.
+ *   q     [q_tokens][heads][192] (128 without rotation, then 64 rotary)
+ *   w_uk, w_uv [heads][128][512], contiguous
+ *   out   [q_tokens][heads][128]; lse fp32 [q_tokens][heads] or NULL
+ *   rows  [k_tokens] rows of row_stride bytes
+ * with types, alignments and strides as in hs_latent_attend.  The keys' and
+ * values' expanded channels and the softmax weights are rounded to `dtype`.
+ * Source: no passage (as hs_latent_attend).
+ */
+typedef struct {
+    int32_t dtype;
+    int32_t row_format;
+    int32_t batch, heads;
+    int64_t q_tokens, k_tokens;
+    const void* q;
+    int64_t q_stride[2];  /* token, head */
+    const void* rows;
+    int64_t row_stride;
+    const void* w_uk;
+    const void* w_uv;
+    const int32_t* q_start;
+    const int32_t* k_start;
+    void* out;
+    int64_t out_stride[2];
+    float* lse;
+    float scale;
+    void* workspace;
+    size_t workspace_bytes;
+} hs_prefill_t;
+
+size_t hs_latent_prefill_workspace(int64_t k_tokens, int heads);
+int hs_latent_prefill(const hs_prefill_t* args, hs_stream_t stream);
+
+/*
+ * Root-mean-square norm of `tokens` rows, with an optional residual:
+ *   h = x[:dim] + residual;  residual_out = h
+ *   y = [h / sqrt(mean(h^2) + eps) * weight ; x[dim : dim + carry]]
+ * written as `dtype` (scales NULL), or as e4m3 with a scale for each `group`
+ * channels of y (0: one for the whole row; the last group may be short):
+ *   scale = max|y| / 448 over the group,  out = e4m3(y / scale)
+ * (all zeros: scale 0, out 0; a NaN makes its group's scale NaN).  h stays in
+ * fp32 between the sum and the norm.  With carry = 64, dim = 512 and out,
+ * scales pointing at bytes 0 and HS_ROW8_SCALE of 592-byte rows, it writes
+ * cache rows in the HS_ROWS_E4M3 form.
+ *   x [tokens][dim + carry], residual and residual_out [tokens][dim] (both or
+ *   neither), weight [dim], all of `dtype`; out [tokens][dim + carry]; scales
+ *   fp32 [tokens][groups].  Strides between rows are in elements of each
+ *   array; channels and groups are contiguous.  Any stride and any alignment
+ *   of the element; rows that are 16-byte aligned go faster.  residual_out may
+ *   be residual or x; out (of `dtype`) may be x with x's stride.
+ * Source: no passage (the producer of the rows; the pages start from the rows).
+ */
+typedef struct {
+    int32_t dtype;        /* HS_TYPE_* of x, residual, weight, and of out without scales */
+    int32_t dim, carry, group;
+    int64_t tokens;
+    const void* x;
+    int64_t x_stride;
+    const void* residual;
+    int64_t residual_stride;
+    void* residual_out;
+    int64_t residual_out_stride;
+    const void* weight;
+    float eps;
+    void* out;
+    int64_t out_stride;
+    float* scales;
+    int64_t scales_stride;
+} hs_norm_t;
+
+int hs_rms_norm(const hs_norm_t* args, hs_stream_t stream);
+
 /* Static text for a return code.  Source: no passage. */
 const char* hs_error_string(int code);
 
