@@ -1,76 +1,722 @@
 // hs_latent_attend: absorbed latent attention over listed or leading rows.
 //
-// One warp per (request, position, head); it keeps the query (18 channels a
-// lane), the running maximum and sum and the 16 output channels of each lane
-// in registers, and walks the rows once.
+// For one request and position, S = Q K^T and O = softmax(S) K[:, :512], with
+// the same 576-channel rows as keys and values of up to 128 heads.  A pair of
+// SMs (a cluster of two CTAs) takes up to 128 heads, 64 in each CTA, and walks
+// the rows in tiles of 64; tcgen05 products of the pair (cta_group::2, M = 128)
+// accumulate S (two buffers) and the whole of O (64 heads x 512 channels, 256
+// columns a CTA) in tensor memory.  Each CTA brings half the tile's rows whole
+// (its half of Q K^T's B operand) and all 64 rows' half of the latent channels
+// (its half of the second product's B operand, read along the channels).
+//
+// Warps of a CTA: 0-3 softmax, 4-7 bring rows (two warps a stage), 8 issues the
+// products (in the pair's first CTA).  A rescale of O is rare: the running
+// reference moves only when a maximum exceeds it by more than 2^8.
+//
+// Work split: the tiles of all units (a unit: request, position, 128 heads) form
+// one line that is cut into equal pieces, one a pair; units cut in two leave
+// their sums in the workspace and a second kernel joins them.
 #include "hs_ops.h"
+#include "hs_tc.h"
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kTile = 64;         // rows a tile
+constexpr int kThreads = 288;
+constexpr int kMaxPairs = 76;     // pairs of SMs
+constexpr int kPrefetch = 4;      // tiles brought to L2 ahead
 
-template <typename T, bool E4M3>
-__global__ void __launch_bounds__(kWarps * 32) hs_attend_kernel(hs_attend_t a)
+// Shared memory of a CTA.
+constexpr int kQBytes = 9 * 64 * 128;            // 9 blocks of 64 channels, [64 heads][128 B]
+constexpr int kKBytes = 9 * 32 * 128;            // 9 blocks, [32 rows][128 B]
+constexpr int kVBytes = 4 * 64 * 128;            // 4 blocks, [64 rows][128 B]
+constexpr int kPBytes = 64 * 128;                // [64 heads][64 rows]
+constexpr int kOffK = kQBytes;
+constexpr int kOffV = kOffK + 2 * kKBytes;
+constexpr int kOffP = kOffV + 2 * kVBytes;
+constexpr int kOffAux = kOffP + 2 * kPBytes;
+
+struct Aux {
+    uint64_t full[2], sfull[2], pready[2], pvdone[2], spare;
+    uint32_t tmem;
+    int dead;
+    long long start_unit;  // where this pair's piece of the line begins
+    long long count;       // its tiles
+    int start_tile;
+    uint16_t valid[2][2][2];  // [stage][half][warp]: one bit a row
+    float scale[2][kTile], log_scale[2][kTile];
+    float red[2][128];
+};
+constexpr int kSmem = kOffAux + (int)sizeof(Aux);
+static_assert(kSmem <= 232448, "shared memory");
+
+// Tensor memory columns.
+constexpr uint32_t kColO = 0, kColS = 256;
+
+struct Args {
+    hs_attend_t a;
+    int head_blocks;  // of 128
+    int flat;         // 1: equal pieces of the line of tiles; 0: whole units
+    int64_t units;
+};
+
+// Workspace: an error word, where each pair's piece starts, and two partial results a pair.
+struct Partial {
+    float o[2][256][128];  // [CTA][column][lane]
+    float ref[2][128], sum[2][128];
+};
+struct Start {
+    long long unit;
+    int tile, pad;
+};
+constexpr size_t kOffStart = 256;
+constexpr size_t kOffPartial = kOffStart + sizeof(Start) * (kMaxPairs + 4);
+
+__device__ __forceinline__ int request_tiles(const hs_attend_t& a, long long b)
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (unit >= (int64_t)a.batch * a.positions * a.heads) return;
-    const int head = (int)(unit % a.heads);
-    const int pos = (int)(unit / a.heads % a.positions);
-    const int64_t b = unit / a.heads / a.positions;
-    const T* q = static_cast<const T*>(a.q) + b * a.q_stride[0] + pos * a.q_stride[1] + head * a.q_stride[2];
-    const uint8_t* rows = static_cast<const uint8_t*>(a.rows) + b * a.request_stride;
-    float qr[18], acc[16];
-    for (int i = 0; i < 18; ++i) qr[i] = HsType<T>::to_float(q[lane + 32 * i]);
-    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-    float m = -INFINITY, l = 0.f;
-    const int32_t* slots = a.slots ? a.slots + b * a.slots_stride[0] + pos * a.slots_stride[1] : nullptr;
-    int64_t n = a.entries;
-    if (!slots) {
-        int64_t len = a.lengths[b];
-        len = len < 0 ? 0 : len > a.n_rows ? a.n_rows : len;
-        n = len - a.positions + 1 + pos;
+    long long n = a.entries;
+    if (!a.slots) {
+        n = a.lengths[b];
+        n = n < 0 ? 0 : n > a.n_rows ? a.n_rows : n;
     }
-    for (int64_t i = 0; i < n; ++i) {
-        const int64_t slot = slots ? slots[i] : i;
-        if (slot < 0 || slot >= a.n_rows) continue;
-        const uint8_t* row = rows + slot * a.row_stride;
-        float v[18], s = 0.f;
-        for (int j = 0; j < 18; ++j) {
-            v[j] = E4M3 ? hs_e4m3_to_float(row[lane + 32 * j])
-                        : HsType<T>::to_float(reinterpret_cast<const T*>(row)[lane + 32 * j]);
-            s += qr[j] * v[j];
-        }
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-        float w = 1.f;
-        if (E4M3) w = *reinterpret_cast<const float*>(row + HS_ROW8_SCALE);
-        s *= a.scale * w;
-        const float top = fmaxf(m, s);
-        const float keep = m == -INFINITY ? 0.f : __expf(m - top);
-        const float p = __expf(s - top);
-        l = l * keep + p;
-        for (int j = 0; j < 16; ++j) acc[j] = acc[j] * keep + p * w * v[j];
-        m = top;
-    }
-    T* out = static_cast<T*>(a.out) + b * a.out_stride[0] + pos * a.out_stride[1] + head * a.out_stride[2];
-    for (int j = 0; j < 16; ++j) out[lane + 32 * j] = HsType<T>::from_float(l > 0.f || l != l ? acc[j] / l : 0.f);
-    if (a.lse && lane == 0) a.lse[unit] = l > 0.f || l != l ? m + __logf(l) : -INFINITY;
+    return n <= kTile ? 1 : (int)((n + kTile - 1) / kTile);
 }
 
-template <typename T>
-cudaError_t launch(const hs_attend_t& a, cudaStream_t s)
+// One pair's pieces of units, in order.
+struct Walk {
+    const Args& g;
+    long long unit, left;
+    int tile;
+    // the current piece
+    long long b;
+    int p, hb, t0, t1, tiles;
+    long long rows;  // entries, or allowed rows
+
+    __device__ Walk(const Args& args, const Aux* x) : g(args), unit(x->start_unit), left(x->count), tile(x->start_tile) {}
+
+    __device__ bool next()
+    {
+        if (left <= 0) return false;
+        const hs_attend_t& a = g.a;
+        const int upr = a.positions * g.head_blocks;
+        b = unit / upr;
+        const int rem = (int)(unit - b * upr);
+        p = rem / g.head_blocks;
+        hb = rem - p * g.head_blocks;
+        tiles = request_tiles(a, b);
+        rows = a.entries;
+        if (!a.slots) {
+            rows = a.lengths[b];
+            rows = rows > a.n_rows ? a.n_rows : rows;
+            rows = rows - a.positions + 1 + p;
+            rows = rows < 0 ? 0 : rows;
+        }
+        t0 = tile;
+        t1 = (long long)(tiles - t0) <= left ? tiles : t0 + (int)left;
+        left -= t1 - t0;
+        ++unit;
+        tile = 0;
+        return true;
+    }
+};
+
+// Bounded wait: on a timeout the CTA is marked dead and every later wait returns at once.
+__device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, Aux* x, int* error)
 {
-    const int64_t units = (int64_t)a.batch * a.positions * a.heads;
-    auto k = a.row_format == HS_ROWS_E4M3 ? hs_attend_kernel<T, true> : hs_attend_kernel<T, false>;
-    k<<<(unsigned)((units + kWarps - 1) / kWarps), kWarps * 32, 0, s>>>(a);
+    if (tc::mbar_try(bar, parity)) return;
+    const long long t0 = clock64();
+    while (!tc::mbar_try(bar, parity)) {
+        if (*(volatile int*)&x->dead) return;
+        if (clock64() - t0 > tc::kWaitClocks) {
+            *(volatile int*)&x->dead = 1;
+            if (error) atomicExch(error, 1);
+            return;
+        }
+    }
+}
+
+// Four e4m3 values as two pairs of T.
+template <typename T> __device__ __forceinline__ void widen(uint32_t v, uint32_t& lo, uint32_t& hi);
+template <> __device__ __forceinline__ void widen<__half>(uint32_t v, uint32_t& lo, uint32_t& hi)
+{
+    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v & 0xffff), __NV_E4M3);
+    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v >> 16), __NV_E4M3);
+    lo = a.x | (uint32_t)a.y << 16;
+    hi = b.x | (uint32_t)b.y << 16;
+}
+template <> __device__ __forceinline__ void widen<__nv_bfloat16>(uint32_t v, uint32_t& lo, uint32_t& hi)
+{
+    // An e4m3's exponent and mantissa bits, placed at a bf16's low exponent bits,
+    // are its value times 2^-120 (subnormals too); the product is exact.
+    auto half = [](uint32_t bytes) {
+        const uint32_t m = (bytes & 0x80008000u) | ((bytes & 0x7f007f00u) >> 4);
+        const __nv_bfloat162 big = __halves2bfloat162(__ushort_as_bfloat16(0x7B80), __ushort_as_bfloat16(0x7B80));
+        __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&m);
+        x = __hmul2(x, big);
+        return *reinterpret_cast<uint32_t*>(&x);
+    };
+    lo = half(__byte_perm(v, 0, 0x1404));
+    hi = half(__byte_perm(v, 0, 0x3424));
+    if (((v & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) {  // a NaN among them
+        if ((v & 0x7fu) == 0x7fu) lo |= 0x7fffu;
+        if ((v & 0x7f00u) == 0x7f00u) lo |= 0x7fff0000u;
+        if ((v & 0x7f0000u) == 0x7f0000u) hi |= 0x7fffu;
+        if ((v & 0x7f000000u) == 0x7f000000u) hi |= 0x7fff0000u;
+    }
+}
+
+template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b)
+{
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// ---- the warps' parts ------------------------------------------------------------
+
+// Rows into shared memory: two warps a stage (tiles of one parity).
+template <typename T, bool E4M3>
+__device__ void bring(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int* error)
+{
+    const hs_attend_t& a = g.a;
+    const int lane = threadIdx.x & 31, wg = (threadIdx.x >> 5) - 4;
+    const int stage = wg >> 1, w = wg & 1;  // the stage it fills, its half of the tokens
+    const uint32_t full = tc::map_to_rank(tc::smem_addr(&x->full[stage]), 0);
+    const uint32_t k_smem = sbase + kOffK + stage * kKBytes, v_smem = sbase + kOffV + stage * kVBytes;
+    const int row_bytes = E4M3 ? HS_ROW8_BYTES : 2 * HS_ROW_DIM;
+    const int own0 = 32 * (int)rank + 16 * w, other0 = 32 * (1 - (int)rank) + 16 * w;
+    const int mine = lane < 16 ? own0 + lane : other0 + lane - 16;  // the token of the tile this lane looks up
+    const int block0 = 4 * (int)rank;                               // this CTA's blocks of value channels
+    long long j = 0;                                                // tiles so far
+    Walk walk(g, x);
+    while (walk.next()) {
+        const uint8_t* rows = static_cast<const uint8_t*>(a.rows) + walk.b * a.request_stride;
+        const int32_t* slots = a.slots ? a.slots + walk.b * a.slots_stride[0] + walk.p * a.slots_stride[1] : nullptr;
+        auto lookup = [&](int t) -> long long {  // the row of this lane's token in tile t, or -1
+            const long long i = (long long)t * kTile + mine;
+            if (i >= walk.rows) return -1;
+            const long long r = slots ? slots[i] : i;
+            return r >= 0 && r < a.n_rows ? r : -1;
+        };
+        bool q_due = (j & 1) == stage;  // the first tile's warps bring Q too
+        for (int t = walk.t0; t < walk.t1; ++t, ++j) {
+            if ((j & 1) != stage) continue;
+            const long long row = lookup(t);
+            if (t == walk.t0 || t == walk.t0 + 1) {  // the first tiles of a piece: start the L2 prefetches
+                for (int n = 2; n < kPrefetch && t + n < walk.t1; n += 2) {
+                    const long long r = lookup(t + n);
+                    if (lane < 16 && r >= 0) tc::prefetch_l2(rows + r * a.row_stride, row_bytes);
+                }
+            }
+            if (t + kPrefetch < walk.t1) {
+                const long long r = lookup(t + kPrefetch);
+                if (lane < 16 && r >= 0) tc::prefetch_l2(rows + r * a.row_stride, row_bytes);
+            }
+            if (j >= 2) wait(tc::smem_addr(&x->pvdone[stage]), ((j - 2) >> 1) & 1, x, error);
+            if (q_due && j > 0)  // Q's readers are done (after the wait above: a parity tells two phases apart)
+                wait(tc::smem_addr(&x->pvdone[(j - 1) & 1]), ((j - 1) >> 1) & 1, x, error);
+            if (q_due) {
+                q_due = false;
+                const T* q = static_cast<const T*>(a.q) + walk.b * a.q_stride[0] + walk.p * a.q_stride[1];
+                for (int n = 0; n < 8; ++n) {
+                    const int r = n * 8 + w * 4 + (lane >> 3);
+                    const int head = walk.hb * 128 + (int)rank * 64 + r;
+                    const bool ok = head < a.heads;
+                    const uint8_t* src = reinterpret_cast<const uint8_t*>(q + (ok ? head : 0) * a.q_stride[2]) + (lane & 7) * 16;
+                    const uint32_t dst = sbase + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
+#pragma unroll
+                    for (int c = 0; c < 9; ++c) tc::cp_async16(dst + c * 8192, src + c * 128, ok);
+                }
+            }
+            const unsigned ok_bits = __ballot_sync(~0u, row >= 0);
+            if (lane == 0) {
+                x->valid[stage][rank][w] = (uint16_t)(ok_bits & 0xffff);
+                x->valid[stage][1 - rank][w] = (uint16_t)(ok_bits >> 16);
+            }
+            if constexpr (!E4M3) {
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const int tok = n * 4 + (lane >> 3), ch = lane & 7;  // of 16 tokens; 16-byte piece of a block
+                    const long long r_own = __shfl_sync(~0u, row, tok), r_other = __shfl_sync(~0u, row, 16 + tok);
+                    // absent rows are zeros (nothing is read; q is only an address that exists)
+                    const uint8_t* none = static_cast<const uint8_t*>(a.q);
+                    const uint8_t* own = (r_own < 0 ? none : rows + r_own * a.row_stride) + ch * 16;
+                    const uint8_t* other = (r_other < 0 ? none : rows + r_other * a.row_stride) + ch * 16 + block0 * 128;
+                    const uint32_t kd = k_smem + (16 * w + tok) * 128 + ((ch ^ (tok & 7)) << 4);
+                    const uint32_t vd_own = v_smem + (own0 + tok) * 128 + ((ch ^ (tok & 7)) << 4);
+                    const uint32_t vd_other = v_smem + (other0 + tok) * 128 + ((ch ^ (tok & 7)) << 4);
+#pragma unroll
+                    for (int c = 0; c < 9; ++c) tc::cp_async16(kd + c * 4096, own + c * 128, r_own >= 0);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tc::cp_async16(vd_own + c * 8192, own + (block0 + c) * 128, r_own >= 0);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tc::cp_async16(vd_other + c * 8192, other + c * 128, r_other >= 0);
+                }
+            } else {
+#pragma unroll 1
+                for (int n = 0; n < 2; ++n) {
+                    const int tok = n * 8 + (lane >> 2), ch = lane & 3;  // 16 channels of a block
+                    const long long r_own = __shfl_sync(~0u, row, tok), r_other = __shfl_sync(~0u, row, 16 + tok);
+                    uint4 v[13];
+                    const uint4 zero = make_uint4(0, 0, 0, 0);
+                    const uint8_t* own = rows + (r_own < 0 ? 0 : r_own) * a.row_stride;
+                    const uint8_t* other = rows + (r_other < 0 ? 0 : r_other) * a.row_stride;
+#pragma unroll
+                    for (int c = 0; c < 9; ++c)
+                        v[c] = r_own >= 0 ? *reinterpret_cast<const uint4*>(own + c * 64 + ch * 16) : zero;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        v[9 + c] = r_other >= 0 ? *reinterpret_cast<const uint4*>(other + (block0 + c) * 64 + ch * 16) : zero;
+                    if (ch < 2) {
+                        const bool is_own = ch == 0;
+                        const int at = (is_own ? own0 : other0) + tok;
+                        const bool ok = is_own ? r_own >= 0 : r_other >= 0;
+                        const float sc = ok ? *reinterpret_cast<const float*>((is_own ? own : other) + HS_ROW8_SCALE) : 1.f;
+                        x->scale[stage][at] = sc;
+                        x->log_scale[stage][at] = log2f(fabsf(sc));
+                    }
+                    const int r0 = tok & 7, c0 = ((2 * ch) ^ r0) << 4, c1 = ((2 * ch + 1) ^ r0) << 4;
+                    const uint32_t kd = k_smem + (16 * w + tok) * 128;
+#pragma unroll
+                    for (int c = 0; c < 13; ++c) {
+                        uint32_t e[8];
+                        widen<T>(v[c].x, e[0], e[1]);
+                        widen<T>(v[c].y, e[2], e[3]);
+                        widen<T>(v[c].z, e[4], e[5]);
+                        widen<T>(v[c].w, e[6], e[7]);
+                        if (c < 9) {
+                            tc::st_shared16(kd + c * 4096 + c0, e[0], e[1], e[2], e[3]);
+                            tc::st_shared16(kd + c * 4096 + c1, e[4], e[5], e[6], e[7]);
+                            const int vb = c - block0;
+                            if (vb >= 0 && vb < 4) {
+                                const uint32_t vd = v_smem + vb * 8192 + (own0 + tok) * 128;
+                                tc::st_shared16(vd + c0, e[0], e[1], e[2], e[3]);
+                                tc::st_shared16(vd + c1, e[4], e[5], e[6], e[7]);
+                            }
+                        } else {
+                            const uint32_t vd = v_smem + (c - 9) * 8192 + (other0 + tok) * 128;
+                            tc::st_shared16(vd + c0, e[0], e[1], e[2], e[3]);
+                            tc::st_shared16(vd + c1, e[4], e[5], e[6], e[7]);
+                        }
+                    }
+                }
+            }
+            tc::cp_async_commit();
+            tc::cp_async_wait<0>();
+            tc::fence_async_shared();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_cluster(full);
+        }
+    }
+}
+
+// The products, issued by one thread of the pair's first CTA.
+template <typename T> __device__ void multiply(const Args& g, uint32_t sbase, Aux* x, int* error)
+{
+    constexpr bool bf = HsType<T>::is_bf16;
+    constexpr uint32_t d_qk = tc::inst_desc(bf, 128, kTile, false, false);
+    constexpr uint32_t d_pv = tc::inst_desc(bf, 128, 256, false, true);
+    const uint32_t tmem = x->tmem;
+    const uint64_t q_desc = tc::smem_desc(sbase, 16, 1024);
+    const long long n = x->count;
+    Walk walk(g, x);
+    walk.next();
+    int piece_left = walk.t1 - walk.t0;
+    bool first = true;
+    long long qk = 0, pv = 0;
+    long long t0 = clock64();
+    while (pv < n) {
+        if (qk < n && qk <= pv + 1 && tc::mbar_test(tc::smem_addr(&x->full[qk & 1]), (qk >> 1) & 1)) {
+            const int s = qk & 1;
+            tc::fence_after();
+            const uint64_t k_desc = tc::smem_desc(sbase + kOffK + s * kKBytes, 16, 1024);
+#pragma unroll
+            for (int c = 0; c < 9; ++c)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    tc::mma_ss<2>(tmem + kColS + 32 * s, q_desc + ((c * 8192 + k * 32) >> 4),
+                                  k_desc + ((c * 4096 + k * 32) >> 4), d_qk, (c | k) != 0);
+            tc::commit<2>(tc::smem_addr(&x->sfull[s]));
+            ++qk;
+            t0 = clock64();
+        } else if (pv < qk && tc::mbar_test(tc::smem_addr(&x->pready[pv & 1]), (pv >> 1) & 1)) {
+            const int s = pv & 1;
+            tc::fence_after();
+            const uint64_t p_desc = tc::smem_desc(sbase + kOffP + s * kPBytes, 16, 1024);
+            const uint64_t v_desc = tc::smem_desc(sbase + kOffV + s * kVBytes, 8192, 1024);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    tc::mma_ss<2>(tmem + kColO + 128 * h, p_desc + ((k * 32) >> 4),
+                                  v_desc + ((h * 16384 + k * 2048) >> 4), d_pv, !(first && k == 0));
+            tc::commit<2>(tc::smem_addr(&x->pvdone[s]));
+            first = false;
+            if (--piece_left == 0 && walk.next()) {
+                piece_left = walk.t1 - walk.t0;
+                first = true;
+            }
+            ++pv;
+            t0 = clock64();
+        } else if (*(volatile int*)&x->dead || clock64() - t0 > tc::kWaitClocks) {
+            *(volatile int*)&x->dead = 1;
+            if (error) atomicExch(error, 1);
+            // what was issued must be complete before tensor memory is freed
+            tc::commit<2>(tc::smem_addr(&x->spare));
+            tc::mbar_wait(tc::smem_addr(&x->spare), 0);
+            return;
+        }
+    }
+}
+
+// Softmax of 64 heads: thread (head, half) takes 32 of a tile's 64 rows.
+template <typename T, bool E4M3>
+__device__ void soften(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int pair, uint8_t* ws, int* error)
+{
+    const hs_attend_t& a = g.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = threadIdx.x & 63, half = threadIdx.x >> 6;
+    const uint32_t tmem = x->tmem + ((uint32_t)warp << 21);  // this warp's 32 lanes
+    const float c = a.scale * 1.4426950408889634f;
+    long long j = 0;
+    Walk walk(g, x);
+    const uint32_t pready[2] = {tc::map_to_rank(tc::smem_addr(&x->pready[0]), 0),
+                                tc::map_to_rank(tc::smem_addr(&x->pready[1]), 0)};
+    while (walk.next()) {
+        float ref = 0.f, sum = 0.f;
+        bool seen = false;  // a row that counts has been met: ref is a maximum
+        for (int t = walk.t0; t < walk.t1; ++t, ++j) {
+            const int s = j & 1;
+            wait(tc::smem_addr(&x->sfull[s]), (j >> 1) & 1, x, error);
+            tc::fence_after();
+            uint32_t r[32];
+            tc::tmem_ld32(tmem + kColS + 32 * s, r);
+            tc::tmem_wait_ld();
+            const uint32_t valid = reinterpret_cast<const uint32_t*>(x->valid[s])[half];
+            const float* wt = x->scale[s] + 32 * half;
+            const float* lw = x->log_scale[s] + 32 * half;
+            float v[32], top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                v[i] = __uint_as_float(r[i]) * c;
+                if constexpr (E4M3) v[i] *= wt[i];
+            }
+            if (valid != ~0u)
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (!(valid >> i & 1)) v[i] = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) top = fmaxf(top, E4M3 ? v[i] + lw[i] : v[i]);
+            x->red[s][threadIdx.x] = top;
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            top = fmaxf(top, x->red[s][threadIdx.x ^ 64]);
+            float keep = 1.f;
+            if (top > -INFINITY && (!seen || top > ref + 8.f)) {
+                keep = tc::exp2_approx(fminf(ref - top, 126.f));
+                sum *= keep;
+                ref = top;
+            }
+            const bool scale_o = seen && keep != 1.f;
+            seen = seen || top > -INFINITY;
+            // the buffer of P is free once the product two tiles ago is done
+            if (j >= 2) wait(tc::smem_addr(&x->pvdone[s]), ((j - 2) >> 1) & 1, x, error);
+            if (__any_sync(~0u, scale_o)) {
+                if (!scale_o) keep = 1.f;
+                wait(tc::smem_addr(&x->pvdone[1 - s]), ((j - 1) >> 1) & 1, x, error);
+                tc::fence_after();
+#pragma unroll 1
+                for (int n = 0; n < 256; n += 32) {
+                    tc::tmem_ld32(tmem + kColO + n, r);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * keep);
+                    tc::tmem_st32(tmem + kColO + n, r);
+                }
+                tc::tmem_wait_st();
+            }
+            const uint32_t dst = sbase + kOffP + s * kPBytes + row * 128;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                uint32_t e[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int k = n * 8 + 2 * i;
+                    float p0 = tc::exp2_approx(v[k] - ref), p1 = tc::exp2_approx(v[k + 1] - ref);
+                    sum += p0 + p1;
+                    if constexpr (E4M3) {
+                        p0 *= wt[k];
+                        p1 *= wt[k + 1];
+                    }
+                    e[i] = pack2<T>(p0, p1);
+                }
+                tc::st_shared16(dst + (((half * 4 + n) ^ (row & 7)) << 4), e[0], e[1], e[2], e[3]);
+            }
+            tc::fence_async_shared();
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_cluster(pready[s]);
+        }
+        // The piece's end: O and the sums leave.
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        x->red[0][threadIdx.x] = sum;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        sum += x->red[0][threadIdx.x ^ 64];
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        wait(tc::smem_addr(&x->pvdone[(j - 1) & 1]), ((j - 1) >> 1) & 1, x, error);
+        tc::fence_after();
+        const int head = walk.hb * 128 + (int)rank * 64 + row;
+        const bool whole = walk.t0 == 0 && walk.t1 == walk.tiles;
+        Partial* part = reinterpret_cast<Partial*>(ws + kOffPartial) + 2 * pair + (walk.t0 == 0 ? 1 : 0);
+        const bool some = sum > 0.f || sum != sum;
+        const float inv = some ? 1.f / sum : 0.f;
+        T* out = static_cast<T*>(a.out) + walk.b * a.out_stride[0] + walk.p * a.out_stride[1] +
+                 (int64_t)head * a.out_stride[2] + 256 * half;
+#pragma unroll 1
+        for (int n = 0; n < 256; n += 32) {
+            uint32_t r[32];
+            __syncwarp();
+            tc::tmem_ld32(tmem + kColO + n, r);
+            tc::tmem_wait_ld();
+            if (head >= a.heads) {
+                // a lane without a head has nothing to write
+            } else if (whole) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                    uint4 e;
+                    auto f = [&](int k) { return some ? __uint_as_float(r[i + k]) * inv : 0.f; };
+                    e.x = pack2<T>(f(0), f(1));
+                    e.y = pack2<T>(f(2), f(3));
+                    e.z = pack2<T>(f(4), f(5));
+                    e.w = pack2<T>(f(6), f(7));
+                    *reinterpret_cast<uint4*>(out + n + i) = e;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) part->o[rank][n + i][threadIdx.x] = __uint_as_float(r[i]);
+            }
+        }
+        if (head < a.heads) {
+            if (!whole) {
+                part->ref[rank][threadIdx.x] = ref;
+                part->sum[rank][threadIdx.x] = sum;
+            } else if (a.lse && half == 0) {
+                a.lse[(walk.b * a.positions + walk.p) * a.heads + head] =
+                    some ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+            }
+        }
+        tc::fence_before();
+    }
+}
+
+template <typename T, bool E4M3>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_attend_kernel(const __grid_constant__ Args g)
+{
+    extern __shared__ __align__(1024) uint8_t base[];  // the swizzled tiles need 1024
+    const uint32_t sbase = tc::smem_addr(base);
+    Aux* x = reinterpret_cast<Aux*>(base + kOffAux);
+    const hs_attend_t& a = g.a;
+    const uint32_t rank = tc::cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    int* error = reinterpret_cast<int*>(ws);
+
+    if (warp == 0) tc::tmem_alloc<2>(tc::smem_addr(&x->tmem), 512);
+    if (warp == 8) {
+        // This pair's piece of the line of tiles.
+        const int upr = a.positions * g.head_blocks;
+        long long total, lo, hi, unit, tile;
+        if (a.slots) {
+            const int tiles = request_tiles(a, 0);
+            total = g.units * tiles;
+            const long long n = total < pairs ? total : pairs;
+            if (pair >= n) {
+                lo = hi = 0;
+            } else if (g.flat) {
+                lo = total * pair / n;
+                hi = total * (pair + 1) / n;
+            } else {
+                lo = g.units * pair / pairs * tiles;
+                hi = g.units * (pair + 1) / pairs * tiles;
+            }
+            unit = lo / tiles;
+            tile = lo - unit * tiles;
+        } else {
+            total = 0;
+            for (int b = lane; b < a.batch; b += 32) total += (long long)request_tiles(a, b) * upr;
+            for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
+            const long long n = total < pairs ? total : pairs;
+            lo = pair < n ? total * pair / n : 0;
+            hi = pair < n ? total * (pair + 1) / n : 0;
+            unit = tile = 0;
+            long long before = 0;
+            for (int b0 = 0; b0 < a.batch; b0 += 32) {
+                const int b = b0 + lane;
+                const long long tiles = b < a.batch ? request_tiles(a, b) : 0;
+                long long incl = tiles * upr;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long up = __shfl_up_sync(~0u, incl, o);
+                    if (lane >= o) incl += up;
+                }
+                const long long at = before + incl - tiles * upr;  // where request b begins
+                const bool here = b < a.batch && lo >= at && lo < at + tiles * upr;
+                const unsigned who = __ballot_sync(~0u, here);
+                if (who) {
+                    const int src = __ffs(who) - 1;
+                    const long long u = here ? (long long)b * upr + (lo - at) / tiles : 0;
+                    const long long tl = here ? (lo - at) % tiles : 0;
+                    unit = __shfl_sync(~0u, u, src);
+                    tile = __shfl_sync(~0u, tl, src);
+                    break;
+                }
+                before += __shfl_sync(~0u, incl, 31);
+            }
+        }
+        if (lane == 0) {
+            x->start_unit = unit;
+            x->start_tile = (int)tile;
+            x->count = hi - lo;
+            x->dead = 0;
+            if (rank == 0) {
+                Start* st = reinterpret_cast<Start*>(ws + kOffStart) + pair;
+                st->unit = hi > lo ? unit : -1;
+                st->tile = (int)tile;
+            }
+            for (int i = 0; i < 2; ++i) {
+                tc::mbar_init(tc::smem_addr(&x->full[i]), 4);
+                tc::mbar_init(tc::smem_addr(&x->sfull[i]), 1);
+                tc::mbar_init(tc::smem_addr(&x->pready[i]), 8);
+                tc::mbar_init(tc::smem_addr(&x->pvdone[i]), 1);
+            }
+            tc::mbar_init(tc::smem_addr(&x->spare), 1);
+            tc::mbar_init_fence();
+        }
+    }
+    tc::fence_before();
+    __syncwarp();
+    __syncthreads();
+    tc::cluster_sync();
+    tc::fence_after();
+
+    if (x->count > 0) {
+        if (warp < 4)
+            soften<T, E4M3>(g, sbase, x, rank, pair, ws, error);
+        else if (warp < 8)
+            bring<T, E4M3>(g, sbase, x, rank, error);
+        else if (rank == 0 && lane == 0)
+            multiply<T>(g, sbase, x, error);
+    }
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();
+    tc::cluster_sync();
+    tc::fence_after();
+    if (warp == 0) tc::tmem_free<2>(x->tmem, 512);
+}
+
+// Join the pieces of a unit that several pairs worked on: block i takes the unit
+// cut first at the start of pair i + 1's piece.
+template <typename T> __global__ void __launch_bounds__(128) hs_attend_join_kernel(const __grid_constant__ Args g, int pairs)
+{
+    const hs_attend_t& a = g.a;
+    const uint8_t* ws = static_cast<const uint8_t*>(a.workspace);
+    const Start* start = reinterpret_cast<const Start*>(ws + kOffStart);
+    const Partial* parts = reinterpret_cast<const Partial*>(ws + kOffPartial);
+    const int i = blockIdx.x + 1, rank = blockIdx.y, c0 = 32 * blockIdx.z;
+    const long long unit = start[i].unit;
+    if (unit < 0 || start[i].tile == 0) return;
+    if (i > 1 && start[i - 1].unit == unit && start[i - 1].tile > 0) return;
+    int last = i;
+    while (last + 1 < pairs && start[last + 1].unit == unit && start[last + 1].tile > 0) ++last;
+    const int upr = a.positions * g.head_blocks;
+    const long long b = unit / upr;
+    const int rem = (int)(unit - b * upr), p = rem / g.head_blocks, hb = rem - p * g.head_blocks;
+    const int lane = threadIdx.x, row = lane & 63, half = lane >> 6;
+    const int head = hb * 128 + rank * 64 + row;
+    if (head >= a.heads) return;
+    float top = -INFINITY;
+    for (int n = i - 1; n <= last; ++n) {
+        const Partial& q = parts[2 * n + (n == i - 1)];
+        if (q.sum[rank][lane] != 0.f) top = fmaxf(top, q.ref[rank][lane]);
+    }
+    float acc[32] = {}, sum = 0.f;
+    for (int n = i - 1; n <= last; ++n) {
+        const Partial& q = parts[2 * n + (n == i - 1)];
+        const float l = q.sum[rank][lane];
+        if (l == 0.f) continue;
+        const float w = tc::exp2_approx(q.ref[rank][lane] - top);
+        sum += w * l;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) acc[k] += w * q.o[rank][c0 + k][lane];
+    }
+    const bool some = sum > 0.f || sum != sum;
+    const float inv = some ? 1.f / sum : 0.f;
+    T* out = static_cast<T*>(a.out) + b * a.out_stride[0] + p * a.out_stride[1] + (int64_t)head * a.out_stride[2] +
+             256 * half + c0;
+#pragma unroll
+    for (int k = 0; k < 32; k += 8) {
+        uint4 e;
+        e.x = pack2<T>(acc[k] * inv, acc[k + 1] * inv);
+        e.y = pack2<T>(acc[k + 2] * inv, acc[k + 3] * inv);
+        e.z = pack2<T>(acc[k + 4] * inv, acc[k + 5] * inv);
+        e.w = pack2<T>(acc[k + 6] * inv, acc[k + 7] * inv);
+        *reinterpret_cast<uint4*>(out + k) = e;
+    }
+    if (a.lse && half == 0 && c0 == 0)
+        a.lse[(b * a.positions + p) * a.heads + head] = some ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+}
+
+// Pairs a call can use, from the most tiles its sizes allow.
+int64_t pairs_for(int64_t units, int64_t rows)
+{
+    const int64_t tiles = rows <= kTile ? 1 : (rows + kTile - 1) / kTile;
+    return units * tiles < kMaxPairs ? units * tiles : kMaxPairs;
+}
+
+template <typename T, bool E4M3> cudaError_t launch(const Args& g, int pairs, cudaStream_t s)
+{
+    cudaError_t e = cudaFuncSetAttribute(hs_attend_kernel<T, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    hs_attend_kernel<T, E4M3><<<2 * pairs, kThreads, kSmem, s>>>(g);
+    if (g.flat && pairs > 1) hs_attend_join_kernel<T><<<dim3(pairs - 1, 2, 8), 128, 0, s>>>(g, pairs);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t hs_attend_workspace_bytes(int, int, int, int64_t) { return 256; }
+size_t hs_attend_workspace_bytes(int batch, int positions, int heads, int64_t rows)
+{
+    const int64_t units = (int64_t)batch * positions * ((heads + 127) / 128);
+    return kOffPartial + sizeof(Partial) * 2 * (size_t)pairs_for(units, rows);
+}
 
 cudaError_t hs_launch_attend(const hs_attend_t& a, cudaStream_t s)
 {
-    return a.dtype == HS_TYPE_BF16 ? launch<__nv_bfloat16>(a, s) : launch<__half>(a, s);
+    Args g;
+    g.a = a;
+    g.head_blocks = (a.heads + 127) / 128;
+    g.units = (int64_t)a.batch * a.positions * g.head_blocks;
+    const int64_t rows = a.slots ? a.entries : a.n_rows;
+    const int64_t tiles = rows <= kTile ? 1 : (rows + kTile - 1) / kTile;
+    int64_t pairs = pairs_for(g.units, rows);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    if (sms >= 2 && pairs > sms / 2) pairs = sms / 2;
+    // Whole units to a pair, or equal pieces: equal pieces also write and join
+    // up to two partial results a pair (about 12 tiles' time for 128 heads).
+    const int64_t whole = (g.units + pairs - 1) / pairs * tiles;
+    const int64_t pieces = (g.units * tiles + pairs - 1) / pairs + 2 + 10 * (a.heads < 128 ? a.heads : 128) / 128;
+    g.flat = !a.slots || whole > pieces;
+    if (!g.flat && pairs > g.units) pairs = g.units;
+    const bool e4m3 = a.row_format == HS_ROWS_E4M3;
+    if (a.dtype == HS_TYPE_BF16)
+        return e4m3 ? launch<__nv_bfloat16, true>(g, (int)pairs, s) : launch<__nv_bfloat16, false>(g, (int)pairs, s);
+    return e4m3 ? launch<__half, true>(g, (int)pairs, s) : launch<__half, false>(g, (int)pairs, s);
 }

@@ -23,11 +23,13 @@ constexpr float HS_E4M3_MAX = 448.0f;
 template <typename T> struct HsType;
 template <> struct HsType<__nv_bfloat16> {
     using Pair = __nv_bfloat162;
+    static constexpr bool is_bf16 = true;
     static __device__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
     static __device__ __nv_bfloat16 from_float(float v) { return __float2bfloat16_rn(v); }
 };
 template <> struct HsType<__half> {
     using Pair = __half2;
+    static constexpr bool is_bf16 = false;
     static __device__ float to_float(__half v) { return __half2float(v); }
     static __device__ __half from_float(float v) { return __float2half_rn(v); }
 };

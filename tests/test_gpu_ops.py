@@ -85,7 +85,7 @@ def _check_attend(out, lse, ref, dtype):
     tol = half * o.abs() + (half + 2 * score) * mean_abs + 1e-30
     err = (out.double() - o).abs()
     assert torch.isfinite(out).all()
-    assert (err <= tol).all(), (err / tol).max().item()
+    assert bool((err <= tol).all()), (err / tol).max().item()
     # roundings are independent: two of at most half a step each, in the 2-norm
     assert err.norm() <= (1.5 * half + 1e-4) * o.norm() + 1e-30, (err.norm() / o.norm()).item()
     empty = want_lse == -math.inf
@@ -342,7 +342,7 @@ def _check_prefill(out, lse, q, rows, w_uk, w_uv, nq, nk, e4m3):
             tol = half * o.abs() + (2 * half + 2.0 ** -12 + 2 * score) * mean_abs + 1e-30
             err = (got[some].double() - o).abs()
             assert torch.isfinite(got).all()
-            assert (err <= tol).all(), (err / tol).max().item()
+            assert bool((err <= tol).all()), (err / tol).max().item()
             lse_err = (got_lse[some].double() - torch.logsumexp(s[some], -1)).abs()
             assert (lse_err <= score.squeeze(-1) + 2.0 ** -20 * 20).all()
             off += err.square().sum().item()
