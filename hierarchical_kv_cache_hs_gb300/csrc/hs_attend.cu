@@ -9,8 +9,8 @@
 // (its half of Q K^T's B operand) and all 64 rows' half of the latent channels
 // (its half of the second product's B operand, read along the channels).
 //
-// Warps of a CTA: 0-3 softmax, 4-7 bring rows (two warps a stage), 8 issues the
-// products (in the pair's first CTA).  A rescale of O is rare: the running
+// Warps of a CTA: 0-3 softmax, 4-7 bring the keys (two warps a stage), 8-11 the
+// values and the queries, 12 and 13 issue the products (in the pair's first CTA).  A rescale of O is rare: the running
 // reference moves only when a maximum exceeds it by more than 2^8.
 //
 // Work split: the tiles of all units (a unit: request, position, 128 heads) form
@@ -22,7 +22,7 @@
 namespace {
 
 constexpr int kTile = 64;         // rows a tile
-constexpr int kThreads = 288;
+constexpr int kThreads = 14 * 32;
 constexpr int kMaxPairs = 76;     // pairs of SMs
 constexpr int kPrefetch = 4;      // tiles brought to L2 ahead
 
@@ -37,14 +37,16 @@ constexpr int kOffP = kOffV + 2 * kVBytes;
 constexpr int kOffAux = kOffP + 2 * kPBytes;
 
 struct Aux {
-    uint64_t full[2], sfull[2], pready[2], pvdone[2], spare;
+    uint64_t kfull[2], vfull[2], qfull, sfull[2], pready[2], pvdone[2], spare[2];
     uint32_t tmem;
     int dead;
     long long start_unit;  // where this pair's piece of the line begins
     long long count;       // its tiles
     int start_tile;
-    uint16_t valid[2][2][2];  // [stage][half][warp]: one bit a row
-    float scale[2][kTile], log_scale[2][kTile];
+    // Per tile, four deep: a tile's keys arrive while the softmax two tiles back still reads these.
+    uint16_t valid[4][2][2];  // [half][warp]: one bit a row
+    float scale[4][kTile];
+    __half log_scale[4][kTile];  // only moves the reference: its rounding cancels
     float red[2][128];
 };
 constexpr int kSmem = kOffAux + (int)sizeof(Aux);
@@ -179,131 +181,196 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b)
 
 // ---- the warps' parts ------------------------------------------------------------
 
-// Rows into shared memory: two warps a stage (tiles of one parity).
+// This lane's row of a tile: request rows at `rows`, entry i of the list (or the i-th row).
+struct Lookup {
+    const hs_attend_t& a;
+    const int32_t* slots;
+    long long n;
+    __device__ Lookup(const hs_attend_t& args, const Walk& w)
+        : a(args), slots(args.slots ? args.slots + w.b * args.slots_stride[0] + w.p * args.slots_stride[1] : nullptr), n(w.rows)
+    {
+    }
+    __device__ int operator()(int tile, int at) const  // the row, or -1
+    {
+        const long long i = (long long)tile * kTile + at;
+        if (i >= n) return -1;
+        if (!slots) return (int)i;
+        const int r = slots[i];
+        return r >= 0 && r < a.n_rows ? r : -1;
+    }
+};
+
+// 16 e4m3 values as two 16-byte pieces of T at dst + c0 and dst + c1.
+template <typename T> __device__ __forceinline__ void store_wide(const uint4& v, uint32_t dst, int c0, int c1)
+{
+    uint32_t e[8];
+    widen<T>(v.x, e[0], e[1]);
+    widen<T>(v.y, e[2], e[3]);
+    widen<T>(v.z, e[4], e[5]);
+    widen<T>(v.w, e[6], e[7]);
+    tc::st_shared16(dst + c0, e[0], e[1], e[2], e[3]);
+    tc::st_shared16(dst + c1, e[4], e[5], e[6], e[7]);
+}
+
+// Keys: this CTA's 32 rows of each tile, whole.  Two warps a stage (tiles of one
+// parity), 16 rows each; they also say which of the tile's 64 rows count.
 template <typename T, bool E4M3>
-__device__ void bring(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int* error)
+__device__ void bring_keys(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int* error)
 {
     const hs_attend_t& a = g.a;
     const int lane = threadIdx.x & 31, wg = (threadIdx.x >> 5) - 4;
-    const int stage = wg >> 1, w = wg & 1;  // the stage it fills, its half of the tokens
-    const uint32_t full = tc::map_to_rank(tc::smem_addr(&x->full[stage]), 0);
-    const uint32_t k_smem = sbase + kOffK + stage * kKBytes, v_smem = sbase + kOffV + stage * kVBytes;
+    const int stage = wg >> 1, w = wg & 1;
+    const uint32_t full = tc::map_to_rank(tc::smem_addr(&x->kfull[stage]), 0);
+    const uint32_t k_smem = sbase + kOffK + stage * kKBytes;
     const int row_bytes = E4M3 ? HS_ROW8_BYTES : 2 * HS_ROW_DIM;
-    const int own0 = 32 * (int)rank + 16 * w, other0 = 32 * (1 - (int)rank) + 16 * w;
-    const int mine = lane < 16 ? own0 + lane : other0 + lane - 16;  // the token of the tile this lane looks up
-    const int block0 = 4 * (int)rank;                               // this CTA's blocks of value channels
-    long long j = 0;                                                // tiles so far
+    // lanes 0-15 look up the rows to bring, the others 16 of the other CTA's
+    const int mine = (lane < 16 ? 32 * (int)rank : 32 * (1 - (int)rank)) + 16 * w + (lane & 15);
+    long long j = 0;  // tiles so far
     Walk walk(g, x);
     while (walk.next()) {
         const uint8_t* rows = static_cast<const uint8_t*>(a.rows) + walk.b * a.request_stride;
-        const int32_t* slots = a.slots ? a.slots + walk.b * a.slots_stride[0] + walk.p * a.slots_stride[1] : nullptr;
-        auto lookup = [&](int t) -> long long {  // the row of this lane's token in tile t, or -1
-            const long long i = (long long)t * kTile + mine;
-            if (i >= walk.rows) return -1;
-            const long long r = slots ? slots[i] : i;
-            return r >= 0 && r < a.n_rows ? r : -1;
+        const Lookup lookup(a, walk);
+        auto prefetch = [&](int t) {
+            if (t >= walk.t1 || lane >= 16) return;
+            const int r = lookup(t, mine);
+            if (r >= 0) tc::prefetch_l2(rows + r * a.row_stride, row_bytes);
         };
-        bool q_due = (j & 1) == stage;  // the first tile's warps bring Q too
-        for (int t = walk.t0; t < walk.t1; ++t, ++j) {
-            if ((j & 1) != stage) continue;
-            const long long row = lookup(t);
-            if (t == walk.t0 || t == walk.t0 + 1) {  // the first tiles of a piece: start the L2 prefetches
-                for (int n = 2; n < kPrefetch && t + n < walk.t1; n += 2) {
-                    const long long r = lookup(t + n);
-                    if (lane < 16 && r >= 0) tc::prefetch_l2(rows + r * a.row_stride, row_bytes);
-                }
-            }
-            if (t + kPrefetch < walk.t1) {
-                const long long r = lookup(t + kPrefetch);
-                if (lane < 16 && r >= 0) tc::prefetch_l2(rows + r * a.row_stride, row_bytes);
-            }
-            if (j >= 2) wait(tc::smem_addr(&x->pvdone[stage]), ((j - 2) >> 1) & 1, x, error);
-            if (q_due && j > 0)  // Q's readers are done (after the wait above: a parity tells two phases apart)
-                wait(tc::smem_addr(&x->pvdone[(j - 1) & 1]), ((j - 1) >> 1) & 1, x, error);
-            if (q_due) {
-                q_due = false;
-                const T* q = static_cast<const T*>(a.q) + walk.b * a.q_stride[0] + walk.p * a.q_stride[1];
-                for (int n = 0; n < 8; ++n) {
-                    const int r = n * 8 + w * 4 + (lane >> 3);
-                    const int head = walk.hb * 128 + (int)rank * 64 + r;
-                    const bool ok = head < a.heads;
-                    const uint8_t* src = reinterpret_cast<const uint8_t*>(q + (ok ? head : 0) * a.q_stride[2]) + (lane & 7) * 16;
-                    const uint32_t dst = sbase + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
-#pragma unroll
-                    for (int c = 0; c < 9; ++c) tc::cp_async16(dst + c * 8192, src + c * 128, ok);
-                }
-            }
+        int t = walk.t0;
+        if ((j & 1) != stage) ++t;  // this stage's first tile of the piece
+        for (int n = 2; n < kPrefetch; n += 2) prefetch(t + n);
+        int next = t < walk.t1 ? lookup(t, mine) : -1;
+        for (; t < walk.t1; t += 2) {
+            const long long jt = j + t - walk.t0;
+            const int row = next;
+            if (t + 2 < walk.t1) next = lookup(t + 2, mine);
+            prefetch(t + kPrefetch);
+            const int m = (int)(jt & 3);
             const unsigned ok_bits = __ballot_sync(~0u, row >= 0);
-            if (lane == 0) {
-                x->valid[stage][rank][w] = (uint16_t)(ok_bits & 0xffff);
-                x->valid[stage][1 - rank][w] = (uint16_t)(ok_bits >> 16);
-            }
             if constexpr (!E4M3) {
+                if (jt >= 2) wait(tc::smem_addr(&x->sfull[stage]), ((jt - 2) >> 1) & 1, x, error);
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
-                    const int tok = n * 4 + (lane >> 3), ch = lane & 7;  // of 16 tokens; 16-byte piece of a block
-                    const long long r_own = __shfl_sync(~0u, row, tok), r_other = __shfl_sync(~0u, row, 16 + tok);
+                    const int tok = n * 4 + (lane >> 3), ch = lane & 7;  // 16-byte piece of a block
+                    const int r = __shfl_sync(~0u, row, tok);
                     // absent rows are zeros (nothing is read; q is only an address that exists)
-                    const uint8_t* none = static_cast<const uint8_t*>(a.q);
-                    const uint8_t* own = (r_own < 0 ? none : rows + r_own * a.row_stride) + ch * 16;
-                    const uint8_t* other = (r_other < 0 ? none : rows + r_other * a.row_stride) + ch * 16 + block0 * 128;
-                    const uint32_t kd = k_smem + (16 * w + tok) * 128 + ((ch ^ (tok & 7)) << 4);
-                    const uint32_t vd_own = v_smem + (own0 + tok) * 128 + ((ch ^ (tok & 7)) << 4);
-                    const uint32_t vd_other = v_smem + (other0 + tok) * 128 + ((ch ^ (tok & 7)) << 4);
+                    const uint8_t* src = (r < 0 ? static_cast<const uint8_t*>(a.q) : rows + r * a.row_stride) + ch * 16;
+                    const uint32_t dst = k_smem + (16 * w + tok) * 128 + ((ch ^ (tok & 7)) << 4);
 #pragma unroll
-                    for (int c = 0; c < 9; ++c) tc::cp_async16(kd + c * 4096, own + c * 128, r_own >= 0);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tc::cp_async16(vd_own + c * 8192, own + (block0 + c) * 128, r_own >= 0);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tc::cp_async16(vd_other + c * 8192, other + c * 128, r_other >= 0);
+                    for (int c = 0; c < 9; ++c) tc::cp_async16(dst + c * 4096, src + c * 128, r >= 0);
                 }
             } else {
-#pragma unroll 1
+                const float sc = row >= 0 ? *reinterpret_cast<const float*>(rows + row * a.row_stride + HS_ROW8_SCALE) : 1.f;
+                const int ch = lane & 3;  // 16 channels of a block
+                uint4 v[2][9];
+#pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    const int tok = n * 8 + (lane >> 2), ch = lane & 3;  // 16 channels of a block
-                    const long long r_own = __shfl_sync(~0u, row, tok), r_other = __shfl_sync(~0u, row, 16 + tok);
-                    uint4 v[13];
-                    const uint4 zero = make_uint4(0, 0, 0, 0);
-                    const uint8_t* own = rows + (r_own < 0 ? 0 : r_own) * a.row_stride;
-                    const uint8_t* other = rows + (r_other < 0 ? 0 : r_other) * a.row_stride;
+                    const int r = __shfl_sync(~0u, row, n * 8 + (lane >> 2));
 #pragma unroll
                     for (int c = 0; c < 9; ++c)
-                        v[c] = r_own >= 0 ? *reinterpret_cast<const uint4*>(own + c * 64 + ch * 16) : zero;
+                        v[n][c] = r >= 0 ? *reinterpret_cast<const uint4*>(rows + r * a.row_stride + c * 64 + ch * 16)
+                                         : make_uint4(0, 0, 0, 0);
+                }
+                if (jt >= 2) wait(tc::smem_addr(&x->sfull[stage]), ((jt - 2) >> 1) & 1, x, error);
+                x->scale[m][mine] = sc;
+                x->log_scale[m][mine] = __float2half(log2f(fabsf(sc)));
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const int tok = n * 8 + (lane >> 2), r0 = tok & 7;
+                    const uint32_t dst = k_smem + (16 * w + tok) * 128;
+#pragma unroll
+                    for (int c = 0; c < 9; ++c)
+                        store_wide<T>(v[n][c], dst + c * 4096, ((2 * ch) ^ r0) << 4, ((2 * ch + 1) ^ r0) << 4);
+                }
+            }
+            if (lane == 0) {
+                x->valid[m][rank][w] = (uint16_t)(ok_bits & 0xffff);
+                x->valid[m][1 - rank][w] = (uint16_t)(ok_bits >> 16);
+            }
+            tc::cp_async_commit();
+            tc::cp_async_wait<0>();
+            tc::fence_async_shared();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_cluster(full);
+        }
+        j += walk.t1 - walk.t0;
+    }
+}
+
+// Values: the latent channels of this CTA's half, of a tile's 64 rows.  Two warps
+// a stage, 32 rows each.  All four warps bring a piece's queries first.
+template <typename T, bool E4M3>
+__device__ void bring_values(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int* error)
+{
+    const hs_attend_t& a = g.a;
+    const int lane = threadIdx.x & 31, wg = (threadIdx.x >> 5) - 8;
+    const int stage = wg >> 1, w = wg & 1;
+    const uint32_t full = tc::map_to_rank(tc::smem_addr(&x->vfull[stage]), 0);
+    const uint32_t qfull = tc::map_to_rank(tc::smem_addr(&x->qfull), 0);
+    const uint32_t v_smem = sbase + kOffV + stage * kVBytes;
+    const int mine = 32 * w + lane;
+    const int block0 = 4 * (int)rank;  // the first of this CTA's blocks of 64 channels
+    long long j = 0;
+    Walk walk(g, x);
+    while (walk.next()) {
+        const uint8_t* rows = static_cast<const uint8_t*>(a.rows) + walk.b * a.request_stride;
+        const Lookup lookup(a, walk);
+        int t = walk.t0;
+        if ((j & 1) != stage) ++t;
+        int next = t < walk.t1 ? lookup(t, mine) : -1;
+        // Q's readers, the products of the earlier pieces' keys, are done.  (A parity tells two
+        // phases apart, so the tile before the last one is waited for first.)
+        if (j >= 2) wait(tc::smem_addr(&x->pvdone[j & 1]), ((j - 2) >> 1) & 1, x, error);
+        if (j >= 1) wait(tc::smem_addr(&x->sfull[(j - 1) & 1]), ((j - 1) >> 1) & 1, x, error);
+        const T* q = static_cast<const T*>(a.q) + walk.b * a.q_stride[0] + walk.p * a.q_stride[1];
+#pragma unroll 1
+        for (int n = 0; n < 4; ++n) {
+            const int r = 16 * wg + n * 4 + (lane >> 3);
+            const int head = walk.hb * 128 + (int)rank * 64 + r;
+            const bool ok = head < a.heads;
+            const uint8_t* src = reinterpret_cast<const uint8_t*>(q + (ok ? head : 0) * a.q_stride[2]) + (lane & 7) * 16;
+            const uint32_t dst = sbase + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
+#pragma unroll
+            for (int c = 0; c < 9; ++c) tc::cp_async16(dst + c * 8192, src + c * 128, ok);
+        }
+        tc::cp_async_commit();
+        tc::cp_async_wait<0>();
+        tc::fence_async_shared();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_cluster(qfull);
+        for (; t < walk.t1; t += 2) {
+            const long long jt = j + t - walk.t0;
+            const int row = next;
+            if (t + 2 < walk.t1) next = lookup(t + 2, mine);
+            if constexpr (!E4M3) {
+                if (jt >= 2) wait(tc::smem_addr(&x->pvdone[stage]), ((jt - 2) >> 1) & 1, x, error);
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    const int tok = n * 4 + (lane >> 3), ch = lane & 7;
+                    const int r = __shfl_sync(~0u, row, tok);
+                    const uint8_t* src = (r < 0 ? static_cast<const uint8_t*>(a.q) : rows + r * a.row_stride) + ch * 16 + block0 * 128;
+                    const uint32_t dst = v_smem + (32 * w + tok) * 128 + ((ch ^ (tok & 7)) << 4);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tc::cp_async16(dst + c * 8192, src + c * 128, r >= 0);
+                }
+            } else {
+                const int ch = lane & 3;
+                uint4 v[4][4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const int r = __shfl_sync(~0u, row, n * 8 + (lane >> 2));
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        v[9 + c] = r_other >= 0 ? *reinterpret_cast<const uint4*>(other + (block0 + c) * 64 + ch * 16) : zero;
-                    if (ch < 2) {
-                        const bool is_own = ch == 0;
-                        const int at = (is_own ? own0 : other0) + tok;
-                        const bool ok = is_own ? r_own >= 0 : r_other >= 0;
-                        const float sc = ok ? *reinterpret_cast<const float*>((is_own ? own : other) + HS_ROW8_SCALE) : 1.f;
-                        x->scale[stage][at] = sc;
-                        x->log_scale[stage][at] = log2f(fabsf(sc));
-                    }
-                    const int r0 = tok & 7, c0 = ((2 * ch) ^ r0) << 4, c1 = ((2 * ch + 1) ^ r0) << 4;
-                    const uint32_t kd = k_smem + (16 * w + tok) * 128;
+                        v[n][c] = r >= 0 ? *reinterpret_cast<const uint4*>(rows + r * a.row_stride + (block0 + c) * 64 + ch * 16)
+                                         : make_uint4(0, 0, 0, 0);
+                }
+                if (jt >= 2) wait(tc::smem_addr(&x->pvdone[stage]), ((jt - 2) >> 1) & 1, x, error);
 #pragma unroll
-                    for (int c = 0; c < 13; ++c) {
-                        uint32_t e[8];
-                        widen<T>(v[c].x, e[0], e[1]);
-                        widen<T>(v[c].y, e[2], e[3]);
-                        widen<T>(v[c].z, e[4], e[5]);
-                        widen<T>(v[c].w, e[6], e[7]);
-                        if (c < 9) {
-                            tc::st_shared16(kd + c * 4096 + c0, e[0], e[1], e[2], e[3]);
-                            tc::st_shared16(kd + c * 4096 + c1, e[4], e[5], e[6], e[7]);
-                            const int vb = c - block0;
-                            if (vb >= 0 && vb < 4) {
-                                const uint32_t vd = v_smem + vb * 8192 + (own0 + tok) * 128;
-                                tc::st_shared16(vd + c0, e[0], e[1], e[2], e[3]);
-                                tc::st_shared16(vd + c1, e[4], e[5], e[6], e[7]);
-                            }
-                        } else {
-                            const uint32_t vd = v_smem + (c - 9) * 8192 + (other0 + tok) * 128;
-                            tc::st_shared16(vd + c0, e[0], e[1], e[2], e[3]);
-                            tc::st_shared16(vd + c1, e[4], e[5], e[6], e[7]);
-                        }
-                    }
+                for (int n = 0; n < 4; ++n) {
+                    const int tok = n * 8 + (lane >> 2), r0 = tok & 7;
+                    const uint32_t dst = v_smem + (32 * w + tok) * 128;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        store_wide<T>(v[n][c], dst + c * 8192, ((2 * ch) ^ r0) << 4, ((2 * ch + 1) ^ r0) << 4);
                 }
             }
             tc::cp_async_commit();
@@ -312,66 +379,97 @@ __device__ void bring(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int*
             __syncwarp();
             if (lane == 0) tc::mbar_arrive_cluster(full);
         }
+        j += walk.t1 - walk.t0;
     }
 }
 
-// The products, issued by one thread of the pair's first CTA.
-template <typename T> __device__ void multiply(const Args& g, uint32_t sbase, Aux* x, int* error)
+// Q K^T of one tile into buffer S, and P V into O (the warp's elected lane).
+template <typename T, int S> __device__ __forceinline__ void issue_qk(uint32_t sbase, uint32_t tmem, Aux* x)
 {
-    constexpr bool bf = HsType<T>::is_bf16;
-    constexpr uint32_t d_qk = tc::inst_desc(bf, 128, kTile, false, false);
-    constexpr uint32_t d_pv = tc::inst_desc(bf, 128, 256, false, true);
-    const uint32_t tmem = x->tmem;
-    const uint64_t q_desc = tc::smem_desc(sbase, 16, 1024);
-    const long long n = x->count;
+    constexpr uint32_t id = tc::inst_desc(HsType<T>::is_bf16, 128, kTile, false, false);
+    const uint64_t q_desc = tc::smem_desc(sbase, 16, 1024), k_desc = tc::smem_desc(sbase + kOffK + S * kKBytes, 16, 1024);
+    if (tc::elect_one()) {
+#pragma unroll
+        for (int c = 0; c < 9; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                tc::mma_ss<2>(tmem + kColS + 32 * S, q_desc + ((c * 8192 + k * 32) >> 4), k_desc + ((c * 4096 + k * 32) >> 4),
+                              id, (c | k) != 0);
+        tc::commit<2>(tc::smem_addr(&x->sfull[S]));
+    }
+    __syncwarp();
+}
+template <typename T, int S> __device__ __forceinline__ void issue_pv(uint32_t sbase, uint32_t tmem, Aux* x, bool first)
+{
+    constexpr uint32_t id = tc::inst_desc(HsType<T>::is_bf16, 128, 256, false, true);
+    const uint64_t p_desc = tc::smem_desc(sbase + kOffP + S * kPBytes, 16, 1024);
+    const uint64_t v_desc = tc::smem_desc(sbase + kOffV + S * kVBytes, 8192, 1024);
+    if (tc::elect_one()) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                tc::mma_ss<2>(tmem + kColO + 128 * h, p_desc + ((k * 32) >> 4), v_desc + ((h * 16384 + k * 2048) >> 4), id,
+                              !(first && k == 0));
+        tc::commit<2>(tc::smem_addr(&x->pvdone[S]));
+    }
+    __syncwarp();
+}
+
+// After a wait that gave up: what was issued must be complete before tensor memory is freed.
+__device__ void drain(Aux* x, int which)
+{
+    if (!*(volatile int*)&x->dead) return;
+    if (tc::elect_one()) tc::commit<2>(tc::smem_addr(&x->spare[which]));
+    __syncwarp();
+    tc::mbar_wait(tc::smem_addr(&x->spare[which]), 0);
+}
+
+// The products are issued by two warps of the pair's first CTA, one for Q K^T and
+// one for P V: a warp does not get past products it has issued until they have
+// nearly run, and would bring the other product late.
+template <typename T> __device__ void multiply_qk(const Args& g, uint32_t sbase, Aux* x, int* error)
+{
+    const uint32_t tmem = __shfl_sync(~0u, x->tmem, 0);
+    long long j = 0;
+    int pieces = 0;
     Walk walk(g, x);
-    walk.next();
-    int piece_left = walk.t1 - walk.t0;
-    bool first = true;
-    long long qk = 0, pv = 0;
-    long long t0 = clock64();
-    while (pv < n) {
-        if (qk < n && qk <= pv + 1 && tc::mbar_test(tc::smem_addr(&x->full[qk & 1]), (qk >> 1) & 1)) {
-            const int s = qk & 1;
+    while (walk.next()) {
+        wait(tc::smem_addr(&x->qfull), pieces++ & 1, x, error);
+        for (int t = walk.t0; t < walk.t1; ++t, ++j) {
+            const int s = (int)(j & 1);
+            // S's buffer has been read
+            if (j >= 2) wait(tc::smem_addr(&x->pready[s]), ((j - 2) >> 1) & 1, x, error);
+            wait(tc::smem_addr(&x->kfull[s]), (j >> 1) & 1, x, error);
+            __syncwarp();
             tc::fence_after();
-            const uint64_t k_desc = tc::smem_desc(sbase + kOffK + s * kKBytes, 16, 1024);
-#pragma unroll
-            for (int c = 0; c < 9; ++c)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    tc::mma_ss<2>(tmem + kColS + 32 * s, q_desc + ((c * 8192 + k * 32) >> 4),
-                                  k_desc + ((c * 4096 + k * 32) >> 4), d_qk, (c | k) != 0);
-            tc::commit<2>(tc::smem_addr(&x->sfull[s]));
-            ++qk;
-            t0 = clock64();
-        } else if (pv < qk && tc::mbar_test(tc::smem_addr(&x->pready[pv & 1]), (pv >> 1) & 1)) {
-            const int s = pv & 1;
-            tc::fence_after();
-            const uint64_t p_desc = tc::smem_desc(sbase + kOffP + s * kPBytes, 16, 1024);
-            const uint64_t v_desc = tc::smem_desc(sbase + kOffV + s * kVBytes, 8192, 1024);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    tc::mma_ss<2>(tmem + kColO + 128 * h, p_desc + ((k * 32) >> 4),
-                                  v_desc + ((h * 16384 + k * 2048) >> 4), d_pv, !(first && k == 0));
-            tc::commit<2>(tc::smem_addr(&x->pvdone[s]));
-            first = false;
-            if (--piece_left == 0 && walk.next()) {
-                piece_left = walk.t1 - walk.t0;
-                first = true;
-            }
-            ++pv;
-            t0 = clock64();
-        } else if (*(volatile int*)&x->dead || clock64() - t0 > tc::kWaitClocks) {
-            *(volatile int*)&x->dead = 1;
-            if (error) atomicExch(error, 1);
-            // what was issued must be complete before tensor memory is freed
-            tc::commit<2>(tc::smem_addr(&x->spare));
-            tc::mbar_wait(tc::smem_addr(&x->spare), 0);
-            return;
+            if (s)
+                issue_qk<T, 1>(sbase, tmem, x);
+            else
+                issue_qk<T, 0>(sbase, tmem, x);
         }
     }
+    drain(x, 0);
+}
+template <typename T> __device__ void multiply_pv(const Args& g, uint32_t sbase, Aux* x, int* error)
+{
+    const uint32_t tmem = __shfl_sync(~0u, x->tmem, 0);
+    long long j = 0;
+    Walk walk(g, x);
+    while (walk.next()) {
+        for (int t = walk.t0; t < walk.t1; ++t, ++j) {
+            const int s = (int)(j & 1);
+            wait(tc::smem_addr(&x->vfull[s]), (j >> 1) & 1, x, error);
+            wait(tc::smem_addr(&x->pready[s]), (j >> 1) & 1, x, error);
+            __syncwarp();
+            tc::fence_after();
+            if (s)
+                issue_pv<T, 1>(sbase, tmem, x, t == walk.t0);
+            else
+                issue_pv<T, 0>(sbase, tmem, x, t == walk.t0);
+        }
+    }
+    drain(x, 1);
 }
 
 // Softmax of 64 heads: thread (head, half) takes 32 of a tile's 64 rows.
@@ -397,9 +495,9 @@ __device__ void soften(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int
             uint32_t r[32];
             tc::tmem_ld32(tmem + kColS + 32 * s, r);
             tc::tmem_wait_ld();
-            const uint32_t valid = reinterpret_cast<const uint32_t*>(x->valid[s])[half];
-            const float* wt = x->scale[s] + 32 * half;
-            const float* lw = x->log_scale[s] + 32 * half;
+            const uint32_t valid = reinterpret_cast<const uint32_t*>(x->valid[j & 3])[half];
+            const float* wt = x->scale[j & 3] + 32 * half;
+            const __half* lw = x->log_scale[j & 3] + 32 * half;
             float v[32], top = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -411,7 +509,7 @@ __device__ void soften(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int
                 for (int i = 0; i < 32; ++i)
                     if (!(valid >> i & 1)) v[i] = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) top = fmaxf(top, E4M3 ? v[i] + lw[i] : v[i]);
+            for (int i = 0; i < 32; ++i) top = fmaxf(top, E4M3 ? v[i] + __half2float(lw[i]) : v[i]);
             x->red[s][threadIdx.x] = top;
             asm volatile("bar.sync 1, 128;" ::: "memory");
             top = fmaxf(top, x->red[s][threadIdx.x ^ 64]);
@@ -527,7 +625,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_atte
     int* error = reinterpret_cast<int*>(ws);
 
     if (warp == 0) tc::tmem_alloc<2>(tc::smem_addr(&x->tmem), 512);
-    if (warp == 8) {
+    if (warp == 12) {
         // This pair's piece of the line of tiles.
         const int upr = a.positions * g.head_blocks;
         long long total, lo, hi, unit, tile;
@@ -588,12 +686,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_atte
                 st->tile = (int)tile;
             }
             for (int i = 0; i < 2; ++i) {
-                tc::mbar_init(tc::smem_addr(&x->full[i]), 4);
+                tc::mbar_init(tc::smem_addr(&x->kfull[i]), 4);
+                tc::mbar_init(tc::smem_addr(&x->vfull[i]), 4);
                 tc::mbar_init(tc::smem_addr(&x->sfull[i]), 1);
                 tc::mbar_init(tc::smem_addr(&x->pready[i]), 8);
                 tc::mbar_init(tc::smem_addr(&x->pvdone[i]), 1);
+                tc::mbar_init(tc::smem_addr(&x->spare[i]), 1);
             }
-            tc::mbar_init(tc::smem_addr(&x->spare), 1);
+            tc::mbar_init(tc::smem_addr(&x->qfull), 8);
             tc::mbar_init_fence();
         }
     }
@@ -607,9 +707,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_atte
         if (warp < 4)
             soften<T, E4M3>(g, sbase, x, rank, pair, ws, error);
         else if (warp < 8)
-            bring<T, E4M3>(g, sbase, x, rank, error);
-        else if (rank == 0 && lane == 0)
-            multiply<T>(g, sbase, x, error);
+            bring_keys<T, E4M3>(g, sbase, x, rank, error);
+        else if (warp < 12)
+            bring_values<T, E4M3>(g, sbase, x, rank, error);
+        else if (rank == 0 && warp == 12)
+            multiply_qk<T>(g, sbase, x, error);
+        else if (rank == 0)
+            multiply_pv<T>(g, sbase, x, error);
     }
     __syncwarp();
     tc::fence_before();
