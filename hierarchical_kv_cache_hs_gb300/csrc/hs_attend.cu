@@ -16,6 +16,8 @@
 // Work split: the tiles of all units (a unit: request, position, 128 heads) form
 // one line that is cut into equal pieces, one a pair; units cut in two leave
 // their sums in the workspace and a second kernel joins them.
+#include <type_traits>
+
 #include "hs_ops.h"
 #include "hs_tc.h"
 
@@ -45,8 +47,9 @@ struct Aux {
     int start_tile;
     // Per tile, four deep: a tile's keys arrive while the softmax two tiles back still reads these.
     uint16_t valid[4][2][2];  // [half][warp]: one bit a row
-    float scale[4][kTile];
+    alignas(16) float scale[4][kTile];
     __half log_scale[4][kTile];  // only moves the reference: its rounding cancels
+    int8_t q_up[2][64];          // power of two on a bf16 query held in fp16, by the parity of the piece
     float red[2][128];
 };
 constexpr int kSmem = kOffAux + (int)sizeof(Aux);
@@ -137,34 +140,13 @@ __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, Aux* x, int*
     }
 }
 
-// Four e4m3 values as two pairs of T.
-template <typename T> __device__ __forceinline__ void widen(uint32_t v, uint32_t& lo, uint32_t& hi);
-template <> __device__ __forceinline__ void widen<__half>(uint32_t v, uint32_t& lo, uint32_t& hi)
+// Four e4m3 values as two pairs of fp16, which holds each of them (and NaN).
+__device__ __forceinline__ void widen(uint32_t v, uint32_t& lo, uint32_t& hi)
 {
-    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v & 0xffff), __NV_E4M3);
-    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v >> 16), __NV_E4M3);
-    lo = a.x | (uint32_t)a.y << 16;
-    hi = b.x | (uint32_t)b.y << 16;
-}
-template <> __device__ __forceinline__ void widen<__nv_bfloat16>(uint32_t v, uint32_t& lo, uint32_t& hi)
-{
-    // An e4m3's exponent and mantissa bits, placed at a bf16's low exponent bits,
-    // are its value times 2^-120 (subnormals too); the product is exact.
-    auto half = [](uint32_t bytes) {
-        const uint32_t m = (bytes & 0x80008000u) | ((bytes & 0x7f007f00u) >> 4);
-        const __nv_bfloat162 big = __halves2bfloat162(__ushort_as_bfloat16(0x7B80), __ushort_as_bfloat16(0x7B80));
-        __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&m);
-        x = __hmul2(x, big);
-        return *reinterpret_cast<uint32_t*>(&x);
-    };
-    lo = half(__byte_perm(v, 0, 0x1404));
-    hi = half(__byte_perm(v, 0, 0x3424));
-    if (((v & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) {  // a NaN among them
-        if ((v & 0x7fu) == 0x7fu) lo |= 0x7fffu;
-        if ((v & 0x7f00u) == 0x7f00u) lo |= 0x7fff0000u;
-        if ((v & 0x7f0000u) == 0x7f0000u) hi |= 0x7fffu;
-        if ((v & 0x7f000000u) == 0x7f000000u) hi |= 0x7fff0000u;
-    }
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(v));
 }
 
 template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
@@ -200,14 +182,14 @@ struct Lookup {
     }
 };
 
-// 16 e4m3 values as two 16-byte pieces of T at dst + c0 and dst + c1.
-template <typename T> __device__ __forceinline__ void store_wide(const uint4& v, uint32_t dst, int c0, int c1)
+// 16 e4m3 values as two 16-byte pieces of fp16 at dst + c0 and dst + c1.
+__device__ __forceinline__ void store_wide(const uint4& v, uint32_t dst, int c0, int c1)
 {
     uint32_t e[8];
-    widen<T>(v.x, e[0], e[1]);
-    widen<T>(v.y, e[2], e[3]);
-    widen<T>(v.z, e[4], e[5]);
-    widen<T>(v.w, e[6], e[7]);
+    widen(v.x, e[0], e[1]);
+    widen(v.y, e[2], e[3]);
+    widen(v.z, e[4], e[5]);
+    widen(v.w, e[6], e[7]);
     tc::st_shared16(dst + c0, e[0], e[1], e[2], e[3]);
     tc::st_shared16(dst + c1, e[4], e[5], e[6], e[7]);
 }
@@ -259,7 +241,7 @@ __device__ void bring_keys(const Args& g, uint32_t sbase, Aux* x, uint32_t rank,
                     for (int c = 0; c < 9; ++c) tc::cp_async16(dst + c * 4096, src + c * 128, r >= 0);
                 }
             } else {
-                const float sc = row >= 0 ? *reinterpret_cast<const float*>(rows + row * a.row_stride + HS_ROW8_SCALE) : 1.f;
+                float sc = row >= 0 ? *reinterpret_cast<const float*>(rows + row * a.row_stride + HS_ROW8_SCALE) : 1.f;
                 const int ch = lane & 3;  // 16 channels of a block
                 uint4 v[2][9];
 #pragma unroll
@@ -279,7 +261,7 @@ __device__ void bring_keys(const Args& g, uint32_t sbase, Aux* x, uint32_t rank,
                     const uint32_t dst = k_smem + (16 * w + tok) * 128;
 #pragma unroll
                     for (int c = 0; c < 9; ++c)
-                        store_wide<T>(v[n][c], dst + c * 4096, ((2 * ch) ^ r0) << 4, ((2 * ch + 1) ^ r0) << 4);
+                        store_wide(v[n][c], dst + c * 4096, ((2 * ch) ^ r0) << 4, ((2 * ch + 1) ^ r0) << 4);
                 }
             }
             if (lane == 0) {
@@ -311,7 +293,7 @@ __device__ void bring_values(const Args& g, uint32_t sbase, Aux* x, uint32_t ran
     const int block0 = 4 * (int)rank;  // the first of this CTA's blocks of 64 channels
     long long j = 0;
     Walk walk(g, x);
-    while (walk.next()) {
+    for (int pieces = 0; walk.next(); ++pieces) {
         const uint8_t* rows = static_cast<const uint8_t*>(a.rows) + walk.b * a.request_stride;
         const Lookup lookup(a, walk);
         int t = walk.t0;
@@ -329,8 +311,37 @@ __device__ void bring_values(const Args& g, uint32_t sbase, Aux* x, uint32_t ran
             const bool ok = head < a.heads;
             const uint8_t* src = reinterpret_cast<const uint8_t*>(q + (ok ? head : 0) * a.q_stride[2]) + (lane & 7) * 16;
             const uint32_t dst = sbase + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
+            if constexpr (E4M3 && HsType<T>::is_bf16) {
+                // The products are in fp16 (which holds e4m3): the head's query is scaled by a power of two
+                // that takes its largest magnitude to [2^13, 2^14); what is 2^-28 of it or more stays exact.
+                uint4 v[9];
+                float top = 0.f;
 #pragma unroll
-            for (int c = 0; c < 9; ++c) tc::cp_async16(dst + c * 8192, src + c * 128, ok);
+                for (int c = 0; c < 9; ++c) {
+                    v[c] = ok ? *reinterpret_cast<const uint4*>(src + c * 128) : make_uint4(0, 0, 0, 0);
+                    const __nv_bfloat162* e = reinterpret_cast<const __nv_bfloat162*>(&v[c]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(__low2float(e[i])), fabsf(__high2float(e[i]))));
+                }
+                for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+                // 2^(13 - exponent), kept for the scores; zeros and infinities stay as they are
+                const int ex = (int)(__float_as_uint(top) >> 23);
+                const bool plain = ex == 0 || ex == 255;
+                const int up = plain ? 0 : min(max(140 - ex, -100), 100);
+                const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+                if ((lane & 7) == 0) x->q_up[pieces & 1][r] = (int8_t)up;
+#pragma unroll
+                for (int c = 0; c < 9; ++c) {
+                    const __nv_bfloat162* e = reinterpret_cast<const __nv_bfloat162*>(&v[c]);
+                    uint32_t h[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) h[i] = pack2<__half>(__low2float(e[i]) * f, __high2float(e[i]) * f);
+                    tc::st_shared16(dst + c * 8192, h[0], h[1], h[2], h[3]);
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < 9; ++c) tc::cp_async16(dst + c * 8192, src + c * 128, ok);
+            }
         }
         tc::cp_async_commit();
         tc::cp_async_wait<0>();
@@ -370,7 +381,7 @@ __device__ void bring_values(const Args& g, uint32_t sbase, Aux* x, uint32_t ran
                     const uint32_t dst = v_smem + (32 * w + tok) * 128;
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        store_wide<T>(v[n][c], dst + c * 8192, ((2 * ch) ^ r0) << 4, ((2 * ch + 1) ^ r0) << 4);
+                        store_wide(v[n][c], dst + c * 8192, ((2 * ch) ^ r0) << 4, ((2 * ch + 1) ^ r0) << 4);
                 }
             }
             tc::cp_async_commit();
@@ -480,12 +491,12 @@ __device__ void soften(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = threadIdx.x & 63, half = threadIdx.x >> 6;
     const uint32_t tmem = x->tmem + ((uint32_t)warp << 21);  // this warp's 32 lanes
-    const float c = a.scale * 1.4426950408889634f;
+    float c = a.scale * 1.4426950408889634f;
     long long j = 0;
     Walk walk(g, x);
     const uint32_t pready[2] = {tc::map_to_rank(tc::smem_addr(&x->pready[0]), 0),
                                 tc::map_to_rank(tc::smem_addr(&x->pready[1]), 0)};
-    while (walk.next()) {
+    for (int pieces = 0; walk.next(); ++pieces) {
         float ref = 0.f, sum = 0.f;
         bool seen = false;  // a row that counts has been met: ref is a maximum
         for (int t = walk.t0; t < walk.t1; ++t, ++j) {
@@ -495,6 +506,9 @@ __device__ void soften(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int
             uint32_t r[32];
             tc::tmem_ld32(tmem + kColS + 32 * s, r);
             tc::tmem_wait_ld();
+            if constexpr (E4M3 && HsType<T>::is_bf16)
+                if (t == walk.t0)
+                    c = __uint_as_float((uint32_t)(127 - x->q_up[pieces & 1][row]) << 23) * (a.scale * 1.4426950408889634f);
             const uint32_t valid = reinterpret_cast<const uint32_t*>(x->valid[j & 3])[half];
             const float* wt = x->scale[j & 3] + 32 * half;
             const __half* lw = x->log_scale[j & 3] + 32 * half;
@@ -550,7 +564,7 @@ __device__ void soften(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int
                         p0 *= wt[k];
                         p1 *= wt[k + 1];
                     }
-                    e[i] = pack2<T>(p0, p1);
+                    e[i] = pack2<std::conditional_t<E4M3, __half, T>>(p0, p1);
                 }
                 tc::st_shared16(dst + (((half * 4 + n) ^ (row & 7)) << 4), e[0], e[1], e[2], e[3]);
             }
@@ -614,6 +628,7 @@ __device__ void soften(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int
 template <typename T, bool E4M3>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_attend_kernel(const __grid_constant__ Args g)
 {
+    using Operand = std::conditional_t<E4M3, __half, T>;
     extern __shared__ __align__(1024) uint8_t base[];  // the swizzled tiles need 1024
     const uint32_t sbase = tc::smem_addr(base);
     Aux* x = reinterpret_cast<Aux*>(base + kOffAux);
@@ -624,6 +639,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_atte
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     int* error = reinterpret_cast<int*>(ws);
 
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may queue up behind this grid
     if (warp == 0) tc::tmem_alloc<2>(tc::smem_addr(&x->tmem), 512);
     if (warp == 12) {
         // This pair's piece of the line of tiles.
@@ -711,9 +727,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_atte
         else if (warp < 12)
             bring_values<T, E4M3>(g, sbase, x, rank, error);
         else if (rank == 0 && warp == 12)
-            multiply_qk<T>(g, sbase, x, error);
+            multiply_qk<Operand>(g, sbase, x, error);
         else if (rank == 0)
-            multiply_pv<T>(g, sbase, x, error);
+            multiply_pv<Operand>(g, sbase, x, error);
     }
     __syncwarp();
     tc::fence_before();
@@ -724,46 +740,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_atte
 }
 
 // Join the pieces of a unit that several pairs worked on: block i takes the unit
-// cut first at the start of pair i + 1's piece.
-template <typename T> __global__ void __launch_bounds__(128) hs_attend_join_kernel(const __grid_constant__ Args g, int pairs)
+// cut first at the start of pair i + 1's piece, one CTA's half, 16 columns.  Four
+// groups of 128 threads (one a lane) take every fourth piece; the order of the
+// sums is fixed.
+constexpr int kJoinCols = 16;
+template <typename T> __global__ void __launch_bounds__(512) hs_attend_join_kernel(const __grid_constant__ Args g, int pairs)
 {
+    __shared__ float tops[4][128], sums[4][128], cols[3][kJoinCols][128];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const hs_attend_t& a = g.a;
     const uint8_t* ws = static_cast<const uint8_t*>(a.workspace);
     const Start* start = reinterpret_cast<const Start*>(ws + kOffStart);
     const Partial* parts = reinterpret_cast<const Partial*>(ws + kOffPartial);
-    const int i = blockIdx.x + 1, rank = blockIdx.y, c0 = 32 * blockIdx.z;
+    const int i = blockIdx.x + 1, rank = blockIdx.y, c0 = kJoinCols * blockIdx.z;
     const long long unit = start[i].unit;
     if (unit < 0 || start[i].tile == 0) return;
-    if (i > 1 && start[i - 1].unit == unit && start[i - 1].tile > 0) return;
-    int last = i;
-    while (last + 1 < pairs && start[last + 1].unit == unit && start[last + 1].tile > 0) ++last;
+    // pair i - 1 holds the unit's first piece, pairs i..last the others
+    const int n = threadIdx.x;
+    const bool of_unit = n < pairs && start[n].unit == unit && start[n].tile > 0;
+    if (__syncthreads_or(of_unit && n < i)) return;
+    const int last = i - 1 + __syncthreads_count(of_unit);
     const int upr = a.positions * g.head_blocks;
     const long long b = unit / upr;
     const int rem = (int)(unit - b * upr), p = rem / g.head_blocks, hb = rem - p * g.head_blocks;
-    const int lane = threadIdx.x, row = lane & 63, half = lane >> 6;
+    const int lane = threadIdx.x & 127, group = threadIdx.x >> 7, row = lane & 63, half = lane >> 6;
     const int head = hb * 128 + rank * 64 + row;
-    if (head >= a.heads) return;
+    if (hb * 128 + rank * 64 >= a.heads) return;
+    const bool live = head < a.heads;
     float top = -INFINITY;
-    for (int n = i - 1; n <= last; ++n) {
-        const Partial& q = parts[2 * n + (n == i - 1)];
-        if (q.sum[rank][lane] != 0.f) top = fmaxf(top, q.ref[rank][lane]);
-    }
-    float acc[32] = {}, sum = 0.f;
-    for (int n = i - 1; n <= last; ++n) {
-        const Partial& q = parts[2 * n + (n == i - 1)];
-        const float l = q.sum[rank][lane];
-        if (l == 0.f) continue;
-        const float w = tc::exp2_approx(q.ref[rank][lane] - top);
-        sum += w * l;
+    if (live)
+#pragma unroll 4
+        for (int n = i - 1 + group; n <= last; n += 4) {
+            const Partial& q = parts[2 * n + (n == i - 1)];
+            const float ref = q.ref[rank][lane];
+            if (q.sum[rank][lane] != 0.f) top = fmaxf(top, ref);
+        }
+    tops[group][lane] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(tops[0][lane], tops[1][lane]), fmaxf(tops[2][lane], tops[3][lane]));
+    float acc[kJoinCols] = {}, sum = 0.f;
+    if (live)
+#pragma unroll 2
+        for (int n = i - 1 + group; n <= last; n += 4) {
+            const Partial& q = parts[2 * n + (n == i - 1)];
+            const float l = q.sum[rank][lane];
+            const float w = l == 0.f ? 0.f : tc::exp2_approx(q.ref[rank][lane] - top);
+            sum += w * l;
 #pragma unroll
-        for (int k = 0; k < 32; ++k) acc[k] += w * q.o[rank][c0 + k][lane];
-    }
+            for (int k = 0; k < kJoinCols; ++k) acc[k] += w * q.o[rank][c0 + k][lane];
+        }
+    sums[group][lane] = sum;
+    if (group)
+#pragma unroll
+        for (int k = 0; k < kJoinCols; ++k) cols[group - 1][k][lane] = acc[k];
+    __syncthreads();
+    if (group || !live) return;
+    sum = sums[0][lane] + sums[1][lane] + sums[2][lane] + sums[3][lane];
+#pragma unroll
+    for (int k = 0; k < kJoinCols; ++k) acc[k] += cols[0][k][lane] + cols[1][k][lane] + cols[2][k][lane];
     const bool some = sum > 0.f || sum != sum;
     const float inv = some ? 1.f / sum : 0.f;
     T* out = static_cast<T*>(a.out) + b * a.out_stride[0] + p * a.out_stride[1] + (int64_t)head * a.out_stride[2] +
              256 * half + c0;
 #pragma unroll
-    for (int k = 0; k < 32; k += 8) {
+    for (int k = 0; k < kJoinCols; k += 8) {
         uint4 e;
         e.x = pack2<T>(acc[k] * inv, acc[k + 1] * inv);
         e.y = pack2<T>(acc[k + 2] * inv, acc[k + 3] * inv);
@@ -787,8 +827,18 @@ template <typename T, bool E4M3> cudaError_t launch(const Args& g, int pairs, cu
     cudaError_t e = cudaFuncSetAttribute(hs_attend_kernel<T, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     hs_attend_kernel<T, E4M3><<<2 * pairs, kThreads, kSmem, s>>>(g);
-    if (g.flat && pairs > 1) hs_attend_join_kernel<T><<<dim3(pairs - 1, 2, 8), 128, 0, s>>>(g, pairs);
-    return cudaGetLastError();
+    e = cudaGetLastError();
+    if (e != cudaSuccess || !g.flat || pairs <= 1) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(pairs - 1, g.a.heads > 64 ? 2 : 1, 256 / kJoinCols);
+    cfg.blockDim = 512;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, hs_attend_join_kernel<T>, g, pairs);
 }
 
 }  // namespace
