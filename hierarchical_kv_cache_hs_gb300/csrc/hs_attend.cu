@@ -739,78 +739,95 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_atte
     if (warp == 0) tc::tmem_free<2>(x->tmem, 512);
 }
 
-// Join the pieces of a unit that several pairs worked on: block i takes the unit
-// cut first at the start of pair i + 1's piece, one CTA's half, 16 columns.  Four
-// groups of 128 threads (one a lane) take every fourth piece; the order of the
-// sums is fixed.
-constexpr int kJoinCols = 16;
-template <typename T> __global__ void __launch_bounds__(512) hs_attend_join_kernel(const __grid_constant__ Args g, int pairs)
+// Join the pieces of the units that several pairs worked on: block x takes the
+// x-th such unit (found at the first start of a piece inside it), one CTA's half
+// of its heads, COLS columns.  Four groups of 128 threads, one a lane, take every
+// fourth piece, in one pass; the order of the sums is fixed.
+template <typename T, int COLS>
+__global__ void __launch_bounds__(512) hs_attend_join_kernel(const __grid_constant__ Args g, int pairs)
 {
-    __shared__ float tops[4][128], sums[4][128], cols[3][kJoinCols][128];
+    __shared__ float tops[4][128], sums[4][128], cols[3][COLS][128];
+    __shared__ int counts[4], first_cut, last_cut;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const hs_attend_t& a = g.a;
     const uint8_t* ws = static_cast<const uint8_t*>(a.workspace);
-    const Start* start = reinterpret_cast<const Start*>(ws + kOffStart);
     const Partial* parts = reinterpret_cast<const Partial*>(ws + kOffPartial);
-    const int i = blockIdx.x + 1, rank = blockIdx.y, c0 = kJoinCols * blockIdx.z;
-    const long long unit = start[i].unit;
-    if (unit < 0 || start[i].tile == 0) return;
-    // pair i - 1 holds the unit's first piece, pairs i..last the others
-    const int n = threadIdx.x;
-    const bool of_unit = n < pairs && start[n].unit == unit && start[n].tile > 0;
-    if (__syncthreads_or(of_unit && n < i)) return;
-    const int last = i - 1 + __syncthreads_count(of_unit);
+    const int t = threadIdx.x;
+    if (t == 0) first_cut = 0;
+    long long my_unit = -1;
+    bool inside = false, cut = false;  // pair t begins inside a unit; the first to
+    if (t < 128) {
+        const Start* start = reinterpret_cast<const Start*>(ws + kOffStart);
+        if (t > 0 && t < pairs) {
+            my_unit = start[t].unit;
+            inside = my_unit >= 0 && start[t].tile > 0;
+            cut = inside && !(start[t - 1].unit == my_unit && start[t - 1].tile > 0);
+        }
+        const unsigned m = __ballot_sync(~0u, cut);
+        if ((t & 31) == 0) counts[t >> 5] = __popc(m);
+    }
+    __syncthreads();
+    if (t < 128) {
+        int before = __popc(__ballot_sync(~0u, cut) & ((1u << (t & 31)) - 1));
+        for (int w = 0; w < t >> 5; ++w) before += counts[w];
+        if (cut && before == (int)blockIdx.x) first_cut = t;
+    }
+    __syncthreads();
+    if (first_cut == 0) return;
+    const long long unit = reinterpret_cast<const Start*>(ws + kOffStart)[first_cut].unit;
+    const int first = first_cut - 1, last = first + __syncthreads_count(inside && my_unit == unit);
+    const int rank = blockIdx.y, c0 = COLS * blockIdx.z;
+    const int lane = t & 127, group = t >> 7, row = lane & 63, half = lane >> 6;
     const int upr = a.positions * g.head_blocks;
     const long long b = unit / upr;
     const int rem = (int)(unit - b * upr), p = rem / g.head_blocks, hb = rem - p * g.head_blocks;
-    const int lane = threadIdx.x & 127, group = threadIdx.x >> 7, row = lane & 63, half = lane >> 6;
     const int head = hb * 128 + rank * 64 + row;
     if (hb * 128 + rank * 64 >= a.heads) return;
     const bool live = head < a.heads;
-    float top = -INFINITY;
+    float acc[COLS] = {}, sum = 0.f, top = -INFINITY;
     if (live)
 #pragma unroll 4
-        for (int n = i - 1 + group; n <= last; n += 4) {
-            const Partial& q = parts[2 * n + (n == i - 1)];
-            const float ref = q.ref[rank][lane];
-            if (q.sum[rank][lane] != 0.f) top = fmaxf(top, ref);
+        for (int n = first + group; n <= last; n += 4) {
+            const Partial& q = parts[2 * n + (n == first)];
+            const float ref = q.ref[rank][lane], l = q.sum[rank][lane];
+            float o[COLS];
+#pragma unroll
+            for (int k = 0; k < COLS; ++k) o[k] = q.o[rank][c0 + k][lane];
+            if (l == 0.f) continue;  // no row counted
+            const float up = fmaxf(top, ref);
+            const float keep = tc::exp2_approx(top - up), w = tc::exp2_approx(ref - up);
+            top = up;
+            sum = sum * keep + w * l;
+#pragma unroll
+            for (int k = 0; k < COLS; ++k) acc[k] = acc[k] * keep + w * o[k];
         }
     tops[group][lane] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(tops[0][lane], tops[1][lane]), fmaxf(tops[2][lane], tops[3][lane]));
-    float acc[kJoinCols] = {}, sum = 0.f;
-    if (live)
-#pragma unroll 2
-        for (int n = i - 1 + group; n <= last; n += 4) {
-            const Partial& q = parts[2 * n + (n == i - 1)];
-            const float l = q.sum[rank][lane];
-            const float w = l == 0.f ? 0.f : tc::exp2_approx(q.ref[rank][lane] - top);
-            sum += w * l;
-#pragma unroll
-            for (int k = 0; k < kJoinCols; ++k) acc[k] += w * q.o[rank][c0 + k][lane];
-        }
     sums[group][lane] = sum;
     if (group)
 #pragma unroll
-        for (int k = 0; k < kJoinCols; ++k) cols[group - 1][k][lane] = acc[k];
+        for (int k = 0; k < COLS; ++k) cols[group - 1][k][lane] = acc[k];
     __syncthreads();
     if (group || !live) return;
-    sum = sums[0][lane] + sums[1][lane] + sums[2][lane] + sums[3][lane];
+    top = fmaxf(fmaxf(tops[0][lane], tops[1][lane]), fmaxf(tops[2][lane], tops[3][lane]));
+    const float base = top == -INFINITY ? 0.f : top;
+    float w = tc::exp2_approx(tops[0][lane] - base);
+    sum *= w;
 #pragma unroll
-    for (int k = 0; k < kJoinCols; ++k) acc[k] += cols[0][k][lane] + cols[1][k][lane] + cols[2][k][lane];
+    for (int k = 0; k < COLS; ++k) acc[k] *= w;
+    for (int n = 1; n < 4; ++n) {
+        w = tc::exp2_approx(tops[n][lane] - base);
+        sum += w * sums[n][lane];
+#pragma unroll
+        for (int k = 0; k < COLS; ++k) acc[k] += w * cols[n - 1][k][lane];
+    }
     const bool some = sum > 0.f || sum != sum;
     const float inv = some ? 1.f / sum : 0.f;
     T* out = static_cast<T*>(a.out) + b * a.out_stride[0] + p * a.out_stride[1] + (int64_t)head * a.out_stride[2] +
              256 * half + c0;
 #pragma unroll
-    for (int k = 0; k < kJoinCols; k += 8) {
-        uint4 e;
-        e.x = pack2<T>(acc[k] * inv, acc[k + 1] * inv);
-        e.y = pack2<T>(acc[k + 2] * inv, acc[k + 3] * inv);
-        e.z = pack2<T>(acc[k + 4] * inv, acc[k + 5] * inv);
-        e.w = pack2<T>(acc[k + 6] * inv, acc[k + 7] * inv);
-        *reinterpret_cast<uint4*>(out + k) = e;
-    }
+    for (int k = 0; k < COLS; k += 4)
+        *reinterpret_cast<uint2*>(out + k) =
+            make_uint2(pack2<T>(acc[k] * inv, acc[k + 1] * inv), pack2<T>(acc[k + 2] * inv, acc[k + 3] * inv));
     if (a.lse && half == 0 && c0 == 0)
         a.lse[(b * a.positions + p) * a.heads + head] = some ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
@@ -830,7 +847,10 @@ template <typename T, bool E4M3> cudaError_t launch(const Args& g, int pairs, cu
     e = cudaGetLastError();
     if (e != cudaSuccess || !g.flat || pairs <= 1) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(pairs - 1, g.a.heads > 64 ? 2 : 1, 256 / kJoinCols);
+    // At most this many units are cut; few units take more blocks each, by narrower columns.
+    const int cut = (int)(g.units < pairs - 1 ? g.units : pairs - 1);
+    const int cols = cut * (g.a.heads > 64 ? 2 : 1) <= 8 ? 4 : 16;
+    cfg.gridDim = dim3(cut, g.a.heads > 64 ? 2 : 1, 256 / cols);
     cfg.blockDim = 512;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -838,7 +858,7 @@ template <typename T, bool E4M3> cudaError_t launch(const Args& g, int pairs, cu
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, hs_attend_join_kernel<T>, g, pairs);
+    return cudaLaunchKernelEx(&cfg, cols == 4 ? hs_attend_join_kernel<T, 4> : hs_attend_join_kernel<T, 16>, g, pairs);
 }
 
 }  // namespace
