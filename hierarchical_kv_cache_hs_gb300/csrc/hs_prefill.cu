@@ -1,119 +1,914 @@
-// hs_latent_prefill: expanded latent attention of ragged prompts.
+// hs_latent_prefill: expanded latent attention of ragged prompts, causal.
 //
-// Two launches.  The first expands the rows: keys and values of every head
-// (k_j = w_uk latent_j, v_j = w_uv latent_j) into the workspace.  The second
-// is the attention: a warp per (query, head) that walks its request's keys.
+// Three launches.
+// (1) Expansion: keys and values of every head, [k; v] = [w_uk; w_uv] latent, a
+//     product of k_tokens x 256 heads x 512.  A pair of SMs (cta_group::2, M = N =
+//     256) keeps 256 tokens' latents in shared memory and runs through heads; the
+//     weights' half that each CTA brings serves both.
+// (2) Attention: one SM takes 256 queries of a head as two tiles of 128 that take
+//     turns: while one tile's scores are softened, the other's products run.  The
+//     scores (then the weights, in place) and the sums of both tiles fill tensor
+//     memory; keys (192 channels) and values pass through shared memory in blocks
+//     of 128.
+// (3) Join: the blocks of all units (head, 256 queries) form one line that is cut
+//     into equal pieces, one an SM; units cut in two or more are joined.
+#include <type_traits>
+
 #include "hs_ops.h"
+#include "hs_tc.h"
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kTokens = 8;  // rows a CTA of the expansion takes
+constexpr int kMaxCtas = 152;
 
-// Workspace: keys [k_tokens][heads][128], then values [k_tokens][heads][128].
-template <typename T, bool E4M3>
-__global__ void __launch_bounds__(2 * HS_HEAD_DIM) hs_expand_kernel(hs_prefill_t a)
+// Workspace: an error word, where each CTA's piece starts, two partial results a
+// CTA, keys [heads][k_tokens][128], values likewise, rotary channels [k_tokens][64]
+// (of 8-bit rows).
+struct Start {
+    int b, h, qt, kb;
+};
+struct Partial {
+    float o[2][128][128];  // [tile][channel][query]
+    float ref[2][128], sum[2][128];
+};
+constexpr size_t kOffStart = 256;
+constexpr size_t kOffPartial = kOffStart + sizeof(Start) * kMaxCtas;
+constexpr size_t kOffKeys = kOffPartial + sizeof(Partial) * 2 * kMaxCtas;
+
+struct Args {
+    hs_prefill_t a;
+    uint8_t* keys;
+    uint8_t* values;
+    const uint8_t* rope;  // 64 channels a token
+    int64_t rope_stride;  // bytes
+    uint8_t* rope_out;    // where the expansion writes them, or NULL
+};
+
+template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b)
 {
-    __shared__ float lat[kTokens][HS_LATENT_DIM];
-    const int64_t t0 = (int64_t)blockIdx.x * kTokens;
-    const int head = blockIdx.y;
-    for (int i = threadIdx.x; i < kTokens * HS_LATENT_DIM; i += blockDim.x) {
-        const int t = i / HS_LATENT_DIM, c = i % HS_LATENT_DIM;
-        float v = 0.f;
-        if (t0 + t < a.k_tokens) {
-            const uint8_t* row = static_cast<const uint8_t*>(a.rows) + (t0 + t) * a.row_stride;
-            v = E4M3 ? hs_e4m3_to_float(row[c]) * *reinterpret_cast<const float*>(row + HS_ROW8_SCALE)
-                     : HsType<T>::to_float(reinterpret_cast<const T*>(row)[c]);
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b)
+{
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+// A NaN or an infinity among two values of T.
+template <typename T> __device__ __forceinline__ bool not_finite(uint32_t v)
+{
+    const uint32_t m = HsType<T>::is_bf16 ? 0x7f80u : 0x7c00u;
+    return (v & m) == m || (v >> 16 & m) == m;
+}
+// Two e4m3 values as T (exact).
+template <typename T> __device__ __forceinline__ uint32_t widen2(uint32_t v)
+{
+    uint32_t h;
+    asm("{\n\t.reg .b16 a;\n\tcvt.u16.u32 a, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(h) : "r"(v));
+    if constexpr (!HsType<T>::is_bf16) return h;
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    return pack2<T>(f.x, f.y);
+}
+
+// Bounded wait: on a timeout the CTA is marked dead and every later wait returns at once.
+__device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, int* dead, int* error)
+{
+    if (tc::mbar_try(bar, parity)) return;
+    const long long t0 = clock64();
+    while (!tc::mbar_try(bar, parity)) {
+        if (*(volatile int*)dead) return;
+        if (clock64() - t0 > tc::kWaitClocks) {
+            *(volatile int*)dead = 1;
+            atomicExch(error, 1);
+            return;
         }
-        lat[t][c] = v;
+    }
+}
+
+// ---- (1) expansion -----------------------------------------------------------------
+
+constexpr int kEStages = 4;
+constexpr int kEThreads = 9 * 32;  // warps 0-3 write, 4-7 bring (one a stage), 8 issues the products
+constexpr int kEOffB = 8 * 16384;  // latents: 8 blocks of 64 channels, [128 tokens][128 B]
+constexpr int kEOffAux = kEOffB + kEStages * 16384;
+struct EAux {
+    uint64_t afull, bfull[kEStages], bfree[kEStages], dfull[2], dfree[2], spare;
+    uint32_t tmem;
+    int dead;
+};
+constexpr int kESmem = kEOffAux + (int)sizeof(EAux);
+
+template <typename T, bool E4M3>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kEThreads, 1) hs_expand_kernel(const __grid_constant__ Args g)
+{
+    extern __shared__ __align__(1024) uint8_t base[];
+    const uint32_t sbase = tc::smem_addr(base);
+    EAux* x = reinterpret_cast<EAux*>(base + kEOffAux);
+    const hs_prefill_t& a = g.a;
+    const uint32_t rank = tc::cluster_rank();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int* error = static_cast<int*>(a.workspace);
+    // This pair's piece of the line of jobs (256 tokens, head).
+    const int64_t jobs = (a.k_tokens + 255) / 256 * a.heads;
+    const int64_t pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+    const int64_t lo = jobs * pair / pairs, hi = jobs * (pair + 1) / pairs;
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == 0) tc::tmem_alloc<2>(tc::smem_addr(&x->tmem), 512);
+    if (threadIdx.x == 0) {
+        x->dead = 0;
+        tc::mbar_init(tc::smem_addr(&x->afull), 8);
+        for (int i = 0; i < kEStages; ++i) {
+            tc::mbar_init(tc::smem_addr(&x->bfull[i]), 2);
+            tc::mbar_init(tc::smem_addr(&x->bfree[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(tc::smem_addr(&x->dfull[i]), 1);
+            tc::mbar_init(tc::smem_addr(&x->dfree[i]), 8);
+        }
+        tc::mbar_init(tc::smem_addr(&x->spare), 1);
+        tc::mbar_init_fence();
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::cluster_sync();
+    tc::fence_after();
+
+    if (warp < 4) {
+        // A token a thread: values first (a value that is not finite becomes 0 and its key NaN: a weight
+        // of 0 must hide it from the queries that do not see it, and the others must get NaN).
+        const uint32_t tmem = x->tmem + ((uint32_t)warp << 21);
+        const uint32_t dfree[2] = {tc::map_to_rank(tc::smem_addr(&x->dfree[0]), 0),
+                                   tc::map_to_rank(tc::smem_addr(&x->dfree[1]), 0)};
+        for (int64_t job = lo; job < hi; ++job) {
+            const int n = (int)(job - lo), d = n & 1;
+            const int64_t mt = job / a.heads, h = job - mt * a.heads;
+            const int64_t token = mt * 256 + 128 * (int)rank + threadIdx.x;
+            const bool live = token < a.k_tokens;
+            float scale = 1.f;
+            if (E4M3 && live)
+                scale = *reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.rows) + token * a.row_stride + HS_ROW8_SCALE);
+            wait(tc::smem_addr(&x->dfull[d]), (n >> 1) & 1, &x->dead, error);
+            tc::fence_after();
+            bool bad = false;
+#pragma unroll 1
+            for (int c = 7; c >= 0; --c) {
+                uint32_t r[32], e[16];
+                __syncwarp();
+                tc::tmem_ld32(tmem + 256 * d + c * 32, r);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float p = __uint_as_float(r[2 * i]), q = __uint_as_float(r[2 * i + 1]);
+                    if (E4M3) p *= scale, q *= scale;
+                    e[i] = pack2<T>(p, q);
+                }
+                if (c >= 4) {  // columns 128-255: values
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (not_finite<T>(e[i])) bad = true, e[i] = 0;
+                } else if (bad) {
+                    e[0] = ~0u;
+                }
+                if (live) {
+                    uint8_t* dst = (c >= 4 ? g.values : g.keys) + ((h * a.k_tokens + token) * HS_HEAD_DIM + (c & 3) * 32) * 2;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<uint4*>(dst + 16 * i) = make_uint4(e[4 * i], e[4 * i + 1], e[4 * i + 2], e[4 * i + 3]);
+                }
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_cluster(dfree[d]);
+        }
+    } else if (warp < 8) {
+        const int s = warp - 4;
+        const uint32_t bfull = tc::map_to_rank(tc::smem_addr(&x->bfull[s]), 0);
+        const uint32_t afull = tc::map_to_rank(tc::smem_addr(&x->afull), 0);
+        const uint8_t* w = static_cast<const uint8_t*>(rank ? a.w_uv : a.w_uk);
+        const int ch = lane & 7;
+        int fills = 0;  // of this warp's stage
+        int64_t at = -1;
+        for (int64_t job = lo; job < hi; ++job) {
+            const int64_t mt = job / a.heads, h = job - mt * a.heads;
+            if (mt != at) {
+                // The earlier tokens' products are done: each stage's last one is (the four warps' arrivals
+                // make up the barrier, and each has waited for its own stage).
+                if (fills) wait(tc::smem_addr(&x->bfree[s]), (fills - 1) & 1, &x->dead, error);
+                asm volatile("bar.sync 2, 128;" ::: "memory");
+                at = mt;
+                for (int kb = 2 * s; kb < 2 * s + 2; ++kb) {
+#pragma unroll 4
+                    for (int n = 0; n < 32; ++n) {
+                        const int r = n * 4 + (lane >> 3);
+                        const int64_t token = mt * 256 + 128 * (int)rank + r;
+                        const bool live = token < a.k_tokens;
+                        const uint8_t* src = static_cast<const uint8_t*>(a.rows) + (live ? token : 0) * a.row_stride;
+                        const uint32_t dst = sbase + kb * 16384 + r * 128 + ((ch ^ (r & 7)) << 4);
+                        if constexpr (!E4M3) {
+                            tc::cp_async16(dst, src + kb * 128 + ch * 16, live);
+                        } else {
+                            const uint2 v = live ? *reinterpret_cast<const uint2*>(src + kb * 64 + ch * 8) : make_uint2(0, 0);
+                            tc::st_shared16(dst, widen2<T>(v.x & 0xffff), widen2<T>(v.x >> 16), widen2<T>(v.y & 0xffff),
+                                            widen2<T>(v.y >> 16));
+                        }
+                    }
+                }
+                if (E4M3 && h == 0) {  // the rotary channels of 8-bit rows, rounded to T
+                    for (int i = 32 * s + lane; i < 128 * 8; i += 128) {
+                        const int64_t token = mt * 256 + 128 * (int)rank + (i >> 3);
+                        if (token >= a.k_tokens) continue;
+                        const uint8_t* src = static_cast<const uint8_t*>(a.rows) + token * a.row_stride;
+                        const float f = *reinterpret_cast<const float*>(src + HS_ROW8_SCALE);
+                        const uint2 v = *reinterpret_cast<const uint2*>(src + HS_LATENT_DIM + (i & 7) * 8);
+                        uint32_t e[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t two = ((k & 2 ? v.y : v.x) >> (16 * (k & 1))) & 0xffff;
+                            e[k] = pack2<T>(hs_e4m3_to_float(two & 0xff) * f, hs_e4m3_to_float(two >> 8) * f);
+                        }
+                        *reinterpret_cast<uint4*>(g.rope_out + token * 128 + (i & 7) * 16) = make_uint4(e[0], e[1], e[2], e[3]);
+                    }
+                }
+                tc::cp_async_commit();
+                tc::cp_async_wait<0>();
+                tc::fence_async_shared();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_cluster(afull);
+            }
+            for (int kb = s; kb < 8; kb += kEStages, ++fills) {
+                if (fills) wait(tc::smem_addr(&x->bfree[s]), (fills - 1) & 1, &x->dead, error);
+                const uint8_t* src = w + ((h * HS_HEAD_DIM + (lane >> 3)) * HS_LATENT_DIM + kb * 64 + ch * 8) * 2;
+                const uint32_t dst = sbase + kEOffB + s * 16384 + (lane >> 3) * 128;
+#pragma unroll 8
+                for (int n = 0; n < 32; ++n)
+                    tc::cp_async16(dst + n * 512 + ((ch ^ ((n * 4 + (lane >> 3)) & 7)) << 4), src + (int64_t)n * 4 * HS_LATENT_DIM * 2, true);
+                tc::cp_async_commit();
+                tc::cp_async_wait<0>();
+                tc::fence_async_shared();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_cluster(bfull);
+            }
+        }
+    } else if (rank == 0) {
+        const uint32_t tmem = __shfl_sync(~0u, x->tmem, 0);
+        constexpr uint32_t id = tc::inst_desc(HsType<T>::is_bf16, 256, 256, false, false);
+        int64_t at = -1;
+        int tiles = 0, fill = 0;
+        for (int64_t job = lo; job < hi; ++job) {
+            const int n = (int)(job - lo), d = n & 1;
+            const int64_t mt = job / a.heads;
+            if (mt != at) wait(tc::smem_addr(&x->afull), tiles++ & 1, &x->dead, error);
+            at = mt;
+            if (n >= 2) wait(tc::smem_addr(&x->dfree[d]), ((n - 2) >> 1) & 1, &x->dead, error);
+#pragma unroll
+            for (int kb = 0; kb < 8; ++kb, ++fill) {
+                constexpr int S = kEStages;
+                wait(tc::smem_addr(&x->bfull[kb % S]), (fill / S) & 1, &x->dead, error);
+                __syncwarp();
+                tc::fence_after();
+                const uint64_t a_desc = tc::smem_desc(sbase + kb * 16384, 16, 1024);
+                const uint64_t b_desc = tc::smem_desc(sbase + kEOffB + (kb % S) * 16384, 16, 1024);
+                if (tc::elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tc::mma_ss<2>(tmem + 256 * d, a_desc + 2 * k, b_desc + 2 * k, id, (kb | k) != 0);
+                    tc::commit<2>(tc::smem_addr(&x->bfree[kb % S]));
+                    if (kb == 7) tc::commit<2>(tc::smem_addr(&x->dfull[d]));
+                }
+                __syncwarp();
+            }
+        }
+        if (*(volatile int*)&x->dead) {  // what was issued must be complete before tensor memory is freed
+            if (tc::elect_one()) tc::commit<2>(tc::smem_addr(&x->spare));
+            __syncwarp();
+            tc::mbar_wait(tc::smem_addr(&x->spare), 0);
+        }
+    }
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();
+    tc::cluster_sync();
+    tc::fence_after();
+    if (warp == 0) tc::tmem_free<2>(x->tmem, 512);
+}
+
+// ---- (2) attention -----------------------------------------------------------------
+
+constexpr int kThreads = 14 * 32;  // warps 0-7 softmax (four a tile), 8-9 keys and queries, 10-11 values, 12-13 products
+constexpr int kQTile = 3 * 16384;  // 3 blocks of 64 channels, [128 queries][128 B]
+constexpr int kOffK = 2 * kQTile;
+constexpr int kKStage = 3 * 16384;
+constexpr int kOffV = kOffK + 2 * kKStage;
+constexpr int kOffAux = kOffV + 2 * 16384;
+struct Aux {
+    uint64_t qfull, kfull[2], kfree[2], vfull, vfree, sfull[2], pfull[2], odone[2], spare[2];
+    uint32_t tmem;
+    int dead;
+    Start start;
+    long long count;
+};
+constexpr int kSmem = kOffAux + (int)sizeof(Aux);
+static_assert(kSmem <= 232448, "shared memory");
+
+// Tensor memory of tile s: scores (then weights) at 256 s, sums at 256 s + 128.
+
+struct Request {
+    long long q0, k0;
+    int n, m;  // queries, rows
+    __device__ Request(const hs_prefill_t& a, int b)
+    {
+        auto clamp = [](long long v, long long most) { return v < 0 ? 0 : v > most ? most : v; };
+        q0 = clamp(a.q_start[b], a.q_tokens);
+        k0 = clamp(a.k_start[b], a.k_tokens);
+        const long long q1 = clamp(a.q_start[b + 1], a.q_tokens), k1 = clamp(a.k_start[b + 1], a.k_tokens);
+        n = q1 > q0 ? (int)(q1 - q0) : 0;
+        m = k1 > k0 ? (int)(k1 - k0) : 0;
+    }
+    __device__ int q_tiles() const { return (n + 255) / 256; }
+    // Key blocks that queries below `end` see.
+    __device__ int blocks_to(int end) const
+    {
+        const long long keys = (long long)(end < n ? end : n) + m - n;  // the last of them sees this many
+        return keys <= 0 ? 0 : (int)((keys + 127) / 128);
+    }
+    __device__ int blocks(int qt) const { return max(1, blocks_to(256 * qt + 256)); }
+    __device__ long long blocks_of_head() const
+    {
+        long long t = 0;
+        for (int i = 0; i < q_tiles(); ++i) t += blocks(i);
+        return t;
+    }
+};
+
+struct Walk {
+    const hs_prefill_t& a;
+    int b, h, qt, kb;
+    long long left;
+    Request r;
+    // the current piece
+    int head, tile, t0, t1, blocks;
+    __device__ Walk(const hs_prefill_t& args, const Aux* x)
+        : a(args), b(x->start.b), h(x->start.h), qt(x->start.qt), kb(x->start.kb), left(x->count), r(args, x->start.b)
+    {
+    }
+    __device__ bool next()
+    {
+        if (left <= 0) return false;
+        while (qt >= r.q_tiles()) {
+            qt = 0;
+            if (r.n == 0 || ++h >= a.heads) {
+                h = 0;
+                if (++b >= a.batch) return false;
+                r = Request(a, b);
+            }
+        }
+        head = h;
+        tile = qt;
+        blocks = r.blocks(qt);
+        t0 = kb;
+        t1 = blocks - t0 <= left ? blocks : t0 + (int)left;
+        left -= t1 - t0;
+        kb = 0;
+        ++qt;
+        return true;
+    }
+    // Blocks that tile s of the piece works on: [t0, end(s)).
+    __device__ int end(int s) const
+    {
+        if (256 * tile + 128 * s >= r.n) return t0;
+        const int e = r.blocks_to(256 * tile + 128 * s + 128);
+        return e < t0 ? t0 : e < t1 ? e : t1;
+    }
+};
+
+template <typename T> __device__ void bring_keys(const Args& g, uint32_t sbase, Aux* x, int* error)
+{
+    const hs_prefill_t& a = g.a;
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 8, ch = lane & 7;
+    long long j = 0;
+    Walk walk(a, x);
+    while (walk.next()) {
+        // Q's readers are done: the last piece's products with keys.
+        if (j >= 2) wait(tc::smem_addr(&x->kfree[j & 1]), ((j - 2) >> 1) & 1, &x->dead, error);
+        if (j >= 1) wait(tc::smem_addr(&x->kfree[(j - 1) & 1]), ((j - 1) >> 1) & 1, &x->dead, error);
+        const T* q = static_cast<const T*>(a.q) + walk.head * a.q_stride[1];
+        const int q_first = 256 * walk.tile;
+#pragma unroll 4
+        for (int n = 0; n < 32; ++n) {  // warp w: tile w's queries
+            const int r = n * 4 + (lane >> 3), at = q_first + 128 * w + r;
+            const bool live = at < walk.r.n;
+            const uint8_t* src = reinterpret_cast<const uint8_t*>(q + (walk.r.q0 + (live ? at : 0)) * a.q_stride[0]) + ch * 16;
+            const uint32_t dst = sbase + w * kQTile + r * 128 + ((ch ^ (r & 7)) << 4);
+#pragma unroll
+            for (int c = 0; c < 3; ++c) tc::cp_async16(dst + c * 16384, src + c * 128, live);
+        }
+        const uint8_t* keys = g.keys + ((int64_t)walk.head * a.k_tokens + walk.r.k0) * HS_HEAD_DIM * 2 + ch * 16;
+        const uint8_t* rope = g.rope + walk.r.k0 * g.rope_stride + ch * 16;
+        for (int t = walk.t0; t < walk.t1; ++t, ++j) {
+            const int s = (int)(j & 1);
+            if (j >= 2) wait(tc::smem_addr(&x->kfree[s]), ((j - 2) >> 1) & 1, &x->dead, error);
+            const uint32_t stage = sbase + kOffK + s * kKStage;
+#pragma unroll 4
+            for (int n = 0; n < 16; ++n) {
+                const int r = 64 * w + n * 4 + (lane >> 3);
+                const int at = t * 128 + r;
+                const bool live = at < walk.r.m;
+                const uint32_t dst = stage + r * 128 + ((ch ^ (r & 7)) << 4);
+                const uint8_t* src = keys + (int64_t)(live ? at : 0) * (HS_HEAD_DIM * 2);
+                tc::cp_async16(dst, src, live);
+                tc::cp_async16(dst + 16384, src + 128, live);
+                tc::cp_async16(dst + 32768, rope + (live ? at : 0) * g.rope_stride, live);
+            }
+            tc::cp_async_commit();
+            tc::cp_async_wait<0>();
+            tc::fence_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+                if (t == walk.t0) tc::mbar_arrive(tc::smem_addr(&x->qfull));
+                tc::mbar_arrive(tc::smem_addr(&x->kfull[s]));
+            }
+        }
+    }
+}
+
+__device__ void bring_values(const Args& g, uint32_t sbase, Aux* x, int* error)
+{
+    const hs_prefill_t& a = g.a;
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 10, ch = lane & 7;
+    long long j = 0;
+    Walk walk(a, x);
+    while (walk.next()) {
+        const uint8_t* values = g.values + ((int64_t)walk.head * a.k_tokens + walk.r.k0) * HS_HEAD_DIM * 2 + ch * 16;
+        for (int t = walk.t0; t < walk.t1; ++t, ++j) {
+            if (j >= 1) wait(tc::smem_addr(&x->vfree), (j - 1) & 1, &x->dead, error);
+#pragma unroll 4
+            for (int n = 0; n < 16; ++n) {
+                const int r = 64 * w + n * 4 + (lane >> 3);
+                const int at = t * 128 + r;
+                const bool live = at < walk.r.m;
+                const uint32_t dst = sbase + kOffV + r * 128 + ((ch ^ (r & 7)) << 4);
+                const uint8_t* src = values + (int64_t)(live ? at : 0) * (HS_HEAD_DIM * 2);
+                tc::cp_async16(dst, src, live);
+                tc::cp_async16(dst + 16384, src + 128, live);
+            }
+            tc::cp_async_commit();
+            tc::cp_async_wait<0>();
+            tc::fence_async_shared();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(tc::smem_addr(&x->vfull));
+        }
+    }
+}
+
+// The products of tile S: its warp issues both kinds, in order.
+template <typename T, int S> __device__ void multiply(const Args& g, uint32_t sbase, Aux* x, int* error)
+{
+    constexpr uint32_t d_qk = tc::inst_desc(HsType<T>::is_bf16, 128, 128, false, false);
+    constexpr uint32_t d_pv = tc::inst_desc(HsType<T>::is_bf16, 128, 128, false, true);
+    const uint32_t tmem = __shfl_sync(~0u, x->tmem, 0) + 256 * S;
+    long long j = 0, mine = 0;
+    int pieces = 0;
+    Walk walk(g.a, x);
+    while (walk.next()) {
+        wait(tc::smem_addr(&x->qfull), pieces++ & 1, &x->dead, error);
+        const int end = walk.end(S);
+        for (int t = walk.t0; t < walk.t1; ++t, ++j) {
+            const int s = (int)(j & 1);
+            wait(tc::smem_addr(&x->kfull[s]), (j >> 1) & 1, &x->dead, error);
+            if (t < end) {
+                __syncwarp();
+                tc::fence_after();
+                const uint64_t q_desc = tc::smem_desc(sbase + S * kQTile, 16, 1024);
+                const uint64_t k_desc = tc::smem_desc(sbase + kOffK, 16, 1024) + (s ? kKStage >> 4 : 0);
+                if (tc::elect_one()) {
+#pragma unroll
+                    for (int c = 0; c < 3; ++c)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            tc::mma_ss<1>(tmem, q_desc + ((c * 16384 + k * 32) >> 4), k_desc + ((c * 16384 + k * 32) >> 4), d_qk,
+                                          (c | k) != 0);
+                    tc::commit<1>(tc::smem_addr(&x->sfull[S]));
+                    tc::commit<1>(tc::smem_addr(&x->kfree[s]));
+                }
+                __syncwarp();
+                wait(tc::smem_addr(&x->vfull), j & 1, &x->dead, error);
+                wait(tc::smem_addr(&x->pfull[S]), mine & 1, &x->dead, error);
+                ++mine;
+                __syncwarp();
+                tc::fence_after();
+                const uint64_t v_desc = tc::smem_desc(sbase + kOffV, 16384, 1024);
+                if (tc::elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        tc::mma_ts(tmem + 128, tmem + 8 * k, v_desc + ((k * 2048) >> 4), d_pv, !(t == walk.t0 && k == 0));
+                    tc::commit<1>(tc::smem_addr(&x->odone[S]));
+                    tc::commit<1>(tc::smem_addr(&x->vfree));
+                }
+                __syncwarp();
+            } else {
+                // nothing for this tile: it only lets go of the block
+                wait(tc::smem_addr(&x->vfull), j & 1, &x->dead, error);
+                if ((threadIdx.x & 31) == 0) {
+                    tc::mbar_arrive(tc::smem_addr(&x->kfree[s]));
+                    tc::mbar_arrive(tc::smem_addr(&x->vfree));
+                }
+                __syncwarp();
+            }
+        }
+    }
+    if (*(volatile int*)&x->dead) {  // what was issued must be complete before tensor memory is freed
+        if (tc::elect_one()) tc::commit<1>(tc::smem_addr(&x->spare[S]));
+        __syncwarp();
+        tc::mbar_wait(tc::smem_addr(&x->spare[S]), 0);
+    }
+}
+
+// Softmax of one tile: a query a thread.
+template <typename T> __device__ void soften(const Args& g, Aux* x, uint8_t* ws, int* error)
+{
+    const hs_prefill_t& a = g.a;
+    const int lane = threadIdx.x & 31, tile = threadIdx.x >> 7, row = threadIdx.x & 127;
+    const uint32_t tmem = x->tmem + 256 * tile + ((uint32_t)((threadIdx.x >> 5) & 3) << 21);
+    const bool flip = a.scale < 0.f;  // scores are negated then, so that the scale is not negative
+    const float c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f);  // not 0: a masked score stays -inf
+    long long mine = 0;
+    Walk walk(a, x);
+    while (walk.next()) {
+        const int end = walk.end(tile);
+        const int at = 256 * walk.tile + 128 * tile + row;
+        const int keys = min(at + 1 + walk.r.m - walk.r.n, walk.r.m);  // the keys this query sees
+        float ref = 0.f, sum = 0.f;
+        bool seen = false;
+        for (int t = walk.t0; t < end; ++t, ++mine) {
+            wait(tc::smem_addr(&x->sfull[tile]), mine & 1, &x->dead, error);
+            tc::fence_after();
+            const int some = keys - 128 * t;  // of this block's keys
+            uint32_t r[32];
+            float top = -INFINITY;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                __syncwarp();
+                tc::tmem_ld32(tmem + 32 * n, r);
+                tc::tmem_wait_ld();
+                if (flip)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) r[i] ^= 0x80000000u;
+                if (some < 32 * n + 32)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (32 * n + i >= some) r[i] = 0xff800000u;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(r[i]));
+            }
+            top *= c;
+            float keep = 1.f;
+            if (top > -INFINITY && (!seen || top > ref + 8.f)) {
+                keep = tc::exp2_approx(fminf(ref - top, 126.f));
+                sum *= keep;
+                ref = top;
+            }
+            const bool scale_o = seen && keep != 1.f;
+            seen = seen || top > -INFINITY;
+            if (__any_sync(~0u, scale_o)) {
+                if (!scale_o) keep = 1.f;
+                if (t > walk.t0) {
+                    wait(tc::smem_addr(&x->odone[tile]), (mine - 1) & 1, &x->dead, error);
+                    tc::fence_after();
+                }
+#pragma unroll 1
+                for (int n = 0; n < 128; n += 32) {
+                    tc::tmem_ld32(tmem + 128 + n, r);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * keep);
+                    tc::tmem_st32(tmem + 128 + n, r);
+                }
+                tc::tmem_wait_st();
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                uint32_t e[16];
+                __syncwarp();
+                tc::tmem_ld32(tmem + 32 * n, r);
+                tc::tmem_wait_ld();
+                if (flip)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) r[i] ^= 0x80000000u;
+                if (some < 32 * n + 32)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (32 * n + i >= some) r[i] = 0xff800000u;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float p0 = tc::exp2_approx(fmaf(__uint_as_float(r[2 * i]), c, -ref));
+                    const float p1 = tc::exp2_approx(fmaf(__uint_as_float(r[2 * i + 1]), c, -ref));
+                    sum += p0 + p1;
+                    e[i] = pack2<T>(p0, p1);
+                }
+                tc::tmem_st16(tmem + 16 * n, e);
+            }
+            tc::tmem_wait_st();
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(tc::smem_addr(&x->pfull[tile]));
+        }
+        // The piece's end.
+        const bool worked = end > walk.t0;
+        if (worked) {
+            wait(tc::smem_addr(&x->odone[tile]), (mine - 1) & 1, &x->dead, error);
+            tc::fence_after();
+        }
+        const bool live = at < walk.r.n;
+        const bool whole = walk.t0 == 0 && walk.t1 == walk.blocks;
+        Partial* part = reinterpret_cast<Partial*>(ws + kOffPartial) + 2 * blockIdx.x + (walk.t0 == 0 ? 1 : 0);
+        const bool some = worked && (sum > 0.f || sum != sum);
+        const float inv = some ? 1.f / sum : 0.f;
+        T* out = static_cast<T*>(a.out) + (walk.r.q0 + at) * a.out_stride[0] + walk.head * a.out_stride[1];
+#pragma unroll 1
+        for (int n = 0; n < 128; n += 32) {
+            uint32_t r[32];
+            __syncwarp();
+            tc::tmem_ld32(tmem + 128 + n, r);
+            tc::tmem_wait_ld();
+            if (!live) {
+                // a thread without a query has nothing to write
+            } else if (whole) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                    auto f = [&](int k) { return some ? __uint_as_float(r[i + k]) * inv : 0.f; };
+                    *reinterpret_cast<uint4*>(out + n + i) = make_uint4(pack2<T>(f(0), f(1)), pack2<T>(f(2), f(3)),
+                                                                        pack2<T>(f(4), f(5)), pack2<T>(f(6), f(7)));
+                }
+            } else if (worked) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) part->o[tile][n + i][row] = __uint_as_float(r[i]);
+            }
+        }
+        if (live) {
+            if (!whole) {
+                part->ref[tile][row] = ref;
+                part->sum[tile][row] = worked ? sum : 0.f;
+            } else if (a.lse) {
+                a.lse[(walk.r.q0 + at) * a.heads + walk.head] = some ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+            }
+        }
+        tc::fence_before();
+    }
+}
+
+template <typename T> __global__ void __launch_bounds__(kThreads, 1) hs_prefill_kernel(const __grid_constant__ Args g)
+{
+    extern __shared__ __align__(1024) uint8_t base[];
+    const uint32_t sbase = tc::smem_addr(base);
+    Aux* x = reinterpret_cast<Aux*>(base + kOffAux);
+    const hs_prefill_t& a = g.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    int* error = reinterpret_cast<int*>(ws);
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == 0) tc::tmem_alloc<1>(tc::smem_addr(&x->tmem), 512);
+    if (warp == 12) {
+        // This CTA's piece of the line of blocks.
+        long long total = 0;
+        for (int b = lane; b < a.batch; b += 32) total += Request(a, b).blocks_of_head() * a.heads;
+        for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
+        const long long n = total < gridDim.x ? total : gridDim.x, i = blockIdx.x;
+        const long long lo = i < n ? total * i / n : 0, hi = i < n ? total * (i + 1) / n : 0;
+        Start st = {-1, 0, 0, 0};
+        long long before = 0;
+        for (int b0 = 0; lo < hi && b0 < a.batch; b0 += 32) {
+            const int b = b0 + lane;
+            const long long per = b < a.batch ? Request(a, b).blocks_of_head() : 0;
+            long long incl = per * a.heads;
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long up = __shfl_up_sync(~0u, incl, o);
+                if (lane >= o) incl += up;
+            }
+            const long long at = before + incl - per * a.heads;
+            const bool here = lo >= at && lo < at + per * a.heads;
+            const unsigned who = __ballot_sync(~0u, here);
+            if (who) {
+                if (here) {
+                    const Request r(a, b);
+                    long long off = lo - at;
+                    st.b = b;
+                    st.h = (int)(off / per);
+                    off -= st.h * per;
+                    while (off >= r.blocks(st.qt)) off -= r.blocks(st.qt++);
+                    st.kb = (int)off;
+                }
+                const int src = __ffs(who) - 1;
+                st.b = __shfl_sync(~0u, st.b, src);
+                st.h = __shfl_sync(~0u, st.h, src);
+                st.qt = __shfl_sync(~0u, st.qt, src);
+                st.kb = __shfl_sync(~0u, st.kb, src);
+                break;
+            }
+            before += __shfl_sync(~0u, incl, 31);
+        }
+        if (lane == 0) {
+            x->start = st;
+            if (st.b < 0) x->start.b = 0;
+            x->count = st.b < 0 ? 0 : hi - lo;
+            x->dead = 0;
+            reinterpret_cast<Start*>(ws + kOffStart)[i] = st;
+            tc::mbar_init(tc::smem_addr(&x->qfull), 2);
+            tc::mbar_init(tc::smem_addr(&x->vfull), 2);
+            tc::mbar_init(tc::smem_addr(&x->vfree), 2);
+            for (int k = 0; k < 2; ++k) {
+                tc::mbar_init(tc::smem_addr(&x->kfull[k]), 2);
+                tc::mbar_init(tc::smem_addr(&x->kfree[k]), 2);
+                tc::mbar_init(tc::smem_addr(&x->sfull[k]), 1);
+                tc::mbar_init(tc::smem_addr(&x->pfull[k]), 4);
+                tc::mbar_init(tc::smem_addr(&x->odone[k]), 1);
+                tc::mbar_init(tc::smem_addr(&x->spare[k]), 1);
+            }
+            tc::mbar_init_fence();
+        }
+    }
+    tc::fence_before();
+    __syncwarp();
+    __syncthreads();
+    tc::fence_after();
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the expansion's keys and values
+
+    if (x->count > 0) {
+        if (warp < 8)
+            soften<T>(g, x, ws, error);
+        else if (warp < 10)
+            bring_keys<T>(g, sbase, x, error);
+        else if (warp < 12)
+            bring_values(g, sbase, x, error);
+        else if (warp == 12)
+            multiply<T, 0>(g, sbase, x, error);
+        else
+            multiply<T, 1>(g, sbase, x, error);
+    }
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == 0) tc::tmem_free<1>(x->tmem, 512);
+}
+
+// ---- (3) join ------------------------------------------------------------------------
+
+// Block x takes the x-th unit that several CTAs worked on (found at the first start
+// of a piece inside it), one tile of it, 16 channels.  Four groups of 128 threads,
+// one a query, take every fourth piece; the order of the sums is fixed.
+constexpr int kJoinCols = 16;
+template <typename T> __global__ void __launch_bounds__(512) hs_prefill_join_kernel(const __grid_constant__ Args g, int ctas)
+{
+    __shared__ float tops[4][128], sums[4][128], cols[3][kJoinCols][128];
+    __shared__ int counts[8], first_cut;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const hs_prefill_t& a = g.a;
+    const uint8_t* ws = static_cast<const uint8_t*>(a.workspace);
+    const Partial* parts = reinterpret_cast<const Partial*>(ws + kOffPartial);
+    const Start* start = reinterpret_cast<const Start*>(ws + kOffStart);
+    const int t = threadIdx.x;
+    if (t == 0) first_cut = 0;
+    auto same = [](const Start& p, const Start& q) { return p.b == q.b && p.h == q.h && p.qt == q.qt; };
+    Start mine = {-1, 0, 0, 0};
+    bool inside = false, cut = false;
+    if (t > 0 && t < ctas) {
+        mine = start[t];
+        const Start prev = start[t - 1];
+        inside = mine.b >= 0 && mine.kb > 0;
+        cut = inside && !(same(mine, prev) && prev.kb > 0);
+    }
+    const unsigned ballot = __ballot_sync(~0u, cut);
+    if (t < 256 && (t & 31) == 0) counts[t >> 5] = __popc(ballot);
+    __syncthreads();
+    if (cut) {
+        int before = __popc(ballot & ((1u << (t & 31)) - 1));
+        for (int w = 0; w < t >> 5; ++w) before += counts[w];
+        if (before == (int)blockIdx.x) first_cut = t;
     }
     __syncthreads();
-    const int d = threadIdx.x % HS_HEAD_DIM;
-    const bool value = threadIdx.x >= HS_HEAD_DIM;
-    const T* w = static_cast<const T*>(value ? a.w_uv : a.w_uk) + ((int64_t)head * HS_HEAD_DIM + d) * HS_LATENT_DIM;
-    float acc[kTokens] = {};
-    for (int c = 0; c < HS_LATENT_DIM; ++c) {
-        const float wv = HsType<T>::to_float(w[c]);
-        for (int t = 0; t < kTokens; ++t) acc[t] += wv * lat[t][c];
-    }
-    T* dst = static_cast<T*>(a.workspace) + (value ? a.k_tokens * a.heads * HS_HEAD_DIM : 0);
-    for (int t = 0; t < kTokens; ++t)
-        if (t0 + t < a.k_tokens)
-            dst[((t0 + t) * a.heads + head) * HS_HEAD_DIM + d] = HsType<T>::from_float(acc[t]);
-}
-
-template <typename T, bool E4M3>
-__global__ void __launch_bounds__(kWarps * 32) hs_prefill_kernel(hs_prefill_t a)
-{
-    const int lane = threadIdx.x & 31;
-    const int64_t i = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int head = blockIdx.y;
-    int r = 0;  // the request of query i: the last with q_start[r] <= i
-    int64_t q0 = 0, q1 = 0;
-    for (; r < a.batch; ++r) {
-        q0 = a.q_start[r];
-        q1 = a.q_start[r + 1];
-        if (i >= q0 && i < q1) break;
-    }
-    if (r == a.batch || i >= a.q_tokens) return;
-    int64_t k0 = a.k_start[r], k1 = a.k_start[r + 1];
-    k0 = k0 < 0 ? 0 : k0;
-    k1 = k1 > a.k_tokens ? a.k_tokens : k1;
-    q1 = q1 > a.q_tokens ? a.q_tokens : q1;
-    const int64_t n = (i - q0) + (k1 - k0) - (q1 - q0) + 1;
-    const T* q = static_cast<const T*>(a.q) + i * a.q_stride[0] + head * a.q_stride[1];
-    float qr[6], acc[4] = {};
-    for (int j = 0; j < 6; ++j) qr[j] = HsType<T>::to_float(q[lane + 32 * j]);
-    float m = -INFINITY, l = 0.f;
-    for (int64_t t = k0; t < k0 + n; ++t) {
-        const T* k = static_cast<const T*>(a.workspace) + (t * a.heads + head) * HS_HEAD_DIM;
-        const T* v = k + a.k_tokens * a.heads * HS_HEAD_DIM;
-        const uint8_t* row = static_cast<const uint8_t*>(a.rows) + t * a.row_stride;
-        float s = 0.f, w = 1.f;
-        if (E4M3) w = *reinterpret_cast<const float*>(row + HS_ROW8_SCALE);
-        for (int j = 0; j < 4; ++j) s += qr[j] * HsType<T>::to_float(k[lane + 32 * j]);
-        for (int j = 0; j < 2; ++j) {
-            const int c = HS_LATENT_DIM + lane + 32 * j;
-            s += qr[4 + j] * (E4M3 ? hs_e4m3_to_float(row[c]) * w
-                                   : HsType<T>::to_float(reinterpret_cast<const T*>(row)[c]));
+    if (first_cut == 0) return;
+    const Start unit = start[first_cut];
+    const int first = first_cut - 1, last = first + __syncthreads_count(inside && same(mine, unit));
+    const Request r(a, unit.b);
+    const int tile = blockIdx.y, c0 = kJoinCols * blockIdx.z;
+    const int row = t & 127, group = t >> 7;
+    const int at = 256 * unit.qt + 128 * tile + row;
+    if (256 * unit.qt + 128 * tile >= r.n) return;
+    const bool live = at < r.n;
+    float acc[kJoinCols] = {}, sum = 0.f, top = -INFINITY;
+    if (live)
+#pragma unroll 2
+        for (int n = first + group; n <= last; n += 4) {
+            const Partial& q = parts[2 * n + (n == first)];
+            const float ref = q.ref[tile][row], l = q.sum[tile][row];
+            if (l == 0.f) continue;  // no key counted
+            float o[kJoinCols];
+#pragma unroll
+            for (int k = 0; k < kJoinCols; ++k) o[k] = q.o[tile][c0 + k][row];
+            const float up = fmaxf(top, ref);
+            const float keep = tc::exp2_approx(top - up), w = tc::exp2_approx(ref - up);
+            top = up;
+            sum = sum * keep + w * l;
+#pragma unroll
+            for (int k = 0; k < kJoinCols; ++k) acc[k] = acc[k] * keep + w * o[k];
         }
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-        s *= a.scale;
-        const float top = fmaxf(m, s);
-        const float keep = m == -INFINITY ? 0.f : __expf(m - top);
-        const float p = __expf(s - top);
-        l = l * keep + p;
-        for (int j = 0; j < 4; ++j) acc[j] = acc[j] * keep + p * HsType<T>::to_float(v[lane + 32 * j]);
-        m = top;
+    tops[group][row] = top;
+    sums[group][row] = sum;
+    if (group)
+#pragma unroll
+        for (int k = 0; k < kJoinCols; ++k) cols[group - 1][k][row] = acc[k];
+    __syncthreads();
+    if (group || !live) return;
+    top = fmaxf(fmaxf(tops[0][row], tops[1][row]), fmaxf(tops[2][row], tops[3][row]));
+    const float ref = top == -INFINITY ? 0.f : top;
+    float w = tc::exp2_approx(tops[0][row] - ref);
+    sum *= w;
+#pragma unroll
+    for (int k = 0; k < kJoinCols; ++k) acc[k] *= w;
+    for (int n = 1; n < 4; ++n) {
+        w = tc::exp2_approx(tops[n][row] - ref);
+        sum += w * sums[n][row];
+#pragma unroll
+        for (int k = 0; k < kJoinCols; ++k) acc[k] += w * cols[n - 1][k][row];
     }
-    T* out = static_cast<T*>(a.out) + i * a.out_stride[0] + head * a.out_stride[1];
-    for (int j = 0; j < 4; ++j) out[lane + 32 * j] = HsType<T>::from_float(n > 0 ? acc[j] / l : 0.f);
-    if (a.lse && lane == 0) a.lse[i * a.heads + head] = n > 0 ? m + __logf(l) : -INFINITY;
+    const bool some = sum > 0.f || sum != sum;
+    const float inv = some ? 1.f / sum : 0.f;
+    T* out = static_cast<T*>(a.out) + (r.q0 + at) * a.out_stride[0] + unit.h * a.out_stride[1] + c0;
+#pragma unroll
+    for (int k = 0; k < kJoinCols; k += 8)
+        *reinterpret_cast<uint4*>(out + k) = make_uint4(pack2<T>(acc[k] * inv, acc[k + 1] * inv), pack2<T>(acc[k + 2] * inv, acc[k + 3] * inv),
+                                                        pack2<T>(acc[k + 4] * inv, acc[k + 5] * inv), pack2<T>(acc[k + 6] * inv, acc[k + 7] * inv));
+    if (a.lse && c0 == 0)
+        a.lse[(r.q0 + at) * a.heads + unit.h] = some ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
-template <typename T, bool E4M3>
-cudaError_t launch(const hs_prefill_t& a, cudaStream_t s)
+template <typename... Params, typename... Values>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s, Values... values)
 {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = threads;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, values...);
+}
+
+template <typename T, bool E4M3> cudaError_t launch(const Args& g, int sms, cudaStream_t s)
+{
+    const hs_prefill_t& a = g.a;
+    cudaError_t e = cudaFuncSetAttribute(hs_expand_kernel<T, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kESmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(hs_prefill_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
     if (a.k_tokens > 0) {
-        const dim3 grid((unsigned)((a.k_tokens + kTokens - 1) / kTokens), a.heads);
-        hs_expand_kernel<T, E4M3><<<grid, 2 * HS_HEAD_DIM, 0, s>>>(a);
+        const int64_t jobs = (a.k_tokens + 255) / 256 * a.heads;
+        const int pairs = (int)(jobs < sms / 2 ? jobs : sms / 2);
+        hs_expand_kernel<T, E4M3><<<2 * pairs, kEThreads, kESmem, s>>>(g);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
     }
-    const dim3 grid((unsigned)((a.q_tokens + kWarps - 1) / kWarps), a.heads);
-    hs_prefill_kernel<T, E4M3><<<grid, kWarps * 32, 0, s>>>(a);
-    return cudaGetLastError();
+    // Behind the expansion, whose start means that all earlier work is done, it may set up early.
+    if (a.k_tokens > 0) {
+        e = launch_after(hs_prefill_kernel<T>, dim3(sms), kThreads, kSmem, s, g);
+    } else {
+        hs_prefill_kernel<T><<<sms, kThreads, kSmem, s>>>(g);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) return e;
+    const int64_t units = (a.q_tokens / 256 + a.batch) * a.heads;  // at most
+    return launch_after(hs_prefill_join_kernel<T>, dim3((unsigned)(units < sms - 1 ? units : sms - 1), 2, HS_HEAD_DIM / kJoinCols), 512, 0, s, g, sms);
 }
 
 }  // namespace
 
 size_t hs_prefill_workspace_bytes(int64_t k_tokens, int heads)
 {
-    return 256 + (size_t)k_tokens * heads * 2 * HS_HEAD_DIM * 2;
+    return kOffKeys + (size_t)k_tokens * heads * 2 * HS_HEAD_DIM * 2 + (size_t)k_tokens * HS_ROPE_DIM * 2;
 }
 
 cudaError_t hs_launch_prefill(const hs_prefill_t& a, cudaStream_t s)
 {
+    int dev = 0, sms = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (err != cudaSuccess) return err;
+    sms = sms > kMaxCtas ? kMaxCtas : sms < 2 ? 2 : sms;
     const bool e = a.row_format == HS_ROWS_E4M3;
+    Args g;
+    g.a = a;
+    g.keys = static_cast<uint8_t*>(a.workspace) + kOffKeys;
+    g.values = g.keys + (size_t)a.k_tokens * a.heads * HS_HEAD_DIM * 2;
+    g.rope_out = e ? g.values + (size_t)a.k_tokens * a.heads * HS_HEAD_DIM * 2 : nullptr;
+    g.rope = e ? g.rope_out : static_cast<const uint8_t*>(a.rows) + HS_LATENT_DIM * 2;
+    g.rope_stride = e ? HS_ROPE_DIM * 2 : a.row_stride;
     if (a.dtype == HS_TYPE_BF16)
-        return e ? launch<__nv_bfloat16, true>(a, s) : launch<__nv_bfloat16, false>(a, s);
-    return e ? launch<__half, true>(a, s) : launch<__half, false>(a, s);
+        return e ? launch<__nv_bfloat16, true>(g, sms, s) : launch<__nv_bfloat16, false>(g, sms, s);
+    return e ? launch<__half, true>(g, sms, s) : launch<__half, false>(g, sms, s);
 }
