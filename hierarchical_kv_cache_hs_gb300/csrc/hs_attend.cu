@@ -505,7 +505,7 @@ __device__ void soften(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int
             tc::fence_after();
             uint32_t r[32];
             tc::tmem_ld32(tmem + kColS + 32 * s, r);
-            tc::tmem_wait_ld();
+            tc::tmem_wait_ld(r);
             if constexpr (E4M3 && HsType<T>::is_bf16)
                 if (t == walk.t0)
                     c = __uint_as_float((uint32_t)(127 - x->q_up[pieces & 1][row]) << 23) * (a.scale * 1.4426950408889634f);
@@ -544,7 +544,7 @@ __device__ void soften(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int
 #pragma unroll 1
                 for (int n = 0; n < 256; n += 32) {
                     tc::tmem_ld32(tmem + kColO + n, r);
-                    tc::tmem_wait_ld();
+                    tc::tmem_wait_ld(r);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * keep);
                     tc::tmem_st32(tmem + kColO + n, r);
@@ -593,7 +593,7 @@ __device__ void soften(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int
             uint32_t r[32];
             __syncwarp();
             tc::tmem_ld32(tmem + kColO + n, r);
-            tc::tmem_wait_ld();
+            tc::tmem_wait_ld(r);
             if (head >= a.heads) {
                 // a lane without a head has nothing to write
             } else if (whole) {
@@ -747,7 +747,7 @@ template <typename T, int COLS>
 __global__ void __launch_bounds__(512) hs_attend_join_kernel(const __grid_constant__ Args g, int pairs)
 {
     __shared__ float tops[4][128], sums[4][128], cols[3][COLS][128];
-    __shared__ int counts[4], first_cut, last_cut;
+    __shared__ int counts[4], first_cut;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const hs_attend_t& a = g.a;
     const uint8_t* ws = static_cast<const uint8_t*>(a.workspace);

@@ -157,7 +157,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kEThreads, 1) hs_exp
                 uint32_t r[32], e[16];
                 __syncwarp();
                 tc::tmem_ld32(tmem + 256 * d + c * 32, r);
-                tc::tmem_wait_ld();
+                tc::tmem_wait_ld(r);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     float p = __uint_as_float(r[2 * i]), q = __uint_as_float(r[2 * i + 1]);
@@ -296,14 +296,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kEThreads, 1) hs_exp
 
 // ---- (2) attention -----------------------------------------------------------------
 
-constexpr int kThreads = 14 * 32;  // warps 0-7 softmax (four a tile), 8-9 keys and queries, 10-11 values, 12-13 products
+constexpr int kThreads = 12 * 32;  // warps 0-7 softmax (four a tile), 8-9 keys and queries, 10 values, 11 products
 constexpr int kQTile = 3 * 16384;  // 3 blocks of 64 channels, [128 queries][128 B]
 constexpr int kOffK = 2 * kQTile;
 constexpr int kKStage = 3 * 16384;
 constexpr int kOffV = kOffK + 2 * kKStage;
 constexpr int kOffAux = kOffV + 2 * 16384;
 struct Aux {
-    uint64_t qfull, kfull[2], kfree[2], vfull, vfree, sfull[2], pfull[2], odone[2], spare[2];
+    uint64_t qfull, kfull[2], kfree[2], vfull, vfree, sfull[2], pfull[2], odone[2], spare;
     uint32_t tmem;
     int dead;
     Start start;
@@ -436,7 +436,7 @@ template <typename T> __device__ void bring_keys(const Args& g, uint32_t sbase, 
 __device__ void bring_values(const Args& g, uint32_t sbase, Aux* x, int* error)
 {
     const hs_prefill_t& a = g.a;
-    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 10, ch = lane & 7;
+    const int lane = threadIdx.x & 31, ch = lane & 7;
     long long j = 0;
     Walk walk(a, x);
     while (walk.next()) {
@@ -444,8 +444,8 @@ __device__ void bring_values(const Args& g, uint32_t sbase, Aux* x, int* error)
         for (int t = walk.t0; t < walk.t1; ++t, ++j) {
             if (j >= 1) wait(tc::smem_addr(&x->vfree), (j - 1) & 1, &x->dead, error);
 #pragma unroll 4
-            for (int n = 0; n < 16; ++n) {
-                const int r = 64 * w + n * 4 + (lane >> 3);
+            for (int n = 0; n < 32; ++n) {
+                const int r = n * 4 + (lane >> 3);
                 const int at = t * 128 + r;
                 const bool live = at < walk.r.m;
                 const uint32_t dst = sbase + kOffV + r * 128 + ((ch ^ (r & 7)) << 4);
@@ -462,66 +462,91 @@ __device__ void bring_values(const Args& g, uint32_t sbase, Aux* x, int* error)
     }
 }
 
-// The products of tile S: its warp issues both kinds, in order.
-template <typename T, int S> __device__ void multiply(const Args& g, uint32_t sbase, Aux* x, int* error)
+// Q K^T of tile S with the keys in stage ST, and P V of tile S.
+template <typename T, int S, int ST> __device__ __forceinline__ void issue_qk(uint32_t sbase, uint32_t tmem, Aux* x)
 {
-    constexpr uint32_t d_qk = tc::inst_desc(HsType<T>::is_bf16, 128, 128, false, false);
-    constexpr uint32_t d_pv = tc::inst_desc(HsType<T>::is_bf16, 128, 128, false, true);
-    const uint32_t tmem = __shfl_sync(~0u, x->tmem, 0) + 256 * S;
-    long long j = 0, mine = 0;
+    constexpr uint32_t id = tc::inst_desc(HsType<T>::is_bf16, 128, 128, false, false);
+    const uint64_t q_desc = tc::smem_desc(sbase + S * kQTile, 16, 1024);
+    const uint64_t k_desc = tc::smem_desc(sbase + kOffK + ST * kKStage, 16, 1024);
+    if (tc::elect_one()) {
+#pragma unroll
+        for (int c = 0; c < 3; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                tc::mma_ss<1>(tmem + 256 * S, q_desc + ((c * 16384 + k * 32) >> 4), k_desc + ((c * 16384 + k * 32) >> 4), id,
+                              (c | k) != 0);
+        tc::commit<1>(tc::smem_addr(&x->sfull[S]));
+    }
+    __syncwarp();
+}
+template <typename T, int S> __device__ __forceinline__ void issue_pv(uint32_t sbase, uint32_t tmem, Aux* x, bool first)
+{
+    constexpr uint32_t id = tc::inst_desc(HsType<T>::is_bf16, 128, 128, false, true);
+    const uint64_t v_desc = tc::smem_desc(sbase + kOffV, 16384, 1024);
+    if (tc::elect_one()) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            tc::mma_ts(tmem + 256 * S + 128, tmem + 256 * S + 8 * k, v_desc + ((k * 2048) >> 4), id, !(first && k == 0));
+        tc::commit<1>(tc::smem_addr(&x->odone[S]));
+    }
+    __syncwarp();
+}
+
+// The products, issued by one warp in the order in which the tiles take turns: P V
+// of a block, then Q K^T of the next one, of tile 0 and then of tile 1.  (Issued by
+// a warp a tile, the two tiles' products ran interleaved, both tiles' scores came
+// at the same time, and the tensor core idled through both softmaxes.)
+template <typename T> __device__ void multiply(const Args& g, uint32_t sbase, Aux* x, int* error)
+{
+    const uint32_t tmem = __shfl_sync(~0u, x->tmem, 0);
+    long long j = 0;
     int pieces = 0;
+    uint32_t phase[2] = {0, 0};  // of pfull
     Walk walk(g.a, x);
+    auto release = [](uint64_t& bar) {  // when all products so far are complete
+        if (tc::elect_one()) tc::commit<1>(tc::smem_addr(&bar));
+        __syncwarp();
+    };
+    auto scores = [&](int tile, int stage) {
+        if (tile == 0)
+            stage ? issue_qk<T, 0, 1>(sbase, tmem, x) : issue_qk<T, 0, 0>(sbase, tmem, x);
+        else
+            stage ? issue_qk<T, 1, 1>(sbase, tmem, x) : issue_qk<T, 1, 0>(sbase, tmem, x);
+    };
     while (walk.next()) {
+        const int end[2] = {walk.end(0), walk.end(1)};
         wait(tc::smem_addr(&x->qfull), pieces++ & 1, &x->dead, error);
-        const int end = walk.end(S);
+        wait(tc::smem_addr(&x->kfull[j & 1]), (j >> 1) & 1, &x->dead, error);
+        __syncwarp();
+        tc::fence_after();
+        for (int tile = 0; tile < 2; ++tile)
+            if (walk.t0 < end[tile]) scores(tile, (int)(j & 1));
+        release(x->kfree[j & 1]);
         for (int t = walk.t0; t < walk.t1; ++t, ++j) {
-            const int s = (int)(j & 1);
-            wait(tc::smem_addr(&x->kfull[s]), (j >> 1) & 1, &x->dead, error);
-            if (t < end) {
-                __syncwarp();
-                tc::fence_after();
-                const uint64_t q_desc = tc::smem_desc(sbase + S * kQTile, 16, 1024);
-                const uint64_t k_desc = tc::smem_desc(sbase + kOffK, 16, 1024) + (s ? kKStage >> 4 : 0);
-                if (tc::elect_one()) {
+            const int next = (int)((j + 1) & 1);
+            wait(tc::smem_addr(&x->vfull), j & 1, &x->dead, error);
+            if (t + 1 < walk.t1) wait(tc::smem_addr(&x->kfull[next]), ((j + 1) >> 1) & 1, &x->dead, error);
 #pragma unroll
-                    for (int c = 0; c < 3; ++c)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            tc::mma_ss<1>(tmem, q_desc + ((c * 16384 + k * 32) >> 4), k_desc + ((c * 16384 + k * 32) >> 4), d_qk,
-                                          (c | k) != 0);
-                    tc::commit<1>(tc::smem_addr(&x->sfull[S]));
-                    tc::commit<1>(tc::smem_addr(&x->kfree[s]));
+            for (int tile = 0; tile < 2; ++tile) {
+                if (t < end[tile]) {
+                    wait(tc::smem_addr(&x->pfull[tile]), phase[tile], &x->dead, error);
+                    phase[tile] ^= 1;
+                    __syncwarp();
+                    tc::fence_after();
+                    if (tile == 0)
+                        issue_pv<T, 0>(sbase, tmem, x, t == walk.t0);
+                    else
+                        issue_pv<T, 1>(sbase, tmem, x, t == walk.t0);
                 }
-                __syncwarp();
-                wait(tc::smem_addr(&x->vfull), j & 1, &x->dead, error);
-                wait(tc::smem_addr(&x->pfull[S]), mine & 1, &x->dead, error);
-                ++mine;
-                __syncwarp();
-                tc::fence_after();
-                const uint64_t v_desc = tc::smem_desc(sbase + kOffV, 16384, 1024);
-                if (tc::elect_one()) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        tc::mma_ts(tmem + 128, tmem + 8 * k, v_desc + ((k * 2048) >> 4), d_pv, !(t == walk.t0 && k == 0));
-                    tc::commit<1>(tc::smem_addr(&x->odone[S]));
-                    tc::commit<1>(tc::smem_addr(&x->vfree));
-                }
-                __syncwarp();
-            } else {
-                // nothing for this tile: it only lets go of the block
-                wait(tc::smem_addr(&x->vfull), j & 1, &x->dead, error);
-                if ((threadIdx.x & 31) == 0) {
-                    tc::mbar_arrive(tc::smem_addr(&x->kfree[s]));
-                    tc::mbar_arrive(tc::smem_addr(&x->vfree));
-                }
-                __syncwarp();
+                if (tile == 1) release(x->vfree);
+                if (t + 1 < end[tile]) scores(tile, next);
             }
+            if (t + 1 < walk.t1) release(x->kfree[next]);
         }
     }
     if (*(volatile int*)&x->dead) {  // what was issued must be complete before tensor memory is freed
-        if (tc::elect_one()) tc::commit<1>(tc::smem_addr(&x->spare[S]));
-        __syncwarp();
-        tc::mbar_wait(tc::smem_addr(&x->spare[S]), 0);
+        release(x->spare);
+        tc::mbar_wait(tc::smem_addr(&x->spare), 0);
     }
 }
 
@@ -545,23 +570,25 @@ template <typename T> __device__ void soften(const Args& g, Aux* x, uint8_t* ws,
             wait(tc::smem_addr(&x->sfull[tile]), mine & 1, &x->dead, error);
             tc::fence_after();
             const int some = keys - 128 * t;  // of this block's keys
-            uint32_t r[32];
-            float top = -INFINITY;
+            uint32_t v[4][32];  // the scores
+#pragma unroll
+            for (int n = 0; n < 4; ++n) tc::tmem_ld32(tmem + 32 * n, v[n]);
+            float tops[4];
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                __syncwarp();
-                tc::tmem_ld32(tmem + 32 * n, r);
-                tc::tmem_wait_ld();
+                tc::tmem_wait_ld(v[n]);
                 if (flip)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) r[i] ^= 0x80000000u;
+                    for (int i = 0; i < 32; ++i) v[n][i] ^= 0x80000000u;
                 if (some < 32 * n + 32)
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if (32 * n + i >= some) r[i] = 0xff800000u;
+                        if (32 * n + i >= some) v[n][i] = 0xff800000u;
+                tops[n] = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(r[i]));
+                for (int i = 0; i < 32; ++i) tops[n] = fmaxf(tops[n], __uint_as_float(v[n][i]));
             }
+            float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
             top *= c;
             float keep = 1.f;
             if (top > -INFINITY && (!seen || top > ref + 8.f)) {
@@ -579,36 +606,29 @@ template <typename T> __device__ void soften(const Args& g, Aux* x, uint8_t* ws,
                 }
 #pragma unroll 1
                 for (int n = 0; n < 128; n += 32) {
+                    uint32_t r[32];
                     tc::tmem_ld32(tmem + 128 + n, r);
-                    tc::tmem_wait_ld();
+                    tc::tmem_wait_ld(r);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * keep);
                     tc::tmem_st32(tmem + 128 + n, r);
                 }
                 tc::tmem_wait_st();
             }
+            float sums[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 uint32_t e[16];
-                __syncwarp();
-                tc::tmem_ld32(tmem + 32 * n, r);
-                tc::tmem_wait_ld();
-                if (flip)
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) r[i] ^= 0x80000000u;
-                if (some < 32 * n + 32)
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (32 * n + i >= some) r[i] = 0xff800000u;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float p0 = tc::exp2_approx(fmaf(__uint_as_float(r[2 * i]), c, -ref));
-                    const float p1 = tc::exp2_approx(fmaf(__uint_as_float(r[2 * i + 1]), c, -ref));
-                    sum += p0 + p1;
+                    const float p0 = tc::exp2_approx(fmaf(__uint_as_float(v[n][2 * i]), c, -ref));
+                    const float p1 = tc::exp2_approx(fmaf(__uint_as_float(v[n][2 * i + 1]), c, -ref));
+                    sums[i & 3] += p0 + p1;
                     e[i] = pack2<T>(p0, p1);
                 }
                 tc::tmem_st16(tmem + 16 * n, e);
             }
+            sum += (sums[0] + sums[1]) + (sums[2] + sums[3]);
             tc::tmem_wait_st();
             tc::fence_before();
             __syncwarp();
@@ -631,7 +651,7 @@ template <typename T> __device__ void soften(const Args& g, Aux* x, uint8_t* ws,
             uint32_t r[32];
             __syncwarp();
             tc::tmem_ld32(tmem + 128 + n, r);
-            tc::tmem_wait_ld();
+            tc::tmem_wait_ld(r);
             if (!live) {
                 // a thread without a query has nothing to write
             } else if (whole) {
@@ -670,7 +690,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) hs_prefill_
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == 0) tc::tmem_alloc<1>(tc::smem_addr(&x->tmem), 512);
-    if (warp == 12) {
+    if (warp == 11) {
         // This CTA's piece of the line of blocks.
         long long total = 0;
         for (int b = lane; b < a.batch; b += 32) total += Request(a, b).blocks_of_head() * a.heads;
@@ -716,15 +736,15 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) hs_prefill_
             x->dead = 0;
             reinterpret_cast<Start*>(ws + kOffStart)[i] = st;
             tc::mbar_init(tc::smem_addr(&x->qfull), 2);
-            tc::mbar_init(tc::smem_addr(&x->vfull), 2);
-            tc::mbar_init(tc::smem_addr(&x->vfree), 2);
+            tc::mbar_init(tc::smem_addr(&x->vfull), 1);
+            tc::mbar_init(tc::smem_addr(&x->vfree), 1);
+            tc::mbar_init(tc::smem_addr(&x->spare), 1);
             for (int k = 0; k < 2; ++k) {
                 tc::mbar_init(tc::smem_addr(&x->kfull[k]), 2);
-                tc::mbar_init(tc::smem_addr(&x->kfree[k]), 2);
+                tc::mbar_init(tc::smem_addr(&x->kfree[k]), 1);
                 tc::mbar_init(tc::smem_addr(&x->sfull[k]), 1);
                 tc::mbar_init(tc::smem_addr(&x->pfull[k]), 4);
                 tc::mbar_init(tc::smem_addr(&x->odone[k]), 1);
-                tc::mbar_init(tc::smem_addr(&x->spare[k]), 1);
             }
             tc::mbar_init_fence();
         }
@@ -740,12 +760,10 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) hs_prefill_
             soften<T>(g, x, ws, error);
         else if (warp < 10)
             bring_keys<T>(g, sbase, x, error);
-        else if (warp < 12)
+        else if (warp == 10)
             bring_values(g, sbase, x, error);
-        else if (warp == 12)
-            multiply<T, 0>(g, sbase, x, error);
         else
-            multiply<T, 1>(g, sbase, x, error);
+            multiply<T>(g, sbase, x, error);
     }
     __syncwarp();
     tc::fence_before();
