@@ -22,8 +22,12 @@ namespace {
 constexpr int kMaxCtas = 152;
 
 // Workspace: an error word, where each CTA's piece starts, two partial results a
-// CTA, keys [heads][k_tokens][128], values likewise, rotary channels [k_tokens][64]
-// (of 8-bit rows).
+// CTA; then, for blocks of 128 tokens (counted over all requests, the tail padded to
+// 256 tokens with zeros), the tiles that the attention copies to shared memory as
+// they are, rows of 128 bytes with the 128-byte swizzle:
+//   keys    [head][block][2 x 64 channels][128 tokens]
+//   values  [head][block][2 x 64 tokens][2 x 64 channels][64 tokens]
+//   rotary  [block][128 tokens]
 struct Start {
     int b, h, qt, kb;
 };
@@ -35,13 +39,15 @@ constexpr size_t kOffStart = 256;
 constexpr size_t kOffPartial = kOffStart + sizeof(Start) * kMaxCtas;
 constexpr size_t kOffKeys = kOffPartial + sizeof(Partial) * 2 * kMaxCtas;
 
+constexpr int kBlock = 32768;  // keys, or values, of a block and head
+constexpr int kRope = 16384;   // rotary channels of a block
+
 struct Args {
     hs_prefill_t a;
     uint8_t* keys;
     uint8_t* values;
-    const uint8_t* rope;  // 64 channels a token
-    int64_t rope_stride;  // bytes
-    uint8_t* rope_out;    // where the expansion writes them, or NULL
+    uint8_t* rope;
+    int64_t blocks;
 };
 
 template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
@@ -171,12 +177,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kEThreads, 1) hs_exp
                 } else if (bad) {
                     e[0] = ~0u;
                 }
-                if (live) {
-                    uint8_t* dst = (c >= 4 ? g.values : g.keys) + ((h * a.k_tokens + token) * HS_HEAD_DIM + (c & 3) * 32) * 2;
+                // 32 channels are half a row of the tile
+                const int64_t tile = h * g.blocks + mt * 2 + rank;
+                const int tok = threadIdx.x, cb = c >> 1 & 1;
+                uint8_t* row = c >= 4 ? g.values + tile * kBlock + (tok >> 6) * 16384 + cb * 8192 + (tok & 63) * 128
+                                      : g.keys + tile * kBlock + cb * 16384 + tok * 128;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        *reinterpret_cast<uint4*>(dst + 16 * i) = make_uint4(e[4 * i], e[4 * i + 1], e[4 * i + 2], e[4 * i + 3]);
-                }
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint4*>(row + ((((c & 1) * 4 + i) ^ (tok & 7)) << 4)) =
+                        make_uint4(e[4 * i], e[4 * i + 1], e[4 * i + 2], e[4 * i + 3]);
             }
             tc::fence_before();
             __syncwarp();
@@ -215,20 +224,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kEThreads, 1) hs_exp
                         }
                     }
                 }
-                if (E4M3 && h == 0) {  // the rotary channels of 8-bit rows, rounded to T
+                if (h == 0) {  // the rotary channels' tile (of 8-bit rows: scaled, and rounded to T)
                     for (int i = 32 * s + lane; i < 128 * 8; i += 128) {
-                        const int64_t token = mt * 256 + 128 * (int)rank + (i >> 3);
-                        if (token >= a.k_tokens) continue;
+                        const int tok = i >> 3;
+                        const int64_t token = mt * 256 + 128 * (int)rank + tok;
                         const uint8_t* src = static_cast<const uint8_t*>(a.rows) + token * a.row_stride;
-                        const float f = *reinterpret_cast<const float*>(src + HS_ROW8_SCALE);
-                        const uint2 v = *reinterpret_cast<const uint2*>(src + HS_LATENT_DIM + (i & 7) * 8);
-                        uint32_t e[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t two = ((k & 2 ? v.y : v.x) >> (16 * (k & 1))) & 0xffff;
-                            e[k] = pack2<T>(hs_e4m3_to_float(two & 0xff) * f, hs_e4m3_to_float(two >> 8) * f);
+                        uint4 e = make_uint4(0, 0, 0, 0);
+                        if (token < a.k_tokens) {
+                            if constexpr (!E4M3) {
+                                e = *reinterpret_cast<const uint4*>(src + (HS_LATENT_DIM + (i & 7) * 8) * 2);
+                            } else {
+                                const float f = *reinterpret_cast<const float*>(src + HS_ROW8_SCALE);
+                                const uint2 v = *reinterpret_cast<const uint2*>(src + HS_LATENT_DIM + (i & 7) * 8);
+                                auto two = [&](uint32_t w) { return pack2<T>(hs_e4m3_to_float(w & 0xff) * f, hs_e4m3_to_float(w >> 8 & 0xff) * f); };
+                                e = make_uint4(two(v.x), two(v.x >> 16), two(v.y), two(v.y >> 16));
+                            }
                         }
-                        *reinterpret_cast<uint4*>(g.rope_out + token * 128 + (i & 7) * 16) = make_uint4(e[0], e[1], e[2], e[3]);
+                        *reinterpret_cast<uint4*>(g.rope + (mt * 2 + rank) * kRope + tok * 128 + (((i & 7) ^ (tok & 7)) << 4)) = e;
                     }
                 }
                 tc::cp_async_commit();
@@ -296,14 +308,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kEThreads, 1) hs_exp
 
 // ---- (2) attention -----------------------------------------------------------------
 
-constexpr int kThreads = 12 * 32;  // warps 0-7 softmax (four a tile), 8-9 keys and queries, 10 values, 11 products
+constexpr int kThreads = 12 * 32;  // warps 0-7 softmax (four a tile), 8-9 queries, 10 keys and values, 11 products
 constexpr int kQTile = 3 * 16384;  // 3 blocks of 64 channels, [128 queries][128 B]
 constexpr int kOffK = 2 * kQTile;
 constexpr int kKStage = 3 * 16384;
 constexpr int kOffV = kOffK + 2 * kKStage;
-constexpr int kOffAux = kOffV + 2 * 16384;
+constexpr int kOffAux = kOffV + kBlock;  // values in two halves of 64 tokens
 struct Aux {
-    uint64_t qfull, kfull[2], kfree[2], vfull, vfree, sfull[2], pfull[2], odone[2], spare;
+    uint64_t qfull, kfull[2], kfree[2], vfull[2], vfree[2], sfull[2], pfull[2], odone[2], spare;
     uint32_t tmem;
     int dead;
     Start start;
@@ -327,11 +339,11 @@ struct Request {
         m = k1 > k0 ? (int)(k1 - k0) : 0;
     }
     __device__ int q_tiles() const { return (n + 255) / 256; }
-    // Key blocks that queries below `end` see.
+    // Key blocks, from the one that holds the request's first row, that queries below `end` see.
     __device__ int blocks_to(int end) const
     {
         const long long keys = (long long)(end < n ? end : n) + m - n;  // the last of them sees this many
-        return keys <= 0 ? 0 : (int)((keys + 127) / 128);
+        return keys <= 0 ? 0 : (int)(((k0 & 127) + keys + 127) / 128);
     }
     __device__ int blocks(int qt) const { return max(1, blocks_to(256 * qt + 256)); }
     __device__ long long blocks_of_head() const
@@ -383,82 +395,76 @@ struct Walk {
     }
 };
 
-template <typename T> __device__ void bring_keys(const Args& g, uint32_t sbase, Aux* x, int* error)
+// Queries of a piece: a tile a warp.
+template <typename T> __device__ void bring_queries(const Args& g, uint32_t sbase, Aux* x, int* error)
 {
     const hs_prefill_t& a = g.a;
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 8, ch = lane & 7;
     long long j = 0;
     Walk walk(a, x);
     while (walk.next()) {
-        // Q's readers are done: the last piece's products with keys.
+        // Q's readers are done: the earlier pieces' products with keys.  (A parity tells two phases
+        // apart, so the block before the last one is waited for first.)
         if (j >= 2) wait(tc::smem_addr(&x->kfree[j & 1]), ((j - 2) >> 1) & 1, &x->dead, error);
         if (j >= 1) wait(tc::smem_addr(&x->kfree[(j - 1) & 1]), ((j - 1) >> 1) & 1, &x->dead, error);
         const T* q = static_cast<const T*>(a.q) + walk.head * a.q_stride[1];
-        const int q_first = 256 * walk.tile;
-#pragma unroll 4
-        for (int n = 0; n < 32; ++n) {  // warp w: tile w's queries
-            const int r = n * 4 + (lane >> 3), at = q_first + 128 * w + r;
+        const int first = 256 * walk.tile + 128 * w;
+#pragma unroll 8
+        for (int n = 0; n < 32; ++n) {
+            const int r = n * 4 + (lane >> 3), at = first + r;
             const bool live = at < walk.r.n;
             const uint8_t* src = reinterpret_cast<const uint8_t*>(q + (walk.r.q0 + (live ? at : 0)) * a.q_stride[0]) + ch * 16;
             const uint32_t dst = sbase + w * kQTile + r * 128 + ((ch ^ (r & 7)) << 4);
 #pragma unroll
             for (int c = 0; c < 3; ++c) tc::cp_async16(dst + c * 16384, src + c * 128, live);
         }
-        const uint8_t* keys = g.keys + ((int64_t)walk.head * a.k_tokens + walk.r.k0) * HS_HEAD_DIM * 2 + ch * 16;
-        const uint8_t* rope = g.rope + walk.r.k0 * g.rope_stride + ch * 16;
-        for (int t = walk.t0; t < walk.t1; ++t, ++j) {
-            const int s = (int)(j & 1);
-            if (j >= 2) wait(tc::smem_addr(&x->kfree[s]), ((j - 2) >> 1) & 1, &x->dead, error);
-            const uint32_t stage = sbase + kOffK + s * kKStage;
-#pragma unroll 4
-            for (int n = 0; n < 16; ++n) {
-                const int r = 64 * w + n * 4 + (lane >> 3);
-                const int at = t * 128 + r;
-                const bool live = at < walk.r.m;
-                const uint32_t dst = stage + r * 128 + ((ch ^ (r & 7)) << 4);
-                const uint8_t* src = keys + (int64_t)(live ? at : 0) * (HS_HEAD_DIM * 2);
-                tc::cp_async16(dst, src, live);
-                tc::cp_async16(dst + 16384, src + 128, live);
-                tc::cp_async16(dst + 32768, rope + (live ? at : 0) * g.rope_stride, live);
-            }
-            tc::cp_async_commit();
-            tc::cp_async_wait<0>();
-            tc::fence_async_shared();
-            __syncwarp();
-            if (lane == 0) {
-                if (t == walk.t0) tc::mbar_arrive(tc::smem_addr(&x->qfull));
-                tc::mbar_arrive(tc::smem_addr(&x->kfull[s]));
-            }
-        }
+        tc::cp_async_commit();
+        tc::cp_async_wait<0>();
+        tc::fence_async_shared();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::smem_addr(&x->qfull));
+        // keep in step with the phases of kfree
+        for (int t = walk.t0; t < walk.t1; ++t, ++j)
+            if (j >= 2) wait(tc::smem_addr(&x->kfree[j & 1]), ((j - 2) >> 1) & 1, &x->dead, error);
     }
 }
 
-__device__ void bring_values(const Args& g, uint32_t sbase, Aux* x, int* error)
+// Keys and values: whole tiles, by one thread.
+__device__ void bring_tiles(const Args& g, uint32_t sbase, Aux* x, int* error)
 {
-    const hs_prefill_t& a = g.a;
-    const int lane = threadIdx.x & 31, ch = lane & 7;
     long long j = 0;
-    Walk walk(a, x);
+    Walk walk(g.a, x);
     while (walk.next()) {
-        const uint8_t* values = g.values + ((int64_t)walk.head * a.k_tokens + walk.r.k0) * HS_HEAD_DIM * 2 + ch * 16;
+        const int64_t block0 = walk.r.k0 / 128;
         for (int t = walk.t0; t < walk.t1; ++t, ++j) {
-            if (j >= 1) wait(tc::smem_addr(&x->vfree), (j - 1) & 1, &x->dead, error);
-#pragma unroll 4
-            for (int n = 0; n < 32; ++n) {
-                const int r = n * 4 + (lane >> 3);
-                const int at = t * 128 + r;
-                const bool live = at < walk.r.m;
-                const uint32_t dst = sbase + kOffV + r * 128 + ((ch ^ (r & 7)) << 4);
-                const uint8_t* src = values + (int64_t)(live ? at : 0) * (HS_HEAD_DIM * 2);
-                tc::cp_async16(dst, src, live);
-                tc::cp_async16(dst + 16384, src + 128, live);
+            // a block past the rows (a piece without any key) is any block that exists
+            const int64_t block = block0 + t < g.blocks ? block0 + t : 0, tile = walk.head * g.blocks + block;
+            const int s = (int)(j & 1);
+            if (j >= 2) wait(tc::smem_addr(&x->kfree[s]), ((j - 2) >> 1) & 1, &x->dead, error);
+            const uint32_t kbar = tc::smem_addr(&x->kfull[s]), stage = sbase + kOffK + s * kKStage;
+            if (g.blocks == 0) {  // no rows at all
+                tc::mbar_arrive(kbar);
+            } else {
+                tc::mbar_expect(kbar, kBlock + kRope);
+                tc::bulk_load(stage, g.keys + tile * kBlock, kBlock, kbar);
+                tc::bulk_load(stage + kBlock, g.rope + block * kRope, kRope, kbar);
             }
-            tc::cp_async_commit();
-            tc::cp_async_wait<0>();
-            tc::fence_async_shared();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(tc::smem_addr(&x->vfull));
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t vbar = tc::smem_addr(&x->vfull[h]);
+                if (j >= 1) wait(tc::smem_addr(&x->vfree[h]), (j - 1) & 1, &x->dead, error);
+                if (g.blocks == 0) {
+                    tc::mbar_arrive(vbar);
+                } else {
+                    tc::mbar_expect(vbar, kBlock / 2);
+                    tc::bulk_load(sbase + kOffV + h * (kBlock / 2), g.values + tile * kBlock + h * (kBlock / 2), kBlock / 2, vbar);
+                }
+            }
         }
+    }
+    // what is in flight has landed before the CTA ends (a piece's readers wait for it, unless one gave up)
+    if (j >= 1) {
+        wait(tc::smem_addr(&x->kfull[(j - 1) & 1]), ((j - 1) >> 1) & 1, &x->dead, error);
+        for (int h = 0; h < 2; ++h) tc::mbar_wait(tc::smem_addr(&x->vfull[h]), (j - 1) & 1);
     }
 }
 
@@ -479,15 +485,16 @@ template <typename T, int S, int ST> __device__ __forceinline__ void issue_qk(ui
     }
     __syncwarp();
 }
-template <typename T, int S> __device__ __forceinline__ void issue_pv(uint32_t sbase, uint32_t tmem, Aux* x, bool first)
+template <typename T, int S, int HALF> __device__ __forceinline__ void issue_pv(uint32_t sbase, uint32_t tmem, Aux* x, bool first)
 {
     constexpr uint32_t id = tc::inst_desc(HsType<T>::is_bf16, 128, 128, false, true);
-    const uint64_t v_desc = tc::smem_desc(sbase + kOffV, 16384, 1024);
+    const uint64_t v_desc = tc::smem_desc(sbase + kOffV + HALF * (kBlock / 2), 8192, 1024);
     if (tc::elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            tc::mma_ts(tmem + 256 * S + 128, tmem + 256 * S + 8 * k, v_desc + ((k * 2048) >> 4), id, !(first && k == 0));
-        tc::commit<1>(tc::smem_addr(&x->odone[S]));
+        for (int k = 0; k < 4; ++k)
+            tc::mma_ts(tmem + 256 * S + 128, tmem + 256 * S + 8 * (4 * HALF + k), v_desc + ((k * 2048) >> 4), id,
+                       HALF || !(first && k == 0));
+        if (HALF) tc::commit<1>(tc::smem_addr(&x->odone[S]));
     }
     __syncwarp();
 }
@@ -524,21 +531,36 @@ template <typename T> __device__ void multiply(const Args& g, uint32_t sbase, Au
         release(x->kfree[j & 1]);
         for (int t = walk.t0; t < walk.t1; ++t, ++j) {
             const int next = (int)((j + 1) & 1);
-            wait(tc::smem_addr(&x->vfull), j & 1, &x->dead, error);
-            if (t + 1 < walk.t1) wait(tc::smem_addr(&x->kfull[next]), ((j + 1) >> 1) & 1, &x->dead, error);
+            wait(tc::smem_addr(&x->vfull[0]), j & 1, &x->dead, error);
 #pragma unroll
             for (int tile = 0; tile < 2; ++tile) {
-                if (t < end[tile]) {
+                const bool active = t < end[tile];
+                if (active) {
                     wait(tc::smem_addr(&x->pfull[tile]), phase[tile], &x->dead, error);
                     phase[tile] ^= 1;
                     __syncwarp();
                     tc::fence_after();
                     if (tile == 0)
-                        issue_pv<T, 0>(sbase, tmem, x, t == walk.t0);
+                        issue_pv<T, 0, 0>(sbase, tmem, x, t == walk.t0);
                     else
-                        issue_pv<T, 1>(sbase, tmem, x, t == walk.t0);
+                        issue_pv<T, 1, 0>(sbase, tmem, x, t == walk.t0);
                 }
-                if (tile == 1) release(x->vfree);
+                if (tile == 1) release(x->vfree[0]);
+                if (tile == 0) wait(tc::smem_addr(&x->vfull[1]), j & 1, &x->dead, error);
+                if (active) {
+                    __syncwarp();
+                    tc::fence_after();
+                    if (tile == 0)
+                        issue_pv<T, 0, 1>(sbase, tmem, x, false);
+                    else
+                        issue_pv<T, 1, 1>(sbase, tmem, x, false);
+                }
+                if (tile == 1) release(x->vfree[1]);
+                if (tile == 0 && t + 1 < walk.t1) {
+                    wait(tc::smem_addr(&x->kfull[next]), ((j + 1) >> 1) & 1, &x->dead, error);
+                    __syncwarp();
+                    tc::fence_after();
+                }
                 if (t + 1 < end[tile]) scores(tile, next);
             }
             if (t + 1 < walk.t1) release(x->kfree[next]);
@@ -563,13 +585,15 @@ template <typename T> __device__ void soften(const Args& g, Aux* x, uint8_t* ws,
     while (walk.next()) {
         const int end = walk.end(tile);
         const int at = 256 * walk.tile + 128 * tile + row;
+        const int skip = (int)(walk.r.k0 & 127);                       // the first block's tokens of other requests
         const int keys = min(at + 1 + walk.r.m - walk.r.n, walk.r.m);  // the keys this query sees
         float ref = 0.f, sum = 0.f;
         bool seen = false;
         for (int t = walk.t0; t < end; ++t, ++mine) {
             wait(tc::smem_addr(&x->sfull[tile]), mine & 1, &x->dead, error);
             tc::fence_after();
-            const int some = keys - 128 * t;  // of this block's keys
+            const int some = keys + skip - 128 * t;  // this block's keys are [lead, some)
+            const int lead = t == 0 ? skip : 0;
             uint32_t v[4][32];  // the scores
 #pragma unroll
             for (int n = 0; n < 4; ++n) tc::tmem_ld32(tmem + 32 * n, v[n]);
@@ -580,10 +604,10 @@ template <typename T> __device__ void soften(const Args& g, Aux* x, uint8_t* ws,
                 if (flip)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[n][i] ^= 0x80000000u;
-                if (some < 32 * n + 32)
+                if (some < 32 * n + 32 || lead > 32 * n)
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if (32 * n + i >= some) v[n][i] = 0xff800000u;
+                        if (32 * n + i >= some || 32 * n + i < lead) v[n][i] = 0xff800000u;
                 tops[n] = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < 32; ++i) tops[n] = fmaxf(tops[n], __uint_as_float(v[n][i]));
@@ -736,11 +760,11 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) hs_prefill_
             x->dead = 0;
             reinterpret_cast<Start*>(ws + kOffStart)[i] = st;
             tc::mbar_init(tc::smem_addr(&x->qfull), 2);
-            tc::mbar_init(tc::smem_addr(&x->vfull), 1);
-            tc::mbar_init(tc::smem_addr(&x->vfree), 1);
             tc::mbar_init(tc::smem_addr(&x->spare), 1);
             for (int k = 0; k < 2; ++k) {
-                tc::mbar_init(tc::smem_addr(&x->kfull[k]), 2);
+                tc::mbar_init(tc::smem_addr(&x->kfull[k]), 1);
+                tc::mbar_init(tc::smem_addr(&x->vfull[k]), 1);
+                tc::mbar_init(tc::smem_addr(&x->vfree[k]), 1);
                 tc::mbar_init(tc::smem_addr(&x->kfree[k]), 1);
                 tc::mbar_init(tc::smem_addr(&x->sfull[k]), 1);
                 tc::mbar_init(tc::smem_addr(&x->pfull[k]), 4);
@@ -759,11 +783,11 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) hs_prefill_
         if (warp < 8)
             soften<T>(g, x, ws, error);
         else if (warp < 10)
-            bring_keys<T>(g, sbase, x, error);
-        else if (warp == 10)
-            bring_values(g, sbase, x, error);
-        else
+            bring_queries<T>(g, sbase, x, error);
+        else if (warp == 11)
             multiply<T>(g, sbase, x, error);
+        else if (lane == 0)
+            bring_tiles(g, sbase, x, error);
     }
     __syncwarp();
     tc::fence_before();
@@ -908,7 +932,8 @@ template <typename T, bool E4M3> cudaError_t launch(const Args& g, int sms, cuda
 
 size_t hs_prefill_workspace_bytes(int64_t k_tokens, int heads)
 {
-    return kOffKeys + (size_t)k_tokens * heads * 2 * HS_HEAD_DIM * 2 + (size_t)k_tokens * HS_ROPE_DIM * 2;
+    const size_t blocks = (size_t)((k_tokens + 255) / 256) * 2;
+    return kOffKeys + blocks * ((size_t)heads * 2 * kBlock + kRope);
 }
 
 cudaError_t hs_launch_prefill(const hs_prefill_t& a, cudaStream_t s)
@@ -921,11 +946,10 @@ cudaError_t hs_launch_prefill(const hs_prefill_t& a, cudaStream_t s)
     const bool e = a.row_format == HS_ROWS_E4M3;
     Args g;
     g.a = a;
+    g.blocks = (a.k_tokens + 255) / 256 * 2;
     g.keys = static_cast<uint8_t*>(a.workspace) + kOffKeys;
-    g.values = g.keys + (size_t)a.k_tokens * a.heads * HS_HEAD_DIM * 2;
-    g.rope_out = e ? g.values + (size_t)a.k_tokens * a.heads * HS_HEAD_DIM * 2 : nullptr;
-    g.rope = e ? g.rope_out : static_cast<const uint8_t*>(a.rows) + HS_LATENT_DIM * 2;
-    g.rope_stride = e ? HS_ROPE_DIM * 2 : a.row_stride;
+    g.values = g.keys + (size_t)g.blocks * a.heads * kBlock;
+    g.rope = g.values + (size_t)g.blocks * a.heads * kBlock;
     if (a.dtype == HS_TYPE_BF16)
         return e ? launch<__nv_bfloat16, true>(g, sms, s) : launch<__nv_bfloat16, false>(g, sms, s);
     return e ? launch<__half, true>(g, sms, s) : launch<__half, false>(g, sms, s);
