@@ -608,9 +608,10 @@ template <typename T> __device__ void soften(const Args& g, Aux* x, uint8_t* ws,
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         if (32 * n + i >= some || 32 * n + i < lead) v[n][i] = 0xff800000u;
-                tops[n] = -INFINITY;
+                tops[n] = fmaxf(__uint_as_float(v[n][0]), __uint_as_float(v[n][1]));
 #pragma unroll
-                for (int i = 0; i < 32; ++i) tops[n] = fmaxf(tops[n], __uint_as_float(v[n][i]));
+                for (int i = 2; i < 32; i += 2)
+                    tops[n] = tc::max3(tops[n], __uint_as_float(v[n][i]), __uint_as_float(v[n][i + 1]));
             }
             float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
             top *= c;
@@ -629,13 +630,13 @@ template <typename T> __device__ void soften(const Args& g, Aux* x, uint8_t* ws,
                     tc::fence_after();
                 }
 #pragma unroll 1
-                for (int n = 0; n < 128; n += 32) {
-                    uint32_t r[32];
-                    tc::tmem_ld32(tmem + 128 + n, r);
+                for (int n = 0; n < 128; n += 16) {
+                    uint32_t r[16];
+                    tc::tmem_ld16(tmem + 128 + n, r);
                     tc::tmem_wait_ld(r);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * keep);
-                    tc::tmem_st32(tmem + 128 + n, r);
+                    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * keep);
+                    tc::tmem_st16(tmem + 128 + n, r);
                 }
                 tc::tmem_wait_st();
             }
@@ -645,9 +646,11 @@ template <typename T> __device__ void soften(const Args& g, Aux* x, uint8_t* ws,
                 uint32_t e[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float p0 = tc::exp2_approx(fmaf(__uint_as_float(v[n][2 * i]), c, -ref));
-                    const float p1 = tc::exp2_approx(fmaf(__uint_as_float(v[n][2 * i + 1]), c, -ref));
-                    sums[i & 3] += p0 + p1;
+                    float p0, p1;
+                    tc::fma2(p0, p1, __uint_as_float(v[n][2 * i]), __uint_as_float(v[n][2 * i + 1]), c, -ref);
+                    p0 = tc::exp2_approx(p0);
+                    p1 = tc::exp2_approx(p1);
+                    tc::add2(sums[2 * (i & 1)], sums[2 * (i & 1) + 1], p0, p1);
                     e[i] = pack2<T>(p0, p1);
                 }
                 tc::tmem_st16(tmem + 16 * n, e);
