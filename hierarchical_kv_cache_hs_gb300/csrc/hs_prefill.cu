@@ -5,13 +5,14 @@
 //     product of k_tokens x 256 heads x 512.  A pair of SMs (cta_group::2, M = N =
 //     256) keeps 256 tokens' latents in shared memory and runs through heads; the
 //     weights' half that each CTA brings serves both.
-// (2) Attention: one SM takes 256 queries of a head as two tiles of 128 that take
-//     turns: while one tile's scores are softened, the other's products run.  The
-//     scores (then the weights, in place) and the sums of both tiles fill tensor
-//     memory; keys (192 channels) and values pass through shared memory in blocks
-//     of 128.
-// (3) Join: the blocks of all units (head, 256 queries) form one line that is cut
-//     into equal pieces, one an SM; units cut in two or more are joined.
+// (2) Attention: a pair of SMs takes 512 queries of a head as two tiles of 256 that
+//     take turns: while one tile's scores are softened, the other's products run.
+//     The scores (then the weights, in place) and the sums of both tiles fill tensor
+//     memory; keys (192 channels) and values pass through shared memory in blocks of
+//     128 tokens, which the expansion has written as they lie there; each CTA holds
+//     half of a block.
+// (3) Join: the blocks of all units (head, 512 queries) form one line that is cut
+//     into equal pieces, one a pair; units cut in two or more are joined.
 #include <type_traits>
 
 #include "hs_ops.h"
@@ -19,25 +20,25 @@
 
 namespace {
 
-constexpr int kMaxCtas = 152;
+constexpr int kMaxPairs = 76;
 
-// Workspace: an error word, where each CTA's piece starts, two partial results a
-// CTA; then, for blocks of 128 tokens (counted over all requests, the tail padded to
+// Workspace: an error word, where each pair's piece starts, two partial results a
+// pair; then, for blocks of 128 tokens (counted over all requests, the tail padded to
 // 256 tokens with zeros), the tiles that the attention copies to shared memory as
 // they are, rows of 128 bytes with the 128-byte swizzle:
-//   keys    [head][block][2 x 64 channels][128 tokens]
-//   values  [head][block][2 x 64 tokens][2 x 64 channels][64 tokens]
+//   keys    [head][block][2 x 64 tokens][2 x 64 channels][64 tokens]
+//   values  [head][block][2 x 64 channels][128 tokens]
 //   rotary  [block][128 tokens]
 struct Start {
     int b, h, qt, kb;
 };
 struct Partial {
-    float o[2][128][128];  // [tile][channel][query]
-    float ref[2][128], sum[2][128];
+    float o[4][128][128];  // [128 queries][channel][query]
+    float ref[4][128], sum[4][128];
 };
 constexpr size_t kOffStart = 256;
-constexpr size_t kOffPartial = kOffStart + sizeof(Start) * kMaxCtas;
-constexpr size_t kOffKeys = kOffPartial + sizeof(Partial) * 2 * kMaxCtas;
+constexpr size_t kOffPartial = kOffStart + sizeof(Start) * (kMaxPairs + 4);
+constexpr size_t kOffKeys = kOffPartial + sizeof(Partial) * 2 * kMaxPairs;
 
 constexpr int kBlock = 32768;  // keys, or values, of a block and head
 constexpr int kRope = 16384;   // rotary channels of a block
@@ -180,8 +181,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kEThreads, 1) hs_exp
                 // 32 channels are half a row of the tile
                 const int64_t tile = h * g.blocks + mt * 2 + rank;
                 const int tok = threadIdx.x, cb = c >> 1 & 1;
-                uint8_t* row = c >= 4 ? g.values + tile * kBlock + (tok >> 6) * 16384 + cb * 8192 + (tok & 63) * 128
-                                      : g.keys + tile * kBlock + cb * 16384 + tok * 128;
+                uint8_t* row = c >= 4 ? g.values + tile * kBlock + cb * 16384 + tok * 128
+                                      : g.keys + tile * kBlock + (tok >> 6) * 16384 + cb * 8192 + (tok & 63) * 128;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     *reinterpret_cast<uint4*>(row + ((((c & 1) * 4 + i) ^ (tok & 7)) << 4)) =
@@ -309,13 +310,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kEThreads, 1) hs_exp
 // ---- (2) attention -----------------------------------------------------------------
 
 constexpr int kThreads = 12 * 32;  // warps 0-7 softmax (four a tile), 8-9 queries, 10 keys and values, 11 products
-constexpr int kQTile = 3 * 16384;  // 3 blocks of 64 channels, [128 queries][128 B]
+constexpr int kStages = 3;
+constexpr int kQTile = 3 * 16384;                 // 3 blocks of 64 channels, [128 queries][128 B]
 constexpr int kOffK = 2 * kQTile;
-constexpr int kKStage = 3 * 16384;
-constexpr int kOffV = kOffK + 2 * kKStage;
-constexpr int kOffAux = kOffV + kBlock;  // values in two halves of 64 tokens
+constexpr int kKStage = kBlock / 2 + kRope / 2;   // 64 tokens: 3 blocks of 64 channels, [64][128 B]
+constexpr int kOffV = kOffK + kStages * kKStage;
+constexpr int kVStage = kBlock / 2;               // 64 channels of 128 tokens
+constexpr int kOffAux = kOffV + kStages * kVStage;
 struct Aux {
-    uint64_t qfull, kfull[2], kfree[2], vfull[2], vfree[2], sfull[2], pfull[2], odone[2], spare;
+    // kfull, vfull: this CTA's half; kpeer, vpeer (first CTA): the other's
+    uint64_t qfull, qfree, kfull[kStages], kpeer[kStages], kfree[kStages], vfull[kStages], vpeer[kStages], vfree[kStages];
+    uint64_t sfull[2], pfull[2], odone[2], spare;
     uint32_t tmem;
     int dead;
     Start start;
@@ -325,6 +330,16 @@ constexpr int kSmem = kOffAux + (int)sizeof(Aux);
 static_assert(kSmem <= 232448, "shared memory");
 
 // Tensor memory of tile s: scores (then weights) at 256 s, sums at 256 s + 128.
+
+// Stage and phase of the block after this one.
+struct Ring {
+    int s = 0;
+    uint32_t phase = 0;
+    __device__ void step()
+    {
+        if (++s == kStages) s = 0, phase ^= 1;
+    }
+};
 
 struct Request {
     long long q0, k0;
@@ -338,14 +353,14 @@ struct Request {
         n = q1 > q0 ? (int)(q1 - q0) : 0;
         m = k1 > k0 ? (int)(k1 - k0) : 0;
     }
-    __device__ int q_tiles() const { return (n + 255) / 256; }
+    __device__ int q_tiles() const { return (n + 511) / 512; }
     // Key blocks, from the one that holds the request's first row, that queries below `end` see.
     __device__ int blocks_to(int end) const
     {
         const long long keys = (long long)(end < n ? end : n) + m - n;  // the last of them sees this many
         return keys <= 0 ? 0 : (int)(((k0 & 127) + keys + 127) / 128);
     }
-    __device__ int blocks(int qt) const { return max(1, blocks_to(256 * qt + 256)); }
+    __device__ int blocks(int qt) const { return max(1, blocks_to(512 * qt + 512)); }
     __device__ long long blocks_of_head() const
     {
         long long t = 0;
@@ -389,29 +404,27 @@ struct Walk {
     // Blocks that tile s of the piece works on: [t0, end(s)).
     __device__ int end(int s) const
     {
-        if (256 * tile + 128 * s >= r.n) return t0;
-        const int e = r.blocks_to(256 * tile + 128 * s + 128);
+        if (512 * tile + 256 * s >= r.n) return t0;
+        const int e = r.blocks_to(512 * tile + 256 * s + 256);
         return e < t0 ? t0 : e < t1 ? e : t1;
     }
 };
 
-// Queries of a piece: a tile a warp.
-template <typename T> __device__ void bring_queries(const Args& g, uint32_t sbase, Aux* x, int* error)
+// Queries of a piece: this CTA's 128 of a tile a warp.
+template <typename T> __device__ void bring_queries(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int* error)
 {
     const hs_prefill_t& a = g.a;
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 8, ch = lane & 7;
-    long long j = 0;
+    const uint32_t qfull = tc::map_to_rank(tc::smem_addr(&x->qfull), 0);
     Walk walk(a, x);
-    while (walk.next()) {
-        // Q's readers are done: the earlier pieces' products with keys.  (A parity tells two phases
-        // apart, so the block before the last one is waited for first.)
-        if (j >= 2) wait(tc::smem_addr(&x->kfree[j & 1]), ((j - 2) >> 1) & 1, &x->dead, error);
-        if (j >= 1) wait(tc::smem_addr(&x->kfree[(j - 1) & 1]), ((j - 1) >> 1) & 1, &x->dead, error);
+    for (int pieces = 0; walk.next(); ++pieces) {
+        // Q's readers, the last piece's products with keys, are done.
+        if (pieces) wait(tc::smem_addr(&x->qfree), (pieces - 1) & 1, &x->dead, error);
         const T* q = static_cast<const T*>(a.q) + walk.head * a.q_stride[1];
-        const int first = 256 * walk.tile + 128 * w;
+        const int q0 = 512 * walk.tile + 256 * w + 128 * (int)rank;
 #pragma unroll 8
         for (int n = 0; n < 32; ++n) {
-            const int r = n * 4 + (lane >> 3), at = first + r;
+            const int r = n * 4 + (lane >> 3), at = q0 + r;
             const bool live = at < walk.r.n;
             const uint8_t* src = reinterpret_cast<const uint8_t*>(q + (walk.r.q0 + (live ? at : 0)) * a.q_stride[0]) + ch * 16;
             const uint32_t dst = sbase + w * kQTile + r * 128 + ((ch ^ (r & 7)) << 4);
@@ -422,148 +435,158 @@ template <typename T> __device__ void bring_queries(const Args& g, uint32_t sbas
         tc::cp_async_wait<0>();
         tc::fence_async_shared();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(tc::smem_addr(&x->qfull));
-        // keep in step with the phases of kfree
-        for (int t = walk.t0; t < walk.t1; ++t, ++j)
-            if (j >= 2) wait(tc::smem_addr(&x->kfree[j & 1]), ((j - 2) >> 1) & 1, &x->dead, error);
+        if (lane == 0) tc::mbar_arrive_cluster(qfull);
     }
 }
 
-// Keys and values: whole tiles, by one thread.
-__device__ void bring_tiles(const Args& g, uint32_t sbase, Aux* x, int* error)
+// Keys and values: this CTA's half of whole tiles, by one thread.
+__device__ void bring_tiles(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int* error)
 {
     long long j = 0;
+    Ring ring, last;
     Walk walk(g.a, x);
     while (walk.next()) {
         const int64_t block0 = walk.r.k0 / 128;
         for (int t = walk.t0; t < walk.t1; ++t, ++j) {
             // a block past the rows (a piece without any key) is any block that exists
             const int64_t block = block0 + t < g.blocks ? block0 + t : 0, tile = walk.head * g.blocks + block;
-            const int s = (int)(j & 1);
-            if (j >= 2) wait(tc::smem_addr(&x->kfree[s]), ((j - 2) >> 1) & 1, &x->dead, error);
-            const uint32_t kbar = tc::smem_addr(&x->kfull[s]), stage = sbase + kOffK + s * kKStage;
+            const int s = ring.s;
+            const uint32_t kbar = tc::smem_addr(&x->kfull[s]), vbar = tc::smem_addr(&x->vfull[s]);
+            const uint32_t kdst = sbase + kOffK + s * kKStage, vdst = sbase + kOffV + s * kVStage;
+            if (j >= kStages) wait(tc::smem_addr(&x->kfree[s]), ring.phase ^ 1, &x->dead, error);
             if (g.blocks == 0) {  // no rows at all
                 tc::mbar_arrive(kbar);
             } else {
-                tc::mbar_expect(kbar, kBlock + kRope);
-                tc::bulk_load(stage, g.keys + tile * kBlock, kBlock, kbar);
-                tc::bulk_load(stage + kBlock, g.rope + block * kRope, kRope, kbar);
+                tc::mbar_expect(kbar, kKStage);
+                tc::bulk_load(kdst, g.keys + tile * kBlock + rank * (kBlock / 2), kBlock / 2, kbar);
+                tc::bulk_load(kdst + kBlock / 2, g.rope + block * kRope + rank * (kRope / 2), kRope / 2, kbar);
             }
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t vbar = tc::smem_addr(&x->vfull[h]);
-                if (j >= 1) wait(tc::smem_addr(&x->vfree[h]), (j - 1) & 1, &x->dead, error);
-                if (g.blocks == 0) {
-                    tc::mbar_arrive(vbar);
-                } else {
-                    tc::mbar_expect(vbar, kBlock / 2);
-                    tc::bulk_load(sbase + kOffV + h * (kBlock / 2), g.values + tile * kBlock + h * (kBlock / 2), kBlock / 2, vbar);
-                }
+            if (j >= kStages) wait(tc::smem_addr(&x->vfree[s]), ring.phase ^ 1, &x->dead, error);
+            if (g.blocks == 0) {
+                tc::mbar_arrive(vbar);
+            } else {
+                tc::mbar_expect(vbar, kVStage);
+                tc::bulk_load(vdst, g.values + tile * kBlock + rank * kVStage, kVStage, vbar);
             }
+            last = ring;
+            ring.step();
         }
     }
-    // what is in flight has landed before the CTA ends (a piece's readers wait for it, unless one gave up)
-    if (j >= 1) {
-        wait(tc::smem_addr(&x->kfull[(j - 1) & 1]), ((j - 1) >> 1) & 1, &x->dead, error);
-        for (int h = 0; h < 2; ++h) tc::mbar_wait(tc::smem_addr(&x->vfull[h]), (j - 1) & 1);
+    // What is in flight has landed before the CTA ends; after a wait that gave up nothing else sees to it.
+    if (j >= 1 && *(volatile int*)&x->dead)
+        for (int s = 0; s < kStages && s < j; ++s) {
+            const uint32_t phase = s <= last.s ? last.phase : last.phase ^ 1;
+            tc::mbar_wait(tc::smem_addr(&x->kfull[s]), phase);
+            tc::mbar_wait(tc::smem_addr(&x->vfull[s]), phase);
+        }
+}
+
+// The second CTA tells the first that its half of a block has come.
+__device__ void forward(Aux* x, int* error)
+{
+    Ring ring;
+    const long long n = x->count;
+    for (long long j = 0; j < n; ++j, ring.step()) {
+        wait(tc::smem_addr(&x->kfull[ring.s]), ring.phase, &x->dead, error);
+        tc::mbar_arrive_cluster(tc::map_to_rank(tc::smem_addr(&x->kpeer[ring.s]), 0));
+        wait(tc::smem_addr(&x->vfull[ring.s]), ring.phase, &x->dead, error);
+        tc::mbar_arrive_cluster(tc::map_to_rank(tc::smem_addr(&x->vpeer[ring.s]), 0));
     }
 }
 
-// Q K^T of tile S with the keys in stage ST, and P V of tile S.
-template <typename T, int S, int ST> __device__ __forceinline__ void issue_qk(uint32_t sbase, uint32_t tmem, Aux* x)
+// Q K^T of tile S with the keys at k_desc, and P V of tile S with the values at v_desc.
+template <typename T, int S> __device__ __forceinline__ void issue_qk(uint32_t sbase, uint32_t tmem, uint64_t k_desc, Aux* x)
 {
-    constexpr uint32_t id = tc::inst_desc(HsType<T>::is_bf16, 128, 128, false, false);
+    constexpr uint32_t id = tc::inst_desc(HsType<T>::is_bf16, 256, 128, false, false);
     const uint64_t q_desc = tc::smem_desc(sbase + S * kQTile, 16, 1024);
-    const uint64_t k_desc = tc::smem_desc(sbase + kOffK + ST * kKStage, 16, 1024);
     if (tc::elect_one()) {
 #pragma unroll
         for (int c = 0; c < 3; ++c)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                tc::mma_ss<1>(tmem + 256 * S, q_desc + ((c * 16384 + k * 32) >> 4), k_desc + ((c * 16384 + k * 32) >> 4), id,
+                tc::mma_ss<2>(tmem + 256 * S, q_desc + ((c * 16384 + k * 32) >> 4), k_desc + ((c * 8192 + k * 32) >> 4), id,
                               (c | k) != 0);
-        tc::commit<1>(tc::smem_addr(&x->sfull[S]));
+        tc::commit<2>(tc::smem_addr(&x->sfull[S]));
     }
     __syncwarp();
 }
-template <typename T, int S, int HALF> __device__ __forceinline__ void issue_pv(uint32_t sbase, uint32_t tmem, Aux* x, bool first)
+template <typename T, int S> __device__ __forceinline__ void issue_pv(uint32_t tmem, uint64_t v_desc, Aux* x, bool first)
 {
-    constexpr uint32_t id = tc::inst_desc(HsType<T>::is_bf16, 128, 128, false, true);
-    const uint64_t v_desc = tc::smem_desc(sbase + kOffV + HALF * (kBlock / 2), 8192, 1024);
+    constexpr uint32_t id = tc::inst_desc(HsType<T>::is_bf16, 256, 128, false, true);
     if (tc::elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            tc::mma_ts(tmem + 256 * S + 128, tmem + 256 * S + 8 * (4 * HALF + k), v_desc + ((k * 2048) >> 4), id,
-                       HALF || !(first && k == 0));
-        if (HALF) tc::commit<1>(tc::smem_addr(&x->odone[S]));
+        for (int k = 0; k < 8; ++k)
+            tc::mma_ts<2>(tmem + 256 * S + 128, tmem + 256 * S + 8 * k, v_desc + ((k * 2048) >> 4), id, !(first && k == 0));
+        tc::commit<2>(tc::smem_addr(&x->odone[S]));
     }
     __syncwarp();
 }
 
-// The products, issued by one warp in the order in which the tiles take turns: P V
-// of a block, then Q K^T of the next one, of tile 0 and then of tile 1.  (Issued by
-// a warp a tile, the two tiles' products ran interleaved, both tiles' scores came
-// at the same time, and the tensor core idled through both softmaxes.)
+// The products, issued by one warp of the first CTA in the order in which the tiles
+// take turns: P V of a block, then Q K^T of the next one, of tile 0 and then of tile
+// 1.  (Issued by a warp a tile, the two tiles' products ran interleaved, both tiles'
+// scores came at the same time, and the tensor core idled through both softmaxes.)
 template <typename T> __device__ void multiply(const Args& g, uint32_t sbase, Aux* x, int* error)
 {
     const uint32_t tmem = __shfl_sync(~0u, x->tmem, 0);
-    long long j = 0;
+    const uint64_t k_base = tc::smem_desc(sbase + kOffK, 16, 1024), v_base = tc::smem_desc(sbase + kOffV, 16384, 1024);
     int pieces = 0;
     uint32_t phase[2] = {0, 0};  // of pfull
+    Ring now, next;              // the block of P V, and of Q K^T
     Walk walk(g.a, x);
-    auto release = [](uint64_t& bar) {  // when all products so far are complete
-        if (tc::elect_one()) tc::commit<1>(tc::smem_addr(&bar));
+    auto release = [](uint64_t& bar) {  // in both CTAs, when all products so far are complete
+        if (tc::elect_one()) tc::commit<2>(tc::smem_addr(&bar));
         __syncwarp();
     };
-    auto scores = [&](int tile, int stage) {
-        if (tile == 0)
-            stage ? issue_qk<T, 0, 1>(sbase, tmem, x) : issue_qk<T, 0, 0>(sbase, tmem, x);
-        else
-            stage ? issue_qk<T, 1, 1>(sbase, tmem, x) : issue_qk<T, 1, 0>(sbase, tmem, x);
+    auto keys_come = [&]() {
+        wait(tc::smem_addr(&x->kfull[next.s]), next.phase, &x->dead, error);
+        wait(tc::smem_addr(&x->kpeer[next.s]), next.phase, &x->dead, error);
+        __syncwarp();
+        tc::fence_after();
     };
     while (walk.next()) {
         const int end[2] = {walk.end(0), walk.end(1)};
         wait(tc::smem_addr(&x->qfull), pieces++ & 1, &x->dead, error);
-        wait(tc::smem_addr(&x->kfull[j & 1]), (j >> 1) & 1, &x->dead, error);
-        __syncwarp();
-        tc::fence_after();
-        for (int tile = 0; tile < 2; ++tile)
-            if (walk.t0 < end[tile]) scores(tile, (int)(j & 1));
-        release(x->kfree[j & 1]);
-        for (int t = walk.t0; t < walk.t1; ++t, ++j) {
-            const int next = (int)((j + 1) & 1);
-            wait(tc::smem_addr(&x->vfull[0]), j & 1, &x->dead, error);
+        keys_come();
+        uint64_t k_desc = k_base + next.s * (kKStage >> 4);
+        if (walk.t0 < end[0]) issue_qk<T, 0>(sbase, tmem, k_desc, x);
+        if (walk.t0 < end[1]) issue_qk<T, 1>(sbase, tmem, k_desc, x);
+        release(x->kfree[next.s]);
+        if (walk.t1 - walk.t0 == 1) release(x->qfree);
+        next.step();
+        for (int t = walk.t0; t < walk.t1; ++t) {
+            const bool more = t + 1 < walk.t1;
+            wait(tc::smem_addr(&x->vfull[now.s]), now.phase, &x->dead, error);
+            wait(tc::smem_addr(&x->vpeer[now.s]), now.phase, &x->dead, error);
+            const uint64_t v_desc = v_base + now.s * (kVStage >> 4);
+            k_desc = k_base + next.s * (kKStage >> 4);
 #pragma unroll
             for (int tile = 0; tile < 2; ++tile) {
-                const bool active = t < end[tile];
-                if (active) {
+                if (t < end[tile]) {
                     wait(tc::smem_addr(&x->pfull[tile]), phase[tile], &x->dead, error);
                     phase[tile] ^= 1;
                     __syncwarp();
                     tc::fence_after();
                     if (tile == 0)
-                        issue_pv<T, 0, 0>(sbase, tmem, x, t == walk.t0);
+                        issue_pv<T, 0>(tmem, v_desc, x, t == walk.t0);
                     else
-                        issue_pv<T, 1, 0>(sbase, tmem, x, t == walk.t0);
+                        issue_pv<T, 1>(tmem, v_desc, x, t == walk.t0);
                 }
-                if (tile == 1) release(x->vfree[0]);
-                if (tile == 0) wait(tc::smem_addr(&x->vfull[1]), j & 1, &x->dead, error);
-                if (active) {
-                    __syncwarp();
-                    tc::fence_after();
+                if (tile == 1) release(x->vfree[now.s]);
+                if (tile == 0 && more) keys_come();
+                if (t + 1 < end[tile]) {
                     if (tile == 0)
-                        issue_pv<T, 0, 1>(sbase, tmem, x, false);
+                        issue_qk<T, 0>(sbase, tmem, k_desc, x);
                     else
-                        issue_pv<T, 1, 1>(sbase, tmem, x, false);
+                        issue_qk<T, 1>(sbase, tmem, k_desc, x);
                 }
-                if (tile == 1) release(x->vfree[1]);
-                if (tile == 0 && t + 1 < walk.t1) {
-                    wait(tc::smem_addr(&x->kfull[next]), ((j + 1) >> 1) & 1, &x->dead, error);
-                    __syncwarp();
-                    tc::fence_after();
-                }
-                if (t + 1 < end[tile]) scores(tile, next);
             }
-            if (t + 1 < walk.t1) release(x->kfree[next]);
+            now.step();
+            if (more) {
+                release(x->kfree[next.s]);
+                if (t + 2 == walk.t1) release(x->qfree);
+                next.step();
+            }
         }
     }
     if (*(volatile int*)&x->dead) {  // what was issued must be complete before tensor memory is freed
@@ -573,18 +596,19 @@ template <typename T> __device__ void multiply(const Args& g, uint32_t sbase, Au
 }
 
 // Softmax of one tile: a query a thread.
-template <typename T> __device__ void soften(const Args& g, Aux* x, uint8_t* ws, int* error)
+template <typename T> __device__ void soften(const Args& g, Aux* x, uint32_t rank, uint8_t* ws, int* error)
 {
     const hs_prefill_t& a = g.a;
     const int lane = threadIdx.x & 31, tile = threadIdx.x >> 7, row = threadIdx.x & 127;
     const uint32_t tmem = x->tmem + 256 * tile + ((uint32_t)((threadIdx.x >> 5) & 3) << 21);
     const bool flip = a.scale < 0.f;  // scores are negated then, so that the scale is not negative
     const float c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f);  // not 0: a masked score stays -inf
+    const uint32_t pfull = tc::map_to_rank(tc::smem_addr(&x->pfull[tile]), 0);
     long long mine = 0;
     Walk walk(a, x);
     while (walk.next()) {
         const int end = walk.end(tile);
-        const int at = 256 * walk.tile + 128 * tile + row;
+        const int at = 512 * walk.tile + 256 * tile + 128 * (int)rank + row;
         const int skip = (int)(walk.r.k0 & 127);                       // the first block's tokens of other requests
         const int keys = min(at + 1 + walk.r.m - walk.r.n, walk.r.m);  // the keys this query sees
         float ref = 0.f, sum = 0.f;
@@ -659,7 +683,7 @@ template <typename T> __device__ void soften(const Args& g, Aux* x, uint8_t* ws,
             tc::tmem_wait_st();
             tc::fence_before();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(tc::smem_addr(&x->pfull[tile]));
+            if (lane == 0) tc::mbar_arrive_cluster(pfull);
         }
         // The piece's end.
         const bool worked = end > walk.t0;
@@ -669,7 +693,8 @@ template <typename T> __device__ void soften(const Args& g, Aux* x, uint8_t* ws,
         }
         const bool live = at < walk.r.n;
         const bool whole = walk.t0 == 0 && walk.t1 == walk.blocks;
-        Partial* part = reinterpret_cast<Partial*>(ws + kOffPartial) + 2 * blockIdx.x + (walk.t0 == 0 ? 1 : 0);
+        Partial* part = reinterpret_cast<Partial*>(ws + kOffPartial) + 2 * (blockIdx.x >> 1) + (walk.t0 == 0 ? 1 : 0);
+        const int quarter = 2 * tile + (int)rank;
         const bool some = worked && (sum > 0.f || sum != sum);
         const float inv = some ? 1.f / sum : 0.f;
         T* out = static_cast<T*>(a.out) + (walk.r.q0 + at) * a.out_stride[0] + walk.head * a.out_stride[1];
@@ -690,13 +715,13 @@ template <typename T> __device__ void soften(const Args& g, Aux* x, uint8_t* ws,
                 }
             } else if (worked) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) part->o[tile][n + i][row] = __uint_as_float(r[i]);
+                for (int i = 0; i < 32; ++i) part->o[quarter][n + i][row] = __uint_as_float(r[i]);
             }
         }
         if (live) {
             if (!whole) {
-                part->ref[tile][row] = ref;
-                part->sum[tile][row] = worked ? sum : 0.f;
+                part->ref[quarter][row] = ref;
+                part->sum[quarter][row] = worked ? sum : 0.f;
             } else if (a.lse) {
                 a.lse[(walk.r.q0 + at) * a.heads + walk.head] = some ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
             }
@@ -705,24 +730,27 @@ template <typename T> __device__ void soften(const Args& g, Aux* x, uint8_t* ws,
     }
 }
 
-template <typename T> __global__ void __launch_bounds__(kThreads, 1) hs_prefill_kernel(const __grid_constant__ Args g)
+template <typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_prefill_kernel(const __grid_constant__ Args g)
 {
     extern __shared__ __align__(1024) uint8_t base[];
     const uint32_t sbase = tc::smem_addr(base);
     Aux* x = reinterpret_cast<Aux*>(base + kOffAux);
     const hs_prefill_t& a = g.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = tc::cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     int* error = reinterpret_cast<int*>(ws);
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (warp == 0) tc::tmem_alloc<1>(tc::smem_addr(&x->tmem), 512);
+    if (warp == 0) tc::tmem_alloc<2>(tc::smem_addr(&x->tmem), 512);
     if (warp == 11) {
-        // This CTA's piece of the line of blocks.
+        // This pair's piece of the line of blocks.
         long long total = 0;
         for (int b = lane; b < a.batch; b += 32) total += Request(a, b).blocks_of_head() * a.heads;
         for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
-        const long long n = total < gridDim.x ? total : gridDim.x, i = blockIdx.x;
+        const long long n = total < pairs ? total : pairs, i = pair;
         const long long lo = i < n ? total * i / n : 0, hi = i < n ? total * (i + 1) / n : 0;
         Start st = {-1, 0, 0, 0};
         long long before = 0;
@@ -761,51 +789,60 @@ template <typename T> __global__ void __launch_bounds__(kThreads, 1) hs_prefill_
             if (st.b < 0) x->start.b = 0;
             x->count = st.b < 0 ? 0 : hi - lo;
             x->dead = 0;
-            reinterpret_cast<Start*>(ws + kOffStart)[i] = st;
-            tc::mbar_init(tc::smem_addr(&x->qfull), 2);
-            tc::mbar_init(tc::smem_addr(&x->spare), 1);
-            for (int k = 0; k < 2; ++k) {
+            if (rank == 0) reinterpret_cast<Start*>(ws + kOffStart)[i] = st;
+            tc::mbar_init(tc::smem_addr(&x->qfull), 4);
+            tc::mbar_init(tc::smem_addr(&x->qfree), 1);
+            for (int k = 0; k < kStages; ++k) {
                 tc::mbar_init(tc::smem_addr(&x->kfull[k]), 1);
-                tc::mbar_init(tc::smem_addr(&x->vfull[k]), 1);
-                tc::mbar_init(tc::smem_addr(&x->vfree[k]), 1);
+                tc::mbar_init(tc::smem_addr(&x->kpeer[k]), 1);
                 tc::mbar_init(tc::smem_addr(&x->kfree[k]), 1);
+                tc::mbar_init(tc::smem_addr(&x->vfull[k]), 1);
+                tc::mbar_init(tc::smem_addr(&x->vpeer[k]), 1);
+                tc::mbar_init(tc::smem_addr(&x->vfree[k]), 1);
+            }
+            for (int k = 0; k < 2; ++k) {
                 tc::mbar_init(tc::smem_addr(&x->sfull[k]), 1);
-                tc::mbar_init(tc::smem_addr(&x->pfull[k]), 4);
+                tc::mbar_init(tc::smem_addr(&x->pfull[k]), 8);
                 tc::mbar_init(tc::smem_addr(&x->odone[k]), 1);
             }
+            tc::mbar_init(tc::smem_addr(&x->spare), 1);
             tc::mbar_init_fence();
         }
     }
     tc::fence_before();
     __syncwarp();
     __syncthreads();
+    tc::cluster_sync();
     tc::fence_after();
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the expansion's keys and values
 
     if (x->count > 0) {
         if (warp < 8)
-            soften<T>(g, x, ws, error);
+            soften<T>(g, x, rank, ws, error);
         else if (warp < 10)
-            bring_queries<T>(g, sbase, x, error);
-        else if (warp == 11)
+            bring_queries<T>(g, sbase, x, rank, error);
+        else if (warp == 11 && rank == 0)
             multiply<T>(g, sbase, x, error);
-        else if (lane == 0)
-            bring_tiles(g, sbase, x, error);
+        else if (warp == 11 && lane == 0)
+            forward(x, error);
+        else if (warp == 10 && lane == 0)
+            bring_tiles(g, sbase, x, rank, error);
     }
     __syncwarp();
     tc::fence_before();
     __syncthreads();
+    tc::cluster_sync();
     tc::fence_after();
-    if (warp == 0) tc::tmem_free<1>(x->tmem, 512);
+    if (warp == 0) tc::tmem_free<2>(x->tmem, 512);
 }
 
 // ---- (3) join ------------------------------------------------------------------------
 
-// Block x takes the x-th unit that several CTAs worked on (found at the first start
-// of a piece inside it), one tile of it, 16 channels.  Four groups of 128 threads,
+// Block x takes the x-th unit that several pairs worked on (found at the first start
+// of a piece inside it), 128 of its queries, 16 channels.  Four groups of 128 threads,
 // one a query, take every fourth piece; the order of the sums is fixed.
 constexpr int kJoinCols = 16;
-template <typename T> __global__ void __launch_bounds__(512) hs_prefill_join_kernel(const __grid_constant__ Args g, int ctas)
+template <typename T> __global__ void __launch_bounds__(512) hs_prefill_join_kernel(const __grid_constant__ Args g, int pairs)
 {
     __shared__ float tops[4][128], sums[4][128], cols[3][kJoinCols][128];
     __shared__ int counts[8], first_cut;
@@ -819,7 +856,7 @@ template <typename T> __global__ void __launch_bounds__(512) hs_prefill_join_ker
     auto same = [](const Start& p, const Start& q) { return p.b == q.b && p.h == q.h && p.qt == q.qt; };
     Start mine = {-1, 0, 0, 0};
     bool inside = false, cut = false;
-    if (t > 0 && t < ctas) {
+    if (t > 0 && t < pairs) {
         mine = start[t];
         const Start prev = start[t - 1];
         inside = mine.b >= 0 && mine.kb > 0;
@@ -838,21 +875,21 @@ template <typename T> __global__ void __launch_bounds__(512) hs_prefill_join_ker
     const Start unit = start[first_cut];
     const int first = first_cut - 1, last = first + __syncthreads_count(inside && same(mine, unit));
     const Request r(a, unit.b);
-    const int tile = blockIdx.y, c0 = kJoinCols * blockIdx.z;
+    const int quarter = blockIdx.y, c0 = kJoinCols * blockIdx.z;
     const int row = t & 127, group = t >> 7;
-    const int at = 256 * unit.qt + 128 * tile + row;
-    if (256 * unit.qt + 128 * tile >= r.n) return;
+    const int at = 512 * unit.qt + 128 * quarter + row;
+    if (512 * unit.qt + 128 * quarter >= r.n) return;
     const bool live = at < r.n;
     float acc[kJoinCols] = {}, sum = 0.f, top = -INFINITY;
     if (live)
 #pragma unroll 2
         for (int n = first + group; n <= last; n += 4) {
             const Partial& q = parts[2 * n + (n == first)];
-            const float ref = q.ref[tile][row], l = q.sum[tile][row];
+            const float ref = q.ref[quarter][row], l = q.sum[quarter][row];
             if (l == 0.f) continue;  // no key counted
             float o[kJoinCols];
 #pragma unroll
-            for (int k = 0; k < kJoinCols; ++k) o[k] = q.o[tile][c0 + k][row];
+            for (int k = 0; k < kJoinCols; ++k) o[k] = q.o[quarter][c0 + k][row];
             const float up = fmaxf(top, ref);
             const float keep = tc::exp2_approx(top - up), w = tc::exp2_approx(ref - up);
             top = up;
@@ -906,7 +943,7 @@ cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size
     return cudaLaunchKernelEx(&cfg, kernel, values...);
 }
 
-template <typename T, bool E4M3> cudaError_t launch(const Args& g, int sms, cudaStream_t s)
+template <typename T, bool E4M3> cudaError_t launch(const Args& g, int pairs, cudaStream_t s)
 {
     const hs_prefill_t& a = g.a;
     cudaError_t e = cudaFuncSetAttribute(hs_expand_kernel<T, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kESmem);
@@ -914,21 +951,21 @@ template <typename T, bool E4M3> cudaError_t launch(const Args& g, int sms, cuda
     if (e != cudaSuccess) return e;
     if (a.k_tokens > 0) {
         const int64_t jobs = (a.k_tokens + 255) / 256 * a.heads;
-        const int pairs = (int)(jobs < sms / 2 ? jobs : sms / 2);
-        hs_expand_kernel<T, E4M3><<<2 * pairs, kEThreads, kESmem, s>>>(g);
+        hs_expand_kernel<T, E4M3><<<2 * (int)(jobs < pairs ? jobs : pairs), kEThreads, kESmem, s>>>(g);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     // Behind the expansion, whose start means that all earlier work is done, it may set up early.
     if (a.k_tokens > 0) {
-        e = launch_after(hs_prefill_kernel<T>, dim3(sms), kThreads, kSmem, s, g);
+        e = launch_after(hs_prefill_kernel<T>, dim3(2 * pairs), kThreads, kSmem, s, g);
     } else {
-        hs_prefill_kernel<T><<<sms, kThreads, kSmem, s>>>(g);
+        hs_prefill_kernel<T><<<2 * pairs, kThreads, kSmem, s>>>(g);
         e = cudaGetLastError();
     }
     if (e != cudaSuccess) return e;
-    const int64_t units = (a.q_tokens / 256 + a.batch) * a.heads;  // at most
-    return launch_after(hs_prefill_join_kernel<T>, dim3((unsigned)(units < sms - 1 ? units : sms - 1), 2, HS_HEAD_DIM / kJoinCols), 512, 0, s, g, sms);
+    if (pairs < 2) return cudaSuccess;
+    const int64_t units = (a.q_tokens / 512 + a.batch) * a.heads;  // at most
+    return launch_after(hs_prefill_join_kernel<T>, dim3((unsigned)(units < pairs - 1 ? units : pairs - 1), 4, HS_HEAD_DIM / kJoinCols), 512, 0, s, g, pairs);
 }
 
 }  // namespace
@@ -945,7 +982,7 @@ cudaError_t hs_launch_prefill(const hs_prefill_t& a, cudaStream_t s)
     cudaError_t err = cudaGetDevice(&dev);
     if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (err != cudaSuccess) return err;
-    sms = sms > kMaxCtas ? kMaxCtas : sms < 2 ? 2 : sms;
+    const int pairs = sms / 2 > kMaxPairs ? kMaxPairs : sms < 2 ? 1 : sms / 2;
     const bool e = a.row_format == HS_ROWS_E4M3;
     Args g;
     g.a = a;
@@ -954,6 +991,6 @@ cudaError_t hs_launch_prefill(const hs_prefill_t& a, cudaStream_t s)
     g.values = g.keys + (size_t)g.blocks * a.heads * kBlock;
     g.rope = g.values + (size_t)g.blocks * a.heads * kBlock;
     if (a.dtype == HS_TYPE_BF16)
-        return e ? launch<__nv_bfloat16, true>(g, sms, s) : launch<__nv_bfloat16, false>(g, sms, s);
-    return e ? launch<__half, true>(g, sms, s) : launch<__half, false>(g, sms, s);
+        return e ? launch<__nv_bfloat16, true>(g, pairs, s) : launch<__nv_bfloat16, false>(g, pairs, s);
+    return e ? launch<__half, true>(g, pairs, s) : launch<__half, false>(g, pairs, s);
 }
