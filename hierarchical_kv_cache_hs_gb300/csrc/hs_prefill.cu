@@ -320,7 +320,7 @@ constexpr int kOffAux = kOffV + kStages * kVStage;
 struct Aux {
     // kfull, vfull: this CTA's half; kpeer, vpeer (first CTA): the other's
     uint64_t qfull, qfree, kfull[kStages], kpeer[kStages], kfree[kStages], vfull[kStages], vpeer[kStages], vfree[kStages];
-    uint64_t sfull[2], pfull[2], odone[2], spare;
+    uint64_t sfull[2], pfull[2][2], odone[2], spare;  // pfull: weights of a block's first and second 64 keys
     uint32_t tmem;
     int dead;
     Start start;
@@ -510,14 +510,14 @@ template <typename T, int S> __device__ __forceinline__ void issue_qk(uint32_t s
     }
     __syncwarp();
 }
-template <typename T, int S> __device__ __forceinline__ void issue_pv(uint32_t tmem, uint64_t v_desc, Aux* x, bool first)
+template <typename T, int S, int HALF> __device__ __forceinline__ void issue_pv(uint32_t tmem, uint64_t v_desc, Aux* x, bool first)
 {
     constexpr uint32_t id = tc::inst_desc(HsType<T>::is_bf16, 256, 128, false, true);
     if (tc::elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 4 * HALF; k < 4 * HALF + 4; ++k)
             tc::mma_ts<2>(tmem + 256 * S + 128, tmem + 256 * S + 8 * k, v_desc + ((k * 2048) >> 4), id, !(first && k == 0));
-        tc::commit<2>(tc::smem_addr(&x->odone[S]));
+        if (HALF) tc::commit<2>(tc::smem_addr(&x->odone[S]));
     }
     __syncwarp();
 }
@@ -563,14 +563,21 @@ template <typename T> __device__ void multiply(const Args& g, uint32_t sbase, Au
 #pragma unroll
             for (int tile = 0; tile < 2; ++tile) {
                 if (t < end[tile]) {
-                    wait(tc::smem_addr(&x->pfull[tile]), phase[tile], &x->dead, error);
+                    wait(tc::smem_addr(&x->pfull[tile][0]), phase[tile], &x->dead, error);
+                    __syncwarp();
+                    tc::fence_after();
+                    if (tile == 0)
+                        issue_pv<T, 0, 0>(tmem, v_desc, x, t == walk.t0);
+                    else
+                        issue_pv<T, 1, 0>(tmem, v_desc, x, t == walk.t0);
+                    wait(tc::smem_addr(&x->pfull[tile][1]), phase[tile], &x->dead, error);
                     phase[tile] ^= 1;
                     __syncwarp();
                     tc::fence_after();
                     if (tile == 0)
-                        issue_pv<T, 0>(tmem, v_desc, x, t == walk.t0);
+                        issue_pv<T, 0, 1>(tmem, v_desc, x, false);
                     else
-                        issue_pv<T, 1>(tmem, v_desc, x, t == walk.t0);
+                        issue_pv<T, 1, 1>(tmem, v_desc, x, false);
                 }
                 if (tile == 1) release(x->vfree[now.s]);
                 if (tile == 0 && more) keys_come();
@@ -603,7 +610,8 @@ template <typename T> __device__ void soften(const Args& g, Aux* x, uint32_t ran
     const uint32_t tmem = x->tmem + 256 * tile + ((uint32_t)((threadIdx.x >> 5) & 3) << 21);
     const bool flip = a.scale < 0.f;  // scores are negated then, so that the scale is not negative
     const float c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f);  // not 0: a masked score stays -inf
-    const uint32_t pfull = tc::map_to_rank(tc::smem_addr(&x->pfull[tile]), 0);
+    const uint32_t pfull[2] = {tc::map_to_rank(tc::smem_addr(&x->pfull[tile][0]), 0),
+                               tc::map_to_rank(tc::smem_addr(&x->pfull[tile][1]), 0)};
     long long mine = 0;
     Walk walk(a, x);
     while (walk.next()) {
@@ -678,12 +686,14 @@ template <typename T> __device__ void soften(const Args& g, Aux* x, uint32_t ran
                     e[i] = pack2<T>(p0, p1);
                 }
                 tc::tmem_st16(tmem + 16 * n, e);
+                if (n & 1) {  // the product may begin with the first half
+                    tc::tmem_wait_st();
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive_cluster(pfull[n >> 1]);
+                }
             }
             sum += (sums[0] + sums[1]) + (sums[2] + sums[3]);
-            tc::tmem_wait_st();
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive_cluster(pfull);
         }
         // The piece's end.
         const bool worked = end > walk.t0;
@@ -802,7 +812,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_pref
             }
             for (int k = 0; k < 2; ++k) {
                 tc::mbar_init(tc::smem_addr(&x->sfull[k]), 1);
-                tc::mbar_init(tc::smem_addr(&x->pfull[k]), 8);
+                tc::mbar_init(tc::smem_addr(&x->pfull[k][0]), 8);
+                tc::mbar_init(tc::smem_addr(&x->pfull[k][1]), 8);
                 tc::mbar_init(tc::smem_addr(&x->odone[k]), 1);
             }
             tc::mbar_init(tc::smem_addr(&x->spare), 1);
