@@ -95,8 +95,8 @@ __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, int* dead, i
 
 // ---- (1) expansion -----------------------------------------------------------------
 
-constexpr int kEStages = 4;
-constexpr int kEThreads = 9 * 32;  // warps 0-3 write, 4-7 bring (one a stage), 8 issues the products
+constexpr int kEStages = 6;
+constexpr int kEThreads = (5 + kEStages) * 32;  // warps 0-3 write, then one a stage brings weights, the last issues the products
 constexpr int kEOffB = 8 * 16384;  // latents: 8 blocks of 64 channels, [128 tokens][128 B]
 constexpr int kEOffAux = kEOffB + kEStages * 16384;
 struct EAux {
@@ -125,7 +125,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kEThreads, 1) hs_exp
     if (warp == 0) tc::tmem_alloc<2>(tc::smem_addr(&x->tmem), 512);
     if (threadIdx.x == 0) {
         x->dead = 0;
-        tc::mbar_init(tc::smem_addr(&x->afull), 8);
+        tc::mbar_init(tc::smem_addr(&x->afull), 2 * kEStages);
         for (int i = 0; i < kEStages; ++i) {
             tc::mbar_init(tc::smem_addr(&x->bfull[i]), 2);
             tc::mbar_init(tc::smem_addr(&x->bfree[i]), 1);
@@ -192,7 +192,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kEThreads, 1) hs_exp
             __syncwarp();
             if (lane == 0) tc::mbar_arrive_cluster(dfree[d]);
         }
-    } else if (warp < 8) {
+    } else if (warp < 4 + kEStages) {
         const int s = warp - 4;
         const uint32_t bfull = tc::map_to_rank(tc::smem_addr(&x->bfull[s]), 0);
         const uint32_t afull = tc::map_to_rank(tc::smem_addr(&x->afull), 0);
@@ -203,15 +203,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kEThreads, 1) hs_exp
         for (int64_t job = lo; job < hi; ++job) {
             const int64_t mt = job / a.heads, h = job - mt * a.heads;
             if (mt != at) {
-                // The earlier tokens' products are done: each stage's last one is (the four warps' arrivals
-                // make up the barrier, and each has waited for its own stage).
+                // The earlier tokens' products are done: each stage's last one is (each of these warps waits
+                // for its own stage).
                 if (fills) wait(tc::smem_addr(&x->bfree[s]), (fills - 1) & 1, &x->dead, error);
-                asm volatile("bar.sync 2, 128;" ::: "memory");
+                asm volatile("bar.sync 2, %0;" ::"n"(32 * kEStages) : "memory");
                 at = mt;
-                for (int kb = 2 * s; kb < 2 * s + 2; ++kb) {
-#pragma unroll 4
-                    for (int n = 0; n < 32; ++n) {
-                        const int r = n * 4 + (lane >> 3);
+                for (int i = s; i < 32; i += kEStages) {  // a quarter of a block of channels each
+                    const int kb = i >> 2;
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) {
+                        const int r = (i & 3) * 32 + n * 4 + (lane >> 3);
                         const int64_t token = mt * 256 + 128 * (int)rank + r;
                         const bool live = token < a.k_tokens;
                         const uint8_t* src = static_cast<const uint8_t*>(a.rows) + (live ? token : 0) * a.row_stride;
@@ -226,7 +227,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kEThreads, 1) hs_exp
                     }
                 }
                 if (h == 0) {  // the rotary channels' tile (of 8-bit rows: scaled, and rounded to T)
-                    for (int i = 32 * s + lane; i < 128 * 8; i += 128) {
+                    for (int i = 32 * s + lane; i < 128 * 8; i += 32 * kEStages) {
                         const int tok = i >> 3;
                         const int64_t token = mt * 256 + 128 * (int)rank + tok;
                         const uint8_t* src = static_cast<const uint8_t*>(a.rows) + token * a.row_stride;
@@ -250,8 +251,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kEThreads, 1) hs_exp
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive_cluster(afull);
             }
-            for (int kb = s; kb < 8; kb += kEStages, ++fills) {
+            // the piece's n-th block of channels goes to stage n % kEStages
+            for (int kb = 0; kb < 8; ++kb) {
+                if ((8 * (job - lo) + kb) % kEStages != s) continue;
                 if (fills) wait(tc::smem_addr(&x->bfree[s]), (fills - 1) & 1, &x->dead, error);
+                ++fills;
                 const uint8_t* src = w + ((h * HS_HEAD_DIM + (lane >> 3)) * HS_LATENT_DIM + kb * 64 + ch * 8) * 2;
                 const uint32_t dst = sbase + kEOffB + s * 16384 + (lane >> 3) * 128;
 #pragma unroll 8
@@ -268,29 +272,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kEThreads, 1) hs_exp
         const uint32_t tmem = __shfl_sync(~0u, x->tmem, 0);
         constexpr uint32_t id = tc::inst_desc(HsType<T>::is_bf16, 256, 256, false, false);
         int64_t at = -1;
-        int tiles = 0, fill = 0;
+        int tiles = 0, stage = 0;
+        uint32_t phase = 0;
+        const uint64_t a_desc = tc::smem_desc(sbase, 16, 1024), b_desc = tc::smem_desc(sbase + kEOffB, 16, 1024);
         for (int64_t job = lo; job < hi; ++job) {
             const int n = (int)(job - lo), d = n & 1;
             const int64_t mt = job / a.heads;
             if (mt != at) wait(tc::smem_addr(&x->afull), tiles++ & 1, &x->dead, error);
             at = mt;
             if (n >= 2) wait(tc::smem_addr(&x->dfree[d]), ((n - 2) >> 1) & 1, &x->dead, error);
-#pragma unroll
-            for (int kb = 0; kb < 8; ++kb, ++fill) {
-                constexpr int S = kEStages;
-                wait(tc::smem_addr(&x->bfull[kb % S]), (fill / S) & 1, &x->dead, error);
+#pragma unroll 1
+            for (int kb = 0; kb < 8; ++kb) {
+                wait(tc::smem_addr(&x->bfull[stage]), phase, &x->dead, error);
                 __syncwarp();
                 tc::fence_after();
-                const uint64_t a_desc = tc::smem_desc(sbase + kb * 16384, 16, 1024);
-                const uint64_t b_desc = tc::smem_desc(sbase + kEOffB + (kb % S) * 16384, 16, 1024);
+                const uint64_t ad = a_desc + kb * 1024, bd = b_desc + stage * 1024;
                 if (tc::elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        tc::mma_ss<2>(tmem + 256 * d, a_desc + 2 * k, b_desc + 2 * k, id, (kb | k) != 0);
-                    tc::commit<2>(tc::smem_addr(&x->bfree[kb % S]));
+                    for (int k = 0; k < 4; ++k) tc::mma_ss<2>(tmem + 256 * d, ad + 2 * k, bd + 2 * k, id, (kb | k) != 0);
+                    tc::commit<2>(tc::smem_addr(&x->bfree[stage]));
                     if (kb == 7) tc::commit<2>(tc::smem_addr(&x->dfull[d]));
                 }
                 __syncwarp();
+                if (++stage == kEStages) stage = 0, phase ^= 1;
             }
         }
         if (*(volatile int*)&x->dead) {  // what was issued must be complete before tensor memory is freed
