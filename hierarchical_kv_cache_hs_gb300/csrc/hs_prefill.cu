@@ -95,10 +95,11 @@ __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, int* dead, i
 
 // ---- (1) expansion -----------------------------------------------------------------
 
-constexpr int kEStages = 6;
+constexpr int kEStages = 4;
 constexpr int kEThreads = (5 + kEStages) * 32;  // warps 0-3 write, then one a stage brings weights, the last issues the products
 constexpr int kEOffB = 8 * 16384;  // latents: 8 blocks of 64 channels, [128 tokens][128 B]
-constexpr int kEOffAux = kEOffB + kEStages * 16384;
+constexpr int kEOffOut = kEOffB + kEStages * 16384;  // two pieces on their way out, 64 channels of 128 tokens each
+constexpr int kEOffAux = kEOffOut + 2 * 16384;
 struct EAux {
     uint64_t afull, bfull[kEStages], bfree[kEStages], dfull[2], dfree[2], spare;
     uint32_t tmem;
@@ -159,39 +160,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kEThreads, 1) hs_exp
             wait(tc::smem_addr(&x->dfull[d]), (n >> 1) & 1, &x->dead, error);
             tc::fence_after();
             bool bad = false;
+            const int64_t tile = h * g.blocks + mt * 2 + rank;
+            const int tok = threadIdx.x;
 #pragma unroll 1
-            for (int c = 7; c >= 0; --c) {
-                uint32_t r[32], e[16];
-                __syncwarp();
-                tc::tmem_ld32(tmem + 256 * d + c * 32, r);
-                tc::tmem_wait_ld(r);
+            for (int piece = 0; piece < 4; ++piece) {  // 64 channels: values, then keys
+                const bool keys = piece >= 2;
+                const int cb = piece & 1;
+                const uint32_t buf = sbase + kEOffOut + cb * 16384;
+                uint32_t r[2][32];
+                tc::tmem_ld32(tmem + 256 * d + (keys ? 0 : 128) + 64 * cb, r[0]);
+                tc::tmem_ld32(tmem + 256 * d + (keys ? 0 : 128) + 64 * cb + 32, r[1]);
+                // the piece that was in this buffer has been read
+                if (threadIdx.x == 0) tc::bulk_wait_read<1>();
+                asm volatile("bar.sync 3, 128;" ::: "memory");
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float p = __uint_as_float(r[2 * i]), q = __uint_as_float(r[2 * i + 1]);
-                    if (E4M3) p *= scale, q *= scale;
-                    e[i] = pack2<T>(p, q);
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t e[16];
+                    tc::tmem_wait_ld(r[half]);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float p = __uint_as_float(r[half][2 * i]), q = __uint_as_float(r[half][2 * i + 1]);
+                        if (E4M3) p *= scale, q *= scale;
+                        e[i] = pack2<T>(p, q);
+                        if (!keys && not_finite<T>(e[i])) bad = true, e[i] = 0;
+                    }
+                    if (keys && bad) e[0] = ~0u;
+                    // keys lie as two tiles of 64 tokens, values as one of 128: the same bytes
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        tc::st_shared16(buf + tok * 128 + (((half * 4 + i) ^ (tok & 7)) << 4), e[4 * i], e[4 * i + 1], e[4 * i + 2],
+                                        e[4 * i + 3]);
                 }
-                if (c >= 4) {  // columns 128-255: values
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (not_finite<T>(e[i])) bad = true, e[i] = 0;
-                } else if (bad) {
-                    e[0] = ~0u;
+                tc::fence_async_shared();
+                asm volatile("bar.sync 3, 128;" ::: "memory");
+                if (threadIdx.x == 0) {
+                    if (keys) {
+                        uint8_t* dst = g.keys + tile * kBlock + cb * 8192;
+                        tc::bulk_store(dst, buf, 8192);
+                        tc::bulk_store(dst + 16384, buf + 8192, 8192);
+                    } else {
+                        tc::bulk_store(g.values + tile * kBlock + cb * 16384, buf, 16384);
+                    }
+                    tc::bulk_commit();
                 }
-                // 32 channels are half a row of the tile
-                const int64_t tile = h * g.blocks + mt * 2 + rank;
-                const int tok = threadIdx.x, cb = c >> 1 & 1;
-                uint8_t* row = c >= 4 ? g.values + tile * kBlock + cb * 16384 + tok * 128
-                                      : g.keys + tile * kBlock + (tok >> 6) * 16384 + cb * 8192 + (tok & 63) * 128;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<uint4*>(row + ((((c & 1) * 4 + i) ^ (tok & 7)) << 4)) =
-                        make_uint4(e[4 * i], e[4 * i + 1], e[4 * i + 2], e[4 * i + 3]);
             }
             tc::fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive_cluster(dfree[d]);
         }
+        if (threadIdx.x == 0) tc::bulk_wait_all();
     } else if (warp < 4 + kEStages) {
         const int s = warp - 4;
         const uint32_t bfull = tc::map_to_rank(tc::smem_addr(&x->bfull[s]), 0);
