@@ -1,35 +1,218 @@
 // hs_rms_norm: h = x + residual, y = h * rsqrt(mean(h^2) + eps) * weight,
 // written in the input's type or as e4m3 with a scale for each group.
 //
-// One CTA per row.  The row's h stays in registers between the sum of squares
-// and the scaling, so each input is read once and each output written once;
-// the pass is bound by HBM.
+// A row's h stays in fp32 registers between the sum of squares and the scaling, so
+// each input is read once and each output written once; the pass is bound by HBM.
+// Rows whose pieces lie on 16-byte boundaries go through hs_norm_kernel: 16-byte
+// loads, a warp a row up to 128 pieces (576 16-bit channels are 72), else 256 threads
+// a row.  Any other row (odd widths, odd alignments, groups that are not a power of
+// two of pieces) goes through hs_norm_any_kernel, element by element with the row in
+// shared memory.
 #include "hs_ops.h"
 
 namespace {
 
-constexpr int kThreads = 256;
-
-__device__ float block_sum(float v, float* red)
+__device__ __forceinline__ float nan_max(float a, float b)  // keeps a NaN
 {
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float t = 0.f;
-    for (int i = 0; i < kThreads / 32; ++i) t += red[i];
-    __syncthreads();
-    return t;
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
 }
 
-// max that keeps a NaN
-__device__ float nan_max(float a, float b) { return a != a ? a : (b != b ? b : fmaxf(a, b)); }
+template <typename T> struct Piece;  // 16 bytes of T as floats
+template <> struct Piece<float> {
+    static constexpr int n = 4;
+    static __device__ void unpack(const uint4& v, float* f)
+    {
+        f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+    }
+    static __device__ uint4 pack(const float* f)
+    {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+};
+template <> struct Piece<__nv_bfloat16> {
+    static constexpr int n = 8;
+    static __device__ void unpack(const uint4& v, float* f)
+    {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+    static __device__ uint4 pack(const float* f)
+    {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+template <> struct Piece<__half> {
+    static constexpr int n = 8;
+    static __device__ void unpack(const uint4& v, float* f)
+    {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            f[2 * i] = p.x, f[2 * i + 1] = p.y;
+        }
+    }
+    static __device__ uint4 pack(const float* f)
+    {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2 p = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
 
-template <typename T, bool E4M3>
-__global__ void __launch_bounds__(kThreads) hs_norm_kernel(hs_norm_t a)
+// y / scale, as a product where the reciprocal is an ordinary number.
+struct Divide {
+    float scale, inv;
+    bool product;
+    __device__ explicit Divide(float s) : scale(s == 0.f ? 1.f : s), inv(1.f / scale), product(scale > 1e-30f && scale < 1e30f) {}
+    __device__ float operator()(float y) const { return product ? y * inv : y / scale; }
+};
+
+constexpr int kWarps = 8;  // a block
+
+// NV: 16-byte pieces a thread; WIDE: the block's 256 threads share a row, else each
+// warp has its own.
+template <typename T, bool E4M3, int NV, bool WIDE>
+__global__ void __launch_bounds__(kWarps * 32) hs_norm_kernel(const __grid_constant__ hs_norm_t a)
 {
+    constexpr int P = Piece<T>::n, kTeam = WIDE ? kWarps * 32 : 32;
+    __shared__ float red[2][kWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int me = WIDE ? threadIdx.x : lane;
+    const int64_t row = WIDE ? blockIdx.x : (int64_t)blockIdx.x * kWarps + warp;
+    if (!WIDE && row >= a.tokens) return;
+    const int normed = a.dim / P, pieces = normed + a.carry / P;
+    const uint4* x = reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + row * a.x_stride);
+    const uint4* res = reinterpret_cast<const uint4*>(static_cast<const T*>(a.residual) + row * a.residual_stride);
+    uint4* res_out = reinterpret_cast<uint4*>(static_cast<T*>(a.residual_out) + row * a.residual_out_stride);
+    const uint4* weight = static_cast<const uint4*>(a.weight);
+    float h[NV][P];
+    uint4 xv[NV], rv[NV], wv[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int i = v * kTeam + me;
+        xv[v] = i < pieces ? x[i] : make_uint4(0, 0, 0, 0);
+        if (a.residual && i < normed) rv[v] = res[i];
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int i = v * kTeam + me;
+        if (NV <= 4 && i < normed) wv[v] = weight[i];
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int i = v * kTeam + me;
+        Piece<T>::unpack(xv[v], h[v]);
+        if (i < normed) {
+            if (a.residual) {
+                float r[P];
+                Piece<T>::unpack(rv[v], r);
+#pragma unroll
+                for (int k = 0; k < P; ++k) h[v][k] += r[k];
+            }
+#pragma unroll
+            for (int k = 0; k < P; ++k) sum += h[v][k] * h[v][k];
+        }
+    }
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    if constexpr (WIDE) {
+        if (lane == 0) red[0][warp] = sum;
+        __syncthreads();  // and every input of the row has been read: outputs may overwrite it
+        sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) sum += red[0][w];
+    } else {
+        __syncwarp();
+    }
+    const float r = rsqrtf(sum / a.dim + a.eps);
+    float top = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int i = v * kTeam + me;
+        if (i < normed) {
+            if (a.residual) res_out[i] = Piece<T>::pack(h[v]);
+            float w[P];
+            Piece<T>::unpack(NV <= 4 ? wv[v] : weight[i], w);
+#pragma unroll
+            for (int k = 0; k < P; ++k) h[v][k] *= r * w[k];
+        }
+        if constexpr (!E4M3) {
+            if (i < pieces) reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row * a.out_stride)[i] = Piece<T>::pack(h[v]);
+        } else if (a.group == 0) {
+#pragma unroll
+            for (int k = 0; k < P; ++k) top = nan_max(top, fabsf(h[v][k]));
+        }
+    }
+    if constexpr (E4M3) {
+        float* scales = a.scales + row * a.scales_stride;
+        uint8_t* out = static_cast<uint8_t*>(a.out) + row * a.out_stride;
+        auto store = [&](int i, const float* y, const Divide& div) {
+            if (i >= pieces) return;
+            uint32_t q[P / 4];
+#pragma unroll
+            for (int k = 0; k < P / 4; ++k) {
+                const float2 lo = make_float2(div(y[4 * k]), div(y[4 * k + 1])), hi = make_float2(div(y[4 * k + 2]), div(y[4 * k + 3]));
+                q[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3) |
+                       (uint32_t)__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3) << 16;
+            }
+            if constexpr (P == 8)
+                *reinterpret_cast<uint2*>(out + i * 8) = make_uint2(q[0], q[1]);
+            else
+                *reinterpret_cast<uint32_t*>(out + i * 4) = q[0];
+        };
+        if (a.group == 0) {
+            for (int o = 16; o; o >>= 1) top = nan_max(top, __shfl_xor_sync(~0u, top, o));
+            if constexpr (WIDE) {
+                if (lane == 0) red[1][warp] = top;
+                __syncthreads();
+                top = red[1][0];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) top = nan_max(top, red[1][w]);
+            }
+            const float scale = top / HS_E4M3_MAX;
+            if (me == 0) scales[0] = scale;
+            const Divide div(scale);
+#pragma unroll
+            for (int v = 0; v < NV; ++v) store(v * kTeam + me, h[v], div);
+        } else {
+            const int lanes = a.group / P;  // a power of two: a group is this many neighbouring lanes
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const int i = v * kTeam + me;
+                float m = 0.f;
+#pragma unroll
+                for (int k = 0; k < P; ++k) m = nan_max(m, fabsf(h[v][k]));
+                for (int o = 1; o < lanes; o <<= 1) m = nan_max(m, __shfl_xor_sync(~0u, m, o));
+                const float scale = m / HS_E4M3_MAX;
+                if (i < pieces && (lane & (lanes - 1)) == 0) scales[i / lanes] = scale;
+                store(i, h[v], Divide(scale));
+            }
+        }
+    }
+}
+
+// Any width, alignment and group: one block a row, the row in shared memory.
+template <typename T, bool E4M3> __global__ void __launch_bounds__(kWarps * 32) hs_norm_any_kernel(const __grid_constant__ hs_norm_t a)
+{
+    constexpr int kThreads = kWarps * 32;
     extern __shared__ float y[];  // [dim + carry]
-    __shared__ float red[kThreads / 32];
+    __shared__ float red[kWarps];
     const int64_t row = blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int width = a.dim + a.carry;
     const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
     const T* res = a.residual ? static_cast<const T*>(a.residual) + row * a.residual_stride : nullptr;
@@ -42,13 +225,16 @@ __global__ void __launch_bounds__(kThreads) hs_norm_kernel(hs_norm_t a)
         }
         y[i] = h;
     }
-    sum = block_sum(sum, red);
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    if (lane == 0) red[warp] = sum;
+    __syncthreads();  // and every input of the row has been read: outputs may overwrite it
+    sum = 0.f;
+    for (int w = 0; w < kWarps; ++w) sum += red[w];
     const float r = rsqrtf(sum / a.dim + a.eps);
     for (int i = threadIdx.x; i < a.dim; i += kThreads) {
         const float h = y[i];
-        if (res)
-            static_cast<T*>(a.residual_out)[row * a.residual_out_stride + i] = HsType<T>::from_float(h);
-        y[i] = h * r * HsType<T>::to_float(static_cast<const T*>(a.weight)[i]);
+        if (res) static_cast<T*>(a.residual_out)[row * a.residual_out_stride + i] = HsType<T>::from_float(h);
+        y[i] = h * (r * HsType<T>::to_float(static_cast<const T*>(a.weight)[i]));
     }
     __syncthreads();
     if constexpr (!E4M3) {
@@ -56,31 +242,83 @@ __global__ void __launch_bounds__(kThreads) hs_norm_kernel(hs_norm_t a)
         for (int i = threadIdx.x; i < width; i += kThreads) out[i] = HsType<T>::from_float(y[i]);
     } else {
         uint8_t* out = static_cast<uint8_t*>(a.out) + row * a.out_stride;
-        const int group = a.group ? a.group : width;
-        const int groups = (width + group - 1) / group;
-        for (int g = threadIdx.x >> 5; g < groups; g += kThreads / 32) {  // a warp per group
-            const int end = min(width, (g + 1) * group);
+        auto put = [&](int i, const Divide& div) { out[i] = __nv_cvt_float_to_fp8(div(y[i]), __NV_SATFINITE, __NV_E4M3); };
+        if (a.group == 0) {  // the block together
             float m = 0.f;
-            for (int i = g * group + (threadIdx.x & 31); i < end; i += 32) m = nan_max(m, fabsf(y[i]));
+            for (int i = threadIdx.x; i < width; i += kThreads) m = nan_max(m, fabsf(y[i]));
+            for (int o = 16; o; o >>= 1) m = nan_max(m, __shfl_xor_sync(~0u, m, o));
+            if (lane == 0) red[warp] = m;
+            __syncthreads();
+            for (int w = 0; w < kWarps; ++w) m = nan_max(m, red[w]);
+            const float scale = m / HS_E4M3_MAX;
+            if (threadIdx.x == 0) a.scales[row * a.scales_stride] = scale;
+            const Divide div(scale);
+            for (int i = threadIdx.x; i < width; i += kThreads) put(i, div);
+            return;
+        }
+        for (int g = warp; g * a.group < width; g += kWarps) {  // a warp a group
+            const int end = min(width, (g + 1) * a.group);
+            float m = 0.f;
+            for (int i = g * a.group + lane; i < end; i += 32) m = nan_max(m, fabsf(y[i]));
             for (int o = 16; o; o >>= 1) m = nan_max(m, __shfl_xor_sync(~0u, m, o));
             const float scale = m / HS_E4M3_MAX;
-            if ((threadIdx.x & 31) == 0) a.scales[row * a.scales_stride + g] = scale;
-            for (int i = g * group + (threadIdx.x & 31); i < end; i += 32)
-                out[i] = __nv_cvt_float_to_fp8(scale == 0.f ? y[i] : y[i] / scale, __NV_SATFINITE, __NV_E4M3);
+            if (lane == 0) a.scales[row * a.scales_stride + g] = scale;
+            const Divide div(scale);
+            for (int i = g * a.group + lane; i < end; i += 32) put(i, div);
         }
     }
 }
 
-template <typename T>
-cudaError_t launch(const hs_norm_t& a, cudaStream_t s)
+template <typename T, bool E4M3> cudaError_t launch(const hs_norm_t& a, cudaStream_t s)
 {
-    const size_t smem = sizeof(float) * (size_t)(a.dim + a.carry);
-    auto k = a.scales ? hs_norm_kernel<T, true> : hs_norm_kernel<T, false>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)sizeof(float) * HS_MAX_NORM_DIM);
-    if (e != cudaSuccess) return e;
-    k<<<(unsigned)a.tokens, kThreads, smem, s>>>(a);
+    constexpr int P = Piece<T>::n, el = sizeof(T);
+    auto fits = [](const void* p, int64_t stride_bytes, int64_t rows, uintptr_t to) {
+        return ((uintptr_t)p % to) == 0 && (rows <= 1 || stride_bytes % (int64_t)to == 0);
+    };
+    bool pieces16 = a.dim % P == 0 && a.carry % P == 0 && fits(a.x, a.x_stride * el, a.tokens, 16) &&
+                    fits(a.weight, 0, 1, 16) && fits(a.residual, a.residual_stride * el, a.tokens, 16) &&
+                    fits(a.residual_out, a.residual_out_stride * el, a.tokens, 16) &&
+                    (E4M3 ? fits(a.out, a.out_stride, a.tokens, P) : fits(a.out, a.out_stride * el, a.tokens, 16));
+    if (E4M3 && a.group) {
+        const int lanes = a.group / P;
+        pieces16 = pieces16 && a.group % P == 0 && lanes <= 32 && (lanes & (lanes - 1)) == 0;
+    }
+    const int pieces = (a.dim + a.carry) / P;
+    if (!pieces16) {
+        auto k = hs_norm_any_kernel<T, E4M3>;
+        const size_t smem = sizeof(float) * (size_t)(a.dim + a.carry);
+        if (smem > 48 * 1024) {
+            cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(float) * HS_MAX_NORM_DIM);
+            if (e != cudaSuccess) return e;
+        }
+        k<<<(unsigned)a.tokens, kWarps * 32, smem, s>>>(a);
+    } else if (pieces <= 128) {
+        const unsigned grid = (unsigned)((a.tokens + kWarps - 1) / kWarps);
+        if (pieces <= 32)
+            hs_norm_kernel<T, E4M3, 1, false><<<grid, kWarps * 32, 0, s>>>(a);
+        else if (pieces <= 96)
+            hs_norm_kernel<T, E4M3, 3, false><<<grid, kWarps * 32, 0, s>>>(a);
+        else
+            hs_norm_kernel<T, E4M3, 4, false><<<grid, kWarps * 32, 0, s>>>(a);
+    } else {
+        const unsigned grid = (unsigned)a.tokens;
+        if (pieces <= 256)
+            hs_norm_kernel<T, E4M3, 1, true><<<grid, kWarps * 32, 0, s>>>(a);
+        else if (pieces <= 512)
+            hs_norm_kernel<T, E4M3, 2, true><<<grid, kWarps * 32, 0, s>>>(a);
+        else if (pieces <= 1024)
+            hs_norm_kernel<T, E4M3, 4, true><<<grid, kWarps * 32, 0, s>>>(a);
+        else if (pieces <= 2048)
+            hs_norm_kernel<T, E4M3, 8, true><<<grid, kWarps * 32, 0, s>>>(a);
+        else
+            hs_norm_kernel<T, E4M3, 16, true><<<grid, kWarps * 32, 0, s>>>(a);
+    }
     return cudaGetLastError();
+}
+
+template <typename T> cudaError_t launch(const hs_norm_t& a, cudaStream_t s)
+{
+    return a.scales ? launch<T, true>(a, s) : launch<T, false>(a, s);
 }
 
 }  // namespace
