@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import numpy as np
@@ -550,29 +551,43 @@ def hs_profile_events(h: int, before_copy=None, after_copy=None) -> None:
 # ---- Operators beside the swap-in path -------------------------------------
 # These take torch tensors and check them (type, shape, layout, device) before
 # the call; a mismatch raises ValueError.  What the library itself refuses
-# (alignments, limits, a workspace that is too small) raises HsError.
+# (alignments, limits, a workspace that is too small) raises HsError.  The
+# argument blocks are packed by struct: a small call's time is the host's, and
+# a ctypes.Structure takes several times as long to fill.
+_ATTEND = struct.Struct("@6iqP3qPqqP2qPP3qPfPN")
+_PREFILL = struct.Struct("@4i2qP2qPqPPPPP2qPfPN")
+_NORM = struct.Struct("@4iqPqPqPqPfPqPq")
+assert (_ATTEND.size, _PREFILL.size, _NORM.size) == tuple(
+    ctypes.sizeof(t) for t in (hs_attend_t, hs_prefill_t, hs_norm_t))
+_ROW_WIDTH = {HS_ROWS_16BIT: 2 * HS_ROW_DIM, HS_ROWS_E4M3: HS_ROW8_BYTES}
+_TYPES = {}  # torch dtype -> HS_TYPE_*, filled at the first call (torch is imported late)
+
 
 def _type_of(x, name, fp32=False):
-    import torch
-    if x.dtype == torch.bfloat16:
-        return HS_TYPE_BF16
-    if x.dtype == torch.float16:
-        return HS_TYPE_FP16
-    if fp32 and x.dtype == torch.float32:
-        return HS_TYPE_FP32
-    raise ValueError("%s: type %s is not taken" % (name, x.dtype))
+    kind = _TYPES.get(x.dtype)
+    if kind is None and not _TYPES:
+        import torch
+        _TYPES.update({torch.bfloat16: HS_TYPE_BF16, torch.float16: HS_TYPE_FP16,
+                       torch.float32: HS_TYPE_FP32})
+        kind = _TYPES.get(x.dtype)
+    if kind is None or (kind == HS_TYPE_FP32 and not fp32):
+        raise ValueError("%s: type %s is not taken" % (name, x.dtype))
+    return kind
 
 
 def _want(x, name, shape, dtype, device):
-    """One tensor of a call: its shape, type, contiguous last axis and device."""
+    """One tensor of a call: its shape, type, contiguous last axis and device.  Returns its strides."""
+    stride = x.stride()
+    if (x.shape == shape and x.dtype == dtype and (stride[-1] == 1 or shape[-1] <= 1)
+            and x.device == device):
+        return stride
     if tuple(x.shape) != shape:
         raise ValueError("%s must have shape %s, has %s" % (name, shape, tuple(x.shape)))
     if x.dtype != dtype:
         raise ValueError("%s must be %s, got %s" % (name, dtype, x.dtype))
-    if shape and shape[-1] > 1 and x.stride(-1) != 1:
-        raise ValueError("the last axis of %s must be contiguous" % name)
     if x.device != device:
         raise ValueError("%s must be on %s, is on %s" % (name, device, x.device))
+    raise ValueError("the last axis of %s must be contiguous" % name)
 
 
 def _on_current_device(device):
@@ -581,11 +596,10 @@ def _on_current_device(device):
         raise ValueError("tensors must be on the current CUDA device, are on %s" % device)
 
 
-def _rows_of(rows, row_format, q, lead):
+def _rows_of(rows, row_format, dtype, device, lead):
     """(address, rows a request, row stride, request stride) in bytes of a row array
     [*lead, n, channels or bytes], or of a handle's device buffer."""
-    import torch
-    width = {HS_ROWS_16BIT: 2 * HS_ROW_DIM, HS_ROWS_E4M3: HS_ROW8_BYTES}.get(row_format)
+    width = _ROW_WIDTH.get(row_format)
     if width is None:
         raise ValueError("unknown row_format %r" % (row_format,))
     if isinstance(rows, Handle):
@@ -593,27 +607,38 @@ def _rows_of(rows, row_format, q, lead):
             raise ValueError("the handle has %d requests of %d-byte rows" % (rows.B, rows.R))
         n = rows.S + rows.T
         return hs_device_buffer(rows.h), n, rows.R, n * rows.R
-    if rows.dim() != len(lead) + 2 or tuple(rows.shape[:-2]) != lead:
-        raise ValueError("rows must have shape %s + (rows, channels), has %s" % (lead, tuple(rows.shape)))
-    if rows.dtype == torch.uint8:
-        wide = rows.shape[-1] >= width
-    else:
-        wide = row_format == HS_ROWS_16BIT and rows.dtype == q.dtype and rows.shape[-1] == HS_ROW_DIM
-    if not wide:
-        raise ValueError("rows: %s of %s are not rows of this format" % (rows.dtype, tuple(rows.shape)))
-    if rows.stride(-1) != 1 or rows.device != q.device:
-        raise ValueError("rows must be contiguous in the last axis and on %s" % q.device)
+    shape = rows.shape
+    if len(shape) != len(lead) + 2 or shape[:-2] != lead:
+        raise ValueError("rows must have shape %s + (rows, channels), has %s" % (lead, tuple(shape)))
     e = rows.element_size()
-    return (rows.data_ptr(), rows.shape[-2], rows.stride(-2) * e,
-            rows.stride(0) * e if lead else 0)
+    if e == 1:
+        wide = shape[-1] >= width and not rows.is_floating_point()
+    else:
+        wide = row_format == HS_ROWS_16BIT and rows.dtype == dtype and shape[-1] == HS_ROW_DIM
+    if not wide:
+        raise ValueError("rows: %s of %s are not rows of this format" % (rows.dtype, tuple(shape)))
+    stride = rows.stride()
+    if stride[-1] != 1 or rows.device != device:
+        raise ValueError("rows must be contiguous in the last axis and on %s" % device)
+    return rows.data_ptr(), shape[-2], stride[-2] * e, stride[0] * e if lead else 0
 
 
 def _workspace_of(workspace, device):
     if workspace is None:
-        return None, 0
+        return 0, 0
     if not workspace.is_contiguous() or workspace.device != device:
         raise ValueError("workspace must be contiguous and on %s" % device)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _lse_of(lse, shape, device):
+    if lse is None:
+        return 0
+    import torch
+    _want(lse, "lse", shape, torch.float32, device)
+    if not lse.is_contiguous():
+        raise ValueError("lse must be contiguous")
+    return lse.data_ptr()
 
 
 def hs_latent_attend_workspace(batch: int, positions: int, heads: int, rows: int) -> int:
@@ -635,36 +660,31 @@ def hs_latent_attend(q, rows, out, scale: float, slots=None, lengths=None,
     (int32 [B], the P positions being the last).  lse: fp32 [B][P][H] or None.
     """
     import torch
+    dtype, device, shape = q.dtype, q.device, q.shape
     kind = _type_of(q, "q")
-    if q.dim() != 4:
-        raise ValueError("q must have 4 axes, has %d" % q.dim())
-    B, P, H, _ = q.shape
-    device = q.device
-    _want(q, "q", (B, P, H, HS_ROW_DIM), q.dtype, device)
-    _want(out, "out", (B, P, H, HS_LATENT_DIM), q.dtype, device)
-    address, n_rows, row_stride, request_stride = _rows_of(rows, row_format, q, (B,))
+    if len(shape) != 4:
+        raise ValueError("q must have 4 axes, has %d" % len(shape))
+    B, P, H, _ = shape
+    q0, q1, q2, _ = _want(q, "q", (B, P, H, HS_ROW_DIM), dtype, device)
+    o0, o1, o2, _ = _want(out, "out", (B, P, H, HS_LATENT_DIM), dtype, device)
+    address, n_rows, row_stride, request_stride = _rows_of(rows, row_format, dtype, device, (B,))
     if (slots is None) == (lengths is None):
         raise ValueError("give slots or lengths, and not both")
-    entries, slots_stride = 0, (0, 0, 1)
+    entries = slots_at = lengths_at = s0 = s1 = 0
     if slots is not None:
         entries = slots.shape[-1] if slots.dim() else 0
-        _want(slots, "slots", (B, P, entries), torch.int32, device)
-        slots_stride = slots.stride()
+        s0, s1, _ = _want(slots, "slots", (B, P, entries), torch.int32, device)
+        slots_at = slots.data_ptr() or 16  # an empty list has no address
     else:
         _want(lengths, "lengths", (B,), torch.int32, device)
-    if lse is not None:
-        _want(lse, "lse", (B, P, H), torch.float32, device)
-        if not lse.is_contiguous():
-            raise ValueError("lse must be contiguous")
+        lengths_at = lengths.data_ptr()
+    lse_at = _lse_of(lse, (B, P, H), device)
     space, space_bytes = _workspace_of(workspace, device)
     _on_current_device(device)
-    qs, os_ = q.stride(), out.stride()
-    args = hs_attend_t(kind, row_format, B, P, H, entries, n_rows, q.data_ptr(), qs[:3], address,
-                       row_stride, request_stride, None if slots is None else slots.data_ptr() or 16,
-                       slots_stride[:2], None if lengths is None else lengths.data_ptr(),
-                       out.data_ptr(), os_[:3], None if lse is None else lse.data_ptr(), scale,
-                       space, space_bytes)
-    _check(lib.hs_latent_attend(ctypes.byref(args), _stream(stream)), "hs_latent_attend")
+    _check(lib.hs_latent_attend(
+        _ATTEND.pack(kind, row_format, B, P, H, entries, n_rows, q.data_ptr(), q0, q1, q2, address,
+                     row_stride, request_stride, slots_at, s0, s1, lengths_at, out.data_ptr(), o0, o1,
+                     o2, lse_at, scale, space, space_bytes), _stream(stream)), "hs_latent_attend")
 
 
 def hs_latent_prefill_workspace(k_tokens: int, heads: int) -> int:
@@ -683,31 +703,29 @@ def hs_latent_prefill(q, rows, w_uk, w_uv, q_start, k_start, out, scale: float,
     rows k_start[b]..k_start[b + 1] (int32 [B + 1]), its queries being its last tokens.
     """
     import torch
+    dtype, device, shape = q.dtype, q.device, q.shape
     kind = _type_of(q, "q")
-    if q.dim() != 3:
-        raise ValueError("q must have 3 axes, has %d" % q.dim())
-    Tq, H, _ = q.shape
-    device, B = q.device, q_start.numel() - 1
-    _want(q, "q", (Tq, H, HS_HEAD_DIM + HS_ROPE_DIM), q.dtype, device)
-    _want(out, "out", (Tq, H, HS_HEAD_DIM), q.dtype, device)
+    if len(shape) != 3:
+        raise ValueError("q must have 3 axes, has %d" % len(shape))
+    Tq, H, _ = shape
+    B = q_start.numel() - 1
+    q0, q1, _ = _want(q, "q", (Tq, H, HS_HEAD_DIM + HS_ROPE_DIM), dtype, device)
+    o0, o1, _ = _want(out, "out", (Tq, H, HS_HEAD_DIM), dtype, device)
     for w, name in ((w_uk, "w_uk"), (w_uv, "w_uv")):
-        _want(w, name, (H, HS_HEAD_DIM, HS_LATENT_DIM), q.dtype, device)
+        _want(w, name, (H, HS_HEAD_DIM, HS_LATENT_DIM), dtype, device)
         if not w.is_contiguous():
             raise ValueError("%s must be contiguous" % name)
-    for x, name in ((q_start, "q_start"), (k_start, "k_start")):
-        _want(x, name, (B + 1,), torch.int32, device)
-    address, k_tokens, row_stride, _ = _rows_of(rows, row_format, q, ())
-    if lse is not None:
-        _want(lse, "lse", (Tq, H), torch.float32, device)
-        if not lse.is_contiguous():
-            raise ValueError("lse must be contiguous")
+    _want(q_start, "q_start", (B + 1,), torch.int32, device)
+    _want(k_start, "k_start", (B + 1,), torch.int32, device)
+    address, k_tokens, row_stride, _ = _rows_of(rows, row_format, dtype, device, ())
+    lse_at = _lse_of(lse, (Tq, H), device)
     space, space_bytes = _workspace_of(workspace, device)
     _on_current_device(device)
-    args = hs_prefill_t(kind, row_format, B, H, Tq, k_tokens, q.data_ptr(), q.stride()[:2], address,
-                        row_stride, w_uk.data_ptr(), w_uv.data_ptr(), q_start.data_ptr(),
-                        k_start.data_ptr(), out.data_ptr(), out.stride()[:2],
-                        None if lse is None else lse.data_ptr(), scale, space, space_bytes)
-    _check(lib.hs_latent_prefill(ctypes.byref(args), _stream(stream)), "hs_latent_prefill")
+    _check(lib.hs_latent_prefill(
+        _PREFILL.pack(kind, row_format, B, H, Tq, k_tokens, q.data_ptr(), q0, q1, address, row_stride,
+                      w_uk.data_ptr(), w_uv.data_ptr(), q_start.data_ptr(), k_start.data_ptr(),
+                      out.data_ptr(), o0, o1, lse_at, scale, space, space_bytes), _stream(stream)),
+        "hs_latent_prefill")
 
 
 def hs_rms_norm(x, weight, out, eps: float, residual=None, residual_out=None, carry: int = 0,
@@ -719,38 +737,37 @@ def hs_rms_norm(x, weight, out, eps: float, residual=None, residual_out=None, ca
     [N][groups], one for each `group` channels (0: one for the row).
     """
     import torch
+    dtype, device, shape = x.dtype, x.device, x.shape
     kind = _type_of(x, "x", fp32=True)
-    if x.dim() != 2 or not 0 <= carry < max(x.shape[1], 1):
+    if len(shape) != 2 or not 0 <= carry < max(shape[1], 1):
         raise ValueError("x must be [tokens][dim + carry] with dim > 0")
-    n, width = x.shape
-    dim, device = width - carry, x.device
-    _want(x, "x", (n, width), x.dtype, device)
-    _want(weight, "weight", (dim,), x.dtype, device)
+    n, width = shape
+    dim = width - carry
+    x0, _ = _want(x, "x", (n, width), dtype, device)
+    _want(weight, "weight", (dim,), dtype, device)
     if (residual is None) != (residual_out is None):
         raise ValueError("give both residual and residual_out, or neither")
-    r = ro = s = (None, 0)
+    r_at = r0 = ro_at = ro0 = s_at = s0 = 0
     if residual is not None:
-        _want(residual, "residual", (n, dim), x.dtype, device)
-        _want(residual_out, "residual_out", (n, dim), x.dtype, device)
-        r = residual.data_ptr(), residual.stride(0)
-        ro = residual_out.data_ptr(), residual_out.stride(0)
+        r0, _ = _want(residual, "residual", (n, dim), dtype, device)
+        ro0, _ = _want(residual_out, "residual_out", (n, dim), dtype, device)
+        r_at, ro_at = residual.data_ptr(), residual_out.data_ptr()
     if scales is None:
         if group:
             raise ValueError("group needs scales")
-        _want(out, "out", (n, width), x.dtype, device)
+        o0, _ = _want(out, "out", (n, width), dtype, device)
     else:
         if group < 0:
             raise ValueError("group must not be negative")
-        if out.dtype != torch.uint8:
-            _want(out, "out", (n, width), torch.float8_e4m3fn, device)
-        else:
-            _want(out, "out", (n, width), torch.uint8, device)
-        _want(scales, "scales", (n, -(-width // group) if group else 1), torch.float32, device)
-        s = scales.data_ptr(), scales.stride(0)
+        o0, _ = _want(out, "out", (n, width),
+                      torch.uint8 if out.dtype == torch.uint8 else torch.float8_e4m3fn, device)
+        s0, _ = _want(scales, "scales", (n, -(-width // group) if group else 1), torch.float32, device)
+        s_at = scales.data_ptr()
     _on_current_device(device)
-    args = hs_norm_t(kind, dim, carry, group, n, x.data_ptr(), x.stride(0), r[0], r[1], ro[0], ro[1],
-                     weight.data_ptr(), eps, out.data_ptr(), out.stride(0), s[0], s[1])
-    _check(lib.hs_rms_norm(ctypes.byref(args), _stream(stream)), "hs_rms_norm")
+    _check(lib.hs_rms_norm(
+        _NORM.pack(kind, dim, carry, group, n, x.data_ptr(), x0, r_at, r0, ro_at, ro0,
+                   weight.data_ptr(), eps, out.data_ptr(), o0, s_at, s0), _stream(stream)),
+        "hs_rms_norm")
 
 
 class Handle:
