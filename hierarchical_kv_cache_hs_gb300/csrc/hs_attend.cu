@@ -26,29 +26,31 @@ namespace {
 constexpr int kTile = 64;         // rows a tile
 constexpr int kThreads = 14 * 32;
 constexpr int kMaxPairs = 76;     // pairs of SMs
-constexpr int kPrefetch = 4;      // tiles brought to L2 ahead
 
 // Shared memory of a CTA.
-constexpr int kQBytes = 9 * 64 * 128;            // 9 blocks of 64 channels, [64 heads][128 B]
+constexpr int kQTmem = 6;                        // of Q's 9 blocks of 64 channels, those in tensor memory; the others here:
+constexpr int kQBytes = (9 - kQTmem) * 64 * 128; // [64 heads][128 B] each
+constexpr int kKStages = 3;
+constexpr int kMeta = 8;
 constexpr int kKBytes = 9 * 32 * 128;            // 9 blocks, [32 rows][128 B]
 constexpr int kVBytes = 4 * 64 * 128;            // 4 blocks, [64 rows][128 B]
 constexpr int kPBytes = 64 * 128;                // [64 heads][64 rows]
 constexpr int kOffK = kQBytes;
-constexpr int kOffV = kOffK + 2 * kKBytes;
+constexpr int kOffV = kOffK + kKStages * kKBytes;  // (a piece's queries on their way to tensor memory pass here)
 constexpr int kOffP = kOffV + 2 * kVBytes;
 constexpr int kOffAux = kOffP + 2 * kPBytes;
 
 struct Aux {
-    uint64_t kfull[2], vfull[2], qfull, sfull[2], pready[2], pvdone[2], spare[2];
+    uint64_t kfull[kKStages], kfree[kKStages], vfull[2], qhere, lifted, qfull, sfull[2], pready[2], pvdone[2], spare[2];
     uint32_t tmem;
     int dead;
     long long start_unit;  // where this pair's piece of the line begins
     long long count;       // its tiles
     int start_tile;
-    // Per tile, four deep: a tile's keys arrive while the softmax two tiles back still reads these.
-    uint16_t valid[4][2][2];  // [half][warp]: one bit a row
-    alignas(16) float scale[4][kTile];
-    __half log_scale[4][kTile];  // only moves the reference: its rounding cancels
+    // Per tile, kMeta deep: a tile's keys may arrive while the softmax four tiles back still reads these.
+    uint16_t valid[kMeta][2][2];  // [half][warp]: one bit a row
+    alignas(16) float scale[kMeta][kTile];
+    __half log_scale[kMeta][kTile];  // only moves the reference: its rounding cancels
     int8_t q_up[2][64];          // power of two on a bf16 query held in fp16, by the parity of the piece
     float red[2][128];
 };
@@ -56,7 +58,7 @@ constexpr int kSmem = kOffAux + (int)sizeof(Aux);
 static_assert(kSmem <= 232448, "shared memory");
 
 // Tensor memory columns.
-constexpr uint32_t kColO = 0, kColS = 256;
+constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;
 
 struct Args {
     hs_attend_t a;
@@ -172,14 +174,13 @@ struct Lookup {
         : a(args), slots(args.slots ? args.slots + w.b * args.slots_stride[0] + w.p * args.slots_stride[1] : nullptr), n(w.rows)
     {
     }
-    __device__ int operator()(int tile, int at) const  // the row, or -1
+    // The list's entry, unchecked: looked at an iteration later, so that no warp waits for it here.
+    __device__ int raw(int tile, int at) const
     {
         const long long i = (long long)tile * kTile + at;
-        if (i >= n) return -1;
-        if (!slots) return (int)i;
-        const int r = slots[i];
-        return r >= 0 && r < a.n_rows ? r : -1;
+        return i >= n ? -1 : slots ? slots[i] : (int)i;
     }
+    __device__ int row(int raw) const { return raw >= 0 && raw < a.n_rows ? raw : -1; }  // or -1
 };
 
 // 16 e4m3 values as two 16-byte pieces of fp16 at dst + c0 and dst + c1.
@@ -194,16 +195,14 @@ __device__ __forceinline__ void store_wide(const uint4& v, uint32_t dst, int c0,
     tc::st_shared16(dst + c1, e[4], e[5], e[6], e[7]);
 }
 
-// Keys: this CTA's 32 rows of each tile, whole.  Two warps a stage (tiles of one
-// parity), 16 rows each; they also say which of the tile's 64 rows count.
+// Keys: this CTA's 32 rows of each tile, whole.  Two warps take the even tiles and two
+// the odd ones, 16 rows a warp; they also say which of the tile's 64 rows count.
 template <typename T, bool E4M3>
 __device__ void bring_keys(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int* error)
 {
     const hs_attend_t& a = g.a;
     const int lane = threadIdx.x & 31, wg = (threadIdx.x >> 5) - 4;
-    const int stage = wg >> 1, w = wg & 1;
-    const uint32_t full = tc::map_to_rank(tc::smem_addr(&x->kfull[stage]), 0);
-    const uint32_t k_smem = sbase + kOffK + stage * kKBytes;
+    const int turn = wg >> 1, w = wg & 1;
     const int row_bytes = E4M3 ? HS_ROW8_BYTES : 2 * HS_ROW_DIM;
     // lanes 0-15 look up the rows to bring, the others 16 of the other CTA's
     const int mine = (lane < 16 ? 32 * (int)rank : 32 * (1 - (int)rank)) + 16 * w + (lane & 15);
@@ -212,24 +211,38 @@ __device__ void bring_keys(const Args& g, uint32_t sbase, Aux* x, uint32_t rank,
     while (walk.next()) {
         const uint8_t* rows = static_cast<const uint8_t*>(a.rows) + walk.b * a.request_stride;
         const Lookup lookup(a, walk);
-        auto prefetch = [&](int t) {
-            if (t >= walk.t1 || lane >= 16) return;
-            const int r = lookup(t, mine);
-            if (r >= 0) tc::prefetch_l2(rows + r * a.row_stride, row_bytes);
+        // Lines of 16 rows to L2, eight lanes a row (a bulk prefetch a row took about 2,000 clocks a tile to issue).
+        auto prefetch = [&](int at) {
+#pragma unroll
+            for (int n = 0; n < 16; n += 4) {
+                const int r = __shfl_sync(~0u, at, n + (lane >> 3));
+                if (r < 0) continue;
+                const uint8_t* line = rows + r * a.row_stride;
+                const int c = (lane & 7) * 128;
+                if (c < row_bytes) tc::prefetch_l2(line + c);
+                if ((lane & 7) == 0) tc::prefetch_l2(line + row_bytes - 1);
+            }
         };
         int t = walk.t0;
-        if ((j & 1) != stage) ++t;  // this stage's first tile of the piece
-        for (int n = 2; n < kPrefetch; n += 2) prefetch(t + n);
-        int next = t < walk.t1 ? lookup(t, mine) : -1;
+        if ((j & 1) != turn) ++t;  // these warps' first tile of the piece
+        // Rows of these warps' next three tiles: the third is prefetched, and each was looked up an
+        // iteration before it is used.
+        int next = lookup.row(lookup.raw(t, mine)), after = lookup.row(lookup.raw(t + 2, mine));
+        int ahead = lookup.raw(t + 4, mine);
+        prefetch(after);
         for (; t < walk.t1; t += 2) {
             const long long jt = j + t - walk.t0;
             const int row = next;
-            if (t + 2 < walk.t1) next = lookup(t + 2, mine);
-            prefetch(t + kPrefetch);
-            const int m = (int)(jt & 3);
+            next = after;
+            after = lookup.row(ahead);
+            if (t + 4 < walk.t1) prefetch(after);
+            ahead = lookup.raw(t + 6, mine);
+            const int m = (int)(jt % kMeta), stage = (int)(jt % kKStages);
+            const uint32_t reuse = (uint32_t)(jt / kKStages - 1) & 1;
+            const uint32_t k_smem = sbase + kOffK + stage * kKBytes;
             const unsigned ok_bits = __ballot_sync(~0u, row >= 0);
             if constexpr (!E4M3) {
-                if (jt >= 2) wait(tc::smem_addr(&x->sfull[stage]), ((jt - 2) >> 1) & 1, x, error);
+                if (jt >= kKStages) wait(tc::smem_addr(&x->kfree[stage]), reuse, x, error);
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
                     const int tok = n * 4 + (lane >> 3), ch = lane & 7;  // 16-byte piece of a block
@@ -252,7 +265,7 @@ __device__ void bring_keys(const Args& g, uint32_t sbase, Aux* x, uint32_t rank,
                         v[n][c] = r >= 0 ? *reinterpret_cast<const uint4*>(rows + r * a.row_stride + c * 64 + ch * 16)
                                          : make_uint4(0, 0, 0, 0);
                 }
-                if (jt >= 2) wait(tc::smem_addr(&x->sfull[stage]), ((jt - 2) >> 1) & 1, x, error);
+                if (jt >= kKStages) wait(tc::smem_addr(&x->kfree[stage]), reuse, x, error);
                 x->scale[m][mine] = sc;
                 x->log_scale[m][mine] = __float2half(log2f(fabsf(sc)));
 #pragma unroll
@@ -272,7 +285,7 @@ __device__ void bring_keys(const Args& g, uint32_t sbase, Aux* x, uint32_t rank,
             tc::cp_async_wait<0>();
             tc::fence_async_shared();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive_cluster(full);
+            if (lane == 0) tc::mbar_arrive_cluster(tc::map_to_rank(tc::smem_addr(&x->kfull[stage]), 0));
         }
         j += walk.t1 - walk.t0;
     }
@@ -287,7 +300,6 @@ __device__ void bring_values(const Args& g, uint32_t sbase, Aux* x, uint32_t ran
     const int lane = threadIdx.x & 31, wg = (threadIdx.x >> 5) - 8;
     const int stage = wg >> 1, w = wg & 1;
     const uint32_t full = tc::map_to_rank(tc::smem_addr(&x->vfull[stage]), 0);
-    const uint32_t qfull = tc::map_to_rank(tc::smem_addr(&x->qfull), 0);
     const uint32_t v_smem = sbase + kOffV + stage * kVBytes;
     const int mine = 32 * w + lane;
     const int block0 = 4 * (int)rank;  // the first of this CTA's blocks of 64 channels
@@ -298,11 +310,11 @@ __device__ void bring_values(const Args& g, uint32_t sbase, Aux* x, uint32_t ran
         const Lookup lookup(a, walk);
         int t = walk.t0;
         if ((j & 1) != stage) ++t;
-        int next = t < walk.t1 ? lookup(t, mine) : -1;
-        // Q's readers, the products of the earlier pieces' keys, are done.  (A parity tells two
-        // phases apart, so the tile before the last one is waited for first.)
+        int next = lookup.raw(t, mine);
+        // The last piece's products are done.  (A parity tells two phases apart, so the tile before the
+        // last one is waited for first.)
         if (j >= 2) wait(tc::smem_addr(&x->pvdone[j & 1]), ((j - 2) >> 1) & 1, x, error);
-        if (j >= 1) wait(tc::smem_addr(&x->sfull[(j - 1) & 1]), ((j - 1) >> 1) & 1, x, error);
+        if (j >= 1) wait(tc::smem_addr(&x->pvdone[(j - 1) & 1]), ((j - 1) >> 1) & 1, x, error);
         const T* q = static_cast<const T*>(a.q) + walk.b * a.q_stride[0] + walk.p * a.q_stride[1];
 #pragma unroll 1
         for (int n = 0; n < 4; ++n) {
@@ -310,7 +322,8 @@ __device__ void bring_values(const Args& g, uint32_t sbase, Aux* x, uint32_t ran
             const int head = walk.hb * 128 + (int)rank * 64 + r;
             const bool ok = head < a.heads;
             const uint8_t* src = reinterpret_cast<const uint8_t*>(q + (ok ? head : 0) * a.q_stride[2]) + (lane & 7) * 16;
-            const uint32_t dst = sbase + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
+            const uint32_t dst = r * 128 + (((lane & 7) ^ (r & 7)) << 4);
+            auto block = [&](int c) { return dst + sbase + (c < kQTmem ? kOffV + c * 8192 : (c - kQTmem) * 8192); };
             if constexpr (E4M3 && HsType<T>::is_bf16) {
                 // The products are in fp16 (which holds e4m3): the head's query is scaled by a power of two
                 // that takes its largest magnitude to [2^13, 2^14); what is 2^-28 of it or more stays exact.
@@ -336,22 +349,23 @@ __device__ void bring_values(const Args& g, uint32_t sbase, Aux* x, uint32_t ran
                     uint32_t h[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) h[i] = pack2<__half>(__low2float(e[i]) * f, __high2float(e[i]) * f);
-                    tc::st_shared16(dst + c * 8192, h[0], h[1], h[2], h[3]);
+                    tc::st_shared16(block(c), h[0], h[1], h[2], h[3]);
                 }
             } else {
 #pragma unroll
-                for (int c = 0; c < 9; ++c) tc::cp_async16(dst + c * 8192, src + c * 128, ok);
+                for (int c = 0; c < 9; ++c) tc::cp_async16(block(c), src + c * 128, ok);
             }
         }
         tc::cp_async_commit();
         tc::cp_async_wait<0>();
         tc::fence_async_shared();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive_cluster(qfull);
+        if (lane == 0) tc::mbar_arrive(tc::smem_addr(&x->qhere));
+        wait(tc::smem_addr(&x->lifted), pieces & 1, x, error);
         for (; t < walk.t1; t += 2) {
             const long long jt = j + t - walk.t0;
-            const int row = next;
-            if (t + 2 < walk.t1) next = lookup(t + 2, mine);
+            const int row = lookup.row(next);
+            next = lookup.raw(t + 2, mine);
             if constexpr (!E4M3) {
                 if (jt >= 2) wait(tc::smem_addr(&x->pvdone[stage]), ((jt - 2) >> 1) & 1, x, error);
 #pragma unroll
@@ -395,18 +409,26 @@ __device__ void bring_values(const Args& g, uint32_t sbase, Aux* x, uint32_t ran
 }
 
 // Q K^T of one tile into buffer S, and P V into O (the warp's elected lane).
-template <typename T, int S> __device__ __forceinline__ void issue_qk(uint32_t sbase, uint32_t tmem, Aux* x)
+template <typename T, int S>
+__device__ __forceinline__ void issue_qk(uint32_t sbase, uint32_t tmem, uint64_t k_desc, uint64_t& kfree, Aux* x)
 {
     constexpr uint32_t id = tc::inst_desc(HsType<T>::is_bf16, 128, kTile, false, false);
-    const uint64_t q_desc = tc::smem_desc(sbase, 16, 1024), k_desc = tc::smem_desc(sbase + kOffK + S * kKBytes, 16, 1024);
+    const uint64_t q_desc = tc::smem_desc(sbase, 16, 1024);
     if (tc::elect_one()) {
 #pragma unroll
-        for (int c = 0; c < 9; ++c)
+        for (int c = 0; c < kQTmem; ++c)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                tc::mma_ss<2>(tmem + kColS + 32 * S, q_desc + ((c * 8192 + k * 32) >> 4), k_desc + ((c * 4096 + k * 32) >> 4),
-                              id, (c | k) != 0);
+                tc::mma_ts<2>(tmem + kColS + 32 * S, tmem + kColQ + 32 * c + 8 * k, k_desc + ((c * 4096 + k * 32) >> 4), id,
+                              (c | k) != 0);
+#pragma unroll
+        for (int c = kQTmem; c < 9; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                tc::mma_ss<2>(tmem + kColS + 32 * S, q_desc + (((c - kQTmem) * 8192 + k * 32) >> 4),
+                              k_desc + ((c * 4096 + k * 32) >> 4), id, true);
         tc::commit<2>(tc::smem_addr(&x->sfull[S]));
+        tc::commit<2>(tc::smem_addr(&kfree));
     }
     __syncwarp();
 }
@@ -442,8 +464,10 @@ __device__ void drain(Aux* x, int which)
 template <typename T> __device__ void multiply_qk(const Args& g, uint32_t sbase, Aux* x, int* error)
 {
     const uint32_t tmem = __shfl_sync(~0u, x->tmem, 0);
+    const uint64_t k_base = tc::smem_desc(sbase + kOffK, 16, 1024);
     long long j = 0;
-    int pieces = 0;
+    int pieces = 0, stage = 0;
+    uint32_t phase = 0;
     Walk walk(g, x);
     while (walk.next()) {
         wait(tc::smem_addr(&x->qfull), pieces++ & 1, x, error);
@@ -451,13 +475,15 @@ template <typename T> __device__ void multiply_qk(const Args& g, uint32_t sbase,
             const int s = (int)(j & 1);
             // S's buffer has been read
             if (j >= 2) wait(tc::smem_addr(&x->pready[s]), ((j - 2) >> 1) & 1, x, error);
-            wait(tc::smem_addr(&x->kfull[s]), (j >> 1) & 1, x, error);
+            wait(tc::smem_addr(&x->kfull[stage]), phase, x, error);
             __syncwarp();
             tc::fence_after();
+            const uint64_t k_desc = k_base + stage * (kKBytes >> 4);
             if (s)
-                issue_qk<T, 1>(sbase, tmem, x);
+                issue_qk<T, 1>(sbase, tmem, k_desc, x->kfree[stage], x);
             else
-                issue_qk<T, 0>(sbase, tmem, x);
+                issue_qk<T, 0>(sbase, tmem, k_desc, x->kfree[stage], x);
+            if (++stage == kKStages) stage = 0, phase ^= 1;
         }
     }
     drain(x, 0);
@@ -483,6 +509,31 @@ template <typename T> __device__ void multiply_pv(const Args& g, uint32_t sbase,
     drain(x, 1);
 }
 
+// Copy 6 of Q's 9 blocks of channels to tensor memory: products that read A there leave
+// shared memory, whose bandwidth bounds a tile, to the others.  A pair's product of
+// 128 rows computes half of its columns in lanes 64-127, which read their own copy of A.
+__device__ __forceinline__ void lift_queries(uint32_t sbase, uint32_t tmem, uint32_t qfull, uint32_t lifted)
+{
+    const int row = threadIdx.x & 63;
+#pragma unroll
+    for (int c = 0; c < kQTmem; ++c) {
+        uint32_t r[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint4 v = tc::ld_shared16(sbase + kOffV + c * 8192 + row * 128 + ((i ^ (row & 7)) << 4));
+            r[4 * i] = v.x, r[4 * i + 1] = v.y, r[4 * i + 2] = v.z, r[4 * i + 3] = v.w;
+        }
+        tc::tmem_st32(tmem + kColQ + 32 * c, r);
+    }
+    tc::tmem_wait_st();
+    tc::fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+        tc::mbar_arrive_cluster(qfull);
+        tc::mbar_arrive(lifted);
+    }
+}
+
 // Softmax of 64 heads: thread (head, half) takes 32 of a tile's 64 rows.
 template <typename T, bool E4M3>
 __device__ void soften(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int pair, uint8_t* ws, int* error)
@@ -496,7 +547,10 @@ __device__ void soften(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int
     Walk walk(g, x);
     const uint32_t pready[2] = {tc::map_to_rank(tc::smem_addr(&x->pready[0]), 0),
                                 tc::map_to_rank(tc::smem_addr(&x->pready[1]), 0)};
+    const uint32_t qfull = tc::map_to_rank(tc::smem_addr(&x->qfull), 0);
     for (int pieces = 0; walk.next(); ++pieces) {
+        wait(tc::smem_addr(&x->qhere), pieces & 1, x, error);
+        lift_queries(sbase, tmem, qfull, tc::smem_addr(&x->lifted));
         float ref = 0.f, sum = 0.f;
         bool seen = false;  // a row that counts has been met: ref is a maximum
         for (int t = walk.t0; t < walk.t1; ++t, ++j) {
@@ -509,9 +563,9 @@ __device__ void soften(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int
             if constexpr (E4M3 && HsType<T>::is_bf16)
                 if (t == walk.t0)
                     c = __uint_as_float((uint32_t)(127 - x->q_up[pieces & 1][row]) << 23) * (a.scale * 1.4426950408889634f);
-            const uint32_t valid = reinterpret_cast<const uint32_t*>(x->valid[j & 3])[half];
-            const float* wt = x->scale[j & 3] + 32 * half;
-            const __half* lw = x->log_scale[j & 3] + 32 * half;
+            const uint32_t valid = reinterpret_cast<const uint32_t*>(x->valid[j % kMeta])[half];
+            const float* wt = x->scale[j % kMeta] + 32 * half;
+            const __half* lw = x->log_scale[j % kMeta] + 32 * half;
             float v[32], top = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -702,13 +756,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_atte
                 st->tile = (int)tile;
             }
             for (int i = 0; i < 2; ++i) {
-                tc::mbar_init(tc::smem_addr(&x->kfull[i]), 4);
                 tc::mbar_init(tc::smem_addr(&x->vfull[i]), 4);
                 tc::mbar_init(tc::smem_addr(&x->sfull[i]), 1);
                 tc::mbar_init(tc::smem_addr(&x->pready[i]), 8);
                 tc::mbar_init(tc::smem_addr(&x->pvdone[i]), 1);
                 tc::mbar_init(tc::smem_addr(&x->spare[i]), 1);
             }
+            for (int i = 0; i < kKStages; ++i) {
+                tc::mbar_init(tc::smem_addr(&x->kfull[i]), 4);
+                tc::mbar_init(tc::smem_addr(&x->kfree[i]), 1);
+            }
+            tc::mbar_init(tc::smem_addr(&x->qhere), 4);
+            tc::mbar_init(tc::smem_addr(&x->lifted), 4);
             tc::mbar_init(tc::smem_addr(&x->qfull), 8);
             tc::mbar_init_fence();
         }
