@@ -852,13 +852,13 @@ __global__ void __launch_bounds__(512) hs_attend_join_kernel(const __grid_consta
             float o[COLS];
 #pragma unroll
             for (int k = 0; k < COLS; ++k) o[k] = q.o[rank][c0 + k][lane];
-            if (l == 0.f) continue;  // no row counted
-            const float up = fmaxf(top, ref);
-            const float keep = tc::exp2_approx(top - up), w = tc::exp2_approx(ref - up);
+            // without a branch, so that the loads of several pieces are in flight; a sum of 0: no row counted
+            const float up = l == 0.f ? top : fmaxf(top, ref), base = up == -INFINITY ? 0.f : up;
+            const float keep = tc::exp2_approx(top - base), w = l == 0.f ? 0.f : tc::exp2_approx(ref - base);
             top = up;
             sum = sum * keep + w * l;
 #pragma unroll
-            for (int k = 0; k < COLS; ++k) acc[k] = acc[k] * keep + w * o[k];
+            for (int k = 0; k < COLS; ++k) acc[k] = acc[k] * keep + (l == 0.f ? 0.f : w * o[k]);
         }
     tops[group][lane] = top;
     sums[group][lane] = sum;

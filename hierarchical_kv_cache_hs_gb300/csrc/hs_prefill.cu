@@ -918,16 +918,16 @@ template <typename T> __global__ void __launch_bounds__(512) hs_prefill_join_ker
         for (int n = first + group; n <= last; n += 4) {
             const Partial& q = parts[2 * n + (n == first)];
             const float ref = q.ref[quarter][row], l = q.sum[quarter][row];
-            if (l == 0.f) continue;  // no key counted
+            // without a branch, so that the loads of several pieces are in flight; a sum of 0: no key counted
             float o[kJoinCols];
 #pragma unroll
             for (int k = 0; k < kJoinCols; ++k) o[k] = q.o[quarter][c0 + k][row];
-            const float up = fmaxf(top, ref);
-            const float keep = tc::exp2_approx(top - up), w = tc::exp2_approx(ref - up);
+            const float up = l == 0.f ? top : fmaxf(top, ref), base = up == -INFINITY ? 0.f : up;
+            const float keep = tc::exp2_approx(top - base), w = l == 0.f ? 0.f : tc::exp2_approx(ref - base);
             top = up;
             sum = sum * keep + w * l;
 #pragma unroll
-            for (int k = 0; k < kJoinCols; ++k) acc[k] = acc[k] * keep + w * o[k];
+            for (int k = 0; k < kJoinCols; ++k) acc[k] = acc[k] * keep + (l == 0.f ? 0.f : w * o[k]);
         }
     tops[group][row] = top;
     sums[group][row] = sum;
