@@ -16,14 +16,11 @@
 // Work split: the tiles of all units (a unit: request, position, 128 heads) form
 // one line that is cut into equal pieces, one a pair; units cut in two leave
 // their sums in the workspace and a second kernel joins them.
-#include <type_traits>
+#include "hs_attend.h"
 
-#include "hs_ops.h"
-#include "hs_tc.h"
-
+namespace hs_attn {
 namespace {
 
-constexpr int kTile = 64;         // rows a tile
 constexpr int kThreads = 14 * 32;
 constexpr int kMaxPairs = 76;     // pairs of SMs
 
@@ -44,9 +41,7 @@ struct Aux {
     uint64_t kfull[kKStages], kfree[kKStages], vfull[2], qhere, lifted, qfull, sfull[2], pready[2], pvdone[2], spare[2];
     uint32_t tmem;
     int dead;
-    long long start_unit;  // where this pair's piece of the line begins
-    long long count;       // its tiles
-    int start_tile;
+    Piece piece;
     // Per tile, kMeta deep: a tile's keys may arrive while the softmax four tiles back still reads these.
     uint16_t valid[kMeta][2][2];  // [half][warp]: one bit a row
     alignas(16) float scale[kMeta][kTile];
@@ -60,140 +55,15 @@ static_assert(kSmem <= 232448, "shared memory");
 // Tensor memory columns.
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;
 
-struct Args {
-    hs_attend_t a;
-    int head_blocks;  // of 128
-    int flat;         // 1: equal pieces of the line of tiles; 0: whole units
-    int64_t units;
-};
-
 // Workspace: an error word, where each pair's piece starts, and two partial results a pair.
 struct Partial {
     float o[2][256][128];  // [CTA][column][lane]
     float ref[2][128], sum[2][128];
 };
-struct Start {
-    long long unit;
-    int tile, pad;
-};
 constexpr size_t kOffStart = 256;
 constexpr size_t kOffPartial = kOffStart + sizeof(Start) * (kMaxPairs + 4);
 
-__device__ __forceinline__ int request_tiles(const hs_attend_t& a, long long b)
-{
-    long long n = a.entries;
-    if (!a.slots) {
-        n = a.lengths[b];
-        n = n < 0 ? 0 : n > a.n_rows ? a.n_rows : n;
-    }
-    return n <= kTile ? 1 : (int)((n + kTile - 1) / kTile);
-}
-
-// One pair's pieces of units, in order.
-struct Walk {
-    const Args& g;
-    long long unit, left;
-    int tile;
-    // the current piece
-    long long b;
-    int p, hb, t0, t1, tiles;
-    long long rows;  // entries, or allowed rows
-
-    __device__ Walk(const Args& args, const Aux* x) : g(args), unit(x->start_unit), left(x->count), tile(x->start_tile) {}
-
-    __device__ bool next()
-    {
-        if (left <= 0) return false;
-        const hs_attend_t& a = g.a;
-        const int upr = a.positions * g.head_blocks;
-        b = unit / upr;
-        const int rem = (int)(unit - b * upr);
-        p = rem / g.head_blocks;
-        hb = rem - p * g.head_blocks;
-        tiles = request_tiles(a, b);
-        rows = a.entries;
-        if (!a.slots) {
-            rows = a.lengths[b];
-            rows = rows > a.n_rows ? a.n_rows : rows;
-            rows = rows - a.positions + 1 + p;
-            rows = rows < 0 ? 0 : rows;
-        }
-        t0 = tile;
-        t1 = (long long)(tiles - t0) <= left ? tiles : t0 + (int)left;
-        left -= t1 - t0;
-        ++unit;
-        tile = 0;
-        return true;
-    }
-};
-
-// Bounded wait: on a timeout the CTA is marked dead and every later wait returns at once.
-__device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, Aux* x, int* error)
-{
-    if (tc::mbar_try(bar, parity)) return;
-    const long long t0 = clock64();
-    while (!tc::mbar_try(bar, parity)) {
-        if (*(volatile int*)&x->dead) return;
-        if (clock64() - t0 > tc::kWaitClocks) {
-            *(volatile int*)&x->dead = 1;
-            if (error) atomicExch(error, 1);
-            return;
-        }
-    }
-}
-
-// Four e4m3 values as two pairs of fp16, which holds each of them (and NaN).
-__device__ __forceinline__ void widen(uint32_t v, uint32_t& lo, uint32_t& hi)
-{
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(v));
-}
-
-template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
-template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b)
-{
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b)
-{
-    const __half2 v = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 // ---- the warps' parts ------------------------------------------------------------
-
-// This lane's row of a tile: request rows at `rows`, entry i of the list (or the i-th row).
-struct Lookup {
-    const hs_attend_t& a;
-    const int32_t* slots;
-    long long n;
-    __device__ Lookup(const hs_attend_t& args, const Walk& w)
-        : a(args), slots(args.slots ? args.slots + w.b * args.slots_stride[0] + w.p * args.slots_stride[1] : nullptr), n(w.rows)
-    {
-    }
-    // The list's entry, unchecked: looked at an iteration later, so that no warp waits for it here.
-    __device__ int raw(int tile, int at) const
-    {
-        const long long i = (long long)tile * kTile + at;
-        return i >= n ? -1 : slots ? slots[i] : (int)i;
-    }
-    __device__ int row(int raw) const { return raw >= 0 && raw < a.n_rows ? raw : -1; }  // or -1
-};
-
-// 16 e4m3 values as two 16-byte pieces of fp16 at dst + c0 and dst + c1.
-__device__ __forceinline__ void store_wide(const uint4& v, uint32_t dst, int c0, int c1)
-{
-    uint32_t e[8];
-    widen(v.x, e[0], e[1]);
-    widen(v.y, e[2], e[3]);
-    widen(v.z, e[4], e[5]);
-    widen(v.w, e[6], e[7]);
-    tc::st_shared16(dst + c0, e[0], e[1], e[2], e[3]);
-    tc::st_shared16(dst + c1, e[4], e[5], e[6], e[7]);
-}
 
 // Keys: this CTA's 32 rows of each tile, whole.  Two warps take the even tiles and two
 // the odd ones, 16 rows a warp; they also say which of the tile's 64 rows count.
@@ -207,42 +77,30 @@ __device__ void bring_keys(const Args& g, uint32_t sbase, Aux* x, uint32_t rank,
     // lanes 0-15 look up the rows to bring, the others 16 of the other CTA's
     const int mine = (lane < 16 ? 32 * (int)rank : 32 * (1 - (int)rank)) + 16 * w + (lane & 15);
     long long j = 0;  // tiles so far
-    Walk walk(g, x);
+    Walk walk(g, x->piece);
     while (walk.next()) {
         const uint8_t* rows = static_cast<const uint8_t*>(a.rows) + walk.b * a.request_stride;
         const Lookup lookup(a, walk);
-        // Lines of 16 rows to L2, eight lanes a row (a bulk prefetch a row took about 2,000 clocks a tile to issue).
-        auto prefetch = [&](int at) {
-#pragma unroll
-            for (int n = 0; n < 16; n += 4) {
-                const int r = __shfl_sync(~0u, at, n + (lane >> 3));
-                if (r < 0) continue;
-                const uint8_t* line = rows + r * a.row_stride;
-                const int c = (lane & 7) * 128;
-                if (c < row_bytes) tc::prefetch_l2(line + c);
-                if ((lane & 7) == 0) tc::prefetch_l2(line + row_bytes - 1);
-            }
-        };
         int t = walk.t0;
         if ((j & 1) != turn) ++t;  // these warps' first tile of the piece
         // Rows of these warps' next three tiles: the third is prefetched, and each was looked up an
         // iteration before it is used.
         int next = lookup.row(lookup.raw(t, mine)), after = lookup.row(lookup.raw(t + 2, mine));
         int ahead = lookup.raw(t + 4, mine);
-        prefetch(after);
+        prefetch_rows(rows, a.row_stride, row_bytes, after);
         for (; t < walk.t1; t += 2) {
             const long long jt = j + t - walk.t0;
             const int row = next;
             next = after;
             after = lookup.row(ahead);
-            if (t + 4 < walk.t1) prefetch(after);
+            if (t + 4 < walk.t1) prefetch_rows(rows, a.row_stride, row_bytes, after);
             ahead = lookup.raw(t + 6, mine);
             const int m = (int)(jt % kMeta), stage = (int)(jt % kKStages);
             const uint32_t reuse = (uint32_t)(jt / kKStages - 1) & 1;
             const uint32_t k_smem = sbase + kOffK + stage * kKBytes;
             const unsigned ok_bits = __ballot_sync(~0u, row >= 0);
             if constexpr (!E4M3) {
-                if (jt >= kKStages) wait(tc::smem_addr(&x->kfree[stage]), reuse, x, error);
+                if (jt >= kKStages) wait(tc::smem_addr(&x->kfree[stage]), reuse, &x->dead, error);
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
                     const int tok = n * 4 + (lane >> 3), ch = lane & 7;  // 16-byte piece of a block
@@ -265,7 +123,7 @@ __device__ void bring_keys(const Args& g, uint32_t sbase, Aux* x, uint32_t rank,
                         v[n][c] = r >= 0 ? *reinterpret_cast<const uint4*>(rows + r * a.row_stride + c * 64 + ch * 16)
                                          : make_uint4(0, 0, 0, 0);
                 }
-                if (jt >= kKStages) wait(tc::smem_addr(&x->kfree[stage]), reuse, x, error);
+                if (jt >= kKStages) wait(tc::smem_addr(&x->kfree[stage]), reuse, &x->dead, error);
                 x->scale[m][mine] = sc;
                 x->log_scale[m][mine] = __float2half(log2f(fabsf(sc)));
 #pragma unroll
@@ -304,7 +162,7 @@ __device__ void bring_values(const Args& g, uint32_t sbase, Aux* x, uint32_t ran
     const int mine = 32 * w + lane;
     const int block0 = 4 * (int)rank;  // the first of this CTA's blocks of 64 channels
     long long j = 0;
-    Walk walk(g, x);
+    Walk walk(g, x->piece);
     for (int pieces = 0; walk.next(); ++pieces) {
         const uint8_t* rows = static_cast<const uint8_t*>(a.rows) + walk.b * a.request_stride;
         const Lookup lookup(a, walk);
@@ -313,8 +171,8 @@ __device__ void bring_values(const Args& g, uint32_t sbase, Aux* x, uint32_t ran
         int next = lookup.raw(t, mine);
         // The last piece's products are done.  (A parity tells two phases apart, so the tile before the
         // last one is waited for first.)
-        if (j >= 2) wait(tc::smem_addr(&x->pvdone[j & 1]), ((j - 2) >> 1) & 1, x, error);
-        if (j >= 1) wait(tc::smem_addr(&x->pvdone[(j - 1) & 1]), ((j - 1) >> 1) & 1, x, error);
+        if (j >= 2) wait(tc::smem_addr(&x->pvdone[j & 1]), ((j - 2) >> 1) & 1, &x->dead, error);
+        if (j >= 1) wait(tc::smem_addr(&x->pvdone[(j - 1) & 1]), ((j - 1) >> 1) & 1, &x->dead, error);
         const T* q = static_cast<const T*>(a.q) + walk.b * a.q_stride[0] + walk.p * a.q_stride[1];
 #pragma unroll 1
         for (int n = 0; n < 4; ++n) {
@@ -325,31 +183,20 @@ __device__ void bring_values(const Args& g, uint32_t sbase, Aux* x, uint32_t ran
             const uint32_t dst = r * 128 + (((lane & 7) ^ (r & 7)) << 4);
             auto block = [&](int c) { return dst + sbase + (c < kQTmem ? kOffV + c * 8192 : (c - kQTmem) * 8192); };
             if constexpr (E4M3 && HsType<T>::is_bf16) {
-                // The products are in fp16 (which holds e4m3): the head's query is scaled by a power of two
-                // that takes its largest magnitude to [2^13, 2^14); what is 2^-28 of it or more stays exact.
                 uint4 v[9];
                 float top = 0.f;
 #pragma unroll
                 for (int c = 0; c < 9; ++c) {
                     v[c] = ok ? *reinterpret_cast<const uint4*>(src + c * 128) : make_uint4(0, 0, 0, 0);
-                    const __nv_bfloat162* e = reinterpret_cast<const __nv_bfloat162*>(&v[c]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(__low2float(e[i])), fabsf(__high2float(e[i]))));
+                    top = fmaxf(top, largest_bf16(v[c]));
                 }
                 for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-                // 2^(13 - exponent), kept for the scores; zeros and infinities stay as they are
-                const int ex = (int)(__float_as_uint(top) >> 23);
-                const bool plain = ex == 0 || ex == 255;
-                const int up = plain ? 0 : min(max(140 - ex, -100), 100);
-                const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+                const int up = power_up(top);
                 if ((lane & 7) == 0) x->q_up[pieces & 1][r] = (int8_t)up;
 #pragma unroll
                 for (int c = 0; c < 9; ++c) {
-                    const __nv_bfloat162* e = reinterpret_cast<const __nv_bfloat162*>(&v[c]);
-                    uint32_t h[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) h[i] = pack2<__half>(__low2float(e[i]) * f, __high2float(e[i]) * f);
-                    tc::st_shared16(block(c), h[0], h[1], h[2], h[3]);
+                    const uint4 e = bf16_to_half(v[c], power_of_two(up));
+                    tc::st_shared16(block(c), e.x, e.y, e.z, e.w);
                 }
             } else {
 #pragma unroll
@@ -361,13 +208,13 @@ __device__ void bring_values(const Args& g, uint32_t sbase, Aux* x, uint32_t ran
         tc::fence_async_shared();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(tc::smem_addr(&x->qhere));
-        wait(tc::smem_addr(&x->lifted), pieces & 1, x, error);
+        wait(tc::smem_addr(&x->lifted), pieces & 1, &x->dead, error);
         for (; t < walk.t1; t += 2) {
             const long long jt = j + t - walk.t0;
             const int row = lookup.row(next);
             next = lookup.raw(t + 2, mine);
             if constexpr (!E4M3) {
-                if (jt >= 2) wait(tc::smem_addr(&x->pvdone[stage]), ((jt - 2) >> 1) & 1, x, error);
+                if (jt >= 2) wait(tc::smem_addr(&x->pvdone[stage]), ((jt - 2) >> 1) & 1, &x->dead, error);
 #pragma unroll
                 for (int n = 0; n < 8; ++n) {
                     const int tok = n * 4 + (lane >> 3), ch = lane & 7;
@@ -388,7 +235,7 @@ __device__ void bring_values(const Args& g, uint32_t sbase, Aux* x, uint32_t ran
                         v[n][c] = r >= 0 ? *reinterpret_cast<const uint4*>(rows + r * a.row_stride + (block0 + c) * 64 + ch * 16)
                                          : make_uint4(0, 0, 0, 0);
                 }
-                if (jt >= 2) wait(tc::smem_addr(&x->pvdone[stage]), ((jt - 2) >> 1) & 1, x, error);
+                if (jt >= 2) wait(tc::smem_addr(&x->pvdone[stage]), ((jt - 2) >> 1) & 1, &x->dead, error);
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
                     const int tok = n * 8 + (lane >> 2), r0 = tok & 7;
@@ -468,14 +315,14 @@ template <typename T> __device__ void multiply_qk(const Args& g, uint32_t sbase,
     long long j = 0;
     int pieces = 0, stage = 0;
     uint32_t phase = 0;
-    Walk walk(g, x);
+    Walk walk(g, x->piece);
     while (walk.next()) {
-        wait(tc::smem_addr(&x->qfull), pieces++ & 1, x, error);
+        wait(tc::smem_addr(&x->qfull), pieces++ & 1, &x->dead, error);
         for (int t = walk.t0; t < walk.t1; ++t, ++j) {
             const int s = (int)(j & 1);
             // S's buffer has been read
-            if (j >= 2) wait(tc::smem_addr(&x->pready[s]), ((j - 2) >> 1) & 1, x, error);
-            wait(tc::smem_addr(&x->kfull[stage]), phase, x, error);
+            if (j >= 2) wait(tc::smem_addr(&x->pready[s]), ((j - 2) >> 1) & 1, &x->dead, error);
+            wait(tc::smem_addr(&x->kfull[stage]), phase, &x->dead, error);
             __syncwarp();
             tc::fence_after();
             const uint64_t k_desc = k_base + stage * (kKBytes >> 4);
@@ -492,12 +339,12 @@ template <typename T> __device__ void multiply_pv(const Args& g, uint32_t sbase,
 {
     const uint32_t tmem = __shfl_sync(~0u, x->tmem, 0);
     long long j = 0;
-    Walk walk(g, x);
+    Walk walk(g, x->piece);
     while (walk.next()) {
         for (int t = walk.t0; t < walk.t1; ++t, ++j) {
             const int s = (int)(j & 1);
-            wait(tc::smem_addr(&x->vfull[s]), (j >> 1) & 1, x, error);
-            wait(tc::smem_addr(&x->pready[s]), (j >> 1) & 1, x, error);
+            wait(tc::smem_addr(&x->vfull[s]), (j >> 1) & 1, &x->dead, error);
+            wait(tc::smem_addr(&x->pready[s]), (j >> 1) & 1, &x->dead, error);
             __syncwarp();
             tc::fence_after();
             if (s)
@@ -544,25 +391,25 @@ __device__ void soften(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int
     const uint32_t tmem = x->tmem + ((uint32_t)warp << 21);  // this warp's 32 lanes
     float c = a.scale * 1.4426950408889634f;
     long long j = 0;
-    Walk walk(g, x);
+    Walk walk(g, x->piece);
     const uint32_t pready[2] = {tc::map_to_rank(tc::smem_addr(&x->pready[0]), 0),
                                 tc::map_to_rank(tc::smem_addr(&x->pready[1]), 0)};
     const uint32_t qfull = tc::map_to_rank(tc::smem_addr(&x->qfull), 0);
     for (int pieces = 0; walk.next(); ++pieces) {
-        wait(tc::smem_addr(&x->qhere), pieces & 1, x, error);
+        wait(tc::smem_addr(&x->qhere), pieces & 1, &x->dead, error);
         lift_queries(sbase, tmem, qfull, tc::smem_addr(&x->lifted));
         float ref = 0.f, sum = 0.f;
         bool seen = false;  // a row that counts has been met: ref is a maximum
         for (int t = walk.t0; t < walk.t1; ++t, ++j) {
             const int s = j & 1;
-            wait(tc::smem_addr(&x->sfull[s]), (j >> 1) & 1, x, error);
+            wait(tc::smem_addr(&x->sfull[s]), (j >> 1) & 1, &x->dead, error);
             tc::fence_after();
             uint32_t r[32];
             tc::tmem_ld32(tmem + kColS + 32 * s, r);
             tc::tmem_wait_ld(r);
             if constexpr (E4M3 && HsType<T>::is_bf16)
                 if (t == walk.t0)
-                    c = __uint_as_float((uint32_t)(127 - x->q_up[pieces & 1][row]) << 23) * (a.scale * 1.4426950408889634f);
+                    c = power_of_two(-x->q_up[pieces & 1][row]) * (a.scale * 1.4426950408889634f);
             const uint32_t valid = reinterpret_cast<const uint32_t*>(x->valid[j % kMeta])[half];
             const float* wt = x->scale[j % kMeta] + 32 * half;
             const __half* lw = x->log_scale[j % kMeta] + 32 * half;
@@ -590,10 +437,10 @@ __device__ void soften(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int
             const bool scale_o = seen && keep != 1.f;
             seen = seen || top > -INFINITY;
             // the buffer of P is free once the product two tiles ago is done
-            if (j >= 2) wait(tc::smem_addr(&x->pvdone[s]), ((j - 2) >> 1) & 1, x, error);
+            if (j >= 2) wait(tc::smem_addr(&x->pvdone[s]), ((j - 2) >> 1) & 1, &x->dead, error);
             if (__any_sync(~0u, scale_o)) {
                 if (!scale_o) keep = 1.f;
-                wait(tc::smem_addr(&x->pvdone[1 - s]), ((j - 1) >> 1) & 1, x, error);
+                wait(tc::smem_addr(&x->pvdone[1 - s]), ((j - 1) >> 1) & 1, &x->dead, error);
                 tc::fence_after();
 #pragma unroll 1
                 for (int n = 0; n < 256; n += 32) {
@@ -633,7 +480,7 @@ __device__ void soften(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int
         asm volatile("bar.sync 1, 128;" ::: "memory");
         sum += x->red[0][threadIdx.x ^ 64];
         asm volatile("bar.sync 1, 128;" ::: "memory");
-        wait(tc::smem_addr(&x->pvdone[(j - 1) & 1]), ((j - 1) >> 1) & 1, x, error);
+        wait(tc::smem_addr(&x->pvdone[(j - 1) & 1]), ((j - 1) >> 1) & 1, &x->dead, error);
         tc::fence_after();
         const int head = walk.hb * 128 + (int)rank * 64 + row;
         const bool whole = walk.t0 == 0 && walk.t1 == walk.tiles;
@@ -696,65 +543,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_atte
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may queue up behind this grid
     if (warp == 0) tc::tmem_alloc<2>(tc::smem_addr(&x->tmem), 512);
     if (warp == 12) {
-        // This pair's piece of the line of tiles.
-        const int upr = a.positions * g.head_blocks;
-        long long total, lo, hi, unit, tile;
-        if (a.slots) {
-            const int tiles = request_tiles(a, 0);
-            total = g.units * tiles;
-            const long long n = total < pairs ? total : pairs;
-            if (pair >= n) {
-                lo = hi = 0;
-            } else if (g.flat) {
-                lo = total * pair / n;
-                hi = total * (pair + 1) / n;
-            } else {
-                lo = g.units * pair / pairs * tiles;
-                hi = g.units * (pair + 1) / pairs * tiles;
-            }
-            unit = lo / tiles;
-            tile = lo - unit * tiles;
-        } else {
-            total = 0;
-            for (int b = lane; b < a.batch; b += 32) total += (long long)request_tiles(a, b) * upr;
-            for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
-            const long long n = total < pairs ? total : pairs;
-            lo = pair < n ? total * pair / n : 0;
-            hi = pair < n ? total * (pair + 1) / n : 0;
-            unit = tile = 0;
-            long long before = 0;
-            for (int b0 = 0; b0 < a.batch; b0 += 32) {
-                const int b = b0 + lane;
-                const long long tiles = b < a.batch ? request_tiles(a, b) : 0;
-                long long incl = tiles * upr;
-                for (int o = 1; o < 32; o <<= 1) {
-                    const long long up = __shfl_up_sync(~0u, incl, o);
-                    if (lane >= o) incl += up;
-                }
-                const long long at = before + incl - tiles * upr;  // where request b begins
-                const bool here = b < a.batch && lo >= at && lo < at + tiles * upr;
-                const unsigned who = __ballot_sync(~0u, here);
-                if (who) {
-                    const int src = __ffs(who) - 1;
-                    const long long u = here ? (long long)b * upr + (lo - at) / tiles : 0;
-                    const long long tl = here ? (lo - at) % tiles : 0;
-                    unit = __shfl_sync(~0u, u, src);
-                    tile = __shfl_sync(~0u, tl, src);
-                    break;
-                }
-                before += __shfl_sync(~0u, incl, 31);
-            }
-        }
+        const Piece p = find_piece(g, pair, pairs);
         if (lane == 0) {
-            x->start_unit = unit;
-            x->start_tile = (int)tile;
-            x->count = hi - lo;
+            x->piece = p;
             x->dead = 0;
-            if (rank == 0) {
-                Start* st = reinterpret_cast<Start*>(ws + kOffStart) + pair;
-                st->unit = hi > lo ? unit : -1;
-                st->tile = (int)tile;
-            }
+            if (rank == 0) reinterpret_cast<Start*>(ws + kOffStart)[pair] = {p.count > 0 ? p.unit : -1, p.tile, 0};
             for (int i = 0; i < 2; ++i) {
                 tc::mbar_init(tc::smem_addr(&x->vfull[i]), 4);
                 tc::mbar_init(tc::smem_addr(&x->sfull[i]), 1);
@@ -778,7 +571,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_atte
     tc::cluster_sync();
     tc::fence_after();
 
-    if (x->count > 0) {
+    if (x->piece.count > 0) {
         if (warp < 4)
             soften<T, E4M3>(g, sbase, x, rank, pair, ws, error);
         else if (warp < 8)
@@ -806,35 +599,14 @@ template <typename T, int COLS>
 __global__ void __launch_bounds__(512) hs_attend_join_kernel(const __grid_constant__ Args g, int pairs)
 {
     __shared__ float tops[4][128], sums[4][128], cols[3][COLS][128];
-    __shared__ int counts[4], first_cut;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const hs_attend_t& a = g.a;
     const uint8_t* ws = static_cast<const uint8_t*>(a.workspace);
     const Partial* parts = reinterpret_cast<const Partial*>(ws + kOffPartial);
+    long long unit;
+    int first, last;
+    if (!find_cut(reinterpret_cast<const Start*>(ws + kOffStart), pairs, blockIdx.x, unit, first, last)) return;
     const int t = threadIdx.x;
-    if (t == 0) first_cut = 0;
-    long long my_unit = -1;
-    bool inside = false, cut = false;  // pair t begins inside a unit; the first to
-    if (t < 128) {
-        const Start* start = reinterpret_cast<const Start*>(ws + kOffStart);
-        if (t > 0 && t < pairs) {
-            my_unit = start[t].unit;
-            inside = my_unit >= 0 && start[t].tile > 0;
-            cut = inside && !(start[t - 1].unit == my_unit && start[t - 1].tile > 0);
-        }
-        const unsigned m = __ballot_sync(~0u, cut);
-        if ((t & 31) == 0) counts[t >> 5] = __popc(m);
-    }
-    __syncthreads();
-    if (t < 128) {
-        int before = __popc(__ballot_sync(~0u, cut) & ((1u << (t & 31)) - 1));
-        for (int w = 0; w < t >> 5; ++w) before += counts[w];
-        if (cut && before == (int)blockIdx.x) first_cut = t;
-    }
-    __syncthreads();
-    if (first_cut == 0) return;
-    const long long unit = reinterpret_cast<const Start*>(ws + kOffStart)[first_cut].unit;
-    const int first = first_cut - 1, last = first + __syncthreads_count(inside && my_unit == unit);
     const int rank = blockIdx.y, c0 = COLS * blockIdx.z;
     const int lane = t & 127, group = t >> 7, row = lane & 63, half = lane >> 6;
     const int upr = a.positions * g.head_blocks;
@@ -891,13 +663,6 @@ __global__ void __launch_bounds__(512) hs_attend_join_kernel(const __grid_consta
         a.lse[(b * a.positions + p) * a.heads + head] = some ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
-// Pairs a call can use, from the most tiles its sizes allow.
-int64_t pairs_for(int64_t units, int64_t rows)
-{
-    const int64_t tiles = rows <= kTile ? 1 : (rows + kTile - 1) / kTile;
-    return units * tiles < kMaxPairs ? units * tiles : kMaxPairs;
-}
-
 template <typename T, bool E4M3> cudaError_t launch(const Args& g, int pairs, cudaStream_t s)
 {
     cudaError_t e = cudaFuncSetAttribute(hs_attend_kernel<T, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
@@ -905,30 +670,21 @@ template <typename T, bool E4M3> cudaError_t launch(const Args& g, int pairs, cu
     hs_attend_kernel<T, E4M3><<<2 * pairs, kThreads, kSmem, s>>>(g);
     e = cudaGetLastError();
     if (e != cudaSuccess || !g.flat || pairs <= 1) return e;
-    cudaLaunchConfig_t cfg = {};
     // At most this many units are cut; few units take more blocks each, by narrower columns.
     const int cut = (int)(g.units < pairs - 1 ? g.units : pairs - 1);
     const int cols = cut * (g.a.heads > 64 ? 2 : 1) <= 8 ? 4 : 16;
-    cfg.gridDim = dim3(cut, g.a.heads > 64 ? 2 : 1, 256 / cols);
-    cfg.blockDim = 512;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cols == 4 ? hs_attend_join_kernel<T, 4> : hs_attend_join_kernel<T, 16>, g, pairs);
+    return launch_after(cols == 4 ? hs_attend_join_kernel<T, 4> : hs_attend_join_kernel<T, 16>,
+                        dim3(cut, g.a.heads > 64 ? 2 : 1, 256 / cols), 512, s, g, pairs);
 }
 
 }  // namespace
 
-size_t hs_attend_workspace_bytes(int batch, int positions, int heads, int64_t rows)
+size_t pair_workspace(int64_t units, int64_t tiles)
 {
-    const int64_t units = (int64_t)batch * positions * ((heads + 127) / 128);
-    return kOffPartial + sizeof(Partial) * 2 * (size_t)pairs_for(units, rows);
+    return kOffPartial + sizeof(Partial) * 2 * (size_t)(units * tiles < kMaxPairs ? units * tiles : kMaxPairs);
 }
 
-cudaError_t hs_launch_attend(const hs_attend_t& a, cudaStream_t s)
+cudaError_t launch_pair(const hs_attend_t& a, int sms, cudaStream_t s)
 {
     Args g;
     g.a = a;
@@ -936,20 +692,34 @@ cudaError_t hs_launch_attend(const hs_attend_t& a, cudaStream_t s)
     g.units = (int64_t)a.batch * a.positions * g.head_blocks;
     const int64_t rows = a.slots ? a.entries : a.n_rows;
     const int64_t tiles = rows <= kTile ? 1 : (rows + kTile - 1) / kTile;
-    int64_t pairs = pairs_for(g.units, rows);
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-    if (sms >= 2 && pairs > sms / 2) pairs = sms / 2;
-    // Whole units to a pair, or equal pieces: equal pieces also write and join
-    // up to two partial results a pair (about 12 tiles' time for 128 heads).
-    const int64_t whole = (g.units + pairs - 1) / pairs * tiles;
-    const int64_t pieces = (g.units * tiles + pairs - 1) / pairs + 2 + 10 * (a.heads < 128 ? a.heads : 128) / 128;
-    g.flat = !a.slots || whole > pieces;
+    int64_t pairs = sms / 2 < kMaxPairs ? sms / 2 : kMaxPairs;
+    pairs = g.units * tiles < pairs ? g.units * tiles : pairs < 1 ? 1 : pairs;
+    // Whole units to a pair, or equal pieces: pieces also write and join up to two partial
+    // results a pair, about 10 us, or 10 tiles' time.
+    const int64_t whole = (g.units + pairs - 1) / pairs * tiles, pieces = (g.units * tiles + pairs - 1) / pairs + 10;
+    g.flat = whole > pieces;
     if (!g.flat && pairs > g.units) pairs = g.units;
     const bool e4m3 = a.row_format == HS_ROWS_E4M3;
     if (a.dtype == HS_TYPE_BF16)
         return e4m3 ? launch<__nv_bfloat16, true>(g, (int)pairs, s) : launch<__nv_bfloat16, false>(g, (int)pairs, s);
     return e4m3 ? launch<__half, true>(g, (int)pairs, s) : launch<__half, false>(g, (int)pairs, s);
+}
+
+}  // namespace hs_attn
+
+size_t hs_attend_workspace_bytes(int batch, int positions, int heads, int64_t rows)
+{
+    const int64_t tiles = rows <= hs_attn::kTile ? 1 : (rows + hs_attn::kTile - 1) / hs_attn::kTile;
+    const int64_t units = (int64_t)batch * positions;
+    return heads <= 64 ? hs_attn::narrow_workspace(units, tiles, heads)
+                       : hs_attn::pair_workspace(units * ((heads + 127) / 128), tiles);
+}
+
+cudaError_t hs_launch_attend(const hs_attend_t& a, cudaStream_t s)
+{
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    return a.heads <= 64 ? hs_attn::launch_narrow(a, sms, s) : hs_attn::launch_pair(a, sms, s);
 }

@@ -1,0 +1,309 @@
+// What the two kernels of hs_latent_attend share: how the work is cut, which rows a
+// tile holds, and how 8-bit rows become operands.
+#pragma once
+
+#include <type_traits>
+
+#include "hs_ops.h"
+#include "hs_tc.h"
+
+namespace hs_attn {
+
+constexpr int kTile = 64;  // rows a tile
+
+// A unit is a request, a position and a block of heads; its rows come in tiles, one at
+// least.  The tiles of all units form one line, which the workers (an SM, or a pair of
+// SMs) cut into equal pieces (flat), or whole units go to each.
+struct Args {
+    hs_attend_t a;
+    int head_blocks;
+    int flat;
+    int64_t units;
+};
+
+struct Start {  // where a worker's piece of the line begins (unit -1: it has none)
+    long long unit;
+    int tile, pad;
+};
+struct Piece {
+    long long unit, count;  // count: its tiles
+    int tile;
+};
+
+__device__ __forceinline__ int request_tiles(const hs_attend_t& a, long long b)
+{
+    long long n = a.entries;
+    if (!a.slots) {
+        n = a.lengths[b];
+        n = n < 0 ? 0 : n > a.n_rows ? a.n_rows : n;
+    }
+    return n <= kTile ? 1 : (int)((n + kTile - 1) / kTile);
+}
+
+// Worker i's piece of n workers' (one warp; every lane gets it).
+__device__ __forceinline__ Piece find_piece(const Args& g, int i, int workers)
+{
+    const hs_attend_t& a = g.a;
+    const int lane = threadIdx.x & 31;
+    const int upr = a.positions * g.head_blocks;  // units a request
+    Piece p;
+    if (a.slots) {
+        const int tiles = request_tiles(a, 0);
+        const long long total = g.units * tiles, n = total < workers ? total : workers;
+        long long lo, hi;
+        if (i >= n) {
+            lo = hi = 0;
+        } else if (g.flat) {
+            lo = total * i / n;
+            hi = total * (i + 1) / n;
+        } else {
+            lo = g.units * i / workers * tiles;
+            hi = g.units * (i + 1) / workers * tiles;
+        }
+        p.unit = lo / tiles;
+        p.tile = (int)(lo - p.unit * tiles);
+        p.count = hi - lo;
+        return p;
+    }
+    if (!g.flat) {
+        const long long u0 = g.units * i / workers, u1 = g.units * (i + 1) / workers;
+        long long count = 0;
+        for (int b = lane; b < a.batch; b += 32) {
+            const long long first = (long long)b * upr, lo = first > u0 ? first : u0, hi = first + upr < u1 ? first + upr : u1;
+            if (hi > lo) count += (hi - lo) * request_tiles(a, b);
+        }
+        for (int o = 16; o; o >>= 1) count += __shfl_xor_sync(~0u, count, o);
+        p.unit = u0;
+        p.tile = 0;
+        p.count = count;
+        return p;
+    }
+    long long total = 0;
+    for (int b = lane; b < a.batch; b += 32) total += (long long)request_tiles(a, b) * upr;
+    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
+    const long long n = total < workers ? total : workers;
+    const long long lo = i < n ? total * i / n : 0, hi = i < n ? total * (i + 1) / n : 0;
+    p.unit = 0;
+    p.tile = 0;
+    p.count = hi - lo;
+    long long before = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+        const int b = b0 + lane;
+        const long long tiles = b < a.batch ? request_tiles(a, b) : 0;
+        long long incl = tiles * upr;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long up = __shfl_up_sync(~0u, incl, o);
+            if (lane >= o) incl += up;
+        }
+        const long long at = before + incl - tiles * upr;  // where request b begins
+        const bool here = b < a.batch && lo >= at && lo < at + tiles * upr;
+        const unsigned who = __ballot_sync(~0u, here);
+        if (who) {
+            const int src = __ffs(who) - 1;
+            const long long u = here ? (long long)b * upr + (lo - at) / tiles : 0;
+            const int t = here ? (int)((lo - at) % tiles) : 0;
+            p.unit = __shfl_sync(~0u, u, src);
+            p.tile = __shfl_sync(~0u, t, src);
+            break;
+        }
+        before += __shfl_sync(~0u, incl, 31);
+    }
+    return p;
+}
+
+// The units, or parts of units, of a piece, in order.
+struct Walk {
+    const Args& g;
+    long long unit, left;
+    int tile;
+    // the current one: tiles [t0, t1) of `tiles`
+    long long b;
+    int p, hb, t0, t1, tiles;
+    long long rows;  // entries, or allowed rows
+
+    __device__ Walk(const Args& args, const Piece& x) : g(args), unit(x.unit), left(x.count), tile(x.tile) {}
+
+    __device__ bool next()
+    {
+        if (left <= 0) return false;
+        const hs_attend_t& a = g.a;
+        const int upr = a.positions * g.head_blocks;
+        b = unit / upr;
+        const int rem = (int)(unit - b * upr);
+        p = rem / g.head_blocks;
+        hb = rem - p * g.head_blocks;
+        tiles = request_tiles(a, b);
+        rows = a.entries;
+        if (!a.slots) {
+            rows = a.lengths[b];
+            rows = rows > a.n_rows ? a.n_rows : rows;
+            rows = rows - a.positions + 1 + p;
+            rows = rows < 0 ? 0 : rows;
+        }
+        t0 = tile;
+        t1 = (long long)(tiles - t0) <= left ? tiles : t0 + (int)left;
+        left -= t1 - t0;
+        ++unit;
+        tile = 0;
+        return true;
+    }
+};
+
+// The row at a place of a tile: entry i of the list, or the i-th row.
+struct Lookup {
+    const hs_attend_t& a;
+    const int32_t* slots;
+    long long n;
+    __device__ Lookup(const hs_attend_t& args, const Walk& w)
+        : a(args), slots(args.slots ? args.slots + w.b * args.slots_stride[0] + w.p * args.slots_stride[1] : nullptr), n(w.rows)
+    {
+    }
+    // The list's entry, unchecked: looked at an iteration later, so that no warp waits for it here.
+    __device__ int raw(int tile, int at) const
+    {
+        const long long i = (long long)tile * kTile + at;
+        return i >= n ? -1 : slots ? slots[i] : (int)i;
+    }
+    __device__ int row(int raw) const { return raw >= 0 && raw < a.n_rows ? raw : -1; }  // or -1
+};
+
+// Lines of 16 rows (row of lane l < 16: at) to L2, eight lanes a row.  (A bulk prefetch a
+// row took about 2,000 clocks a tile to issue.)
+__device__ __forceinline__ void prefetch_rows(const uint8_t* rows, int64_t row_stride, int row_bytes, int at)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int n = 0; n < 16; n += 4) {
+        const int r = __shfl_sync(~0u, at, n + (lane >> 3));
+        if (r < 0) continue;
+        const uint8_t* line = rows + r * row_stride;
+        const int c = (lane & 7) * 128;
+        if (c < row_bytes) tc::prefetch_l2(line + c);
+        if ((lane & 7) == 0) tc::prefetch_l2(line + row_bytes - 1);
+    }
+}
+
+// Bounded wait: on a timeout the CTA is marked dead and every later wait returns at once.
+__device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, int* dead, int* error)
+{
+    if (tc::mbar_try(bar, parity)) return;
+    const long long t0 = clock64();
+    while (!tc::mbar_try(bar, parity)) {
+        if (*(volatile int*)dead) return;
+        if (clock64() - t0 > tc::kWaitClocks) {
+            *(volatile int*)dead = 1;
+            atomicExch(error, 1);
+            return;
+        }
+    }
+}
+
+template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b)
+{
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Four e4m3 values as two pairs of fp16, which holds each of them (and NaN).
+__device__ __forceinline__ void widen(uint32_t v, uint32_t& lo, uint32_t& hi)
+{
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(v));
+}
+// 16 e4m3 values as two 16-byte pieces of fp16 at dst + c0 and dst + c1.
+__device__ __forceinline__ void store_wide(const uint4& v, uint32_t dst, int c0, int c1)
+{
+    uint32_t e[8];
+    widen(v.x, e[0], e[1]);
+    widen(v.y, e[2], e[3]);
+    widen(v.z, e[4], e[5]);
+    widen(v.w, e[6], e[7]);
+    tc::st_shared16(dst + c0, e[0], e[1], e[2], e[3]);
+    tc::st_shared16(dst + c1, e[4], e[5], e[6], e[7]);
+}
+
+// With 8-bit rows the products are in fp16; a bf16 query is scaled by a power of two that
+// takes its largest magnitude `top` to [2^13, 2^14), so that what is 2^-28 of it or more
+// stays exact.  The power; zeros and infinities stay as they are.
+__device__ __forceinline__ int power_up(float top)
+{
+    const int ex = (int)(__float_as_uint(top) >> 23);
+    return ex == 0 || ex == 255 ? 0 : min(max(140 - ex, -100), 100);
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+__device__ __forceinline__ float largest_bf16(const uint4& v)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
+    return top;
+}
+__device__ __forceinline__ uint4 bf16_to_half(const uint4& v, float f)
+{
+    auto two = [&](uint32_t w) { return pack2<__half>(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f); };
+    return make_uint4(two(v.x), two(v.y), two(v.z), two(v.w));
+}
+
+// The x-th unit that several workers worked on, found at the first start of a piece inside
+// it: workers first..last have its pieces (false: there is no such unit).  The whole block
+// calls it, at least 256 threads for up to 256 workers.
+__device__ __forceinline__ bool find_cut(const Start* start, int workers, int x, long long& unit, int& first, int& last)
+{
+    __shared__ int counts[8], at;
+    const int t = threadIdx.x;
+    if (t == 0) at = 0;
+    long long mine = -1;
+    bool inside = false, cut = false;
+    if (t > 0 && t < workers) {
+        mine = start[t].unit;
+        inside = mine >= 0 && start[t].tile > 0;
+        cut = inside && !(start[t - 1].unit == mine && start[t - 1].tile > 0);
+    }
+    const unsigned m = __ballot_sync(~0u, cut);
+    if (t < 256 && (t & 31) == 0) counts[t >> 5] = __popc(m);
+    __syncthreads();
+    if (cut) {
+        int before = __popc(m & ((1u << (t & 31)) - 1));
+        for (int w = 0; w < t >> 5; ++w) before += counts[w];
+        if (before == x) at = t;
+    }
+    __syncthreads();
+    if (at == 0) return false;
+    unit = start[at].unit;
+    first = at - 1;
+    last = first + __syncthreads_count(inside && mine == unit);
+    return true;
+}
+
+// The kernels: a pair of SMs for up to 128 heads, and one SM for up to 64.
+cudaError_t launch_pair(const hs_attend_t& a, int sms, cudaStream_t s);
+cudaError_t launch_narrow(const hs_attend_t& a, int sms, cudaStream_t s);
+size_t pair_workspace(int64_t units, int64_t tiles);
+size_t narrow_workspace(int64_t units, int64_t tiles, int heads);
+
+template <typename... Params, typename... Values>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t s, Values... values)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = threads;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, values...);
+}
+
+}  // namespace hs_attn
