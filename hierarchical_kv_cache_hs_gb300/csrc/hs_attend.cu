@@ -38,7 +38,7 @@ constexpr int kOffP = kOffV + 2 * kVBytes;
 constexpr int kOffAux = kOffP + 2 * kPBytes;
 
 struct Aux {
-    uint64_t kfull[kKStages], kfree[kKStages], vfull[2], qhere, lifted, qfull, sfull[2], pready[2], pvdone[2], spare[2];
+    uint64_t kfull[kKStages], kfree[kKStages], vfull[2], qhere, lifted, qfull, sfull[2], sread[2], pready[2], pvdone[2], spare[2];
     uint32_t tmem;
     int dead;
     Piece piece;
@@ -321,7 +321,7 @@ template <typename T> __device__ void multiply_qk(const Args& g, uint32_t sbase,
         for (int t = walk.t0; t < walk.t1; ++t, ++j) {
             const int s = (int)(j & 1);
             // S's buffer has been read
-            if (j >= 2) wait(tc::smem_addr(&x->pready[s]), ((j - 2) >> 1) & 1, &x->dead, error);
+            if (j >= 2) wait(tc::smem_addr(&x->sread[s]), ((j - 2) >> 1) & 1, &x->dead, error);
             wait(tc::smem_addr(&x->kfull[stage]), phase, &x->dead, error);
             __syncwarp();
             tc::fence_after();
@@ -392,6 +392,8 @@ __device__ void soften(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int
     float c = a.scale * 1.4426950408889634f;
     long long j = 0;
     Walk walk(g, x->piece);
+    const uint32_t sread[2] = {tc::map_to_rank(tc::smem_addr(&x->sread[0]), 0),
+                               tc::map_to_rank(tc::smem_addr(&x->sread[1]), 0)};
     const uint32_t pready[2] = {tc::map_to_rank(tc::smem_addr(&x->pready[0]), 0),
                                 tc::map_to_rank(tc::smem_addr(&x->pready[1]), 0)};
     const uint32_t qfull = tc::map_to_rank(tc::smem_addr(&x->qfull), 0);
@@ -407,6 +409,9 @@ __device__ void soften(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int
             uint32_t r[32];
             tc::tmem_ld32(tmem + kColS + 32 * s, r);
             tc::tmem_wait_ld(r);
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_cluster(sread[s]);  // the tile after next may come
             if constexpr (E4M3 && HsType<T>::is_bf16)
                 if (t == walk.t0)
                     c = power_of_two(-x->q_up[pieces & 1][row]) * (a.scale * 1.4426950408889634f);
@@ -487,30 +492,47 @@ __device__ void soften(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int
         Partial* part = reinterpret_cast<Partial*>(ws + kOffPartial) + 2 * pair + (walk.t0 == 0 ? 1 : 0);
         const bool some = sum > 0.f || sum != sum;
         const float inv = some ? 1.f / sum : 0.f;
-        T* out = static_cast<T*>(a.out) + walk.b * a.out_stride[0] + walk.p * a.out_stride[1] +
-                 (int64_t)head * a.out_stride[2] + 256 * half;
+        if (whole) {
+            // Through the buffers of P, so that eight lanes write 128 bytes of a head together: 64 channels
+            // of each half at a time, [half][head][128 B].
+            T* out = static_cast<T*>(a.out) + walk.b * a.out_stride[0] + walk.p * a.out_stride[1];
+            const uint32_t mine = sbase + kOffP + threadIdx.x * 128;
 #pragma unroll 1
-        for (int n = 0; n < 256; n += 32) {
-            uint32_t r[32];
-            __syncwarp();
-            tc::tmem_ld32(tmem + kColO + n, r);
-            tc::tmem_wait_ld(r);
-            if (head >= a.heads) {
-                // a lane without a head has nothing to write
-            } else if (whole) {
+            for (int n = 0; n < 256; n += 64) {
+                uint32_t r[32];
 #pragma unroll
-                for (int i = 0; i < 32; i += 8) {
-                    uint4 e;
-                    auto f = [&](int k) { return some ? __uint_as_float(r[i + k]) * inv : 0.f; };
-                    e.x = pack2<T>(f(0), f(1));
-                    e.y = pack2<T>(f(2), f(3));
-                    e.z = pack2<T>(f(4), f(5));
-                    e.w = pack2<T>(f(6), f(7));
-                    *reinterpret_cast<uint4*>(out + n + i) = e;
+                for (int q = 0; q < 2; ++q) {
+                    __syncwarp();
+                    tc::tmem_ld32(tmem + kColO + n + 32 * q, r);
+                    tc::tmem_wait_ld(r);
+                    auto f = [&](int k) { return some ? __uint_as_float(r[k]) * inv : 0.f; };
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        tc::st_shared16(mine + (((4 * q + i) ^ (row & 7)) << 4), pack2<T>(f(8 * i), f(8 * i + 1)),
+                                        pack2<T>(f(8 * i + 2), f(8 * i + 3)), pack2<T>(f(8 * i + 4), f(8 * i + 5)),
+                                        pack2<T>(f(8 * i + 6), f(8 * i + 7)));
                 }
-            } else {
+                asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll
-                for (int i = 0; i < 32; ++i) part->o[rank][n + i][threadIdx.x] = __uint_as_float(r[i]);
+                for (int i = 0; i < 8; ++i) {
+                    const int at = 16 * i + (threadIdx.x >> 3), ch = threadIdx.x & 7;  // of 128 rows of the buffer
+                    const int h = walk.hb * 128 + (int)rank * 64 + (at & 63);
+                    const uint4 v = tc::ld_shared16(sbase + kOffP + at * 128 + ((ch ^ (at & 7)) << 4));
+                    if (h < a.heads)
+                        *reinterpret_cast<uint4*>(out + (int64_t)h * a.out_stride[2] + 256 * (at >> 6) + n + 8 * ch) = v;
+                }
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+            }
+        } else {
+#pragma unroll 1
+            for (int n = 0; n < 256; n += 32) {
+                uint32_t r[32];
+                __syncwarp();
+                tc::tmem_ld32(tmem + kColO + n, r);
+                tc::tmem_wait_ld(r);
+                if (head < a.heads)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) part->o[rank][n + i][threadIdx.x] = __uint_as_float(r[i]);
             }
         }
         if (head < a.heads) {
@@ -535,7 +557,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_atte
     Aux* x = reinterpret_cast<Aux*>(base + kOffAux);
     const hs_attend_t& a = g.a;
     const uint32_t rank = tc::cluster_rank();
-    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int pair = blockIdx.x >> 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     int* error = reinterpret_cast<int*>(ws);
@@ -543,14 +565,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_atte
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may queue up behind this grid
     if (warp == 0) tc::tmem_alloc<2>(tc::smem_addr(&x->tmem), 512);
     if (warp == 12) {
-        const Piece p = find_piece(g, pair, pairs);
+        const Piece p = find_piece(g, pair);
         if (lane == 0) {
             x->piece = p;
             x->dead = 0;
-            if (rank == 0) reinterpret_cast<Start*>(ws + kOffStart)[pair] = {p.count > 0 ? p.unit : -1, p.tile, 0};
+            if (rank == 0) reinterpret_cast<Start*>(ws + kOffStart)[pair] = {p.count > 0 ? p.unit : -1, p.tile};
             for (int i = 0; i < 2; ++i) {
                 tc::mbar_init(tc::smem_addr(&x->vfull[i]), 4);
                 tc::mbar_init(tc::smem_addr(&x->sfull[i]), 1);
+                tc::mbar_init(tc::smem_addr(&x->sread[i]), 8);
                 tc::mbar_init(tc::smem_addr(&x->pready[i]), 8);
                 tc::mbar_init(tc::smem_addr(&x->pvdone[i]), 1);
                 tc::mbar_init(tc::smem_addr(&x->spare[i]), 1);
@@ -586,7 +609,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_atte
     __syncwarp();
     tc::fence_before();
     __syncthreads();
-    tc::cluster_sync();
+    tc::cluster_sync_relaxed();  // no CTA leaves while the other may signal it
     tc::fence_after();
     if (warp == 0) tc::tmem_free<2>(x->tmem, 512);
 }
@@ -603,15 +626,14 @@ __global__ void __launch_bounds__(512) hs_attend_join_kernel(const __grid_consta
     const hs_attend_t& a = g.a;
     const uint8_t* ws = static_cast<const uint8_t*>(a.workspace);
     const Partial* parts = reinterpret_cast<const Partial*>(ws + kOffPartial);
-    long long unit;
-    int first, last;
+    int unit, first, last;
     if (!find_cut(reinterpret_cast<const Start*>(ws + kOffStart), pairs, blockIdx.x, unit, first, last)) return;
     const int t = threadIdx.x;
     const int rank = blockIdx.y, c0 = COLS * blockIdx.z;
     const int lane = t & 127, group = t >> 7, row = lane & 63, half = lane >> 6;
-    const int upr = a.positions * g.head_blocks;
-    const long long b = unit / upr;
-    const int rem = (int)(unit - b * upr), p = rem / g.head_blocks, hb = rem - p * g.head_blocks;
+    const int pos = unit / g.head_blocks, hb = unit - pos * g.head_blocks;
+    const long long b = pos / a.positions;
+    const int p = pos - (int)b * a.positions;
     const int head = hb * 128 + rank * 64 + row;
     if (hb * 128 + rank * 64 >= a.heads) return;
     const bool live = head < a.heads;
@@ -663,18 +685,18 @@ __global__ void __launch_bounds__(512) hs_attend_join_kernel(const __grid_consta
         a.lse[(b * a.positions + p) * a.heads + head] = some ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
-template <typename T, bool E4M3> cudaError_t launch(const Args& g, int pairs, cudaStream_t s)
+template <typename T, bool E4M3> cudaError_t launch(const Args& g, cudaStream_t s)
 {
     cudaError_t e = cudaFuncSetAttribute(hs_attend_kernel<T, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    hs_attend_kernel<T, E4M3><<<2 * pairs, kThreads, kSmem, s>>>(g);
+    hs_attend_kernel<T, E4M3><<<2 * g.workers, kThreads, kSmem, s>>>(g);
     e = cudaGetLastError();
-    if (e != cudaSuccess || !g.flat || pairs <= 1) return e;
+    if (e != cudaSuccess || !g.flat || g.workers <= 1) return e;
     // At most this many units are cut; few units take more blocks each, by narrower columns.
-    const int cut = (int)(g.units < pairs - 1 ? g.units : pairs - 1);
+    const int cut = g.units < g.workers - 1 ? g.units : g.workers - 1;
     const int cols = cut * (g.a.heads > 64 ? 2 : 1) <= 8 ? 4 : 16;
     return launch_after(cols == 4 ? hs_attend_join_kernel<T, 4> : hs_attend_join_kernel<T, 16>,
-                        dim3(cut, g.a.heads > 64 ? 2 : 1, 256 / cols), 512, s, g, pairs);
+                        dim3(cut, g.a.heads > 64 ? 2 : 1, 256 / cols), 512, s, g, g.workers);
 }
 
 }  // namespace
@@ -689,20 +711,13 @@ cudaError_t launch_pair(const hs_attend_t& a, int sms, cudaStream_t s)
     Args g;
     g.a = a;
     g.head_blocks = (a.heads + 127) / 128;
-    g.units = (int64_t)a.batch * a.positions * g.head_blocks;
-    const int64_t rows = a.slots ? a.entries : a.n_rows;
-    const int64_t tiles = rows <= kTile ? 1 : (rows + kTile - 1) / kTile;
-    int64_t pairs = sms / 2 < kMaxPairs ? sms / 2 : kMaxPairs;
-    pairs = g.units * tiles < pairs ? g.units * tiles : pairs < 1 ? 1 : pairs;
-    // Whole units to a pair, or equal pieces: pieces also write and join up to two partial
-    // results a pair, about 10 us, or 10 tiles' time.
-    const int64_t whole = (g.units + pairs - 1) / pairs * tiles, pieces = (g.units * tiles + pairs - 1) / pairs + 10;
-    g.flat = whole > pieces;
-    if (!g.flat && pairs > g.units) pairs = g.units;
+    g.units = a.batch * a.positions * g.head_blocks;
+    // Pieces also write and join up to two partial results a pair: about 10 us, 10 tiles' time.
+    g.cut(sms / 2 < kMaxPairs ? (sms > 1 ? sms / 2 : 1) : kMaxPairs, a.slots ? a.entries : a.n_rows, 10);
     const bool e4m3 = a.row_format == HS_ROWS_E4M3;
     if (a.dtype == HS_TYPE_BF16)
-        return e4m3 ? launch<__nv_bfloat16, true>(g, (int)pairs, s) : launch<__nv_bfloat16, false>(g, (int)pairs, s);
-    return e4m3 ? launch<__half, true>(g, (int)pairs, s) : launch<__half, false>(g, (int)pairs, s);
+        return e4m3 ? launch<__nv_bfloat16, true>(g, s) : launch<__nv_bfloat16, false>(g, s);
+    return e4m3 ? launch<__half, true>(g, s) : launch<__half, false>(g, s);
 }
 
 }  // namespace hs_attn
@@ -711,8 +726,10 @@ size_t hs_attend_workspace_bytes(int batch, int positions, int heads, int64_t ro
 {
     const int64_t tiles = rows <= hs_attn::kTile ? 1 : (rows + hs_attn::kTile - 1) / hs_attn::kTile;
     const int64_t units = (int64_t)batch * positions;
-    return heads <= 64 ? hs_attn::narrow_workspace(units, tiles, heads)
-                       : hs_attn::pair_workspace(units * ((heads + 127) / 128), tiles);
+    const size_t pair = hs_attn::pair_workspace(units * ((heads + 127) / 128), tiles);
+    if (heads > hs_attn::kNarrowHeads) return pair;
+    const size_t narrow = hs_attn::narrow_workspace(units, tiles, heads);  // either, by the rows' form
+    return narrow > pair ? narrow : pair;
 }
 
 cudaError_t hs_launch_attend(const hs_attend_t& a, cudaStream_t s)
@@ -721,5 +738,6 @@ cudaError_t hs_launch_attend(const hs_attend_t& a, cudaStream_t s)
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    return a.heads <= 64 ? hs_attn::launch_narrow(a, sms, s) : hs_attn::launch_pair(a, sms, s);
+    return a.row_format == HS_ROWS_E4M3 && a.heads <= hs_attn::kNarrowHeads ? hs_attn::launch_narrow(a, sms, s)
+                                                                            : hs_attn::launch_pair(a, sms, s);
 }

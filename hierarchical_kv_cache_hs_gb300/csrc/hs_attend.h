@@ -18,16 +18,34 @@ struct Args {
     hs_attend_t a;
     int head_blocks;
     int flat;
-    int64_t units;
+    int units;         // at most HS_MAX_BATCH x HS_MAX_POSITIONS x HS_MAX_HEADS / 128, below 2^31
+    int unit_tiles;    // tiles of a unit; with lengths, the most that one has
+    int workers;
+    int64_t share;     // slots: tiles a worker, and how many workers have one more
+    int extra;
+    int unit_share, unit_extra;  // units a worker, likewise
+
+    // Fill in the cut: whole units, or pieces where those are `join` tiles' time shorter.
+    void cut(int most, int64_t rows, int join)
+    {
+        unit_tiles = rows <= kTile ? 1 : (int)((rows + kTile - 1) / kTile);
+        const int64_t total = (int64_t)units * unit_tiles;
+        workers = (int)(total < most ? total : most);
+        flat = (int64_t)((units + workers - 1) / workers) * unit_tiles > (total + workers - 1) / workers + join;
+        if (!flat && workers > units) workers = units;
+        share = total / workers;
+        extra = (int)(total % workers);
+        unit_share = units / workers;
+        unit_extra = units % workers;
+    }
 };
 
 struct Start {  // where a worker's piece of the line begins (unit -1: it has none)
-    long long unit;
-    int tile, pad;
+    int unit, tile;
 };
 struct Piece {
-    long long unit, count;  // count: its tiles
-    int tile;
+    long long count;  // its tiles
+    int unit, tile;
 };
 
 __device__ __forceinline__ int request_tiles(const hs_attend_t& a, long long b)
@@ -40,48 +58,38 @@ __device__ __forceinline__ int request_tiles(const hs_attend_t& a, long long b)
     return n <= kTile ? 1 : (int)((n + kTile - 1) / kTile);
 }
 
-// Worker i's piece of n workers' (one warp; every lane gets it).
-__device__ __forceinline__ Piece find_piece(const Args& g, int i, int workers)
+// Worker i's piece (one warp; every lane gets it).
+__device__ __forceinline__ Piece find_piece(const Args& g, int i)
 {
     const hs_attend_t& a = g.a;
     const int lane = threadIdx.x & 31;
     const int upr = a.positions * g.head_blocks;  // units a request
     Piece p;
-    if (a.slots) {
-        const int tiles = request_tiles(a, 0);
-        const long long total = g.units * tiles, n = total < workers ? total : workers;
-        long long lo, hi;
-        if (i >= n) {
-            lo = hi = 0;
-        } else if (g.flat) {
-            lo = total * i / n;
-            hi = total * (i + 1) / n;
-        } else {
-            lo = g.units * i / workers * tiles;
-            hi = g.units * (i + 1) / workers * tiles;
+    if (!g.flat) {
+        p.unit = g.unit_share * i + min(i, g.unit_extra);
+        p.tile = 0;
+        const int n = g.unit_share + (i < g.unit_extra);
+        p.count = (long long)n * g.unit_tiles;
+        if (!a.slots) {
+            const int end = p.unit + n;
+            p.count = 0;
+            for (int b = p.unit / upr + lane; b < a.batch && b * upr < end; b += 32)
+                p.count += (long long)(min(b * upr + upr, end) - max(b * upr, p.unit)) * request_tiles(a, b);
+            for (int o = 16; o; o >>= 1) p.count += __shfl_xor_sync(~0u, p.count, o);
         }
-        p.unit = lo / tiles;
-        p.tile = (int)(lo - p.unit * tiles);
-        p.count = hi - lo;
         return p;
     }
-    if (!g.flat) {
-        const long long u0 = g.units * i / workers, u1 = g.units * (i + 1) / workers;
-        long long count = 0;
-        for (int b = lane; b < a.batch; b += 32) {
-            const long long first = (long long)b * upr, lo = first > u0 ? first : u0, hi = first + upr < u1 ? first + upr : u1;
-            if (hi > lo) count += (hi - lo) * request_tiles(a, b);
-        }
-        for (int o = 16; o; o >>= 1) count += __shfl_xor_sync(~0u, count, o);
-        p.unit = u0;
-        p.tile = 0;
-        p.count = count;
+    if (a.slots) {
+        const long long lo = g.share * i + min(i, g.extra);
+        p.count = g.share + (i < g.extra);
+        p.unit = lo < 0x7fffffff ? (int)((unsigned)lo / (unsigned)g.unit_tiles) : (int)(lo / g.unit_tiles);
+        p.tile = (int)(lo - (long long)p.unit * g.unit_tiles);
         return p;
     }
     long long total = 0;
     for (int b = lane; b < a.batch; b += 32) total += (long long)request_tiles(a, b) * upr;
     for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
-    const long long n = total < workers ? total : workers;
+    const long long n = total < g.workers ? total : g.workers;
     const long long lo = i < n ? total * i / n : 0, hi = i < n ? total * (i + 1) / n : 0;
     p.unit = 0;
     p.tile = 0;
@@ -100,7 +108,7 @@ __device__ __forceinline__ Piece find_piece(const Args& g, int i, int workers)
         const unsigned who = __ballot_sync(~0u, here);
         if (who) {
             const int src = __ffs(who) - 1;
-            const long long u = here ? (long long)b * upr + (lo - at) / tiles : 0;
+            const int u = here ? b * upr + (int)((lo - at) / tiles) : 0;
             const int t = here ? (int)((lo - at) % tiles) : 0;
             p.unit = __shfl_sync(~0u, u, src);
             p.tile = __shfl_sync(~0u, t, src);
@@ -114,24 +122,23 @@ __device__ __forceinline__ Piece find_piece(const Args& g, int i, int workers)
 // The units, or parts of units, of a piece, in order.
 struct Walk {
     const Args& g;
-    long long unit, left;
-    int tile;
+    long long left;
+    int unit, tile;
     // the current one: tiles [t0, t1) of `tiles`
     long long b;
     int p, hb, t0, t1, tiles;
     long long rows;  // entries, or allowed rows
 
-    __device__ Walk(const Args& args, const Piece& x) : g(args), unit(x.unit), left(x.count), tile(x.tile) {}
+    __device__ Walk(const Args& args, const Piece& x) : g(args), left(x.count), unit(x.unit), tile(x.tile) {}
 
     __device__ bool next()
     {
         if (left <= 0) return false;
         const hs_attend_t& a = g.a;
-        const int upr = a.positions * g.head_blocks;
-        b = unit / upr;
-        const int rem = (int)(unit - b * upr);
-        p = rem / g.head_blocks;
-        hb = rem - p * g.head_blocks;
+        const int pos = unit / g.head_blocks, request = pos / a.positions;
+        b = request;
+        p = pos - request * a.positions;
+        hb = unit - pos * g.head_blocks;
         tiles = request_tiles(a, b);
         rows = a.entries;
         if (!a.slots) {
@@ -257,12 +264,12 @@ __device__ __forceinline__ uint4 bf16_to_half(const uint4& v, float f)
 // The x-th unit that several workers worked on, found at the first start of a piece inside
 // it: workers first..last have its pieces (false: there is no such unit).  The whole block
 // calls it, at least 256 threads for up to 256 workers.
-__device__ __forceinline__ bool find_cut(const Start* start, int workers, int x, long long& unit, int& first, int& last)
+__device__ __forceinline__ bool find_cut(const Start* start, int workers, int x, int& unit, int& first, int& last)
 {
     __shared__ int counts[8], at;
     const int t = threadIdx.x;
     if (t == 0) at = 0;
-    long long mine = -1;
+    int mine = -1;
     bool inside = false, cut = false;
     if (t > 0 && t < workers) {
         mine = start[t].unit;
@@ -285,7 +292,11 @@ __device__ __forceinline__ bool find_cut(const Start* start, int workers, int x,
     return true;
 }
 
-// The kernels: a pair of SMs for up to 128 heads, and one SM for up to 64.
+// The kernels: a pair of SMs for up to 128 heads; and one SM for up to 32 heads and 8-bit
+// rows, whose conversion, done twice by a pair, bounds them there (256 requests x 2048
+// rows: 108 against 200 us with 16 heads, 134 against 202 with 32, but 262 against 207
+// with 48; with 16-bit rows the pair is faster at any number: 154 against 140 us with 16).
+constexpr int kNarrowHeads = 32;
 cudaError_t launch_pair(const hs_attend_t& a, int sms, cudaStream_t s);
 cudaError_t launch_narrow(const hs_attend_t& a, int sms, cudaStream_t s);
 size_t pair_workspace(int64_t units, int64_t tiles);

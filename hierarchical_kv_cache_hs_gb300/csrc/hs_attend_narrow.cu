@@ -1,10 +1,11 @@
-// hs_latent_attend for up to 64 heads: one SM takes all heads of a request and position.
+// hs_latent_attend over 8-bit rows for up to 32 heads: one SM takes all heads of a request
+// and position.
 //
 // The products are turned around, so that rows and channels, not heads, fill the tensor
 // core's 128 (or 64) rows: S^T = K Q^T for a tile of 64 rows (M = 64, N = heads), and
 // O^T += V^T P^T (M = 128 channels four times, N = heads), where V^T is the key tile read
-// along its channels.  A row is brought to shared memory once and read twice; with so few
-// heads the kernel is bound by bringing the rows.
+// along its channels.  A row is widened to fp16 and brought to shared memory once, and
+// read twice; with so few heads the kernel is bound by that.
 //
 // Warps: 0-3 softmax, 4-11 bring the rows (four a stage) and the queries, 12 and 13 issue
 // the products.  The running reference of a head moves only when a maximum exceeds it by
@@ -21,13 +22,12 @@ constexpr int kBlock = 64 * 128;
 
 // NH: heads, padded to the products' N.
 template <int NH> struct Layout {
-    static constexpr int P = NH <= 32 ? 2 : 1;  // buffers of weights
     static constexpr int off_q = 2 * kStageBytes;              // 9 blocks, [NH][128 B]
-    static constexpr int off_p = off_q + 9 * NH * 128;         // [NH][128 B] each
-    static constexpr int off_aux = off_p + P * NH * 128;
+    static constexpr int off_p = off_q + 9 * NH * 128;         // two buffers, [NH][128 B] each
+    static constexpr int off_aux = off_p + 2 * NH * 128;
     // Tensor memory: sums of the four groups of 128 channels, then two buffers of scores.
     static constexpr uint32_t col_s = 4 * NH;
-    static constexpr uint32_t cols = NH == 64 ? 512 : NH == 32 ? 256 : 128;
+    static constexpr uint32_t cols = NH == 32 ? 256 : 128;
 };
 
 template <int NH> struct Aux {
@@ -38,11 +38,12 @@ template <int NH> struct Aux {
     uint16_t valid[4][4];          // by tile, four deep; one bit a row
     alignas(8) float scale[4][kTile];
     int8_t q_up[2][NH];            // power of two on a bf16 query held in fp16, by the parity of the piece
-    float red[4][NH];              // by warp: maxima, sums, and factors on O
+    float top[2][4][NH];           // maxima by warp, by the parity of the tile
+    float red[4][NH];              // by warp: sums, and factors on O
     float inv[NH];                 // of the sums at a piece's end
 };
 template <int NH> constexpr int smem_bytes() { return Layout<NH>::off_aux + (int)sizeof(Aux<NH>); }
-static_assert(smem_bytes<64>() <= 232448, "shared memory");
+static_assert(smem_bytes<32>() <= 232448, "shared memory");
 
 template <int NH> struct Partial {
     float o[4][NH][128];  // [channels / 128][head][channel]
@@ -52,13 +53,12 @@ constexpr size_t kOffStart = 256;
 constexpr size_t kOffPartial = kOffStart + sizeof(Start) * kMaxCtas;
 
 // Rows of a tile, four warps of 16 rows each; and the queries, eight warps a head at a time.
-template <typename T, bool E4M3, int NH> __device__ void bring(const Args& g, uint32_t sbase, Aux<NH>* x, int* error)
+template <typename T, int NH> __device__ void bring(const Args& g, uint32_t sbase, Aux<NH>* x, int* error)
 {
     const hs_attend_t& a = g.a;
     const int lane = threadIdx.x & 31, wg = (threadIdx.x >> 5) - 4;
     const int stage = wg >> 2, w = wg & 3;
     const uint32_t k_smem = sbase + stage * kStageBytes, full = tc::smem_addr(&x->full[stage]);
-    const int row_bytes = E4M3 ? HS_ROW8_BYTES : 2 * HS_ROW_DIM;
     const int mine = 16 * w + (lane & 15);
     long long j = 0;
     Walk walk(g, x->piece);
@@ -71,7 +71,7 @@ template <typename T, bool E4M3, int NH> __device__ void bring(const Args& g, ui
         // before it is used.
         int next = lookup.row(lookup.raw(t, mine)), after = lookup.row(lookup.raw(t + 2, mine));
         int ahead = lookup.raw(t + 4, mine);
-        prefetch_rows(rows, a.row_stride, row_bytes, after);
+        prefetch_rows(rows, a.row_stride, HS_ROW8_BYTES, after);
         // Q, once the last piece's products with keys are done.
         if (pieces) wait(tc::smem_addr(&x->qfree), (pieces - 1) & 1, &x->dead, error);
         const T* q = static_cast<const T*>(a.q) + walk.b * a.q_stride[0] + walk.p * a.q_stride[1];
@@ -85,9 +85,9 @@ template <typename T, bool E4M3, int NH> __device__ void bring(const Args& g, ui
             for (int i = 0; i < 3; ++i) {
                 const int c = 32 * i + lane;  // of 72 pieces
                 v[i] = ok && c < 72 ? src[c] : make_uint4(0, 0, 0, 0);
-                if constexpr (E4M3 && HsType<T>::is_bf16) top = fmaxf(top, largest_bf16(v[i]));
+                if constexpr (HsType<T>::is_bf16) top = fmaxf(top, largest_bf16(v[i]));
             }
-            if constexpr (E4M3 && HsType<T>::is_bf16) {
+            if constexpr (HsType<T>::is_bf16) {
                 for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
                 const int up = power_up(top);
                 if (lane == 0) x->q_up[pieces & 1][h] = (int8_t)up;
@@ -108,48 +108,32 @@ template <typename T, bool E4M3, int NH> __device__ void bring(const Args& g, ui
             const int row = next;
             next = after;
             after = lookup.row(ahead);
-            if (t + 4 < walk.t1) prefetch_rows(rows, a.row_stride, row_bytes, after);
+            if (t + 4 < walk.t1) prefetch_rows(rows, a.row_stride, HS_ROW8_BYTES, after);
             ahead = lookup.raw(t + 6, mine);
             const int m = (int)(jt & 3);
             const unsigned ok_bits = __ballot_sync(~0u, row >= 0);
-            if constexpr (!E4M3) {
-                if (jt >= 2) wait(tc::smem_addr(&x->pvdone[stage]), ((jt - 2) >> 1) & 1, &x->dead, error);
+            const float sc = row >= 0 ? *reinterpret_cast<const float*>(rows + row * a.row_stride + HS_ROW8_SCALE) : 1.f;
+            const int ch = lane & 3;  // 16 channels of a block
+            uint4 v[2][9];
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const int tok = n * 4 + (lane >> 3), ch = lane & 7;  // 16-byte piece of a block
-                    const int r = __shfl_sync(~0u, row, tok);
-                    // absent rows are zeros (nothing is read; q is only an address that exists)
-                    const uint8_t* src = (r < 0 ? static_cast<const uint8_t*>(a.q) : rows + r * a.row_stride) + ch * 16;
-                    const uint32_t dst = k_smem + (16 * w + tok) * 128 + ((ch ^ (tok & 7)) << 4);
+            for (int n = 0; n < 2; ++n) {
+                const int r = __shfl_sync(~0u, row, n * 8 + (lane >> 2));
 #pragma unroll
-                    for (int c = 0; c < 9; ++c) tc::cp_async16(dst + c * kBlock, src + c * 128, r >= 0);
-                }
-            } else {
-                const float sc = row >= 0 ? *reinterpret_cast<const float*>(rows + row * a.row_stride + HS_ROW8_SCALE) : 1.f;
-                const int ch = lane & 3;  // 16 channels of a block
-                uint4 v[2][9];
+                for (int c = 0; c < 9; ++c)
+                    v[n][c] = r >= 0 ? *reinterpret_cast<const uint4*>(rows + r * a.row_stride + c * 64 + ch * 16)
+                                     : make_uint4(0, 0, 0, 0);
+            }
+            if (jt >= 2) wait(tc::smem_addr(&x->pvdone[stage]), ((jt - 2) >> 1) & 1, &x->dead, error);
+            if (lane < 16) x->scale[m][mine] = sc;
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const int r = __shfl_sync(~0u, row, n * 8 + (lane >> 2));
+            for (int n = 0; n < 2; ++n) {
+                const int tok = n * 8 + (lane >> 2), r0 = tok & 7;
+                const uint32_t dst = k_smem + (16 * w + tok) * 128;
 #pragma unroll
-                    for (int c = 0; c < 9; ++c)
-                        v[n][c] = r >= 0 ? *reinterpret_cast<const uint4*>(rows + r * a.row_stride + c * 64 + ch * 16)
-                                         : make_uint4(0, 0, 0, 0);
-                }
-                if (jt >= 2) wait(tc::smem_addr(&x->pvdone[stage]), ((jt - 2) >> 1) & 1, &x->dead, error);
-                if (lane < 16) x->scale[m][mine] = sc;
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const int tok = n * 8 + (lane >> 2), r0 = tok & 7;
-                    const uint32_t dst = k_smem + (16 * w + tok) * 128;
-#pragma unroll
-                    for (int c = 0; c < 9; ++c)
-                        store_wide(v[n][c], dst + c * kBlock, ((2 * ch) ^ r0) << 4, ((2 * ch + 1) ^ r0) << 4);
-                }
+                for (int c = 0; c < 9; ++c)
+                    store_wide(v[n][c], dst + c * kBlock, ((2 * ch) ^ r0) << 4, ((2 * ch + 1) ^ r0) << 4);
             }
             if (lane == 0) x->valid[m][w] = (uint16_t)ok_bits;
-            tc::cp_async_commit();
-            tc::cp_async_wait<0>();
             tc::fence_async_shared();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(full);
@@ -167,9 +151,9 @@ template <int NH> __device__ void drain(Aux<NH>* x, int which)
 }
 
 // S^T = K Q^T, issued by one warp.
-template <typename T, int NH> __device__ void multiply_qk(const Args& g, uint32_t sbase, Aux<NH>* x, int* error)
+template <int NH> __device__ void multiply_qk(const Args& g, uint32_t sbase, Aux<NH>* x, int* error)
 {
-    constexpr uint32_t id = tc::inst_desc(HsType<T>::is_bf16, 64, NH, false, false);
+    constexpr uint32_t id = tc::inst_desc(false, 64, NH, false, false);
     const uint32_t tmem = __shfl_sync(~0u, x->tmem, 0) + Layout<NH>::col_s;
     const uint64_t k_base = tc::smem_desc(sbase, 16, 1024), q_desc = tc::smem_desc(sbase + Layout<NH>::off_q, 16, 1024);
     long long j = 0;
@@ -202,9 +186,9 @@ template <typename T, int NH> __device__ void multiply_qk(const Args& g, uint32_
 }
 
 // O^T += V^T P^T, issued by another.
-template <typename T, int NH> __device__ void multiply_pv(const Args& g, uint32_t sbase, Aux<NH>* x, int* error)
+template <int NH> __device__ void multiply_pv(const Args& g, uint32_t sbase, Aux<NH>* x, int* error)
 {
-    constexpr uint32_t id = tc::inst_desc(HsType<T>::is_bf16, 128, NH, true, false);
+    constexpr uint32_t id = tc::inst_desc(false, 128, NH, true, false);
     const uint32_t tmem = __shfl_sync(~0u, x->tmem, 0);
     const uint64_t v_base = tc::smem_desc(sbase, kBlock, 1024), p_base = tc::smem_desc(sbase + Layout<NH>::off_p, 16, 1024);
     long long j = 0;
@@ -216,7 +200,7 @@ template <typename T, int NH> __device__ void multiply_pv(const Args& g, uint32_
             __syncwarp();
             tc::fence_after();
             const uint64_t v_desc = v_base + s * (kStageBytes >> 4);
-            const uint64_t p_desc = p_base + (Layout<NH>::P == 2 ? s * (NH * 128 >> 4) : 0);
+            const uint64_t p_desc = p_base + s * (NH * 128 >> 4);
             const bool first = t == walk.t0;
             if (tc::elect_one()) {
 #pragma unroll
@@ -241,22 +225,12 @@ template <int NH> __device__ __forceinline__ void load_scores(uint32_t addr, uin
         asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
                      : "r"(addr));
-    else if constexpr (NH == 32)
+    else
         asm volatile(
             "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
             "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
             : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
               "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-            : "r"(addr));
-    else
-        asm volatile(
-            "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-            "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-            "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-            : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-              "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
-              "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
-              "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
             : "r"(addr));
     // the registers pass through the wait, so that nothing reads them before
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
@@ -280,10 +254,9 @@ template <int N> __device__ __forceinline__ void tmem_store(uint32_t addr, const
         tc::tmem_st32(addr, r);
 }
 
-template <typename T, bool E4M3, int NH> __device__ void soften(const Args& g, uint32_t sbase, Aux<NH>* x, uint8_t* ws, int* error)
+template <typename T, int NH> __device__ void soften(const Args& g, uint32_t sbase, Aux<NH>* x, uint8_t* ws, int* error)
 {
-    using Operand = std::conditional_t<E4M3, __half, T>;
-    constexpr int NG = NH / 8, N = NH < 32 ? NH : 32;
+    constexpr int NG = NH / 8, N = NH;
     const hs_attend_t& a = g.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r0 = lane >> 2, c0 = 2 * (lane & 3);
@@ -300,7 +273,7 @@ template <typename T, bool E4M3, int NH> __device__ void soften(const Args& g, u
             const int s = (int)(j & 1), m = (int)(j & 3);
             wait(tc::smem_addr(&x->sfull[s]), (j >> 1) & 1, &x->dead, error);
             tc::fence_after();
-            if constexpr (E4M3 && HsType<T>::is_bf16)
+            if constexpr (HsType<T>::is_bf16)
                 if (t == walk.t0)
 #pragma unroll
                     for (int i = 0; i < 2 * NG; ++i)
@@ -309,11 +282,8 @@ template <typename T, bool E4M3, int NH> __device__ void soften(const Args& g, u
             load_scores<NH>(tmem + Layout<NH>::col_s + NH * s, r);
             const unsigned valid = x->valid[m][warp];
             const bool ok0 = valid >> r0 & 1, ok1 = valid >> (r0 + 8) & 1;
-            float w0 = 1.f, w1 = 1.f, lw0 = 0.f, lw1 = 0.f;
-            if constexpr (E4M3) {
-                w0 = x->scale[m][16 * warp + r0], w1 = x->scale[m][16 * warp + r0 + 8];
-                lw0 = log2f(fabsf(w0)), lw1 = log2f(fabsf(w1));
-            }
+            const float w0 = x->scale[m][16 * warp + r0], w1 = x->scale[m][16 * warp + r0 + 8];
+            const float lw0 = tc::log2_approx(fabsf(w0)), lw1 = tc::log2_approx(fabsf(w1));  // only move the reference
             float v[NH / 2], top[2 * NG];
 #pragma unroll
             for (int i = 0; i < 2 * NG; ++i) {  // column i: registers 4 (i / 2) + i % 2 and + 2
@@ -328,19 +298,18 @@ template <typename T, bool E4M3, int NH> __device__ void soften(const Args& g, u
                 for (int i = 0; i < 2 * NG; ++i) top[i] = fmaxf(top[i], __shfl_xor_sync(~0u, top[i], o));
             if (lane < 4)
 #pragma unroll
-                for (int i = 0; i < NG; ++i) *reinterpret_cast<float2*>(&x->red[warp][8 * i + c0]) = make_float2(top[2 * i], top[2 * i + 1]);
+                for (int i = 0; i < NG; ++i) *reinterpret_cast<float2*>(&x->top[s][warp][8 * i + c0]) = make_float2(top[2 * i], top[2 * i + 1]);
             asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
-                float2 q = *reinterpret_cast<float2*>(&x->red[0][8 * i + c0]);
+                float2 q = *reinterpret_cast<float2*>(&x->top[s][0][8 * i + c0]);
 #pragma unroll
                 for (int k = 1; k < 4; ++k) {
-                    const float2 n = *reinterpret_cast<float2*>(&x->red[k][8 * i + c0]);
+                    const float2 n = *reinterpret_cast<float2*>(&x->top[s][k][8 * i + c0]);
                     q.x = fmaxf(q.x, n.x), q.y = fmaxf(q.y, n.y);
                 }
                 top[2 * i] = q.x, top[2 * i + 1] = q.y;
             }
-            asm volatile("bar.sync 1, 128;" ::: "memory");  // red is free again
             // every warp sees the same maxima, so they agree on what follows
             float keep[2 * NG];
             bool scale_o = false;
@@ -374,23 +343,20 @@ template <typename T, bool E4M3, int NH> __device__ void soften(const Args& g, u
                     uint32_t o[N];
                     tmem_load(tmem + n, o);
 #pragma unroll
-                    for (int i = 0; i < N; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * x->red[warp][(n & (NH - 1)) + i]);
+                    for (int i = 0; i < N; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * x->red[warp][i]);
                     tmem_store(tmem + n, o);
                 }
                 tc::tmem_wait_st();
                 __syncwarp();
-            } else if (Layout<NH>::P == 1 && j >= 1) {
-                wait(tc::smem_addr(&x->pvdone[1 - s]), ((j - 1) >> 1) & 1, &x->dead, error);
             }
             // P^T: row (head), 64 of the tile's rows along it
-            const uint32_t p_smem = sbase + Layout<NH>::off_p + (Layout<NH>::P == 2 ? s * NH * 128 : 0);
+            const uint32_t p_smem = sbase + Layout<NH>::off_p + s * NH * 128;
 #pragma unroll
             for (int i = 0; i < 2 * NG; ++i) {
                 const int k = 4 * (i >> 1) + (i & 1), head = 8 * (i >> 1) + c0 + (i & 1);
-                float p0 = tc::exp2_approx(v[k] - ref[i]), p1 = tc::exp2_approx(v[k + 2] - ref[i]);
+                const float p0 = tc::exp2_approx(v[k] - ref[i]), p1 = tc::exp2_approx(v[k + 2] - ref[i]);
                 sum[i] += p0 + p1;
-                if constexpr (E4M3) p0 *= w0, p1 *= w1;
-                const uint32_t both = pack2<Operand>(p0, p1);
+                const uint32_t both = pack2<__half>(p0 * w0, p1 * w1);
                 const uint32_t dst = p_smem + head * 128 + 2 * r0;
                 const uint32_t sw = (uint32_t)head & 7;
                 asm volatile("st.shared.b16 [%0], %1;" ::"r"(dst + (((2 * warp) ^ sw) << 4)), "h"((uint16_t)(both & 0xffff)) : "memory");
@@ -433,10 +399,10 @@ template <typename T, bool E4M3, int NH> __device__ void soften(const Args& g, u
             uint32_t o[N];
             __syncwarp();
             tmem_load(tmem + n, o);
-            const int i = n / NH, h0 = n & (NH - 1);
+            const int i = n / NH;
 #pragma unroll
             for (int k = 0; k < N; ++k) {
-                const int head = h0 + k;
+                const int head = k;
                 if (head >= a.heads) continue;
                 if (whole) {
                     const float f = x->inv[head];  // 0: no row counted
@@ -447,14 +413,13 @@ template <typename T, bool E4M3, int NH> __device__ void soften(const Args& g, u
             }
         }
         tc::fence_before();
-        asm volatile("bar.sync 1, 128;" ::: "memory");  // red is free again
+        asm volatile("bar.sync 1, 128;" ::: "memory");  // red and inv are free again
     }
 }
 
-template <typename T, bool E4M3, int NH>
+template <typename T, int NH>
 __global__ void __launch_bounds__(kThreads, 1) hs_attend_narrow_kernel(const __grid_constant__ Args g)
 {
-    using Operand = std::conditional_t<E4M3, __half, T>;
     extern __shared__ __align__(1024) uint8_t base[];  // the swizzled tiles need 1024
     const uint32_t sbase = tc::smem_addr(base);
     Aux<NH>* x = reinterpret_cast<Aux<NH>*>(base + Layout<NH>::off_aux);
@@ -466,11 +431,11 @@ __global__ void __launch_bounds__(kThreads, 1) hs_attend_narrow_kernel(const __g
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may queue up behind this grid
     if (warp == 0) tc::tmem_alloc<1>(tc::smem_addr(&x->tmem), Layout<NH>::cols);
     if (warp == 12) {
-        const Piece p = find_piece(g, blockIdx.x, gridDim.x);
+        const Piece p = find_piece(g, blockIdx.x);
         if (lane == 0) {
             x->piece = p;
             x->dead = 0;
-            reinterpret_cast<Start*>(ws + kOffStart)[blockIdx.x] = {p.count > 0 ? p.unit : -1, p.tile, 0};
+            reinterpret_cast<Start*>(ws + kOffStart)[blockIdx.x] = {p.count > 0 ? p.unit : -1, p.tile};
             for (int i = 0; i < 2; ++i) {
                 tc::mbar_init(tc::smem_addr(&x->full[i]), 4);
                 tc::mbar_init(tc::smem_addr(&x->sfull[i]), 1);
@@ -490,13 +455,13 @@ __global__ void __launch_bounds__(kThreads, 1) hs_attend_narrow_kernel(const __g
 
     if (x->piece.count > 0) {
         if (warp < 4)
-            soften<T, E4M3, NH>(g, sbase, x, ws, error);
+            soften<T, NH>(g, sbase, x, ws, error);
         else if (warp < 12)
-            bring<T, E4M3, NH>(g, sbase, x, error);
+            bring<T, NH>(g, sbase, x, error);
         else if (warp == 12)
-            multiply_qk<Operand, NH>(g, sbase, x, error);
+            multiply_qk<NH>(g, sbase, x, error);
         else
-            multiply_pv<Operand, NH>(g, sbase, x, error);
+            multiply_pv<NH>(g, sbase, x, error);
     }
     __syncwarp();
     tc::fence_before();
@@ -516,8 +481,7 @@ __global__ void __launch_bounds__(512) hs_attend_narrow_join_kernel(const __grid
     const hs_attend_t& a = g.a;
     const uint8_t* ws = static_cast<const uint8_t*>(a.workspace);
     const Partial<NH>* parts = reinterpret_cast<const Partial<NH>*>(ws + kOffPartial);
-    long long unit;
-    int first, last;
+    int unit, first, last;
     if (!find_cut(reinterpret_cast<const Start*>(ws + kOffStart), ctas, blockIdx.x, unit, first, last)) return;
     const int t = threadIdx.x, h0 = kJoinHeads * blockIdx.y, n = last - first + 1;
     auto part = [&](int i) -> const Partial<NH>& { return parts[2 * (first + i) + (i == 0)]; };
@@ -547,7 +511,7 @@ __global__ void __launch_bounds__(512) hs_attend_narrow_join_kernel(const __grid
             acc[k] += w == 0.f ? 0.f : w * o;
         }
     const long long b = unit / a.positions;
-    const int p = (int)(unit - b * a.positions);
+    const int p = unit - (int)b * a.positions;
     T* out = static_cast<T*>(a.out) + b * a.out_stride[0] + p * a.out_stride[1] + t;
 #pragma unroll
     for (int k = 0; k < kJoinHeads; ++k) {
@@ -555,33 +519,26 @@ __global__ void __launch_bounds__(512) hs_attend_narrow_join_kernel(const __grid
         const float l = total[k];
         const bool some = l > 0.f || l != l;
         out[(h0 + k) * a.out_stride[2]] = HsType<T>::from_float(some ? acc[k] / l : 0.f);
-        if (a.lse && t == 0) a.lse[unit * a.heads + h0 + k] = some ? (reference[k] + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        if (a.lse && t == 0) a.lse[(int64_t)unit * a.heads + h0 + k] = some ? (reference[k] + log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
 }
 
-template <typename T, bool E4M3, int NH> cudaError_t launch(const Args& g, int ctas, cudaStream_t s)
+template <typename T, int NH> cudaError_t launch(const Args& g, cudaStream_t s)
 {
-    cudaError_t e = cudaFuncSetAttribute(hs_attend_narrow_kernel<T, E4M3, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         smem_bytes<NH>());
+    cudaError_t e = cudaFuncSetAttribute(hs_attend_narrow_kernel<T, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<NH>());
     if (e != cudaSuccess) return e;
-    hs_attend_narrow_kernel<T, E4M3, NH><<<ctas, kThreads, smem_bytes<NH>(), s>>>(g);
+    hs_attend_narrow_kernel<T, NH><<<g.workers, kThreads, smem_bytes<NH>(), s>>>(g);
     e = cudaGetLastError();
-    if (e != cudaSuccess || !g.flat || ctas <= 1) return e;
-    const int cut = (int)(g.units < ctas - 1 ? g.units : ctas - 1);  // at most this many units are cut
-    return launch_after(hs_attend_narrow_join_kernel<T, NH>, dim3(cut, (g.a.heads + kJoinHeads - 1) / kJoinHeads), 512, s, g, ctas);
-}
-
-template <typename T, bool E4M3> cudaError_t launch(const Args& g, int ctas, cudaStream_t s)
-{
-    return g.a.heads <= 16 ? launch<T, E4M3, 16>(g, ctas, s) : g.a.heads <= 32 ? launch<T, E4M3, 32>(g, ctas, s)
-                                                                              : launch<T, E4M3, 64>(g, ctas, s);
+    if (e != cudaSuccess || !g.flat || g.workers <= 1) return e;
+    const int cut = g.units < g.workers - 1 ? g.units : g.workers - 1;  // at most this many units are cut
+    return launch_after(hs_attend_narrow_join_kernel<T, NH>, dim3(cut, (g.a.heads + kJoinHeads - 1) / kJoinHeads), 512, s, g, g.workers);
 }
 
 }  // namespace
 
 size_t narrow_workspace(int64_t units, int64_t tiles, int heads)
 {
-    const size_t part = heads <= 16 ? sizeof(Partial<16>) : heads <= 32 ? sizeof(Partial<32>) : sizeof(Partial<64>);
+    const size_t part = heads <= 16 ? sizeof(Partial<16>) : sizeof(Partial<32>);
     return kOffPartial + part * 2 * (size_t)(units * tiles < kMaxCtas ? units * tiles : kMaxCtas);
 }
 
@@ -590,20 +547,11 @@ cudaError_t launch_narrow(const hs_attend_t& a, int sms, cudaStream_t s)
     Args g;
     g.a = a;
     g.head_blocks = 1;
-    g.units = (int64_t)a.batch * a.positions;
-    const int64_t rows = a.slots ? a.entries : a.n_rows;
-    const int64_t tiles = rows <= kTile ? 1 : (rows + kTile - 1) / kTile;
-    int64_t ctas = sms < kMaxCtas ? sms : kMaxCtas;
-    ctas = g.units * tiles < ctas ? g.units * tiles : ctas;
-    // Whole units to an SM, or equal pieces: pieces also write and join up to two partial results
-    // an SM, about 8 us, or 6 tiles' time.
-    const int64_t whole = (g.units + ctas - 1) / ctas * tiles, pieces = (g.units * tiles + ctas - 1) / ctas + 6;
-    g.flat = whole > pieces;
-    if (!g.flat && ctas > g.units) ctas = g.units;
-    const bool e4m3 = a.row_format == HS_ROWS_E4M3;
-    if (a.dtype == HS_TYPE_BF16)
-        return e4m3 ? launch<__nv_bfloat16, true>(g, (int)ctas, s) : launch<__nv_bfloat16, false>(g, (int)ctas, s);
-    return e4m3 ? launch<__half, true>(g, (int)ctas, s) : launch<__half, false>(g, (int)ctas, s);
+    g.units = a.batch * a.positions;
+    // Pieces also write and join up to two partial results an SM: about 8 us, 6 tiles' time.
+    g.cut(sms < kMaxCtas ? sms : kMaxCtas, a.slots ? a.entries : a.n_rows, 6);
+    if (a.dtype == HS_TYPE_BF16) return a.heads <= 16 ? launch<__nv_bfloat16, 16>(g, s) : launch<__nv_bfloat16, 32>(g, s);
+    return a.heads <= 16 ? launch<__half, 16>(g, s) : launch<__half, 32>(g, s);
 }
 
 }  // namespace hs_attn

@@ -88,6 +88,11 @@ __device__ __forceinline__ void cluster_sync()
                      : "memory");
 }
 
+__device__ __forceinline__ void cluster_sync_relaxed()  // orders no memory
+{
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
 // ---- copies --------------------------------------------------------------------
 
 // 16 bytes from global to shared memory; ok = false writes zeros and reads nothing.
@@ -350,6 +355,13 @@ __device__ __forceinline__ float exp2_approx(float x)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float log2_approx(float x)
+{
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
