@@ -49,6 +49,7 @@ struct Args {
     uint8_t* values;
     uint8_t* rope;
     int64_t blocks;
+    int flat;  // 1: equal pieces of the line of blocks; 0: whole units
 };
 
 template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
@@ -388,17 +389,20 @@ struct Request {
         for (int i = 0; i < q_tiles(); ++i) t += blocks(i);
         return t;
     }
+    // What the line is cut by: blocks, or units.
+    __device__ long long size_of_head(bool flat) const { return flat ? blocks_of_head() : q_tiles(); }
 };
 
 struct Walk {
     const hs_prefill_t& a;
+    const bool flat;
     int b, h, qt, kb;
-    long long left;
+    long long left;  // blocks, or units
     Request r;
     // the current piece
     int head, tile, t0, t1, blocks;
-    __device__ Walk(const hs_prefill_t& args, const Aux* x)
-        : a(args), b(x->start.b), h(x->start.h), qt(x->start.qt), kb(x->start.kb), left(x->count), r(args, x->start.b)
+    __device__ Walk(const Args& g, const Aux* x)
+        : a(g.a), flat(g.flat), b(x->start.b), h(x->start.h), qt(x->start.qt), kb(x->start.kb), left(x->count), r(g.a, x->start.b)
     {
     }
     __device__ bool next()
@@ -416,8 +420,8 @@ struct Walk {
         tile = qt;
         blocks = r.blocks(qt);
         t0 = kb;
-        t1 = blocks - t0 <= left ? blocks : t0 + (int)left;
-        left -= t1 - t0;
+        t1 = !flat || blocks - t0 <= left ? blocks : t0 + (int)left;
+        left -= flat ? t1 - t0 : 1;
         kb = 0;
         ++qt;
         return true;
@@ -437,7 +441,7 @@ template <typename T> __device__ void bring_queries(const Args& g, uint32_t sbas
     const hs_prefill_t& a = g.a;
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 8, ch = lane & 7;
     const uint32_t qfull = tc::map_to_rank(tc::smem_addr(&x->qfull), 0);
-    Walk walk(a, x);
+    Walk walk(g, x);
     for (int pieces = 0; walk.next(); ++pieces) {
         // Q's readers, the last piece's products with keys, are done.
         if (pieces) wait(tc::smem_addr(&x->qfree), (pieces - 1) & 1, &x->dead, error);
@@ -465,7 +469,7 @@ __device__ void bring_tiles(const Args& g, uint32_t sbase, Aux* x, uint32_t rank
 {
     long long j = 0;
     Ring ring, last;
-    Walk walk(g.a, x);
+    Walk walk(g, x);
     while (walk.next()) {
         const int64_t block0 = walk.r.k0 / 128;
         for (int t = walk.t0; t < walk.t1; ++t, ++j) {
@@ -503,16 +507,17 @@ __device__ void bring_tiles(const Args& g, uint32_t sbase, Aux* x, uint32_t rank
 }
 
 // The second CTA tells the first that its half of a block has come.
-__device__ void forward(Aux* x, int* error)
+__device__ void forward(const Args& g, Aux* x, int* error)
 {
     Ring ring;
-    const long long n = x->count;
-    for (long long j = 0; j < n; ++j, ring.step()) {
-        wait(tc::smem_addr(&x->kfull[ring.s]), ring.phase, &x->dead, error);
-        tc::mbar_arrive_cluster(tc::map_to_rank(tc::smem_addr(&x->kpeer[ring.s]), 0));
-        wait(tc::smem_addr(&x->vfull[ring.s]), ring.phase, &x->dead, error);
-        tc::mbar_arrive_cluster(tc::map_to_rank(tc::smem_addr(&x->vpeer[ring.s]), 0));
-    }
+    Walk walk(g, x);
+    while (walk.next())
+        for (int t = walk.t0; t < walk.t1; ++t, ring.step()) {
+            wait(tc::smem_addr(&x->kfull[ring.s]), ring.phase, &x->dead, error);
+            tc::mbar_arrive_cluster(tc::map_to_rank(tc::smem_addr(&x->kpeer[ring.s]), 0));
+            wait(tc::smem_addr(&x->vfull[ring.s]), ring.phase, &x->dead, error);
+            tc::mbar_arrive_cluster(tc::map_to_rank(tc::smem_addr(&x->vpeer[ring.s]), 0));
+        }
 }
 
 // Q K^T of tile S with the keys at k_desc, and P V of tile S with the values at v_desc.
@@ -554,7 +559,7 @@ template <typename T> __device__ void multiply(const Args& g, uint32_t sbase, Au
     int pieces = 0;
     uint32_t phase[2] = {0, 0};  // of pfull
     Ring now, next;              // the block of P V, and of Q K^T
-    Walk walk(g.a, x);
+    Walk walk(g, x);
     auto release = [](uint64_t& bar) {  // in both CTAs, when all products so far are complete
         if (tc::elect_one()) tc::commit<2>(tc::smem_addr(&bar));
         __syncwarp();
@@ -634,7 +639,7 @@ template <typename T> __device__ void soften(const Args& g, Aux* x, uint32_t ran
     const uint32_t pfull[2] = {tc::map_to_rank(tc::smem_addr(&x->pfull[tile][0]), 0),
                                tc::map_to_rank(tc::smem_addr(&x->pfull[tile][1]), 0)};
     long long mine = 0;
-    Walk walk(a, x);
+    Walk walk(g, x);
     while (walk.next()) {
         const int end = walk.end(tile);
         const int at = 512 * walk.tile + 256 * tile + 128 * (int)rank + row;
@@ -779,7 +784,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_pref
     if (warp == 11) {
         // This pair's piece of the line of blocks.
         long long total = 0;
-        for (int b = lane; b < a.batch; b += 32) total += Request(a, b).blocks_of_head() * a.heads;
+        for (int b = lane; b < a.batch; b += 32) total += Request(a, b).size_of_head(g.flat) * a.heads;
         for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
         const long long n = total < pairs ? total : pairs, i = pair;
         const long long lo = i < n ? total * i / n : 0, hi = i < n ? total * (i + 1) / n : 0;
@@ -787,7 +792,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_pref
         long long before = 0;
         for (int b0 = 0; lo < hi && b0 < a.batch; b0 += 32) {
             const int b = b0 + lane;
-            const long long per = b < a.batch ? Request(a, b).blocks_of_head() : 0;
+            const long long per = b < a.batch ? Request(a, b).size_of_head(g.flat) : 0;
             long long incl = per * a.heads;
             for (int o = 1; o < 32; o <<= 1) {
                 const long long up = __shfl_up_sync(~0u, incl, o);
@@ -803,8 +808,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_pref
                     st.b = b;
                     st.h = (int)(off / per);
                     off -= st.h * per;
-                    while (off >= r.blocks(st.qt)) off -= r.blocks(st.qt++);
-                    st.kb = (int)off;
+                    if (g.flat) {
+                        while (off >= r.blocks(st.qt)) off -= r.blocks(st.qt++);
+                        st.kb = (int)off;
+                    } else {
+                        st.qt = (int)off;
+                    }
                 }
                 const int src = __ffs(who) - 1;
                 st.b = __shfl_sync(~0u, st.b, src);
@@ -856,7 +865,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_pref
         else if (warp == 11 && rank == 0)
             multiply<T>(g, sbase, x, error);
         else if (warp == 11 && lane == 0)
-            forward(x, error);
+            forward(g, x, error);
         else if (warp == 10 && lane == 0)
             bring_tiles(g, sbase, x, rank, error);
     }
@@ -995,7 +1004,7 @@ template <typename T, bool E4M3> cudaError_t launch(const Args& g, int pairs, cu
         e = cudaGetLastError();
     }
     if (e != cudaSuccess) return e;
-    if (pairs < 2) return cudaSuccess;
+    if (pairs < 2 || !g.flat) return cudaSuccess;
     const int64_t units = (a.q_tokens / 512 + a.batch) * a.heads;  // at most
     return launch_after(hs_prefill_join_kernel<T>, dim3((unsigned)(units < pairs - 1 ? units : pairs - 1), 4, HS_HEAD_DIM / kJoinCols), 512, 0, s, g, pairs);
 }
@@ -1019,6 +1028,8 @@ cudaError_t hs_launch_prefill(const hs_prefill_t& a, cudaStream_t s)
     Args g;
     g.a = a;
     g.blocks = (a.k_tokens + 255) / 256 * 2;
+    // Short prompts: no unit has more than a few blocks (2 us each), and a join takes about 8 us.
+    g.flat = (a.k_tokens + 127) / 128 > 4;
     g.keys = static_cast<uint8_t*>(a.workspace) + kOffKeys;
     g.values = g.keys + (size_t)g.blocks * a.heads * kBlock;
     g.rope = g.values + (size_t)g.blocks * a.heads * kBlock;
