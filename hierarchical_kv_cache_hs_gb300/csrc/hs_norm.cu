@@ -4,8 +4,7 @@
 // A row's h stays in fp32 registers between the sum of squares and the scaling, so
 // each input is read once and each output written once; the pass is bound by HBM.
 // Rows whose pieces lie on 16-byte boundaries go through hs_norm_kernel: 16-byte
-// loads, a warp a row up to 128 pieces (576 16-bit channels are 72), else 256 threads
-// a row.  Any other row (odd widths, odd alignments, groups that are not a power of
+// loads, a warp a row up to 128 pieces (576 16-bit channels are 72), else 8 or 16 warps.  Any other row (odd widths, odd alignments, groups that are not a power of
 // two of pieces) goes through hs_norm_any_kernel, element by element with the row in
 // shared memory.
 #include "hs_ops.h"
@@ -73,23 +72,24 @@ template <> struct Piece<__half> {
     }
 };
 
-// y / scale, as a product where the reciprocal is an ordinary number.
-struct Divide {
-    float scale, inv;
-    bool product;
-    __device__ explicit Divide(float s) : scale(s == 0.f ? 1.f : s), inv(1.f / scale), product(scale > 1e-30f && scale < 1e30f) {}
-    __device__ float operator()(float y) const { return product ? y * inv : y / scale; }
-};
-
-constexpr int kWarps = 8;  // a block
-
-// NV: 16-byte pieces a thread; WIDE: the block's 256 threads share a row, else each
-// warp has its own.
-template <typename T, bool E4M3, int NV, bool WIDE>
-__global__ void __launch_bounds__(kWarps * 32) hs_norm_kernel(const __grid_constant__ hs_norm_t a)
+// A scale's reciprocal, or 0 where it is no ordinary number (then y / scale is divided out).
+__device__ __forceinline__ float inverse(float scale) { return scale > 1e-30f && scale < 1e30f ? 1.f / scale : 0.f; }
+__device__ __forceinline__ float divided(float y, float scale, float inv)
 {
-    constexpr int P = Piece<T>::n, kTeam = WIDE ? kWarps * 32 : 32;
-    __shared__ float red[2][kWarps];
+    return inv != 0.f ? y * inv : y / (scale == 0.f ? 1.f : scale);
+}
+
+constexpr int kWarps = 8;  // of a block, where rows do not share it
+
+// NV: 16-byte pieces a thread; TEAM: warps that share a row (1: each of the block's has
+// its own).
+template <typename T, bool E4M3, int NV, int TEAM>
+__global__ void __launch_bounds__((TEAM == 1 ? kWarps : TEAM) * 32, TEAM == 8 && NV == 2 ? 6 : TEAM == 1 && NV == 3 ? 5 : 1)
+    hs_norm_kernel(const __grid_constant__ hs_norm_t a)
+{
+    constexpr bool WIDE = TEAM > 1;
+    constexpr int P = Piece<T>::n, kTeam = TEAM * 32;
+    __shared__ float red[2][TEAM];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int me = WIDE ? threadIdx.x : lane;
     const int64_t row = WIDE ? blockIdx.x : (int64_t)blockIdx.x * kWarps + warp;
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kWarps * 32) hs_norm_kernel(const __grid_const
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         const int i = v * kTeam + me;
-        if (NV <= 4 && i < normed) wv[v] = weight[i];
+        if (NV <= 3 && i < normed) wv[v] = weight[i];
     }
     float sum = 0.f;
 #pragma unroll
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kWarps * 32) hs_norm_kernel(const __grid_const
         __syncthreads();  // and every input of the row has been read: outputs may overwrite it
         sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) sum += red[0][w];
+        for (int w = 0; w < TEAM; ++w) sum += red[0][w];
     } else {
         __syncwarp();
     }
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kWarps * 32) hs_norm_kernel(const __grid_const
         if (i < normed) {
             if (a.residual) res_out[i] = Piece<T>::pack(h[v]);
             float w[P];
-            Piece<T>::unpack(NV <= 4 ? wv[v] : weight[i], w);
+            Piece<T>::unpack(NV <= 3 ? wv[v] : weight[i], w);
 #pragma unroll
             for (int k = 0; k < P; ++k) h[v][k] *= r * w[k];
         }
@@ -160,15 +160,20 @@ __global__ void __launch_bounds__(kWarps * 32) hs_norm_kernel(const __grid_const
     if constexpr (E4M3) {
         float* scales = a.scales + row * a.scales_stride;
         uint8_t* out = static_cast<uint8_t*>(a.out) + row * a.out_stride;
-        auto store = [&](int i, const float* y, const Divide& div) {
+        auto store = [&](int i, float* y, float scale) {
             if (i >= pieces) return;
+            const float inv = inverse(scale);
+            if (inv != 0.f)
+#pragma unroll
+                for (int k = 0; k < P; ++k) y[k] *= inv;
+            else
+#pragma unroll
+                for (int k = 0; k < P; ++k) y[k] = divided(y[k], scale, 0.f);
             uint32_t q[P / 4];
 #pragma unroll
-            for (int k = 0; k < P / 4; ++k) {
-                const float2 lo = make_float2(div(y[4 * k]), div(y[4 * k + 1])), hi = make_float2(div(y[4 * k + 2]), div(y[4 * k + 3]));
-                q[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, __NV_E4M3) |
-                       (uint32_t)__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, __NV_E4M3) << 16;
-            }
+            for (int k = 0; k < P / 4; ++k)
+                q[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(y[4 * k], y[4 * k + 1]), __NV_SATFINITE, __NV_E4M3) |
+                       (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(y[4 * k + 2], y[4 * k + 3]), __NV_SATFINITE, __NV_E4M3) << 16;
             if constexpr (P == 8)
                 *reinterpret_cast<uint2*>(out + i * 8) = make_uint2(q[0], q[1]);
             else
@@ -181,13 +186,12 @@ __global__ void __launch_bounds__(kWarps * 32) hs_norm_kernel(const __grid_const
                 __syncthreads();
                 top = red[1][0];
 #pragma unroll
-                for (int w = 1; w < kWarps; ++w) top = nan_max(top, red[1][w]);
+                for (int w = 1; w < TEAM; ++w) top = nan_max(top, red[1][w]);
             }
             const float scale = top / HS_E4M3_MAX;
             if (me == 0) scales[0] = scale;
-            const Divide div(scale);
 #pragma unroll
-            for (int v = 0; v < NV; ++v) store(v * kTeam + me, h[v], div);
+            for (int v = 0; v < NV; ++v) store(v * kTeam + me, h[v], scale);
         } else {
             const int lanes = a.group / P;  // a power of two: a group is this many neighbouring lanes
 #pragma unroll
@@ -199,7 +203,7 @@ __global__ void __launch_bounds__(kWarps * 32) hs_norm_kernel(const __grid_const
                 for (int o = 1; o < lanes; o <<= 1) m = nan_max(m, __shfl_xor_sync(~0u, m, o));
                 const float scale = m / HS_E4M3_MAX;
                 if (i < pieces && (lane & (lanes - 1)) == 0) scales[i / lanes] = scale;
-                store(i, h[v], Divide(scale));
+                store(i, h[v], scale);
             }
         }
     }
@@ -242,7 +246,7 @@ template <typename T, bool E4M3> __global__ void __launch_bounds__(kWarps * 32) 
         for (int i = threadIdx.x; i < width; i += kThreads) out[i] = HsType<T>::from_float(y[i]);
     } else {
         uint8_t* out = static_cast<uint8_t*>(a.out) + row * a.out_stride;
-        auto put = [&](int i, const Divide& div) { out[i] = __nv_cvt_float_to_fp8(div(y[i]), __NV_SATFINITE, __NV_E4M3); };
+        auto put = [&](int i, float scale, float inv) { out[i] = __nv_cvt_float_to_fp8(divided(y[i], scale, inv), __NV_SATFINITE, __NV_E4M3); };
         if (a.group == 0) {  // the block together
             float m = 0.f;
             for (int i = threadIdx.x; i < width; i += kThreads) m = nan_max(m, fabsf(y[i]));
@@ -252,8 +256,8 @@ template <typename T, bool E4M3> __global__ void __launch_bounds__(kWarps * 32) 
             for (int w = 0; w < kWarps; ++w) m = nan_max(m, red[w]);
             const float scale = m / HS_E4M3_MAX;
             if (threadIdx.x == 0) a.scales[row * a.scales_stride] = scale;
-            const Divide div(scale);
-            for (int i = threadIdx.x; i < width; i += kThreads) put(i, div);
+            const float inv = inverse(scale);
+            for (int i = threadIdx.x; i < width; i += kThreads) put(i, scale, inv);
             return;
         }
         for (int g = warp; g * a.group < width; g += kWarps) {  // a warp a group
@@ -263,8 +267,8 @@ template <typename T, bool E4M3> __global__ void __launch_bounds__(kWarps * 32) 
             for (int o = 16; o; o >>= 1) m = nan_max(m, __shfl_xor_sync(~0u, m, o));
             const float scale = m / HS_E4M3_MAX;
             if (lane == 0) a.scales[row * a.scales_stride + g] = scale;
-            const Divide div(scale);
-            for (int i = g * a.group + lane; i < end; i += 32) put(i, div);
+            const float inv = inverse(scale);
+            for (int i = g * a.group + lane; i < end; i += 32) put(i, scale, inv);
         }
     }
 }
@@ -295,23 +299,23 @@ template <typename T, bool E4M3> cudaError_t launch(const hs_norm_t& a, cudaStre
     } else if (pieces <= 128) {
         const unsigned grid = (unsigned)((a.tokens + kWarps - 1) / kWarps);
         if (pieces <= 32)
-            hs_norm_kernel<T, E4M3, 1, false><<<grid, kWarps * 32, 0, s>>>(a);
+            hs_norm_kernel<T, E4M3, 1, 1><<<grid, kWarps * 32, 0, s>>>(a);
         else if (pieces <= 96)
-            hs_norm_kernel<T, E4M3, 3, false><<<grid, kWarps * 32, 0, s>>>(a);
+            hs_norm_kernel<T, E4M3, 3, 1><<<grid, kWarps * 32, 0, s>>>(a);
         else
-            hs_norm_kernel<T, E4M3, 4, false><<<grid, kWarps * 32, 0, s>>>(a);
+            hs_norm_kernel<T, E4M3, 4, 1><<<grid, kWarps * 32, 0, s>>>(a);
     } else {
         const unsigned grid = (unsigned)a.tokens;
         if (pieces <= 256)
-            hs_norm_kernel<T, E4M3, 1, true><<<grid, kWarps * 32, 0, s>>>(a);
+            hs_norm_kernel<T, E4M3, 1, 8><<<grid, 256, 0, s>>>(a);
         else if (pieces <= 512)
-            hs_norm_kernel<T, E4M3, 2, true><<<grid, kWarps * 32, 0, s>>>(a);
+            hs_norm_kernel<T, E4M3, 2, 8><<<grid, 256, 0, s>>>(a);
         else if (pieces <= 1024)
-            hs_norm_kernel<T, E4M3, 4, true><<<grid, kWarps * 32, 0, s>>>(a);
+            hs_norm_kernel<T, E4M3, 2, 16><<<grid, 512, 0, s>>>(a);
         else if (pieces <= 2048)
-            hs_norm_kernel<T, E4M3, 8, true><<<grid, kWarps * 32, 0, s>>>(a);
+            hs_norm_kernel<T, E4M3, 4, 16><<<grid, 512, 0, s>>>(a);
         else
-            hs_norm_kernel<T, E4M3, 16, true><<<grid, kWarps * 32, 0, s>>>(a);
+            hs_norm_kernel<T, E4M3, 8, 16><<<grid, 512, 0, s>>>(a);
     }
     return cudaGetLastError();
 }
