@@ -605,7 +605,10 @@ int hs_resolve_noalloc(int batch, int ctx_len, int row_bytes, int buffer_slots, 
  * the caller's, 16-byte aligned device memory of at least the bytes that the
  * matching _workspace call returns (0 when its sizes are out of range);
  * their contents need not survive a call, and calls that overlap on the GPU
- * need one each.  Errors: HS_ERR_ARG (a NULL or misaligned pointer, a size,
+ * need one each.  The attention kernels' waits are bounded: one that runs out
+ * (a second or two; it cannot in a working kernel) sets the workspace's first
+ * int32 to 1, which is otherwise left as it is, and the call's outputs are not
+ * valid.  Errors: HS_ERR_ARG (a NULL or misaligned pointer, a size,
  * type or stride that the call does not take, a workspace that is too small),
  * HS_ERR_LIMIT, HS_ERR_CUDA; nothing is enqueued then.
  */
@@ -650,7 +653,10 @@ int hs_resolve_noalloc(int batch, int ctx_len, int row_bytes, int buffer_slots, 
  *        multiples of 16; 16-byte aligned (a handle's hs_device_buffer:
  *        n_rows = S + T, row_stride = R, request_stride = (S + T) * R)
  *   lse  fp32 [batch][positions][heads], contiguous, or NULL
- * Softmax weights are rounded to `dtype` before the product with the rows.
+ * Softmax weights are rounded to `dtype` before the product with the rows; with
+ * 8-bit rows, weights times row scales are rounded to fp16, and a bf16 query is
+ * held in fp16 after a scaling by a power of two (what is below 2^-28 of a
+ * head's largest channel may be rounded).
  * The workspace call takes `rows` = entries (slots) or n_rows (lengths).
  * Source: no passage (the pages name the sparse attention that reads the
  * resolved rows as the path's consumer and do not define it).
@@ -694,7 +700,10 @@ int hs_latent_attend(const hs_attend_t* args, hs_stream_t stream);
  *   out   [q_tokens][heads][128]; lse fp32 [q_tokens][heads] or NULL
  *   rows  [k_tokens] rows of row_stride bytes
  * with types, alignments and strides as in hs_latent_attend.  The keys' and
- * values' expanded channels and the softmax weights are rounded to `dtype`.
+ * values' expanded channels, the rotary channels of 8-bit rows and the softmax
+ * weights are rounded to `dtype`.  Rows that a query does not see may hold
+ * anything; a value that is not finite once rounded makes the output NaN of
+ * every query that sees its row.
  * Source: no passage (as hs_latent_attend).
  */
 typedef struct {
