@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(512) hs_attend_join_kernel(const __grid_consta
     const bool live = head < a.heads;
     float acc[COLS] = {}, sum = 0.f, top = -INFINITY;
     if (live)
-#pragma unroll 4
+#pragma unroll(COLS == 4 ? 8 : 2)
         for (int n = first + group; n <= last; n += 4) {
             const Partial& q = parts[2 * n + (n == first)];
             const float ref = q.ref[rank][lane], l = q.sum[rank][lane];

@@ -266,7 +266,7 @@ __device__ __forceinline__ uint4 bf16_to_half(const uint4& v, float f)
 // calls it, at least 256 threads for up to 256 workers.
 __device__ __forceinline__ bool find_cut(const Start* start, int workers, int x, int& unit, int& first, int& last)
 {
-    __shared__ int counts[8], at;
+    __shared__ int counts[8], at, cut_unit;
     const int t = threadIdx.x;
     if (t == 0) at = 0;
     int mine = -1;
@@ -282,11 +282,11 @@ __device__ __forceinline__ bool find_cut(const Start* start, int workers, int x,
     if (cut) {
         int before = __popc(m & ((1u << (t & 31)) - 1));
         for (int w = 0; w < t >> 5; ++w) before += counts[w];
-        if (before == x) at = t;
+        if (before == x) at = t, cut_unit = mine;
     }
     __syncthreads();
     if (at == 0) return false;
-    unit = start[at].unit;
+    unit = cut_unit;
     first = at - 1;
     last = first + __syncthreads_count(inside && mine == unit);
     return true;

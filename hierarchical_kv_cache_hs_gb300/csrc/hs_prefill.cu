@@ -97,7 +97,8 @@ __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, int* dead, i
 // ---- (1) expansion -----------------------------------------------------------------
 
 constexpr int kEStages = 4;
-constexpr int kEThreads = (5 + kEStages) * 32;  // warps 0-3 write, then one a stage brings weights, the last issues the products
+constexpr int kEBring = 2 * kEStages;          // warps that bring weights, two a stage
+constexpr int kEThreads = (5 + kEBring) * 32;  // warps 0-3 write, then those, the last issues the products
 constexpr int kEOffB = 8 * 16384;  // latents: 8 blocks of 64 channels, [128 tokens][128 B]
 constexpr int kEOffOut = kEOffB + kEStages * 16384;  // two pieces on their way out, 64 channels of 128 tokens each
 constexpr int kEOffAux = kEOffOut + 2 * 16384;
@@ -127,9 +128,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kEThreads, 1) hs_exp
     if (warp == 0) tc::tmem_alloc<2>(tc::smem_addr(&x->tmem), 512);
     if (threadIdx.x == 0) {
         x->dead = 0;
-        tc::mbar_init(tc::smem_addr(&x->afull), 2 * kEStages);
+        tc::mbar_init(tc::smem_addr(&x->afull), 2 * kEBring);
         for (int i = 0; i < kEStages; ++i) {
-            tc::mbar_init(tc::smem_addr(&x->bfull[i]), 2);
+            tc::mbar_init(tc::smem_addr(&x->bfull[i]), 4);
             tc::mbar_init(tc::smem_addr(&x->bfree[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -210,8 +211,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kEThreads, 1) hs_exp
             if (lane == 0) tc::mbar_arrive_cluster(dfree[d]);
         }
         if (threadIdx.x == 0) tc::bulk_wait_all();
-    } else if (warp < 4 + kEStages) {
-        const int s = warp - 4;
+    } else if (warp < 4 + kEBring) {
+        const int me = warp - 4, s = me >> 1, half = me & 1;
         const uint32_t bfull = tc::map_to_rank(tc::smem_addr(&x->bfull[s]), 0);
         const uint32_t afull = tc::map_to_rank(tc::smem_addr(&x->afull), 0);
         const uint8_t* w = static_cast<const uint8_t*>(rank ? a.w_uv : a.w_uk);
@@ -224,9 +225,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kEThreads, 1) hs_exp
                 // The earlier tokens' products are done: each stage's last one is (each of these warps waits
                 // for its own stage).
                 if (fills) wait(tc::smem_addr(&x->bfree[s]), (fills - 1) & 1, &x->dead, error);
-                asm volatile("bar.sync 2, %0;" ::"n"(32 * kEStages) : "memory");
+                asm volatile("bar.sync 2, %0;" ::"n"(32 * kEBring) : "memory");
                 at = mt;
-                for (int i = s; i < 32; i += kEStages) {  // a quarter of a block of channels each
+                for (int i = me; i < 32; i += kEBring) {  // a quarter of a block of channels each
                     const int kb = i >> 2;
 #pragma unroll
                     for (int n = 0; n < 8; ++n) {
@@ -245,7 +246,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kEThreads, 1) hs_exp
                     }
                 }
                 if (h == 0) {  // the rotary channels' tile (of 8-bit rows: scaled, and rounded to T)
-                    for (int i = 32 * s + lane; i < 128 * 8; i += 32 * kEStages) {
+                    for (int i = 32 * me + lane; i < 128 * 8; i += 32 * kEBring) {
                         const int tok = i >> 3;
                         const int64_t token = mt * 256 + 128 * (int)rank + tok;
                         const uint8_t* src = static_cast<const uint8_t*>(a.rows) + token * a.row_stride;
@@ -274,11 +275,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kEThreads, 1) hs_exp
                 if ((8 * (job - lo) + kb) % kEStages != s) continue;
                 if (fills) wait(tc::smem_addr(&x->bfree[s]), (fills - 1) & 1, &x->dead, error);
                 ++fills;
-                const uint8_t* src = w + ((h * HS_HEAD_DIM + (lane >> 3)) * HS_LATENT_DIM + kb * 64 + ch * 8) * 2;
-                const uint32_t dst = sbase + kEOffB + s * 16384 + (lane >> 3) * 128;
-#pragma unroll 8
-                for (int n = 0; n < 32; ++n)
-                    tc::cp_async16(dst + n * 512 + ((ch ^ ((n * 4 + (lane >> 3)) & 7)) << 4), src + (int64_t)n * 4 * HS_LATENT_DIM * 2, true);
+                const int r0 = 64 * half + (lane >> 3);
+                const uint8_t* src = w + ((h * HS_HEAD_DIM + r0) * HS_LATENT_DIM + kb * 64 + ch * 8) * 2;
+                const uint32_t dst = sbase + kEOffB + s * 16384 + r0 * 128;
+#pragma unroll
+                for (int n = 0; n < 16; ++n)
+                    tc::cp_async16(dst + n * 512 + ((ch ^ ((n * 4 + r0) & 7)) << 4), src + (int64_t)n * 4 * HS_LATENT_DIM * 2, true);
                 tc::cp_async_commit();
                 tc::cp_async_wait<0>();
                 tc::fence_async_shared();
@@ -345,8 +347,8 @@ struct Aux {
     uint64_t sfull[2], pfull[2][2], odone[2], spare;  // pfull: weights of a block's first and second 64 keys
     uint32_t tmem;
     int dead;
-    Start start;
-    long long count;
+    Start start, stop;  // this pair's piece of the line
+    int any;
 };
 constexpr int kSmem = kOffAux + (int)sizeof(Aux);
 static_assert(kSmem <= 232448, "shared memory");
@@ -362,6 +364,11 @@ struct Ring {
         if (++s == kStages) s = 0, phase ^= 1;
     }
 };
+
+// Blocks' time that a unit's queries, first scores and output take: by it pieces of many
+// short units and pieces of few long ones end together (8192 tokens, 32 heads: 10% apart
+// without it).
+constexpr int kUnitCost = 3;
 
 struct Request {
     long long q0, k0;
@@ -383,31 +390,32 @@ struct Request {
         return keys <= 0 ? 0 : (int)(((k0 & 127) + keys + 127) / 128);
     }
     __device__ int blocks(int qt) const { return max(1, blocks_to(512 * qt + 512)); }
-    __device__ long long blocks_of_head() const
+    // What the line is cut by: blocks, and kUnitCost of them for a unit's own time; or units.
+    __device__ long long size_of_head(bool flat) const
     {
+        if (!flat) return q_tiles();
         long long t = 0;
-        for (int i = 0; i < q_tiles(); ++i) t += blocks(i);
+        for (int i = 0; i < q_tiles(); ++i) t += blocks(i) + kUnitCost;
         return t;
     }
-    // What the line is cut by: blocks, or units.
-    __device__ long long size_of_head(bool flat) const { return flat ? blocks_of_head() : q_tiles(); }
 };
 
+// The units, or parts of units, of a pair's piece, in order.
 struct Walk {
     const hs_prefill_t& a;
-    const bool flat;
+    const Start stop;
     int b, h, qt, kb;
-    long long left;  // blocks, or units
+    bool done;
     Request r;
-    // the current piece
+    // the current one
     int head, tile, t0, t1, blocks;
     __device__ Walk(const Args& g, const Aux* x)
-        : a(g.a), flat(g.flat), b(x->start.b), h(x->start.h), qt(x->start.qt), kb(x->start.kb), left(x->count), r(g.a, x->start.b)
+        : a(g.a), stop(x->stop), b(x->start.b), h(x->start.h), qt(x->start.qt), kb(x->start.kb), done(false), r(g.a, x->start.b)
     {
     }
     __device__ bool next()
     {
-        if (left <= 0) return false;
+        if (done) return false;
         while (qt >= r.q_tiles()) {
             qt = 0;
             if (r.n == 0 || ++h >= a.heads) {
@@ -420,8 +428,12 @@ struct Walk {
         tile = qt;
         blocks = r.blocks(qt);
         t0 = kb;
-        t1 = !flat || blocks - t0 <= left ? blocks : t0 + (int)left;
-        left -= flat ? t1 - t0 : 1;
+        t1 = blocks;
+        if (b == stop.b && h == stop.h && qt == stop.qt) {
+            if (t0 >= stop.kb) return false;
+            t1 = stop.kb;
+            done = true;
+        }
         kb = 0;
         ++qt;
         return true;
@@ -782,15 +794,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_pref
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == 0) tc::tmem_alloc<2>(tc::smem_addr(&x->tmem), 512);
     if (warp == 11) {
-        // This pair's piece of the line of blocks.
+        // This pair's piece of the line: from where its share begins to where the next one's does.
         long long total = 0;
         for (int b = lane; b < a.batch; b += 32) total += Request(a, b).size_of_head(g.flat) * a.heads;
         for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
-        const long long n = total < pairs ? total : pairs, i = pair;
-        const long long lo = i < n ? total * i / n : 0, hi = i < n ? total * (i + 1) / n : 0;
-        Start st = {-1, 0, 0, 0};
+        const long long share = total / pairs;
+        const int extra = (int)(total - share * pairs);
+        const long long lo = share * pair + min(pair, extra), hi = lo + share + (pair < extra);
+        Start lo_at = {a.batch, 0, 0, 0}, hi_at = lo_at;
         long long before = 0;
-        for (int b0 = 0; lo < hi && b0 < a.batch; b0 += 32) {
+        for (int b0 = 0; b0 < a.batch && before <= hi; b0 += 32) {
             const int b = b0 + lane;
             const long long per = b < a.batch ? Request(a, b).size_of_head(g.flat) : 0;
             long long incl = per * a.heads;
@@ -799,18 +812,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_pref
                 if (lane >= o) incl += up;
             }
             const long long at = before + incl - per * a.heads;
-            const bool here = lo >= at && lo < at + per * a.heads;
-            const unsigned who = __ballot_sync(~0u, here);
-            if (who) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const long long pos = k ? hi : lo;
+                const bool here = pos >= at && pos < at + per * a.heads;
+                const unsigned who = __ballot_sync(~0u, here);
+                if (!who) continue;
+                Start st = {b, 0, 0, 0};
                 if (here) {
                     const Request r(a, b);
-                    long long off = lo - at;
-                    st.b = b;
+                    long long off = pos - at;
                     st.h = (int)(off / per);
                     off -= st.h * per;
                     if (g.flat) {
-                        while (off >= r.blocks(st.qt)) off -= r.blocks(st.qt++);
-                        st.kb = (int)off;
+                        for (; off >= r.blocks(st.qt) + kUnitCost; ++st.qt) off -= r.blocks(st.qt) + kUnitCost;
+                        st.kb = off > kUnitCost ? (int)off - kUnitCost : 0;
                     } else {
                         st.qt = (int)off;
                     }
@@ -820,16 +836,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_pref
                 st.h = __shfl_sync(~0u, st.h, src);
                 st.qt = __shfl_sync(~0u, st.qt, src);
                 st.kb = __shfl_sync(~0u, st.kb, src);
-                break;
+                (k ? hi_at : lo_at) = st;
             }
             before += __shfl_sync(~0u, incl, 31);
         }
         if (lane == 0) {
-            x->start = st;
-            if (st.b < 0) x->start.b = 0;
-            x->count = st.b < 0 ? 0 : hi - lo;
+            const bool any = lo_at.b < a.batch &&
+                             !(lo_at.b == hi_at.b && lo_at.h == hi_at.h && lo_at.qt == hi_at.qt && lo_at.kb == hi_at.kb);
+            x->any = any;
+            x->start = lo_at;
+            x->stop = hi_at;
             x->dead = 0;
-            if (rank == 0) reinterpret_cast<Start*>(ws + kOffStart)[i] = st;
+            if (rank == 0) reinterpret_cast<Start*>(ws + kOffStart)[pair] = any ? lo_at : Start{-1, 0, 0, 0};
             tc::mbar_init(tc::smem_addr(&x->qfull), 4);
             tc::mbar_init(tc::smem_addr(&x->qfree), 1);
             for (int k = 0; k < kStages; ++k) {
@@ -857,7 +875,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_pref
     tc::fence_after();
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the expansion's keys and values
 
-    if (x->count > 0) {
+    if (x->any) {
         if (warp < 8)
             soften<T>(g, x, rank, ws, error);
         else if (warp < 10)
