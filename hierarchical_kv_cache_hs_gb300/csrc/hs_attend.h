@@ -174,19 +174,19 @@ struct Lookup {
     __device__ int row(int raw) const { return raw >= 0 && raw < a.n_rows ? raw : -1; }  // or -1
 };
 
-// Lines of 16 rows (row of lane l < 16: at) to L2, eight lanes a row.  (A bulk prefetch a
-// row took about 2,000 clocks a tile to issue.)
-__device__ __forceinline__ void prefetch_rows(const uint8_t* rows, int64_t row_stride, int row_bytes, int at)
+// Lines of 16 8-bit rows (row of lane l < 16: at) to L2, eight lanes a row.  (A bulk
+// prefetch a row took about 2,000 clocks a tile to issue.)
+__device__ __forceinline__ void prefetch_rows(const uint8_t* rows, int64_t row_stride, int at)
 {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int n = 0; n < 16; n += 4) {
         const int r = __shfl_sync(~0u, at, n + (lane >> 3));
         if (r < 0) continue;
-        const uint8_t* line = rows + r * row_stride;
+        const uint8_t* row = rows + r * row_stride;
         const int c = (lane & 7) * 128;
-        if (c < row_bytes) tc::prefetch_l2(line + c);
-        if ((lane & 7) == 0) tc::prefetch_l2(line + row_bytes - 1);
+        if (c < HS_ROW8_BYTES) tc::prefetch_l2(row + c);
+        if ((lane & 7) == 0) tc::prefetch_l2(row + HS_ROW8_BYTES - 1);
     }
 }
 

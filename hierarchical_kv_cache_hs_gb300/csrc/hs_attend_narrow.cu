@@ -67,11 +67,7 @@ template <typename T, int NH> __device__ void bring(const Args& g, uint32_t sbas
         const Lookup lookup(a, walk);
         int t = walk.t0;
         if ((j & 1) != stage) ++t;  // this stage's first tile of the piece
-        // Rows of the stage's next three tiles: the third is prefetched, and each was looked up an iteration
-        // before it is used.
-        int next = lookup.row(lookup.raw(t, mine)), after = lookup.row(lookup.raw(t + 2, mine));
-        int ahead = lookup.raw(t + 4, mine);
-        prefetch_rows(rows, a.row_stride, HS_ROW8_BYTES, after);
+        int next = lookup.raw(t, mine);  // looked at an iteration later
         // Q, once the last piece's products with keys are done.
         if (pieces) wait(tc::smem_addr(&x->qfree), (pieces - 1) & 1, &x->dead, error);
         const T* q = static_cast<const T*>(a.q) + walk.b * a.q_stride[0] + walk.p * a.q_stride[1];
@@ -105,11 +101,8 @@ template <typename T, int NH> __device__ void bring(const Args& g, uint32_t sbas
         if (lane == 0) tc::mbar_arrive(tc::smem_addr(&x->qfull));
         for (; t < walk.t1; t += 2) {
             const long long jt = j + t - walk.t0;
-            const int row = next;
-            next = after;
-            after = lookup.row(ahead);
-            if (t + 4 < walk.t1) prefetch_rows(rows, a.row_stride, HS_ROW8_BYTES, after);
-            ahead = lookup.raw(t + 6, mine);
+            const int row = lookup.row(next);
+            next = lookup.raw(t + 2, mine);
             const int m = (int)(jt & 3);
             const unsigned ok_bits = __ballot_sync(~0u, row >= 0);
             const float sc = row >= 0 ? *reinterpret_cast<const float*>(rows + row * a.row_stride + HS_ROW8_SCALE) : 1.f;
