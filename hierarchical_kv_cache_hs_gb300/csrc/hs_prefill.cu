@@ -898,12 +898,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_pref
 // ---- (3) join ------------------------------------------------------------------------
 
 // Block x takes the x-th unit that several pairs worked on (found at the first start
-// of a piece inside it), 128 of its queries, 16 channels.  Four groups of 128 threads,
-// one a query, take every fourth piece; the order of the sums is fixed.
-constexpr int kJoinCols = 16;
-template <typename T> __global__ void __launch_bounds__(512) hs_prefill_join_kernel(const __grid_constant__ Args g, int pairs)
+// of a piece inside it) and 128 of its queries, a thread of each group of 128 a query.
+// SPLIT: 16 channels a block, four groups that take every fourth piece; else each group
+// takes channels of its own and every piece.  The order of the sums is fixed.
+constexpr int kJoinCols = 16;  // channels a thread
+template <typename T, bool SPLIT>
+__global__ void __launch_bounds__(512) hs_prefill_join_kernel(const __grid_constant__ Args g, int pairs)
 {
-    __shared__ float tops[4][128], sums[4][128], cols[3][kJoinCols][128];
+    constexpr int kGroups = SPLIT ? 4 : 1;  // that share pieces
+    __shared__ float tops[4][128], sums[4][128], cols[SPLIT ? 3 : 1][kJoinCols][128];
     __shared__ int counts[8], first_cut;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const hs_prefill_t& a = g.a;
@@ -934,15 +937,15 @@ template <typename T> __global__ void __launch_bounds__(512) hs_prefill_join_ker
     const Start unit = start[first_cut];
     const int first = first_cut - 1, last = first + __syncthreads_count(inside && same(mine, unit));
     const Request r(a, unit.b);
-    const int quarter = blockIdx.y, c0 = kJoinCols * blockIdx.z;
-    const int row = t & 127, group = t >> 7;
+    const int row = t & 127, group = SPLIT ? t >> 7 : 0;
+    const int quarter = blockIdx.y, c0 = SPLIT ? kJoinCols * blockIdx.z : kJoinCols * (4 * blockIdx.z + (t >> 7));
     const int at = 512 * unit.qt + 128 * quarter + row;
     if (512 * unit.qt + 128 * quarter >= r.n) return;
     const bool live = at < r.n;
     float acc[kJoinCols] = {}, sum = 0.f, top = -INFINITY;
     if (live)
 #pragma unroll 2
-        for (int n = first + group; n <= last; n += 4) {
+        for (int n = first + group; n <= last; n += kGroups) {
             const Partial& q = parts[2 * n + (n == first)];
             const float ref = q.ref[quarter][row], l = q.sum[quarter][row];
             // without a branch, so that the loads of several pieces are in flight; a sum of 0: no key counted
@@ -956,24 +959,28 @@ template <typename T> __global__ void __launch_bounds__(512) hs_prefill_join_ker
 #pragma unroll
             for (int k = 0; k < kJoinCols; ++k) acc[k] = acc[k] * keep + (l == 0.f ? 0.f : w * o[k]);
         }
-    tops[group][row] = top;
-    sums[group][row] = sum;
-    if (group)
+    if (SPLIT) {
+        tops[group][row] = top;
+        sums[group][row] = sum;
+        if (group)
 #pragma unroll
-        for (int k = 0; k < kJoinCols; ++k) cols[group - 1][k][row] = acc[k];
-    __syncthreads();
+            for (int k = 0; k < kJoinCols; ++k) cols[group - 1][k][row] = acc[k];
+        __syncthreads();
+    }
     if (group || !live) return;
-    top = fmaxf(fmaxf(tops[0][row], tops[1][row]), fmaxf(tops[2][row], tops[3][row]));
-    const float ref = top == -INFINITY ? 0.f : top;
-    float w = tc::exp2_approx(tops[0][row] - ref);
-    sum *= w;
+    if (SPLIT) {
+        top = fmaxf(fmaxf(tops[0][row], tops[1][row]), fmaxf(tops[2][row], tops[3][row]));
+        const float ref = top == -INFINITY ? 0.f : top;
+        float w = tc::exp2_approx(tops[0][row] - ref);
+        sum *= w;
 #pragma unroll
-    for (int k = 0; k < kJoinCols; ++k) acc[k] *= w;
-    for (int n = 1; n < 4; ++n) {
-        w = tc::exp2_approx(tops[n][row] - ref);
-        sum += w * sums[n][row];
+        for (int k = 0; k < kJoinCols; ++k) acc[k] *= w;
+        for (int n = 1; n < 4; ++n) {
+            w = tc::exp2_approx(tops[n][row] - ref);
+            sum += w * sums[n][row];
 #pragma unroll
-        for (int k = 0; k < kJoinCols; ++k) acc[k] += w * cols[n - 1][k][row];
+            for (int k = 0; k < kJoinCols; ++k) acc[k] += w * cols[n - 1][k][row];
+        }
     }
     const bool some = sum > 0.f || sum != sum;
     const float inv = some ? 1.f / sum : 0.f;
@@ -1024,7 +1031,12 @@ template <typename T, bool E4M3> cudaError_t launch(const Args& g, int pairs, cu
     if (e != cudaSuccess) return e;
     if (pairs < 2 || !g.flat) return cudaSuccess;
     const int64_t units = (a.q_tokens / 512 + a.batch) * a.heads;  // at most
-    return launch_after(hs_prefill_join_kernel<T>, dim3((unsigned)(units < pairs - 1 ? units : pairs - 1), 4, HS_HEAD_DIM / kJoinCols), 512, 0, s, g, pairs);
+    const unsigned cut = (unsigned)(units < pairs - 1 ? units : pairs - 1);
+    // A block's time is latency, so many units (of few pieces each) take few blocks: 557 against 567 us
+    // for 8192 tokens with 32 heads; 512 queries over 16,384 rows 127 against 135 us with 16 heads (at most
+    // 32 units are cut), 83 and 83 with 8, but 69 against 66 with 4 and 83 against 75 with one.
+    if (cut >= 16) return launch_after(hs_prefill_join_kernel<T, false>, dim3(cut, 4, HS_HEAD_DIM / (4 * kJoinCols)), 512, 0, s, g, pairs);
+    return launch_after(hs_prefill_join_kernel<T, true>, dim3(cut, 4, HS_HEAD_DIM / kJoinCols), 512, 0, s, g, pairs);
 }
 
 }  // namespace
