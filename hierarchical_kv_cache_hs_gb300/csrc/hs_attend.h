@@ -13,7 +13,11 @@ constexpr int kTile = 64;  // rows a tile
 
 // A unit is a request, a position and a block of heads; its rows come in tiles, one at
 // least.  The tiles of all units form one line, which the workers (an SM, or a pair of
-// SMs) cut into equal pieces (flat), or whole units go to each.
+// SMs) cut into equal pieces (flat), or whole units go to each.  A unit's own time (its
+// queries, its sums' way out) counts as `cost` tiles before its first one, but for the
+// line's first unit: every piece has that once.  A cut inside it is a cut at the unit's
+// start, so a worker may get no piece; the one before a piece that starts inside a unit
+// always has one.
 struct Args {
     hs_attend_t a;
     int head_blocks;
@@ -21,20 +25,23 @@ struct Args {
     int units;         // at most HS_MAX_BATCH x HS_MAX_POSITIONS x HS_MAX_HEADS / 128, below 2^31
     int unit_tiles;    // tiles of a unit; with lengths, the most that one has
     int workers;
-    int64_t share;     // slots: tiles a worker, and how many workers have one more
+    int cost;
+    int64_t share;     // slots: tiles (and cost) a worker, and how many workers have one more
     int extra;
     int unit_share, unit_extra;  // units a worker, likewise
 
     // Fill in the cut: whole units, or pieces where those are `join` tiles' time shorter.
-    void cut(int most, int64_t rows, int join)
+    void cut(int most, int64_t rows, int join, int unit_cost)
     {
+        cost = unit_cost;
         unit_tiles = rows <= kTile ? 1 : (int)((rows + kTile - 1) / kTile);
         const int64_t total = (int64_t)units * unit_tiles;
         workers = (int)(total < most ? total : most);
         flat = (int64_t)((units + workers - 1) / workers) * unit_tiles > (total + workers - 1) / workers + join;
         if (!flat && workers > units) workers = units;
-        share = total / workers;
-        extra = (int)(total % workers);
+        const int64_t line = (int64_t)units * (unit_tiles + cost) - cost;
+        share = line / workers;
+        extra = (int)(line % workers);
         unit_share = units / workers;
         unit_extra = units % workers;
     }
@@ -80,42 +87,66 @@ __device__ __forceinline__ Piece find_piece(const Args& g, int i)
         return p;
     }
     if (a.slots) {
-        const long long lo = g.share * i + min(i, g.extra);
-        p.count = g.share + (i < g.extra);
-        p.unit = lo < 0x7fffffff ? (int)((unsigned)lo / (unsigned)g.unit_tiles) : (int)(lo / g.unit_tiles);
-        p.tile = (int)(lo - (long long)p.unit * g.unit_tiles);
+        const int per = g.unit_tiles + g.cost;
+        auto place = [&](int x, int& unit, int& tile) {
+            const long long at = g.cost + g.share * x + min(x, g.extra);
+            unit = at < 0x7fffffff ? (int)((unsigned)at / (unsigned)per) : (int)(at / per);
+            tile = max(0, (int)(at - (long long)unit * per) - g.cost);
+        };
+        int unit, tile;
+        place(i, p.unit, p.tile);
+        place(i + 1, unit, tile);
+        p.count = (long long)(unit - p.unit) * g.unit_tiles + tile - p.tile;
         return p;
     }
     long long total = 0;
     for (int b = lane; b < a.batch; b += 32) total += (long long)request_tiles(a, b) * upr;
     for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
     const long long n = total < g.workers ? total : g.workers;
-    const long long lo = i < n ? total * i / n : 0, hi = i < n ? total * (i + 1) / n : 0;
-    p.unit = 0;
-    p.tile = 0;
-    p.count = hi - lo;
-    long long before = 0;
+    p.unit = p.tile = 0;
+    p.count = 0;
+    if (i >= n) return p;
+    const long long line = total + (long long)g.cost * (g.units - 1);
+    const long long lo = g.cost + line * i / n, hi = g.cost + line * (i + 1) / n;
+    long long before = 0, from = 0, to = total;  // tiles before lo, before hi
     for (int b0 = 0; b0 < a.batch; b0 += 32) {
         const int b = b0 + lane;
-        const long long tiles = b < a.batch ? request_tiles(a, b) : 0;
-        long long incl = tiles * upr;
+        const long long tiles = b < a.batch ? request_tiles(a, b) : 0, per = tiles + g.cost;
+        const long long own = b < a.batch ? per * upr : 0;
+        long long incl = own;
         for (int o = 1; o < 32; o <<= 1) {
             const long long up = __shfl_up_sync(~0u, incl, o);
             if (lane >= o) incl += up;
         }
-        const long long at = before + incl - tiles * upr;  // where request b begins
-        const bool here = b < a.batch && lo >= at && lo < at + tiles * upr;
-        const unsigned who = __ballot_sync(~0u, here);
-        if (who) {
-            const int src = __ffs(who) - 1;
-            const int u = here ? b * upr + (int)((lo - at) / tiles) : 0;
-            const int t = here ? (int)((lo - at) % tiles) : 0;
-            p.unit = __shfl_sync(~0u, u, src);
-            p.tile = __shfl_sync(~0u, t, src);
-            break;
+        const long long at = before + incl - own;  // where request b begins
+        const unsigned at_lo = __ballot_sync(~0u, lo >= at && lo < at + own);
+        const unsigned at_hi = __ballot_sync(~0u, hi >= at && hi < at + own);
+        if (at_lo | at_hi) {
+            auto place = [&](long long x, int& unit, int& tile) {  // and the tiles before it
+                const int u = (int)((x - at) / per);
+                unit = b * upr + u;
+                tile = max(0, (int)(x - at - u * per) - g.cost);
+                return at - (long long)g.cost * upr * b + u * tiles + tile;
+            };
+            int unit = 0, tile = 0;
+            long long tiles_before = 0;
+            if (at_lo) {
+                const int src = __ffs(at_lo) - 1;
+                if (lane == src) tiles_before = place(lo, unit, tile);
+                p.unit = __shfl_sync(~0u, unit, src);
+                p.tile = __shfl_sync(~0u, tile, src);
+                from = __shfl_sync(~0u, tiles_before, src);
+            }
+            if (at_hi) {
+                const int src = __ffs(at_hi) - 1;
+                if (lane == src) tiles_before = place(hi, unit, tile);
+                to = __shfl_sync(~0u, tiles_before, src);
+                break;
+            }
         }
         before += __shfl_sync(~0u, incl, 31);
     }
+    p.count = to - from;
     return p;
 }
 
