@@ -622,12 +622,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_atte
 
 // Join the pieces of the units that several pairs worked on: block x takes the
 // x-th such unit (found at the first start of a piece inside it), one CTA's half
-// of its heads, COLS columns.  Four groups of 128 threads, one a lane, take every
-// fourth piece, in one pass; the order of the sums is fixed.
-template <typename T, int COLS>
+// of its heads.  Four groups of 128 threads, one a lane: with SPLIT they take every
+// fourth piece of COLS columns, else every piece of COLS columns each; in one pass,
+// and the order of the sums is fixed.
+template <typename T, int COLS, bool SPLIT>
 __global__ void __launch_bounds__(512) hs_attend_join_kernel(const __grid_constant__ Args g, int pairs)
 {
-    __shared__ float tops[4][128], sums[4][128], cols[3][COLS][128];
+    constexpr int kGroups = SPLIT ? 4 : 1;  // that share pieces
+    __shared__ float tops[4][128], sums[4][128], cols[SPLIT ? 3 : 1][COLS][128];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const hs_attend_t& a = g.a;
     const uint8_t* ws = static_cast<const uint8_t*>(a.workspace);
@@ -635,8 +637,8 @@ __global__ void __launch_bounds__(512) hs_attend_join_kernel(const __grid_consta
     int unit, first, last;
     if (!find_cut(reinterpret_cast<const Start*>(ws + kOffStart), pairs, blockIdx.x, unit, first, last)) return;
     const int t = threadIdx.x;
-    const int rank = blockIdx.y, c0 = COLS * blockIdx.z;
-    const int lane = t & 127, group = t >> 7, row = lane & 63, half = lane >> 6;
+    const int rank = blockIdx.y, c0 = SPLIT ? COLS * blockIdx.z : COLS * (4 * blockIdx.z + (t >> 7));
+    const int lane = t & 127, group = SPLIT ? t >> 7 : 0, row = lane & 63, half = lane >> 6;
     const int pos = unit / g.head_blocks, hb = unit - pos * g.head_blocks;
     const long long b = pos / a.positions;
     const int p = pos - (int)b * a.positions;
@@ -646,7 +648,7 @@ __global__ void __launch_bounds__(512) hs_attend_join_kernel(const __grid_consta
     float acc[COLS] = {}, sum = 0.f, top = -INFINITY;
     if (live)
 #pragma unroll(COLS == 4 ? 8 : 2)
-        for (int n = first + group; n <= last; n += 4) {
+        for (int n = first + group; n <= last; n += kGroups) {
             const Partial& q = parts[2 * n + (n == first)];
             const float ref = q.ref[rank][lane], l = q.sum[rank][lane];
             float o[COLS];
@@ -660,24 +662,28 @@ __global__ void __launch_bounds__(512) hs_attend_join_kernel(const __grid_consta
 #pragma unroll
             for (int k = 0; k < COLS; ++k) acc[k] = acc[k] * keep + (l == 0.f ? 0.f : w * o[k]);
         }
-    tops[group][lane] = top;
-    sums[group][lane] = sum;
-    if (group)
+    if (SPLIT) {
+        tops[group][lane] = top;
+        sums[group][lane] = sum;
+        if (group)
 #pragma unroll
-        for (int k = 0; k < COLS; ++k) cols[group - 1][k][lane] = acc[k];
-    __syncthreads();
+            for (int k = 0; k < COLS; ++k) cols[group - 1][k][lane] = acc[k];
+        __syncthreads();
+    }
     if (group || !live) return;
-    top = fmaxf(fmaxf(tops[0][lane], tops[1][lane]), fmaxf(tops[2][lane], tops[3][lane]));
-    const float base = top == -INFINITY ? 0.f : top;
-    float w = tc::exp2_approx(tops[0][lane] - base);
-    sum *= w;
+    if (SPLIT) {
+        top = fmaxf(fmaxf(tops[0][lane], tops[1][lane]), fmaxf(tops[2][lane], tops[3][lane]));
+        const float base = top == -INFINITY ? 0.f : top;
+        float w = tc::exp2_approx(tops[0][lane] - base);
+        sum *= w;
 #pragma unroll
-    for (int k = 0; k < COLS; ++k) acc[k] *= w;
-    for (int n = 1; n < 4; ++n) {
-        w = tc::exp2_approx(tops[n][lane] - base);
-        sum += w * sums[n][lane];
+        for (int k = 0; k < COLS; ++k) acc[k] *= w;
+        for (int n = 1; n < 4; ++n) {
+            w = tc::exp2_approx(tops[n][lane] - base);
+            sum += w * sums[n][lane];
 #pragma unroll
-        for (int k = 0; k < COLS; ++k) acc[k] += w * cols[n - 1][k][lane];
+            for (int k = 0; k < COLS; ++k) acc[k] += w * cols[n - 1][k][lane];
+        }
     }
     const bool some = sum > 0.f || sum != sum;
     const float inv = some ? 1.f / sum : 0.f;
@@ -698,11 +704,18 @@ template <typename T, bool E4M3> cudaError_t launch(const Args& g, cudaStream_t 
     hs_attend_kernel<T, E4M3><<<2 * g.workers, kThreads, kSmem, s>>>(g);
     e = cudaGetLastError();
     if (e != cudaSuccess || !g.flat || g.workers <= 1) return e;
-    // At most this many units are cut; few units take more blocks each, by narrower columns.
-    const int cut = g.units < g.workers - 1 ? g.units : g.workers - 1;
-    const int cols = cut * (g.a.heads > 64 ? 2 : 1) <= 8 ? 4 : 16;
-    return launch_after(cols == 4 ? hs_attend_join_kernel<T, 4> : hs_attend_join_kernel<T, 16>,
-                        dim3(cut, g.a.heads > 64 ? 2 : 1, 256 / cols), 512, s, g, g.workers);
+    // At most `cut` units are cut.  A block's time is latency, so many units, of few pieces each, take few
+    // blocks: requests of 2048 listed rows x 128 heads 75 against 86 us with 90 of them, 38 against 43 with
+    // 32, 30 against 32 with 16 (64 heads: 36 and 36 with 32, 28 against 26 with 16).  Of contexts one may
+    // hold most pieces, so they split them (24 ragged ones 45 against 49).  Few units take narrower columns:
+    // 4 ragged contexts (128 heads) 31 against 38, 8 of them 29 against 37 (8 equal ones 37 against 33); but
+    // 8 requests of 2048 listed rows 27 against 23, hence their lower limit.
+    const int cut = g.units < g.workers - 1 ? g.units : g.workers - 1, halves = g.a.heads > 64 ? 2 : 1;
+    if (g.a.slots && cut * halves >= 32)
+        return launch_after(hs_attend_join_kernel<T, 16, false>, dim3(cut, halves, 256 / 64), 512, s, g, g.workers);
+    if (cut * halves <= (g.a.slots ? 8 : 16))
+        return launch_after(hs_attend_join_kernel<T, 4, true>, dim3(cut, halves, 256 / 4), 512, s, g, g.workers);
+    return launch_after(hs_attend_join_kernel<T, 16, true>, dim3(cut, halves, 256 / 16), 512, s, g, g.workers);
 }
 
 }  // namespace
