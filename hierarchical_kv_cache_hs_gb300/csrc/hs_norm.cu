@@ -2,11 +2,14 @@
 // written in the input's type or as e4m3 with a scale for each group.
 //
 // A row's h stays in fp32 registers between the sum of squares and the scaling, so
-// each input is read once and each output written once; the pass is bound by HBM.
+// each input is read once and each output written once; the pass is bound by HBM:
+// 8192 x 4096 bf16 with a residual into e4m3 in groups of 128 takes 39.0 us, 6.05 TB/s
+// (0.89 of a copy's rate).
 // Rows whose pieces lie on 16-byte boundaries go through hs_norm_kernel: 16-byte
-// loads, a warp a row up to 128 pieces (576 16-bit channels are 72), else 8 or 16 warps.  Any other row (odd widths, odd alignments, groups that are not a power of
-// two of pieces) goes through hs_norm_any_kernel, element by element with the row in
-// shared memory.
+// loads, a warp a row up to 128 pieces (576 16-bit channels are 72), else 8 or 16 warps.
+// Any other row (odd widths, odd alignments, groups that are not a power of two of
+// pieces) goes through hs_norm_any_kernel, element by element with the row in shared
+// memory.
 #include "hs_ops.h"
 
 namespace {
@@ -297,6 +300,8 @@ template <typename T, bool E4M3> cudaError_t launch(const hs_norm_t& a, cudaStre
         }
         k<<<(unsigned)a.tokens, kWarps * 32, smem, s>>>(a);
     } else if (pieces <= 128) {
+        // A warp a row (residual, bf16): 1024 channels x 65,536 rows 81 us in 16 bits, 76 into e4m3, against 92
+        // and 117 with eight warps a row; 2048 channels (256 pieces) 84 and 99 against 79 and 79.
         const unsigned grid = (unsigned)((a.tokens + kWarps - 1) / kWarps);
         if (pieces <= 32)
             hs_norm_kernel<T, E4M3, 1, 1><<<grid, kWarps * 32, 0, s>>>(a);
@@ -305,13 +310,15 @@ template <typename T, bool E4M3> cudaError_t launch(const hs_norm_t& a, cudaStre
         else
             hs_norm_kernel<T, E4M3, 4, 1><<<grid, kWarps * 32, 0, s>>>(a);
     } else {
+        // Eight warps: 4096 channels x 16,384 rows into e4m3 73 us against 97 with 16, 8192 x 8192 78 against 91;
+        // 16 warps from there: 12288 x 5461 93 against 117, 16384 x 4096 83 against 102.
         const unsigned grid = (unsigned)a.tokens;
         if (pieces <= 256)
             hs_norm_kernel<T, E4M3, 1, 8><<<grid, 256, 0, s>>>(a);
         else if (pieces <= 512)
             hs_norm_kernel<T, E4M3, 2, 8><<<grid, 256, 0, s>>>(a);
         else if (pieces <= 1024)
-            hs_norm_kernel<T, E4M3, 2, 16><<<grid, 512, 0, s>>>(a);
+            hs_norm_kernel<T, E4M3, 4, 8><<<grid, 256, 0, s>>>(a);
         else if (pieces <= 2048)
             hs_norm_kernel<T, E4M3, 4, 16><<<grid, 512, 0, s>>>(a);
         else
