@@ -193,6 +193,45 @@ def test_attend_lengths(hs, P, H, lengths, dtype, e4m3):
     _check_attend(out, lse, _attend_ref(q, rows, picked, e4m3, SCALE), dtype)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("B,P,H,K", [
+    (40, 1, 128, 2048), (17, 1, 129, 3000), (33, 1, 33, 2000), (5, 2, 100, 2000), (3, 1, 64, 2500), (90, 1, 40, 1999),
+    (13, 1, 16, 3000), (7, 3, 20, 1501)])
+def test_attend_slots_pieces(hs, B, P, H, K, e4m3):
+    """Units cut in pieces and joined, many units and few; requests whose list is empty at its start, its end
+    or throughout (pieces without a row); a second run gives the same bits."""
+    q, rows, slots = _slot_case(B, P, H, K + 100, K, BF, e4m3, seed=B + H)
+    slots[0, :, :K - 70] = -1
+    slots[1, :, 70:] = -1
+    slots[2] = -1
+    out, lse = _attend(hs, q, rows, e4m3=e4m3, slots=slots)
+    _check_attend(out, lse, _attend_ref(q, rows, _picked(slots, K + 100), e4m3, SCALE), BF)
+    again, lse_again = _attend(hs, q, rows, e4m3=e4m3, slots=slots)
+    assert torch.equal(out, again) and torch.equal(lse, lse_again)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("P,H,lengths", [
+    (1, 128, [9000, 1, 0, 63, 64, 65, 4000]), (1, 64, [6000, 1, 5001, 77]), (2, 130, [5000] * 3 + [1]),
+    (1, 16, [12000, 3, 0, 700, 2500]), (1, 128, [1] * 40 + [5000]), (1, 40, [5000] + [1] * 40),
+    (3, 24, [3000, 2, 1, 0] * 6), (1, 100, [0, 0, 0]), (1, 128, [4096] * 20)])
+def test_attend_lengths_pieces(hs, P, H, lengths, e4m3):
+    """Contexts of very unequal lengths, which the pieces' cut weighs with each unit's own time."""
+    g = _gen(H + len(lengths))
+    B, N = len(lengths), max(lengths + [4000])
+    q = _randn(g, B, P, H, 576, dtype=BF)
+    rows = _randn(g, B, N, 576, dtype=BF)
+    for b, n in enumerate(lengths):
+        rows[b, n:] = NAN
+    rows = _pack8(rows) if e4m3 else rows
+    device = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    out, lse = _attend(hs, q, rows, e4m3=e4m3, lengths=device)
+    picked = [[torch.arange(max(0, n - P + 1 + p), device="cuda") for p in range(P)] for n in lengths]
+    _check_attend(out, lse, _attend_ref(q, rows, picked, e4m3, SCALE), BF)
+    again, lse_again = _attend(hs, q, rows, e4m3=e4m3, lengths=device)
+    assert torch.equal(out, again) and torch.equal(lse, lse_again)
+
+
 def test_attend_lengths_clamped(hs):
     g = _gen(3)
     q, rows = _randn(g, 3, 1, 8, 576), _randn(g, 3, 100, 576)
@@ -421,6 +460,19 @@ def test_prefill_replays(hs):
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("H,nq,nk", [
+    (16, [520, 3], [2500, 700]), (20, [700], [5000]), (8, [512], [4000]), (3, [600], [2100]), (1, [515, 513, 1], [4000, 513, 900]),
+    (16, [1100], [1100]), (24, [300, 0, 40, 513], [600, 5, 10, 2000])])
+def test_prefill_pieces(hs, H, nq, nk, e4m3):
+    """Sizes whose units are cut and joined, many units and few; a second run gives the same bits."""
+    q, rows, w_uk, w_uv = _prompt_case(nq, nk, H, BF, e4m3, seed=H + sum(nk))
+    out, lse = _prefill(hs, q, rows, w_uk, w_uv, nq, nk, e4m3)
+    _check_prefill(out, lse, q, rows, w_uk, w_uv, nq, nk, e4m3)
+    again, lse_again = _prefill(hs, q, rows, w_uk, w_uv, nq, nk, e4m3)
+    assert torch.equal(out, again) and torch.equal(lse, lse_again)
 
 
 # ---- norm ------------------------------------------------------------------------------
