@@ -1067,9 +1067,15 @@ cudaError_t hs_launch_prefill(const hs_prefill_t& a, cudaStream_t s)
     Args g;
     g.a = a;
     g.blocks = (a.k_tokens + 255) / 256 * 2;
-    // Short prompts: no unit has more than a few blocks, and a join costs more (243 tokens, 16 heads: 25 against
-    // 32 us with pieces and a join).
-    g.flat = (a.k_tokens + 127) / 128 > 4;
+    // Pieces where whole units (a pair's are consecutive ones) would take longer by more than the join, which
+    // takes about 9 blocks' time, were all tokens one request's; a unit of 512 queries earlier sees 4 blocks fewer.
+    // 4, 16 and 64 heads, whole units against pieces: 768 tokens 29 and 31, 29 and 35, 54 and 62 us; 1024 tokens
+    // 35 and 32, 37 and 39, 62 and 71; 2048 tokens 49 and 38, 57 and 59, 134 and 136.
+    const int64_t tiles = a.q_tokens > 512 ? (a.q_tokens + 511) / 512 : 1, units = (tiles + a.batch - 1) * a.heads;
+    const int64_t longest = ((a.q_tokens > a.k_tokens ? a.q_tokens : a.k_tokens) + 127) / 128 + kUnitCost;
+    auto last = [&](int64_t n) { return n * longest - 2 * n * (n - 1); };  // a head's last n units
+    const int64_t each = (units + pairs - 1) / pairs;
+    g.flat = each / tiles * last(tiles) + last(each % tiles) > units * last(tiles) / (tiles * pairs) + 9;
     g.keys = static_cast<uint8_t*>(a.workspace) + kOffKeys;
     g.values = g.keys + (size_t)g.blocks * a.heads * kBlock;
     g.rope = g.values + (size_t)g.blocks * a.heads * kBlock;
