@@ -42,7 +42,10 @@ template <int NH> struct Aux {
     Piece piece;
     uint16_t valid[4][4];          // by tile, four deep; one bit a row
     alignas(8) float scale[4][kTile];
-    int8_t q_up[2][NH];            // power of two on a bf16 query held in fp16, by the parity of the piece
+    // Power of two on a bf16 query held in fp16, by the piece, three deep: piece n + 3's is written once the
+    // products with keys of piece n + 2 are done.  The last of those waits for the softmax's arrival two tiles
+    // earlier, which follows its read of piece n's power even where a piece has one tile (two deep, it need not).
+    int8_t q_up[3][NH];
     float top[2][4][NH];           // maxima by warp, by the parity of the tile
     float red[4][NH];              // by warp: sums, and factors on O
     float inv[NH];                 // of the sums at a piece's end
@@ -91,7 +94,7 @@ template <typename T, int NH> __device__ void bring(const Args& g, uint32_t sbas
             if constexpr (HsType<T>::is_bf16) {
                 for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
                 const int up = power_up(top);
-                if (lane == 0) x->q_up[pieces & 1][h] = (int8_t)up;
+                if (lane == 0) x->q_up[pieces % 3][h] = (int8_t)up;
 #pragma unroll
                 for (int i = 0; i < 3; ++i) v[i] = bf16_to_half(v[i], power_of_two(up));
             }
@@ -275,7 +278,7 @@ template <typename T, int NH> __device__ void soften(const Args& g, uint32_t sba
                 if (t == walk.t0)
 #pragma unroll
                     for (int i = 0; i < 2 * NG; ++i)
-                        c[i] *= power_of_two(-x->q_up[pieces & 1][8 * (i >> 1) + c0 + (i & 1)]);
+                        c[i] *= power_of_two(-x->q_up[pieces % 3][8 * (i >> 1) + c0 + (i & 1)]);
             uint32_t r[NH / 2];
             load_scores<NH>(tmem + Layout<NH>::col_s + NH * s, r);
             const unsigned valid = x->valid[m][warp];

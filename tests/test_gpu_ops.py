@@ -294,6 +294,18 @@ def test_attend_row_scales_of_many_sizes(hs, dtype):
     _check_attend(out, lse, _attend_ref(q, rows, _picked(slots, 600), True, SCALE), dtype)
 
 
+@pytest.mark.parametrize("H", [16, 32])
+@pytest.mark.parametrize("B,P,K", [(300, 3, 64), (1200, 1, 5), (400, 2, 100)])
+def test_attend_short_units_of_unlike_queries(hs, B, P, K, H):
+    """Many units of one tile (and of two) a worker, whose bf16 queries have unlike magnitudes: each is
+    held in fp16 by a power of two of its own, which the next units' must not replace early."""
+    q, rows, slots = _slot_case(B, P, H, K + 10, K, BF, True, seed=B + K + H)
+    power = torch.randint(0, 6, (B, P, 1, 1), generator=_gen(B), device="cuda") * -4
+    q = q * torch.exp2(power.float()).to(BF)
+    out, lse = _attend(hs, q, rows, e4m3=True, slots=slots)
+    _check_attend(out, lse, _attend_ref(q, rows, _picked(slots, K + 10), True, SCALE), BF)
+
+
 def test_attend_nan_and_inf_propagate(hs):
     q, rows, slots = _slot_case(3, 1, 16, 300, 200, BF, False, seed=8)
     q[0, 0, 3] = NAN
