@@ -138,7 +138,7 @@ __device__ void bring_keys(const Args& g, uint32_t sbase, Aux* x, uint32_t rank,
                 }
                 if (jt >= kKStages) wait(tc::smem_addr(&x->kfree[stage]), reuse, &x->dead, error);
                 x->scale[m][mine] = sc;
-                x->log_scale[m][mine] = __float2half(log2f(fabsf(sc)));
+                x->log_scale[m][mine] = __float2half(fmaxf(log2f(fabsf(sc)), kLeastLogScale));
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
                     const int tok = n * 8 + (lane >> 2), r0 = tok & 7;

@@ -292,6 +292,11 @@ __device__ __forceinline__ uint4 bf16_to_half(const uint4& v, float f)
     return make_uint4(two(v.x), two(v.y), two(v.z), two(v.w));
 }
 
+// A row of 8 bits moves the running reference by its score and the log2 of its scale, so that
+// weights times scales stay in fp16's range.  Scales below 2^-100, 0 among them, count as that:
+// beside rows that score far below, such a row's weight then stays at 2^108 or less.
+constexpr float kLeastLogScale = -100.f;
+
 // The x-th unit that several workers worked on, found at the first start of a piece inside
 // it: workers first..last have its pieces (false: there is no such unit).  The whole block
 // calls it, at least 256 threads for up to 256 workers.

@@ -284,7 +284,8 @@ template <typename T, int NH> __device__ void soften(const Args& g, uint32_t sba
             const unsigned valid = x->valid[m][warp];
             const bool ok0 = valid >> r0 & 1, ok1 = valid >> (r0 + 8) & 1;
             const float w0 = x->scale[m][16 * warp + r0], w1 = x->scale[m][16 * warp + r0 + 8];
-            const float lw0 = tc::log2_approx(fabsf(w0)), lw1 = tc::log2_approx(fabsf(w1));  // only move the reference
+            // only move the reference
+            const float lw0 = fmaxf(tc::log2_approx(fabsf(w0)), kLeastLogScale), lw1 = fmaxf(tc::log2_approx(fabsf(w1)), kLeastLogScale);
             float v[NH / 2], top[2 * NG];
 #pragma unroll
             for (int i = 0; i < 2 * NG; ++i) {  // column i: registers 4 (i / 2) + i % 2 and + 2

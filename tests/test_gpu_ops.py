@@ -306,6 +306,34 @@ def test_attend_short_units_of_unlike_queries(hs, B, P, K, H):
     _check_attend(out, lse, _attend_ref(q, rows, _picked(slots, K + 10), True, SCALE), BF)
 
 
+@pytest.mark.parametrize("dtype", [BF, HALF])
+@pytest.mark.parametrize("H", [16, 64])
+@pytest.mark.parametrize("beta", [1.0, 2.5, 6.0])
+@pytest.mark.parametrize("least", [0.0, 2.0 ** -125])
+@pytest.mark.parametrize("N,small", [(40, [3]), (40, [39]), (300, [0, 1]), (300, [299]), (300, [100, 130]),
+                                     (6000, [5]), (6000, [3000]), (6000, [5999]), (64, list(range(64)))])
+def test_attend_rows_of_no_scale_beside_low_scores(hs, N, small, least, beta, H, dtype):
+    """8-bit rows of scale 0 (what the norm writes for zeros) or nearly 0 score 0.  The other rows score about
+    -60 beta, in powers of two, so those take all the weight, in whichever tile or piece they come."""
+    g = _gen(N + H)
+    u = torch.randn((2, 1, 1, 576), generator=g, device="cuda")
+    q = (u * (1 + 0.01 * torch.randn((2, 1, H, 1), generator=g, device="cuda"))).to(dtype)
+    rows = _pack8(-beta * u[:, 0] + 0.1 * torch.randn((2, N, 576), generator=g, device="cuda"))
+    rows[:, small, 576:580] = torch.full((1,), least, device="cuda").view(torch.uint8)
+    if least == 0:
+        rows[:, small, :576] = 0
+    out, lse = _attend(hs, q, rows, e4m3=True, lengths=torch.tensor([N, N], dtype=torch.int32, device="cuda"))
+    every = [torch.arange(N, device="cuda")]
+    o, want_lse, mean_abs, reach = _attend_ref(q, rows, [every, every], True, SCALE)
+    # as in _check_attend, and half of the least step that the type has
+    half, step = torch.finfo(dtype).eps / 2, torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps
+    score = 576 * 2.0 ** -23 * reach + 2.0 ** -18
+    tol = half * o.abs() + (half + 2 * score) * mean_abs + step / 2 + 1e-30
+    assert torch.isfinite(out).all() and ((out.double() - o).abs() <= tol).all()
+    # a reference of 128 and more has steps of 2^-17, in the exponent and in the logarithm
+    assert ((lse.double() - want_lse).abs() <= score.squeeze(-1) + 2.0 ** -16 + 2.0 ** -21 * want_lse.abs()).all()
+
+
 def test_attend_nan_and_inf_propagate(hs):
     q, rows, slots = _slot_case(3, 1, 16, 300, 200, BF, False, seed=8)
     q[0, 0, 3] = NAN
