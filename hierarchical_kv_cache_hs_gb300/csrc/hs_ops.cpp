@@ -124,7 +124,9 @@ int hs_rms_norm(const hs_norm_t* args, hs_stream_t stream)
                          (a.scales && a.scales_stride < groups)))
         return HS_ERR_ARG;
     if (a.tokens == 0) return HS_OK;
-    return result(hs_launch_norm(a, reinterpret_cast<cudaStream_t>(stream)));
+    hs_norm_t b = a;
+    b.group = hs_norm_group(a.dim, a.carry, a.group);
+    return result(hs_launch_norm(b, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -11,6 +11,10 @@
 
 #include "hs.h"
 
+// The channels that share a scale of hs_rms_norm; 0: the whole row.  A group that holds the whole row is
+// that, so that a kernel's group indices times the group stay below twice the widest row.
+inline int hs_norm_group(int dim, int carry, int group) { return group >= dim + carry ? 0 : group; }
+
 // hs_ops.cpp has checked the arguments; these launch.
 cudaError_t hs_launch_attend(const hs_attend_t& a, cudaStream_t s);
 cudaError_t hs_launch_prefill(const hs_prefill_t& a, cudaStream_t s);

@@ -735,7 +735,8 @@ int hs_latent_prefill(const hs_prefill_t* args, hs_stream_t stream);
  *   h = x[:dim] + residual;  residual_out = h
  *   y = [h / sqrt(mean(h^2) + eps) * weight ; x[dim : dim + carry]]
  * written as `dtype` (scales NULL), or as e4m3 with a scale for each `group`
- * channels of y (0: one for the whole row; the last group may be short):
+ * channels of y (0, or the row's width and more: one for the whole row; the last
+ * group may be short):
  *   scale = max|y| / 448 over the group,  out = e4m3(y / scale)
  * (all zeros: scale 0, out 0; a NaN makes its group's scale NaN).  h stays in
  * fp32 between the sum and the norm.  With carry = 64, dim = 512 and out,

@@ -580,6 +580,22 @@ def test_norm_e4m3(hs, n, d, carry, dtype, group):
     assert (got.abs().view(n, width) <= each * 448).all()
 
 
+@pytest.mark.parametrize("more", [0, 1, 2 ** 31])
+@pytest.mark.parametrize("width,carry", [(64, 0), (577, 65), (1000, 24), (1024, 0), (7000, 3), (8192, 64), (12739, 0)])
+def test_norm_e4m3_group_of_the_whole_row(hs, width, carry, more):
+    """A group as wide as the row, or wider by any amount, is one scale a row."""
+    g = _gen(width)
+    x, w = _randn(g, 40, width), _randn(g, width - carry)
+    got = []
+    for group in (0, min(width + more, 2 ** 31 - 1)):
+        out = torch.full((40, width), 255, dtype=torch.uint8, device="cuda")
+        scales = torch.full((40, 2), NAN, device="cuda")
+        hs.hs_rms_norm(x, w, out, 1e-6, carry=carry, scales=scales[:, :1], group=group)
+        assert scales[:, 1].isnan().all()
+        got.append((out, scales[:, 0]))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
 def test_norm_writes_cache_rows(hs):
     """The 8-bit row form, read back by the attention."""
     g = _gen(1)

@@ -59,3 +59,44 @@ def test_resolve_shared_memory_layout(tmp_path):
     assert r.returncode == 0, r.stderr
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+
+
+NORM_GROUPS = r"""
+#include <cstdint>
+#include <cstdio>
+#include "hs_ops.h"
+
+int main()
+{
+    const int widths[] = {1, 2, 63, 576, 769, 6144, 6145, 12739, HS_MAX_NORM_DIM};
+    const int groups[] = {0, 1, 16, 127, 128, 1000, 8191, HS_MAX_NORM_DIM - 1, HS_MAX_NORM_DIM, HS_MAX_NORM_DIM + 1,
+                          1 << 26, 1 << 28, 1 << 29, 1 << 30, INT32_MAX};
+    for (int width : widths)
+        for (int carry = 0; carry < width; carry += 1 + width / 3)
+            for (int group : groups) {
+                const int g = hs_norm_group(width - carry, carry, group);
+                // one scale a row, or the group itself: the same groups as asked for
+                const int64_t asked = group ? ((int64_t)width + group - 1) / group : 1;
+                const int64_t got = g ? ((int64_t)width + g - 1) / g : 1;
+                if (got != asked || (g && g != group)) { printf("width %d group %d: %d\n", width, group, g); return 1; }
+                // up to 32 warps take a group each in turn: the first product past the row's end
+                if ((int64_t)(got + 31) * g > (int64_t)33 * HS_MAX_NORM_DIM) { printf("width %d group %d\n", width, group); return 1; }
+            }
+    printf("ok\n");
+    return 0;
+}
+"""
+
+
+def test_norm_group_indices_stay_small(tmp_path):
+    cxx = shutil.which("g++")
+    if cxx is None or not os.path.exists(os.path.join(CUDA_INC, "cuda_runtime.h")):
+        pytest.skip("needs g++ and the CUDA headers")
+    src = tmp_path / "groups.cpp"
+    exe = tmp_path / "groups"
+    src.write_text(NORM_GROUPS)
+    r = subprocess.run([cxx, "-std=c++17", "-O1", "-I", CSRC, "-I", INCLUDE, "-I", CUDA_INC,
+                        str(src), "-o", str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
