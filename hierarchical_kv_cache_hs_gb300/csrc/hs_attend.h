@@ -270,11 +270,12 @@ __device__ __forceinline__ void store_wide(const uint4& v, uint32_t dst, int c0,
 
 // With 8-bit rows the products are in fp16; a bf16 query is scaled by a power of two that
 // takes its largest magnitude `top` to [2^13, 2^14), so that what is 2^-28 of it or more
-// stays exact.  The power; zeros and infinities stay as they are.
+// stays exact.  The power, at most 126 (a top below 2^-113 then stays lower, and every bf16
+// from 2^-133 up exact); infinities stay as they are.
 __device__ __forceinline__ int power_up(float top)
 {
     const int ex = (int)(__float_as_uint(top) >> 23);
-    return ex == 0 || ex == 255 ? 0 : min(max(140 - ex, -100), 100);
+    return ex == 255 ? 0 : min(140 - ex, 126);
 }
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 __device__ __forceinline__ float largest_bf16(const uint4& v)

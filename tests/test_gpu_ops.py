@@ -334,6 +334,18 @@ def test_attend_rows_of_no_scale_beside_low_scores(hs, N, small, least, beta, H,
     assert ((lse.double() - want_lse).abs() <= score.squeeze(-1) + 2.0 ** -16 + 2.0 ** -21 * want_lse.abs()).all()
 
 
+@pytest.mark.parametrize("power", [-130, -124, -110, -88, -60, 60, 100, 115, 118])
+@pytest.mark.parametrize("H", [16, 64])
+def test_attend_bf16_queries_of_any_magnitude(hs, H, power):
+    """8-bit rows with bf16 queries from the type's smallest values to its largest, under a scale that makes
+    the scores ordinary ones."""
+    q, rows, slots = _slot_case(2, 1, H, 300, 200, BF, True, seed=13)
+    q = (q.double() * 2.0 ** power).to(BF)
+    scale = SCALE * 2.0 ** min(-power, 126)
+    out, lse = _attend(hs, q, rows, e4m3=True, slots=slots, scale=scale)
+    _check_attend(out, lse, _attend_ref(q, rows, _picked(slots, 300), True, scale), BF)
+
+
 def test_attend_nan_and_inf_propagate(hs):
     q, rows, slots = _slot_case(3, 1, 16, 300, 200, BF, False, seed=8)
     q[0, 0, 3] = NAN
