@@ -737,7 +737,7 @@ int hs_latent_prefill(const hs_prefill_t* args, hs_stream_t stream);
  * written as `dtype` (scales NULL), or as e4m3 with a scale for each `group`
  * channels of y (0, or the row's width and more: one for the whole row; the last
  * group may be short):
- *   scale = max|y| / 448 over the group,  out = e4m3(y / scale)
+ *   scale = max|y| / 448 over the group,  out = e4m3(y / scale), the quotient in fp32
  * (all zeros: scale 0, out 0; a NaN makes its group's scale NaN).  h stays in
  * fp32 between the sum and the norm.  With carry = 64, dim = 512 and out,
  * scales pointing at bytes 0 and HS_ROW8_SCALE of 592-byte rows, it writes

@@ -608,6 +608,23 @@ def test_norm_e4m3_group_of_the_whole_row(hs, width, carry, more):
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
 
 
+@pytest.mark.parametrize("group", [0, 16, 100])
+@pytest.mark.parametrize("dtype", [BF, HALF, torch.float32])
+@pytest.mark.parametrize("n,d,carry", [(2000, 512, 512), (2000, 512, 511), (500, 1024, 1024), (300, 1000, 1001),
+                                       (100, 4096, 4001), (50, 5000, 7001)])
+def test_norm_e4m3_divides_by_the_scale(hs, n, d, carry, dtype, group):
+    """Carried channels, whose values are exact: e4m3 of the fp32 quotient by the scale that is written, bit for bit."""
+    g = _gen(n + d + carry)
+    x, w = _randn(g, n, d + carry, dtype=dtype), _randn(g, d, dtype=dtype)
+    width = d + carry
+    out = torch.empty((n, width), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((n, -(-width // group) if group else 1), device="cuda")
+    hs.hs_rms_norm(x, w, out, 1e-6, carry=carry, scales=scales, group=group)
+    each = scales.repeat_interleave(group or width, 1)[:, :width]
+    want = (x.float() / each).to(torch.float8_e4m3fn).view(torch.uint8)
+    assert torch.equal(out[:, d:], want[:, d:])
+
+
 def test_norm_writes_cache_rows(hs):
     """The 8-bit row form, read back by the attention."""
     g = _gen(1)
