@@ -13,6 +13,9 @@ bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0;
 // Only strides that are used (more than one entry along the axis) must fit.
 bool stride_ok(int64_t stride, int64_t count) { return count <= 1 || (stride >= 0 && stride % 8 == 0); }
 
+// The same of an output: two of its rows must not lie on one another.
+bool out_stride_ok(int64_t stride, int64_t count, int channels) { return stride_ok(stride, count) && (count <= 1 || stride >= channels); }
+
 bool is_16bit(int dtype) { return dtype == HS_TYPE_BF16 || dtype == HS_TYPE_FP16; }
 
 int row_bytes(int format)
@@ -57,7 +60,7 @@ int hs_latent_attend(const hs_attend_t* args, hs_stream_t stream)
         return HS_ERR_ARG;
     const int64_t n[3] = {a.batch, a.positions, a.heads};
     for (int i = 0; i < 3; ++i)
-        if (!stride_ok(a.q_stride[i], n[i]) || !stride_ok(a.out_stride[i], n[i])) return HS_ERR_ARG;
+        if (!stride_ok(a.q_stride[i], n[i]) || !out_stride_ok(a.out_stride[i], n[i], HS_LATENT_DIM)) return HS_ERR_ARG;
     if (a.n_rows > 1 && (a.row_stride < row_bytes(a.row_format) || a.row_stride % 16)) return HS_ERR_ARG;
     if (a.batch > 1 && (a.request_stride < 0 || a.request_stride % 16)) return HS_ERR_ARG;
     if (a.slots && ((a.batch > 1 && a.slots_stride[0] < 0) || (a.positions > 1 && a.slots_stride[1] < 0)))
@@ -93,7 +96,7 @@ int hs_latent_prefill(const hs_prefill_t* args, hs_stream_t stream)
         return HS_ERR_ARG;
     const int64_t n[2] = {a.q_tokens, a.heads};
     for (int i = 0; i < 2; ++i)
-        if (!stride_ok(a.q_stride[i], n[i]) || !stride_ok(a.out_stride[i], n[i])) return HS_ERR_ARG;
+        if (!stride_ok(a.q_stride[i], n[i]) || !out_stride_ok(a.out_stride[i], n[i], HS_HEAD_DIM)) return HS_ERR_ARG;
     if (a.k_tokens > 1 && (a.row_stride < row_bytes(a.row_format) || a.row_stride % 16)) return HS_ERR_ARG;
     const size_t need = hs_prefill_workspace_bytes(a.k_tokens, a.heads);
     if (a.workspace_bytes < need || (need > 0 && !a.workspace)) return HS_ERR_ARG;

@@ -648,7 +648,8 @@ int hs_resolve_noalloc(int batch, int ctx_len, int row_bytes, int buffer_slots, 
  * -inf; rows that are not allowed may hold anything, NaN included.
  *   q    [batch][positions][heads][576], out [batch][positions][heads][512]
  *        of `dtype`; channels contiguous, other strides in elements, multiples
- *        of 8; both 16-byte aligned
+ *        of 8 (out's 512 at least, so that its rows are apart); both 16-byte
+ *        aligned
  *   rows n_rows rows a request, row_stride and request_stride in bytes,
  *        multiples of 16; 16-byte aligned (a handle's hs_device_buffer:
  *        n_rows = S + T, row_stride = R, request_stride = (S + T) * R)
@@ -699,11 +700,11 @@ int hs_latent_attend(const hs_attend_t* args, hs_stream_t stream);
  *   w_uk, w_uv [heads][128][512], contiguous
  *   out   [q_tokens][heads][128]; lse fp32 [q_tokens][heads] or NULL
  *   rows  [k_tokens] rows of row_stride bytes
- * with types, alignments and strides as in hs_latent_attend.  The keys' and
- * values' expanded channels, the rotary channels of 8-bit rows and the softmax
- * weights are rounded to `dtype`.  Rows that a query does not see may hold
- * anything; a value that is not finite once rounded makes the output NaN of
- * every query that sees its row.
+ * with types, alignments and strides as in hs_latent_attend (out's 128 at
+ * least).  The keys' and values' expanded channels, the rotary channels of
+ * 8-bit rows and the softmax weights are rounded to `dtype`.  Rows that a query
+ * does not see may hold anything; a value that is not finite once rounded makes
+ * the output NaN of every query that sees its row.
  * Source: no passage (as hs_latent_attend).
  */
 typedef struct {

@@ -41,6 +41,11 @@ def test_attend_refuses(hs, over):
     assert _attend(hs, **over) == hs.HS_ERR_ARG
 
 
+@pytest.mark.parametrize("strides", [(0, 0, 512), (16 * 512, 0, 0), (504, 0, 512), (16 * 512, 16 * 512, 504)])
+def test_attend_refuses_outputs_on_one_another(hs, strides):
+    assert _attend(hs, out_stride=strides) == hs.HS_ERR_ARG
+
+
 def test_attend_limits(hs):
     assert _attend(hs, batch=hs.HS_MAX_BATCH + 1) == hs.HS_ERR_LIMIT
     assert _attend(hs, heads=hs.HS_MAX_HEADS + 1) == hs.HS_ERR_LIMIT
@@ -71,6 +76,11 @@ def _prefill(hs, **over):
     dict(workspace=None), dict(workspace=(1 << 27) + 8), dict(workspace_bytes=100)])
 def test_prefill_refuses(hs, over):
     assert _prefill(hs, **over) == hs.HS_ERR_ARG
+
+
+@pytest.mark.parametrize("strides", [(0, 128), (16 * 128, 0), (120, 128), (16 * 128, 120)])
+def test_prefill_refuses_outputs_on_one_another(hs, strides):
+    assert _prefill(hs, out_stride=strides) == hs.HS_ERR_ARG
 
 
 def test_prefill_limits_and_nothing_to_do(hs):
