@@ -719,10 +719,10 @@ template <typename T, bool E4M3> cudaError_t launch(const Args& g, cudaStream_t 
     // 8 requests of 2048 listed rows 27 against 23, hence their lower limit.
     const int cut = g.units < g.workers - 1 ? g.units : g.workers - 1, halves = g.a.heads > 64 ? 2 : 1;
     if (g.a.slots && cut * halves >= 32)
-        return launch_after(hs_attend_join_kernel<T, 16, false>, dim3(cut, halves, 256 / 64), 512, s, g, g.workers);
+        return launch_after(hs_attend_join_kernel<T, 16, false>, dim3(cut, halves, 256 / 64), 512, 0, s, g, g.workers);
     if (cut * halves <= (g.a.slots ? 8 : 16))
-        return launch_after(hs_attend_join_kernel<T, 4, true>, dim3(cut, halves, 256 / 4), 512, s, g, g.workers);
-    return launch_after(hs_attend_join_kernel<T, 16, true>, dim3(cut, halves, 256 / 16), 512, s, g, g.workers);
+        return launch_after(hs_attend_join_kernel<T, 4, true>, dim3(cut, halves, 256 / 4), 512, 0, s, g, g.workers);
+    return launch_after(hs_attend_join_kernel<T, 16, true>, dim3(cut, halves, 256 / 16), 512, 0, s, g, g.workers);
 }
 
 }  // namespace

@@ -9,6 +9,8 @@
 
 namespace hs_attn {
 
+using tc::wait;
+
 constexpr int kTile = 64;  // rows a tile
 
 // A unit is a request, a position and a block of heads; its rows come in tiles, one at
@@ -221,33 +223,6 @@ __device__ __forceinline__ void prefetch_rows(const uint8_t* rows, int64_t row_s
     }
 }
 
-// Bounded wait: on a timeout the CTA is marked dead and every later wait returns at once.
-__device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, int* dead, int* error)
-{
-    if (tc::mbar_try(bar, parity)) return;
-    const long long t0 = clock64();
-    while (!tc::mbar_try(bar, parity)) {
-        if (*(volatile int*)dead) return;
-        if (clock64() - t0 > tc::kWaitClocks) {
-            *(volatile int*)dead = 1;
-            atomicExch(error, 1);
-            return;
-        }
-    }
-}
-
-template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
-template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b)
-{
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b)
-{
-    const __half2 v = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-
 // Four e4m3 values as two pairs of fp16, which holds each of them (and NaN).
 __device__ __forceinline__ void widen(uint32_t v, uint32_t& lo, uint32_t& hi)
 {
@@ -338,20 +313,5 @@ cudaError_t launch_pair(const hs_attend_t& a, int sms, cudaStream_t s);
 cudaError_t launch_narrow(const hs_attend_t& a, int sms, cudaStream_t s);
 size_t pair_workspace(int64_t units, int64_t tiles);
 size_t narrow_workspace(int64_t units, int64_t tiles, int heads);
-
-template <typename... Params, typename... Values>
-cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t s, Values... values)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = threads;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, values...);
-}
 
 }  // namespace hs_attn

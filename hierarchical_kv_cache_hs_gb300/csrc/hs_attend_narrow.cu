@@ -533,7 +533,7 @@ template <typename T, int NH> cudaError_t launch(const Args& g, cudaStream_t s)
     e = cudaGetLastError();
     if (e != cudaSuccess || !g.flat || g.workers <= 1) return e;
     const int cut = g.units < g.workers - 1 ? g.units : g.workers - 1;  // at most this many units are cut
-    return launch_after(hs_attend_narrow_join_kernel<T, NH>, dim3(cut, (g.a.heads + kJoinHeads - 1) / kJoinHeads), 512, s, g, g.workers);
+    return launch_after(hs_attend_narrow_join_kernel<T, NH>, dim3(cut, (g.a.heads + kJoinHeads - 1) / kJoinHeads), 512, 0, s, g, g.workers);
 }
 
 }  // namespace

@@ -22,12 +22,12 @@
 // Keys, values and softmax weights are rounded to 16 bits before their products, as the
 // tensor core takes them: bf16 results are 0.0026 to 0.0028 off 64 bits (relative, in
 // norm) where one rounding at the end gives 0.0017; sums and statistics are fp32.
-#include <type_traits>
-
 #include "hs_ops.h"
 #include "hs_tc.h"
 
 namespace {
+
+using tc::wait;
 
 constexpr int kMaxPairs = 76;
 
@@ -61,17 +61,6 @@ struct Args {
     int flat;  // 1: equal pieces of the line of blocks; 0: whole units
 };
 
-template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
-template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b)
-{
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b)
-{
-    const __half2 v = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
 // A NaN or an infinity among two values of T.
 template <typename T> __device__ __forceinline__ bool not_finite(uint32_t v)
 {
@@ -86,21 +75,6 @@ template <typename T> __device__ __forceinline__ uint32_t widen2(uint32_t v)
     if constexpr (!HsType<T>::is_bf16) return h;
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
     return pack2<T>(f.x, f.y);
-}
-
-// Bounded wait: on a timeout the CTA is marked dead and every later wait returns at once.
-__device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, int* dead, int* error)
-{
-    if (tc::mbar_try(bar, parity)) return;
-    const long long t0 = clock64();
-    while (!tc::mbar_try(bar, parity)) {
-        if (*(volatile int*)dead) return;
-        if (clock64() - t0 > tc::kWaitClocks) {
-            *(volatile int*)dead = 1;
-            atomicExch(error, 1);
-            return;
-        }
-    }
 }
 
 // ---- (1) expansion -----------------------------------------------------------------
@@ -1000,22 +974,6 @@ __global__ void __launch_bounds__(512) hs_prefill_join_kernel(const __grid_const
                                                         pack2<T>(acc[k + 4] * inv, acc[k + 5] * inv), pack2<T>(acc[k + 6] * inv, acc[k + 7] * inv));
     if (a.lse && c0 == 0)
         a.lse[(r.q0 + at) * a.heads + unit.h] = some ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
-}
-
-template <typename... Params, typename... Values>
-cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s, Values... values)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = threads;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, values...);
 }
 
 template <typename T, bool E4M3> cudaError_t launch(const Args& g, int pairs, cudaStream_t s)

@@ -51,6 +51,21 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity)
     return true;
 }
 
+// Bounded wait: on a timeout the CTA is marked dead and every later wait returns at once.
+__device__ __forceinline__ void wait(uint32_t bar, uint32_t parity, int* dead, int* error)
+{
+    if (mbar_try(bar, parity)) return;
+    const long long t0 = clock64();
+    while (!mbar_try(bar, parity)) {
+        if (*(volatile int*)dead) return;
+        if (clock64() - t0 > kWaitClocks) {
+            *(volatile int*)dead = 1;
+            atomicExch(error, 1);
+            return;
+        }
+    }
+}
+
 __device__ __forceinline__ void mbar_arrive(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
