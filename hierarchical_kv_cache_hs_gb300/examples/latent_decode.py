@@ -94,8 +94,10 @@ def run(e4m3: bool = True, seed: int = 0) -> dict:
     start = torch.arange(B + 1, device="cuda", dtype=torch.int32) * PROMPT
     out = torch.empty((n, H, HEAD), dtype=torch.bfloat16, device="cuda")
     space = torch.empty(hs.hs_latent_prefill_workspace(n, H), dtype=torch.uint8, device="cuda")
+    hs.hs_workspace_clear(space)
     hs.hs_latent_prefill(q, rows, layer.w_uk, layer.w_uv, start, start, out, SCALE,
                          row_format=layer.row_format, workspace=space, stream=stream)
+    late = hs.hs_workspace_error(space)
     wide = layer.rows64(rows.view(B, PROMPT, -1))
     k0 = torch.cat([wide[0, :, :LATENT] @ layer.w_uk[0].double().t(), wide[0, :, LATENT:]], 1)
     s = SCALE * (q[:PROMPT, 0].double() @ k0.t())
@@ -111,6 +113,7 @@ def run(e4m3: bool = True, seed: int = 0) -> dict:
         slots = torch.empty((B, 1, K), dtype=torch.int32, device="cuda")
         out = torch.empty((B, 1, H, LATENT), dtype=torch.bfloat16, device="cuda")
         space = torch.empty(hs.hs_latent_attend_workspace(B, 1, H, K), dtype=torch.uint8, device="cuda")
+        hs.hs_workspace_clear(space)
         every = layer.rows64(rows.view(B, PROMPT, -1))
         for step in range(STEPS):
             q, row = layer.project(hidden(B), hidden(B))
@@ -130,11 +133,14 @@ def run(e4m3: bool = True, seed: int = 0) -> dict:
             p = torch.softmax(SCALE * torch.einsum("bhc,bkc->bhk", qa[:, 0].double(), k), -1)
             worst = max(worst, _off(out[:, 0], torch.einsum("bhk,bkl->bhl", p, k[..., :LATENT])))
         stats = h.stats()
+        late |= hs.hs_workspace_error(space)
     return {"prompt": prompt, "decode": worst, "misses": stats["misses"], "hits": stats["hits"],
-            "errors": stats["err_bits"]}
+            "errors": stats["err_bits"], "waits_ran_out": late}
 
 
 if __name__ == "__main__":
     got = run(e4m3="--bf16" not in sys.argv[1:])
+    if got["errors"] or got["waits_ran_out"]:
+        sys.exit("device errors %#x, waits that ran out %d" % (got["errors"], got["waits_ran_out"]))
     print("prompt attention: %.2e off 64 bits; decode steps: %.2e; %d misses, %d hits" %
           (got["prompt"], got["decode"], got["misses"], got["hits"]))

@@ -631,6 +631,19 @@ def _workspace_of(workspace, device):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
+def hs_workspace_clear(workspace) -> None:
+    """Zero a workspace's error word, on torch's current stream: once, before the workspace's first call."""
+    import torch
+    workspace.view(-1).view(torch.uint8)[:4].zero_()
+
+
+def hs_workspace_error(workspace) -> int:
+    """A workspace's error word, once torch's current stream is done: 1 when a wait of an attention call ran
+    out since it was cleared.  The outputs of the calls in between are not valid then."""
+    import torch
+    return int(workspace.view(-1).view(torch.uint8)[:4].view(torch.int32).item())
+
+
 def _lse_of(lse, shape, device):
     if lse is None:
         return 0

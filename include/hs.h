@@ -608,7 +608,8 @@ int hs_resolve_noalloc(int batch, int ctx_len, int row_bytes, int buffer_slots, 
  * need one each.  The attention kernels' waits are bounded: one that runs out
  * (a second or two; it cannot in a working kernel) sets the workspace's first
  * int32 to 1, which is otherwise left as it is, and the call's outputs are not
- * valid.  Errors: HS_ERR_ARG (a NULL or misaligned pointer, a size,
+ * valid.  To see that, zero the word before a workspace's first call and read
+ * it with the results.  Errors: HS_ERR_ARG (a NULL or misaligned pointer, a size,
  * type or stride that the call does not take, a workspace that is too small),
  * HS_ERR_LIMIT, HS_ERR_CUDA; nothing is enqueued then.
  */

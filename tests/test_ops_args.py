@@ -167,3 +167,12 @@ def test_binding_checks_tensors(hs):
                  dict(out=good["out"].to(torch.uint8), scales=torch.zeros(3, 1), group=-1)]:
         with pytest.raises(ValueError):
             hs.hs_rms_norm(**dict(good, **over))
+
+
+@pytest.mark.parametrize("dtype", [torch.uint8, torch.int32, torch.float32])
+def test_workspace_error_word(hs, dtype):
+    space = torch.full((3, 64), 5, dtype=torch.uint8).view(dtype)
+    assert hs.hs_workspace_error(space) == 0x05050505
+    hs.hs_workspace_clear(space)
+    assert hs.hs_workspace_error(space) == 0
+    assert (space.view(-1).view(torch.uint8)[4:] == 5).all()
