@@ -527,6 +527,36 @@ def test_prefill_pieces(hs, H, nq, nk, e4m3):
     assert torch.equal(out, again) and torch.equal(lse, lse_again)
 
 
+@pytest.mark.parametrize("scale", [-SCALE, 0.0, 1e-30])
+@pytest.mark.parametrize("H,nq,nk", [(2, [257, 40], [257, 300]), (3, [600], [2100])])
+def test_prefill_scale(hs, H, nq, nk, scale):
+    """Negative scales and 0 (every seen row weighs the same)."""
+    q, rows, w_uk, w_uv = _prompt_case(nq, nk, H, BF, False, seed=17)
+    start = [torch.tensor([0] + n, device="cuda").cumsum(0).int() for n in (nq, nk)]
+    out = torch.full((sum(nq), H, 128), NAN, dtype=BF, device="cuda")
+    lse = torch.full((sum(nq), H), NAN, device="cuda")
+    ws = torch.empty(hs.hs_latent_prefill_workspace(sum(nk), H), dtype=torch.uint8, device="cuda")
+    hs.hs_latent_prefill(q, rows, w_uk, w_uv, *start, out, scale, lse=lse, workspace=ws)
+    half = 2.0 ** -8
+    q0 = k0 = 0
+    for n, m in zip(nq, nk):
+        kv = rows[k0:k0 + m].double()
+        allowed = torch.ones((n, m), dtype=torch.bool, device="cuda").tril(m - n)
+        for h in range(H):
+            k = torch.cat([kv[:, :512] @ w_uk[h].double().t(), kv[:, 512:]], 1)
+            v = kv[:, :512] @ w_uv[h].double().t()
+            qh = q[q0:q0 + n, h].double()
+            s = torch.where(allowed, scale * (qh @ k.t()), -math.inf)
+            o, want_lse, mean_abs = _softmax_ref(s, v)
+            reach = abs(scale) * torch.where(allowed, qh.abs() @ k.abs().t(), 0.0).amax(-1, keepdim=True)
+            score = (half + 2.0 ** -12) * reach + 2.0 ** -18
+            tol = half * o.abs() + (2 * half + 2.0 ** -12 + 2 * score) * mean_abs + 1e-30
+            err = (out[q0:q0 + n, h].double() - o).abs()
+            assert bool((err <= tol).all()), (err / tol).max().item()
+            assert ((lse[q0:q0 + n, h].double() - want_lse).abs() <= score.squeeze(-1) + 2.0 ** -20 * 20).all()
+        q0, k0 = q0 + n, k0 + m
+
+
 # ---- norm ------------------------------------------------------------------------------
 
 def _norm_ref(x, w, eps, residual, carry):
@@ -623,6 +653,26 @@ def test_norm_e4m3_divides_by_the_scale(hs, n, d, carry, dtype, group):
     each = scales.repeat_interleave(group or width, 1)[:, :width]
     want = (x.float() / each).to(torch.float8_e4m3fn).view(torch.uint8)
     assert torch.equal(out[:, d:], want[:, d:])
+
+
+@pytest.mark.parametrize("dtype", [BF, HALF, torch.float32])
+@pytest.mark.parametrize("d,carry", [(6145, 0), (7001, 3), (12739, 64), (16384, 0)])
+def test_norm_wide_rows_of_odd_alignment(hs, d, carry, dtype):
+    """The widest rows, element by element: as the type, and as e4m3 with one scale."""
+    g = _gen(d)
+    x, w = _randn(g, 3, d + carry + 1, dtype=dtype)[:, 1:], _randn(g, d, dtype=dtype)
+    out = torch.full((3, d + carry), NAN, dtype=dtype, device="cuda")
+    hs.hs_rms_norm(x, w, out, 1e-6, carry=carry)
+    want = _norm_ref(x, w, 1e-6, None, carry)
+    half = torch.finfo(dtype).eps / 2
+    tol = (half * 1.01 + 2.0 ** -24 * (8 + math.sqrt(d))) * want.abs()
+    assert ((out.double() - want).abs() <= tol + (2.0 ** -25 if dtype == HALF else 1e-37)).all()
+    q, s = torch.full((3, d + carry), 255, dtype=torch.uint8, device="cuda"), torch.full((3, 1), NAN, device="cuda")
+    hs.hs_rms_norm(x, w, q, 1e-6, carry=carry, scales=s)
+    top = want.abs().amax(1, keepdim=True) / 448
+    assert ((s.double() - top).abs() <= 2.0 ** -22 * (8 + math.sqrt(d)) * top).all()
+    got = q.view(torch.float8_e4m3fn).double() * s.double()
+    assert ((got - want).abs() <= 2.0 ** -4 * 1.001 * want.abs() + 2.0 ** -10 * 1.001 * s.double()).all()
 
 
 def test_norm_writes_cache_rows(hs):
