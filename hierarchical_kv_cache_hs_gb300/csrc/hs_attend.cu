@@ -15,11 +15,12 @@
 // only when a maximum exceeds it by more than 2^8.
 //
 // Bound by the chain of a tile's steps (rows, scores, softmax, values; 26 clocks a
-// 128 x 64 x 16 product of the pair): 64 requests x 2048 rows x 128 heads take 43 us, 0.58
-// of a copy's rate in bytes and 0.45 of a product's in operations.  128 heads a pair,
-// since rows are the traffic: each row's latent half comes twice from L2, once from HBM.
-// 131072 8-bit rows x 128 heads take 69 us, 55 of them 27 tiles in a row on each pair,
-// whose rows both CTAs widen, and the rest the join.
+// 128 x 64 x 16 product of the pair): 64 requests x 2048 rows x 128 heads take 43 us, 0.59
+// of a copy's rate in bytes and 0.45 of a product's in operations, on 64 of 76 pairs.  128
+// heads a pair, since rows are the traffic: each row's latent half comes twice from L2,
+// once from HBM.  8-bit rows are bound by their widening, which both CTAs do: 64 requests x
+// 2048 x 128 heads take 67 us, 131072 rows x 128 heads 69, 55 of them 27 tiles in a row on
+// each pair and the rest the join.
 //
 // Work split: the tiles of all units (a unit: request, position, 128 heads) form
 // one line that is cut into equal pieces, one a pair; units cut in two leave

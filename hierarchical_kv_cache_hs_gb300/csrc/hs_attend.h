@@ -306,8 +306,8 @@ __device__ __forceinline__ bool find_cut(const Start* start, int workers, int x,
 
 // The kernels: a pair of SMs for up to 128 heads; and one SM for up to 32 heads and 8-bit
 // rows, whose conversion, done twice by a pair, bounds them there (256 requests x 2048
-// rows: 108 against 200 us with 16 heads, 134 against 202 with 32, but 262 against 207
-// with 48; with 16-bit rows the pair is faster at any number: 154 against 140 us with 16).
+// rows: 102 against 204 us with 16 heads, 128 against 206 with 32; a form for 48 heads took
+// 262 where the pair takes 209, one for 16-bit rows 154 where it takes 140 with 16).
 constexpr int kNarrowHeads = 32;
 cudaError_t launch_pair(const hs_attend_t& a, int sms, cudaStream_t s);
 cudaError_t launch_narrow(const hs_attend_t& a, int sms, cudaStream_t s);

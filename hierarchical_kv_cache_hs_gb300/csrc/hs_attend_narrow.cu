@@ -5,9 +5,10 @@
 // core's 128 (or 64) rows: S^T = K Q^T for a tile of 64 rows (M = 64, N = heads), and
 // O^T += V^T P^T (M = 128 channels four times, N = heads), where V^T is the key tile read
 // along its channels.  A row is widened to fp16 and brought to shared memory once, and
-// read twice.  Bound by the chain of a stage (widening, scores, softmax, values) with two
-// stages, all that shared memory holds: 256 requests x 2048 rows x 16 heads take 101 us,
-// 3.2 TB/s (0.47 of a copy's rate), 92 of them here and the rest the join.
+// read twice.  Bound by the chain of a stage (rows, widening, scores, softmax, values) with
+// two stages of widened rows; a third (72 KB) does not fit, one of rows as they come (36 KB)
+// would with 16 heads and was not tried.  256 requests x 2048 rows x 16 heads take 102 us,
+// 3.2 TB/s (0.47 of a copy's rate), 93 of them here and the rest the join; 32 heads 128.
 //
 // Warps: 0-3 softmax, 4-11 bring the rows (four a stage) and the queries, 12 and 13 issue
 // the products.  The running reference of a head moves only when a maximum exceeds it by
@@ -19,7 +20,7 @@ namespace {
 
 constexpr int kThreads = 14 * 32;
 // Tiles' time that a unit's queries, first scores and output take: 24 ragged contexts of up to 16,384
-// rows 47 -> 35 us, 200 requests x 1000 rows x 32 heads 76 -> 72, 256 x 2048 x 16 101 (7: 34, 73, 105).
+// rows 47 -> 35 us, 200 requests x 1000 rows x 32 heads 76 -> 72, 256 x 2048 x 16 102 (7: 34, 73, 105).
 constexpr int kUnitCost = 3;
 constexpr int kMaxCtas = 152;
 constexpr int kStageBytes = 9 * 64 * 128;  // 9 blocks of 64 channels, [64 rows][128 B]

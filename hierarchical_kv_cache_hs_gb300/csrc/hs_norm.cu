@@ -3,13 +3,15 @@
 //
 // A row's h stays in fp32 registers between the sum of squares and the scaling, so
 // each input is read once and each output written once; the pass is bound by HBM:
-// 8192 x 4096 bf16 with a residual into e4m3 in groups of 128 takes 39.0 us, 6.05 TB/s
-// (0.89 of a copy's rate).
+// 8192 x 4096 bf16 with a residual into e4m3 in groups of 128 takes 39.2 us, 6.02 TB/s
+// (0.89 of a copy's rate); 65,536 cache rows (512 + 64 channels) 31 us, 3.7 TB/s, with a
+// row a warp, one in flight, and a quarter of its lanes' pieces empty.
 // Rows whose pieces lie on 16-byte boundaries go through hs_norm_kernel: 16-byte
 // loads, a warp a row up to 128 pieces (576 16-bit channels are 72), else 8 or 16 warps.
 // Any other row (odd widths, odd alignments, groups that are not a power of two of
 // pieces) goes through hs_norm_any_kernel, element by element with the row in shared
-// memory.
+// memory, bound by its instructions: 16,000 x 1021 (fp16, residual, into e4m3) takes 92 us
+// where its bytes take 17.
 #include "hs_ops.h"
 
 namespace {
@@ -101,9 +103,9 @@ __device__ __forceinline__ float divided(float y, float scale, float inv)
 
 constexpr int kWarps = 8;  // of a block, where rows do not share it
 // Rows element by element: up to kAnyNarrow channels a warp a row, above kAnyWide 32 warps, else 8 (fp16,
-// residual, e4m3 with one scale): 22,132 x 417 40 us against 72 with 8 warps, 20,000 x 717 67 against 88, but
-// 16,000 x 1021 98 against 93; 2000 x 8191 96 with 32 warps against 128 with 8, 7 x 12739 15 against 31, but
-// 3000 x 5003 93 against 84.
+// residual, e4m3 with one scale): 22,132 x 417 40 us against 71 with 8 warps, 20,000 x 717 67 against 87, but
+// 16,000 x 1021 97 against 92; 2000 x 8191 95 with 32 warps against 125 with 8, 7 x 12739 15 against 31, but
+// 3000 x 5003 92 against 82.
 constexpr int kAnyNarrow = 768, kAnyWide = 6144;
 
 // NV: 16-byte pieces a thread; TEAM: warps that share a row (1: each of the block's has
@@ -349,8 +351,8 @@ template <typename T, bool E4M3> cudaError_t launch(const hs_norm_t& a, cudaStre
         const int width = a.dim + a.carry;
         return width <= kAnyNarrow ? launch_any<T, E4M3, 1>(a, s) : width <= kAnyWide ? launch_any<T, E4M3, 8>(a, s) : launch_any<T, E4M3, 32>(a, s);
     } else if (pieces <= 128) {
-        // A warp a row (residual, bf16): 1024 channels x 65,536 rows 81 us in 16 bits, 76 into e4m3, against 92
-        // and 117 with eight warps a row; 2048 channels (256 pieces) 84 and 99 against 79 and 79.
+        // A warp a row (residual, bf16): 1024 channels x 65,536 rows 81 us in 16 bits, 77 into e4m3, against 93
+        // and 119 with eight warps a row; 2048 channels (256 pieces) 84 and 99 against 79 and 81.
         const unsigned grid = (unsigned)((a.tokens + kWarps - 1) / kWarps);
         if (pieces <= 32)
             hs_norm_kernel<T, E4M3, 1, 1><<<grid, kWarps * 32, 0, s>>>(a);
@@ -359,8 +361,8 @@ template <typename T, bool E4M3> cudaError_t launch(const hs_norm_t& a, cudaStre
         else
             hs_norm_kernel<T, E4M3, 4, 1><<<grid, kWarps * 32, 0, s>>>(a);
     } else {
-        // Eight warps: 4096 channels x 16,384 rows into e4m3 73 us against 97 with 16, 8192 x 8192 78 against 91;
-        // 16 warps from there: 12288 x 5461 93 against 117, 16384 x 4096 83 against 102.
+        // Eight warps: 4096 channels x 16,384 rows into e4m3 74 us against 98 with 16, 8192 x 8192 78 against 93;
+        // 16 warps from there: 12288 x 5461 94 against 119, 16384 x 4096 84 against 103.
         const unsigned grid = (unsigned)a.tokens;
         if (pieces <= 256)
             hs_norm_kernel<T, E4M3, 1, 8><<<grid, 256, 0, s>>>(a);

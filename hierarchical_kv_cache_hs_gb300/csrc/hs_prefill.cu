@@ -14,14 +14,17 @@
 // (3) Join: the blocks of all units (head, 512 queries) form one line that is cut
 //     into equal pieces, one a pair; units cut in two or more are joined.
 //
-// 8192 tokens x 32 heads (bf16) take 561 us, 1,348 TFLOP/s (0.71 of a product's rate):
-// (1) 53, bound by what it writes and L2; (2) 471, bound by the softmax of a tile where it
+// 8192 tokens x 32 heads (bf16) take 562 us, 1,345 TFLOP/s (0.70 of a product's rate):
+// (1) 52, bound by what it writes and L2; (2) 471, bound by the softmax of a tile where it
 // outlasts the other tile's products.  512 tokens after 15,872 cached 8-bit rows x 16
-// heads (fp16): 134, of them 60 and 73, the second's start within the first's end.
+// heads (fp16): 135, of them 60 and 72, the second's start within the first's end.
 //
-// Keys, values and softmax weights are rounded to 16 bits before their products, as the
-// tensor core takes them: bf16 results are 0.0026 to 0.0028 off 64 bits (relative, in
-// norm) where one rounding at the end gives 0.0017; sums and statistics are fp32.
+// Keys, values and softmax weights are rounded to the call's type before their products,
+// as the tensor core takes them: bf16 results are 0.0026 to 0.0028 off 64 bits (relative,
+// in norm) where one rounding at the end gives 0.0017; sums and statistics are fp32.
+// Values and weights in fp16 for bf16 calls would come closer, but bf16 values reach past
+// fp16's range: each token would need a power of two of its own, on each weight, in the
+// softmax, which is the bound.
 #include "hs_ops.h"
 #include "hs_tc.h"
 

@@ -79,11 +79,16 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank)
     return r;
 }
 
-// Arrive on a barrier of another CTA of the cluster.  The default semantics
-// (release) order this thread's earlier writes to its own shared memory, fenced
-// for the tensor core, before the arrival; with .release.cluster spelled out each
-// arrival also waited for the thread's loads in flight (61 against 53 us for 64
-// requests x 2048 rows x 128 heads).
+// Arrive on a barrier of another CTA of the cluster.  Without a scope this releases
+// at CTA scope only, and gives no order to ordinary reads of this thread's writes by
+// the other CTA.  There are none.  What the other CTA goes on to start are the pair's
+// products: they read this CTA's part of the operands from its own shared memory, by
+// its own SM, and those writes are fenced for that (fence.proxy.async) before the
+// arrival; accesses to tensor memory are complete (tcgen05.wait) and fenced likewise
+// (tcgen05.fence).  What a CTA's warps write for its other warps beside the operands
+// (rows that count, scales) they read after the products' own arrival in that CTA.
+// With .release.cluster spelled out each arrival also waited for the thread's loads
+// in flight (61 against 53 us for 64 requests x 2048 rows x 128 heads, when tried).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar)
 {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)

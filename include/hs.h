@@ -611,7 +611,8 @@ int hs_resolve_noalloc(int batch, int ctx_len, int row_bytes, int buffer_slots, 
  * valid.  To see that, zero the word before a workspace's first call and read
  * it with the results.  Errors: HS_ERR_ARG (a NULL or misaligned pointer, a size,
  * type or stride that the call does not take, a workspace that is too small),
- * HS_ERR_LIMIT, HS_ERR_CUDA; nothing is enqueued then.
+ * HS_ERR_LIMIT, with nothing enqueued; HS_ERR_CUDA where a launch failed (a
+ * call's earlier launches may have been made).
  */
 #define HS_LATENT_DIM  512
 #define HS_ROPE_DIM    64
@@ -705,7 +706,9 @@ int hs_latent_attend(const hs_attend_t* args, hs_stream_t stream);
  * least).  The keys' and values' expanded channels, the rotary channels of
  * 8-bit rows and the softmax weights are rounded to `dtype`.  Rows that a query
  * does not see may hold anything; a value that is not finite once rounded makes
- * the output NaN of every query that sees its row.
+ * the output NaN of every query that sees its row.  A call expands all of its
+ * rows; the workspace holds them, 512 bytes a token and head and 128 a token, and
+ * 40 MB beside (8192 tokens x 32 heads: 176 MB; 131,072 x 128: 8.6 GB).
  * Source: no passage (as hs_latent_attend).
  */
 typedef struct {
