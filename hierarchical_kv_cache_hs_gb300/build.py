@@ -20,10 +20,11 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libhs.so")
 
 SOURCES = ["hs_api.cpp", "hs_resolve.cu", "hs_copy.cu", "hs_noalloc.cu",
-           "hs_ops.cpp", "hs_attend.cu", "hs_attend_narrow.cu", "hs_prefill.cu", "hs_norm.cu"]
+           "hs_ops.cpp", "hs_attend.cu", "hs_attend_narrow.cu", "hs_attend_shared.cu", "hs_prefill.cu", "hs_norm.cu",
+           "hs_rows.cu", "hs_rotate.cu"]
 HEADERS = [os.path.join(CSRC, "hs_internal.h"), os.path.join(CSRC, "hs_gather_pool.h"),
            os.path.join(CSRC, "hs_ops.h"), os.path.join(CSRC, "hs_tc.h"),
-           os.path.join(CSRC, "hs_attend.h"),
+           os.path.join(CSRC, "hs_attend.h"), os.path.join(CSRC, "hs_pieces.h"),
            os.path.join(INCLUDE, "hs.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -1,5 +1,5 @@
-// What the two kernels of hs_latent_attend share: how the work is cut, which rows a
-// tile holds, and how 8-bit rows become operands.
+// What the kernels of hs_latent_attend and hs_latent_attend_shared share: how the work is
+// cut, which rows a tile holds, how 8-bit rows become operands, and the joining of pieces.
 #pragma once
 
 #include <type_traits>
@@ -20,9 +20,7 @@ constexpr int kTile = 64;  // rows a tile
 // line's first unit: every piece has that once.  A cut inside it is a cut at the unit's
 // start, so a worker may get no piece; the one before a piece that starts inside a unit
 // always has one.
-struct Args {
-    hs_attend_t a;
-    int head_blocks;
+struct Cut {
     int flat;
     int units;         // at most HS_MAX_BATCH x HS_MAX_POSITIONS x HS_MAX_HEADS / 128, below 2^31
     int unit_tiles;    // tiles of a unit; with lengths, the most that one has
@@ -33,10 +31,10 @@ struct Args {
     int unit_share, unit_extra;  // units a worker, likewise
 
     // Fill in the cut: whole units, or pieces where those are `join` tiles' time shorter.
-    void cut(int most, int64_t rows, int join, int unit_cost)
+    void cut(int most, int64_t rows, int join, int unit_cost, int tile = kTile)
     {
         cost = unit_cost;
-        unit_tiles = rows <= kTile ? 1 : (int)((rows + kTile - 1) / kTile);
+        unit_tiles = rows <= tile ? 1 : (int)((rows + tile - 1) / tile);
         const int64_t total = (int64_t)units * unit_tiles;
         workers = (int)(total < most ? total : most);
         flat = (int64_t)((units + workers - 1) / workers) * unit_tiles > (total + workers - 1) / workers + join;
@@ -47,6 +45,10 @@ struct Args {
         unit_share = units / workers;
         unit_extra = units % workers;
     }
+};
+struct Args : Cut {
+    hs_attend_t a;
+    int head_blocks;
 };
 
 struct Start {  // where a worker's piece of the line begins (unit -1: it has none)
@@ -67,6 +69,28 @@ __device__ __forceinline__ int request_tiles(const hs_attend_t& a, long long b)
     return n <= kTile ? 1 : (int)((n + kTile - 1) / kTile);
 }
 
+// Worker i's piece of whole units, or of a line whose units all have the same tiles.
+__device__ __forceinline__ Piece whole_piece(const Cut& g, int i)
+{
+    const int n = g.unit_share + (i < g.unit_extra);
+    return {(long long)n * g.unit_tiles, g.unit_share * i + min(i, g.unit_extra), 0};
+}
+__device__ __forceinline__ Piece line_piece(const Cut& g, int i)
+{
+    const int per = g.unit_tiles + g.cost;
+    auto place = [&](int x, int& unit, int& tile) {
+        const long long at = g.cost + g.share * x + min(x, g.extra);
+        unit = at < 0x7fffffff ? (int)((unsigned)at / (unsigned)per) : (int)(at / per);
+        tile = max(0, (int)(at - (long long)unit * per) - g.cost);
+    };
+    Piece p;
+    int unit, tile;
+    place(i, p.unit, p.tile);
+    place(i + 1, unit, tile);
+    p.count = (long long)(unit - p.unit) * g.unit_tiles + tile - p.tile;
+    return p;
+}
+
 // Worker i's piece (one warp; every lane gets it).
 __device__ __forceinline__ Piece find_piece(const Args& g, int i)
 {
@@ -75,12 +99,9 @@ __device__ __forceinline__ Piece find_piece(const Args& g, int i)
     const int upr = a.positions * g.head_blocks;  // units a request
     Piece p;
     if (!g.flat) {
-        p.unit = g.unit_share * i + min(i, g.unit_extra);
-        p.tile = 0;
-        const int n = g.unit_share + (i < g.unit_extra);
-        p.count = (long long)n * g.unit_tiles;
+        p = whole_piece(g, i);
         if (!a.slots) {
-            const int end = p.unit + n;
+            const int end = p.unit + g.unit_share + (i < g.unit_extra);
             p.count = 0;
             for (int b = p.unit / upr + lane; b < a.batch && b * upr < end; b += 32)
                 p.count += (long long)(min(b * upr + upr, end) - max(b * upr, p.unit)) * request_tiles(a, b);
@@ -88,19 +109,7 @@ __device__ __forceinline__ Piece find_piece(const Args& g, int i)
         }
         return p;
     }
-    if (a.slots) {
-        const int per = g.unit_tiles + g.cost;
-        auto place = [&](int x, int& unit, int& tile) {
-            const long long at = g.cost + g.share * x + min(x, g.extra);
-            unit = at < 0x7fffffff ? (int)((unsigned)at / (unsigned)per) : (int)(at / per);
-            tile = max(0, (int)(at - (long long)unit * per) - g.cost);
-        };
-        int unit, tile;
-        place(i, p.unit, p.tile);
-        place(i + 1, unit, tile);
-        p.count = (long long)(unit - p.unit) * g.unit_tiles + tile - p.tile;
-        return p;
-    }
+    if (a.slots) return line_piece(g, i);
     long long total = 0;
     for (int b = lane; b < a.batch; b += 32) total += (long long)request_tiles(a, b) * upr;
     for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
@@ -302,6 +311,64 @@ __device__ __forceinline__ bool find_cut(const Start* start, int workers, int x,
     first = at - 1;
     last = first + __syncthreads_count(inside && mine == unit);
     return true;
+}
+
+constexpr int kMaxPairs = 76;  // pairs of SMs
+
+// What a pair of SMs leaves of a unit that it does not have whole: the sums of 128 queries, unscaled.
+struct PairSums {
+    float o[2][256][128];  // [CTA][column][lane]
+    float ref[2][128], sum[2][128];
+};
+
+// The sums of a unit's pieces in workers first..last, one lane's COLS columns from c0: the whole block of 512
+// calls it, four groups of 128 threads, which with SPLIT take every fourth piece each (the first then has the
+// result), else every piece; in one pass, and the order of the sums is fixed.
+template <int COLS, bool SPLIT>
+__device__ __forceinline__ void join_pieces(const PairSums* parts, int first, int last, int rank, int lane, int c0, int group,
+                                            bool live, float (&acc)[COLS], float& sum, float& top)
+{
+    constexpr int kGroups = SPLIT ? 4 : 1;  // that share pieces
+    __shared__ float tops[4][128], sums[4][128], cols[SPLIT ? 3 : 1][COLS][128];
+    sum = 0.f, top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < COLS; ++k) acc[k] = 0.f;
+    if (live)
+#pragma unroll(COLS == 4 ? 8 : 2)
+        for (int n = first + group; n <= last; n += kGroups) {
+            const PairSums& q = parts[2 * n + (n == first)];
+            const float ref = q.ref[rank][lane], l = q.sum[rank][lane];
+            float o[COLS];
+#pragma unroll
+            for (int k = 0; k < COLS; ++k) o[k] = q.o[rank][c0 + k][lane];
+            // without a branch, so that the loads of several pieces are in flight; a sum of 0: no row counted
+            const float up = l == 0.f ? top : fmaxf(top, ref), base = up == -INFINITY ? 0.f : up;
+            const float keep = tc::exp2_approx(top - base), w = l == 0.f ? 0.f : tc::exp2_approx(ref - base);
+            top = up;
+            sum = sum * keep + w * l;
+#pragma unroll
+            for (int k = 0; k < COLS; ++k) acc[k] = acc[k] * keep + (l == 0.f ? 0.f : w * o[k]);
+        }
+    if (!SPLIT) return;
+    tops[group][lane] = top;
+    sums[group][lane] = sum;
+    if (group)
+#pragma unroll
+        for (int k = 0; k < COLS; ++k) cols[group - 1][k][lane] = acc[k];
+    __syncthreads();
+    if (group || !live) return;
+    top = fmaxf(fmaxf(tops[0][lane], tops[1][lane]), fmaxf(tops[2][lane], tops[3][lane]));
+    const float base = top == -INFINITY ? 0.f : top;
+    float w = tc::exp2_approx(tops[0][lane] - base);
+    sum *= w;
+#pragma unroll
+    for (int k = 0; k < COLS; ++k) acc[k] *= w;
+    for (int n = 1; n < 4; ++n) {
+        w = tc::exp2_approx(tops[n][lane] - base);
+        sum += w * sums[n][lane];
+#pragma unroll
+        for (int k = 0; k < COLS; ++k) acc[k] += w * cols[n - 1][k][lane];
+    }
 }
 
 // The kernels: a pair of SMs for up to 128 heads; and one SM for up to 32 heads and 8-bit

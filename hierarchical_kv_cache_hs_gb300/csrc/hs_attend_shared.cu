@@ -1,0 +1,736 @@
+// hs_latent_attend_shared: absorbed latent attention of a batch over a prefix that all its
+// requests share, joined with their own rows' part (hs_latent_attend).
+//
+// All queries of the batch (request, position, head) form one line; a unit is 128 of them
+// and the prefix's rows are the same for every unit, so this is one dense product: S = Q K^T,
+// O = softmax(S) K[:, :512].  A pair of SMs (a cluster of two CTAs) takes a unit, 64 queries
+// in each CTA, and walks the rows in tiles of 128: tcgen05 products of the pair (M = 128)
+// accumulate S (64 columns a CTA) and the whole of O (256 columns) in tensor memory, which
+// also holds 6 of the queries' 9 blocks of 64 channels (192 columns).  The copy engine
+// brings rows by a tensor map: of each tile a CTA gets its 64 rows whole (its half of
+// Q K^T's B operand, in three groups of three blocks) and all 128 rows' half of the latent
+// channels (its half of the second product's B operand, in four groups of two blocks); both
+// kinds go through rings, so that copies run about a tile ahead.
+//
+// Bound by shared memory: a tile's products read 192 KB of operands a CTA and its copies
+// write 139 KB, at 128 bytes a clock 2,700 clocks, where the tensor core alone needs 2,200.
+// Tiles of 128 rows, since a product of 128 x 64 x 16 takes 26 clocks where one of
+// 128 x 128 x 16 takes 33 (its A operand is read once for twice the columns).
+//
+// Warps of a CTA: 0-3 queries, softmax and outputs, 4 brings keys, 5 values, 6 issues the
+// products (in the pair's first CTA), in the order S(t+1), O(t), so that a tile's softmax
+// has the time of both.
+//
+// A prefix of 8-bit rows is widened to fp16 in the workspace first (exactly; the row scales
+// multiply scores and weights): each row is read by every unit, so it is widened once
+// instead of once a unit.  So is one with lengths: there a row that some requests do not
+// see may hold anything, and weights of 0 times values that are not finite would be NaN;
+// such a row becomes zeros with a NaN in its rotary channels, which only keys have.
+#include <cuda.h>
+
+#include <atomic>
+
+#include "hs_attend.h"
+#include "hs_pieces.h"
+
+namespace hs_attn {
+namespace {
+
+constexpr int kThreads = 7 * 32;
+constexpr int kRows = 128;  // rows a tile
+constexpr int kUnitCost = 4;
+
+constexpr int kQTmem = 6;
+constexpr int kBlock = 64 * 128;                   // bytes of 64 rows x 64 channels
+constexpr int kKGroup = 3 * kBlock, kVGroup = 2 * kBlock;
+constexpr int kKStages = 4, kVStages = 5;
+constexpr int kOffK = (9 - kQTmem) * kBlock;       // the queries' other blocks lie before
+constexpr int kOffV = kOffK + kKStages * kKGroup;
+constexpr int kOffP = kOffV + kVStages * kVGroup;  // [64 keys' block][64 queries][128 B]
+constexpr int kOffAux = kOffP + 2 * kBlock;
+
+struct Aux {
+    uint64_t kfull[kKStages], kfree[kKStages], vfull[kVStages], vfree[kVStages], qready, sfull, sread, pready, pvdone, spare;
+    uint32_t tmem;
+    int dead;
+    Piece piece;
+    float red[2][128];
+};
+constexpr int kSmem = kOffAux + (int)sizeof(Aux);
+static_assert(kSmem <= 232448, "shared memory");
+
+constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;  // tensor memory columns
+
+struct SharedArgs : Cut {
+    hs_attend_t a;              // queries and outputs
+    const int32_t* prefix_lengths;
+    int64_t prefix_rows;
+    int64_t queries;            // below 2^31
+    const float* scales;        // of 8-bit rows
+    const __half* log_scales;   // base 2, not below kLeastLogScale
+    const float* own_lse;       // NULL: no own rows
+    Start* starts;
+    PairSums* parts;
+    int* error;
+};
+
+__device__ __forceinline__ int64_t seen_rows(const SharedArgs& g, int64_t request)  // of the prefix
+{
+    if (!g.prefix_lengths) return g.prefix_rows;
+    const int64_t n = g.prefix_lengths[request];
+    return n < 0 ? 0 : n > g.prefix_rows ? g.prefix_rows : n;
+}
+__device__ __forceinline__ int request_of(const SharedArgs& g, int64_t query)
+{
+    return (int)((unsigned)query / ((unsigned)g.a.positions * (unsigned)g.a.heads));
+}
+// Where a query's vector begins in an array of these strides.
+__device__ __forceinline__ int64_t offset_of(const SharedArgs& g, int64_t query, const int64_t* stride)
+{
+    const unsigned pos = (unsigned)query / (unsigned)g.a.heads, b = pos / (unsigned)g.a.positions;
+    return b * stride[0] + (pos - b * g.a.positions) * stride[1] + ((unsigned)query - pos * g.a.heads) * stride[2];
+}
+
+struct Stretch {  // the units, or parts of units, of a piece (a whole warp walks it)
+    const SharedArgs& g;
+    long long left;
+    int unit, tile;
+    int at, t0, t1;  // the current unit and its tiles, without those that no query of it sees
+    bool whole;
+    __device__ Stretch(const SharedArgs& args, const Piece& x) : g(args), left(x.count), unit(x.unit), tile(x.tile) {}
+    __device__ bool next()
+    {
+        if (left <= 0) return false;
+        at = unit;
+        t0 = tile;
+        t1 = (long long)(g.unit_tiles - t0) <= left ? g.unit_tiles : t0 + (int)left;
+        whole = t0 == 0 && t1 == g.unit_tiles;
+        left -= t1 - t0;
+        ++unit;
+        tile = 0;
+        if (g.prefix_lengths) {
+            const int64_t q0 = (int64_t)at * 128, q1 = min(q0 + 128, g.queries) - 1;
+            const int last = request_of(g, q1);
+            long long most = 0;
+            for (int b = request_of(g, q0) + (threadIdx.x & 31); b <= last; b += 32) most = max(most, (long long)seen_rows(g, b));
+            for (int o = 16; o; o >>= 1) most = max(most, __shfl_xor_sync(~0u, most, o));
+            t1 = min(t1, (int)((most + kRows - 1) / kRows));
+        }
+        return true;
+    }
+};
+
+// One block of 64 rows x 64 channels by the tensor map; its bytes count on the barrier of the pair's first CTA.
+__device__ __forceinline__ void tile_load(uint32_t dst, const CUtensorMap* map, int channel, int row, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+                 "l"(map), "r"(channel), "r"(row), "r"(bar)
+                 : "memory");
+}
+
+// Keys or values of a piece's tiles (a warp; its first lane starts the copies).
+template <bool KEYS> __device__ void bring(const SharedArgs& g, const CUtensorMap* map, uint32_t sbase, Aux* x, uint32_t rank)
+{
+    constexpr int kStages = KEYS ? kKStages : kVStages, kBlocks = KEYS ? 3 : 2, kBytes = kBlocks * kBlock;
+    uint64_t* full = KEYS ? x->kfull : x->vfull;
+    uint64_t* free = KEYS ? x->kfree : x->vfree;
+    int stage = 0;
+    uint32_t phase = 1;  // the first round waits for nothing
+    Stretch w(g, x->piece);
+    while (w.next())
+        for (int t = w.t0; t < w.t1; ++t)
+#pragma unroll 1
+            for (int n = 0; n < (KEYS ? 3 : 4); ++n) {
+                if ((threadIdx.x & 31) == 0) {
+                    wait(tc::smem_addr(&free[stage]), phase, &x->dead, g.error);
+                    if (!*(volatile int*)&x->dead) {
+                        const uint32_t bar = tc::smem_addr(&full[stage]), bar0 = tc::map_to_rank(bar, 0);
+                        if (rank == 0) tc::mbar_expect(bar, 2 * kBytes);
+                        const uint32_t dst = sbase + (KEYS ? kOffK : kOffV) + stage * kBytes;
+                        const int channel = 64 * (KEYS ? 3 * n : 4 * (int)rank + 2 * (n & 1));
+                        const int row = t * kRows + 64 * (KEYS ? (int)rank : n >> 1);
+#pragma unroll
+                        for (int c = 0; c < kBlocks; ++c) tile_load(dst + c * kBlock, map, channel + 64 * c, row, bar0);
+                    }
+                }
+                __syncwarp();
+                if (++stage == kStages) stage = 0, phase ^= 1;
+            }
+}
+
+// After a wait that gave up: what was issued must be complete before tensor memory is freed.
+__device__ void drain(Aux* x)
+{
+    if (!*(volatile int*)&x->dead) return;
+    if (tc::elect_one()) tc::commit<2>(tc::smem_addr(&x->spare));
+    __syncwarp();
+    tc::mbar_wait(tc::smem_addr(&x->spare), 0);
+}
+
+template <typename T> __device__ void multiply(const SharedArgs& g, uint32_t sbase, Aux* x)
+{
+    constexpr uint32_t id_s = tc::inst_desc(HsType<T>::is_bf16, 128, kRows, false, false);
+    constexpr uint32_t id_o = tc::inst_desc(HsType<T>::is_bf16, 128, 256, false, true);
+    const uint32_t tmem = __shfl_sync(~0u, x->tmem, 0);
+    const uint64_t q_desc = tc::smem_desc(sbase, 16, 1024), k_base = tc::smem_desc(sbase + kOffK, 16, 1024);
+    const uint64_t p_desc = tc::smem_desc(sbase + kOffP, 16, 1024), v_base = tc::smem_desc(sbase + kOffV, kBlock, 1024);
+    int ks = 0, vs = 0;
+    uint32_t kphase = 0, vphase = 0;
+    long long j = 0;  // tiles so far
+    int pieces = 0;
+    auto values = [&](long long i, bool first) {  // O of tile i
+        wait(tc::smem_addr(&x->pready), i & 1, &x->dead, g.error);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const int keys = n >> 1, half = n & 1;
+            wait(tc::smem_addr(&x->vfull[vs]), vphase, &x->dead, g.error);
+            __syncwarp();
+            tc::fence_after();
+            const uint64_t v_desc = v_base + vs * (kVGroup >> 4);
+            if (tc::elect_one()) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    tc::mma_ss<2>(tmem + kColO + 128 * half, p_desc + ((keys * kBlock + k * 32) >> 4), v_desc + ((k * 2048) >> 4), id_o,
+                                  !(first && keys == 0 && k == 0));
+                tc::commit<2>(tc::smem_addr(&x->vfree[vs]));
+                if (n == 3) tc::commit<2>(tc::smem_addr(&x->pvdone));
+            }
+            __syncwarp();
+            if (++vs == kVStages) vs = 0, vphase ^= 1;
+        }
+    };
+    Stretch w(g, x->piece);
+    while (w.next()) {
+        if (w.t0 >= w.t1) continue;
+        wait(tc::smem_addr(&x->qready), pieces++ & 1, &x->dead, g.error);
+        for (int t = w.t0; t < w.t1; ++t, ++j) {
+            if (j >= 1) wait(tc::smem_addr(&x->sread), (j - 1) & 1, &x->dead, g.error);  // S has been read
+#pragma unroll
+            for (int n = 0; n < 3; ++n) {
+                wait(tc::smem_addr(&x->kfull[ks]), kphase, &x->dead, g.error);
+                __syncwarp();
+                tc::fence_after();
+                const uint64_t k_desc = k_base + ks * (kKGroup >> 4);
+                if (tc::elect_one()) {
+#pragma unroll
+                    for (int i = 0; i < 3; ++i)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int c = 3 * n + i;
+                            const uint64_t b = k_desc + ((i * kBlock + k * 32) >> 4);
+                            if (c < kQTmem)
+                                tc::mma_ts<2>(tmem + kColS, tmem + kColQ + 32 * c + 8 * k, b, id_s, (c | k) != 0);
+                            else
+                                tc::mma_ss<2>(tmem + kColS, q_desc + (((c - kQTmem) * kBlock + k * 32) >> 4), b, id_s, true);
+                        }
+                    tc::commit<2>(tc::smem_addr(&x->kfree[ks]));
+                    if (n == 2) tc::commit<2>(tc::smem_addr(&x->sfull));
+                }
+                __syncwarp();
+                if (++ks == kKStages) ks = 0, kphase ^= 1;
+            }
+            if (t > w.t0) values(j - 1, t - 1 == w.t0);
+        }
+        values(j - 1, w.t1 - 1 == w.t0);
+    }
+    drain(x);
+}
+
+// A query's 576 channels to tensor and shared memory (each row by two threads, for lanes 0-63 and 64-127: a pair's
+// product of 128 rows computes half of its columns in each, and each reads its own copy of A).  Returns the power of
+// two that a bf16 query is scaled by into fp16.
+template <typename T, bool E4M3> __device__ int bring_query(const SharedArgs& g, uint32_t sbase, uint32_t tmem, int64_t query, uint32_t qready)
+{
+    const int row = threadIdx.x & 63;
+    const bool ok = query < g.queries;
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const T*>(g.a.q) + (ok ? offset_of(g, query, g.a.q_stride) : 0));
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    int up = 0;
+    if constexpr (E4M3 && HsType<T>::is_bf16) {
+        float top = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < 9; ++c) {
+            uint4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = ok ? q[8 * c + i] : zero;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, largest_bf16(v[i]));
+        }
+        up = power_up(top);
+    }
+#pragma unroll
+    for (int c = 0; c < 9; ++c) {
+        uint32_t r[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint4 v = ok ? q[8 * c + i] : zero;
+            if constexpr (E4M3 && HsType<T>::is_bf16) v = bf16_to_half(v, power_of_two(up));
+            if (c < kQTmem)
+                r[4 * i] = v.x, r[4 * i + 1] = v.y, r[4 * i + 2] = v.z, r[4 * i + 3] = v.w;
+            else if ((i >> 2) == (int)(threadIdx.x >> 6))  // each of the two threads stores half
+                tc::st_shared16(sbase + (c - kQTmem) * kBlock + row * 128 + ((i ^ (row & 7)) << 4), v.x, v.y, v.z, v.w);
+        }
+        if (c < kQTmem) tc::tmem_st32(tmem + kColQ + 32 * c, r);
+    }
+    tc::tmem_wait_st();
+    tc::fence_async_shared();
+    tc::fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) tc::mbar_arrive_cluster(qready);
+    return up;
+}
+
+// The two parts of a query, the prefix's (sum at reference ref, in powers of two) and the own rows' (lse): the
+// factors on the prefix's unscaled sums and on the own rows' output, and the whole's lse.
+struct Mix {
+    float prefix, own, lse;
+};
+__device__ __forceinline__ Mix mix(float ref, float sum, float own_lse)
+{
+    const bool some = sum > 0.f || sum != sum, mine = own_lse != -INFINITY;
+    if (!some && !mine) return {0.f, 0.f, -INFINITY};
+    const float l = own_lse * 1.4426950408889634f;
+    const float top = !mine ? ref : !some ? l : fmaxf(ref, l);
+    const float a = some ? tc::exp2_approx(ref - top) : 0.f, b = mine ? tc::exp2_approx(l - top) : 0.f;
+    const float total = (some ? sum * a : 0.f) + b, inv = 1.f / total;
+    return {a * inv, b * inv, (top + log2f(total)) * 0.6931471805599453f};
+}
+
+template <typename T, bool E4M3> __device__ void soften(const SharedArgs& g, uint32_t sbase, Aux* x, uint32_t rank, int pair)
+{
+    const hs_attend_t& a = g.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = threadIdx.x & 63, half = threadIdx.x >> 6;
+    const uint32_t tmem = x->tmem + ((uint32_t)warp << 21);  // this warp's 32 lanes
+    const uint32_t sread = tc::map_to_rank(tc::smem_addr(&x->sread), 0), pready = tc::map_to_rank(tc::smem_addr(&x->pready), 0),
+                   qready = tc::map_to_rank(tc::smem_addr(&x->qready), 0);
+    const float c0 = a.scale * 1.4426950408889634f;
+    long long j = 0;
+    Stretch w(g, x->piece);
+    while (w.next()) {
+        const int64_t query = (int64_t)w.at * 128 + rank * 64 + row;
+        float ref = 0.f, sum = 0.f;
+        if (w.t0 < w.t1) {
+            const int up = bring_query<T, E4M3>(g, sbase, tmem, query, qready);
+            const float c = E4M3 ? power_of_two(-up) * c0 : c0;
+            const int64_t limit = query < g.queries ? seen_rows(g, request_of(g, query)) : 0;
+            bool seen = false;  // a row that counts has been met: ref is a maximum
+            for (int t = w.t0; t < w.t1; ++t, ++j) {
+                const int64_t key0 = (int64_t)t * kRows + 64 * half;
+                const int live = (int)min(max(limit - key0, (int64_t)0), (int64_t)64);  // keys of these 64 that count
+                const int s = j & 1;
+                float wt[E4M3 ? 64 : 1];
+                if constexpr (E4M3)
+#pragma unroll
+                    for (int i = 0; i < 64; i += 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(g.scales + key0 + i);
+                        wt[i] = f.x, wt[i + 1] = f.y, wt[i + 2] = f.z, wt[i + 3] = f.w;
+                    }
+                wait(tc::smem_addr(&x->sfull), j & 1, &x->dead, g.error);
+                tc::fence_after();
+                uint32_t r[2][32];
+                tc::tmem_ld32(tmem + kColS, r[0]);
+                tc::tmem_ld32(tmem + kColS + 32, r[1]);
+                tc::tmem_wait_ld(r[0]);
+                tc::tmem_wait_ld(r[1]);
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_cluster(sread);  // the next tile's scores may come
+                float v[64], top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 64; ++i) {
+                    v[i] = __uint_as_float(r[i >> 5][i & 31]) * c;
+                    if constexpr (E4M3) v[i] *= wt[i];
+                }
+                if (live < 64)
+#pragma unroll
+                    for (int i = 0; i < 64; ++i)
+                        if (i >= live) v[i] = -INFINITY;
+                if constexpr (E4M3) {
+#pragma unroll
+                    for (int i = 0; i < 64; i += 8) {
+                        float lw[8];
+                        ::Piece<__half>::unpack(*reinterpret_cast<const uint4*>(g.log_scales + key0 + i), lw);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) top = fmaxf(top, v[i + k] + lw[k]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 64; i += 2) top = tc::max3(top, v[i], v[i + 1]);
+                }
+                x->red[s][threadIdx.x] = top;
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                top = fmaxf(top, x->red[s][threadIdx.x ^ 64]);
+                float keep = 1.f;
+                if (top > -INFINITY && (!seen || top > ref + 8.f)) {
+                    keep = tc::exp2_approx(fminf(ref - top, 126.f));
+                    sum *= keep;
+                    ref = top;
+                }
+                const bool scale_o = seen && keep != 1.f;
+                seen = seen || top > -INFINITY;
+                uint32_t e[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    float p0 = tc::exp2_approx(v[2 * i] - ref), p1 = tc::exp2_approx(v[2 * i + 1] - ref);
+                    sum += p0 + p1;
+                    if constexpr (E4M3) p0 *= wt[2 * i], p1 *= wt[2 * i + 1];
+                    e[i] = pack2<std::conditional_t<E4M3, __half, T>>(p0, p1);
+                }
+                // P's buffer and O are free once the last tile's product is done
+                if (j >= 1) wait(tc::smem_addr(&x->pvdone), (j - 1) & 1, &x->dead, g.error);
+                if (__any_sync(~0u, scale_o)) {
+                    if (!scale_o) keep = 1.f;
+                    tc::fence_after();
+#pragma unroll 1
+                    for (int n = 0; n < 256; n += 32) {
+                        tc::tmem_ld32(tmem + kColO + n, r[0]);
+                        tc::tmem_wait_ld(r[0]);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) r[0][i] = __float_as_uint(__uint_as_float(r[0][i]) * keep);
+                        tc::tmem_st32(tmem + kColO + n, r[0]);
+                    }
+                    tc::tmem_wait_st();
+                }
+                const uint32_t dst = sbase + kOffP + half * kBlock + row * 128;
+#pragma unroll
+                for (int n = 0; n < 8; ++n) tc::st_shared16(dst + ((n ^ (row & 7)) << 4), e[4 * n], e[4 * n + 1], e[4 * n + 2], e[4 * n + 3]);
+                tc::fence_async_shared();
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_cluster(pready);
+            }
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            x->red[0][threadIdx.x] = sum;
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            sum += x->red[0][threadIdx.x ^ 64];
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            wait(tc::smem_addr(&x->pvdone), (j - 1) & 1, &x->dead, g.error);
+            tc::fence_after();
+        }
+        // The piece's end: O and the sums leave.
+        const bool there = query < g.queries, some = sum > 0.f || sum != sum;
+        if (w.whole) {
+            // Through P's buffer, so that eight lanes write 128 bytes of a query together: 64 channels of each half
+            // at a time, [half][query][128 B].
+            const Mix m = mix(ref, sum, there && g.own_lse ? g.own_lse[query] : -INFINITY);
+            const bool mine = there && m.own != 0.f;
+            T* out = static_cast<T*>(a.out);
+            const uint4* own = reinterpret_cast<const uint4*>(out + (there ? offset_of(g, query, a.out_stride) : 0) + 256 * half);
+            const uint32_t buffer = sbase + kOffP + threadIdx.x * 128;
+#pragma unroll 1
+            for (int n = 0; n < 256; n += 64) {
+                uint4 old[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) old[i] = mine ? own[n / 8 + i] : make_uint4(0, 0, 0, 0);
+                uint32_t r[32];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    __syncwarp();
+                    tc::tmem_ld32(tmem + kColO + n + 32 * q, r);
+                    tc::tmem_wait_ld(r);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float f[8], h[8];
+                        ::Piece<T>::unpack(old[4 * q + i], h);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) f[k] = (some ? __uint_as_float(r[8 * i + k]) * m.prefix : 0.f) + (mine ? h[k] * m.own : 0.f);
+                        const uint4 o = ::Piece<T>::pack(f);
+                        tc::st_shared16(buffer + (((4 * q + i) ^ (row & 7)) << 4), o.x, o.y, o.z, o.w);
+                    }
+                }
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int at = 16 * i + (threadIdx.x >> 3), ch = threadIdx.x & 7;  // of 128 rows of the buffer
+                    const int64_t to = (int64_t)w.at * 128 + rank * 64 + (at & 63);
+                    const uint4 o = tc::ld_shared16(sbase + kOffP + at * 128 + ((ch ^ (at & 7)) << 4));
+                    if (to < g.queries)
+                        *reinterpret_cast<uint4*>(out + offset_of(g, to, a.out_stride) + 256 * (at >> 6) + n + 8 * ch) = o;
+                }
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+            }
+            if (there && a.lse && half == 0) a.lse[query] = m.lse;
+        } else {
+            PairSums* part = g.parts + 2 * pair + (w.t0 == 0 ? 1 : 0);
+#pragma unroll 1
+            for (int n = 0; n < 256; n += 32) {
+                uint32_t r[32];
+                __syncwarp();
+                tc::tmem_ld32(tmem + kColO + n, r);
+                tc::tmem_wait_ld(r);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) part->o[rank][n + i][threadIdx.x] = __uint_as_float(r[i]);
+            }
+            part->ref[rank][threadIdx.x] = ref;
+            part->sum[rank][threadIdx.x] = sum;
+        }
+        tc::fence_before();
+    }
+}
+
+template <typename T, bool E4M3>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    hs_attend_shared_kernel(const __grid_constant__ SharedArgs g, const __grid_constant__ CUtensorMap map)
+{
+    using Operand = std::conditional_t<E4M3, __half, T>;
+    extern __shared__ __align__(1024) uint8_t base[];  // the swizzled blocks need 1024
+    const uint32_t sbase = tc::smem_addr(base);
+    Aux* x = reinterpret_cast<Aux*>(base + kOffAux);
+    const uint32_t rank = tc::cluster_rank();
+    const int pair = blockIdx.x >> 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (warp == 0) tc::tmem_alloc<2>(tc::smem_addr(&x->tmem), 512);
+    if (warp == 6 && lane == 0) {
+        const Piece p = g.flat ? line_piece(g, pair) : whole_piece(g, pair);
+        x->piece = p;
+        x->dead = 0;
+        if (rank == 0) g.starts[pair] = {p.count > 0 ? p.unit : -1, p.tile};
+        for (int i = 0; i < kKStages; ++i) tc::mbar_init(tc::smem_addr(&x->kfull[i]), 1), tc::mbar_init(tc::smem_addr(&x->kfree[i]), 1);
+        for (int i = 0; i < kVStages; ++i) tc::mbar_init(tc::smem_addr(&x->vfull[i]), 1), tc::mbar_init(tc::smem_addr(&x->vfree[i]), 1);
+        tc::mbar_init(tc::smem_addr(&x->qready), 8);
+        tc::mbar_init(tc::smem_addr(&x->sfull), 1);
+        tc::mbar_init(tc::smem_addr(&x->sread), 8);
+        tc::mbar_init(tc::smem_addr(&x->pready), 8);
+        tc::mbar_init(tc::smem_addr(&x->pvdone), 1);
+        tc::mbar_init(tc::smem_addr(&x->spare), 1);
+        tc::mbar_init_fence();
+    }
+    tc::fence_before();
+    __syncwarp();
+    __syncthreads();
+    tc::cluster_sync();
+    tc::fence_after();
+
+    if (x->piece.count > 0) {
+        if (warp < 4)
+            soften<T, E4M3>(g, sbase, x, rank, pair);
+        else if (warp == 4)
+            bring<true>(g, &map, sbase, x, rank);
+        else if (warp == 5)
+            bring<false>(g, &map, sbase, x, rank);
+        else if (rank == 0)
+            multiply<Operand>(g, sbase, x);
+        if (*(volatile int*)&x->dead) {  // copies may be in flight, and count on the first CTA's barriers: half a millisecond
+            const long long t0 = clock64();
+            while (clock64() - t0 < 1000000) {}
+        }
+    }
+    __syncwarp();
+    tc::fence_before();
+    __syncthreads();
+    tc::cluster_sync_relaxed();  // no CTA leaves while the other may signal it
+    tc::fence_after();
+    if (warp == 0) tc::tmem_free<2>(x->tmem, 512);
+}
+
+// Join the pieces of the units that several pairs worked on (as hs_latent_attend's) with the own rows' part.
+template <typename T, int COLS, bool SPLIT>
+__global__ void __launch_bounds__(512) hs_attend_shared_join_kernel(const __grid_constant__ SharedArgs g)
+{
+    const hs_attend_t& a = g.a;
+    int unit, first, last;
+    if (!find_cut(g.starts, g.workers, blockIdx.x, unit, first, last)) return;
+    const int t = threadIdx.x;
+    const int rank = blockIdx.y, c0 = SPLIT ? COLS * blockIdx.z : COLS * (4 * blockIdx.z + (t >> 7));
+    const int lane = t & 127, group = SPLIT ? t >> 7 : 0, half = lane >> 6;
+    const int64_t query = (int64_t)unit * 128 + rank * 64 + (lane & 63);
+    if ((int64_t)unit * 128 + rank * 64 >= g.queries) return;
+    const bool live = query < g.queries;
+    float acc[COLS], sum, top;
+    join_pieces<COLS, SPLIT>(g.parts, first, last, rank, lane, c0, group, live, acc, sum, top);
+    if (group || !live) return;
+    const Mix m = mix(top, sum, g.own_lse ? g.own_lse[query] : -INFINITY);
+    T* out = static_cast<T*>(a.out) + offset_of(g, query, a.out_stride) + 256 * half + c0;
+#pragma unroll
+    for (int k = 0; k < COLS; k += 4) {
+        float f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[i] = sum == 0.f ? 0.f : acc[k + i] * m.prefix;
+            if (m.own != 0.f) f[i] += HsType<T>::to_float(out[k + i]) * m.own;
+        }
+        *reinterpret_cast<uint2*>(out + k) = make_uint2(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]));
+    }
+    if (a.lse && half == 0 && c0 == 0) a.lse[query] = m.lse;
+}
+
+// The prefix's rows as 16-bit operands: a warp a row.  8-bit values become fp16 beside their scales (and base-2
+// logarithms; those of the last tile's absent rows too).  A row with a value that is not finite becomes zeros with
+// NaN in a rotary channel.
+template <typename T, bool E4M3>
+__global__ void __launch_bounds__(256) hs_prefix_kernel(const uint8_t* rows, int64_t row_stride, int64_t n, int64_t padded, uint4* wide,
+                                                        float* scales, __half* log_scales)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (i >= n) {
+        if (E4M3 && lane == 0 && i < padded) scales[i] = 1.f, log_scales[i] = __float2half(0.f);
+        return;
+    }
+    const uint8_t* row = rows + i * row_stride;
+    constexpr int kPieces = HS_ROW_DIM / 8;
+    uint4 v[3];
+    bool bad = false;
+    float scale = 1.f;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const int p = 32 * k + lane;
+        v[k] = make_uint4(0, 0, 0, 0);
+        if (p >= kPieces) continue;
+        if constexpr (E4M3) {
+            const uint2 e = reinterpret_cast<const uint2*>(row)[p];
+            widen(e.x, v[k].x, v[k].y);
+            widen(e.y, v[k].z, v[k].w);
+        } else {
+            v[k] = reinterpret_cast<const uint4*>(row)[p];
+        }
+        constexpr uint32_t kAll = HsType<T>::is_bf16 ? 0x7f80u : 0x7c00u;  // the exponent of what is not finite
+        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) bad = bad || (w[q] & kAll) == kAll || (w[q] >> 16 & kAll) == kAll;
+    }
+    if constexpr (E4M3) {
+        scale = *reinterpret_cast<const float*>(row + HS_ROW8_SCALE);
+        bad = bad || !(fabsf(scale) < INFINITY);
+    }
+    bad = __any_sync(~0u, bad);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const int p = 32 * k + lane;
+        if (p >= kPieces) continue;
+        if (bad) v[k] = make_uint4(p == kPieces - 1 ? 0x7fffu : 0u, 0, 0, 0);
+        wide[i * kPieces + p] = v[k];
+    }
+    if (E4M3 && lane == 0) {
+        scales[i] = bad ? 1.f : scale;
+        log_scales[i] = __float2half(bad ? 0.f : fmaxf(log2f(fabsf(scale)), kLeastLogScale));
+    }
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                   const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+std::atomic<EncodeTiledFn> g_encode{nullptr};
+
+// A map of rows [n][576] of 16 bits, in blocks of 64 x 64; rows behind the last are zeros.
+cudaError_t map_rows(CUtensorMap* map, const void* rows, int64_t n, int64_t stride)
+{
+    EncodeTiledFn fn = g_encode.load();
+    if (!fn) {  // found through the runtime, so that the library does not link the driver library itself
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
+        if (e != cudaSuccess) return e;
+        if (q != cudaDriverEntryPointSuccess || !p) return cudaErrorSymbolNotFound;
+        fn = reinterpret_cast<EncodeTiledFn>(p);
+        g_encode.store(fn);
+    }
+    const cuuint64_t dims[2] = {HS_ROW_DIM, (cuuint64_t)n}, strides[1] = {(cuuint64_t)(n > 1 ? stride : 2 * HS_ROW_DIM)};
+    const cuuint32_t box[2] = {64, 64}, step[2] = {1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(rows), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+int64_t padded_rows(int64_t n) { return (n + kRows - 1) / kRows * kRows; }
+
+// Workspace: hs_latent_attend's for the own rows (its error word is the call's), then their lse, where each pair's
+// piece starts, two partial results a pair, the prefix's rows in 16 bits, scales and their logarithms.
+struct Layout {
+    size_t lse, starts, parts, rows, scales, logs, end;
+    Layout(int batch, int positions, int heads, int64_t own_rows, int64_t prefix_rows)
+    {
+        auto after = [](size_t at, size_t bytes) { return (at + bytes + 255) / 256 * 256; };
+        lse = after(0, hs_attend_workspace_bytes(batch, positions, heads, own_rows));
+        starts = after(lse, sizeof(float) * batch * positions * (size_t)heads);
+        parts = after(starts, sizeof(Start) * kMaxPairs);
+        rows = after(parts, sizeof(PairSums) * 2 * kMaxPairs);
+        scales = after(rows, 2 * HS_ROW_DIM * (size_t)prefix_rows);
+        logs = after(scales, sizeof(float) * padded_rows(prefix_rows));
+        end = after(logs, sizeof(__half) * padded_rows(prefix_rows));
+    }
+};
+
+template <typename T, bool E4M3> cudaError_t launch(const SharedArgs& g, const CUtensorMap& map, cudaStream_t s)
+{
+    cudaError_t e = cudaFuncSetAttribute(hs_attend_shared_kernel<T, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    hs_attend_shared_kernel<T, E4M3><<<2 * g.workers, kThreads, kSmem, s>>>(g, map);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || !g.flat || g.workers <= 1) return e;
+    const int cut = g.units < g.workers - 1 ? g.units : g.workers - 1;
+    if (cut >= 16)
+        hs_attend_shared_join_kernel<T, 16, false><<<dim3(cut, 2, 256 / 64), 512, 0, s>>>(g);
+    else
+        hs_attend_shared_join_kernel<T, 4, true><<<dim3(cut, 2, 256 / 4), 512, 0, s>>>(g);
+    return cudaGetLastError();
+}
+
+template <typename T> cudaError_t run(SharedArgs& g, const hs_prefix_t& p, uint8_t* ws, const Layout& at, cudaStream_t s)
+{
+    const bool e4m3 = g.a.row_format == HS_ROWS_E4M3;
+    const void* rows = p.rows;
+    int64_t stride = p.row_stride;
+    if (e4m3 || p.lengths) {
+        const int64_t padded = padded_rows(p.n_rows);
+        const unsigned grid = (unsigned)(padded / 8);
+        const uint8_t* from = static_cast<const uint8_t*>(p.rows);
+        uint4* wide = reinterpret_cast<uint4*>(ws + at.rows);
+        float* scales = reinterpret_cast<float*>(ws + at.scales);
+        __half* logs = reinterpret_cast<__half*>(ws + at.logs);
+        if (e4m3)
+            hs_prefix_kernel<__half, true><<<grid, 256, 0, s>>>(from, p.row_stride, p.n_rows, padded, wide, scales, logs);
+        else
+            hs_prefix_kernel<T, false><<<grid, 256, 0, s>>>(from, p.row_stride, p.n_rows, padded, wide, scales, logs);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        rows = wide;
+        stride = 2 * HS_ROW_DIM;
+        g.scales = scales;
+        g.log_scales = logs;
+    }
+    CUtensorMap map;
+    const cudaError_t e = map_rows(&map, rows, p.n_rows, stride);
+    if (e != cudaSuccess) return e;
+    return e4m3 ? launch<T, true>(g, map, s) : launch<T, false>(g, map, s);
+}
+
+}  // namespace
+}  // namespace hs_attn
+
+size_t hs_attend_shared_workspace_bytes(int batch, int positions, int heads, int64_t rows, int64_t prefix_rows)
+{
+    return hs_attn::Layout(batch, positions, heads, rows, prefix_rows).end;
+}
+
+cudaError_t hs_launch_attend_shared(const hs_attend_t& a, const hs_prefix_t& p, cudaStream_t s)
+{
+    using namespace hs_attn;
+    if (p.n_rows == 0) return hs_launch_attend(a, s);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const Layout at(a.batch, a.positions, a.heads, a.slots ? a.entries : a.n_rows, p.n_rows);
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    SharedArgs g = {};
+    g.a = a;
+    g.prefix_lengths = p.lengths;
+    g.prefix_rows = p.n_rows;
+    g.queries = (int64_t)a.batch * a.positions * a.heads;
+    g.starts = reinterpret_cast<Start*>(ws + at.starts);
+    g.parts = reinterpret_cast<PairSums*>(ws + at.parts);
+    g.error = reinterpret_cast<int*>(ws);
+    if (a.n_rows > 0 && (!a.slots || a.entries > 0)) {
+        hs_attend_t own = a;
+        own.lse = reinterpret_cast<float*>(ws + at.lse);
+        g.own_lse = own.lse;
+        e = hs_launch_attend(own, s);
+        if (e != cudaSuccess) return e;
+    }
+    g.units = (int)((g.queries + 127) / 128);
+    g.cut(sms / 2 < kMaxPairs ? (sms > 1 ? sms / 2 : 1) : kMaxPairs, p.n_rows, 5, kUnitCost, kRows);
+    return a.dtype == HS_TYPE_BF16 ? run<__nv_bfloat16>(g, p, ws, at, s) : run<__half>(g, p, ws, at, s);
+}

@@ -1,5 +1,6 @@
 // Private declarations of the operators beside the swap-in path
-// (hs_latent_attend, hs_latent_prefill, hs_rms_norm).
+// (hs_latent_attend, hs_latent_attend_shared, hs_latent_prefill, hs_rms_norm,
+// hs_latent_write, hs_latent_read, hs_norm_rotate).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -19,8 +20,13 @@ inline int hs_norm_group(int dim, int carry, int group) { return group >= dim + 
 cudaError_t hs_launch_attend(const hs_attend_t& a, cudaStream_t s);
 cudaError_t hs_launch_prefill(const hs_prefill_t& a, cudaStream_t s);
 cudaError_t hs_launch_norm(const hs_norm_t& a, cudaStream_t s);
+cudaError_t hs_launch_write(const hs_write_t& a, cudaStream_t s);
+cudaError_t hs_launch_read(const hs_read_t& a, cudaStream_t s);
+cudaError_t hs_launch_rotate(const hs_rotate_t& a, cudaStream_t s);
+cudaError_t hs_launch_attend_shared(const hs_attend_t& a, const hs_prefix_t& p, cudaStream_t s);
 size_t hs_attend_workspace_bytes(int batch, int positions, int heads, int64_t rows);
 size_t hs_prefill_workspace_bytes(int64_t k_tokens, int heads);
+size_t hs_attend_shared_workspace_bytes(int batch, int positions, int heads, int64_t rows, int64_t prefix_rows);
 
 constexpr float HS_E4M3_MAX = 448.0f;
 

@@ -76,6 +76,10 @@ HS_MAX_HEADS = 1024
 HS_MAX_POSITIONS = 1024
 HS_MAX_TOKENS = 1 << 24
 HS_MAX_NORM_DIM = 16384
+HS_ROTATE_NONE = 0
+HS_ROTATE_PAIRS = 1
+HS_ROTATE_HALVES = 2
+HS_MAX_HEAD_CHANNELS = 1024
 
 
 class HsError(RuntimeError):
@@ -169,6 +173,78 @@ class hs_norm_t(ctypes.Structure):
     ]
 
 
+class hs_write_t(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32),
+        ("row_format", ctypes.c_int32),
+        ("rotation", ctypes.c_int32),
+        ("batch", ctypes.c_int32),
+        ("tokens", ctypes.c_int64),
+        ("x", ctypes.c_void_p),
+        ("x_stride", ctypes.c_int64),
+        ("weight", ctypes.c_void_p),
+        ("eps", ctypes.c_float),
+        ("positions", ctypes.c_void_p),
+        ("inv_freq", ctypes.c_void_p),
+        ("start", ctypes.c_void_p),
+        ("lengths", ctypes.c_void_p),
+        ("rows", ctypes.c_void_p),
+        ("n_rows", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+        ("request_stride", ctypes.c_int64),
+    ]
+
+
+class hs_read_t(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32),
+        ("row_format", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("batch", ctypes.c_int32),
+        ("entries", ctypes.c_int32),
+        ("tokens", ctypes.c_int64),
+        ("rows", ctypes.c_void_p),
+        ("n_rows", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+        ("request_stride", ctypes.c_int64),
+        ("slots", ctypes.c_void_p),
+        ("slots_stride", ctypes.c_int64),
+        ("start", ctypes.c_void_p),
+        ("lengths", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("out_stride", ctypes.c_int64),
+    ]
+
+
+class hs_rotate_t(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32),
+        ("rotation", ctypes.c_int32),
+        ("dim", ctypes.c_int32),
+        ("rope_at", ctypes.c_int32),
+        ("rope", ctypes.c_int32),
+        ("heads", ctypes.c_int32 * 2),
+        ("tokens", ctypes.c_int64),
+        ("x", ctypes.c_void_p * 2),
+        ("x_stride", ctypes.c_int64 * 4),  # [array][token, head]
+        ("weight", ctypes.c_void_p * 2),
+        ("eps", ctypes.c_float),
+        ("positions", ctypes.c_void_p),
+        ("inv_freq", ctypes.c_void_p),
+        ("out", ctypes.c_void_p * 2),
+        ("out_stride", ctypes.c_int64 * 4),
+    ]
+
+
+class hs_prefix_t(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_void_p),
+        ("n_rows", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+        ("lengths", ctypes.c_void_p),
+    ]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError("libhs.so is not built (run __graft_entry__.build() or "
@@ -217,6 +293,11 @@ def _load():
         "hs_latent_prefill_workspace": ([ctypes.c_int64, I], Z),
         "hs_latent_prefill": ([P, P], I),
         "hs_rms_norm": ([P, P], I),
+        "hs_latent_write": ([P, P], I),
+        "hs_latent_read": ([P, P], I),
+        "hs_norm_rotate": ([P, P], I),
+        "hs_latent_attend_shared_workspace": ([I, I, I, ctypes.c_int64, ctypes.c_int64, I], Z),
+        "hs_latent_attend_shared": ([P, P, P], I),
         "hs_error_string": ([I], ctypes.c_char_p),
     }
     for name, (args, res) in sig.items():
@@ -557,8 +638,13 @@ def hs_profile_events(h: int, before_copy=None, after_copy=None) -> None:
 _ATTEND = struct.Struct("@6iqP3qPqqP2qPP3qPfPN")
 _PREFILL = struct.Struct("@4i2qP2qPqPPPPP2qPfPN")
 _NORM = struct.Struct("@4iqPqPqPqPfPqPq")
-assert (_ATTEND.size, _PREFILL.size, _NORM.size) == tuple(
-    ctypes.sizeof(t) for t in (hs_attend_t, hs_prefill_t, hs_norm_t))
+_WRITE = struct.Struct("@4iqPqPfPPPPPqqq")
+_READ = struct.Struct("@5iqPqqqPqPPPq")
+_ROTATE = struct.Struct("@7iq2P4q2PfPP2P4q")
+_PREFIX = struct.Struct("@PqqP")
+assert (_ATTEND.size, _PREFILL.size, _NORM.size, _WRITE.size, _READ.size, _ROTATE.size, _PREFIX.size) == tuple(
+    ctypes.sizeof(t) for t in (hs_attend_t, hs_prefill_t, hs_norm_t, hs_write_t, hs_read_t, hs_rotate_t,
+                               hs_prefix_t))
 _ROW_WIDTH = {HS_ROWS_16BIT: 2 * HS_ROW_DIM, HS_ROWS_E4M3: HS_ROW8_BYTES}
 _TYPES = {}  # torch dtype -> HS_TYPE_*, filled at the first call (torch is imported late)
 
@@ -672,6 +758,12 @@ def hs_latent_attend(q, rows, out, scale: float, slots=None, lengths=None,
     [B][P][K], from hs_resolve; entries outside [0, N) are absent) or lengths
     (int32 [B], the P positions being the last).  lse: fp32 [B][P][H] or None.
     """
+    _check(lib.hs_latent_attend(_attend_block(q, rows, out, scale, slots, lengths, row_format, lse, workspace),
+                                _stream(stream)), "hs_latent_attend")
+
+
+def _attend_block(q, rows, out, scale, slots, lengths, row_format, lse, workspace):
+    """The checked hs_attend_t of a call, packed."""
     import torch
     dtype, device, shape = q.dtype, q.device, q.shape
     kind = _type_of(q, "q")
@@ -694,10 +786,39 @@ def hs_latent_attend(q, rows, out, scale: float, slots=None, lengths=None,
     lse_at = _lse_of(lse, (B, P, H), device)
     space, space_bytes = _workspace_of(workspace, device)
     _on_current_device(device)
-    _check(lib.hs_latent_attend(
-        _ATTEND.pack(kind, row_format, B, P, H, entries, n_rows, q.data_ptr(), q0, q1, q2, address,
-                     row_stride, request_stride, slots_at, s0, s1, lengths_at, out.data_ptr(), o0, o1,
-                     o2, lse_at, scale, space, space_bytes), _stream(stream)), "hs_latent_attend")
+    return _ATTEND.pack(kind, row_format, B, P, H, entries, n_rows, q.data_ptr(), q0, q1, q2, address,
+                        row_stride, request_stride, slots_at, s0, s1, lengths_at, out.data_ptr(), o0, o1,
+                        o2, lse_at, scale, space, space_bytes)
+
+
+def hs_latent_attend_shared_workspace(batch: int, positions: int, heads: int, rows: int, prefix_rows: int,
+                                      row_format: int = HS_ROWS_16BIT) -> int:
+    """Bytes of workspace of hs_latent_attend_shared: hs_latent_attend's sizes, and the prefix's rows."""
+    n = int(lib.hs_latent_attend_shared_workspace(int(batch), int(positions), int(heads), int(rows),
+                                                  int(prefix_rows), int(row_format)))
+    if n == 0:
+        raise HsError(HS_ERR_ARG, "hs_latent_attend_shared_workspace")
+    return n
+
+
+def hs_latent_attend_shared(q, prefix, rows, out, scale: float, slots=None, lengths=None, prefix_lengths=None,
+                            row_format: int = HS_ROWS_16BIT, lse=None, workspace=None, stream=None) -> None:
+    """hs_latent_attend of requests that share a prefix: each attends to the prefix's first
+    prefix_lengths[b] rows (int32 [B]; None: all of them) and to its own rows.
+
+    prefix: a tensor [n][576] of q's type, or a uint8 tensor [n][bytes] of rows in
+    `row_format`, which is the own rows' form too; the rest as in hs_latent_attend (own
+    rows may be none: N or K 0).
+    """
+    block = _attend_block(q, rows, out, scale, slots, lengths, row_format, lse, workspace)
+    address, n, stride, _ = _rows_of(prefix, row_format, q.dtype, q.device, ())
+    lengths_at = 0
+    if prefix_lengths is not None:
+        import torch
+        _want(prefix_lengths, "prefix_lengths", (q.shape[0],), torch.int32, q.device)
+        lengths_at = prefix_lengths.data_ptr()
+    _check(lib.hs_latent_attend_shared(block, _PREFIX.pack(address, n, stride, lengths_at), _stream(stream)),
+           "hs_latent_attend_shared")
 
 
 def hs_latent_prefill_workspace(k_tokens: int, heads: int) -> int:
@@ -781,6 +902,185 @@ def hs_rms_norm(x, weight, out, eps: float, residual=None, residual_out=None, ca
         _NORM.pack(kind, dim, carry, group, n, x.data_ptr(), x0, r_at, r0, ro_at, ro0,
                    weight.data_ptr(), eps, out.data_ptr(), o0, s_at, s0), _stream(stream)),
         "hs_rms_norm")
+
+
+def _turn_of(positions, inv_freq, rotation, tokens, pairs, device):
+    """(rotation, address of the positions, of the frequencies): none without positions."""
+    import torch
+    if positions is None and inv_freq is None:
+        return HS_ROTATE_NONE, 0, 0
+    if positions is None or inv_freq is None:
+        raise ValueError("give both positions and inv_freq, or neither")
+    if rotation not in (HS_ROTATE_PAIRS, HS_ROTATE_HALVES):
+        raise ValueError("unknown rotation %r" % (rotation,))
+    _want(positions, "positions", (tokens,), torch.int32, device)
+    _want(inv_freq, "inv_freq", (pairs,), torch.float32, device)
+    return rotation, positions.data_ptr(), inv_freq.data_ptr()
+
+
+def _places_of(start, lengths, device, B):
+    import torch
+    _want(start, "start", (B + 1,), torch.int32, device)
+    if lengths is None:
+        return start.data_ptr(), 0
+    _want(lengths, "lengths", (B,), torch.int32, device)
+    return start.data_ptr(), lengths.data_ptr()
+
+
+def _pool_of(h, row_format):
+    """(address, rows a request, row stride, request stride) of a handle's host pool."""
+    if h.R < _ROW_WIDTH.get(row_format, 1 << 30):
+        raise ValueError("the handle has rows of %d bytes" % h.R)
+    return hs_host_pool(h.h), h.H, h.R, h.H * h.R
+
+
+def hs_latent_write(x, rows, weight=None, eps: float = 0.0, positions=None, inv_freq=None,
+                    rotation: int = HS_ROTATE_PAIRS, start=None, lengths=None,
+                    row_format: int = HS_ROWS_16BIT, stream=None) -> None:
+    """Cache rows of tokens from their projections x [N][576]: the first 512 channels normed (with
+    weight [512]), the last 64 rotated (with positions int32 [N] and inv_freq fp32 [32]).
+
+    rows: without start, [at least N][576] of x's type or uint8 [..][bytes], token t's being row t
+    (what hs_append takes).  With start (int32 [B + 1]) and lengths (int32 [B]) [B][rows][...], or a
+    Handle (its host pool): request b's tokens start[b]..start[b + 1] are the last of its lengths[b]
+    rows.
+    """
+    dtype, device, shape = x.dtype, x.device, x.shape
+    kind = _type_of(x, "x")
+    if len(shape) != 2:
+        raise ValueError("x must have 2 axes, has %d" % len(shape))
+    n = shape[0]
+    x0, _ = _want(x, "x", (n, HS_ROW_DIM), dtype, device)
+    w_at = 0
+    if weight is not None:
+        _want(weight, "weight", (HS_LATENT_DIM,), dtype, device)
+        w_at = weight.data_ptr()
+    turn, positions_at, freq_at = _turn_of(positions, inv_freq, rotation, n, HS_ROPE_DIM // 2, device)
+    batch = start_at = lengths_at = 0
+    if start is None:
+        if lengths is not None or isinstance(rows, Handle):
+            raise ValueError("lengths and a handle need start")
+        address, n_rows, row_stride, request_stride = _rows_of(rows, row_format, dtype, device, ())
+    else:
+        if lengths is None:
+            raise ValueError("start needs lengths")
+        batch = start.numel() - 1
+        start_at, lengths_at = _places_of(start, lengths, device, batch)
+        if isinstance(rows, Handle):
+            if rows.B != batch:
+                raise ValueError("the handle has %d requests" % rows.B)
+            address, n_rows, row_stride, request_stride = _pool_of(rows, row_format)
+        else:
+            address, n_rows, row_stride, request_stride = _rows_of(rows, row_format, dtype, device, (batch,))
+    _on_current_device(device)
+    _check(lib.hs_latent_write(
+        _WRITE.pack(kind, row_format, turn, batch, n, x.data_ptr(), x0, w_at, eps, positions_at, freq_at,
+                    start_at, lengths_at, address, n_rows, row_stride, request_stride), _stream(stream)),
+        "hs_latent_write")
+
+
+def hs_latent_read(rows, out, slots=None, start=None, lengths=None, row_format: int = HS_ROWS_16BIT,
+                   dtype=None, stream=None) -> None:
+    """Rows as values, in bf16, fp16 or fp32.  Either slots int32 [B][K] into out [B][K][576] (a Handle's
+    rows are then its device buffer; entries outside [0, N) give zeros), or start int32 [B + 1] into out
+    [T][576], whose rows start[b]..start[b + 1] are the last of request b's lengths[b] rows (int32 [B];
+    None: its first rows; a Handle's are its host pool).
+
+    rows: [B][N][576], uint8 [B][N][bytes] or a Handle; dtype: the type of 16-bit rows that are
+    given as bytes (default: out's).
+    """
+    import torch
+    device = out.device
+    out_kind = _type_of(out, "out", fp32=True)
+    if (slots is None) == (start is None):
+        raise ValueError("give slots or start, and not both")
+    if dtype is None:
+        dtype = rows.dtype if getattr(rows, "dtype", None) in (torch.bfloat16, torch.float16) else out.dtype
+        if dtype == torch.float32:
+            if row_format == HS_ROWS_16BIT:
+                raise ValueError("dtype: say which type the rows have")
+            dtype = torch.bfloat16
+    kind = HS_TYPE_BF16 if dtype == torch.bfloat16 else HS_TYPE_FP16
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("dtype: type %s is not taken" % (dtype,))
+    entries = slots_at = s0 = start_at = lengths_at = 0
+    if slots is not None:
+        if lengths is not None:
+            raise ValueError("lengths need start")
+        if slots.dim() != 2:
+            raise ValueError("slots must have 2 axes, has %d" % slots.dim())
+        B, entries = slots.shape
+        s0, _ = _want(slots, "slots", (B, entries), torch.int32, device)
+        slots_at = slots.data_ptr() or 16  # an empty list has no address
+        o0, o1, _ = _want(out, "out", (B, entries, HS_ROW_DIM), out.dtype, device)
+        if B > 1 and entries > 1 and o0 != entries * o1:
+            raise ValueError("out's rows must be evenly apart")
+        tokens, o0 = B * entries, o1 if entries > 1 else o0
+    else:
+        B = start.numel() - 1
+        start_at, lengths_at = _places_of(start, lengths, device, B)
+        if out.dim() != 2:
+            raise ValueError("out must have 2 axes, has %d" % out.dim())
+        tokens = out.shape[0]
+        o0, _ = _want(out, "out", (tokens, HS_ROW_DIM), out.dtype, device)
+    if isinstance(rows, Handle) and start is not None:
+        if rows.B != B:
+            raise ValueError("the handle has %d requests" % rows.B)
+        address, n_rows, row_stride, request_stride = _pool_of(rows, row_format)
+    else:
+        address, n_rows, row_stride, request_stride = _rows_of(rows, row_format, dtype, device, (B,))
+    _on_current_device(device)
+    _check(lib.hs_latent_read(
+        _READ.pack(kind, row_format, out_kind, B, entries, tokens, address, n_rows, row_stride,
+                   request_stride, slots_at, s0, start_at, lengths_at, out.data_ptr(), o0),
+        _stream(stream)), "hs_latent_read")
+
+
+def hs_norm_rotate(q, q_out, k=None, k_out=None, q_weight=None, k_weight=None, eps: float = 0.0,
+                   positions=None, inv_freq=None, rotation: int = HS_ROTATE_PAIRS, rope_at=None,
+                   stream=None) -> None:
+    """Norm of each head's channels (with a weight [D]) and their rotation, of q [N][H][D] into q_out and,
+    where given, of k [N][Hk][D] into k_out; bf16, fp16 or fp32.
+
+    positions int32 [N] and inv_freq fp32 [rope / 2] rotate the channels rope_at .. rope_at + rope of
+    each head (rope_at None: the last ones).  q_out may be q, k_out k.
+    """
+    dtype, device, shape = q.dtype, q.device, q.shape
+    kind = _type_of(q, "q", fp32=True)
+    if len(shape) != 3:
+        raise ValueError("q must have 3 axes, has %d" % len(shape))
+    n, heads, dim = shape
+    rope = 0
+    if inv_freq is not None:
+        rope = 2 * inv_freq.numel()
+    if rope_at is None:
+        rope_at = dim - rope
+    if not 0 <= rope_at <= dim - rope:
+        raise ValueError("%d rotary channels at %d do not fit into %d" % (rope, rope_at, dim))
+    turn, positions_at, freq_at = _turn_of(positions, inv_freq, rotation, n, rope // 2, device)
+    x0, x1, _ = _want(q, "q", (n, heads, dim), dtype, device)
+    o0, o1, _ = _want(q_out, "q_out", (n, heads, dim), dtype, device)
+    k_heads = k_at = k0 = k1 = ko_at = ko0 = ko1 = w_at = kw_at = 0
+    if (k is None) != (k_out is None) or (k is None and k_weight is not None):
+        raise ValueError("give both k and k_out, or neither (nor k_weight)")
+    if k is not None:
+        if k.dim() != 3:
+            raise ValueError("k must have 3 axes, has %d" % k.dim())
+        k_heads = k.shape[1]
+        k0, k1, _ = _want(k, "k", (n, k_heads, dim), dtype, device)
+        ko0, ko1, _ = _want(k_out, "k_out", (n, k_heads, dim), dtype, device)
+        k_at, ko_at = k.data_ptr(), k_out.data_ptr()
+        if k_weight is not None:
+            _want(k_weight, "k_weight", (dim,), dtype, device)
+            kw_at = k_weight.data_ptr()
+    if q_weight is not None:
+        _want(q_weight, "q_weight", (dim,), dtype, device)
+        w_at = q_weight.data_ptr()
+    _on_current_device(device)
+    _check(lib.hs_norm_rotate(
+        _ROTATE.pack(kind, turn, dim, rope_at, rope, heads, k_heads, n, q.data_ptr(), k_at, x0, x1, k0, k1, w_at,
+                     kw_at, eps, positions_at, freq_at, q_out.data_ptr(), ko_at, o0, o1, ko0, ko1),
+        _stream(stream)), "hs_norm_rotate")
 
 
 class Handle:

@@ -775,6 +775,178 @@ typedef struct {
 
 int hs_rms_norm(const hs_norm_t* args, hs_stream_t stream);
 
+/*
+ * Rotation of channels by a token's position: pair i of a token at position t
+ * turns by the angle t * inv_freq[i] (radians),
+ *   (a, b) -> (a cos - b sin, a sin + b cos),
+ * where the pairs of n rotary channels are
+ *   HS_ROTATE_PAIRS   channels 2i and 2i + 1
+ *   HS_ROTATE_HALVES  channels i and i + n / 2
+ * HS_ROTATE_NONE leaves the channels as they are (positions and inv_freq are
+ * then not read).  positions: device int32 [tokens], any value; inv_freq: device
+ * fp32 [n / 2], of magnitude below 2^16.  The angle is reduced to one turn in
+ * integers, exact to 2^-31 of a turn at any position for frequencies up to 1
+ * (above, the frequency times that), before its sine and cosine in fp32.
+ */
+#define HS_ROTATE_NONE   0
+#define HS_ROTATE_PAIRS  1
+#define HS_ROTATE_HALVES 2
+
+/*
+ * Write cache rows: for each token t, from its projection x[t] (512 latent, 64
+ * rotary channels),
+ *   y = [x[:512] / sqrt(mean(x[:512]^2) + eps) * weight ; rotated x[512:]]
+ * as a row in the form `row_format` (HS_ROWS_E4M3: scale = max|y| / 448, values
+ * e4m3(y / scale) with the quotient in fp32; all zeros: scale 0; a NaN makes the
+ * scale NaN).  Without weight (NULL) the latent channels stay as they are.
+ * Each row is written once and whole, but for the 12 last bytes of an 8-bit row
+ * and what lies between rows, which are left as they were.  Where it goes:
+ *   start NULL  row t of `rows` (batch is ignored; n_rows >= tokens): the rows
+ *               that hs_append takes
+ *   start       device int32 [batch + 1], non-decreasing from 0: tokens
+ *               [start[b], start[b + 1]) are request b's, the last of its
+ *               lengths[b] (device int32 [batch], these tokens included, as in
+ *               hs_latent_attend): the i-th of n goes to row lengths[b] - n + i of
+ *               request b.  Not written: tokens of no request, and rows outside
+ *               [0, n_rows).  (start is clamped to [0, tokens].)
+ * So no two tokens go to one row; with batch > 1, request_stride has to keep the
+ * requests' rows apart.  `rows` is device memory, or pinned host memory mapped
+ * into the device address space (a handle's hs_host_pool: n_rows = H, row_stride
+ * = R, request_stride = H * R; a prompt's rows then cross the host link once, as
+ * they are written).
+ *   x       [tokens][576] of `dtype` (bf16 or fp16, also the type of 16-bit
+ *           rows), channels contiguous, x_stride elements between tokens, a
+ *           multiple of 8; x, rows and weight 16-byte aligned, row_stride and
+ *           request_stride in bytes, multiples of 16
+ *   weight  [512] of `dtype`
+ * Source: no passage (the producer of the rows; the pages start from the rows).
+ */
+typedef struct {
+    int32_t dtype;
+    int32_t row_format;
+    int32_t rotation;      /* HS_ROTATE_* */
+    int32_t batch;
+    int64_t tokens;
+    const void* x;
+    int64_t x_stride;
+    const void* weight;
+    float eps;
+    const int32_t* positions;
+    const float* inv_freq; /* [32] */
+    const int32_t* start;
+    const int32_t* lengths;
+    void* rows;
+    int64_t n_rows, row_stride, request_stride;
+} hs_write_t;
+
+int hs_latent_write(const hs_write_t* args, hs_stream_t stream);
+
+/*
+ * Read rows back as values, out[t] = the row's 576 channels (times its scale),
+ * each rounded once to out's type:
+ *   slots  device int32 [batch][entries], slots_stride between requests: out row
+ *          b * entries + i is row slots[b][i] of request b; an entry < 0 or >=
+ *          n_rows gives zeros (tokens must be batch * entries)
+ *   start  device int32 [batch + 1] as in hs_latent_write: request b's n out rows
+ *          [start[b], start[b + 1]) are its rows lengths[b] - n + i (lengths
+ *          NULL: row i), zeros outside [0, n_rows).  Out rows of no request are
+ *          left as they were.
+ * Exactly one of the two is not NULL.  The out rows of ragged contexts are what
+ * hs_latent_prefill takes as its rows (k_start = start).
+ *   rows   n_rows rows a request in `row_format`; 16-bit rows are of `dtype`;
+ *          strides, alignment and memory as in hs_latent_write
+ *   out    [tokens][576] of out_dtype (bf16, fp16 or fp32), out_stride elements
+ *          between rows (576 at least); 16-byte aligned, rows too
+ * Source: no passage (the reader of the rows).
+ */
+typedef struct {
+    int32_t dtype;
+    int32_t row_format;
+    int32_t out_dtype;
+    int32_t batch, entries;
+    int64_t tokens;
+    const void* rows;
+    int64_t n_rows, row_stride, request_stride;
+    const int32_t* slots;
+    int64_t slots_stride;
+    const int32_t* start;
+    const int32_t* lengths;
+    void* out;
+    int64_t out_stride;
+} hs_read_t;
+
+int hs_latent_read(const hs_read_t* args, hs_stream_t stream);
+
+/*
+ * Norm of each head's channels and their rotation, for one or two arrays of heads
+ * (queries, and keys where there are any) of the same tokens:
+ *   y = x / sqrt(mean(x^2) + eps) * weight   over a head's `dim` channels
+ *   out = y with channels [rope_at, rope_at + rope) rotated
+ * Without an array's weight (NULL) its y = x.  fp32 throughout, each output
+ * rounded once.  With weight NULL and strides, it rotates the last 64 of a
+ * query's 192 channels, or writes them rotated into the last 64 of an absorbed
+ * query's 576.
+ *   x, out  [tokens][heads][dim] of `dtype` (bf16, fp16 or fp32), channels
+ *           contiguous, strides (token, head) in elements, not negative; out's
+ *           rows apart from one another.  out may be x with x's strides; else the
+ *           two must not overlap.  Any alignment of the element; 16-byte aligned
+ *           rows (and rope_at, and half of rope for HS_ROTATE_HALVES) go faster.
+ *   weight  [dim] of `dtype`
+ * x[1] NULL: one array.  rope: even, 0 without a rotation.
+ * Source: no passage (the producer of the queries that hs_latent_prefill and
+ * hs_latent_attend take).
+ */
+#define HS_MAX_HEAD_CHANNELS 1024
+typedef struct {
+    int32_t dtype;
+    int32_t rotation;      /* HS_ROTATE_* */
+    int32_t dim, rope_at, rope;
+    int32_t heads[2];
+    int64_t tokens;
+    const void* x[2];
+    int64_t x_stride[2][2];
+    const void* weight[2];
+    float eps;
+    const int32_t* positions;
+    const float* inv_freq; /* [rope / 2] */
+    void* out[2];
+    int64_t out_stride[2][2];
+} hs_rotate_t;
+
+int hs_norm_rotate(const hs_rotate_t* args, hs_stream_t stream);
+
+/*
+ * hs_latent_attend of a batch whose requests share a prefix: request b attends to
+ * rows [0, prefix_lengths[b]) of one array of rows, all its positions and heads
+ * alike, and to its own rows as hs_latent_attend defines them (`args`: slots, or
+ * lengths, with n_rows or entries 0 where there are none); one softmax over both.
+ * The prefix is held and read once for all requests, and its products are those
+ * of all their queries together.
+ *   rows            n_rows rows of args->row_format (16-bit ones of args->dtype),
+ *                   row_stride bytes apart, a multiple of 16; 16-byte aligned
+ *   lengths         device int32 [batch], clamped to [0, n_rows]; NULL: all rows
+ *                   for every request
+ * A prefix row that a request does not see has no part in its outputs, whatever it
+ * holds; one with a value that is not finite makes the output NaN of every request
+ * that sees it.
+ * Roundings as in hs_latent_attend, and the own rows' part is rounded to `dtype`
+ * before it is joined.  out and lse: whole, as there.  With no row at all out is 0
+ * and lse -inf.
+ * The workspace call takes what hs_latent_attend's does, and the prefix's rows
+ * and form.  8-bit prefixes, and prefixes with lengths, are copied into the
+ * workspace in 16 bits at every call (1152 bytes a row).
+ * Source: no passage (as hs_latent_attend).
+ */
+typedef struct {
+    const void* rows;
+    int64_t n_rows, row_stride;
+    const int32_t* lengths;
+} hs_prefix_t;
+
+size_t hs_latent_attend_shared_workspace(int batch, int positions, int heads, int64_t rows,
+                                         int64_t prefix_rows, int row_format);
+int hs_latent_attend_shared(const hs_attend_t* args, const hs_prefix_t* prefix, hs_stream_t stream);
+
 /* Static text for a return code.  Source: no passage. */
 const char* hs_error_string(int code);
 
