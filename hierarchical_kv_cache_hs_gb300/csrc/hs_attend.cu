@@ -69,6 +69,10 @@ static_assert(kSmem <= 232448, "shared memory");
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;
 
 // Workspace: an error word, where each pair's piece starts, and two partial results a pair.
+struct Partial {
+    float o[2][256][128];  // [CTA][column][lane]
+    float ref[2][128], sum[2][128];
+};
 constexpr size_t kOffStart = 256;
 constexpr size_t kOffPartial = kOffStart + sizeof(Start) * (kMaxPairs + 4);
 
@@ -498,7 +502,7 @@ __device__ void soften(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int
         tc::fence_after();
         const int head = walk.hb * 128 + (int)rank * 64 + row;
         const bool whole = walk.t0 == 0 && walk.t1 == walk.tiles;
-        PairSums* part = reinterpret_cast<PairSums*>(ws + kOffPartial) + 2 * pair + (walk.t0 == 0 ? 1 : 0);
+        Partial* part = reinterpret_cast<Partial*>(ws + kOffPartial) + 2 * pair + (walk.t0 == 0 ? 1 : 0);
         const bool some = sum > 0.f || sum != sum;
         const float inv = some ? 1.f / sum : 0.f;
         if (whole) {
@@ -625,15 +629,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_atte
 
 // Join the pieces of the units that several pairs worked on: block x takes the
 // x-th such unit (found at the first start of a piece inside it), one CTA's half
-// of its heads.  Four groups of 128 threads, one a lane: with SPLIT they share the
-// pieces of COLS columns, else each has COLS columns of its own.
+// of its heads.  Four groups of 128 threads, one a lane: with SPLIT they take every
+// fourth piece of COLS columns, else every piece of COLS columns each; in one pass,
+// and the order of the sums is fixed.
 template <typename T, int COLS, bool SPLIT>
 __global__ void __launch_bounds__(512) hs_attend_join_kernel(const __grid_constant__ Args g, int pairs)
 {
+    constexpr int kGroups = SPLIT ? 4 : 1;  // that share pieces
+    __shared__ float tops[4][128], sums[4][128], cols[SPLIT ? 3 : 1][COLS][128];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const hs_attend_t& a = g.a;
     const uint8_t* ws = static_cast<const uint8_t*>(a.workspace);
-    const PairSums* parts = reinterpret_cast<const PairSums*>(ws + kOffPartial);
+    const Partial* parts = reinterpret_cast<const Partial*>(ws + kOffPartial);
     int unit, first, last;
     if (!find_cut(reinterpret_cast<const Start*>(ws + kOffStart), pairs, blockIdx.x, unit, first, last)) return;
     const int t = threadIdx.x;
@@ -645,9 +652,46 @@ __global__ void __launch_bounds__(512) hs_attend_join_kernel(const __grid_consta
     const int head = hb * 128 + rank * 64 + row;
     if (hb * 128 + rank * 64 >= a.heads) return;
     const bool live = head < a.heads;
-    float acc[COLS], sum, top;
-    join_pieces<COLS, SPLIT>(parts, first, last, rank, lane, c0, group, live, acc, sum, top);
+    float acc[COLS] = {}, sum = 0.f, top = -INFINITY;
+    if (live)
+#pragma unroll(COLS == 4 ? 8 : 2)
+        for (int n = first + group; n <= last; n += kGroups) {
+            const Partial& q = parts[2 * n + (n == first)];
+            const float ref = q.ref[rank][lane], l = q.sum[rank][lane];
+            float o[COLS];
+#pragma unroll
+            for (int k = 0; k < COLS; ++k) o[k] = q.o[rank][c0 + k][lane];
+            // without a branch, so that the loads of several pieces are in flight; a sum of 0: no row counted
+            const float up = l == 0.f ? top : fmaxf(top, ref), base = up == -INFINITY ? 0.f : up;
+            const float keep = tc::exp2_approx(top - base), w = l == 0.f ? 0.f : tc::exp2_approx(ref - base);
+            top = up;
+            sum = sum * keep + w * l;
+#pragma unroll
+            for (int k = 0; k < COLS; ++k) acc[k] = acc[k] * keep + (l == 0.f ? 0.f : w * o[k]);
+        }
+    if (SPLIT) {
+        tops[group][lane] = top;
+        sums[group][lane] = sum;
+        if (group)
+#pragma unroll
+            for (int k = 0; k < COLS; ++k) cols[group - 1][k][lane] = acc[k];
+        __syncthreads();
+    }
     if (group || !live) return;
+    if (SPLIT) {
+        top = fmaxf(fmaxf(tops[0][lane], tops[1][lane]), fmaxf(tops[2][lane], tops[3][lane]));
+        const float base = top == -INFINITY ? 0.f : top;
+        float w = tc::exp2_approx(tops[0][lane] - base);
+        sum *= w;
+#pragma unroll
+        for (int k = 0; k < COLS; ++k) acc[k] *= w;
+        for (int n = 1; n < 4; ++n) {
+            w = tc::exp2_approx(tops[n][lane] - base);
+            sum += w * sums[n][lane];
+#pragma unroll
+            for (int k = 0; k < COLS; ++k) acc[k] += w * cols[n - 1][k][lane];
+        }
+    }
     const bool some = sum > 0.f || sum != sum;
     const float inv = some ? 1.f / sum : 0.f;
     T* out = static_cast<T*>(a.out) + b * a.out_stride[0] + p * a.out_stride[1] + (int64_t)head * a.out_stride[2] +
@@ -685,7 +729,7 @@ template <typename T, bool E4M3> cudaError_t launch(const Args& g, cudaStream_t 
 
 size_t pair_workspace(int64_t units, int64_t tiles)
 {
-    return kOffPartial + sizeof(PairSums) * 2 * (size_t)(units * tiles < kMaxPairs ? units * tiles : kMaxPairs);
+    return kOffPartial + sizeof(Partial) * 2 * (size_t)(units * tiles < kMaxPairs ? units * tiles : kMaxPairs);
 }
 
 cudaError_t launch_pair(const hs_attend_t& a, int sms, cudaStream_t s)

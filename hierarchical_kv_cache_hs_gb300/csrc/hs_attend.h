@@ -1,5 +1,5 @@
 // What the kernels of hs_latent_attend and hs_latent_attend_shared share: how the work is
-// cut, which rows a tile holds, how 8-bit rows become operands, and the joining of pieces.
+// cut, which rows a tile holds, and how 8-bit rows become operands.
 #pragma once
 
 #include <type_traits>
@@ -314,62 +314,6 @@ __device__ __forceinline__ bool find_cut(const Start* start, int workers, int x,
 }
 
 constexpr int kMaxPairs = 76;  // pairs of SMs
-
-// What a pair of SMs leaves of a unit that it does not have whole: the sums of 128 queries, unscaled.
-struct PairSums {
-    float o[2][256][128];  // [CTA][column][lane]
-    float ref[2][128], sum[2][128];
-};
-
-// The sums of a unit's pieces in workers first..last, one lane's COLS columns from c0: the whole block of 512
-// calls it, four groups of 128 threads, which with SPLIT take every fourth piece each (the first then has the
-// result), else every piece; in one pass, and the order of the sums is fixed.
-template <int COLS, bool SPLIT>
-__device__ __forceinline__ void join_pieces(const PairSums* parts, int first, int last, int rank, int lane, int c0, int group,
-                                            bool live, float (&acc)[COLS], float& sum, float& top)
-{
-    constexpr int kGroups = SPLIT ? 4 : 1;  // that share pieces
-    __shared__ float tops[4][128], sums[4][128], cols[SPLIT ? 3 : 1][COLS][128];
-    sum = 0.f, top = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < COLS; ++k) acc[k] = 0.f;
-    if (live)
-#pragma unroll(COLS == 4 ? 8 : 2)
-        for (int n = first + group; n <= last; n += kGroups) {
-            const PairSums& q = parts[2 * n + (n == first)];
-            const float ref = q.ref[rank][lane], l = q.sum[rank][lane];
-            float o[COLS];
-#pragma unroll
-            for (int k = 0; k < COLS; ++k) o[k] = q.o[rank][c0 + k][lane];
-            // without a branch, so that the loads of several pieces are in flight; a sum of 0: no row counted
-            const float up = l == 0.f ? top : fmaxf(top, ref), base = up == -INFINITY ? 0.f : up;
-            const float keep = tc::exp2_approx(top - base), w = l == 0.f ? 0.f : tc::exp2_approx(ref - base);
-            top = up;
-            sum = sum * keep + w * l;
-#pragma unroll
-            for (int k = 0; k < COLS; ++k) acc[k] = acc[k] * keep + (l == 0.f ? 0.f : w * o[k]);
-        }
-    if (!SPLIT) return;
-    tops[group][lane] = top;
-    sums[group][lane] = sum;
-    if (group)
-#pragma unroll
-        for (int k = 0; k < COLS; ++k) cols[group - 1][k][lane] = acc[k];
-    __syncthreads();
-    if (group || !live) return;
-    top = fmaxf(fmaxf(tops[0][lane], tops[1][lane]), fmaxf(tops[2][lane], tops[3][lane]));
-    const float base = top == -INFINITY ? 0.f : top;
-    float w = tc::exp2_approx(tops[0][lane] - base);
-    sum *= w;
-#pragma unroll
-    for (int k = 0; k < COLS; ++k) acc[k] *= w;
-    for (int n = 1; n < 4; ++n) {
-        w = tc::exp2_approx(tops[n][lane] - base);
-        sum += w * sums[n][lane];
-#pragma unroll
-        for (int k = 0; k < COLS; ++k) acc[k] += w * cols[n - 1][k][lane];
-    }
-}
 
 // The kernels: a pair of SMs for up to 128 heads; and one SM for up to 32 heads and 8-bit
 // rows, whose conversion, done twice by a pair, bounds them there (256 requests x 2048

@@ -54,10 +54,17 @@ struct Aux {
     uint32_t tmem;
     int dead;
     Piece piece;
+    int8_t q_up[64];  // power of two on a bf16 query held in fp16
     float red[2][128];
 };
 constexpr int kSmem = kOffAux + (int)sizeof(Aux);
 static_assert(kSmem <= 232448, "shared memory");
+
+// What a pair leaves of a unit that it does not have whole: its queries' sums, unscaled.
+struct Sums {
+    float o[128][512];
+    float ref[128], sum[128];
+};
 
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;  // tensor memory columns
 
@@ -69,8 +76,7 @@ struct SharedArgs : Cut {
     const float* scales;        // of 8-bit rows
     const __half* log_scales;   // base 2, not below kLeastLogScale
     const float* own_lse;       // NULL: no own rows
-    Start* starts;
-    PairSums* parts;
+    Sums* parts;                // two a pair
     int* error;
 };
 
@@ -236,48 +242,66 @@ template <typename T> __device__ void multiply(const SharedArgs& g, uint32_t sba
     drain(x);
 }
 
-// A query's 576 channels to tensor and shared memory (each row by two threads, for lanes 0-63 and 64-127: a pair's
-// product of 128 rows computes half of its columns in each, and each reads its own copy of A).  Returns the power of
-// two that a bf16 query is scaled by into fp16.
-template <typename T, bool E4M3> __device__ int bring_query(const SharedArgs& g, uint32_t sbase, uint32_t tmem, int64_t query, uint32_t qready)
+// A CTA's 64 queries to tensor and shared memory, by the four softmax warps: eight lanes read 128 bytes of a query
+// together, all of a thread's 36 pieces in flight; two blocks at a time then pass through P's buffer to tensor memory
+// (a pair's product of 128 rows computes half of its columns in lanes 64-127, which read their own copy of A).
+template <typename T, bool E4M3>
+__device__ void bring_queries(const SharedArgs& g, uint32_t sbase, uint32_t tmem, Aux* x, int64_t first, uint32_t qready)
 {
-    const int row = threadIdx.x & 63;
-    const bool ok = query < g.queries;
-    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const T*>(g.a.q) + (ok ? offset_of(g, query, g.a.q_stride) : 0));
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    int up = 0;
-    if constexpr (E4M3 && HsType<T>::is_bf16) {
-        float top = 0.f;
-#pragma unroll 1
-        for (int c = 0; c < 9; ++c) {
-            uint4 v[8];
+    const int t = threadIdx.x, ch = t & 7;
+    uint4 v[4][9];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = ok ? q[8 * c + i] : zero;
+    for (int n = 0; n < 4; ++n) {
+        const int64_t query = first + 16 * n + (t >> 3);
+        const bool ok = query < g.queries;
+        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const T*>(g.a.q) + (ok ? offset_of(g, query, g.a.q_stride) : 0)) + ch;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, largest_bf16(v[i]));
-        }
-        up = power_up(top);
+        for (int c = 0; c < 9; ++c) v[n][c] = ok ? q[8 * c] : make_uint4(0, 0, 0, 0);
     }
+    if constexpr (E4M3 && HsType<T>::is_bf16)
 #pragma unroll
-    for (int c = 0; c < 9; ++c) {
-        uint32_t r[32];
+        for (int n = 0; n < 4; ++n) {
+            float top = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            uint4 v = ok ? q[8 * c + i] : zero;
-            if constexpr (E4M3 && HsType<T>::is_bf16) v = bf16_to_half(v, power_of_two(up));
-            if (c < kQTmem)
-                r[4 * i] = v.x, r[4 * i + 1] = v.y, r[4 * i + 2] = v.z, r[4 * i + 3] = v.w;
-            else if ((i >> 2) == (int)(threadIdx.x >> 6))  // each of the two threads stores half
-                tc::st_shared16(sbase + (c - kQTmem) * kBlock + row * 128 + ((i ^ (row & 7)) << 4), v.x, v.y, v.z, v.w);
+            for (int c = 0; c < 9; ++c) top = fmaxf(top, largest_bf16(v[n][c]));
+            for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+            const int up = power_up(top);
+            if (ch == 0) x->q_up[16 * n + (t >> 3)] = (int8_t)up;
+#pragma unroll
+            for (int c = 0; c < 9; ++c) v[n][c] = bf16_to_half(v[n][c], power_of_two(up));
         }
-        if (c < kQTmem) tc::tmem_st32(tmem + kColQ + 32 * c, r);
+    auto store = [&](uint32_t block, const uint4& w, int row) {
+        tc::st_shared16(block + row * 128 + ((ch ^ (row & 7)) << 4), w.x, w.y, w.z, w.w);
+    };
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int c = kQTmem; c < 9; ++c) store(sbase + (c - kQTmem) * kBlock, v[n][c], 16 * n + (t >> 3));
+    const int row = t & 63;
+#pragma unroll
+    for (int c = 0; c < kQTmem; c += 2) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) store(sbase + kOffP + k * kBlock, v[n][c + k], 16 * n + (t >> 3));
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint32_t r[32];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint4 w = tc::ld_shared16(sbase + kOffP + k * kBlock + row * 128 + ((i ^ (row & 7)) << 4));
+                r[4 * i] = w.x, r[4 * i + 1] = w.y, r[4 * i + 2] = w.z, r[4 * i + 3] = w.w;
+            }
+            tc::tmem_st32(tmem + kColQ + 32 * (c + k), r);
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
     }
     tc::tmem_wait_st();
     tc::fence_async_shared();
     tc::fence_before();
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) tc::mbar_arrive_cluster(qready);
-    return up;
+    if ((t & 31) == 0) tc::mbar_arrive_cluster(qready);
 }
 
 // The two parts of a query, the prefix's (sum at reference ref, in powers of two) and the own rows' (lse): the
@@ -311,8 +335,8 @@ template <typename T, bool E4M3> __device__ void soften(const SharedArgs& g, uin
         const int64_t query = (int64_t)w.at * 128 + rank * 64 + row;
         float ref = 0.f, sum = 0.f;
         if (w.t0 < w.t1) {
-            const int up = bring_query<T, E4M3>(g, sbase, tmem, query, qready);
-            const float c = E4M3 ? power_of_two(-up) * c0 : c0;
+            bring_queries<T, E4M3>(g, sbase, tmem, x, (int64_t)w.at * 128 + rank * 64, qready);
+            const float c = E4M3 && HsType<T>::is_bf16 ? power_of_two(-x->q_up[row]) * c0 : c0;
             const int64_t limit = query < g.queries ? seen_rows(g, request_of(g, query)) : 0;
             bool seen = false;  // a row that counts has been met: ref is a maximum
             for (int t = w.t0; t < w.t1; ++t, ++j) {
@@ -413,6 +437,7 @@ template <typename T, bool E4M3> __device__ void soften(const SharedArgs& g, uin
         if (w.whole) {
             // Through P's buffer, so that eight lanes write 128 bytes of a query together: 64 channels of each half
             // at a time, [half][query][128 B].
+            asm volatile("griddepcontrol.wait;" ::: "memory");  // the own rows' part
             const Mix m = mix(ref, sum, there && g.own_lse ? g.own_lse[query] : -INFINITY);
             const bool mine = there && m.own != 0.f;
             T* out = static_cast<T*>(a.out);
@@ -452,7 +477,7 @@ template <typename T, bool E4M3> __device__ void soften(const SharedArgs& g, uin
             }
             if (there && a.lse && half == 0) a.lse[query] = m.lse;
         } else {
-            PairSums* part = g.parts + 2 * pair + (w.t0 == 0 ? 1 : 0);
+            Sums* part = g.parts + 2 * pair + (w.t0 == 0 ? 1 : 0);  // likewise, 32 channels at a time
 #pragma unroll 1
             for (int n = 0; n < 256; n += 32) {
                 uint32_t r[32];
@@ -460,10 +485,18 @@ template <typename T, bool E4M3> __device__ void soften(const SharedArgs& g, uin
                 tc::tmem_ld32(tmem + kColO + n, r);
                 tc::tmem_wait_ld(r);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) part->o[rank][n + i][threadIdx.x] = __uint_as_float(r[i]);
+                for (int i = 0; i < 8; ++i)
+                    tc::st_shared16(sbase + kOffP + threadIdx.x * 128 + ((i ^ (row & 7)) << 4), r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int at = 16 * i + (threadIdx.x >> 3), ch = threadIdx.x & 7;
+                    *reinterpret_cast<uint4*>(&part->o[rank * 64 + (at & 63)][256 * (at >> 6) + n + 4 * ch]) =
+                        tc::ld_shared16(sbase + kOffP + at * 128 + ((ch ^ (at & 7)) << 4));
+                }
+                asm volatile("bar.sync 1, 128;" ::: "memory");
             }
-            part->ref[rank][threadIdx.x] = ref;
-            part->sum[rank][threadIdx.x] = sum;
+            if (half == 0) part->ref[rank * 64 + row] = ref, part->sum[rank * 64 + row] = sum;
         }
         tc::fence_before();
     }
@@ -481,12 +514,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int pair = blockIdx.x >> 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may queue up behind this grid
     if (warp == 0) tc::tmem_alloc<2>(tc::smem_addr(&x->tmem), 512);
     if (warp == 6 && lane == 0) {
         const Piece p = g.flat ? line_piece(g, pair) : whole_piece(g, pair);
         x->piece = p;
         x->dead = 0;
-        if (rank == 0) g.starts[pair] = {p.count > 0 ? p.unit : -1, p.tile};
         for (int i = 0; i < kKStages; ++i) tc::mbar_init(tc::smem_addr(&x->kfull[i]), 1), tc::mbar_init(tc::smem_addr(&x->kfree[i]), 1);
         for (int i = 0; i < kVStages; ++i) tc::mbar_init(tc::smem_addr(&x->vfull[i]), 1), tc::mbar_init(tc::smem_addr(&x->vfree[i]), 1);
         tc::mbar_init(tc::smem_addr(&x->qready), 8);
@@ -523,37 +556,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc::cluster_sync_relaxed();  // no CTA leaves while the other may signal it
     tc::fence_after();
     if (warp == 0) tc::tmem_free<2>(x->tmem, 512);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // so that the join comes after the own rows' part, too
 }
 
-// Join the pieces of the units that several pairs worked on (as hs_latent_attend's) with the own rows' part.
-template <typename T, int COLS, bool SPLIT>
-__global__ void __launch_bounds__(512) hs_attend_shared_join_kernel(const __grid_constant__ SharedArgs g)
+// Where pair i's piece of the line begins, and the pair whose piece holds a place.
+__device__ __forceinline__ long long piece_begin(const Cut& g, int i) { return g.cost + g.share * i + min(i, g.extra); }
+__device__ __forceinline__ int piece_at(const Cut& g, long long at)
+{
+    at -= g.cost;
+    const long long longer = (g.share + 1) * g.extra;
+    return (int)(at < longer ? at / (g.share + 1) : g.extra + (at - longer) / g.share);
+}
+
+// Join the pieces of the units that several pairs worked on, with the own rows' part: blocks y take the unit that pair
+// y + 1 begins inside, where that is the first to do so; a warp takes 128 channels of a query, one pass over its
+// pieces in their order.
+template <typename T> __global__ void __launch_bounds__(256) hs_attend_shared_join_kernel(const __grid_constant__ SharedArgs g)
 {
     const hs_attend_t& a = g.a;
-    int unit, first, last;
-    if (!find_cut(g.starts, g.workers, blockIdx.x, unit, first, last)) return;
-    const int t = threadIdx.x;
-    const int rank = blockIdx.y, c0 = SPLIT ? COLS * blockIdx.z : COLS * (4 * blockIdx.z + (t >> 7));
-    const int lane = t & 127, group = SPLIT ? t >> 7 : 0, half = lane >> 6;
-    const int64_t query = (int64_t)unit * 128 + rank * 64 + (lane & 63);
-    if ((int64_t)unit * 128 + rank * 64 >= g.queries) return;
-    const bool live = query < g.queries;
-    float acc[COLS], sum, top;
-    join_pieces<COLS, SPLIT>(g.parts, first, last, rank, lane, c0, group, live, acc, sum, top);
-    if (group || !live) return;
-    const Mix m = mix(top, sum, g.own_lse ? g.own_lse[query] : -INFINITY);
-    T* out = static_cast<T*>(a.out) + offset_of(g, query, a.out_stride) + 256 * half + c0;
-#pragma unroll
-    for (int k = 0; k < COLS; k += 4) {
-        float f[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[i] = sum == 0.f ? 0.f : acc[k + i] * m.prefix;
-            if (m.own != 0.f) f[i] += HsType<T>::to_float(out[k + i]) * m.own;
-        }
-        *reinterpret_cast<uint2*>(out + k) = make_uint2(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]));
+    const int per = g.unit_tiles + g.cost, pair = blockIdx.y + 1;
+    const long long here = piece_begin(g, pair);
+    const int unit = (int)(here / per);
+    const long long begin = (long long)unit * per + g.cost;  // the unit's first tile
+    const int first = piece_at(g, begin), last = piece_at(g, begin + g.unit_tiles - 1);
+    if (here <= begin || first != pair - 1) return;
+    const int id = blockIdx.x * 8 + (threadIdx.x >> 5), row = id >> 2, ch = 128 * (id & 3) + 4 * (threadIdx.x & 31);
+    const int64_t query = (int64_t)unit * 128 + row;
+    if (query >= g.queries) return;
+    T* out = static_cast<T*>(a.out) + offset_of(g, query, a.out_stride) + ch;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const float own_lse = g.own_lse ? g.own_lse[query] : -INFINITY;
+    uint2 old = make_uint2(0, 0);
+    if (g.own_lse) old = *reinterpret_cast<const uint2*>(out);
+    float acc[4] = {}, sum = 0.f, top = -INFINITY;
+#pragma unroll 4
+    for (int n = first; n <= last; ++n) {
+        const Sums& p = g.parts[2 * n + (n == first)];
+        const float ref = p.ref[row], l = p.sum[row];
+        const float4 o = *reinterpret_cast<const float4*>(&p.o[row][ch]);
+        // without a branch, so that the loads of several pieces are in flight; a sum of 0: no row counted
+        const float up = l == 0.f ? top : fmaxf(top, ref), base = up == -INFINITY ? 0.f : up;
+        const float keep = tc::exp2_approx(top - base), w = l == 0.f ? 0.f : tc::exp2_approx(ref - base);
+        top = up;
+        sum = sum * keep + w * l;
+        acc[0] = acc[0] * keep + (l == 0.f ? 0.f : w * o.x);
+        acc[1] = acc[1] * keep + (l == 0.f ? 0.f : w * o.y);
+        acc[2] = acc[2] * keep + (l == 0.f ? 0.f : w * o.z);
+        acc[3] = acc[3] * keep + (l == 0.f ? 0.f : w * o.w);
     }
-    if (a.lse && half == 0 && c0 == 0) a.lse[query] = m.lse;
+    const Mix m = mix(top, sum, own_lse);
+    const uint32_t halves[2] = {old.x, old.y};
+    uint32_t e[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float2 h = unpack2<T>(halves[i]);
+        float f0 = sum == 0.f ? 0.f : acc[2 * i] * m.prefix, f1 = sum == 0.f ? 0.f : acc[2 * i + 1] * m.prefix;
+        if (m.own != 0.f) f0 += h.x * m.own, f1 += h.y * m.own;
+        e[i] = pack2<T>(f0, f1);
+    }
+    *reinterpret_cast<uint2*>(out) = make_uint2(e[0], e[1]);
+    if (a.lse && ch == 0) a.lse[query] = m.lse;
 }
 
 // The prefix's rows as 16-bit operands: a warp a row.  8-bit values become fp16 beside their scales (and base-2
@@ -636,17 +698,16 @@ cudaError_t map_rows(CUtensorMap* map, const void* rows, int64_t n, int64_t stri
 
 int64_t padded_rows(int64_t n) { return (n + kRows - 1) / kRows * kRows; }
 
-// Workspace: hs_latent_attend's for the own rows (its error word is the call's), then their lse, where each pair's
-// piece starts, two partial results a pair, the prefix's rows in 16 bits, scales and their logarithms.
+// Workspace: hs_latent_attend's for the own rows (its error word is the call's), then their lse, two partial results a
+// pair, the prefix's rows in 16 bits, scales and their logarithms.
 struct Layout {
-    size_t lse, starts, parts, rows, scales, logs, end;
+    size_t lse, parts, rows, scales, logs, end;
     Layout(int batch, int positions, int heads, int64_t own_rows, int64_t prefix_rows)
     {
         auto after = [](size_t at, size_t bytes) { return (at + bytes + 255) / 256 * 256; };
         lse = after(0, hs_attend_workspace_bytes(batch, positions, heads, own_rows));
-        starts = after(lse, sizeof(float) * batch * positions * (size_t)heads);
-        parts = after(starts, sizeof(Start) * kMaxPairs);
-        rows = after(parts, sizeof(PairSums) * 2 * kMaxPairs);
+        parts = after(lse, sizeof(float) * batch * positions * (size_t)heads);
+        rows = after(parts, sizeof(Sums) * 2 * kMaxPairs);
         scales = after(rows, 2 * HS_ROW_DIM * (size_t)prefix_rows);
         logs = after(scales, sizeof(float) * padded_rows(prefix_rows));
         end = after(logs, sizeof(__half) * padded_rows(prefix_rows));
@@ -657,15 +718,12 @@ template <typename T, bool E4M3> cudaError_t launch(const SharedArgs& g, const C
 {
     cudaError_t e = cudaFuncSetAttribute(hs_attend_shared_kernel<T, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    hs_attend_shared_kernel<T, E4M3><<<2 * g.workers, kThreads, kSmem, s>>>(g, map);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || !g.flat || g.workers <= 1) return e;
-    const int cut = g.units < g.workers - 1 ? g.units : g.workers - 1;
-    if (cut >= 16)
-        hs_attend_shared_join_kernel<T, 16, false><<<dim3(cut, 2, 256 / 64), 512, 0, s>>>(g);
+    if (g.own_lse)  // may begin while the own rows' part runs out, and reads it at its units' ends
+        e = launch_after(hs_attend_shared_kernel<T, E4M3>, dim3(2 * g.workers), kThreads, kSmem, s, g, map);
     else
-        hs_attend_shared_join_kernel<T, 4, true><<<dim3(cut, 2, 256 / 4), 512, 0, s>>>(g);
-    return cudaGetLastError();
+        hs_attend_shared_kernel<T, E4M3><<<2 * g.workers, kThreads, kSmem, s>>>(g, map), e = cudaGetLastError();
+    if (e != cudaSuccess || !g.flat || g.workers <= 1) return e;
+    return launch_after(hs_attend_shared_join_kernel<T>, dim3(128 * 4 / 8, g.workers - 1), 256, 0, s, g);
 }
 
 template <typename T> cudaError_t run(SharedArgs& g, const hs_prefix_t& p, uint8_t* ws, const Layout& at, cudaStream_t s)
@@ -720,8 +778,7 @@ cudaError_t hs_launch_attend_shared(const hs_attend_t& a, const hs_prefix_t& p, 
     g.prefix_lengths = p.lengths;
     g.prefix_rows = p.n_rows;
     g.queries = (int64_t)a.batch * a.positions * a.heads;
-    g.starts = reinterpret_cast<Start*>(ws + at.starts);
-    g.parts = reinterpret_cast<PairSums*>(ws + at.parts);
+    g.parts = reinterpret_cast<Sums*>(ws + at.parts);
     g.error = reinterpret_cast<int*>(ws);
     if (a.n_rows > 0 && (!a.slots || a.entries > 0)) {
         hs_attend_t own = a;

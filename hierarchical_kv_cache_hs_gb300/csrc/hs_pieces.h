@@ -88,3 +88,12 @@ __device__ __forceinline__ float divided(float y, float scale, float inv)
 {
     return inv != 0.f ? quotient(y, scale, inv) : y / (scale == 0.f ? 1.f : scale);
 }
+
+// Two 16-bit values as floats, the low half first.
+template <typename T> __device__ __forceinline__ float2 unpack2(uint32_t v)
+{
+    if constexpr (HsType<T>::is_bf16)
+        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+    else
+        return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}

@@ -38,15 +38,6 @@ __device__ Place find_place(const int32_t* start, const int32_t* lengths, int ba
     return {first, (lengths ? (int64_t)lengths[first] - end : -clamped(start[first], tokens)) + token};
 }
 
-// Two channels of a row as floats.
-template <typename T> __device__ __forceinline__ float2 unpack2(uint32_t v)
-{
-    if constexpr (HsType<T>::is_bf16)
-        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
-    else
-        return __half22float2(*reinterpret_cast<const __half2*>(&v));
-}
-
 template <typename T, bool E4M3>
 __global__ void __launch_bounds__(kWarps * 32) hs_write_kernel(const __grid_constant__ hs_write_t a)
 {
