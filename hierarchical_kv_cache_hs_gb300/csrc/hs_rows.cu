@@ -3,186 +3,327 @@
 // as values.
 //
 // Both read each input once and write each output once, and are bound by memory.
-// Writing: a warp a row; a lane has two 16-byte pieces of the latent channels (32 lanes x
-// 2 x 8 = 512) and two of the 64 rotary channels, so every lane has the same work.
-// Reading: 72 threads a row, 8 channels each (16 bytes of 16 bits).
 #include "hs_pieces.h"
 #include "hs_rotation.h"
 
 namespace {
 
-constexpr int kWarps = 8;  // rows of a block, writing
-
-// The request of a token, and the row that it has in the request's context.  A warp's search in start: the last
-// request that starts at or before the token (every lane gets it); -1: none.
-struct Place {
-    int request;
-    int64_t row;
-};
 __device__ __forceinline__ int64_t clamped(int start, int64_t tokens) { return start < 0 ? 0 : start > tokens ? tokens : start; }
-__device__ Place find_place(const int32_t* start, const int32_t* lengths, int batch, int64_t tokens, int64_t token)
+
+// The request whose tokens [begin, end) hold a token, by a warp's search in start: the last request that starts at or
+// before it (every lane gets it); -1: none.
+struct Span {
+    int request;
+    int64_t begin, end;
+};
+__device__ Span find_span(const int32_t* start, int batch, int64_t tokens, int64_t token)
 {
     const int lane = threadIdx.x & 31;
     int first = 0, count = batch;
     for (;;) {
-        const int step = (count + 31) >> 5, at = first + lane * step;
-        const bool before = lane * step < count && clamped(start[at], tokens) <= token;
+        const int step = (count + 31) >> 5;
+        const bool before = lane * step < count && clamped(start[first + lane * step], tokens) <= token;
         const int n = __popc(__ballot_sync(~0u, before));
-        if (n == 0) return {-1, 0};
+        if (n == 0) return {-1, 0, 0};
         first += (n - 1) * step;
         count = min(step, count - (n - 1) * step);
         if (step == 1) break;
     }
-    const int64_t end = clamped(start[first + 1], tokens);
-    if (token >= end) return {-1, 0};
-    return {first, (lengths ? (int64_t)lengths[first] - end : -clamped(start[first], tokens)) + token};
+    const Span s = {first, clamped(start[first], tokens), clamped(start[first + 1], tokens)};
+    return token < s.end ? s : Span{-1, 0, 0};
 }
+// A token's row among those of its request.
+__device__ __forceinline__ int64_t row_of(const Span& s, const int32_t* lengths, int64_t token)
+{
+    return lengths ? lengths[s.request] - s.end + token : token - s.begin;
+}
+
+// ---- write -----------------------------------------------------------------------------
+//
+// A warp takes some tokens, one after the other, with the next one's channels on their way.  A lane has two
+// 16-byte pieces of the latent channels (32 lanes x 2 x 8 = 512) and two of the 64 rotary channels, so every lane
+// has the same work; the weights and its pair's frequency stay in registers.
+
+constexpr int kWarps = 8;        // of a block
+constexpr int kWriteBlocks = 3;  // an SM: what their registers allow
+
+__device__ __forceinline__ void mul2(float& a0, float& a1, float b0, float b1)
+{
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a0), "+f"(a1)
+        : "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void square2(float& s0, float& s1, float a0, float a1)  // added to the sums
+{
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%0, %1};\n\tfma.rn.f32x2 y, x, x, y;\n\tmov.b64 {%0, %1}, y;\n\t}"
+        : "+f"(s0), "+f"(s1)
+        : "f"(a0), "f"(a1));
+}
+__device__ __forceinline__ float top3(float a, float b, float c)  // of magnitudes; keeps a NaN
+{
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float warp_top(float v)  // likewise
+{
+    float d;
+    asm("redux.sync.max.abs.NaN.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(v));
+    return d;
+}
+
+__device__ __noinline__ float rare_quotient(float y, float scale) { return divided(y, scale, 0.f); }
 
 template <typename T, bool E4M3>
-__global__ void __launch_bounds__(kWarps * 32) hs_write_kernel(const __grid_constant__ hs_write_t a)
+__global__ void __launch_bounds__(kWarps * 32, kWriteBlocks) hs_write_kernel(const __grid_constant__ hs_write_t a)
 {
     const int lane = threadIdx.x & 31;
-    const int64_t token = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (token >= a.tokens) return;
-    const T* x = static_cast<const T*>(a.x) + token * a.x_stride;
-    uint4 in[2], wv[2];
-#pragma unroll
-    for (int v = 0; v < 2; ++v) in[v] = reinterpret_cast<const uint4*>(x)[v * 32 + lane];
-    float2 r = unpack2<T>(reinterpret_cast<const uint32_t*>(x + HS_LATENT_DIM)[lane]);
+    constexpr int step = kWarps;
+    const int first = (int)(a.tokens * blockIdx.x / gridDim.x) + (threadIdx.x >> 5), last = (int)(a.tokens * (blockIdx.x + 1) / gridDim.x);  // below 2^24
+    if (first >= last) return;
+    uint4 weight[2];
     if (a.weight)
 #pragma unroll
-        for (int v = 0; v < 2; ++v) wv[v] = static_cast<const uint4*>(a.weight)[v * 32 + lane];
-    Place place = {0, token};
-    if (a.start) place = find_place(a.start, a.lengths, a.batch, a.tokens, token);
-    if (place.request < 0 || place.row < 0 || place.row >= a.n_rows) return;
-    uint8_t* out = static_cast<uint8_t*>(a.rows) + place.request * a.request_stride + place.row * a.row_stride;
+        for (int v = 0; v < 2; ++v) weight[v] = static_cast<const uint4*>(a.weight)[v * 32 + lane];
+    HsTurn freq = {0, true};
+    if (a.rotation != HS_ROTATE_NONE) freq = hs_turn(a.inv_freq[lane]);
+    // The tokens up to `end` belong to one request, or to none; those in [low, high) have a row, this one at `out`.
+    int end = a.start ? first : last, low = first, high = last;
+    uint8_t* out = static_cast<uint8_t*>(a.rows) + first * a.row_stride;
 
-    if (a.rotation != HS_ROTATE_NONE) {
-        float2 t = hs_rotation(a.positions[token], a.inv_freq[lane]);  // of pair `lane`
-        if (a.rotation == HS_ROTATE_PAIRS) {
-            r = make_float2(r.x * t.x - r.y * t.y, r.x * t.y + r.y * t.x);
-        } else {  // lanes 0-15 have both first channels of two pairs, lanes 16-31 their second ones
-            const int pair = 2 * (lane & 15);
-            const float c0 = __shfl_sync(~0u, t.x, pair), s0 = __shfl_sync(~0u, t.y, pair);
-            const float c1 = __shfl_sync(~0u, t.x, pair + 1), s1 = __shfl_sync(~0u, t.y, pair + 1);
-            const float ox = __shfl_xor_sync(~0u, r.x, 16), oy = __shfl_xor_sync(~0u, r.y, 16);
-            r = lane < 16 ? make_float2(r.x * c0 - ox * s0, r.y * c1 - oy * s1)
-                          : make_float2(ox * s0 + r.x * c0, oy * s1 + r.y * c1);
+    const T* x = static_cast<const T*>(a.x) + first * a.x_stride;
+    uint4 in[2];
+    uint32_t rope;
+    int position = 0;
+    auto bring = [&](int token) {
+#pragma unroll
+        for (int v = 0; v < 2; ++v) in[v] = __ldcs(reinterpret_cast<const uint4*>(x) + v * 32 + lane);
+        rope = __ldcs(reinterpret_cast<const uint32_t*>(x + HS_LATENT_DIM) + lane);
+        if (a.rotation != HS_ROTATE_NONE) position = a.positions[token];
+        x += step * a.x_stride;
+    };
+    bring(first);
+    for (int token = first; token < last; token += step, out += step * a.row_stride) {
+        float h[2][8];
+#pragma unroll
+        for (int v = 0; v < 2; ++v) Piece<T>::unpack(in[v], h[v]);
+        float2 r = unpack2<T>(rope);
+        const int at = position;
+        if (token + step < last) bring(token + step);
+        if (token >= end) {
+            const Span s = find_span(a.start, a.batch, a.tokens, token);
+            low = high = end = token + 1;
+            if (s.request >= 0) {
+                const int64_t zero = s.end - a.lengths[s.request];  // the token whose row is 0
+                end = (int)s.end;
+                low = (int)min(max(zero, (int64_t)0), a.tokens);
+                high = (int)min(max(zero + a.n_rows, (int64_t)0), a.tokens);
+                out = static_cast<uint8_t*>(a.rows) + s.request * a.request_stride + (token - zero) * a.row_stride;
+            }
         }
-    }
-    float h[2][8];
-#pragma unroll
-    for (int v = 0; v < 2; ++v) Piece<T>::unpack(in[v], h[v]);
-    if (a.weight) {
-        float sum = 0.f;
-#pragma unroll
-        for (int v = 0; v < 2; ++v)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) sum += h[v][k] * h[v][k];
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-        const float f = rsqrtf(sum / HS_LATENT_DIM + a.eps);
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-            float w[8];
-            Piece<T>::unpack(wv[v], w);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) h[v][k] = h[v][k] * f * w[k];
+        if (token < low || token >= high) continue;
+
+        if (a.rotation != HS_ROTATE_NONE) {
+            const float2 t = hs_rotation(at, freq);  // of pair `lane`
+            if (a.rotation == HS_ROTATE_PAIRS) {
+                r = make_float2(r.x * t.x - r.y * t.y, r.x * t.y + r.y * t.x);
+            } else {  // lanes 0-15 have both first channels of two pairs, lanes 16-31 their second ones
+                const int pair = 2 * (lane & 15);
+                const float c0 = __shfl_sync(~0u, t.x, pair), s0 = __shfl_sync(~0u, t.y, pair);
+                const float c1 = __shfl_sync(~0u, t.x, pair + 1), s1 = __shfl_sync(~0u, t.y, pair + 1);
+                const float ox = __shfl_xor_sync(~0u, r.x, 16), oy = __shfl_xor_sync(~0u, r.y, 16);
+                r = lane < 16 ? make_float2(r.x * c0 - ox * s0, r.y * c1 - oy * s1)
+                              : make_float2(ox * s0 + r.x * c0, oy * s1 + r.y * c1);
+            }
         }
-    }
-    if constexpr (!E4M3) {
+        if (a.weight) {
+            float sum = 0.f, odd = 0.f;
 #pragma unroll
-        for (int v = 0; v < 2; ++v) reinterpret_cast<uint4*>(out)[v * 32 + lane] = Piece<T>::pack(h[v]);
-        reinterpret_cast<uint32_t*>(out + 2 * HS_LATENT_DIM)[lane] = pack2<T>(r.x, r.y);
-    } else {
-        float top = nan_max(fabsf(r.x), fabsf(r.y));
+            for (int v = 0; v < 2; ++v)
 #pragma unroll
-        for (int v = 0; v < 2; ++v)
+                for (int k = 0; k < 8; k += 2) square2(sum, odd, h[v][k], h[v][k + 1]);
+            sum += odd;
+            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+            const float f = rsqrtf(sum / HS_LATENT_DIM + a.eps);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) top = nan_max(top, fabsf(h[v][k]));
-        for (int o = 16; o; o >>= 1) top = nan_max(top, __shfl_xor_sync(~0u, top, o));
-        const float scale = top / HS_E4M3_MAX, inv = inverse(scale);
-        auto two = [&](float y0, float y1) -> uint32_t {
-            if (inv != 0.f)
-                quotients(y0, y1, scale, inv);
-            else
-                y0 = divided(y0, scale, 0.f), y1 = divided(y1, scale, 0.f);
-            return __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3);
-        };
+            for (int v = 0; v < 2; ++v) {
+                float w[8];
+                Piece<T>::unpack(weight[v], w);
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-            uint32_t q[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) q[k] = two(h[v][4 * k], h[v][4 * k + 1]) | two(h[v][4 * k + 2], h[v][4 * k + 3]) << 16;
-            reinterpret_cast<uint2*>(out)[v * 32 + lane] = make_uint2(q[0], q[1]);
+                for (int k = 0; k < 8; k += 2) {
+                    mul2(h[v][k], h[v][k + 1], f, f);
+                    mul2(h[v][k], h[v][k + 1], w[k], w[k + 1]);
+                }
+            }
         }
-        reinterpret_cast<uint16_t*>(out + HS_LATENT_DIM)[lane] = (uint16_t)two(r.x, r.y);
-        if (lane == 0) *reinterpret_cast<float*>(out + HS_ROW8_SCALE) = scale;
+        if constexpr (!E4M3) {
+#pragma unroll
+            for (int v = 0; v < 2; ++v) reinterpret_cast<uint4*>(out)[v * 32 + lane] = Piece<T>::pack(h[v]);
+            reinterpret_cast<uint32_t*>(out + 2 * HS_LATENT_DIM)[lane] = pack2<T>(r.x, r.y);
+        } else {
+            float top = nan_max(fabsf(r.x), fabsf(r.y));
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
+#pragma unroll
+                for (int k = 0; k < 8; k += 2) top = top3(top, h[v][k], h[v][k + 1]);
+            const float scale = warp_top(top) / HS_E4M3_MAX, inv = inverse(scale);
+            if (inv != 0.f) {
+#pragma unroll
+                for (int v = 0; v < 2; ++v)
+#pragma unroll
+                    for (int k = 0; k < 8; k += 2) quotients(h[v][k], h[v][k + 1], scale, inv);
+                quotients(r.x, r.y, scale, inv);
+            } else {  // zeros, or beyond what a reciprocal serves
+#pragma unroll
+                for (int v = 0; v < 2; ++v)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) h[v][k] = rare_quotient(h[v][k], scale);
+                r = make_float2(rare_quotient(r.x, scale), rare_quotient(r.y, scale));
+            }
+            auto two = [](float y0, float y1) -> uint32_t { return __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3); };
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
+                reinterpret_cast<uint2*>(out)[v * 32 + lane] = make_uint2(two(h[v][0], h[v][1]) | two(h[v][2], h[v][3]) << 16,
+                                                                         two(h[v][4], h[v][5]) | two(h[v][6], h[v][7]) << 16);
+            reinterpret_cast<uint16_t*>(out + HS_LATENT_DIM)[lane] = (uint16_t)two(r.x, r.y);
+            if (lane == 0) *reinterpret_cast<float*>(out + HS_ROW8_SCALE) = scale;
+        }
     }
 }
 
-constexpr int kRowThreads = HS_ROW_DIM / 8, kReadRows = 4;  // rows of a block
+// ---- read ------------------------------------------------------------------------------
+//
+// 36 threads a row, 16 channels each, and kReadAhead rows of a thread on their way together.
+
+constexpr int kRowThreads = HS_ROW_DIM / 16, kReadLine = 8, kReadAhead = 3;  // threads of a row, rows side by side, rows of a thread
+constexpr int kReadRows = kReadLine * kReadAhead;                            // of a block
+static_assert(kReadRows <= 32, "a warp finds the rows");
+
+// 32 bytes at once where they are aligned so.
+__device__ __forceinline__ void load32(const void* p, bool whole, uint4 (&v)[2])
+{
+    if (whole) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x), "=r"(v[1].y), "=r"(v[1].z), "=r"(v[1].w)
+                     : "l"(p));
+    } else {
+        v[0] = static_cast<const uint4*>(p)[0];
+        v[1] = static_cast<const uint4*>(p)[1];
+    }
+}
+__device__ __forceinline__ void store32(void* p, bool whole, const uint4& a, const uint4& b)
+{
+    if (whole) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y),
+                     "r"(b.z), "r"(b.w)
+                     : "memory");
+    } else {
+        static_cast<uint4*>(p)[0] = a;
+        static_cast<uint4*>(p)[1] = b;
+    }
+}
 
 // R: the type of 16-bit rows, or void for 8-bit ones.
-template <typename R, typename O> __global__ void __launch_bounds__(kRowThreads * kReadRows) hs_read_kernel(const __grid_constant__ hs_read_t a)
+template <typename R, typename O>
+__global__ void __launch_bounds__(kRowThreads * kReadLine) hs_read_kernel(const __grid_constant__ hs_read_t a, const bool rows32, const bool out32)
 {
-    __shared__ Place places[kReadRows];
+    __shared__ const uint8_t* places[kReadRows];  // a row's address; NULL: zeros
+    __shared__ bool mine[kReadRows];              // an out row of a request
     const int64_t first = (int64_t)blockIdx.x * kReadRows;
-    if (a.start) {
-        const int warp = threadIdx.x >> 5;
-        if (warp < kReadRows && first + warp < a.tokens) {
-            const Place p = find_place(a.start, a.lengths, a.batch, a.tokens, first + warp);
-            if ((threadIdx.x & 31) == 0) places[warp] = p;
-        }
-        __syncthreads();
-    }
-    const int i = threadIdx.x / kRowThreads, ch = 8 * (threadIdx.x - i * kRowThreads);
-    const int64_t token = first + i;
-    if (token >= a.tokens) return;
-    Place p;
-    if (a.start) {
-        p = places[i];
-        if (p.request < 0) return;
-    } else {
-        p.request = (int)(token / a.entries);
-        p.row = a.slots[p.request * a.slots_stride + token % a.entries];
-    }
-    float y[8] = {};
-    if (p.row >= 0 && p.row < a.n_rows) {
-        const uint8_t* row = static_cast<const uint8_t*>(a.rows) + p.request * a.request_stride + p.row * a.row_stride;
-        if constexpr (std::is_void_v<R>) {
-            const float scale = *reinterpret_cast<const float*>(row + HS_ROW8_SCALE);
-            const uint2 v = *reinterpret_cast<const uint2*>(row + ch);
-            const uint32_t w[2] = {v.x, v.y};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[k >> 1] >> 16 * (k & 1)), __NV_E4M3);
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-                y[2 * k] = f.x * scale, y[2 * k + 1] = f.y * scale;
+    if (threadIdx.x < 32) {
+        const int64_t token = first + threadIdx.x;
+        const bool there = threadIdx.x < kReadRows && token < a.tokens;
+        Span s = {-1, 0, 0};
+        int64_t row = -1;
+        if (a.start) {
+            Span f = find_span(a.start, a.batch, a.tokens, first);
+            if (there && f.request >= 0 && token < f.end) s = f;  // most blocks lie in one request
+            const unsigned others = __ballot_sync(~0u, there && s.request < 0);
+            for (unsigned left = others; left; left &= left - 1) {
+                const int from = __ffs(left) - 1;
+                f = find_span(a.start, a.batch, a.tokens, first + from);
+                if ((int)threadIdx.x == from) s = f;
             }
+            if (there && s.request >= 0) row = row_of(s, a.lengths, token);
+        } else if (there) {
+            s.request = (int)(token / a.entries);
+            row = a.slots[s.request * a.slots_stride + token % a.entries];
+        }
+        if (threadIdx.x < kReadRows) mine[threadIdx.x] = there && s.request >= 0;
+        if (threadIdx.x < kReadRows) places[threadIdx.x] = s.request >= 0 && row >= 0 && row < a.n_rows
+                                  ? static_cast<const uint8_t*>(a.rows) + s.request * a.request_stride + row * a.row_stride
+                                  : nullptr;
+    }
+    __syncthreads();
+    const int line = threadIdx.x / kRowThreads, ch = 16 * (threadIdx.x - line * kRowThreads);
+    uint4 v[kReadAhead][std::is_void_v<R> ? 1 : 2];
+    float scale[kReadAhead];
+#pragma unroll
+    for (int n = 0; n < kReadAhead; ++n) {
+        const uint8_t* row = places[n * kReadLine + line];
+        scale[n] = 0.f;
+        if constexpr (std::is_void_v<R>) {
+            v[n][0] = make_uint4(0, 0, 0, 0);
+            if (row) v[n][0] = *reinterpret_cast<const uint4*>(row + ch), scale[n] = *reinterpret_cast<const float*>(row + HS_ROW8_SCALE);
         } else {
-            Piece<R>::unpack(*reinterpret_cast<const uint4*>(row + 2 * ch), y);
+            v[n][0] = v[n][1] = make_uint4(0, 0, 0, 0);
+            if (row) load32(row + 2 * ch, rows32, v[n]);
         }
     }
-    uint4* out = reinterpret_cast<uint4*>(static_cast<O*>(a.out) + token * a.out_stride + ch);
-    out[0] = Piece<O>::pack(y);
-    if constexpr (sizeof(O) == 4) out[1] = Piece<O>::pack(y + 4);
+#pragma unroll
+    for (int n = 0; n < kReadAhead; ++n) {
+        const int i = n * kReadLine + line;
+        if (!mine[i]) continue;
+        O* out = static_cast<O*>(a.out) + (first + i) * a.out_stride + ch;
+        if constexpr (std::is_same_v<R, O>) {
+            store32(out, out32, v[n][0], v[n][1]);
+        } else {
+            float y[16];
+            if constexpr (std::is_void_v<R>) {
+                const uint32_t e[4] = {v[n][0].x, v[n][0].y, v[n][0].z, v[n][0].w};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(e[k >> 1] >> 16 * (k & 1)), __NV_E4M3);
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                    y[2 * k] = f.x * scale[n], y[2 * k + 1] = f.y * scale[n];
+                }
+            } else {
+                Piece<R>::unpack(v[n][0], y);
+                Piece<R>::unpack(v[n][1], y + 8);
+            }
+            constexpr int P = Piece<O>::n;
+#pragma unroll
+            for (int k = 0; k < 16; k += 2 * P) store32(out + k, out32, Piece<O>::pack(y + k), Piece<O>::pack(y + k + P));
+        }
+    }
 }
 
+template <typename R, typename O> void launch_read(const hs_read_t& a, cudaStream_t s)
+{
+    auto fits = [](const void* p, int64_t stride) { return (uintptr_t)p % 32 == 0 && stride % 32 == 0; };
+    const bool rows32 = !std::is_void_v<R> && fits(a.rows, a.row_stride | (a.batch > 1 ? a.request_stride : 0));
+    const bool out32 = fits(a.out, a.tokens > 1 ? a.out_stride * (int64_t)sizeof(O) : 0);
+    hs_read_kernel<R, O><<<(unsigned)((a.tokens + kReadRows - 1) / kReadRows), kRowThreads * kReadLine, 0, s>>>(a, rows32, out32);
+}
 template <typename R> cudaError_t launch_read(const hs_read_t& a, cudaStream_t s)
 {
-    const unsigned grid = (unsigned)((a.tokens + kReadRows - 1) / kReadRows);
     if (a.out_dtype == HS_TYPE_BF16)
-        hs_read_kernel<R, __nv_bfloat16><<<grid, kRowThreads * kReadRows, 0, s>>>(a);
+        launch_read<R, __nv_bfloat16>(a, s);
     else if (a.out_dtype == HS_TYPE_FP16)
-        hs_read_kernel<R, __half><<<grid, kRowThreads * kReadRows, 0, s>>>(a);
+        launch_read<R, __half>(a, s);
     else
-        hs_read_kernel<R, float><<<grid, kRowThreads * kReadRows, 0, s>>>(a);
+        launch_read<R, float>(a, s);
     return cudaGetLastError();
 }
 
 template <typename T> cudaError_t launch_write(const hs_write_t& a, cudaStream_t s)
 {
-    const unsigned grid = (unsigned)((a.tokens + kWarps - 1) / kWarps);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const int64_t most = (int64_t)sms * kWriteBlocks, blocks = (a.tokens + kWarps - 1) / kWarps;
+    const unsigned grid = (unsigned)(blocks < most ? blocks : most);
     if (a.row_format == HS_ROWS_E4M3)
         hs_write_kernel<T, true><<<grid, kWarps * 32, 0, s>>>(a);
     else
