@@ -18,8 +18,8 @@ constexpr int kWarpsEnough = 24;  // an SM
 
 struct RotateArgs {
     hs_rotate_t a;
-    int heads_warp;      // of a warp, all of one array
-    int chunks[2];       // warps that share a token's queries, and its keys
+    float inv_dim;
+    int heads_warp;      // of a warp
     int team;            // lanes of a head
     int tokens_block, heads_block;  // of a block (element by element)
 };
@@ -42,20 +42,50 @@ template <typename T> struct Half16 {
 template <> struct Half<__nv_bfloat16> : Half16<__nv_bfloat16> {};
 template <> struct Half<__half> : Half16<__half> {};
 
+__device__ __forceinline__ float2 mul2(const float2& a, const float2& b)  // two operations in one instruction
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(const float2& a, const float2& b, const float2& c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
 // NV: units a lane, AHEAD: heads of a team on their way together.
-template <typename T, int NV, int AHEAD> __global__ void __launch_bounds__(kThreads) hs_rotate_kernel(const __grid_constant__ RotateArgs g)
+template <typename T, int NV, int AHEAD> __global__ void __launch_bounds__(kThreads, NV == 1 ? 3 : 1) hs_rotate_kernel(const __grid_constant__ RotateArgs g)
 {
     constexpr int H = Half<T>::n, U = 2 * H;  // channels of half a unit, of a unit
     extern __shared__ float2 sines[];         // [warp][pair]
     const hs_rotate_t& a = g.a;
-    const int lane = threadIdx.x & 31, all = g.chunks[0] + g.chunks[1];
-    const int64_t id = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), token = id / all;
+    const int lane = threadIdx.x & 31;
+    const int64_t token = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (token >= a.tokens) return;
-    int chunk = (int)(id - token * all);
-    const int k = chunk >= g.chunks[0];  // queries or keys
-    chunk -= k ? g.chunks[0] : 0;
+    const int head_first = blockIdx.y * g.heads_warp, head_last = min(head_first + g.heads_warp, a.heads[0] + a.heads[1]);
     const int pairs = a.rope / 2, units = a.dim / U;
     const bool paired = a.rotation == HS_ROTATE_PAIRS;
+    // Where this lane's units lie: the first half's channel, and how far behind it the second one's is.
+    const int at = lane & (g.team - 1), teams = 32 / g.team, mine = lane / g.team;
+    int low[NV], apart[NV], pair[NV];  // the first pair, -1: not rotary
+    bool there[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int u = v * g.team + at, n = u * U - a.rope_at;
+        there[v] = u < units;
+        pair[v] = there[v] && n >= 0 && n < a.rope ? n / 2 : -1;
+        const bool halves = pair[v] >= 0 && !paired;  // unit i of the rotary channels: H from either half of them
+        low[v] = halves ? a.rope_at + n / 2 : u * U;
+        apart[v] = halves ? pairs : H;
+    }
+
     float2* turns = sines + (threadIdx.x >> 5) * pairs;
     if (pairs) {
         const int position = a.positions[token];
@@ -63,101 +93,104 @@ template <typename T, int NV, int AHEAD> __global__ void __launch_bounds__(kThre
         __syncwarp();
     }
 
-    // This lane's units: where their halves lie, their weights, the sines and cosines of their pairs.
-    const int at = lane & (g.team - 1), teams = 32 / g.team;
-    const T* weight = static_cast<const T*>(a.weight[k]);
-    int low[NV], high[NV];
-    bool turned[NV], mine[NV];
-    uint2 wl[NV], wh[NV];
-    float2 turn[NV][H];
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {  // queries, keys
+        const int before = k ? a.heads[0] : 0;
+        const int first = max(head_first - before, 0), last = min(head_last - before, a.heads[k]);
+        if (first >= last) continue;
+        // A lane's factors, weights times sines and cosines: for a rotary unit of two halves p and q (or of pairs p, q)
+        // c[0] p - c[1] q and c[2] p + c[3] q; else c[0] and c[1] are weights.
+        const T* weight = static_cast<const T*>(a.weight[k]);
+        float c[NV][4][H];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int u = v * g.team + at;
-        mine[v] = u < units;
-        int c = u * U;
-        high[v] = c + H;
-        const int n = c - a.rope_at;
-        turned[v] = mine[v] && n >= 0 && n < a.rope;
-        if (turned[v] && !paired) {  // unit i of the rotary channels: H from either half of them
-            c = a.rope_at + n / 2;
-            high[v] = c + pairs;
-        }
-        low[v] = c;
-        if (weight && mine[v]) {
-            wl[v] = *reinterpret_cast<const uint2*>(weight + low[v]);
-            wh[v] = *reinterpret_cast<const uint2*>(weight + high[v]);
-        }
+        for (int v = 0; v < NV; ++v) {
+            float w[U];
 #pragma unroll
-        for (int i = 0; i < H; ++i) turn[v][i] = turned[v] ? turns[n / 2 + i] : make_float2(1.f, 0.f);
-    }
-
-    const int first = chunk * g.heads_warp + lane / g.team, last = min((chunk + 1) * g.heads_warp, a.heads[k]);
-    const T* x = static_cast<const T*>(a.x[k]) + token * a.x_stride[k][0];
-    T* out = static_cast<T*>(a.out[k]) + token * a.out_stride[k][0];
-    for (int head0 = first; head0 - lane / g.team < last; head0 += AHEAD * teams) {  // the whole warp
-        uint2 xl[AHEAD][NV], xh[AHEAD][NV];
+            for (int i = 0; i < U; ++i) w[i] = 1.f;
+            if (weight && there[v]) {
+                Half<T>::unpack(*reinterpret_cast<const uint2*>(weight + low[v]), w);
+                Half<T>::unpack(*reinterpret_cast<const uint2*>(weight + low[v] + apart[v]), w + H);
+            }
 #pragma unroll
-        for (int m = 0; m < AHEAD; ++m) {
-            const int head = head0 + m * teams;
-            const T* from = x + head * a.x_stride[k][1];
-#pragma unroll
-            for (int v = 0; v < NV; ++v)
-                if (mine[v] && head < last) {
-                    xl[m][v] = *reinterpret_cast<const uint2*>(from + low[v]);
-                    xh[m][v] = *reinterpret_cast<const uint2*>(from + high[v]);
-                } else {
-                    xl[m][v] = xh[m][v] = make_uint2(0, 0);
-                }
-        }
-        float f[AHEAD];
-        if (weight) {
-#pragma unroll
-            for (int m = 0; m < AHEAD; ++m) {
-                f[m] = 0.f;
-#pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    float y[U];
-                    Half<T>::unpack(xl[m][v], y), Half<T>::unpack(xh[m][v], y + H);
-#pragma unroll
-                    for (int i = 0; i < U; ++i) f[m] += y[i] * y[i];
+            for (int i = 0; i < H; ++i) {
+                c[v][0][i] = w[i], c[v][1][i] = w[H + i], c[v][2][i] = c[v][3][i] = 0.f;
+                if (pair[v] >= 0) {
+                    const float2 r = turns[pair[v] + i];
+                    const float wp = paired ? w[2 * i] : w[i], wq = paired ? w[2 * i + 1] : w[H + i];
+                    c[v][0][i] = wp * r.x, c[v][1][i] = wq * r.y, c[v][2][i] = wp * r.y, c[v][3][i] = wq * r.x;
                 }
             }
-            for (int o = g.team >> 1; o; o >>= 1)
-#pragma unroll
-                for (int m = 0; m < AHEAD; ++m) f[m] += __shfl_xor_sync(~0u, f[m], o);
-#pragma unroll
-            for (int m = 0; m < AHEAD; ++m) f[m] = rsqrtf(f[m] / a.dim + a.eps);
         }
-        __syncwarp();  // the heads' channels have been read: outputs may overwrite them
+        const int64_t x_step = a.x_stride[k][1] * teams, out_step = a.out_stride[k][1] * teams;
+        const T* x = static_cast<const T*>(a.x[k]) + token * a.x_stride[k][0] + (first + mine) * a.x_stride[k][1];
+        T* out = static_cast<T*>(a.out[k]) + token * a.out_stride[k][0] + (first + mine) * a.out_stride[k][1];
+        for (int head0 = first + mine; head0 - mine < last; head0 += AHEAD * teams) {  // the whole warp
+            uint2 xp[AHEAD][NV], xq[AHEAD][NV];
 #pragma unroll
-        for (int m = 0; m < AHEAD; ++m) {
-            const int head = head0 + m * teams;
-            if (head >= last) break;
-            T* to = out + head * a.out_stride[k][1];
+            for (int m = 0; m < AHEAD; ++m, x += x_step)
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                if (!mine[v]) continue;
-                float y[U];
-                Half<T>::unpack(xl[m][v], y), Half<T>::unpack(xh[m][v], y + H);
-                if (weight) {
-                    float w[U];
-                    Half<T>::unpack(wl[v], w), Half<T>::unpack(wh[v], w + H);
-#pragma unroll
-                    for (int i = 0; i < U; ++i) y[i] = y[i] * f[m] * w[i];
+                for (int v = 0; v < NV; ++v) {
+                    xp[m][v] = xq[m][v] = make_uint2(0, 0);
+                    if (there[v] && head0 + m * teams < last) {
+                        xp[m][v] = __ldcs(reinterpret_cast<const uint2*>(x + low[v]));
+                        xq[m][v] = __ldcs(reinterpret_cast<const uint2*>(x + low[v] + apart[v]));
+                    }
                 }
-                auto rotate = [&](float& p, float& q, const float2& r) {
-                    const float p0 = p, q0 = q;
-                    p = p0 * r.x - q0 * r.y;
-                    q = p0 * r.y + q0 * r.x;
-                };
-                if (turned[v] && paired)
+            float f[AHEAD];
+            if (weight) {
 #pragma unroll
-                    for (int i = 0; i < H; ++i) rotate(y[2 * i], y[2 * i + 1], turn[v][i]);
-                else if (turned[v])
+                for (int m = 0; m < AHEAD; ++m) {
+                    float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-                    for (int i = 0; i < H; ++i) rotate(y[i], y[H + i], turn[v][i]);
-                *reinterpret_cast<uint2*>(to + low[v]) = Half<T>::pack(y);
-                *reinterpret_cast<uint2*>(to + high[v]) = Half<T>::pack(y + H);
+                    for (int v = 0; v < NV; ++v) {
+                        float y[U];
+                        Half<T>::unpack(xp[m][v], y), Half<T>::unpack(xq[m][v], y + H);
+#pragma unroll
+                        for (int i = 0; i < U; i += 2) sum = fma2(make_float2(y[i], y[i + 1]), make_float2(y[i], y[i + 1]), sum);
+                    }
+                    f[m] = sum.x + sum.y;
+                }
+                for (int o = g.team >> 1; o; o >>= 1)
+#pragma unroll
+                    for (int m = 0; m < AHEAD; ++m) f[m] += __shfl_xor_sync(~0u, f[m], o);
+#pragma unroll
+                for (int m = 0; m < AHEAD; ++m) f[m] = rsqrtf(f[m] * g.inv_dim + a.eps);
+            }
+#pragma unroll
+            for (int m = 0; m < AHEAD; ++m, out += out_step) {
+                if (head0 + m * teams >= last) continue;
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    if (!there[v]) continue;
+                    float y[U];
+                    Half<T>::unpack(xp[m][v], y), Half<T>::unpack(xq[m][v], y + H);
+                    auto two = [&](int i) { return make_float2(y[i], y[i + 1]); };
+                    auto put = [&](int i, const float2& d) { y[i] = d.x, y[i + 1] = d.y; };
+                    auto factor = [&](int n, int i) { return make_float2(c[v][n][i], c[v][n][i + 1]); };
+                    if (weight)
+#pragma unroll
+                        for (int i = 0; i < U; i += 2) put(i, mul2(two(i), make_float2(f[m], f[m])));
+                    if (pair[v] >= 0 && paired) {
+#pragma unroll
+                        for (int i = 0; i < H; ++i) {
+                            const float p = y[2 * i], q = y[2 * i + 1];
+                            put(2 * i, fma2(make_float2(q, q), make_float2(-c[v][1][i], c[v][3][i]),
+                                            mul2(make_float2(p, p), make_float2(c[v][0][i], c[v][2][i]))));
+                        }
+                    } else if (pair[v] >= 0) {
+#pragma unroll
+                        for (int i = 0; i < H; i += 2) {
+                            const float2 p = two(i), q = two(H + i), s = factor(1, i);
+                            put(i, fma2(make_float2(-s.x, -s.y), q, mul2(p, factor(0, i))));
+                            put(H + i, fma2(q, factor(3, i), mul2(p, factor(2, i))));
+                        }
+                    } else if (weight) {
+#pragma unroll
+                        for (int i = 0; i < H; i += 2) put(i, mul2(two(i), factor(0, i))), put(H + i, mul2(two(H + i), factor(1, i)));
+                    }
+                    *reinterpret_cast<uint2*>(out + low[v]) = Half<T>::pack(y);
+                    *reinterpret_cast<uint2*>(out + low[v] + apart[v]) = Half<T>::pack(y + H);
+                }
             }
         }
     }
@@ -268,23 +301,24 @@ template <typename T> cudaError_t launch(const hs_rotate_t& a, cudaStream_t s)
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    const int most = a.heads[0] > a.heads[1] ? a.heads[0] : a.heads[1];
-    g.heads_warp = (most + once - 1) / once * once;
-    while (g.heads_warp > once && a.tokens * ((a.heads[0] + g.heads_warp - 1) / g.heads_warp) < (int64_t)sms * kWarpsEnough)
+    const int heads = a.heads[0] + a.heads[1];
+    g.inv_dim = 1.f / a.dim;
+    g.heads_warp = (heads + once - 1) / once * once;
+    while (g.heads_warp > once && a.tokens * ((heads + g.heads_warp - 1) / g.heads_warp) < (int64_t)sms * kWarpsEnough)
         g.heads_warp = (g.heads_warp / 2 + once - 1) / once * once;
-    for (int k = 0; k < 2; ++k) g.chunks[k] = (a.heads[k] + g.heads_warp - 1) / g.heads_warp;
-    const int64_t grid = (a.tokens * (g.chunks[0] + g.chunks[1]) + kWarps - 1) / kWarps;
+    // a block takes the same heads of eight tokens
+    const dim3 grid((unsigned)((a.tokens + kWarps - 1) / kWarps), (heads + g.heads_warp - 1) / g.heads_warp);
     const size_t smem = sizeof(float2) * kWarps * (g.a.rope / 2);
     if (nv == 1)
-        hs_rotate_kernel<T, 1, 4><<<(unsigned)grid, kThreads, smem, s>>>(g);
+        hs_rotate_kernel<T, 1, 4><<<grid, kThreads, smem, s>>>(g);
     else if (nv == 2)
-        hs_rotate_kernel<T, 2, 2><<<(unsigned)grid, kThreads, smem, s>>>(g);
+        hs_rotate_kernel<T, 2, 2><<<grid, kThreads, smem, s>>>(g);
     else if (nv == 3)
-        hs_rotate_kernel<T, 3, 2><<<(unsigned)grid, kThreads, smem, s>>>(g);
+        hs_rotate_kernel<T, 3, 2><<<grid, kThreads, smem, s>>>(g);
     else if (nv == 4)
-        hs_rotate_kernel<T, 4, 1><<<(unsigned)grid, kThreads, smem, s>>>(g);
+        hs_rotate_kernel<T, 4, 1><<<grid, kThreads, smem, s>>>(g);
     else
-        hs_rotate_kernel<T, 8, 1><<<(unsigned)grid, kThreads, smem, s>>>(g);
+        hs_rotate_kernel<T, 8, 1><<<grid, kThreads, smem, s>>>(g);
     return cudaGetLastError();
 }
 
