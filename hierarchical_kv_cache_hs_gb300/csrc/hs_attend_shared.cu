@@ -142,6 +142,7 @@ template <bool KEYS> __device__ void bring(const SharedArgs& g, const CUtensorMa
     uint64_t* free = KEYS ? x->kfree : x->vfree;
     int stage = 0;
     uint32_t phase = 1;  // the first round waits for nothing
+    asm volatile("bar.sync 2, 192;" ::: "memory");  // the first queries' loads have been sent
     Stretch w(g, x->piece);
     while (w.next())
         for (int t = w.t0; t < w.t1; ++t)
@@ -246,7 +247,7 @@ template <typename T> __device__ void multiply(const SharedArgs& g, uint32_t sba
 // together, all of a thread's 36 pieces in flight; two blocks at a time then pass through P's buffer to tensor memory
 // (a pair's product of 128 rows computes half of its columns in lanes 64-127, which read their own copy of A).
 template <typename T, bool E4M3>
-__device__ void bring_queries(const SharedArgs& g, uint32_t sbase, uint32_t tmem, Aux* x, int64_t first, uint32_t qready)
+__device__ void bring_queries(const SharedArgs& g, uint32_t sbase, uint32_t tmem, Aux* x, int64_t first, bool begin, uint32_t qready)
 {
     const int t = threadIdx.x, ch = t & 7;
     uint4 v[4][9];
@@ -258,6 +259,7 @@ __device__ void bring_queries(const SharedArgs& g, uint32_t sbase, uint32_t tmem
 #pragma unroll
         for (int c = 0; c < 9; ++c) v[n][c] = ok ? q[8 * c] : make_uint4(0, 0, 0, 0);
     }
+    if (begin) asm volatile("bar.arrive 2, 192;" ::: "memory");  // the first rows' copies come behind these loads
     if constexpr (E4M3 && HsType<T>::is_bf16)
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
@@ -330,12 +332,14 @@ template <typename T, bool E4M3> __device__ void soften(const SharedArgs& g, uin
                    qready = tc::map_to_rank(tc::smem_addr(&x->qready), 0);
     const float c0 = a.scale * 1.4426950408889634f;
     long long j = 0;
+    bool begin = true;
     Stretch w(g, x->piece);
     while (w.next()) {
         const int64_t query = (int64_t)w.at * 128 + rank * 64 + row;
         float ref = 0.f, sum = 0.f;
         if (w.t0 < w.t1) {
-            bring_queries<T, E4M3>(g, sbase, tmem, x, (int64_t)w.at * 128 + rank * 64, qready);
+            bring_queries<T, E4M3>(g, sbase, tmem, x, (int64_t)w.at * 128 + rank * 64, begin, qready);
+            begin = false;
             const float c = E4M3 && HsType<T>::is_bf16 ? power_of_two(-x->q_up[row]) * c0 : c0;
             const int64_t limit = query < g.queries ? seen_rows(g, request_of(g, query)) : 0;
             bool seen = false;  // a row that counts has been met: ref is a maximum
@@ -435,16 +439,16 @@ template <typename T, bool E4M3> __device__ void soften(const SharedArgs& g, uin
         // The piece's end: O and the sums leave.
         const bool there = query < g.queries, some = sum > 0.f || sum != sum;
         if (w.whole) {
-            // Through P's buffer, so that eight lanes write 128 bytes of a query together: 64 channels of each half
-            // at a time, [half][query][128 B].
+            // Through shared memory, so that eight lanes write 128 bytes of a query together: 64 channels of each half
+            // at a time, [half][query][128 B], in P's buffer and the queries' by turns.
             asm volatile("griddepcontrol.wait;" ::: "memory");  // the own rows' part
             const Mix m = mix(ref, sum, there && g.own_lse ? g.own_lse[query] : -INFINITY);
             const bool mine = there && m.own != 0.f;
             T* out = static_cast<T*>(a.out);
             const uint4* own = reinterpret_cast<const uint4*>(out + (there ? offset_of(g, query, a.out_stride) : 0) + 256 * half);
-            const uint32_t buffer = sbase + kOffP + threadIdx.x * 128;
-#pragma unroll 1
+#pragma unroll 2
             for (int n = 0; n < 256; n += 64) {
+                const uint32_t buffer = sbase + (n & 64 ? 0 : kOffP);
                 uint4 old[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) old[i] = mine ? own[n / 8 + i] : make_uint4(0, 0, 0, 0);
@@ -461,7 +465,7 @@ template <typename T, bool E4M3> __device__ void soften(const SharedArgs& g, uin
 #pragma unroll
                         for (int k = 0; k < 8; ++k) f[k] = (some ? __uint_as_float(r[8 * i + k]) * m.prefix : 0.f) + (mine ? h[k] * m.own : 0.f);
                         const uint4 o = ::Piece<T>::pack(f);
-                        tc::st_shared16(buffer + (((4 * q + i) ^ (row & 7)) << 4), o.x, o.y, o.z, o.w);
+                        tc::st_shared16(buffer + threadIdx.x * 128 + (((4 * q + i) ^ (row & 7)) << 4), o.x, o.y, o.z, o.w);
                     }
                 }
                 asm volatile("bar.sync 1, 128;" ::: "memory");
@@ -469,37 +473,38 @@ template <typename T, bool E4M3> __device__ void soften(const SharedArgs& g, uin
                 for (int i = 0; i < 8; ++i) {
                     const int at = 16 * i + (threadIdx.x >> 3), ch = threadIdx.x & 7;  // of 128 rows of the buffer
                     const int64_t to = (int64_t)w.at * 128 + rank * 64 + (at & 63);
-                    const uint4 o = tc::ld_shared16(sbase + kOffP + at * 128 + ((ch ^ (at & 7)) << 4));
+                    const uint4 o = tc::ld_shared16(buffer + at * 128 + ((ch ^ (at & 7)) << 4));
                     if (to < g.queries)
                         *reinterpret_cast<uint4*>(out + offset_of(g, to, a.out_stride) + 256 * (at >> 6) + n + 8 * ch) = o;
                 }
-                asm volatile("bar.sync 1, 128;" ::: "memory");
             }
             if (there && a.lse && half == 0) a.lse[query] = m.lse;
         } else {
             Sums* part = g.parts + 2 * pair + (w.t0 == 0 ? 1 : 0);  // likewise, 32 channels at a time
-#pragma unroll 1
+#pragma unroll 2
             for (int n = 0; n < 256; n += 32) {
+                const uint32_t buffer = sbase + (n & 32 ? 0 : kOffP);
                 uint32_t r[32];
                 __syncwarp();
                 tc::tmem_ld32(tmem + kColO + n, r);
                 tc::tmem_wait_ld(r);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    tc::st_shared16(sbase + kOffP + threadIdx.x * 128 + ((i ^ (row & 7)) << 4), r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+                    tc::st_shared16(buffer + threadIdx.x * 128 + ((i ^ (row & 7)) << 4), r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
                 asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int at = 16 * i + (threadIdx.x >> 3), ch = threadIdx.x & 7;
                     *reinterpret_cast<uint4*>(&part->o[rank * 64 + (at & 63)][256 * (at >> 6) + n + 4 * ch]) =
-                        tc::ld_shared16(sbase + kOffP + at * 128 + ((ch ^ (at & 7)) << 4));
+                        tc::ld_shared16(buffer + at * 128 + ((ch ^ (at & 7)) << 4));
                 }
-                asm volatile("bar.sync 1, 128;" ::: "memory");
             }
             if (half == 0) part->ref[rank * 64 + row] = ref, part->sum[rank * 64 + row] = sum;
         }
         tc::fence_before();
+        asm volatile("bar.sync 1, 128;" ::: "memory");  // the buffers have been read
     }
+    if (begin) asm volatile("bar.arrive 2, 192;" ::: "memory");
 }
 
 template <typename T, bool E4M3>
@@ -568,18 +573,19 @@ __device__ __forceinline__ int piece_at(const Cut& g, long long at)
     return (int)(at < longer ? at / (g.share + 1) : g.extra + (at - longer) / g.share);
 }
 
-// Join the pieces of the units that several pairs worked on, with the own rows' part: blocks y take the unit that pair
-// y + 1 begins inside, where that is the first to do so; a warp takes 128 channels of a query, one pass over its
-// pieces in their order.
+// Join the pieces of the units that several pairs worked on, with the own rows' part: blocks y take unit y or, where
+// there are more units than pairs, the unit that pair y + 1 begins inside (if it is the first to do so); a warp takes
+// 128 channels of a query, one pass over its pieces in their order.
 template <typename T> __global__ void __launch_bounds__(256) hs_attend_shared_join_kernel(const __grid_constant__ SharedArgs g)
 {
     const hs_attend_t& a = g.a;
-    const int per = g.unit_tiles + g.cost, pair = blockIdx.y + 1;
-    const long long here = piece_begin(g, pair);
-    const int unit = (int)(here / per);
+    const int per = g.unit_tiles + g.cost;
+    const bool few = g.units < g.workers;
+    const long long here = few ? 0 : piece_begin(g, blockIdx.y + 1);
+    const int unit = few ? blockIdx.y : (int)(here / per);
     const long long begin = (long long)unit * per + g.cost;  // the unit's first tile
     const int first = piece_at(g, begin), last = piece_at(g, begin + g.unit_tiles - 1);
-    if (here <= begin || first != pair - 1) return;
+    if (few ? first == last : here <= begin || first != (int)blockIdx.y) return;
     const int id = blockIdx.x * 8 + (threadIdx.x >> 5), row = id >> 2, ch = 128 * (id & 3) + 4 * (threadIdx.x & 31);
     const int64_t query = (int64_t)unit * 128 + row;
     if (query >= g.queries) return;
@@ -723,36 +729,27 @@ template <typename T, bool E4M3> cudaError_t launch(const SharedArgs& g, const C
     else
         hs_attend_shared_kernel<T, E4M3><<<2 * g.workers, kThreads, kSmem, s>>>(g, map), e = cudaGetLastError();
     if (e != cudaSuccess || !g.flat || g.workers <= 1) return e;
-    return launch_after(hs_attend_shared_join_kernel<T>, dim3(128 * 4 / 8, g.workers - 1), 256, 0, s, g);
+    return launch_after(hs_attend_shared_join_kernel<T>, dim3(128 * 4 / 8, g.units < g.workers ? g.units : g.workers - 1), 256, 0, s, g);
 }
 
-template <typename T> cudaError_t run(SharedArgs& g, const hs_prefix_t& p, uint8_t* ws, const Layout& at, cudaStream_t s)
+// The prefix's rows in the workspace, in 16 bits.
+cudaError_t widen_prefix(SharedArgs& g, const hs_prefix_t& p, uint8_t* ws, const Layout& at, cudaStream_t s)
 {
-    const bool e4m3 = g.a.row_format == HS_ROWS_E4M3;
-    const void* rows = p.rows;
-    int64_t stride = p.row_stride;
-    if (e4m3 || p.lengths) {
-        const int64_t padded = padded_rows(p.n_rows);
-        const unsigned grid = (unsigned)(padded / 8);
-        const uint8_t* from = static_cast<const uint8_t*>(p.rows);
-        uint4* wide = reinterpret_cast<uint4*>(ws + at.rows);
-        float* scales = reinterpret_cast<float*>(ws + at.scales);
-        __half* logs = reinterpret_cast<__half*>(ws + at.logs);
-        if (e4m3)
-            hs_prefix_kernel<__half, true><<<grid, 256, 0, s>>>(from, p.row_stride, p.n_rows, padded, wide, scales, logs);
-        else
-            hs_prefix_kernel<T, false><<<grid, 256, 0, s>>>(from, p.row_stride, p.n_rows, padded, wide, scales, logs);
-        const cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-        rows = wide;
-        stride = 2 * HS_ROW_DIM;
-        g.scales = scales;
-        g.log_scales = logs;
-    }
-    CUtensorMap map;
-    const cudaError_t e = map_rows(&map, rows, p.n_rows, stride);
-    if (e != cudaSuccess) return e;
-    return e4m3 ? launch<T, true>(g, map, s) : launch<T, false>(g, map, s);
+    const int64_t padded = padded_rows(p.n_rows);
+    const unsigned grid = (unsigned)(padded / 8);
+    const uint8_t* from = static_cast<const uint8_t*>(p.rows);
+    uint4* wide = reinterpret_cast<uint4*>(ws + at.rows);
+    float* scales = reinterpret_cast<float*>(ws + at.scales);
+    __half* logs = reinterpret_cast<__half*>(ws + at.logs);
+    if (g.a.row_format == HS_ROWS_E4M3)
+        hs_prefix_kernel<__half, true><<<grid, 256, 0, s>>>(from, p.row_stride, p.n_rows, padded, wide, scales, logs);
+    else if (g.a.dtype == HS_TYPE_BF16)
+        hs_prefix_kernel<__nv_bfloat16, false><<<grid, 256, 0, s>>>(from, p.row_stride, p.n_rows, padded, wide, scales, logs);
+    else
+        hs_prefix_kernel<__half, false><<<grid, 256, 0, s>>>(from, p.row_stride, p.n_rows, padded, wide, scales, logs);
+    g.scales = scales;
+    g.log_scales = logs;
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -780,6 +777,16 @@ cudaError_t hs_launch_attend_shared(const hs_attend_t& a, const hs_prefix_t& p, 
     g.queries = (int64_t)a.batch * a.positions * a.heads;
     g.parts = reinterpret_cast<Sums*>(ws + at.parts);
     g.error = reinterpret_cast<int*>(ws);
+    CUtensorMap map;
+    const bool e4m3 = a.row_format == HS_ROWS_E4M3;
+    if (e4m3 || p.lengths) {
+        e = widen_prefix(g, p, ws, at, s);
+        if (e == cudaSuccess) e = map_rows(&map, ws + at.rows, p.n_rows, 2 * HS_ROW_DIM);
+    } else {
+        e = map_rows(&map, p.rows, p.n_rows, p.row_stride);
+    }
+    if (e != cudaSuccess) return e;
+    // The own rows' part comes directly before the prefix's kernel, which may begin on the SMs that it leaves.
     if (a.n_rows > 0 && (!a.slots || a.entries > 0)) {
         hs_attend_t own = a;
         own.lse = reinterpret_cast<float*>(ws + at.lse);
@@ -788,6 +795,17 @@ cudaError_t hs_launch_attend_shared(const hs_attend_t& a, const hs_prefix_t& p, 
         if (e != cudaSuccess) return e;
     }
     g.units = (int)((g.queries + 127) / 128);
-    g.cut(sms / 2 < kMaxPairs ? (sms > 1 ? sms / 2 : 1) : kMaxPairs, p.n_rows, 5, kUnitCost, kRows);
-    return a.dtype == HS_TYPE_BF16 ? run<__nv_bfloat16>(g, p, ws, at, s) : run<__half>(g, p, ws, at, s);
+    const int pairs = sms / 2 < kMaxPairs ? (sms > 1 ? sms / 2 : 1) : kMaxPairs;
+    g.cut(pairs, p.n_rows, 5, kUnitCost, kRows);
+    if (g.flat) {
+        // Each pair's partial results go out and come back, 1.2 us for ten pairs where a tile takes 1.4: few tiles take
+        // fewer pairs.
+        auto time = [&](int64_t n) { return ((int64_t)g.units * (g.unit_tiles + kUnitCost) + n - 1) / n * 1400 + n * 120; };
+        int best = pairs;
+        for (int n = pairs - 1; n > 0 && n > g.units; --n)
+            if (time(n) < time(best)) best = n;
+        g.cut(best, p.n_rows, 5, kUnitCost, kRows);
+    }
+    if (a.dtype == HS_TYPE_BF16) return e4m3 ? launch<__nv_bfloat16, true>(g, map, s) : launch<__nv_bfloat16, false>(g, map, s);
+    return e4m3 ? launch<__half, true>(g, map, s) : launch<__half, false>(g, map, s);
 }
