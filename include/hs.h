@@ -799,8 +799,8 @@ int hs_rms_norm(const hs_norm_t* args, hs_stream_t stream);
  * as a row in the form `row_format` (HS_ROWS_E4M3: scale = max|y| / 448, values
  * e4m3(y / scale) with the quotient in fp32; all zeros: scale 0; a NaN makes the
  * scale NaN).  Without weight (NULL) the latent channels stay as they are.
- * Each row is written once and whole, but for the 12 last bytes of an 8-bit row
- * and what lies between rows, which are left as they were.  Where it goes:
+ * Each row is written once and whole (the 12 last bytes of an 8-bit row as zeros);
+ * what lies between rows is left as it was.  Where it goes:
  *   start NULL  row t of `rows` (batch is ignored; n_rows >= tokens): the rows
  *               that hs_append takes
  *   start       device int32 [batch + 1], non-decreasing from 0: tokens
