@@ -13,8 +13,8 @@
 
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kWarpsEnough = 24;  // an SM
+constexpr int kThreads = 128, kWarps = kThreads / 32;
+constexpr int kWarpsEnough = 64;  // an SM
 
 struct RotateArgs {
     hs_rotate_t a;
@@ -61,7 +61,7 @@ __device__ __forceinline__ float2 fma2(const float2& a, const float2& b, const f
 }
 
 // NV: units a lane, AHEAD: heads of a team on their way together.
-template <typename T, int NV, int AHEAD> __global__ void __launch_bounds__(kThreads, NV == 1 ? 3 : 1) hs_rotate_kernel(const __grid_constant__ RotateArgs g)
+template <typename T, int NV, int AHEAD> __global__ void __launch_bounds__(kThreads, NV == 1 ? 6 : 1) hs_rotate_kernel(const __grid_constant__ RotateArgs g)
 {
     constexpr int H = Half<T>::n, U = 2 * H;  // channels of half a unit, of a unit
     extern __shared__ float2 sines[];         // [warp][pair]
@@ -306,7 +306,7 @@ template <typename T> cudaError_t launch(const hs_rotate_t& a, cudaStream_t s)
     g.heads_warp = (heads + once - 1) / once * once;
     while (g.heads_warp > once && a.tokens * ((heads + g.heads_warp - 1) / g.heads_warp) < (int64_t)sms * kWarpsEnough)
         g.heads_warp = (g.heads_warp / 2 + once - 1) / once * once;
-    // a block takes the same heads of eight tokens
+    // a block takes the same heads of several tokens
     const dim3 grid((unsigned)((a.tokens + kWarps - 1) / kWarps), (heads + g.heads_warp - 1) / g.heads_warp);
     const size_t smem = sizeof(float2) * kWarps * (g.a.rope / 2);
     if (nv == 1)

@@ -1,12 +1,14 @@
 """A latent-attention layer served from the hierarchical cache, end to end.
 
-For a few requests: the prompt's cache rows are written by the norm (8-bit rows
-of 592 bytes, or bf16 rows of 1152), the prompt's attention runs in the expanded
-form over them, and the rows go to the pinned host pool.  Each decode step then
-appends its token's row to the device tail, resolves the step's top-k indices
-(missing rows come from the host pool into the hot buffer) and attends over the
-slots in the absorbed form.  Weights are random; the indices are recent tokens
-plus random ones, in the indexer's place.
+For a few requests: the prompt's cache rows (8-bit rows of 592 bytes, or bf16 rows
+of 1152) are written with their norm and rotation, for the prompt's attention, which
+runs in the expanded form over them, and straight into the pinned host pool.  Each
+decode step then appends its token's row to the device tail, resolves the step's
+top-k indices (missing rows come from the host pool into the hot buffer) and attends
+over the slots in the absorbed form.  At the end the same requests go on from one
+shared prompt, whose rows are held and read once, with contexts of their own on the
+device.  Weights are random; the indices are recent tokens plus random ones, in the
+indexer's place.
 
     python -m hierarchical_kv_cache_hs_gb300.examples.latent_decode [--bf16]
 
@@ -23,6 +25,7 @@ from .. import hs
 
 B, H, K = 4, 16, 256              # requests, heads, indices a step
 PROMPT, TAIL, SLOTS, STEPS = 1792, 256, 512, 6
+SHARED, CONTEXT = 1500, 64        # rows that all requests share, rows of each one's own
 HIDDEN, EPS = 1024, 1e-6
 LATENT, ROPE, ROW, HEAD = hs.HS_LATENT_DIM, hs.HS_ROPE_DIM, hs.HS_ROW_DIM, hs.HS_HEAD_DIM
 SCALE = (HEAD + ROPE) ** -0.5
@@ -44,22 +47,29 @@ class Layer:
         self.row_bytes = hs.HS_ROW8_BYTES if e4m3 else 2 * ROW
         self.row_format = hs.HS_ROWS_E4M3 if e4m3 else hs.HS_ROWS_16BIT
 
-    def project(self, x, residual):
-        """Queries [n][H][192] and cache rows [n][row_bytes] of tokens with inputs x."""
+        self.inv_freq = 10000.0 ** (-torch.arange(ROPE // 2, device="cuda") * 2 / ROPE)
+
+    def project(self, x, residual, positions):
+        """Rotated queries [n][H][192] and the rows' projections [n][576] of tokens with inputs x."""
         y = torch.empty_like(x)
         hs.hs_rms_norm(x, self.norm_in, y, EPS, residual=residual, residual_out=residual,
                        stream=torch.cuda.current_stream())
         q = (y @ self.w_q.t()).view(-1, H, HEAD + ROPE)
-        kv = y @ self.w_kv.t()       # the rotation of the last 64 channels belongs here
-        rows = torch.zeros((x.shape[0], self.row_bytes), dtype=torch.uint8, device="cuda")
-        if self.e4m3:
-            hs.hs_rms_norm(kv, self.norm_latent, rows[:, :ROW], EPS, carry=ROPE,
-                           scales=rows[:, ROW:ROW + 4].view(torch.float32),
-                           stream=torch.cuda.current_stream())
-        else:
-            hs.hs_rms_norm(kv, self.norm_latent, rows.view(torch.bfloat16), EPS, carry=ROPE,
-                           stream=torch.cuda.current_stream())
-        return q, rows
+        turned = q[..., HEAD:]
+        hs.hs_norm_rotate(turned, turned, positions=positions, inv_freq=self.inv_freq,
+                          stream=torch.cuda.current_stream())
+        return q, y @ self.w_kv.t()
+
+    def write(self, kv, positions, rows, start=None, lengths=None):
+        """The tokens' cache rows: into `rows` one by one, or at their contexts' ends."""
+        hs.hs_latent_write(kv, rows, weight=self.norm_latent, eps=EPS, positions=positions,
+                           inv_freq=self.inv_freq, start=start, lengths=lengths,
+                           row_format=self.row_format, stream=torch.cuda.current_stream())
+
+    def staged(self, kv, positions):
+        rows = torch.empty((kv.shape[0], self.row_bytes), dtype=torch.uint8, device="cuda")
+        self.write(kv, positions, rows)
+        return rows
 
     def absorb(self, q):
         """Queries with the key projection absorbed: [n][H][576]."""
@@ -90,7 +100,9 @@ def run(e4m3: bool = True, seed: int = 0) -> dict:
 
     # The prompts, taken together.
     n = B * PROMPT
-    q, rows = layer.project(hidden(n), hidden(n))
+    positions = torch.arange(PROMPT, device="cuda", dtype=torch.int32).repeat(B)
+    q, kv = layer.project(hidden(n), hidden(n), positions)
+    rows = layer.staged(kv, positions)
     start = torch.arange(B + 1, device="cuda", dtype=torch.int32) * PROMPT
     out = torch.empty((n, H, HEAD), dtype=torch.bfloat16, device="cuda")
     space = torch.empty(hs.hs_latent_prefill_workspace(n, H), dtype=torch.uint8, device="cuda")
@@ -106,17 +118,20 @@ def run(e4m3: bool = True, seed: int = 0) -> dict:
 
     # Decode over the hierarchical cache: prompt rows in the host pool, new ones in the device tail.
     cap = PROMPT + TAIL
-    worst = 0.0
+    worst = read = 0.0
     with hs.Handle(B, cap, layer.row_bytes, SLOTS, -(-PROMPT // SLOTS), TAIL) as h:
-        h.host_pool()[:, :PROMPT] = rows.view(B, PROMPT, -1).cpu().numpy()
+        layer.write(kv, positions, h, start, torch.full((B,), PROMPT, dtype=torch.int32, device="cuda"))
         hs.hs_set_lengths(h.h, np.full(B, PROMPT, dtype=np.int32))
         slots = torch.empty((B, 1, K), dtype=torch.int32, device="cuda")
         out = torch.empty((B, 1, H, LATENT), dtype=torch.bfloat16, device="cuda")
         space = torch.empty(hs.hs_latent_attend_workspace(B, 1, H, K), dtype=torch.uint8, device="cuda")
         hs.hs_workspace_clear(space)
+        picked_rows = torch.empty((B, K, ROW), device="cuda")
         every = layer.rows64(rows.view(B, PROMPT, -1))
         for step in range(STEPS):
-            q, row = layer.project(hidden(B), hidden(B))
+            positions = torch.full((B,), PROMPT + step, dtype=torch.int32, device="cuda")
+            q, kv = layer.project(hidden(B), hidden(B), positions)
+            row = layer.staged(kv, positions)
             hs.hs_append(h.h, row, stream)
             every = torch.cat([every, layer.rows64(row)[:, None]], 1)
             length = PROMPT + step + 1
@@ -130,17 +145,50 @@ def run(e4m3: bool = True, seed: int = 0) -> dict:
             result = torch.einsum("bhl,hdl->bhd", out[:, 0], layer.w_uv)  # the value projection
             assert result.shape == (B, H, HEAD)
             k = torch.gather(every, 1, topk.long()[..., None].expand(-1, -1, ROW))
+            hs.hs_latent_read(h, picked_rows, slots=slots[:, 0], row_format=layer.row_format,
+                              dtype=torch.bfloat16, stream=stream)
+            read = max(read, _off(picked_rows, k))  # the rows that the slots hold are the tokens'
             p = torch.softmax(SCALE * torch.einsum("bhc,bkc->bhk", qa[:, 0].double(), k), -1)
             worst = max(worst, _off(out[:, 0], torch.einsum("bhk,bkl->bhl", p, k[..., :LATENT])))
         stats = h.stats()
         late |= hs.hs_workspace_error(space)
-    return {"prompt": prompt, "decode": worst, "misses": stats["misses"], "hits": stats["hits"],
+    shared, ran_out = _shared_prompt(layer, hidden, gen)
+    late |= ran_out
+    return {"prompt": prompt, "decode": worst, "read": read, "shared": shared, "misses": stats["misses"], "hits": stats["hits"],
             "errors": stats["err_bits"], "waits_ran_out": late}
+
+
+def _shared_prompt(layer, hidden, gen):
+    """One decode step of requests behind a shared prompt: the worst relative error of its attention."""
+    stream = torch.cuda.current_stream()
+    positions = torch.arange(SHARED, device="cuda", dtype=torch.int32)
+    prefix = layer.staged(layer.project(hidden(SHARED), hidden(SHARED), positions)[1], positions)
+    # Each request's own tokens so far, the step's among them, behind the shared ones.
+    lengths = torch.randint(1, CONTEXT + 1, (B,), generator=gen, device="cuda", dtype=torch.int32)
+    start = torch.nn.functional.pad(lengths.cumsum(0), (1, 0)).to(torch.int32)
+    positions = torch.cat([SHARED + torch.arange(n, device="cuda") for n in lengths.tolist()]).to(torch.int32)
+    n = positions.numel()
+    q, kv = layer.project(hidden(n), hidden(n), positions)
+    rows = torch.empty((B, CONTEXT, layer.row_bytes), dtype=torch.uint8, device="cuda")
+    layer.write(kv, positions, rows, start, lengths)
+    qa = layer.absorb(q[start[1:].long() - 1])[:, None]
+    out = torch.empty((B, 1, H, LATENT), dtype=torch.bfloat16, device="cuda")
+    space = torch.empty(hs.hs_latent_attend_shared_workspace(B, 1, H, CONTEXT, SHARED, layer.row_format),
+                        dtype=torch.uint8, device="cuda")
+    hs.hs_workspace_clear(space)
+    hs.hs_latent_attend_shared(qa, prefix if layer.e4m3 else prefix.view(torch.bfloat16), rows, out, SCALE,
+                               lengths=lengths, row_format=layer.row_format, workspace=space, stream=stream)
+    worst = 0.0
+    for b, m in enumerate(lengths.tolist()):
+        k = torch.cat([layer.rows64(prefix), layer.rows64(rows[b, :m])])
+        p = torch.softmax(SCALE * (qa[b, 0].double() @ k.t()), -1)
+        worst = max(worst, _off(out[b, 0], p @ k[:, :LATENT]))
+    return worst, hs.hs_workspace_error(space)
 
 
 if __name__ == "__main__":
     got = run(e4m3="--bf16" not in sys.argv[1:])
     if got["errors"] or got["waits_ran_out"]:
         sys.exit("device errors %#x, waits that ran out %d" % (got["errors"], got["waits_ran_out"]))
-    print("prompt attention: %.2e off 64 bits; decode steps: %.2e; %d misses, %d hits" %
-          (got["prompt"], got["decode"], got["misses"], got["hits"]))
+    print("prompt attention: %.2e off 64 bits; decode steps: %.2e; behind a shared prompt: %.2e; %d misses, %d hits" %
+          (got["prompt"], got["decode"], got["shared"], got["misses"], got["hits"]))

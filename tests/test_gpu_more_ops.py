@@ -652,3 +652,15 @@ def test_shared_same_bits_again_on_another_stream_and_in_a_graph(hs, e4m3):
     graph.replay()
     short, _ = _shared(hs, q, prefix, rows, **kw)
     assert torch.equal(out, short)
+
+
+@pytest.mark.parametrize("e4m3", [True, False])
+def test_together_in_the_example(e4m3):
+    """Rows written into the pool and as contexts, heads rotated, a shared prompt, rows read back, as a serving
+    loop uses them."""
+    from hierarchical_kv_cache_hs_gb300.examples import latent_decode as ex
+    got = ex.run(e4m3=e4m3, seed=3)
+    assert got["errors"] == 0 and got["waits_ran_out"] == 0
+    assert got["read"] <= 2.0 ** -24  # fp32 values of rows: one product each
+    # three roundings of at most half a step (weights, the own rows' part, output), in the 2-norm
+    assert got["shared"] <= 1.75 * 2 ** -8 and got["decode"] <= 1.5 * 2 ** -8
