@@ -119,7 +119,8 @@ int hs_latent_attend_shared(const hs_attend_t* args, const hs_prefix_t* prefix, 
     const hs_prefix_t& p = *prefix;
     if (const int rc = check_attend(a)) return rc;
     if (p.n_rows < 0 || (!p.rows && p.n_rows > 0)) return HS_ERR_ARG;
-    if (p.n_rows > INT32_MAX || (int64_t)a.batch * a.positions * a.heads > INT32_MAX) return HS_ERR_LIMIT;
+    if (p.n_rows > INT32_MAX || (int64_t)a.batch * a.positions * a.heads > INT32_MAX || (p.n_rows > 1 && p.row_stride >= (int64_t)1 << 40))
+        return HS_ERR_LIMIT;
     if (!aligned(p.rows, 16) || !aligned(p.lengths, 4)) return HS_ERR_ARG;
     if (p.n_rows > 1 && (p.row_stride < row_bytes(a.row_format) || p.row_stride % 16)) return HS_ERR_ARG;
     const size_t need = hs_attend_shared_workspace_bytes(a.batch, a.positions, a.heads, a.slots ? a.entries : a.n_rows, p.n_rows);

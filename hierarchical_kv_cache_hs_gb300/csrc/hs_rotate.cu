@@ -216,9 +216,8 @@ template <typename T> __global__ void __launch_bounds__(kThreads) hs_rotate_any_
     extern __shared__ float2 turns[];
     const hs_rotate_t& a = g.a;
     const int heads = a.heads[0] + a.heads[1], pairs = a.rope / 2;
-    const int chunks = (heads + g.heads_block - 1) / g.heads_block;  // blocks that share a token's heads
-    const int64_t first = (int64_t)(blockIdx.x / chunks) * g.tokens_block;
-    const int head0 = (int)(blockIdx.x % chunks) * g.heads_block;
+    const int64_t first = (int64_t)blockIdx.x * g.tokens_block;
+    const int head0 = blockIdx.y * g.heads_block;
     const int tokens = (int)min((int64_t)g.tokens_block, a.tokens - first), some = min(g.heads_block, heads - head0);
     for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
         const int t = i / pairs;
@@ -268,9 +267,9 @@ template <typename T> cudaError_t launch_any(RotateArgs& g, cudaStream_t s)
     const int most = a.rope ? 2048 / a.rope : items;  // sines and cosines: at most 8 KB a block
     if (g.tokens_block > most) g.tokens_block = most;
     if (g.tokens_block > a.tokens) g.tokens_block = (int)a.tokens;
-    const int64_t grid = (a.tokens + g.tokens_block - 1) / g.tokens_block * ((heads + g.heads_block - 1) / g.heads_block);
+    const dim3 grid((unsigned)((a.tokens + g.tokens_block - 1) / g.tokens_block), (heads + g.heads_block - 1) / g.heads_block);
     const size_t smem = sizeof(float2) * g.tokens_block * (a.rope / 2) + sizeof(float) * a.dim * kWarps;
-    hs_rotate_any_kernel<T><<<(unsigned)grid, kThreads, smem, s>>>(g);
+    hs_rotate_any_kernel<T><<<grid, kThreads, smem, s>>>(g);
     return cudaGetLastError();
 }
 

@@ -817,7 +817,7 @@ int hs_rms_norm(const hs_norm_t* args, hs_stream_t stream);
  *   x       [tokens][576] of `dtype` (bf16 or fp16, also the type of 16-bit
  *           rows), channels contiguous, x_stride elements between tokens, a
  *           multiple of 8; x, rows and weight 16-byte aligned, row_stride and
- *           request_stride in bytes, multiples of 16
+ *           request_stride in bytes, multiples of 16; rows do not overlap x
  *   weight  [512] of `dtype`
  * Source: no passage (the producer of the rows; the pages start from the rows).
  */
@@ -923,15 +923,16 @@ int hs_norm_rotate(const hs_rotate_t* args, hs_stream_t stream);
  * The prefix is held and read once for all requests, and its products are those
  * of all their queries together.
  *   rows            n_rows rows of args->row_format (16-bit ones of args->dtype),
- *                   row_stride bytes apart, a multiple of 16; 16-byte aligned
+ *                   row_stride bytes apart, a multiple of 16 below 2^40; device
+ *                   memory, 16-byte aligned
  *   lengths         device int32 [batch], clamped to [0, n_rows]; NULL: all rows
  *                   for every request
  * A prefix row that a request does not see has no part in its outputs, whatever it
  * holds; one with a value that is not finite makes the output NaN of every request
  * that sees it.
  * Roundings as in hs_latent_attend, and the own rows' part is rounded to `dtype`
- * before it is joined.  out and lse: whole, as there.  With no row at all out is 0
- * and lse -inf.
+ * before it is joined.  out and lse are of the whole; with no row at all out is 0 and
+ * lse -inf.  batch * positions * heads stays below 2^31.
  * The workspace call takes what hs_latent_attend's does, and the prefix's rows
  * and form.  8-bit prefixes, and prefixes with lengths, are copied into the
  * workspace in 16 bits at every call (1152 bytes a row).

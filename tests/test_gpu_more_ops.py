@@ -654,6 +654,81 @@ def test_shared_same_bits_again_on_another_stream_and_in_a_graph(hs, e4m3):
     assert torch.equal(out, short)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_shared_two_calls_at_once(hs, e4m3):
+    """Calls on two streams that overlap, each with a workspace of its own."""
+    g = _gen(19)
+    form = hs.HS_ROWS_E4M3 if e4m3 else hs.HS_ROWS_16BIT
+    calls = []
+    for B, H, M, N in ((20, 16, 5000, 300), (3, 128, 9000, 40)):
+        q, prefix, rows = _randn(g, B, 1, H, 576), _form(_randn(g, M, 576), e4m3), _form(_randn(g, B, N, 576), e4m3)
+        lengths = _ints([N] * B)
+        want, _ = _shared(hs, q, prefix, rows, e4m3=e4m3, lengths=lengths)
+        ws = torch.empty(hs.hs_latent_attend_shared_workspace(B, 1, H, N, M, form), dtype=torch.uint8, device="cuda")
+        calls.append((q, prefix, rows, lengths, torch.empty_like(want), ws, torch.cuda.Stream(), want))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for q, prefix, rows, lengths, out, ws, stream, _ in calls:
+            hs.hs_latent_attend_shared(q, prefix, rows, out, SCALE, lengths=lengths, workspace=ws, row_format=form, stream=stream)
+    torch.cuda.synchronize()
+    for call in calls:
+        assert torch.equal(call[4], call[7])
+
+
+_FIRST_IN_A_GRAPH = """
+import torch
+from hierarchical_kv_cache_hs_gb300 import hs
+bf, i32 = torch.bfloat16, torch.int32
+def randn(*s): return torch.randn(s, device="cuda").to(bf)
+x, q, prefix, qa = randn(40, 576), randn(40, 16, 192), randn(300, 576), randn(2, 1, 16, 576)
+rows, back = torch.zeros(2, 30, 576, dtype=bf, device="cuda"), torch.zeros(40, 576, dtype=bf, device="cuda")
+start, lengths = (torch.tensor(v, dtype=i32, device="cuda") for v in ([0, 20, 40], [25, 30]))
+positions, freq, turned = torch.arange(40, dtype=i32, device="cuda"), torch.rand(32, device="cuda"), torch.empty_like(q)
+out = torch.zeros(2, 1, 16, 512, dtype=bf, device="cuda")
+ws = torch.empty(hs.hs_latent_attend_shared_workspace(2, 1, 16, 30, 300), dtype=torch.uint8, device="cuda")
+def calls(s):
+    hs.hs_latent_write(x, rows, positions=positions, inv_freq=freq, start=start, lengths=lengths, stream=s)
+    hs.hs_latent_read(rows, back, start=start, lengths=lengths, stream=s)
+    hs.hs_norm_rotate(q, turned, positions=positions, inv_freq=freq, stream=s)
+    hs.hs_latent_attend_shared(qa, prefix, rows, out, 0.07, lengths=lengths, prefix_lengths=lengths, workspace=ws, stream=s)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    calls(torch.cuda.current_stream())
+graph.replay()
+torch.cuda.synchronize()
+found = [t.clone() for t in (rows, back, turned, out)]
+assert all(f.abs().sum() > 0 for f in found)
+calls(torch.cuda.current_stream())
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(found, (rows, back, turned, out)))
+"""
+
+
+def test_first_calls_in_a_graph():
+    """A program whose first calls are captured."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _FIRST_IN_A_GRAPH], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_rows_behind_32_bits(hs):
+    """Rows whose byte offsets pass 2^32, written and read back."""
+    n = 7_500_000  # 8-bit rows: 4.4 GB
+    rows = torch.zeros((1, n, 592), dtype=torch.uint8, device="cuda")
+    g = _gen(20)
+    x = _randn(g, 33, 576)
+    hs.hs_latent_write(x, rows, start=_ints([0, 33]), lengths=_ints([n]), row_format=hs.HS_ROWS_E4M3)
+    staged = torch.zeros((33, 592), dtype=torch.uint8, device="cuda")
+    hs.hs_latent_write(x, staged, row_format=hs.HS_ROWS_E4M3)
+    assert torch.equal(rows[0, -33:], staged) and not rows[0, :-33].any()
+    out = torch.empty((1, 33, 576), dtype=BF, device="cuda")
+    hs.hs_latent_read(rows, out, slots=torch.arange(n - 33, n, dtype=torch.int32, device="cuda")[None], row_format=hs.HS_ROWS_E4M3)
+    assert torch.equal(out[0], _wide(staged, True).float().to(BF))
+
+
 @pytest.mark.parametrize("e4m3", [True, False])
 def test_together_in_the_example(e4m3):
     """Rows written into the pool and as contexts, heads rotated, a shared prompt, rows read back, as a serving

@@ -142,6 +142,7 @@ def test_shared_refuses(hs, over):
 
 def test_shared_limits(hs):
     assert _shared(hs, dict(n_rows=1 << 31)) == hs.HS_ERR_LIMIT
+    assert _shared(hs, dict(row_stride=1 << 40)) == hs.HS_ERR_LIMIT
     assert _shared(hs, heads=hs.HS_MAX_HEADS + 1) == hs.HS_ERR_LIMIT
     assert _shared(hs, batch=4096, positions=1024, heads=1024) == hs.HS_ERR_LIMIT
     assert hs.lib.hs_latent_attend_shared(None, None, None) == hs.HS_ERR_ARG
