@@ -60,48 +60,31 @@ __device__ __forceinline__ float2 fma2(const float2& a, const float2& b, const f
     return d;
 }
 
-// NV: units a lane, AHEAD: heads of a team on their way together.
-template <typename T, int NV, int AHEAD> __global__ void __launch_bounds__(kThreads, NV == 1 ? 6 : 1) hs_rotate_kernel(const __grid_constant__ RotateArgs g)
-{
-    constexpr int H = Half<T>::n, U = 2 * H;  // channels of half a unit, of a unit
-    extern __shared__ float2 sines[];         // [warp][pair]
-    const hs_rotate_t& a = g.a;
-    const int lane = threadIdx.x & 31;
-    const int64_t token = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (token >= a.tokens) return;
-    const int head_first = blockIdx.y * g.heads_warp, head_last = min(head_first + g.heads_warp, a.heads[0] + a.heads[1]);
-    const int pairs = a.rope / 2, units = a.dim / U;
-    const bool paired = a.rotation == HS_ROTATE_PAIRS;
-    // Where this lane's units lie: the first half's channel, and how far behind it the second one's is.
-    const int at = lane & (g.team - 1), teams = 32 / g.team, mine = lane / g.team;
-    int low[NV], apart[NV], pair[NV];  // the first pair, -1: not rotary
-    bool there[NV];
+// A lane's channels of a head: NV units, where their first halves lie and how far behind it the second ones, and its
+// factors, weights times sines and cosines: for a rotary unit of two halves p and q (or of pairs p, q) c[0] p - c[1] q
+// and c[2] p + c[3] q; else c[0] and c[1] are weights.
+template <typename T, int NV> struct Lane {
+    static constexpr int H = Half<T>::n, U = 2 * H;  // channels of half a unit, of a unit
+    int low[NV], apart[NV], pair[NV];                // pair: the first, -1: not rotary
+    bool there[NV], paired, normed;
+    float c[NV][4][H];
+
+    __device__ Lane(const hs_rotate_t& a, int team, int at) : paired(a.rotation == HS_ROTATE_PAIRS), normed(false)
+    {
+        const int pairs = a.rope / 2, units = a.dim / U;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int u = v * g.team + at, n = u * U - a.rope_at;
-        there[v] = u < units;
-        pair[v] = there[v] && n >= 0 && n < a.rope ? n / 2 : -1;
-        const bool halves = pair[v] >= 0 && !paired;  // unit i of the rotary channels: H from either half of them
-        low[v] = halves ? a.rope_at + n / 2 : u * U;
-        apart[v] = halves ? pairs : H;
+        for (int v = 0; v < NV; ++v) {
+            const int u = v * team + at, n = u * U - a.rope_at;
+            there[v] = u < units;
+            pair[v] = there[v] && n >= 0 && n < a.rope ? n / 2 : -1;
+            const bool halves = pair[v] >= 0 && !paired;  // unit i of the rotary channels: H from either half of them
+            low[v] = halves ? a.rope_at + n / 2 : u * U;
+            apart[v] = halves ? pairs : H;
+        }
     }
-
-    float2* turns = sines + (threadIdx.x >> 5) * pairs;
-    if (pairs) {
-        const int position = a.positions[token];
-        for (int i = lane; i < pairs; i += 32) turns[i] = hs_rotation(position, hs_turn(a.inv_freq[i]));
-        __syncwarp();
-    }
-
-#pragma unroll 1
-    for (int k = 0; k < 2; ++k) {  // queries, keys
-        const int before = k ? a.heads[0] : 0;
-        const int first = max(head_first - before, 0), last = min(head_last - before, a.heads[k]);
-        if (first >= last) continue;
-        // A lane's factors, weights times sines and cosines: for a rotary unit of two halves p and q (or of pairs p, q)
-        // c[0] p - c[1] q and c[2] p + c[3] q; else c[0] and c[1] are weights.
-        const T* weight = static_cast<const T*>(a.weight[k]);
-        float c[NV][4][H];
+    __device__ void load_factors(const T* weight, const float2* turns)
+    {
+        normed = weight != nullptr;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             float w[U];
@@ -121,6 +104,75 @@ template <typename T, int NV, int AHEAD> __global__ void __launch_bounds__(kThre
                 }
             }
         }
+    }
+    __device__ float squares(const uint2 (&xp)[NV], const uint2 (&xq)[NV]) const
+    {
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            float y[U];
+            Half<T>::unpack(xp[v], y), Half<T>::unpack(xq[v], y + H);
+#pragma unroll
+            for (int i = 0; i < U; i += 2) sum = fma2(make_float2(y[i], y[i + 1]), make_float2(y[i], y[i + 1]), sum);
+        }
+        return sum.x + sum.y;
+    }
+    __device__ void turn(int v, uint2& xp, uint2& xq, float f) const  // f: 1 / sqrt of the head's mean square
+    {
+        float y[U];
+        Half<T>::unpack(xp, y), Half<T>::unpack(xq, y + H);
+        auto two = [&](int i) { return make_float2(y[i], y[i + 1]); };
+        auto put = [&](int i, const float2& d) { y[i] = d.x, y[i + 1] = d.y; };
+        auto factor = [&](int n, int i) { return make_float2(c[v][n][i], c[v][n][i + 1]); };
+        if (normed)
+#pragma unroll
+            for (int i = 0; i < U; i += 2) put(i, mul2(two(i), make_float2(f, f)));
+        if (pair[v] >= 0 && paired) {
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                const float p = y[2 * i], q = y[2 * i + 1];
+                put(2 * i, fma2(make_float2(q, q), make_float2(-c[v][1][i], c[v][3][i]),
+                                mul2(make_float2(p, p), make_float2(c[v][0][i], c[v][2][i]))));
+            }
+        } else if (pair[v] >= 0) {
+#pragma unroll
+            for (int i = 0; i < H; i += 2) {
+                const float2 p = two(i), q = two(H + i), s = factor(1, i);
+                put(i, fma2(make_float2(-s.x, -s.y), q, mul2(p, factor(0, i))));
+                put(H + i, fma2(q, factor(3, i), mul2(p, factor(2, i))));
+            }
+        } else if (normed) {
+#pragma unroll
+            for (int i = 0; i < H; i += 2) put(i, mul2(two(i), factor(0, i))), put(H + i, mul2(two(H + i), factor(1, i)));
+        }
+        xp = Half<T>::pack(y), xq = Half<T>::pack(y + H);
+    }
+};
+
+// NV: units a lane, AHEAD: heads of a team on their way together.
+template <typename T, int NV, int AHEAD> __global__ void __launch_bounds__(kThreads, NV == 1 ? 6 : 1) hs_rotate_kernel(const __grid_constant__ RotateArgs g)
+{
+    extern __shared__ float2 sines[];  // [warp][pair]
+    const hs_rotate_t& a = g.a;
+    const int lane = threadIdx.x & 31;
+    const int64_t token = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (token >= a.tokens) return;
+    const int head_first = blockIdx.y * g.heads_warp, head_last = min(head_first + g.heads_warp, a.heads[0] + a.heads[1]);
+    const int pairs = a.rope / 2;
+    float2* turns = sines + (threadIdx.x >> 5) * pairs;
+    if (pairs) {
+        const int position = a.positions[token];
+        for (int i = lane; i < pairs; i += 32) turns[i] = hs_rotation(position, hs_turn(a.inv_freq[i]));
+        __syncwarp();
+    }
+    const int teams = 32 / g.team, mine = lane / g.team;
+    Lane<T, NV> l(a, g.team, lane & (g.team - 1));
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {  // queries, keys
+        const int before = k ? a.heads[0] : 0;
+        const int first = max(head_first - before, 0), last = min(head_last - before, a.heads[k]);
+        if (first >= last) continue;
+        l.load_factors(static_cast<const T*>(a.weight[k]), turns);
         const int64_t x_step = a.x_stride[k][1] * teams, out_step = a.out_stride[k][1] * teams;
         const T* x = static_cast<const T*>(a.x[k]) + token * a.x_stride[k][0] + (first + mine) * a.x_stride[k][1];
         T* out = static_cast<T*>(a.out[k]) + token * a.out_stride[k][0] + (first + mine) * a.out_stride[k][1];
@@ -131,25 +183,15 @@ template <typename T, int NV, int AHEAD> __global__ void __launch_bounds__(kThre
 #pragma unroll
                 for (int v = 0; v < NV; ++v) {
                     xp[m][v] = xq[m][v] = make_uint2(0, 0);
-                    if (there[v] && head0 + m * teams < last) {
-                        xp[m][v] = __ldcs(reinterpret_cast<const uint2*>(x + low[v]));
-                        xq[m][v] = __ldcs(reinterpret_cast<const uint2*>(x + low[v] + apart[v]));
+                    if (l.there[v] && head0 + m * teams < last) {
+                        xp[m][v] = __ldcs(reinterpret_cast<const uint2*>(x + l.low[v]));
+                        xq[m][v] = __ldcs(reinterpret_cast<const uint2*>(x + l.low[v] + l.apart[v]));
                     }
                 }
             float f[AHEAD];
-            if (weight) {
+            if (l.normed) {
 #pragma unroll
-                for (int m = 0; m < AHEAD; ++m) {
-                    float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-                    for (int v = 0; v < NV; ++v) {
-                        float y[U];
-                        Half<T>::unpack(xp[m][v], y), Half<T>::unpack(xq[m][v], y + H);
-#pragma unroll
-                        for (int i = 0; i < U; i += 2) sum = fma2(make_float2(y[i], y[i + 1]), make_float2(y[i], y[i + 1]), sum);
-                    }
-                    f[m] = sum.x + sum.y;
-                }
+                for (int m = 0; m < AHEAD; ++m) f[m] = l.squares(xp[m], xq[m]);
                 for (int o = g.team >> 1; o; o >>= 1)
 #pragma unroll
                     for (int m = 0; m < AHEAD; ++m) f[m] += __shfl_xor_sync(~0u, f[m], o);
@@ -161,35 +203,10 @@ template <typename T, int NV, int AHEAD> __global__ void __launch_bounds__(kThre
                 if (head0 + m * teams >= last) continue;
 #pragma unroll
                 for (int v = 0; v < NV; ++v) {
-                    if (!there[v]) continue;
-                    float y[U];
-                    Half<T>::unpack(xp[m][v], y), Half<T>::unpack(xq[m][v], y + H);
-                    auto two = [&](int i) { return make_float2(y[i], y[i + 1]); };
-                    auto put = [&](int i, const float2& d) { y[i] = d.x, y[i + 1] = d.y; };
-                    auto factor = [&](int n, int i) { return make_float2(c[v][n][i], c[v][n][i + 1]); };
-                    if (weight)
-#pragma unroll
-                        for (int i = 0; i < U; i += 2) put(i, mul2(two(i), make_float2(f[m], f[m])));
-                    if (pair[v] >= 0 && paired) {
-#pragma unroll
-                        for (int i = 0; i < H; ++i) {
-                            const float p = y[2 * i], q = y[2 * i + 1];
-                            put(2 * i, fma2(make_float2(q, q), make_float2(-c[v][1][i], c[v][3][i]),
-                                            mul2(make_float2(p, p), make_float2(c[v][0][i], c[v][2][i]))));
-                        }
-                    } else if (pair[v] >= 0) {
-#pragma unroll
-                        for (int i = 0; i < H; i += 2) {
-                            const float2 p = two(i), q = two(H + i), s = factor(1, i);
-                            put(i, fma2(make_float2(-s.x, -s.y), q, mul2(p, factor(0, i))));
-                            put(H + i, fma2(q, factor(3, i), mul2(p, factor(2, i))));
-                        }
-                    } else if (weight) {
-#pragma unroll
-                        for (int i = 0; i < H; i += 2) put(i, mul2(two(i), factor(0, i))), put(H + i, mul2(two(H + i), factor(1, i)));
-                    }
-                    *reinterpret_cast<uint2*>(out + low[v]) = Half<T>::pack(y);
-                    *reinterpret_cast<uint2*>(out + low[v] + apart[v]) = Half<T>::pack(y + H);
+                    if (!l.there[v]) continue;
+                    l.turn(v, xp[m][v], xq[m][v], f[m]);
+                    *reinterpret_cast<uint2*>(out + l.low[v]) = xp[m][v];
+                    *reinterpret_cast<uint2*>(out + l.low[v] + l.apart[v]) = xq[m][v];
                 }
             }
         }
