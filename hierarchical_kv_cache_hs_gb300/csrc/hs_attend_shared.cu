@@ -51,11 +51,13 @@ constexpr int kOffAux = kOffP + 2 * kBlock;
 
 struct Aux {
     uint64_t kfull[kKStages], kfree[kKStages], vfull[kVStages], vfree[kVStages], qready, sfull, sread, pready, pvdone, spare;
+    uint64_t scales_full[2], scales_free[2];
     uint32_t tmem;
     int dead;
     Piece piece;
     int8_t q_up[64];  // power of two on a bf16 query held in fp16
     float red[2][128];
+    alignas(16) float scales[2][2][kRows];  // of 8-bit rows, and their logarithms, by the tile's parity
 };
 constexpr int kSmem = kOffAux + (int)sizeof(Aux);
 static_assert(kSmem <= 232448, "shared memory");
@@ -74,7 +76,7 @@ struct SharedArgs : Cut {
     int64_t prefix_rows;
     int64_t queries;            // below 2^31
     const float* scales;        // of 8-bit rows
-    const __half* log_scales;   // base 2, not below kLeastLogScale
+    const float* log_scales;    // base 2, not below kLeastLogScale
     const float* own_lse;       // NULL: no own rows
     Sums* parts;                // two a pair
     int* error;
@@ -134,8 +136,8 @@ __device__ __forceinline__ void tile_load(uint32_t dst, const CUtensorMap* map, 
                  : "memory");
 }
 
-// Keys or values of a piece's tiles (a warp; its first lane starts the copies).
-template <bool KEYS> __device__ void bring(const SharedArgs& g, const CUtensorMap* map, uint32_t sbase, Aux* x, uint32_t rank)
+// Keys (and 8-bit rows' scales) or values of a piece's tiles (a warp; its first lane starts the copies).
+template <bool KEYS, bool SCALES> __device__ void bring(const SharedArgs& g, const CUtensorMap* map, uint32_t sbase, Aux* x, uint32_t rank)
 {
     constexpr int kStages = KEYS ? kKStages : kVStages, kBlocks = KEYS ? 3 : 2, kBytes = kBlocks * kBlock;
     uint64_t* full = KEYS ? x->kfull : x->vfull;
@@ -143,9 +145,20 @@ template <bool KEYS> __device__ void bring(const SharedArgs& g, const CUtensorMa
     int stage = 0;
     uint32_t phase = 1;  // the first round waits for nothing
     asm volatile("bar.sync 2, 192;" ::: "memory");  // the first queries' loads have been sent
+    long long j = 0;  // tiles so far
     Stretch w(g, x->piece);
     while (w.next())
-        for (int t = w.t0; t < w.t1; ++t)
+        for (int t = w.t0; t < w.t1; ++t, ++j) {
+            if (SCALES && (threadIdx.x & 31) == 0) {
+                const int s = j & 1;
+                wait(tc::smem_addr(&x->scales_free[s]), (uint32_t)(j >> 1 & 1) ^ 1, &x->dead, g.error);
+                if (!*(volatile int*)&x->dead) {
+                    const uint32_t bar = tc::smem_addr(&x->scales_full[s]);
+                    tc::mbar_expect(bar, 2 * kRows * sizeof(float));
+                    tc::bulk_load(tc::smem_addr(x->scales[s][0]), g.scales + (int64_t)t * kRows, kRows * sizeof(float), bar);
+                    tc::bulk_load(tc::smem_addr(x->scales[s][1]), g.log_scales + (int64_t)t * kRows, kRows * sizeof(float), bar);
+                }
+            }
 #pragma unroll 1
             for (int n = 0; n < (KEYS ? 3 : 4); ++n) {
                 if ((threadIdx.x & 31) == 0) {
@@ -163,6 +176,7 @@ template <bool KEYS> __device__ void bring(const SharedArgs& g, const CUtensorMa
                 __syncwarp();
                 if (++stage == kStages) stage = 0, phase ^= 1;
             }
+        }
 }
 
 // After a wait that gave up: what was issued must be complete before tensor memory is freed.
@@ -348,12 +362,14 @@ template <typename T, bool E4M3> __device__ void soften(const SharedArgs& g, uin
                 const int live = (int)min(max(limit - key0, (int64_t)0), (int64_t)64);  // keys of these 64 that count
                 const int s = j & 1;
                 float wt[E4M3 ? 64 : 1];
-                if constexpr (E4M3)
+                if constexpr (E4M3) {
+                    wait(tc::smem_addr(&x->scales_full[s]), j >> 1 & 1, &x->dead, g.error);
 #pragma unroll
                     for (int i = 0; i < 64; i += 4) {
-                        const float4 f = *reinterpret_cast<const float4*>(g.scales + key0 + i);
+                        const float4 f = *reinterpret_cast<const float4*>(&x->scales[s][0][64 * half + i]);
                         wt[i] = f.x, wt[i + 1] = f.y, wt[i + 2] = f.z, wt[i + 3] = f.w;
                     }
+                }
                 wait(tc::smem_addr(&x->sfull), j & 1, &x->dead, g.error);
                 tc::fence_after();
                 uint32_t r[2][32];
@@ -366,9 +382,10 @@ template <typename T, bool E4M3> __device__ void soften(const SharedArgs& g, uin
                 if (lane == 0) tc::mbar_arrive_cluster(sread);  // the next tile's scores may come
                 float v[64], top = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < 64; ++i) {
-                    v[i] = __uint_as_float(r[i >> 5][i & 31]) * c;
-                    if constexpr (E4M3) v[i] *= wt[i];
+                for (int i = 0; i < 64; i += 2) {
+                    v[i] = __uint_as_float(r[i >> 5][i & 31]), v[i + 1] = __uint_as_float(r[i >> 5][(i & 31) + 1]);
+                    mul2(v[i], v[i + 1], c, c);
+                    if constexpr (E4M3) mul2(v[i], v[i + 1], wt[i], wt[i + 1]);
                 }
                 if (live < 64)
 #pragma unroll
@@ -376,12 +393,15 @@ template <typename T, bool E4M3> __device__ void soften(const SharedArgs& g, uin
                         if (i >= live) v[i] = -INFINITY;
                 if constexpr (E4M3) {
 #pragma unroll
-                    for (int i = 0; i < 64; i += 8) {
-                        float lw[8];
-                        ::Piece<__half>::unpack(*reinterpret_cast<const uint4*>(g.log_scales + key0 + i), lw);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) top = fmaxf(top, v[i + k] + lw[k]);
+                    for (int i = 0; i < 64; i += 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(&x->scales[s][1][64 * half + i]);
+                        float lw[4] = {f.x, f.y, f.z, f.w};
+                        tc::add2(lw[0], lw[1], v[i], v[i + 1]);
+                        tc::add2(lw[2], lw[3], v[i + 2], v[i + 3]);
+                        top = tc::max3(tc::max3(top, lw[0], lw[1]), lw[2], lw[3]);
                     }
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(tc::smem_addr(&x->scales_free[s]));
                 } else {
 #pragma unroll
                     for (int i = 0; i < 64; i += 2) top = tc::max3(top, v[i], v[i + 1]);
@@ -398,13 +418,17 @@ template <typename T, bool E4M3> __device__ void soften(const SharedArgs& g, uin
                 const bool scale_o = seen && keep != 1.f;
                 seen = seen || top > -INFINITY;
                 uint32_t e[32];
+                float sums[2] = {0.f, 0.f};
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
-                    float p0 = tc::exp2_approx(v[2 * i] - ref), p1 = tc::exp2_approx(v[2 * i + 1] - ref);
-                    sum += p0 + p1;
-                    if constexpr (E4M3) p0 *= wt[2 * i], p1 *= wt[2 * i + 1];
+                    float p0 = v[2 * i], p1 = v[2 * i + 1];
+                    tc::add2(p0, p1, -ref, -ref);
+                    p0 = tc::exp2_approx(p0), p1 = tc::exp2_approx(p1);
+                    tc::add2(sums[0], sums[1], p0, p1);
+                    if constexpr (E4M3) mul2(p0, p1, wt[2 * i], wt[2 * i + 1]);
                     e[i] = pack2<std::conditional_t<E4M3, __half, T>>(p0, p1);
                 }
+                sum += sums[0] + sums[1];
                 // P's buffer and O are free once the last tile's product is done
                 if (j >= 1) wait(tc::smem_addr(&x->pvdone), (j - 1) & 1, &x->dead, g.error);
                 if (__any_sync(~0u, scale_o)) {
@@ -527,6 +551,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         x->dead = 0;
         for (int i = 0; i < kKStages; ++i) tc::mbar_init(tc::smem_addr(&x->kfull[i]), 1), tc::mbar_init(tc::smem_addr(&x->kfree[i]), 1);
         for (int i = 0; i < kVStages; ++i) tc::mbar_init(tc::smem_addr(&x->vfull[i]), 1), tc::mbar_init(tc::smem_addr(&x->vfree[i]), 1);
+        for (int i = 0; i < 2; ++i) tc::mbar_init(tc::smem_addr(&x->scales_full[i]), 1), tc::mbar_init(tc::smem_addr(&x->scales_free[i]), 4);
         tc::mbar_init(tc::smem_addr(&x->qready), 8);
         tc::mbar_init(tc::smem_addr(&x->sfull), 1);
         tc::mbar_init(tc::smem_addr(&x->sread), 8);
@@ -545,9 +570,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (warp < 4)
             soften<T, E4M3>(g, sbase, x, rank, pair);
         else if (warp == 4)
-            bring<true>(g, &map, sbase, x, rank);
+            bring<true, E4M3>(g, &map, sbase, x, rank);
         else if (warp == 5)
-            bring<false>(g, &map, sbase, x, rank);
+            bring<false, false>(g, &map, sbase, x, rank);
         else if (rank == 0)
             multiply<Operand>(g, sbase, x);
         if (*(volatile int*)&x->dead) {  // copies may be in flight, and count on the first CTA's barriers: half a millisecond
@@ -574,10 +599,27 @@ __device__ __forceinline__ int piece_at(const Cut& g, long long at)
 }
 
 // Join the pieces of the units that several pairs worked on, with the own rows' part: blocks y take unit y or, where
-// there are more units than pairs, the unit that pair y + 1 begins inside (if it is the first to do so); a warp takes
-// 128 channels of a query, one pass over its pieces in their order.
-template <typename T> __global__ void __launch_bounds__(256) hs_attend_shared_join_kernel(const __grid_constant__ SharedArgs g)
+// there are more units than pairs, the unit that pair y + 1 begins inside (if it is the first to do so).  Each query's
+// 128 channels are one or several warps', which share its pieces; one pass, and the order of the sums is fixed.
+struct Joined {
+    float top, sum;
+    float4 acc;
+    __device__ void add(float ref, float l, const float4& o)
+    {
+        // without a branch, so that the loads of several pieces are in flight; a sum of 0: no row counted
+        const float up = l == 0.f ? top : fmaxf(top, ref), base = up == -INFINITY ? 0.f : up;
+        const float keep = tc::exp2_approx(top - base), w = l == 0.f ? 0.f : tc::exp2_approx(ref - base);
+        top = up;
+        sum = sum * keep + w * l;
+        acc.x = acc.x * keep + (l == 0.f ? 0.f : w * o.x);
+        acc.y = acc.y * keep + (l == 0.f ? 0.f : w * o.y);
+        acc.z = acc.z * keep + (l == 0.f ? 0.f : w * o.z);
+        acc.w = acc.w * keep + (l == 0.f ? 0.f : w * o.w);
+    }
+};
+template <typename T, int WARPS> __global__ void __launch_bounds__(256) hs_attend_shared_join_kernel(const __grid_constant__ SharedArgs g)
 {
+    __shared__ Joined others[WARPS > 1 ? 8 : 1][32];
     const hs_attend_t& a = g.a;
     const int per = g.unit_tiles + g.cost;
     const bool few = g.units < g.workers;
@@ -586,37 +628,39 @@ template <typename T> __global__ void __launch_bounds__(256) hs_attend_shared_jo
     const long long begin = (long long)unit * per + g.cost;  // the unit's first tile
     const int first = piece_at(g, begin), last = piece_at(g, begin + g.unit_tiles - 1);
     if (few ? first == last : here <= begin || first != (int)blockIdx.y) return;
-    const int id = blockIdx.x * 8 + (threadIdx.x >> 5), row = id >> 2, ch = 128 * (id & 3) + 4 * (threadIdx.x & 31);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % WARPS;
+    const int id = blockIdx.x * (8 / WARPS) + warp / WARPS, row = id >> 2, ch = 128 * (id & 3) + 4 * lane;
     const int64_t query = (int64_t)unit * 128 + row;
-    if (query >= g.queries) return;
+    if (query >= g.queries) return;  // all warps of the query
     T* out = static_cast<T*>(a.out) + offset_of(g, query, a.out_stride) + ch;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const float own_lse = g.own_lse ? g.own_lse[query] : -INFINITY;
+    float own_lse = -INFINITY;
     uint2 old = make_uint2(0, 0);
-    if (g.own_lse) old = *reinterpret_cast<const uint2*>(out);
-    float acc[4] = {}, sum = 0.f, top = -INFINITY;
-#pragma unroll 4
-    for (int n = first; n <= last; ++n) {
-        const Sums& p = g.parts[2 * n + (n == first)];
-        const float ref = p.ref[row], l = p.sum[row];
-        const float4 o = *reinterpret_cast<const float4*>(&p.o[row][ch]);
-        // without a branch, so that the loads of several pieces are in flight; a sum of 0: no row counted
-        const float up = l == 0.f ? top : fmaxf(top, ref), base = up == -INFINITY ? 0.f : up;
-        const float keep = tc::exp2_approx(top - base), w = l == 0.f ? 0.f : tc::exp2_approx(ref - base);
-        top = up;
-        sum = sum * keep + w * l;
-        acc[0] = acc[0] * keep + (l == 0.f ? 0.f : w * o.x);
-        acc[1] = acc[1] * keep + (l == 0.f ? 0.f : w * o.y);
-        acc[2] = acc[2] * keep + (l == 0.f ? 0.f : w * o.z);
-        acc[3] = acc[3] * keep + (l == 0.f ? 0.f : w * o.w);
+    if (g.own_lse && part == 0) {
+        own_lse = g.own_lse[query];
+        old = *reinterpret_cast<const uint2*>(out);
     }
-    const Mix m = mix(top, sum, own_lse);
+    Joined j = {-INFINITY, 0.f, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll 4
+    for (int n = first + part; n <= last; n += WARPS) {
+        const Sums& p = g.parts[2 * n + (n == first)];
+        j.add(p.ref[row], p.sum[row], *reinterpret_cast<const float4*>(&p.o[row][ch]));
+    }
+    if constexpr (WARPS > 1) {
+        if (part) others[warp][lane] = j;
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / WARPS), "r"(32 * WARPS) : "memory");
+        if (part) return;
+#pragma unroll
+        for (int w = 1; w < WARPS; ++w) j.add(others[warp + w][lane].top, others[warp + w][lane].sum, others[warp + w][lane].acc);
+    }
+    const Mix m = mix(j.top, j.sum, own_lse);
     const uint32_t halves[2] = {old.x, old.y};
+    const float acc[4] = {j.acc.x, j.acc.y, j.acc.z, j.acc.w};
     uint32_t e[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const float2 h = unpack2<T>(halves[i]);
-        float f0 = sum == 0.f ? 0.f : acc[2 * i] * m.prefix, f1 = sum == 0.f ? 0.f : acc[2 * i + 1] * m.prefix;
+        float f0 = j.sum == 0.f ? 0.f : acc[2 * i] * m.prefix, f1 = j.sum == 0.f ? 0.f : acc[2 * i + 1] * m.prefix;
         if (m.own != 0.f) f0 += h.x * m.own, f1 += h.y * m.own;
         e[i] = pack2<T>(f0, f1);
     }
@@ -629,12 +673,12 @@ template <typename T> __global__ void __launch_bounds__(256) hs_attend_shared_jo
 // NaN in a rotary channel.
 template <typename T, bool E4M3>
 __global__ void __launch_bounds__(256) hs_prefix_kernel(const uint8_t* rows, int64_t row_stride, int64_t n, int64_t padded, uint4* wide,
-                                                        float* scales, __half* log_scales)
+                                                        float* scales, float* log_scales)
 {
     const int lane = threadIdx.x & 31;
     const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (i >= n) {
-        if (E4M3 && lane == 0 && i < padded) scales[i] = 1.f, log_scales[i] = __float2half(0.f);
+        if (E4M3 && lane == 0 && i < padded) scales[i] = 1.f, log_scales[i] = 0.f;
         return;
     }
     const uint8_t* row = rows + i * row_stride;
@@ -673,7 +717,7 @@ __global__ void __launch_bounds__(256) hs_prefix_kernel(const uint8_t* rows, int
     }
     if (E4M3 && lane == 0) {
         scales[i] = bad ? 1.f : scale;
-        log_scales[i] = __float2half(bad ? 0.f : fmaxf(log2f(fabsf(scale)), kLeastLogScale));
+        log_scales[i] = bad ? 0.f : fmaxf(log2f(fabsf(scale)), kLeastLogScale);
     }
 }
 
@@ -716,7 +760,7 @@ struct Layout {
         rows = after(parts, sizeof(Sums) * 2 * kMaxPairs);
         scales = after(rows, 2 * HS_ROW_DIM * (size_t)prefix_rows);
         logs = after(scales, sizeof(float) * padded_rows(prefix_rows));
-        end = after(logs, sizeof(__half) * padded_rows(prefix_rows));
+        end = after(logs, sizeof(float) * padded_rows(prefix_rows));
     }
 };
 
@@ -729,7 +773,12 @@ template <typename T, bool E4M3> cudaError_t launch(const SharedArgs& g, const C
     else
         hs_attend_shared_kernel<T, E4M3><<<2 * g.workers, kThreads, kSmem, s>>>(g, map), e = cudaGetLastError();
     if (e != cudaSuccess || !g.flat || g.workers <= 1) return e;
-    return launch_after(hs_attend_shared_join_kernel<T>, dim3(128 * 4 / 8, g.units < g.workers ? g.units : g.workers - 1), 256, 0, s, g);
+    // Eight warps share the pieces where a unit has many: 1 unit of 76 pieces 58 us against 89 (8 requests x 16 heads,
+    // 65,536 rows); of 10 to 20 pieces 40 and 70 against 43 and 74 with a warp (16 requests x 3 x 32 heads, 4096 rows;
+    // 64 x 32 heads, 16,384 rows), where two warps share them.
+    const int blocks = g.units < g.workers ? g.units : g.workers - 1;
+    if (g.workers >= 16 * g.units) return launch_after(hs_attend_shared_join_kernel<T, 8>, dim3(512, blocks), 256, 0, s, g);
+    return launch_after(hs_attend_shared_join_kernel<T, 1>, dim3(64, blocks), 256, 0, s, g);
 }
 
 // The prefix's rows in the workspace, in 16 bits.
@@ -740,7 +789,7 @@ cudaError_t widen_prefix(SharedArgs& g, const hs_prefix_t& p, uint8_t* ws, const
     const uint8_t* from = static_cast<const uint8_t*>(p.rows);
     uint4* wide = reinterpret_cast<uint4*>(ws + at.rows);
     float* scales = reinterpret_cast<float*>(ws + at.scales);
-    __half* logs = reinterpret_cast<__half*>(ws + at.logs);
+    float* logs = reinterpret_cast<float*>(ws + at.logs);
     if (g.a.row_format == HS_ROWS_E4M3)
         hs_prefix_kernel<__half, true><<<grid, 256, 0, s>>>(from, p.row_stride, p.n_rows, padded, wide, scales, logs);
     else if (g.a.dtype == HS_TYPE_BF16)

@@ -97,3 +97,11 @@ template <typename T> __device__ __forceinline__ float2 unpack2(uint32_t v)
     else
         return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
+
+// Two products in one instruction.
+__device__ __forceinline__ void mul2(float& a0, float& a1, float b0, float b1)
+{
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a0), "+f"(a1)
+        : "f"(b0), "f"(b1));
+}

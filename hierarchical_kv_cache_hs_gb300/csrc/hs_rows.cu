@@ -47,12 +47,6 @@ __device__ __forceinline__ int64_t row_of(const Span& s, const int32_t* lengths,
 constexpr int kWarps = 8;        // of a block
 constexpr int kWriteBlocks = 3;  // an SM: what their registers allow
 
-__device__ __forceinline__ void mul2(float& a0, float& a1, float b0, float b1)
-{
-    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "+f"(a0), "+f"(a1)
-        : "f"(b0), "f"(b1));
-}
 __device__ __forceinline__ void square2(float& s0, float& s1, float a0, float a1)  // added to the sums
 {
     asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%0, %1};\n\tfma.rn.f32x2 y, x, x, y;\n\tmov.b64 {%0, %1}, y;\n\t}"
