@@ -15,6 +15,7 @@ namespace {
 
 constexpr int kThreads = 128, kWarps = kThreads / 32;
 constexpr int kWarpsEnough = 64;  // an SM
+constexpr int kFew = 3;           // heads of a token
 
 struct RotateArgs {
     hs_rotate_t a;
@@ -82,7 +83,7 @@ template <typename T, int NV> struct Lane {
             apart[v] = halves ? pairs : H;
         }
     }
-    __device__ void load_factors(const T* weight, const float2* turns)
+    template <typename Turn> __device__ void load_factors(const T* weight, Turn turn)  // turn(v, i): cos and sin of a pair
     {
         normed = weight != nullptr;
 #pragma unroll
@@ -98,7 +99,7 @@ template <typename T, int NV> struct Lane {
             for (int i = 0; i < H; ++i) {
                 c[v][0][i] = w[i], c[v][1][i] = w[H + i], c[v][2][i] = c[v][3][i] = 0.f;
                 if (pair[v] >= 0) {
-                    const float2 r = turns[pair[v] + i];
+                    const float2 r = turn(v, i);
                     const float wp = paired ? w[2 * i] : w[i], wq = paired ? w[2 * i + 1] : w[H + i];
                     c[v][0][i] = wp * r.x, c[v][1][i] = wq * r.y, c[v][2][i] = wp * r.y, c[v][3][i] = wq * r.x;
                 }
@@ -172,7 +173,7 @@ template <typename T, int NV, int AHEAD> __global__ void __launch_bounds__(kThre
         const int before = k ? a.heads[0] : 0;
         const int first = max(head_first - before, 0), last = min(head_last - before, a.heads[k]);
         if (first >= last) continue;
-        l.load_factors(static_cast<const T*>(a.weight[k]), turns);
+        l.load_factors(static_cast<const T*>(a.weight[k]), [&](int v, int i) { return turns[l.pair[v] + i]; });
         const int64_t x_step = a.x_stride[k][1] * teams, out_step = a.out_stride[k][1] * teams;
         const T* x = static_cast<const T*>(a.x[k]) + token * a.x_stride[k][0] + (first + mine) * a.x_stride[k][1];
         T* out = static_cast<T*>(a.out[k]) + token * a.out_stride[k][0] + (first + mine) * a.out_stride[k][1];
@@ -210,6 +211,65 @@ template <typename T, int NV, int AHEAD> __global__ void __launch_bounds__(kThre
                 }
             }
         }
+    }
+}
+
+// Few heads a token: a team takes heads of one token after another, each lane with the sines of its own pairs, and the
+// next head's channels on their way.
+template <typename T, int NV> __global__ void __launch_bounds__(kThreads, NV == 1 ? 6 : 1) hs_rotate_few_kernel(const __grid_constant__ RotateArgs g)
+{
+    constexpr int H = Half<T>::n;
+    const hs_rotate_t& a = g.a;
+    const int lane = threadIdx.x & 31, teams = 32 / g.team, heads = a.heads[0] + a.heads[1];
+    const uint32_t rows = (uint32_t)(a.tokens * heads), step = gridDim.x * kWarps * teams;  // below 2^28
+    const uint32_t first = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * teams, mine = lane / g.team;
+    Lane<T, NV> l(a, g.team, lane & (g.team - 1));
+    HsTurn freq[NV][H];
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int i = 0; i < H; ++i) freq[v][i] = l.pair[v] >= 0 ? hs_turn(a.inv_freq[l.pair[v] + i]) : HsTurn{0, true};
+    uint2 xp[NV], xq[NV];
+    int position = 0, k = 0;
+    T* out = nullptr;
+    auto bring = [&](uint32_t row) {
+        if (row >= rows) return;
+        const uint32_t token = row / heads;
+        int head = (int)(row - token * heads);
+        k = head >= a.heads[0];
+        head -= k ? a.heads[0] : 0;
+        const T* x = static_cast<const T*>(a.x[k]) + token * a.x_stride[k][0] + head * a.x_stride[k][1];
+        out = static_cast<T*>(a.out[k]) + token * a.out_stride[k][0] + head * a.out_stride[k][1];
+        if (a.rotation != HS_ROTATE_NONE) position = a.positions[token];
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            if (l.there[v]) {
+                xp[v] = __ldcs(reinterpret_cast<const uint2*>(x + l.low[v]));
+                xq[v] = __ldcs(reinterpret_cast<const uint2*>(x + l.low[v] + l.apart[v]));
+            }
+    };
+#pragma unroll
+    for (int v = 0; v < NV; ++v) xp[v] = xq[v] = make_uint2(0, 0);
+    bring(first + mine);
+    for (uint32_t row0 = first; row0 < rows; row0 += step) {  // the whole warp
+        uint2 p[NV], q[NV];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) p[v] = xp[v], q[v] = xq[v];
+        const int at = position, array = k;
+        T* to = out;
+        bring(row0 + step + mine);
+        l.load_factors(static_cast<const T*>(a.weight[array]), [&](int v, int i) { return hs_rotation(at, freq[v][i]); });
+        float f = l.squares(p, q);
+        for (int o = g.team >> 1; o; o >>= 1) f += __shfl_xor_sync(~0u, f, o);
+        f = rsqrtf(f * g.inv_dim + a.eps);
+        if (row0 + mine < rows)
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+                if (l.there[v]) {
+                    l.turn(v, p[v], q[v], f);
+                    *reinterpret_cast<uint2*>(to + l.low[v]) = p[v];
+                    *reinterpret_cast<uint2*>(to + l.low[v] + l.apart[v]) = q[v];
+                }
     }
 }
 
@@ -319,6 +379,17 @@ template <typename T> cudaError_t launch(const hs_rotate_t& a, cudaStream_t s)
     if (e != cudaSuccess) return e;
     const int heads = a.heads[0] + a.heads[1];
     g.inv_dim = 1.f / a.dim;
+    if (heads <= kFew && nv <= 3) {
+        const int64_t teams = (a.tokens * heads + 32 / g.team - 1) / (32 / g.team), most = (int64_t)sms * (nv == 1 ? 6 : 3);
+        const unsigned blocks = (unsigned)((teams + kWarps - 1) / kWarps < most ? (teams + kWarps - 1) / kWarps : most);
+        if (nv == 1)
+            hs_rotate_few_kernel<T, 1><<<blocks, kThreads, 0, s>>>(g);
+        else if (nv == 2)
+            hs_rotate_few_kernel<T, 2><<<blocks, kThreads, 0, s>>>(g);
+        else
+            hs_rotate_few_kernel<T, 3><<<blocks, kThreads, 0, s>>>(g);
+        return cudaGetLastError();
+    }
     g.heads_warp = (heads + once - 1) / once * once;
     while (g.heads_warp > once && a.tokens * ((heads + g.heads_warp - 1) / g.heads_warp) < (int64_t)sms * kWarpsEnough)
         g.heads_warp = (g.heads_warp / 2 + once - 1) / once * once;
