@@ -62,7 +62,7 @@ struct Aux {
 constexpr int kSmem = kOffAux + (int)sizeof(Aux);
 static_assert(kSmem <= 232448, "shared memory");
 
-// What a pair leaves of a unit that it does not have whole: its queries' sums, unscaled.
+// What a pair leaves of a unit: its queries' sums, unscaled.
 struct Sums {
     float o[128][512];
     float ref[128], sum[128];
@@ -78,7 +78,9 @@ struct SharedArgs : Cut {
     const float* scales;        // of 8-bit rows
     const float* log_scales;    // base 2, not below kLeastLogScale
     const float* own_lse;       // NULL: no own rows
-    Sums* parts;                // two a pair
+    Sums* parts;                // two a pair, then one a unit with all_join
+    bool all_join;              // units leave through the join, whole ones too
+    Start* starts;              // with lengths: where each pair's piece starts
     int* error;
 };
 
@@ -99,31 +101,78 @@ __device__ __forceinline__ int64_t offset_of(const SharedArgs& g, int64_t query,
     return b * stride[0] + (pos - b * g.a.positions) * stride[1] + ((unsigned)query - pos * g.a.heads) * stride[2];
 }
 
+// Tiles of a unit: up to the last row that one of its queries sees, one at least.
+__device__ __forceinline__ int tiles_to(long long rows) { return rows <= kRows ? 1 : (int)((rows + kRows - 1) / kRows); }
+__device__ __forceinline__ int tiles_of(const SharedArgs& g, int unit)
+{
+    const int64_t q0 = (int64_t)unit * 128;
+    const int last = request_of(g, min(q0 + 128, g.queries) - 1);
+    long long most = 0;
+    for (int b = request_of(g, q0); b <= last; ++b) most = max(most, (long long)seen_rows(g, b));
+    return tiles_to(most);
+}
+
+// Pair i's piece of a line whose units have tiles of their own, with lengths: the line's equal parts, as line_piece's
+// (a whole warp calls it).
+__device__ Piece ragged_piece(const SharedArgs& g, int i)
+{
+    const int lane = threadIdx.x & 31;
+    long long tiles = 0;
+    for (int u = lane; u < g.units; u += 32) tiles += tiles_of(g, u);
+    for (int o = 16; o; o >>= 1) tiles += __shfl_xor_sync(~0u, tiles, o);
+    const long long n = tiles < g.workers ? tiles : g.workers, line = tiles + (long long)g.cost * (g.units - 1);
+    if (i >= n) return {0, 0, 0};
+    const long long places[2] = {g.cost + line * i / n, g.cost + line * (i + 1) / n};  // of this piece and the next
+    long long passed = 0, before[2] = {0, tiles};  // tiles before each
+    Piece p = {0, 0, 0};
+    for (int u0 = 0; u0 < g.units && passed <= places[1]; u0 += 32) {
+        const int u = u0 + lane, t = u < g.units ? tiles_of(g, u) : 0;
+        const long long mine = t ? t + g.cost : 0;
+        long long incl = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long up = __shfl_up_sync(~0u, incl, o);
+            if (lane >= o) incl += up;
+        }
+        const long long at = passed + incl - mine;  // where this unit begins
+        for (int k = 0; k < 2; ++k) {
+            const unsigned here = __ballot_sync(~0u, places[k] >= at && places[k] < at + mine);
+            if (!here) continue;
+            const int src = __ffs(here) - 1, tile = max(0, (int)(places[k] - at) - g.cost);
+            before[k] = __shfl_sync(~0u, at - (long long)g.cost * u + tile, src);
+            if (k == 0) p.unit = u0 + src, p.tile = __shfl_sync(~0u, tile, src);
+        }
+        passed += __shfl_sync(~0u, incl, 31);
+    }
+    p.count = before[1] - before[0];
+    return p;
+}
+
 struct Stretch {  // the units, or parts of units, of a piece (a whole warp walks it)
     const SharedArgs& g;
     long long left;
     int unit, tile;
-    int at, t0, t1;  // the current unit and its tiles, without those that no query of it sees
+    int at, t0, t1;  // the current unit and its tiles
     bool whole;
     __device__ Stretch(const SharedArgs& args, const Piece& x) : g(args), left(x.count), unit(x.unit), tile(x.tile) {}
     __device__ bool next()
     {
         if (left <= 0) return false;
-        at = unit;
-        t0 = tile;
-        t1 = (long long)(g.unit_tiles - t0) <= left ? g.unit_tiles : t0 + (int)left;
-        whole = t0 == 0 && t1 == g.unit_tiles;
-        left -= t1 - t0;
-        ++unit;
-        tile = 0;
-        if (g.prefix_lengths) {
-            const int64_t q0 = (int64_t)at * 128, q1 = min(q0 + 128, g.queries) - 1;
-            const int last = request_of(g, q1);
+        int tiles = g.unit_tiles;
+        if (g.prefix_lengths) {  // tiles_of, by the warp
+            const int64_t q0 = (int64_t)unit * 128;
+            const int last = request_of(g, min(q0 + 128, g.queries) - 1);
             long long most = 0;
             for (int b = request_of(g, q0) + (threadIdx.x & 31); b <= last; b += 32) most = max(most, (long long)seen_rows(g, b));
             for (int o = 16; o; o >>= 1) most = max(most, __shfl_xor_sync(~0u, most, o));
-            t1 = min(t1, (int)((most + kRows - 1) / kRows));
+            tiles = tiles_to(most);
         }
+        at = unit;
+        t0 = tile;
+        t1 = (long long)(tiles - t0) <= left ? tiles : t0 + (int)left;
+        whole = t0 == 0 && t1 == tiles;
+        left -= t1 - t0;
+        ++unit;
+        tile = 0;
         return true;
     }
 };
@@ -222,7 +271,6 @@ template <typename T> __device__ void multiply(const SharedArgs& g, uint32_t sba
     };
     Stretch w(g, x->piece);
     while (w.next()) {
-        if (w.t0 >= w.t1) continue;
         wait(tc::smem_addr(&x->qready), pieces++ & 1, &x->dead, g.error);
         for (int t = w.t0; t < w.t1; ++t, ++j) {
             if (j >= 1) wait(tc::smem_addr(&x->sread), (j - 1) & 1, &x->dead, g.error);  // S has been read
@@ -351,160 +399,118 @@ template <typename T, bool E4M3> __device__ void soften(const SharedArgs& g, uin
     while (w.next()) {
         const int64_t query = (int64_t)w.at * 128 + rank * 64 + row;
         float ref = 0.f, sum = 0.f;
-        if (w.t0 < w.t1) {
-            bring_queries<T, E4M3>(g, sbase, tmem, x, (int64_t)w.at * 128 + rank * 64, begin, qready);
-            begin = false;
-            const float c = E4M3 && HsType<T>::is_bf16 ? power_of_two(-x->q_up[row]) * c0 : c0;
-            const int64_t limit = query < g.queries ? seen_rows(g, request_of(g, query)) : 0;
-            bool seen = false;  // a row that counts has been met: ref is a maximum
-            for (int t = w.t0; t < w.t1; ++t, ++j) {
-                const int64_t key0 = (int64_t)t * kRows + 64 * half;
-                const int live = (int)min(max(limit - key0, (int64_t)0), (int64_t)64);  // keys of these 64 that count
-                const int s = j & 1;
-                float wt[E4M3 ? 64 : 1];
-                if constexpr (E4M3) {
-                    wait(tc::smem_addr(&x->scales_full[s]), j >> 1 & 1, &x->dead, g.error);
+        bring_queries<T, E4M3>(g, sbase, tmem, x, (int64_t)w.at * 128 + rank * 64, begin, qready);
+        begin = false;
+        const float c = E4M3 && HsType<T>::is_bf16 ? power_of_two(-x->q_up[row]) * c0 : c0;
+        const int64_t limit = query < g.queries ? seen_rows(g, request_of(g, query)) : 0;
+        bool seen = false;  // a row that counts has been met: ref is a maximum
+        for (int t = w.t0; t < w.t1; ++t, ++j) {
+            const int64_t key0 = (int64_t)t * kRows + 64 * half;
+            const int live = (int)min(max(limit - key0, (int64_t)0), (int64_t)64);  // keys of these 64 that count
+            const int s = j & 1;
+            float wt[E4M3 ? 64 : 1];
+            if constexpr (E4M3) {
+                wait(tc::smem_addr(&x->scales_full[s]), j >> 1 & 1, &x->dead, g.error);
 #pragma unroll
-                    for (int i = 0; i < 64; i += 4) {
-                        const float4 f = *reinterpret_cast<const float4*>(&x->scales[s][0][64 * half + i]);
-                        wt[i] = f.x, wt[i + 1] = f.y, wt[i + 2] = f.z, wt[i + 3] = f.w;
-                    }
+                for (int i = 0; i < 64; i += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(&x->scales[s][0][64 * half + i]);
+                    wt[i] = f.x, wt[i + 1] = f.y, wt[i + 2] = f.z, wt[i + 3] = f.w;
                 }
-                wait(tc::smem_addr(&x->sfull), j & 1, &x->dead, g.error);
-                tc::fence_after();
-                uint32_t r[2][32];
-                tc::tmem_ld32(tmem + kColS, r[0]);
-                tc::tmem_ld32(tmem + kColS + 32, r[1]);
-                tc::tmem_wait_ld(r[0]);
-                tc::tmem_wait_ld(r[1]);
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive_cluster(sread);  // the next tile's scores may come
-                float v[64], top = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < 64; i += 2) {
-                    v[i] = __uint_as_float(r[i >> 5][i & 31]), v[i + 1] = __uint_as_float(r[i >> 5][(i & 31) + 1]);
-                    mul2(v[i], v[i + 1], c, c);
-                    if constexpr (E4M3) mul2(v[i], v[i + 1], wt[i], wt[i + 1]);
-                }
-                if (live < 64)
-#pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        if (i >= live) v[i] = -INFINITY;
-                if constexpr (E4M3) {
-#pragma unroll
-                    for (int i = 0; i < 64; i += 4) {
-                        const float4 f = *reinterpret_cast<const float4*>(&x->scales[s][1][64 * half + i]);
-                        float lw[4] = {f.x, f.y, f.z, f.w};
-                        tc::add2(lw[0], lw[1], v[i], v[i + 1]);
-                        tc::add2(lw[2], lw[3], v[i + 2], v[i + 3]);
-                        top = tc::max3(tc::max3(top, lw[0], lw[1]), lw[2], lw[3]);
-                    }
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(tc::smem_addr(&x->scales_free[s]));
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 64; i += 2) top = tc::max3(top, v[i], v[i + 1]);
-                }
-                x->red[s][threadIdx.x] = top;
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                top = fmaxf(top, x->red[s][threadIdx.x ^ 64]);
-                float keep = 1.f;
-                if (top > -INFINITY && (!seen || top > ref + 8.f)) {
-                    keep = tc::exp2_approx(fminf(ref - top, 126.f));
-                    sum *= keep;
-                    ref = top;
-                }
-                const bool scale_o = seen && keep != 1.f;
-                seen = seen || top > -INFINITY;
-                uint32_t e[32];
-                float sums[2] = {0.f, 0.f};
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    float p0 = v[2 * i], p1 = v[2 * i + 1];
-                    tc::add2(p0, p1, -ref, -ref);
-                    p0 = tc::exp2_approx(p0), p1 = tc::exp2_approx(p1);
-                    tc::add2(sums[0], sums[1], p0, p1);
-                    if constexpr (E4M3) mul2(p0, p1, wt[2 * i], wt[2 * i + 1]);
-                    e[i] = pack2<std::conditional_t<E4M3, __half, T>>(p0, p1);
-                }
-                sum += sums[0] + sums[1];
-                // P's buffer and O are free once the last tile's product is done
-                if (j >= 1) wait(tc::smem_addr(&x->pvdone), (j - 1) & 1, &x->dead, g.error);
-                if (__any_sync(~0u, scale_o)) {
-                    if (!scale_o) keep = 1.f;
-                    tc::fence_after();
-#pragma unroll 1
-                    for (int n = 0; n < 256; n += 32) {
-                        tc::tmem_ld32(tmem + kColO + n, r[0]);
-                        tc::tmem_wait_ld(r[0]);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) r[0][i] = __float_as_uint(__uint_as_float(r[0][i]) * keep);
-                        tc::tmem_st32(tmem + kColO + n, r[0]);
-                    }
-                    tc::tmem_wait_st();
-                }
-                const uint32_t dst = sbase + kOffP + half * kBlock + row * 128;
-#pragma unroll
-                for (int n = 0; n < 8; ++n) tc::st_shared16(dst + ((n ^ (row & 7)) << 4), e[4 * n], e[4 * n + 1], e[4 * n + 2], e[4 * n + 3]);
-                tc::fence_async_shared();
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive_cluster(pready);
             }
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            x->red[0][threadIdx.x] = sum;
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            sum += x->red[0][threadIdx.x ^ 64];
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            wait(tc::smem_addr(&x->pvdone), (j - 1) & 1, &x->dead, g.error);
+            wait(tc::smem_addr(&x->sfull), j & 1, &x->dead, g.error);
             tc::fence_after();
-        }
-        // The piece's end: O and the sums leave.
-        const bool there = query < g.queries, some = sum > 0.f || sum != sum;
-        if (w.whole) {
-            // Through shared memory, so that eight lanes write 128 bytes of a query together: 64 channels of each half
-            // at a time, [half][query][128 B], in P's buffer and the queries' by turns.
-            asm volatile("griddepcontrol.wait;" ::: "memory");  // the own rows' part
-            const Mix m = mix(ref, sum, there && g.own_lse ? g.own_lse[query] : -INFINITY);
-            const bool mine = there && m.own != 0.f;
-            T* out = static_cast<T*>(a.out);
-            const uint4* own = reinterpret_cast<const uint4*>(out + (there ? offset_of(g, query, a.out_stride) : 0) + 256 * half);
-#pragma unroll 2
-            for (int n = 0; n < 256; n += 64) {
-                const uint32_t buffer = sbase + (n & 64 ? 0 : kOffP);
-                uint4 old[8];
+            uint32_t r[2][32];
+            tc::tmem_ld32(tmem + kColS, r[0]);
+            tc::tmem_ld32(tmem + kColS + 32, r[1]);
+            tc::tmem_wait_ld(r[0]);
+            tc::tmem_wait_ld(r[1]);
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_cluster(sread);  // the next tile's scores may come
+            float v[64], top = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) old[i] = mine ? own[n / 8 + i] : make_uint4(0, 0, 0, 0);
-                uint32_t r[32];
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    __syncwarp();
-                    tc::tmem_ld32(tmem + kColO + n + 32 * q, r);
-                    tc::tmem_wait_ld(r);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float f[8], h[8];
-                        ::Piece<T>::unpack(old[4 * q + i], h);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) f[k] = (some ? __uint_as_float(r[8 * i + k]) * m.prefix : 0.f) + (mine ? h[k] * m.own : 0.f);
-                        const uint4 o = ::Piece<T>::pack(f);
-                        tc::st_shared16(buffer + threadIdx.x * 128 + (((4 * q + i) ^ (row & 7)) << 4), o.x, o.y, o.z, o.w);
-                    }
-                }
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int at = 16 * i + (threadIdx.x >> 3), ch = threadIdx.x & 7;  // of 128 rows of the buffer
-                    const int64_t to = (int64_t)w.at * 128 + rank * 64 + (at & 63);
-                    const uint4 o = tc::ld_shared16(buffer + at * 128 + ((ch ^ (at & 7)) << 4));
-                    if (to < g.queries)
-                        *reinterpret_cast<uint4*>(out + offset_of(g, to, a.out_stride) + 256 * (at >> 6) + n + 8 * ch) = o;
-                }
+            for (int i = 0; i < 64; i += 2) {
+                v[i] = __uint_as_float(r[i >> 5][i & 31]), v[i + 1] = __uint_as_float(r[i >> 5][(i & 31) + 1]);
+                mul2(v[i], v[i + 1], c, c);
+                if constexpr (E4M3) mul2(v[i], v[i + 1], wt[i], wt[i + 1]);
             }
-            if (there && a.lse && half == 0) a.lse[query] = m.lse;
-        } else {
-            Sums* part = g.parts + 2 * pair + (w.t0 == 0 ? 1 : 0);  // likewise, 32 channels at a time
+            if (live < 64)
+#pragma unroll
+                for (int i = 0; i < 64; ++i)
+                    if (i >= live) v[i] = -INFINITY;
+            if constexpr (E4M3) {
+#pragma unroll
+                for (int i = 0; i < 64; i += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(&x->scales[s][1][64 * half + i]);
+                    float lw[4] = {f.x, f.y, f.z, f.w};
+                    tc::add2(lw[0], lw[1], v[i], v[i + 1]);
+                    tc::add2(lw[2], lw[3], v[i + 2], v[i + 3]);
+                    top = tc::max3(tc::max3(top, lw[0], lw[1]), lw[2], lw[3]);
+                }
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(tc::smem_addr(&x->scales_free[s]));
+            } else {
+#pragma unroll
+                for (int i = 0; i < 64; i += 2) top = tc::max3(top, v[i], v[i + 1]);
+            }
+            x->red[s][threadIdx.x] = top;
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            top = fmaxf(top, x->red[s][threadIdx.x ^ 64]);
+            float keep = 1.f;
+            if (top > -INFINITY && (!seen || top > ref + 8.f)) {
+                keep = tc::exp2_approx(fminf(ref - top, 126.f));
+                sum *= keep;
+                ref = top;
+            }
+            const bool scale_o = seen && keep != 1.f;
+            seen = seen || top > -INFINITY;
+            uint32_t e[32];
+            float sums[2] = {0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                float p0 = v[2 * i], p1 = v[2 * i + 1];
+                tc::add2(p0, p1, -ref, -ref);
+                p0 = tc::exp2_approx(p0), p1 = tc::exp2_approx(p1);
+                tc::add2(sums[0], sums[1], p0, p1);
+                if constexpr (E4M3) mul2(p0, p1, wt[2 * i], wt[2 * i + 1]);
+                e[i] = pack2<std::conditional_t<E4M3, __half, T>>(p0, p1);
+            }
+            sum += sums[0] + sums[1];
+            // P's buffer and O are free once the last tile's product is done
+            if (j >= 1) wait(tc::smem_addr(&x->pvdone), (j - 1) & 1, &x->dead, g.error);
+            if (__any_sync(~0u, scale_o)) {
+                if (!scale_o) keep = 1.f;
+                tc::fence_after();
+#pragma unroll 1
+                for (int n = 0; n < 256; n += 32) {
+                    tc::tmem_ld32(tmem + kColO + n, r[0]);
+                    tc::tmem_wait_ld(r[0]);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) r[0][i] = __float_as_uint(__uint_as_float(r[0][i]) * keep);
+                    tc::tmem_st32(tmem + kColO + n, r[0]);
+                }
+                tc::tmem_wait_st();
+            }
+            const uint32_t dst = sbase + kOffP + half * kBlock + row * 128;
+#pragma unroll
+            for (int n = 0; n < 8; ++n) tc::st_shared16(dst + ((n ^ (row & 7)) << 4), e[4 * n], e[4 * n + 1], e[4 * n + 2], e[4 * n + 3]);
+            tc::fence_async_shared();
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_cluster(pready);
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        x->red[0][threadIdx.x] = sum;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        sum += x->red[0][threadIdx.x ^ 64];
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        wait(tc::smem_addr(&x->pvdone), (j - 1) & 1, &x->dead, g.error);
+        tc::fence_after();
+        // The piece's end: O and the sums leave, through shared memory, so that eight lanes write 128 bytes of a query
+        // together: 32 channels of each half at a time, [half][query][128 B], in P's buffer and the queries' by turns.
+        const int64_t query0 = (int64_t)w.at * 128 + rank * 64;
+        const int row0 = threadIdx.x >> 3, ch = threadIdx.x & 7;  // this thread takes each sixteenth of the buffer's rows
+        auto leave = [&](auto&& put) {
 #pragma unroll 2
             for (int n = 0; n < 256; n += 32) {
                 const uint32_t buffer = sbase + (n & 32 ? 0 : kOffP);
@@ -518,17 +524,50 @@ template <typename T, bool E4M3> __device__ void soften(const SharedArgs& g, uin
                 asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int at = 16 * i + (threadIdx.x >> 3), ch = threadIdx.x & 7;
-                    *reinterpret_cast<uint4*>(&part->o[rank * 64 + (at & 63)][256 * (at >> 6) + n + 4 * ch]) =
-                        tc::ld_shared16(buffer + at * 128 + ((ch ^ (at & 7)) << 4));
+                    const int at = 16 * i + row0;
+                    put(i, 256 * (i >> 2) + n + 4 * ch, tc::ld_shared16(buffer + at * 128 + ((ch ^ (at & 7)) << 4)));
                 }
             }
+        };
+        if (g.all_join || !w.whole) {
+            Sums* part = g.parts + (w.whole ? 2 * kMaxPairs + w.at : 2 * pair + (w.t0 == 0));
+            leave([&](int i, int c, const uint4& v) { *reinterpret_cast<uint4*>(&part->o[rank * 64 + 16 * (i & 3) + row0][c]) = v; });
             if (half == 0) part->ref[rank * 64 + row] = ref, part->sum[rank * 64 + row] = sum;
+        } else {  // joined with the own rows' part: the call's outputs
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            const bool there = query < g.queries;
+            const Mix m = mix(ref, sum, there && g.own_lse ? g.own_lse[query] : -INFINITY);
+            if (half == 0) x->red[0][row] = m.prefix, x->red[1][row] = m.own;
+            if (there && a.lse && half == 0) a.lse[query] = m.lse;
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            T* out[4];  // this thread's rows, and their factors
+            float2 f[4];
+            bool some[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int at = 16 * i + row0;
+                some[i] = query0 + at < g.queries;
+                out[i] = static_cast<T*>(a.out) + (some[i] ? offset_of(g, query0 + at, a.out_stride) : 0);
+                f[i] = make_float2(x->red[0][at], x->red[1][at]);
+            }
+            uint2 old[8];
+            auto bring = [&](int n) {  // a step ahead
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    old[i] = some[i & 3] && f[i & 3].y != 0.f && n < 256 ? *reinterpret_cast<const uint2*>(out[i & 3] + 256 * (i >> 2) + n + 4 * ch) : make_uint2(0, 0);
+            };
+            bring(0);
+            leave([&](int i, int c, const uint4& v) {
+                const float2 e = f[i & 3], h0 = unpack2<T>(old[i].x), h1 = unpack2<T>(old[i].y);
+                auto joined = [&](uint32_t o, float own) { return (e.x != 0.f ? __uint_as_float(o) * e.x : 0.f) + (e.y != 0.f ? own * e.y : 0.f); };
+                if (some[i & 3])
+                    *reinterpret_cast<uint2*>(out[i & 3] + c) = make_uint2(pack2<T>(joined(v.x, h0.x), joined(v.y, h0.y)), pack2<T>(joined(v.z, h1.x), joined(v.w, h1.y)));
+                if (i == 7) bring(c - 256 - 4 * ch + 32);
+            });
         }
         tc::fence_before();
         asm volatile("bar.sync 1, 128;" ::: "memory");  // the buffers have been read
     }
-    if (begin) asm volatile("bar.arrive 2, 192;" ::: "memory");
 }
 
 template <typename T, bool E4M3>
@@ -545,9 +584,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may queue up behind this grid
     if (warp == 0) tc::tmem_alloc<2>(tc::smem_addr(&x->tmem), 512);
+    if (warp == 5 && g.prefix_lengths) {
+        const Piece p = ragged_piece(g, pair);
+        if (lane == 0) x->piece = p;
+        if (lane == 0 && rank == 0) g.starts[pair] = {p.count > 0 ? p.unit : -1, p.tile};
+    }
     if (warp == 6 && lane == 0) {
-        const Piece p = g.flat ? line_piece(g, pair) : whole_piece(g, pair);
-        x->piece = p;
+        if (!g.prefix_lengths) x->piece = g.flat ? line_piece(g, pair) : whole_piece(g, pair);
         x->dead = 0;
         for (int i = 0; i < kKStages; ++i) tc::mbar_init(tc::smem_addr(&x->kfull[i]), 1), tc::mbar_init(tc::smem_addr(&x->kfree[i]), 1);
         for (int i = 0; i < kVStages; ++i) tc::mbar_init(tc::smem_addr(&x->vfull[i]), 1), tc::mbar_init(tc::smem_addr(&x->vfree[i]), 1);
@@ -598,9 +641,10 @@ __device__ __forceinline__ int piece_at(const Cut& g, long long at)
     return (int)(at < longer ? at / (g.share + 1) : g.extra + (at - longer) / g.share);
 }
 
-// Join the pieces of the units that several pairs worked on, with the own rows' part: blocks y take unit y or, where
-// there are more units than pairs, the unit that pair y + 1 begins inside (if it is the first to do so).  Each query's
-// 128 channels are one or several warps', which share its pieces; one pass, and the order of the sums is fixed.
+// Join the pieces of units with one another and with the own rows' part: blocks y take unit y (all_join) or, where
+// whole units have left by themselves, the unit that pair y + 1 begins inside, if it is the first to do so (with lengths,
+// the y-th such unit).  Each query's 128 channels are one or several warps', which share its pieces; one pass, and the
+// order of the sums is fixed.
 struct Joined {
     float top, sum;
     float4 acc;
@@ -621,13 +665,30 @@ template <typename T, int WARPS> __global__ void __launch_bounds__(256) hs_atten
 {
     __shared__ Joined others[WARPS > 1 ? 8 : 1][32];
     const hs_attend_t& a = g.a;
-    const int per = g.unit_tiles + g.cost;
-    const bool few = g.units < g.workers;
-    const long long here = few ? 0 : piece_begin(g, blockIdx.y + 1);
-    const int unit = few ? blockIdx.y : (int)(here / per);
-    const long long begin = (long long)unit * per + g.cost;  // the unit's first tile
-    const int first = piece_at(g, begin), last = piece_at(g, begin + g.unit_tiles - 1);
-    if (few ? first == last : here <= begin || first != (int)blockIdx.y) return;
+    int unit = blockIdx.y, first = 0, last = 0;
+    if (g.prefix_lengths && g.all_join) {
+        // The pairs that have the unit: the last whose piece starts at its start or before, to the last that starts
+        // inside it or before.
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        for (int i0 = 0; i0 < g.workers; i0 += 32) {
+            const int i = i0 + (threadIdx.x & 31);
+            const Start s = i < g.workers ? g.starts[i] : Start{-1, 0};
+            const unsigned before = __ballot_sync(~0u, s.unit >= 0 && (s.unit < unit || (s.unit == unit && s.tile == 0)));
+            const unsigned inside = __ballot_sync(~0u, s.unit >= 0 && s.unit <= unit);
+            if (before) first = i0 + 31 - __clz(before);
+            if (inside) last = i0 + 31 - __clz(inside);
+        }
+    } else if (g.prefix_lengths) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (!find_cut(g.starts, g.workers, blockIdx.y, unit, first, last)) return;
+    } else if (g.flat) {
+        const int per = g.unit_tiles + g.cost;
+        const long long here = piece_begin(g, blockIdx.y + 1);
+        if (!g.all_join) unit = (int)(here / per);
+        const long long begin = (long long)unit * per + g.cost;  // the unit's first tile
+        first = piece_at(g, begin), last = piece_at(g, begin + g.unit_tiles - 1);
+        if (!g.all_join && (here <= begin || first != (int)blockIdx.y)) return;
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % WARPS;
     const int id = blockIdx.x * (8 / WARPS) + warp / WARPS, row = id >> 2, ch = 128 * (id & 3) + 4 * lane;
     const int64_t query = (int64_t)unit * 128 + row;
@@ -643,7 +704,7 @@ template <typename T, int WARPS> __global__ void __launch_bounds__(256) hs_atten
     Joined j = {-INFINITY, 0.f, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll 4
     for (int n = first + part; n <= last; n += WARPS) {
-        const Sums& p = g.parts[2 * n + (n == first)];
+        const Sums& p = g.parts[first == last ? 2 * kMaxPairs + unit : 2 * n + (n == first)];
         j.add(p.ref[row], p.sum[row], *reinterpret_cast<const float4*>(&p.o[row][ch]));
     }
     if constexpr (WARPS > 1) {
@@ -748,16 +809,22 @@ cudaError_t map_rows(CUtensorMap* map, const void* rows, int64_t n, int64_t stri
 
 int64_t padded_rows(int64_t n) { return (n + kRows - 1) / kRows * kRows; }
 
-// Workspace: hs_latent_attend's for the own rows (its error word is the call's), then their lse, two partial results a
-// pair, the prefix's rows in 16 bits, scales and their logarithms.
+// Up to this many units leave through the join: it has many blocks for the work that then is left when the own rows'
+// part is done, where a pair of SMs takes 6 us for a unit.  More have not the place (0.26 MB a unit), and not the need.
+constexpr int64_t kJoinUnits = 2 * kMaxPairs;
+
+// Workspace: hs_latent_attend's for the own rows (its error word is the call's), then their lse, the partial results,
+// where the pairs' pieces start, the prefix's rows in 16 bits, scales and their logarithms.
 struct Layout {
-    size_t lse, parts, rows, scales, logs, end;
+    size_t lse, parts, starts, rows, scales, logs, end;
     Layout(int batch, int positions, int heads, int64_t own_rows, int64_t prefix_rows)
     {
         auto after = [](size_t at, size_t bytes) { return (at + bytes + 255) / 256 * 256; };
         lse = after(0, hs_attend_workspace_bytes(batch, positions, heads, own_rows));
         parts = after(lse, sizeof(float) * batch * positions * (size_t)heads);
-        rows = after(parts, sizeof(Sums) * 2 * kMaxPairs);
+        const int64_t units = ((int64_t)batch * positions * heads + 127) / 128;
+        starts = after(parts, sizeof(Sums) * (2 * kMaxPairs + (units <= kJoinUnits ? units : 0)));
+        rows = after(starts, sizeof(Start) * kMaxPairs);
         scales = after(rows, 2 * HS_ROW_DIM * (size_t)prefix_rows);
         logs = after(scales, sizeof(float) * padded_rows(prefix_rows));
         end = after(logs, sizeof(float) * padded_rows(prefix_rows));
@@ -772,11 +839,11 @@ template <typename T, bool E4M3> cudaError_t launch(const SharedArgs& g, const C
         e = launch_after(hs_attend_shared_kernel<T, E4M3>, dim3(2 * g.workers), kThreads, kSmem, s, g, map);
     else
         hs_attend_shared_kernel<T, E4M3><<<2 * g.workers, kThreads, kSmem, s>>>(g, map), e = cudaGetLastError();
-    if (e != cudaSuccess || !g.flat || g.workers <= 1) return e;
+    if (e != cudaSuccess || (!g.all_join && (!g.flat || g.workers <= 1))) return e;
     // Eight warps share the pieces where a unit has many: 1 unit of 76 pieces 58 us against 89 (8 requests x 16 heads,
     // 65,536 rows); of 10 to 20 pieces 40 and 70 against 43 and 74 with a warp (16 requests x 3 x 32 heads, 4096 rows;
     // 64 x 32 heads, 16,384 rows), where two warps share them.
-    const int blocks = g.units < g.workers ? g.units : g.workers - 1;
+    const int blocks = g.all_join ? g.units : g.workers - 1;
     if (g.workers >= 16 * g.units) return launch_after(hs_attend_shared_join_kernel<T, 8>, dim3(512, blocks), 256, 0, s, g);
     return launch_after(hs_attend_shared_join_kernel<T, 1>, dim3(64, blocks), 256, 0, s, g);
 }
@@ -825,6 +892,8 @@ cudaError_t hs_launch_attend_shared(const hs_attend_t& a, const hs_prefix_t& p, 
     g.prefix_rows = p.n_rows;
     g.queries = (int64_t)a.batch * a.positions * a.heads;
     g.parts = reinterpret_cast<Sums*>(ws + at.parts);
+    g.starts = reinterpret_cast<Start*>(ws + at.starts);
+    g.all_join = g.queries <= 128 * kJoinUnits;
     g.error = reinterpret_cast<int*>(ws);
     CUtensorMap map;
     const bool e4m3 = a.row_format == HS_ROWS_E4M3;
@@ -854,6 +923,11 @@ cudaError_t hs_launch_attend_shared(const hs_attend_t& a, const hs_prefix_t& p, 
         for (int n = pairs - 1; n > 0 && n > g.units; --n)
             if (time(n) < time(best)) best = n;
         g.cut(best, p.n_rows, 5, kUnitCost, kRows);
+    }
+    if (p.lengths && !g.flat) {  // the device cuts the line
+        const int64_t tiles = (int64_t)g.units * g.unit_tiles;
+        g.workers = (int)(tiles < pairs ? tiles : pairs);
+        g.flat = 1;
     }
     if (a.dtype == HS_TYPE_BF16) return e4m3 ? launch<__nv_bfloat16, true>(g, map, s) : launch<__nv_bfloat16, false>(g, map, s);
     return e4m3 ? launch<__half, true>(g, map, s) : launch<__half, false>(g, map, s);

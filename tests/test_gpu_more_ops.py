@@ -472,7 +472,7 @@ def _form(rows, e4m3):
 SHARED = [  # batch, positions, heads, prefix, own rows
     (1, 1, 1, 1, 1), (2, 1, 16, 64, 5), (3, 1, 20, 129, 40), (1, 1, 128, 128, 10), (5, 3, 20, 1000, 70), (2, 1, 200, 333, 30),
     (64, 1, 16, 700, 100), (9, 1, 128, 2000, 64), (300, 1, 3, 65, 9), (1, 2, 7, 9000, 20), (40, 1, 128, 300, 33), (1, 1, 16, 1, 300),
-    (200, 1, 128, 100, 3), (80, 1, 64, 5000, 2)]
+    (200, 1, 128, 100, 3), (80, 1, 64, 5000, 2), (160, 1, 128, 2000, 5), (100, 1, 128, 600, 9)]
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
@@ -494,7 +494,8 @@ def test_shared_lengths(hs, size, dtype, e4m3):
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
-@pytest.mark.parametrize("size", [(3, 1, 16, 200, 90), (7, 2, 20, 600, 60), (70, 1, 16, 3000, 50), (20, 1, 128, 700, 40), (150, 1, 1, 400, 9)])
+@pytest.mark.parametrize("size", [(3, 1, 16, 200, 90), (7, 2, 20, 600, 60), (70, 1, 16, 3000, 50), (20, 1, 128, 700, 40), (150, 1, 1, 400, 9),
+                                  (90, 1, 128, 400, 10), (170, 1, 128, 300, 20)])
 def test_shared_slots_and_lengths_of_the_prefix(hs, size, e4m3):
     """Own rows by lists with absent entries; prefixes of all lengths, 0 and values outside among them; what no one
     sees of either holds NaN."""
