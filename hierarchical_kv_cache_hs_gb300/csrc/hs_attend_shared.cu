@@ -12,10 +12,13 @@
 // channels (its half of the second product's B operand, in four groups of two blocks); both
 // kinds go through rings, so that copies run about a tile ahead.
 //
-// Bound by shared memory: a tile's products read 192 KB of operands a CTA and its copies
-// write 139 KB, at 128 bytes a clock 2,700 clocks, where the tensor core alone needs 2,200.
-// Tiles of 128 rows, since a product of 128 x 64 x 16 takes 26 clocks where one of
-// 128 x 128 x 16 takes 33 (its A operand is read once for twice the columns).
+// Bound by the tensor cores: a tile takes 2,370 clocks where its products alone need 2,210 (8-bit rows 2,600, their
+// softmax multiplies scales): 64 requests x 128 heads x 32,768 rows take 314 us in a burst, 1.86 PFLOP/s, and 340 to
+// 375 under the power cap, with the own rows' part and the join.  Tiles of 128 rows, since a product of 128 x 64 x 16
+// takes 26 clocks where one of 128 x 128 x 16 takes 33 (its A operand is read once for twice the columns); one buffer
+// of S is enough, since O(t) stands between S(t+1) and S(t+2).
+//
+// Few tiles are bound by what surrounds them: the queries' way in (3 us), a pair's sums' way out (3 us), the join.
 //
 // Warps of a CTA: 0-3 queries, softmax and outputs, 4 brings keys, 5 values, 6 issues the
 // products (in the pair's first CTA), in the order S(t+1), O(t), so that a tile's softmax
@@ -38,6 +41,8 @@ namespace {
 
 constexpr int kThreads = 7 * 32;
 constexpr int kRows = 128;  // rows a tile
+// Tiles' time that a unit's queries and output take: 2 instead of 4 costs 3 us (16 requests x 3 x 32 heads, 4096 rows:
+// 42 against 39.5; 64 x 32 heads, 16,384 rows: 70 against 68), 7 changes nothing.
 constexpr int kUnitCost = 4;
 
 constexpr int kQTmem = 6;
@@ -638,32 +643,38 @@ __device__ __forceinline__ int piece_at(const Cut& g, long long at)
 {
     at -= g.cost;
     const long long longer = (g.share + 1) * g.extra;
-    return (int)(at < longer ? at / (g.share + 1) : g.extra + (at - longer) / g.share);
+    const bool in = at < longer;
+    const long long from = in ? at : at - longer, by = g.share + in;
+    return (in ? 0 : g.extra) + (from < 0x7fffffff && by < 0x7fffffff ? (int)((unsigned)from / (unsigned)by) : (int)(from / by));
 }
 
 // Join the pieces of units with one another and with the own rows' part: blocks y take unit y (all_join) or, where
 // whole units have left by themselves, the unit that pair y + 1 begins inside, if it is the first to do so (with lengths,
 // the y-th such unit).  Each query's 128 channels are one or several warps', which share its pieces; one pass, and the
 // order of the sums is fixed.
-struct Joined {
+template <int N> struct Joined {  // of 4 N channels
     float top, sum;
-    float4 acc;
-    __device__ void add(float ref, float l, const float4& o)
+    float4 acc[N];
+    __device__ void add(float ref, float l, const float4 (&o)[N])
     {
         // without a branch, so that the loads of several pieces are in flight; a sum of 0: no row counted
         const float up = l == 0.f ? top : fmaxf(top, ref), base = up == -INFINITY ? 0.f : up;
         const float keep = tc::exp2_approx(top - base), w = l == 0.f ? 0.f : tc::exp2_approx(ref - base);
         top = up;
         sum = sum * keep + w * l;
-        acc.x = acc.x * keep + (l == 0.f ? 0.f : w * o.x);
-        acc.y = acc.y * keep + (l == 0.f ? 0.f : w * o.y);
-        acc.z = acc.z * keep + (l == 0.f ? 0.f : w * o.z);
-        acc.w = acc.w * keep + (l == 0.f ? 0.f : w * o.w);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            acc[k].x = acc[k].x * keep + (l == 0.f ? 0.f : w * o[k].x);
+            acc[k].y = acc[k].y * keep + (l == 0.f ? 0.f : w * o[k].y);
+            acc[k].z = acc[k].z * keep + (l == 0.f ? 0.f : w * o[k].z);
+            acc[k].w = acc[k].w * keep + (l == 0.f ? 0.f : w * o[k].w);
+        }
     }
 };
-template <typename T, int WARPS> __global__ void __launch_bounds__(256) hs_attend_shared_join_kernel(const __grid_constant__ SharedArgs g)
+// N: of 128 channels, a warp's.
+template <typename T, int WARPS, int N> __global__ void __launch_bounds__(256) hs_attend_shared_join_kernel(const __grid_constant__ SharedArgs g)
 {
-    __shared__ Joined others[WARPS > 1 ? 8 : 1][32];
+    __shared__ Joined<N> others[WARPS > 1 ? 8 : 1][32];
     const hs_attend_t& a = g.a;
     int unit = blockIdx.y, first = 0, last = 0;
     if (g.prefix_lengths && g.all_join) {
@@ -684,28 +695,37 @@ template <typename T, int WARPS> __global__ void __launch_bounds__(256) hs_atten
     } else if (g.flat) {
         const int per = g.unit_tiles + g.cost;
         const long long here = piece_begin(g, blockIdx.y + 1);
-        if (!g.all_join) unit = (int)(here / per);
+        if (!g.all_join) unit = here < 0x7fffffff ? (int)((unsigned)here / (unsigned)per) : (int)(here / per);
         const long long begin = (long long)unit * per + g.cost;  // the unit's first tile
         first = piece_at(g, begin), last = piece_at(g, begin + g.unit_tiles - 1);
         if (!g.all_join && (here <= begin || first != (int)blockIdx.y)) return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % WARPS;
-    const int id = blockIdx.x * (8 / WARPS) + warp / WARPS, row = id >> 2, ch = 128 * (id & 3) + 4 * lane;
+    const int id = blockIdx.x * (8 / WARPS) + warp / WARPS, row = id / (4 / N), ch = 128 * N * (id % (4 / N)) + 4 * lane;
     const int64_t query = (int64_t)unit * 128 + row;
     if (query >= g.queries) return;  // all warps of the query
     T* out = static_cast<T*>(a.out) + offset_of(g, query, a.out_stride) + ch;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     float own_lse = -INFINITY;
-    uint2 old = make_uint2(0, 0);
+    uint2 old[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) old[k] = make_uint2(0, 0);
     if (g.own_lse && part == 0) {
         own_lse = g.own_lse[query];
-        old = *reinterpret_cast<const uint2*>(out);
+#pragma unroll
+        for (int k = 0; k < N; ++k) old[k] = *reinterpret_cast<const uint2*>(out + 128 * k);
     }
-    Joined j = {-INFINITY, 0.f, {0.f, 0.f, 0.f, 0.f}};
+    Joined<N> j;
+    j.top = -INFINITY, j.sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) j.acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int n = first + part; n <= last; n += WARPS) {
         const Sums& p = g.parts[first == last ? 2 * kMaxPairs + unit : 2 * n + (n == first)];
-        j.add(p.ref[row], p.sum[row], *reinterpret_cast<const float4*>(&p.o[row][ch]));
+        float4 o[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) o[k] = *reinterpret_cast<const float4*>(&p.o[row][ch + 128 * k]);
+        j.add(p.ref[row], p.sum[row], o);
     }
     if constexpr (WARPS > 1) {
         if (part) others[warp][lane] = j;
@@ -715,17 +735,13 @@ template <typename T, int WARPS> __global__ void __launch_bounds__(256) hs_atten
         for (int w = 1; w < WARPS; ++w) j.add(others[warp + w][lane].top, others[warp + w][lane].sum, others[warp + w][lane].acc);
     }
     const Mix m = mix(j.top, j.sum, own_lse);
-    const uint32_t halves[2] = {old.x, old.y};
-    const float acc[4] = {j.acc.x, j.acc.y, j.acc.z, j.acc.w};
-    uint32_t e[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float2 h = unpack2<T>(halves[i]);
-        float f0 = j.sum == 0.f ? 0.f : acc[2 * i] * m.prefix, f1 = j.sum == 0.f ? 0.f : acc[2 * i + 1] * m.prefix;
-        if (m.own != 0.f) f0 += h.x * m.own, f1 += h.y * m.own;
-        e[i] = pack2<T>(f0, f1);
+    for (int k = 0; k < N; ++k) {
+        const float2 h0 = unpack2<T>(old[k].x), h1 = unpack2<T>(old[k].y);
+        auto joined = [&](float sum, float own) { return (j.sum == 0.f ? 0.f : sum * m.prefix) + (m.own != 0.f ? own * m.own : 0.f); };
+        *reinterpret_cast<uint2*>(out + 128 * k) = make_uint2(pack2<T>(joined(j.acc[k].x, h0.x), joined(j.acc[k].y, h0.y)),
+                                                             pack2<T>(joined(j.acc[k].z, h1.x), joined(j.acc[k].w, h1.y)));
     }
-    *reinterpret_cast<uint2*>(out) = make_uint2(e[0], e[1]);
     if (a.lse && ch == 0) a.lse[query] = m.lse;
 }
 
@@ -842,10 +858,12 @@ template <typename T, bool E4M3> cudaError_t launch(const SharedArgs& g, const C
     if (e != cudaSuccess || (!g.all_join && (!g.flat || g.workers <= 1))) return e;
     // Eight warps share the pieces where a unit has many: 1 unit of 76 pieces 58 us against 89 (8 requests x 16 heads,
     // 65,536 rows); of 10 to 20 pieces 40 and 70 against 43 and 74 with a warp (16 requests x 3 x 32 heads, 4096 rows;
-    // 64 x 32 heads, 16,384 rows), where two warps share them.
+    // 64 x 32 heads, 16,384 rows), where two warps share them.  A warp takes 256 channels where there are enough warps:
+    // 80 units 65 us against 71, 100 units 61 against 66; but 8 units 51.5 against 50.
     const int blocks = g.all_join ? g.units : g.workers - 1;
-    if (g.workers >= 16 * g.units) return launch_after(hs_attend_shared_join_kernel<T, 8>, dim3(512, blocks), 256, 0, s, g);
-    return launch_after(hs_attend_shared_join_kernel<T, 1>, dim3(64, blocks), 256, 0, s, g);
+    if (g.workers >= 16 * g.units) return launch_after(hs_attend_shared_join_kernel<T, 8, 1>, dim3(512, blocks), 256, 0, s, g);
+    if (g.units < 16) return launch_after(hs_attend_shared_join_kernel<T, 1, 1>, dim3(64, blocks), 256, 0, s, g);
+    return launch_after(hs_attend_shared_join_kernel<T, 1, 2>, dim3(32, blocks), 256, 0, s, g);
 }
 
 // The prefix's rows in the workspace, in 16 bits.
