@@ -676,10 +676,23 @@ def _want(x, name, shape, dtype, device):
     raise ValueError("the last axis of %s must be contiguous" % name)
 
 
-def _on_current_device(device):
+def _current_device():
+    global _current_device
     import torch
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
+    _current_device = torch.cuda.current_device
+    return _current_device()
+
+
+def _on_current_device(device):
+    if device.type != "cuda" or device.index != _current_device():
         raise ValueError("tensors must be on the current CUDA device, are on %s" % device)
+
+
+def _vector(x, name, n, dtype, device):
+    """The address of a contiguous vector of n elements."""
+    if x.shape != (n,) or x.dtype is not dtype or x.device != device or not x.is_contiguous():
+        _want(x, name, (n,), dtype, device)
+    return x.data_ptr()
 
 
 def _rows_of(rows, row_format, dtype, device, lead):
@@ -814,9 +827,9 @@ def hs_latent_attend_shared(q, prefix, rows, out, scale: float, slots=None, leng
     address, n, stride, _ = _rows_of(prefix, row_format, q.dtype, q.device, ())
     lengths_at = 0
     if prefix_lengths is not None:
-        import torch
-        _want(prefix_lengths, "prefix_lengths", (q.shape[0],), torch.int32, q.device)
-        lengths_at = prefix_lengths.data_ptr()
+        if _INT32 is None:
+            _torch_types()
+        lengths_at = _vector(prefix_lengths, "prefix_lengths", q.shape[0], _INT32, q.device)
     _check(lib.hs_latent_attend_shared(block, _PREFIX.pack(address, n, stride, lengths_at), _stream(stream)),
            "hs_latent_attend_shared")
 
@@ -904,27 +917,34 @@ def hs_rms_norm(x, weight, out, eps: float, residual=None, residual_out=None, ca
         "hs_rms_norm")
 
 
+_FP32 = _INT32 = None  # torch's types, once it is imported
+
+
+def _torch_types():
+    global _FP32, _INT32
+    import torch
+    _FP32, _INT32 = torch.float32, torch.int32
+
+
 def _turn_of(positions, inv_freq, rotation, tokens, pairs, device):
     """(rotation, address of the positions, of the frequencies): none without positions."""
-    import torch
-    if positions is None and inv_freq is None:
-        return HS_ROTATE_NONE, 0, 0
     if positions is None or inv_freq is None:
+        if positions is inv_freq:
+            return HS_ROTATE_NONE, 0, 0
         raise ValueError("give both positions and inv_freq, or neither")
-    if rotation not in (HS_ROTATE_PAIRS, HS_ROTATE_HALVES):
+    if rotation != HS_ROTATE_PAIRS and rotation != HS_ROTATE_HALVES:
         raise ValueError("unknown rotation %r" % (rotation,))
-    _want(positions, "positions", (tokens,), torch.int32, device)
-    _want(inv_freq, "inv_freq", (pairs,), torch.float32, device)
-    return rotation, positions.data_ptr(), inv_freq.data_ptr()
+    if _INT32 is None:
+        _torch_types()
+    return (rotation, _vector(positions, "positions", tokens, _INT32, device),
+            _vector(inv_freq, "inv_freq", pairs, _FP32, device))
 
 
 def _places_of(start, lengths, device, B):
-    import torch
-    _want(start, "start", (B + 1,), torch.int32, device)
-    if lengths is None:
-        return start.data_ptr(), 0
-    _want(lengths, "lengths", (B,), torch.int32, device)
-    return start.data_ptr(), lengths.data_ptr()
+    if _INT32 is None:
+        _torch_types()
+    return (_vector(start, "start", B + 1, _INT32, device),
+            0 if lengths is None else _vector(lengths, "lengths", B, _INT32, device))
 
 
 def _pool_of(h, row_format):
@@ -951,10 +971,7 @@ def hs_latent_write(x, rows, weight=None, eps: float = 0.0, positions=None, inv_
         raise ValueError("x must have 2 axes, has %d" % len(shape))
     n = shape[0]
     x0, _ = _want(x, "x", (n, HS_ROW_DIM), dtype, device)
-    w_at = 0
-    if weight is not None:
-        _want(weight, "weight", (HS_LATENT_DIM,), dtype, device)
-        w_at = weight.data_ptr()
+    w_at = 0 if weight is None else _vector(weight, "weight", HS_LATENT_DIM, dtype, device)
     turn, positions_at, freq_at = _turn_of(positions, inv_freq, rotation, n, HS_ROPE_DIM // 2, device)
     batch = start_at = lengths_at = 0
     if start is None:
@@ -1050,20 +1067,20 @@ def hs_norm_rotate(q, q_out, k=None, k_out=None, q_weight=None, k_weight=None, e
     if len(shape) != 3:
         raise ValueError("q must have 3 axes, has %d" % len(shape))
     n, heads, dim = shape
-    rope = 0
-    if inv_freq is not None:
-        rope = 2 * inv_freq.numel()
+    rope = 0 if inv_freq is None else 2 * inv_freq.numel()
     if rope_at is None:
         rope_at = dim - rope
     if not 0 <= rope_at <= dim - rope:
         raise ValueError("%d rotary channels at %d do not fit into %d" % (rope, rope_at, dim))
     turn, positions_at, freq_at = _turn_of(positions, inv_freq, rotation, n, rope // 2, device)
-    x0, x1, _ = _want(q, "q", (n, heads, dim), dtype, device)
-    o0, o1, _ = _want(q_out, "q_out", (n, heads, dim), dtype, device)
-    k_heads = k_at = k0 = k1 = ko_at = ko0 = ko1 = w_at = kw_at = 0
-    if (k is None) != (k_out is None) or (k is None and k_weight is not None):
-        raise ValueError("give both k and k_out, or neither (nor k_weight)")
+    x0, x1, x2 = q.stride()
+    o0, o1, o2 = _want(q_out, "q_out", shape, dtype, device)
+    if x2 != 1:
+        _want(q, "q", shape, dtype, device)
+    k_heads = k_at = k0 = k1 = ko_at = ko0 = ko1 = kw_at = 0
     if k is not None:
+        if k_out is None:
+            raise ValueError("give both k and k_out, or neither (nor k_weight)")
         if k.dim() != 3:
             raise ValueError("k must have 3 axes, has %d" % k.dim())
         k_heads = k.shape[1]
@@ -1071,16 +1088,18 @@ def hs_norm_rotate(q, q_out, k=None, k_out=None, q_weight=None, k_weight=None, e
         ko0, ko1, _ = _want(k_out, "k_out", (n, k_heads, dim), dtype, device)
         k_at, ko_at = k.data_ptr(), k_out.data_ptr()
         if k_weight is not None:
-            _want(k_weight, "k_weight", (dim,), dtype, device)
-            kw_at = k_weight.data_ptr()
-    if q_weight is not None:
-        _want(q_weight, "q_weight", (dim,), dtype, device)
-        w_at = q_weight.data_ptr()
-    _on_current_device(device)
-    _check(lib.hs_norm_rotate(
+            kw_at = _vector(k_weight, "k_weight", dim, dtype, device)
+    elif k_out is not None or k_weight is not None:
+        raise ValueError("give both k and k_out, or neither (nor k_weight)")
+    w_at = 0 if q_weight is None else _vector(q_weight, "q_weight", dim, dtype, device)
+    if device.type != "cuda" or device.index != _current_device():
+        _on_current_device(device)
+    rc = lib.hs_norm_rotate(
         _ROTATE.pack(kind, turn, dim, rope_at, rope, heads, k_heads, n, q.data_ptr(), k_at, x0, x1, k0, k1, w_at,
                      kw_at, eps, positions_at, freq_at, q_out.data_ptr(), ko_at, o0, o1, ko0, ko1),
-        _stream(stream)), "hs_norm_rotate")
+        _stream(stream))
+    if rc:
+        _check(rc, "hs_norm_rotate")
 
 
 class Handle:
