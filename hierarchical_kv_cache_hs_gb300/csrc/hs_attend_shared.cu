@@ -698,7 +698,10 @@ template <typename T, int WARPS, int N> __global__ void __launch_bounds__(256) h
         if (!g.all_join) unit = here < 0x7fffffff ? (int)((unsigned)here / (unsigned)per) : (int)(here / per);
         const long long begin = (long long)unit * per + g.cost;  // the unit's first tile
         first = piece_at(g, begin), last = piece_at(g, begin + g.unit_tiles - 1);
-        if (!g.all_join && (here <= begin || first != (int)blockIdx.y)) return;
+        if (!g.all_join && (here <= begin || first != (int)blockIdx.y)) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");  // what follows this grid follows the pairs' too
+            return;
+        }
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % WARPS;
     const int id = blockIdx.x * (8 / WARPS) + warp / WARPS, row = id / (4 / N), ch = 128 * N * (id % (4 / N)) + 4 * lane;
