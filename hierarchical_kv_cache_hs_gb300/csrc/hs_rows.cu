@@ -2,7 +2,16 @@
 // rotation of the rotary ones, the row's form) at its place; hs_latent_read: rows back
 // as values.
 //
-// Both read each input once and write each output once, and are bound by memory.
+//   y = [c w / sqrt(mean c^2 + eps) ; R r],  R: pairs turned by position x frequency
+//   16-bit rows: y rounded; 8-bit rows: s = max |y| / 448, e4m3(y / s)
+//   back: the row's values, times s, rounded once to the output's type
+//
+// Each input is read once and each output written once (1156 + 592 bytes a token written as an 8-bit row), so the
+// floor is memory's.  Inputs larger than L2, on one GB300:
+//   writing 65,536 rows of 8 bits   24.3 us, 4.7 TB/s, 0.69 of a copy's rate: some 250 instructions a row, which
+//                                   take 63 % of the issue slots, and what a warp does between its loads
+//   reading 64 x 2048 8-bit rows by slots   37.0 us, 6.2 TB/s, 0.91 of a copy's rate: memory
+//   64 rows written, 3 x 77 read    2.2 and 2.7 us: a launch and the latency of two loads in a row
 #include "hs_pieces.h"
 #include "hs_rotation.h"
 
@@ -42,10 +51,12 @@ __device__ __forceinline__ int64_t row_of(const Span& s, const int32_t* lengths,
 //
 // A warp takes some tokens, one after the other, with the next one's channels on their way.  A lane has two
 // 16-byte pieces of the latent channels (32 lanes x 2 x 8 = 512) and two of the 64 rotary channels, so every lane
-// has the same work; the weights and its pair's frequency stay in registers.
+// has the same work; the weights and its pair's frequency stay in registers.  A block's tokens are neighbours, and its
+// warps take them by turns, so that the rows that are written at one time lie side by side.  (A warp for each token
+// alone, with its own loads of the weights: 34 us for the 24.3 above.)
 
 constexpr int kWarps = 8;        // of a block
-constexpr int kWriteBlocks = 3;  // an SM: what their registers allow
+constexpr int kWriteBlocks = 3;  // an SM, 72 registers a thread (65,536 rows, 2 / 3 / 4 blocks: 30.3 / 27.0 / 27.6 us when it was chosen)
 
 __device__ __forceinline__ void square2(float& s0, float& s1, float a0, float a1)  // added to the sums
 {
@@ -73,7 +84,8 @@ __global__ void __launch_bounds__(kWarps * 32, kWriteBlocks) hs_write_kernel(con
 {
     const int lane = threadIdx.x & 31;
     constexpr int step = kWarps;
-    const int first = (int)(a.tokens * blockIdx.x / gridDim.x) + (threadIdx.x >> 5), last = (int)(a.tokens * (blockIdx.x + 1) / gridDim.x);  // below 2^24
+    const int first = (int)(a.tokens * blockIdx.x / gridDim.x) + (threadIdx.x >> 5);  // below 2^24
+    const int last = (int)(a.tokens * (blockIdx.x + 1) / gridDim.x);
     if (first >= last) return;
     uint4 weight[2];
     if (a.weight)
@@ -188,7 +200,9 @@ __global__ void __launch_bounds__(kWarps * 32, kWriteBlocks) hs_write_kernel(con
 
 // ---- read ------------------------------------------------------------------------------
 //
-// 36 threads a row, 16 channels each, and kReadAhead rows of a thread on their way together.
+// 36 threads a row, 16 channels each, and kReadAhead rows of a thread on their way together: a load of 16 bytes (32 of
+// 16-bit rows) and stores of 32.  One row a thread and loads and stores of 16 bytes took 63 us where this takes 37; 2, 3
+// and 4 rows a thread 36.6, 36.9 and 37.5.  (Few rows are no faster with fewer a thread: a launch bounds them.)
 
 constexpr int kRowThreads = HS_ROW_DIM / 16, kReadLine = 8, kReadAhead = 3;  // threads of a row, rows side by side, rows of a thread
 constexpr int kReadRows = kReadLine * kReadAhead;                            // of a block
@@ -244,10 +258,12 @@ __global__ void __launch_bounds__(kRowThreads * kReadLine) hs_read_kernel(const 
             s.request = (int)(token / a.entries);
             row = a.slots[s.request * a.slots_stride + token % a.entries];
         }
-        if (threadIdx.x < kReadRows) mine[threadIdx.x] = there && s.request >= 0;
-        if (threadIdx.x < kReadRows) places[threadIdx.x] = s.request >= 0 && row >= 0 && row < a.n_rows
-                                  ? static_cast<const uint8_t*>(a.rows) + s.request * a.request_stride + row * a.row_stride
-                                  : nullptr;
+        if (threadIdx.x < kReadRows) {
+            mine[threadIdx.x] = there && s.request >= 0;
+            places[threadIdx.x] = s.request >= 0 && row >= 0 && row < a.n_rows
+                                      ? static_cast<const uint8_t*>(a.rows) + s.request * a.request_stride + row * a.row_stride
+                                      : nullptr;
+        }
     }
     __syncthreads();
     const int line = threadIdx.x / kRowThreads, ch = 16 * (threadIdx.x - line * kRowThreads);

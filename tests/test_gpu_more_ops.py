@@ -185,6 +185,25 @@ def test_rotate_far_positions(hs, pairs):
     assert (np.abs(sin - np.sin(angle).astype(float)) <= tol).all()
 
 
+@pytest.mark.parametrize("freq", [1.0, 0.3, -1e-4])
+def test_rotate_sine_and_cosine(hs, freq):
+    """Angles in every part of a turn."""
+    n = 65536
+    x = torch.tensor([1.0, 0.0], device="cuda").repeat(n, 1, 1)
+    out = torch.empty_like(x)
+    f = torch.tensor([freq], device="cuda")
+    positions = torch.arange(n, device="cuda", dtype=torch.int32)
+    hs.hs_norm_rotate(x, out, positions=positions, inv_freq=f)
+    angle = positions.cpu().numpy().astype(np.longdouble) * np.longdouble(f.item())
+    # the angle: 2^-31 of a turn, and its distance from a quarter turn (pi / 4 at most) in 24 bits, 2^-25; the series
+    # cut short 2^-24; its evaluation's roundings, steps of values up to 1: 3 half steps of 2^-24 with its last products
+    tol = 2 * math.pi * 2.0 ** -31 + 2.0 ** -25 + 2.0 ** -24 + 3 * 2.0 ** -24
+    got = out[:, 0].double().cpu().numpy()
+    assert np.abs(got[:, 0] - np.cos(angle).astype(float)).max() <= tol
+    assert np.abs(got[:, 1] - np.sin(angle).astype(float)).max() <= tol
+    assert got[0, 0] == 1 and got[0, 1] == 0
+
+
 def test_rotate_frequency_not_finite(hs):
     x = torch.ones((1, 1, 4), device="cuda")
     out = torch.empty_like(x)
