@@ -536,7 +536,10 @@ template <typename T, bool E4M3> __device__ void soften(const SharedArgs& g, uin
         };
         if (g.all_join || !w.whole) {
             Sums* part = g.parts + (w.whole ? 2 * kMaxPairs + w.at : 2 * pair + (w.t0 == 0));
-            leave([&](int i, int c, const uint4& v) { *reinterpret_cast<uint4*>(&part->o[rank * 64 + 16 * (i & 3) + row0][c]) = v; });
+            leave([&](int i, int c, const uint4& v) {
+                const int at = 16 * (i & 3) + row0;
+                if (query0 + at < g.queries) *reinterpret_cast<uint4*>(&part->o[rank * 64 + at][c]) = v;
+            });
             if (half == 0) part->ref[rank * 64 + row] = ref, part->sum[rank * 64 + row] = sum;
         } else {  // joined with the own rows' part: the call's outputs
             asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -748,56 +751,65 @@ template <typename T, int WARPS, int N> __global__ void __launch_bounds__(256) h
     if (a.lse && ch == 0) a.lse[query] = m.lse;
 }
 
-// The prefix's rows as 16-bit operands: a warp a row.  8-bit values become fp16 beside their scales (and base-2
-// logarithms; those of the last tile's absent rows too).  A row with a value that is not finite becomes zeros with
-// NaN in a rotary channel.
+// The prefix's rows as 16-bit operands.  8-bit values become fp16 beside their scales (and base-2 logarithms; those of
+// the last tile's absent rows too).  A row with a value that is not finite becomes zeros with NaN in a rotary channel.
+// Laid out as hs_latent_read's kernel: 36 threads a row, three rows of a thread on their way together (65,536 8-bit rows
+// 18.5 us, the 113 MB at 6.1 TB/s; a warp a row took 1 us more).
+constexpr int kWidenLine = 8, kWidenAhead = 3, kWidenRows = kWidenLine * kWidenAhead;
+
 template <typename T, bool E4M3>
-__global__ void __launch_bounds__(256) hs_prefix_kernel(const uint8_t* rows, int64_t row_stride, int64_t n, int64_t padded, uint4* wide,
-                                                        float* scales, float* log_scales)
+__global__ void __launch_bounds__(kRowThreads * kWidenLine)
+    hs_prefix_kernel(const uint8_t* rows, int64_t row_stride, int64_t n, int64_t padded, uint8_t* wide, float* scales, float* log_scales,
+                     const bool rows32, const bool wide32)
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (i >= n) {
-        if (E4M3 && lane == 0 && i < padded) scales[i] = 1.f, log_scales[i] = 0.f;
-        return;
-    }
-    const uint8_t* row = rows + i * row_stride;
-    constexpr int kPieces = HS_ROW_DIM / 8;
-    uint4 v[3];
-    bool bad = false;
-    float scale = 1.f;
+    __shared__ int bad[kWidenRows];
+    const int line = threadIdx.x / kRowThreads, ch = 16 * (threadIdx.x - line * kRowThreads);
+    const int64_t first = (int64_t)blockIdx.x * kWidenRows + line;
+    if (threadIdx.x < kWidenRows) bad[threadIdx.x] = 0;
+    uint4 v[kWidenAhead][2];
+    float scale[kWidenAhead];
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        const int p = 32 * k + lane;
-        v[k] = make_uint4(0, 0, 0, 0);
-        if (p >= kPieces) continue;
+    for (int m = 0; m < kWidenAhead; ++m) {
+        const int64_t i = first + m * kWidenLine;
+        const uint8_t* row = rows + i * row_stride;
+        v[m][0] = v[m][1] = make_uint4(0, 0, 0, 0);
+        scale[m] = 1.f;
+        if (i >= n) continue;
+        if constexpr (E4M3)
+            v[m][1] = *reinterpret_cast<const uint4*>(row + ch), scale[m] = *reinterpret_cast<const float*>(row + HS_ROW8_SCALE);
+        else
+            load32(row + 2 * ch, rows32, v[m]);
+    }
+    __syncthreads();  // the marks are clear
+#pragma unroll
+    for (int m = 0; m < kWidenAhead; ++m) {
         if constexpr (E4M3) {
-            const uint2 e = reinterpret_cast<const uint2*>(row)[p];
-            widen(e.x, v[k].x, v[k].y);
-            widen(e.y, v[k].z, v[k].w);
-        } else {
-            v[k] = reinterpret_cast<const uint4*>(row)[p];
+            const uint4 e = v[m][1];
+            widen(e.x, v[m][0].x, v[m][0].y), widen(e.y, v[m][0].z, v[m][0].w);
+            widen(e.z, v[m][1].x, v[m][1].y), widen(e.w, v[m][1].z, v[m][1].w);
         }
         constexpr uint32_t kAll = HsType<T>::is_bf16 ? 0x7f80u : 0x7c00u;  // the exponent of what is not finite
-        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+        bool some = E4M3 && !(fabsf(scale[m]) < INFINITY);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) bad = bad || (w[q] & kAll) == kAll || (w[q] >> 16 & kAll) == kAll;
-    }
-    if constexpr (E4M3) {
-        scale = *reinterpret_cast<const float*>(row + HS_ROW8_SCALE);
-        bad = bad || !(fabsf(scale) < INFINITY);
-    }
-    bad = __any_sync(~0u, bad);
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t w[4] = {v[m][k].x, v[m][k].y, v[m][k].z, v[m][k].w};
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        const int p = 32 * k + lane;
-        if (p >= kPieces) continue;
-        if (bad) v[k] = make_uint4(p == kPieces - 1 ? 0x7fffu : 0u, 0, 0, 0);
-        wide[i * kPieces + p] = v[k];
+            for (int q = 0; q < 4; ++q) some = some || (w[q] & kAll) == kAll || (w[q] >> 16 & kAll) == kAll;
+        }
+        if (some) bad[m * kWidenLine + line] = 1;
     }
-    if (E4M3 && lane == 0) {
-        scales[i] = bad ? 1.f : scale;
-        log_scales[i] = bad ? 0.f : fmaxf(log2f(fabsf(scale)), kLeastLogScale);
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < kWidenAhead; ++m) {
+        const int64_t i = first + m * kWidenLine;
+        const bool none = bad[m * kWidenLine + line] != 0;
+        if (none) v[m][0] = make_uint4(0, 0, 0, 0), v[m][1] = make_uint4(0, ch == HS_ROW_DIM - 16 ? 0x7fffu : 0u, 0, 0);
+        if (i < n) store32(wide + i * (2 * HS_ROW_DIM) + 2 * ch, wide32, v[m][0], v[m][1]);
+        if (E4M3 && ch == 0 && i < padded) {
+            const bool plain = i >= n || none;
+            scales[i] = plain ? 1.f : scale[m];
+            log_scales[i] = plain ? 0.f : fmaxf(log2f(fabsf(scale[m])), kLeastLogScale);
+        }
     }
 }
 
@@ -873,17 +885,21 @@ template <typename T, bool E4M3> cudaError_t launch(const SharedArgs& g, const C
 cudaError_t widen_prefix(SharedArgs& g, const hs_prefix_t& p, uint8_t* ws, const Layout& at, cudaStream_t s)
 {
     const int64_t padded = padded_rows(p.n_rows);
-    const unsigned grid = (unsigned)(padded / 8);
     const uint8_t* from = static_cast<const uint8_t*>(p.rows);
-    uint4* wide = reinterpret_cast<uint4*>(ws + at.rows);
+    uint8_t* wide = ws + at.rows;
     float* scales = reinterpret_cast<float*>(ws + at.scales);
     float* logs = reinterpret_cast<float*>(ws + at.logs);
+    const bool rows32 = ((uintptr_t)from | (p.n_rows > 1 ? (uintptr_t)p.row_stride : 0)) % 32 == 0, wide32 = (uintptr_t)wide % 32 == 0;
+    auto run = [&](auto kernel) {
+        const unsigned grid = (unsigned)((padded + kWidenRows - 1) / kWidenRows);
+        kernel<<<grid, kRowThreads * kWidenLine, 0, s>>>(from, p.row_stride, p.n_rows, padded, wide, scales, logs, rows32, wide32);
+    };
     if (g.a.row_format == HS_ROWS_E4M3)
-        hs_prefix_kernel<__half, true><<<grid, 256, 0, s>>>(from, p.row_stride, p.n_rows, padded, wide, scales, logs);
+        run(hs_prefix_kernel<__half, true>);
     else if (g.a.dtype == HS_TYPE_BF16)
-        hs_prefix_kernel<__nv_bfloat16, false><<<grid, 256, 0, s>>>(from, p.row_stride, p.n_rows, padded, wide, scales, logs);
+        run(hs_prefix_kernel<__nv_bfloat16, false>);
     else
-        hs_prefix_kernel<__half, false><<<grid, 256, 0, s>>>(from, p.row_stride, p.n_rows, padded, wide, scales, logs);
+        run(hs_prefix_kernel<__half, false>);
     g.scales = scales;
     g.log_scales = logs;
     return cudaGetLastError();

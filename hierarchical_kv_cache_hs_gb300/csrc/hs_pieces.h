@@ -105,3 +105,30 @@ __device__ __forceinline__ void mul2(float& a0, float& a1, float b0, float b1)
         : "+f"(a0), "+f"(a1)
         : "f"(b0), "f"(b1));
 }
+
+// 32 bytes at once where they are aligned so.
+__device__ __forceinline__ void load32(const void* p, bool whole, uint4 (&v)[2])
+{
+    if (whole) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x), "=r"(v[1].y), "=r"(v[1].z), "=r"(v[1].w)
+                     : "l"(p));
+    } else {
+        v[0] = static_cast<const uint4*>(p)[0];
+        v[1] = static_cast<const uint4*>(p)[1];
+    }
+}
+__device__ __forceinline__ void store32(void* p, bool whole, const uint4& a, const uint4& b)
+{
+    if (whole) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y),
+                     "r"(b.z), "r"(b.w)
+                     : "memory");
+    } else {
+        static_cast<uint4*>(p)[0] = a;
+        static_cast<uint4*>(p)[1] = b;
+    }
+}
+
+// Threads of a cache row, 16 channels each: wide pieces of the row in either form, and of its values.
+constexpr int kRowThreads = HS_ROW_DIM / 16;

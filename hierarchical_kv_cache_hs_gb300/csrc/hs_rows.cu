@@ -204,33 +204,9 @@ __global__ void __launch_bounds__(kWarps * 32, kWriteBlocks) hs_write_kernel(con
 // 16-bit rows) and stores of 32.  One row a thread and loads and stores of 16 bytes took 63 us where this takes 37; 2, 3
 // and 4 rows a thread 36.6, 36.9 and 37.5.  (Few rows are no faster with fewer a thread: a launch bounds them.)
 
-constexpr int kRowThreads = HS_ROW_DIM / 16, kReadLine = 8, kReadAhead = 3;  // threads of a row, rows side by side, rows of a thread
-constexpr int kReadRows = kReadLine * kReadAhead;                            // of a block
+constexpr int kReadLine = 8, kReadAhead = 3;       // rows side by side, rows of a thread
+constexpr int kReadRows = kReadLine * kReadAhead;  // of a block
 static_assert(kReadRows <= 32, "a warp finds the rows");
-
-// 32 bytes at once where they are aligned so.
-__device__ __forceinline__ void load32(const void* p, bool whole, uint4 (&v)[2])
-{
-    if (whole) {
-        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x), "=r"(v[1].y), "=r"(v[1].z), "=r"(v[1].w)
-                     : "l"(p));
-    } else {
-        v[0] = static_cast<const uint4*>(p)[0];
-        v[1] = static_cast<const uint4*>(p)[1];
-    }
-}
-__device__ __forceinline__ void store32(void* p, bool whole, const uint4& a, const uint4& b)
-{
-    if (whole) {
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y),
-                     "r"(b.z), "r"(b.w)
-                     : "memory");
-    } else {
-        static_cast<uint4*>(p)[0] = a;
-        static_cast<uint4*>(p)[1] = b;
-    }
-}
 
 // R: the type of 16-bit rows, or void for 8-bit ones.
 template <typename R, typename O>
