@@ -575,7 +575,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) hs_atte
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     int* error = reinterpret_cast<int*>(ws);
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may queue up behind this grid
+    if (gate(g, pair)) return;
     if (warp == 0) tc::tmem_alloc<2>(tc::smem_addr(&x->tmem), 512);
     if (warp == 12) {
         const Piece p = find_piece(g, pair);
@@ -708,8 +708,10 @@ template <typename T, bool E4M3> cudaError_t launch(const Args& g, cudaStream_t 
 {
     cudaError_t e = cudaFuncSetAttribute(hs_attend_kernel<T, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    hs_attend_kernel<T, E4M3><<<2 * g.workers, kThreads, kSmem, s>>>(g);
-    e = cudaGetLastError();
+    if (g.after)
+        e = launch_after(hs_attend_kernel<T, E4M3>, dim3(2 * (g.workers + 1)), kThreads, kSmem, s, g);
+    else
+        hs_attend_kernel<T, E4M3><<<2 * g.workers, kThreads, kSmem, s>>>(g), e = cudaGetLastError();
     if (e != cudaSuccess || !g.flat || g.workers <= 1) return e;
     // At most `cut` units are cut.  A block's time is latency, so many units, of few pieces each, take few
     // blocks: requests of 2048 listed rows x 128 heads 75 against 86 us with 90 of them, 38 against 43 with
@@ -732,10 +734,11 @@ size_t pair_workspace(int64_t units, int64_t tiles)
     return kOffPartial + sizeof(Partial) * 2 * (size_t)(units * tiles < kMaxPairs ? units * tiles : kMaxPairs);
 }
 
-cudaError_t launch_pair(const hs_attend_t& a, int sms, cudaStream_t s)
+cudaError_t launch_pair(const hs_attend_t& a, int sms, cudaStream_t s, bool after)
 {
     Args g;
     g.a = a;
+    g.after = after;
     g.head_blocks = (a.heads + 127) / 128;
     g.units = a.batch * a.positions * g.head_blocks;
     // Pieces also write and join up to two partial results a pair: about 10 us, 10 tiles' time.
@@ -758,12 +761,12 @@ size_t hs_attend_workspace_bytes(int batch, int positions, int heads, int64_t ro
     return narrow > pair ? narrow : pair;
 }
 
-cudaError_t hs_launch_attend(const hs_attend_t& a, cudaStream_t s)
+cudaError_t hs_launch_attend(const hs_attend_t& a, cudaStream_t s, bool after)
 {
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    return a.row_format == HS_ROWS_E4M3 && a.heads <= hs_attn::kNarrowHeads ? hs_attn::launch_narrow(a, sms, s)
-                                                                            : hs_attn::launch_pair(a, sms, s);
+    return a.row_format == HS_ROWS_E4M3 && a.heads <= hs_attn::kNarrowHeads ? hs_attn::launch_narrow(a, sms, s, after)
+                                                                            : hs_attn::launch_pair(a, sms, s, after);
 }

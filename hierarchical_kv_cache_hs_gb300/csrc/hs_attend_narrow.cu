@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) hs_attend_narrow_kernel(const __g
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     int* error = reinterpret_cast<int*>(ws);
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may queue up behind this grid
+    if (gate(g, blockIdx.x)) return;
     if (warp == 0) tc::tmem_alloc<1>(tc::smem_addr(&x->tmem), Layout<NH>::cols);
     if (warp == 12) {
         const Piece p = find_piece(g, blockIdx.x);
@@ -530,8 +530,10 @@ template <typename T, int NH> cudaError_t launch(const Args& g, cudaStream_t s)
 {
     cudaError_t e = cudaFuncSetAttribute(hs_attend_narrow_kernel<T, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<NH>());
     if (e != cudaSuccess) return e;
-    hs_attend_narrow_kernel<T, NH><<<g.workers, kThreads, smem_bytes<NH>(), s>>>(g);
-    e = cudaGetLastError();
+    if (g.after)
+        e = launch_after(hs_attend_narrow_kernel<T, NH>, dim3(g.workers + 1), kThreads, smem_bytes<NH>(), s, g);
+    else
+        hs_attend_narrow_kernel<T, NH><<<g.workers, kThreads, smem_bytes<NH>(), s>>>(g), e = cudaGetLastError();
     if (e != cudaSuccess || !g.flat || g.workers <= 1) return e;
     const int cut = g.units < g.workers - 1 ? g.units : g.workers - 1;  // at most this many units are cut
     return launch_after(hs_attend_narrow_join_kernel<T, NH>, dim3(cut, (g.a.heads + kJoinHeads - 1) / kJoinHeads), 512, 0, s, g, g.workers);
@@ -545,10 +547,11 @@ size_t narrow_workspace(int64_t units, int64_t tiles, int heads)
     return kOffPartial + part * 2 * (size_t)(units * tiles < kMaxCtas ? units * tiles : kMaxCtas);
 }
 
-cudaError_t launch_narrow(const hs_attend_t& a, int sms, cudaStream_t s)
+cudaError_t launch_narrow(const hs_attend_t& a, int sms, cudaStream_t s, bool after)
 {
     Args g;
     g.a = a;
+    g.after = after;
     g.head_blocks = 1;
     g.units = a.batch * a.positions;
     // Pieces also write and join up to two partial results an SM: about 8 us, 6 tiles' time.

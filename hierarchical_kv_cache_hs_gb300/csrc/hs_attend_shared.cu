@@ -762,6 +762,7 @@ __global__ void __launch_bounds__(kRowThreads * kWidenLine)
     hs_prefix_kernel(const uint8_t* rows, int64_t row_stride, int64_t n, int64_t padded, uint8_t* wide, float* scales, float* log_scales,
                      const bool rows32, const bool wide32)
 {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the own rows' part needs nothing from here
     __shared__ int bad[kWidenRows];
     const int line = threadIdx.x / kRowThreads, ch = 16 * (threadIdx.x - line * kRowThreads);
     const int64_t first = (int64_t)blockIdx.x * kWidenRows + line;
@@ -933,8 +934,8 @@ cudaError_t hs_launch_attend_shared(const hs_attend_t& a, const hs_prefix_t& p, 
     g.all_join = g.queries <= 128 * kJoinUnits;
     g.error = reinterpret_cast<int*>(ws);
     CUtensorMap map;
-    const bool e4m3 = a.row_format == HS_ROWS_E4M3;
-    if (e4m3 || p.lengths) {
+    const bool e4m3 = a.row_format == HS_ROWS_E4M3, widened = e4m3 || p.lengths;
+    if (widened) {
         e = widen_prefix(g, p, ws, at, s);
         if (e == cudaSuccess) e = map_rows(&map, ws + at.rows, p.n_rows, 2 * HS_ROW_DIM);
     } else {
@@ -946,7 +947,7 @@ cudaError_t hs_launch_attend_shared(const hs_attend_t& a, const hs_prefix_t& p, 
         hs_attend_t own = a;
         own.lse = reinterpret_cast<float*>(ws + at.lse);
         g.own_lse = own.lse;
-        e = hs_launch_attend(own, s);
+        e = hs_launch_attend(own, s, widened);
         if (e != cudaSuccess) return e;
     }
     g.units = (int)((g.queries + 127) / 128);

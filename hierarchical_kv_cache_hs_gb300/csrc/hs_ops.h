@@ -17,7 +17,9 @@
 inline int hs_norm_group(int dim, int carry, int group) { return group >= dim + carry ? 0 : group; }
 
 // hs_ops.cpp has checked the arguments; these launch.
-cudaError_t hs_launch_attend(const hs_attend_t& a, cudaStream_t s);
+// after: the call's kernels may begin while the one before them in the stream runs, which has to come from the same call
+// and let them; what is launched behind them with launch_after begins when that one is done.
+cudaError_t hs_launch_attend(const hs_attend_t& a, cudaStream_t s, bool after = false);
 cudaError_t hs_launch_prefill(const hs_prefill_t& a, cudaStream_t s);
 cudaError_t hs_launch_norm(const hs_norm_t& a, cudaStream_t s);
 cudaError_t hs_launch_write(const hs_write_t& a, cudaStream_t s);
