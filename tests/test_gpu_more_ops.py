@@ -150,6 +150,33 @@ def test_rotate_strides_and_in_place(hs, dim, rope, at, pairs):
     assert torch.equal(hold[..., :8], before[..., :8]) and torch.equal(hold[..., 8 + dim:], before[..., 8 + dim:])
 
 
+@pytest.mark.parametrize("heads,keys", [(8, 2), (1, 1), (2, 1), (40, 4)])
+def test_rotate_packed_in_place(hs, heads, keys):
+    """Queries, keys and values side by side in one array, as a projection leaves them; rotated where they lie."""
+    g = _gen(heads)
+    n, dim = 70, 128
+    hold = _randn(g, n, heads + 2 * keys, dim)
+    before = hold.clone()
+    positions = torch.randint(0, 9999, (n,), generator=g, device="cuda", dtype=torch.int32)
+    freq, wq, wk = _freq(dim), _randn(g, dim), _randn(g, dim)
+    q, k = hold[:, :heads], hold[:, heads:heads + keys]
+    hs.hs_norm_rotate(q, q, k=k, k_out=k, q_weight=wq, k_weight=wk, eps=EPS, positions=positions, inv_freq=freq)
+    for got, x, w in ((q, before[:, :heads], wq), (k, before[:, heads:heads + keys], wk)):
+        _close(got, *_rotate_ref(x, w, positions, freq, 0, True), BF)
+    assert torch.equal(hold[:, heads + keys:], before[:, heads + keys:])
+
+
+@pytest.mark.parametrize("heads", [2, 12])
+def test_rotate_broadcast_input(hs, heads):
+    """One head for all, one token for all: strides of 0."""
+    g = _gen(heads + 50)
+    x = _randn(g, 1, 1, 192).expand(33, heads, 192)
+    out = torch.empty((33, heads, 192), dtype=BF, device="cuda")
+    positions, freq, w = torch.arange(33, device="cuda", dtype=torch.int32), _freq(64), _randn(g, 192)
+    hs.hs_norm_rotate(x, out, q_weight=w, eps=EPS, positions=positions, inv_freq=freq)
+    _close(out, *_rotate_ref(x, w, positions, freq, 128, True), BF)
+
+
 def test_rotate_into_the_absorbed_query(hs):
     """A query's last 64 channels, rotated into the last 64 of the absorbed query's 576."""
     g = _gen(1)
@@ -406,6 +433,25 @@ def test_read_contexts(hs, counts, lengths, e4m3):
     assert (out[n:] == 9).all()
 
 
+@pytest.mark.parametrize("out_type", [BF, F32])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_read_rows_of_16_byte_alignment(hs, e4m3, out_type):
+    """Rows inside wider ones, each 16 bytes past a border of 32; outputs likewise; the same row several times."""
+    g = _gen(9)
+    rows = _form(_randn(g, 3, 20, 576), e4m3)
+    raw = rows if e4m3 else rows.view(torch.uint8)
+    hold = torch.full((3, 21, raw.shape[-1] + 48), 255, dtype=torch.uint8, device="cuda")
+    hold[:, :20, 16:16 + raw.shape[-1]] = raw
+    inside = hold[:, :20, 16:16 + raw.shape[-1]]
+    skip = 16 // torch.empty((), dtype=out_type).element_size()
+    out = torch.full((3, 40, 576 + 2 * skip), NAN, dtype=out_type, device="cuda")
+    slots = torch.randint(0, 20, (3, 40), generator=g, device="cuda", dtype=torch.int32)
+    form = hs.HS_ROWS_E4M3 if e4m3 else hs.HS_ROWS_16BIT
+    hs.hs_latent_read(inside, out[..., skip:skip + 576], slots=slots, row_format=form, dtype=BF)
+    _check_read(out[..., skip:skip + 576], _wide(rows, e4m3)[torch.arange(3, device="cuda")[:, None], slots.long()])
+    assert out[..., :skip].isnan().all() and out[..., skip + 576:].isnan().all()
+
+
 def test_read_special_values(hs):
     rows = _pack8(_randn(_gen(5), 1, 4, 576))
     rows[0, 1, 7] = 0x7F                                            # e4m3 NaN
@@ -604,6 +650,23 @@ def test_shared_strides(hs, e4m3):
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
+def test_shared_strides_with_lengths(hs, e4m3):
+    """One query for all requests (a stride of 0), and prefix rows 16 bytes past borders of 32, with lengths."""
+    B, H, M, N = 5, 16, 300, 20
+    g = _gen(21)
+    q, prefix, rows = _randn(g, 1, 1, H, 576), _form(_randn(g, M, 576), e4m3), _form(_randn(g, B, N, 576), e4m3)
+    raw = prefix if e4m3 else prefix.view(torch.uint8)
+    padded = torch.full((M, raw.shape[-1] + 48), 255, dtype=torch.uint8, device="cuda")
+    padded[:, 16:16 + raw.shape[-1]] = raw
+    seen, lengths = [300, 0, 129, 7, 256], [20, 1, 0, 9, 20]
+    kw = dict(e4m3=e4m3, lengths=_ints(lengths), prefix_lengths=_ints(seen))
+    picked = [[torch.arange(n, device="cuda")] for n in lengths]
+    every = q.expand(B, 1, H, 576)
+    got = _shared(hs, every, padded[:, 16:16 + raw.shape[-1]], rows, **kw)
+    _check_shared(*got, _shared_ref(every, prefix, seen, rows, picked, e4m3, SCALE), BF)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("std,scale", [(0.0, SCALE), (30.0, SCALE), (1.0, -0.05), (1.0, 0.0)])
 def test_shared_flat_and_peaked(hs, std, scale, e4m3):
     g = _gen(15)
@@ -672,6 +735,38 @@ def test_shared_same_bits_again_on_another_stream_and_in_a_graph(hs, e4m3):
     graph.replay()
     short, _ = _shared(hs, q, prefix, rows, **kw)
     assert torch.equal(out, short)
+
+
+@pytest.mark.parametrize("partial", [False, True])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_shared_calls_behind_one_another(hs, e4m3, partial):
+    """Calls of several sizes on one stream, in one workspace, none waited for; each is followed at once by work that
+    overwrites its inputs."""
+    g = _gen(22)
+    form = hs.HS_ROWS_E4M3 if e4m3 else hs.HS_ROWS_16BIT
+    sizes = [(20, 1, 16, 5000, 300), (3, 2, 20, 700, 500), (2, 1, 128, 20000, 40), (160, 1, 128, 300, 5), (1, 1, 1, 65, 3000)]
+    ws = torch.empty(max(hs.hs_latent_attend_shared_workspace(B, P, H, N, M, form) for B, P, H, M, N in sizes), dtype=torch.uint8, device="cuda")
+    made = []
+    for B, P, H, M, N in sizes:
+        q, prefix, rows = _randn(g, B, P, H, 576), _form(_randn(g, M, 576), e4m3), _form(_randn(g, B, N, 576), e4m3)
+        lengths = torch.randint(0, N + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+        seen = torch.randint(0, M + 1, (B,), generator=g, device="cuda", dtype=torch.int32) if partial else None
+        kw = dict(lengths=lengths, prefix_lengths=seen)
+        made.append((q, prefix, rows, kw, _shared(hs, q, prefix, rows, e4m3=e4m3, **kw)[0]))
+    kept = [(q.clone(), prefix.clone(), rows.clone()) for q, prefix, rows, _, _ in made]
+    outs = []
+    for _ in range(4):
+        for (q, prefix, rows, kw, _), copies in zip(made, kept):
+            out = torch.empty(q.shape[:-1] + (512,), dtype=BF, device="cuda")
+            hs.hs_latent_attend_shared(q, prefix, rows, out, SCALE, workspace=ws, row_format=form,
+                                       stream=torch.cuda.current_stream(), **kw)
+            for x in (q, prefix, rows):
+                x.zero_()
+            for x, copy in zip((q, prefix, rows), copies):
+                x.copy_(copy)
+            outs.append(out)
+    for i, out in enumerate(outs):
+        assert torch.equal(out, made[i % len(made)][4])
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
