@@ -291,7 +291,9 @@ def test_write_staged(hs, n, dtype, e4m3, turn, norm):
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("new,lengths", [
     ([1], [1]), ([1, 1, 1], [5, 1, 40]), ([3, 0, 40, 1, 0], [3, 7, 40, 33, 0]), ([0, 0, 5], [0, 0, 9]),
-    ([10, 6, 4], [4, 50, 2]), ([2] * 100, list(range(2, 102))), ([1] * 1100, [i % 60 for i in range(1100)])])
+    ([10, 6, 4], [4, 50, 2]), ([2] * 100, list(range(2, 102))), ([1] * 1100, [i % 60 for i in range(1100)]),
+    ([2] + [0] * 30 + [1] + [0] * 31 + [3] + [0] * 200 + [20, 1], [7] * 266), ([40] * 500, [44] * 500),
+    ([0] * 40 + [1] + [0] * 40, [3] * 81)])
 def test_write_contexts(hs, new, lengths, e4m3):
     """Ragged tokens at their contexts' ends.  Rows before 0 and behind the last are dropped, as are tokens
     of no request; nothing else changes."""
@@ -414,7 +416,8 @@ def test_read_slots(hs, B, N, K, kind, out_type):
 
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("counts,lengths", [
-    ([5], None), ([3, 0, 20, 1], None), ([3, 0, 20, 1], [3, 9, 25, 30]), ([4, 4], [2, 33]), ([1] * 40, list(range(40)))])
+    ([5], None), ([3, 0, 20, 1], None), ([3, 0, 20, 1], [3, 9, 25, 30]), ([4, 4], [2, 33]), ([1] * 40, list(range(40))),
+    ([2] + [0] * 30 + [1] + [0] * 31 + [3] + [0] * 200 + [20, 1], [9] * 266), ([0] * 40 + [1] + [0] * 40, None), ([1] * 70, None)])
 def test_read_contexts(hs, counts, lengths, e4m3):
     g = _gen(len(counts))
     B, N, n = len(counts), 30, sum(counts)
