@@ -78,7 +78,7 @@ struct Window {
 // alone, with its own loads of the weights: 34 us for the 24.3 above.)
 
 constexpr int kWarps = 8;        // of a block
-constexpr int kWriteBlocks = 3;  // an SM, 72 registers a thread (65,536 rows, 2 / 3 / 4 blocks: 30.3 / 27.0 / 27.6 us when it was chosen)
+constexpr int kWriteBlocks = 3;  // an SM, at most 80 registers a thread (65,536 rows, 2 / 3 / 4 blocks: 30.3 / 27.0 / 27.6 us when it was chosen)
 
 __device__ __forceinline__ void square2(float& s0, float& s1, float a0, float a1)  // added to the sums
 {
