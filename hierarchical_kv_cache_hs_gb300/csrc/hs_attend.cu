@@ -761,12 +761,13 @@ size_t hs_attend_workspace_bytes(int batch, int positions, int heads, int64_t ro
     return narrow > pair ? narrow : pair;
 }
 
-cudaError_t hs_launch_attend(const hs_attend_t& a, cudaStream_t s, bool after)
+cudaError_t hs_launch_attend(const hs_attend_t& a, cudaStream_t s, bool after, int pairs)
 {
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
+    if (pairs > 0 && 2 * pairs < sms) sms = 2 * pairs;
     return a.row_format == HS_ROWS_E4M3 && a.heads <= hs_attn::kNarrowHeads ? hs_attn::launch_narrow(a, sms, s, after)
                                                                             : hs_attn::launch_pair(a, sms, s, after);
 }

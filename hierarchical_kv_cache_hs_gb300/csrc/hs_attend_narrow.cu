@@ -530,8 +530,8 @@ template <typename T, int NH> cudaError_t launch(const Args& g, cudaStream_t s)
 {
     cudaError_t e = cudaFuncSetAttribute(hs_attend_narrow_kernel<T, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<NH>());
     if (e != cudaSuccess) return e;
-    if (g.after)
-        e = launch_after(hs_attend_narrow_kernel<T, NH>, dim3(g.workers + 1), kThreads, smem_bytes<NH>(), s, g);
+    if (g.after)  // two blocks side by side, which leaves whole pairs of SMs to the kernel that follows
+        e = launch_after_clusters(2, hs_attend_narrow_kernel<T, NH>, dim3(g.workers / 2 * 2 + 2), kThreads, smem_bytes<NH>(), s, g);
     else
         hs_attend_narrow_kernel<T, NH><<<g.workers, kThreads, smem_bytes<NH>(), s>>>(g), e = cudaGetLastError();
     if (e != cudaSuccess || !g.flat || g.workers <= 1) return e;

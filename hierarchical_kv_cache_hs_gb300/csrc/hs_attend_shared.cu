@@ -19,6 +19,8 @@
 // of S is enough, since O(t) stands between S(t+1) and S(t+2).
 //
 // Few tiles are bound by what surrounds them: the queries' way in (3 us), a pair's sums' way out (3 us), the join.
+// The own rows' part, whose tiles follow one another in latency, then runs beside this kernel on SMs of its own
+// (pairs_beside), and a prefix is widened meanwhile.
 //
 // Warps of a CTA: 0-3 queries, softmax and outputs, 4 brings keys, 5 values, 6 issues the
 // products (in the pair's first CTA), in the order S(t+1), O(t), so that a tile's softmax
@@ -107,7 +109,7 @@ __device__ __forceinline__ int64_t offset_of(const SharedArgs& g, int64_t query,
 }
 
 // Tiles of a unit: up to the last row that one of its queries sees, one at least.
-__device__ __forceinline__ int tiles_to(long long rows) { return rows <= kRows ? 1 : (int)((rows + kRows - 1) / kRows); }
+__host__ __device__ __forceinline__ int tiles_to(long long rows) { return rows <= kRows ? 1 : (int)((rows + kRows - 1) / kRows); }
 __device__ __forceinline__ int tiles_of(const SharedArgs& g, int unit)
 {
     const int64_t q0 = (int64_t)unit * 128;
@@ -906,6 +908,35 @@ cudaError_t widen_prefix(SharedArgs& g, const hs_prefix_t& p, uint8_t* ws, const
     return cudaGetLastError();
 }
 
+// Pairs of SMs for the own rows' part: all, so that the prefix's kernel follows it, or some, beside which that runs.  By
+// an estimate in ns, fitted to both kernels' times over 1 to 128 heads, 1 to 16 tiles a unit and 6 to 60 pairs; 5 % less
+// are asked for.  (64 requests x 16 heads, 16,384 shared rows, 1 to 512 own: 50.9 us one after the other, 44.7 with 26
+// pairs, 54.9 with 18, 56.6 with 44; 128 x 8 heads, 1000 shared rows, 64 own: 31.4, and 25.5 with 52; 200 x 128 heads,
+// 4096 shared rows, 64 own: 182, and 216 at best.)  Contexts of more than 512 rows may be far shorter than that, so they
+// are taken one after the other.
+int pairs_beside(const hs_attend_t& a, bool ragged, int units, int tiles, int all)
+{
+    const int64_t rows = a.slots ? a.entries : a.n_rows, own_tiles = rows <= kTile ? 1 : (rows + kTile - 1) / kTile;
+    if (!a.slots && own_tiles > 8) return all;
+    const bool e4m3 = a.row_format == HS_ROWS_E4M3, narrow = e4m3 && a.heads <= kNarrowHeads;  // narrow: an SM a unit
+    const int heads = a.heads < 128 ? a.heads : 128;
+    const int64_t own_units = (int64_t)a.batch * a.positions * ((a.heads + 127) / 128);
+    const int64_t own_unit = narrow ? 1200 + 200 * heads + 1350 * own_tiles : 4200 + 30 * heads + (e4m3 ? 1700 : 1050) * own_tiles;
+    const int64_t unit = (ragged ? (3 * (int64_t)tiles + 3) / 4 : tiles) + kUnitCost;
+    auto own = [&](int64_t n) { return 7000 + (own_units + (narrow ? 2 : 1) * n - 1) / ((narrow ? 2 : 1) * n) * own_unit; };
+    auto prefix = [&](int64_t n) {
+        const int64_t whole = (units + n - 1) / n * unit, pieces = (units * unit + n - 1) / n + 2;
+        return 13000 + (e4m3 ? 1600 : 1450) * (whole < pieces ? whole : pieces);
+    };
+    int best = all;
+    int64_t time = (own(all) + prefix(all) - 2000) * 95 / 100 * 17;
+    for (int n = 1; n < all; ++n) {
+        const int64_t x = own(n), y = prefix(all - n), t = 16 * (x > y ? x : y) + (x < y ? x : y);  // the longer of both counts
+        if (t < time) time = t, best = n;
+    }
+    return best;
+}
+
 }  // namespace
 }  // namespace hs_attn
 
@@ -942,16 +973,18 @@ cudaError_t hs_launch_attend_shared(const hs_attend_t& a, const hs_prefix_t& p, 
         e = map_rows(&map, p.rows, p.n_rows, p.row_stride);
     }
     if (e != cudaSuccess) return e;
-    // The own rows' part comes directly before the prefix's kernel, which may begin on the SMs that it leaves.
-    if (a.n_rows > 0 && (!a.slots || a.entries > 0)) {
+    g.units = (int)((g.queries + 127) / 128);
+    const int all = sms / 2 < kMaxPairs ? (sms > 1 ? sms / 2 : 1) : kMaxPairs;
+    const bool own_rows = a.n_rows > 0 && (!a.slots || a.entries > 0);
+    const int own_pairs = own_rows ? pairs_beside(a, p.lengths, g.units, tiles_to(p.n_rows), all) : 0, pairs = own_pairs < all ? all - own_pairs : all;
+    // The own rows' part comes directly before the prefix's kernel, which begins on the SMs that it leaves.
+    if (own_rows) {
         hs_attend_t own = a;
         own.lse = reinterpret_cast<float*>(ws + at.lse);
         g.own_lse = own.lse;
-        e = hs_launch_attend(own, s, widened);
+        e = hs_launch_attend(own, s, widened, own_pairs);
         if (e != cudaSuccess) return e;
     }
-    g.units = (int)((g.queries + 127) / 128);
-    const int pairs = sms / 2 < kMaxPairs ? (sms > 1 ? sms / 2 : 1) : kMaxPairs;
     g.cut(pairs, p.n_rows, 5, kUnitCost, kRows);
     if (g.flat) {
         // Each pair's partial results go out and come back, 1.2 us for ten pairs where a tile takes 1.4: few tiles take

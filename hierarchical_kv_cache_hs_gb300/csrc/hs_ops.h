@@ -18,8 +18,9 @@ inline int hs_norm_group(int dim, int carry, int group) { return group >= dim + 
 
 // hs_ops.cpp has checked the arguments; these launch.
 // after: the call's kernels may begin while the one before them in the stream runs, which has to come from the same call
-// and let them; what is launched behind them with launch_after begins when that one is done.
-cudaError_t hs_launch_attend(const hs_attend_t& a, cudaStream_t s, bool after = false);
+// and let them; what is launched behind them with launch_after begins when that one is done.  pairs: of SMs that it may
+// take (0: all).
+cudaError_t hs_launch_attend(const hs_attend_t& a, cudaStream_t s, bool after = false, int pairs = 0);
 cudaError_t hs_launch_prefill(const hs_prefill_t& a, cudaStream_t s);
 cudaError_t hs_launch_norm(const hs_norm_t& a, cudaStream_t s);
 cudaError_t hs_launch_write(const hs_write_t& a, cudaStream_t s);
@@ -69,18 +70,30 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b)
 }
 
 // A launch that may set up while the kernel before it in the stream runs out; griddepcontrol.wait waits for its results.
+// Its blocks in clusters of `cluster` where the kernel itself says nothing of them.
 template <typename... Params, typename... Values>
-cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s, Values... values)
+cudaError_t launch_after_clusters(unsigned cluster, void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s, Values... values)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = threads;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
+    if (cluster > 1) {
+        at[1].id = cudaLaunchAttributeClusterDimension;
+        at[1].val.clusterDim.x = cluster;
+        at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
     return cudaLaunchKernelEx(&cfg, kernel, values...);
+}
+template <typename... Params, typename... Values>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s, Values... values)
+{
+    return launch_after_clusters(1, kernel, grid, threads, smem, s, values...);
 }
