@@ -43,8 +43,8 @@ namespace {
 
 constexpr int kThreads = 7 * 32;
 constexpr int kRows = 128;  // rows a tile
-// Tiles' time that a unit's queries and output take: 2 instead of 4 costs 3 us (16 requests x 3 x 32 heads, 4096 rows:
-// 42 against 39.5; 64 x 32 heads, 16,384 rows: 70 against 68), 7 changes nothing.
+// Tiles' time that a unit's queries and output take: with the own rows' part first, 2 instead of 4 cost 3 us (16 requests
+// x 3 x 32 heads, 4096 rows: 42 against 39.5; 64 x 32 heads, 16,384 rows: 70 against 68), 7 changed nothing.
 constexpr int kUnitCost = 4;
 
 constexpr int kQTmem = 6;

@@ -9,7 +9,7 @@
 // A ring of bulk copies through shared memory instead of loads to registers took 49 us for the 36, and values kept
 // unpacked between the norm and the rotation 39 to 43: registers.
 //
-// A warp takes some heads of one token.  Its lanes form teams of 8, 16 or 32, a head each, and a lane has the
+// A warp takes some heads of one token.  Its lanes form teams of 4 to 32, a head each, and a lane has the
 // same channels of every head that its team passes over: its weights, sines and cosines
 // stay in registers.  A lane's channels come in units of 16 bytes, as two halves of 8
 // that lie side by side or, for pairs whose channels are half of the rotary ones apart,
@@ -384,12 +384,14 @@ template <typename T> cudaError_t launch(const hs_rotate_t& a, cudaStream_t s)
     if (a.rotation == HS_ROTATE_NONE) g.a.rope = 0;
     whole = whole && a.rope_at % (2 * H) == 0 && g.a.rope % (2 * H) == 0;
     if (!whole) return launch_any<T>(g, s);
-    // the team and units a lane that leave the fewest lanes without a unit
+    // The team and units a lane that leave the fewest lanes without a unit; teams of 4 for heads of up to 4 units (8192
+    // tokens x 68 heads of 32: 21.1 us against 29.4 with 8) and for few heads (32,768 x 2 of 96: 13.6 against 17.4), but
+    // not with several units a lane for many (8192 x 36 of 96: 40.0 against 34.1; of 80 40.0 against 33.1).
     const int units = a.dim / (2 * H);
     int nv = 1, best = 1 << 30;
     for (int n : {1, 2, 3, 4, 8})
-        for (int team = 8; team <= 32; team *= 2)
-            if (n * team >= units && n * team < best) best = n * team, nv = n, g.team = team;
+        for (int team = 4; team <= 32; team *= 2)
+            if (n * team >= units && n * team < best && (team > 4 || n == 1 || a.heads[0] + a.heads[1] <= kFew)) best = n * team, nv = n, g.team = team;
     const int ahead = nv == 1 ? 4 : nv == 2 ? 2 : 1, once = ahead * (32 / g.team);  // heads of a warp at once
     // all heads of a token to a warp, whose sines and weights serve them all, but where that leaves SMs without work
     int dev = 0, sms = 0;

@@ -91,7 +91,8 @@ ROTATE = [  # tokens, heads, key heads, dim, rope, rope_at
     (1, 16, 0, 192, 64, 128), (64, 128, 0, 192, 64, 128), (3, 1, 0, 64, 64, 0), (5, 8, 2, 128, 128, 0),
     (7, 20, 1, 80, 80, 0), (2, 3, 3, 96, 32, 16), (33, 1, 1, 576, 64, 512), (300, 2, 0, 256, 128, 64),
     (1, 1, 0, 2, 2, 0), (4, 5, 2, 7, 4, 1), (9, 2, 1, 100, 50, 30), (3, 2, 0, 1024, 1024, 0), (2, 300, 5, 72, 24, 24),
-    (1, 1, 1, 1000, 998, 1), (17, 64, 8, 128, 64, 64), (1025, 1, 0, 128, 64, 0)]
+    (1, 1, 1, 1000, 998, 1), (17, 64, 8, 128, 64, 64), (1025, 1, 0, 128, 64, 0), (70, 1, 1, 96, 64, 32),
+    (33, 2, 1, 48, 16, 16), (50, 40, 4, 32, 32, 0), (5, 1, 0, 32, 16, 16), (130, 3, 0, 80, 80, 0), (300, 20, 0, 192, 64, 64)]
 
 
 @pytest.mark.parametrize("pairs", [True, False])
