@@ -727,7 +727,9 @@ template <typename T, int WARPS, int N> __global__ void __launch_bounds__(256) h
     j.top = -INFINITY, j.sum = 0.f;
 #pragma unroll
     for (int k = 0; k < N; ++k) j.acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+    constexpr int kAtOnce = WARPS > 1 ? 8 : 4;  // 75 pieces 31.2 us against 33.1 with 4 (1 request x 16
+                                               // heads, 65,536 rows); units of 6 pieces 48 against 47
+#pragma unroll kAtOnce
     for (int n = first + part; n <= last; n += WARPS) {
         const Sums& p = g.parts[first == last ? 2 * kMaxPairs + unit : 2 * n + (n == first)];
         float4 o[N];
