@@ -505,7 +505,29 @@ __device__ void soften(const Args& g, uint32_t sbase, Aux* x, uint32_t rank, int
         Partial* part = reinterpret_cast<Partial*>(ws + kOffPartial) + 2 * pair + (walk.t0 == 0 ? 1 : 0);
         const bool some = sum > 0.f || sum != sum;
         const float inv = some ? 1.f / sum : 0.f;
-        if (whole) {
+        if (whole && g.wide) {  // as below, 32 channels of each half at a time
+            float* out = g.wide + (walk.b * a.positions + walk.p) * (int64_t)a.heads * HS_LATENT_DIM;
+#pragma unroll 1
+            for (int n = 0; n < 256; n += 32) {
+                uint32_t r[32];
+                __syncwarp();
+                tc::tmem_ld32(tmem + kColO + n, r);
+                tc::tmem_wait_ld(r);
+                auto f = [&](int k) { return some ? __float_as_uint(__uint_as_float(r[k]) * inv) : 0u; };
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    tc::st_shared16(sbase + kOffP + threadIdx.x * 128 + ((i ^ (row & 7)) << 4), f(4 * i), f(4 * i + 1), f(4 * i + 2), f(4 * i + 3));
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int at = 16 * i + (threadIdx.x >> 3), ch = threadIdx.x & 7;
+                    const int h = walk.hb * 128 + (int)rank * 64 + (at & 63);
+                    const uint4 v = tc::ld_shared16(sbase + kOffP + at * 128 + ((ch ^ (at & 7)) << 4));
+                    if (h < a.heads) *reinterpret_cast<uint4*>(out + (int64_t)h * HS_LATENT_DIM + 256 * (at >> 6) + n + 4 * ch) = v;
+                }
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+            }
+        } else if (whole) {
             // Through the buffers of P, so that eight lanes write 128 bytes of a head together: 64 channels
             // of each half at a time, [half][head][128 B].
             T* out = static_cast<T*>(a.out) + walk.b * a.out_stride[0] + walk.p * a.out_stride[1];
@@ -694,8 +716,15 @@ __global__ void __launch_bounds__(512) hs_attend_join_kernel(const __grid_consta
     }
     const bool some = sum > 0.f || sum != sum;
     const float inv = some ? 1.f / sum : 0.f;
+    if (g.wide) {
+        float* out = g.wide + ((b * a.positions + p) * (int64_t)a.heads + head) * HS_LATENT_DIM + 256 * half + c0;
+#pragma unroll
+        for (int k = 0; k < COLS; k += 4)
+            *reinterpret_cast<float4*>(out + k) = make_float4(acc[k] * inv, acc[k + 1] * inv, acc[k + 2] * inv, acc[k + 3] * inv);
+    }
     T* out = static_cast<T*>(a.out) + b * a.out_stride[0] + p * a.out_stride[1] + (int64_t)head * a.out_stride[2] +
              256 * half + c0;
+    if (!g.wide)
 #pragma unroll
     for (int k = 0; k < COLS; k += 4)
         *reinterpret_cast<uint2*>(out + k) =
@@ -734,11 +763,12 @@ size_t pair_workspace(int64_t units, int64_t tiles)
     return kOffPartial + sizeof(Partial) * 2 * (size_t)(units * tiles < kMaxPairs ? units * tiles : kMaxPairs);
 }
 
-cudaError_t launch_pair(const hs_attend_t& a, int sms, cudaStream_t s, bool after)
+cudaError_t launch_pair(const hs_attend_t& a, int sms, cudaStream_t s, bool after, float* wide)
 {
     Args g;
     g.a = a;
     g.after = after;
+    g.wide = wide;
     g.head_blocks = (a.heads + 127) / 128;
     g.units = a.batch * a.positions * g.head_blocks;
     // Pieces also write and join up to two partial results a pair: about 10 us, 10 tiles' time.
@@ -761,13 +791,13 @@ size_t hs_attend_workspace_bytes(int batch, int positions, int heads, int64_t ro
     return narrow > pair ? narrow : pair;
 }
 
-cudaError_t hs_launch_attend(const hs_attend_t& a, cudaStream_t s, bool after, int pairs)
+cudaError_t hs_launch_attend(const hs_attend_t& a, cudaStream_t s, bool after, int pairs, float* wide)
 {
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     if (pairs > 0 && 2 * pairs < sms) sms = 2 * pairs;
-    return a.row_format == HS_ROWS_E4M3 && a.heads <= hs_attn::kNarrowHeads ? hs_attn::launch_narrow(a, sms, s, after)
-                                                                            : hs_attn::launch_pair(a, sms, s, after);
+    return a.row_format == HS_ROWS_E4M3 && a.heads <= hs_attn::kNarrowHeads ? hs_attn::launch_narrow(a, sms, s, after, wide)
+                                                                            : hs_attn::launch_pair(a, sms, s, after, wide);
 }

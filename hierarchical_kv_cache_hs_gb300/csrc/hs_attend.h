@@ -49,7 +49,8 @@ struct Cut {
 struct Args : Cut {
     hs_attend_t a;
     int head_blocks;
-    bool after;  // as in hs_launch_attend
+    bool after;   // as in hs_launch_attend
+    float* wide;  // likewise
 };
 
 // With `after` a grid has one worker more, which only waits for the kernel before and then lets the next one begin.
@@ -332,8 +333,8 @@ constexpr int kMaxPairs = 76;  // pairs of SMs
 // rows: 102 against 204 us with 16 heads, 128 against 206 with 32; a form for 48 heads took
 // 262 where the pair takes 209, one for 16-bit rows 154 where it takes 140 with 16).
 constexpr int kNarrowHeads = 32;
-cudaError_t launch_pair(const hs_attend_t& a, int sms, cudaStream_t s, bool after);  // sms: that it may take
-cudaError_t launch_narrow(const hs_attend_t& a, int sms, cudaStream_t s, bool after);
+cudaError_t launch_pair(const hs_attend_t& a, int sms, cudaStream_t s, bool after, float* wide);  // sms: that it may take
+cudaError_t launch_narrow(const hs_attend_t& a, int sms, cudaStream_t s, bool after, float* wide);
 size_t pair_workspace(int64_t units, int64_t tiles);
 size_t narrow_workspace(int64_t units, int64_t tiles, int heads);
 

@@ -409,7 +409,11 @@ template <typename T, int NH> __device__ void soften(const Args& g, uint32_t sba
                 if (head >= a.heads) continue;
                 if (whole) {
                     const float f = x->inv[head];  // 0: no row counted
-                    out[head * a.out_stride[2] + 128 * i] = HsType<T>::from_float(f == 0.f ? 0.f : __uint_as_float(o[k]) * f);
+                    const float v = f == 0.f ? 0.f : __uint_as_float(o[k]) * f;
+                    if (g.wide)
+                        g.wide[(unit * a.heads + head) * HS_LATENT_DIM + 128 * i + 32 * warp + lane] = v;
+                    else
+                        out[head * a.out_stride[2] + 128 * i] = HsType<T>::from_float(v);
                 } else {
                     part->o[i][head][32 * warp + lane] = __uint_as_float(o[k]);
                 }
@@ -521,7 +525,11 @@ __global__ void __launch_bounds__(512) hs_attend_narrow_join_kernel(const __grid
         if (h0 + k >= a.heads) continue;
         const float l = total[k];
         const bool some = l > 0.f || l != l;
-        out[(h0 + k) * a.out_stride[2]] = HsType<T>::from_float(some ? acc[k] / l : 0.f);
+        const float v = some ? acc[k] / l : 0.f;
+        if (g.wide)
+            g.wide[((int64_t)unit * a.heads + h0 + k) * HS_LATENT_DIM + t] = v;
+        else
+            out[(h0 + k) * a.out_stride[2]] = HsType<T>::from_float(v);
         if (a.lse && t == 0) a.lse[(int64_t)unit * a.heads + h0 + k] = some ? (reference[k] + log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
 }
@@ -547,11 +555,12 @@ size_t narrow_workspace(int64_t units, int64_t tiles, int heads)
     return kOffPartial + part * 2 * (size_t)(units * tiles < kMaxCtas ? units * tiles : kMaxCtas);
 }
 
-cudaError_t launch_narrow(const hs_attend_t& a, int sms, cudaStream_t s, bool after)
+cudaError_t launch_narrow(const hs_attend_t& a, int sms, cudaStream_t s, bool after, float* wide)
 {
     Args g;
     g.a = a;
     g.after = after;
+    g.wide = wide;
     g.head_blocks = 1;
     g.units = a.batch * a.positions;
     // Pieces also write and join up to two partial results an SM: about 8 us, 6 tiles' time.

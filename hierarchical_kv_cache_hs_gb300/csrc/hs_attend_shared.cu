@@ -85,6 +85,7 @@ struct SharedArgs : Cut {
     const float* scales;        // of 8-bit rows
     const float* log_scales;    // base 2, not below kLeastLogScale
     const float* own_lse;       // NULL: no own rows
+    const float* own_out;       // their part, [queries][512]
     Sums* parts;                // two a pair, then one a unit with all_join
     bool all_join;              // units leave through the join, whole ones too
     Start* starts;              // with lengths: where each pair's piece starts
@@ -560,18 +561,21 @@ template <typename T, bool E4M3> __device__ void soften(const SharedArgs& g, uin
                 out[i] = static_cast<T*>(a.out) + (some[i] ? offset_of(g, query0 + at, a.out_stride) : 0);
                 f[i] = make_float2(x->red[0][at], x->red[1][at]);
             }
-            uint2 old[8];
+            const float* own = g.own_out + (query0 + row0) * HS_LATENT_DIM;
+            float4 old[8];
             auto bring = [&](int n) {  // a step ahead
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    old[i] = some[i & 3] && f[i & 3].y != 0.f && n < 256 ? *reinterpret_cast<const uint2*>(out[i & 3] + 256 * (i >> 2) + n + 4 * ch) : make_uint2(0, 0);
+                    old[i] = some[i & 3] && f[i & 3].y != 0.f && n < 256
+                                 ? *reinterpret_cast<const float4*>(own + 16 * (i & 3) * HS_LATENT_DIM + 256 * (i >> 2) + n + 4 * ch)
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
             };
             bring(0);
             leave([&](int i, int c, const uint4& v) {
-                const float2 e = f[i & 3], h0 = unpack2<T>(old[i].x), h1 = unpack2<T>(old[i].y);
+                const float2 e = f[i & 3];
                 auto joined = [&](uint32_t o, float own) { return (e.x != 0.f ? __uint_as_float(o) * e.x : 0.f) + (e.y != 0.f ? own * e.y : 0.f); };
                 if (some[i & 3])
-                    *reinterpret_cast<uint2*>(out[i & 3] + c) = make_uint2(pack2<T>(joined(v.x, h0.x), joined(v.y, h0.y)), pack2<T>(joined(v.z, h1.x), joined(v.w, h1.y)));
+                    *reinterpret_cast<uint2*>(out[i & 3] + c) = make_uint2(pack2<T>(joined(v.x, old[i].x), joined(v.y, old[i].y)), pack2<T>(joined(v.z, old[i].z), joined(v.w, old[i].w)));
                 if (i == 7) bring(c - 256 - 4 * ch + 32);
             });
         }
@@ -715,13 +719,13 @@ template <typename T, int WARPS, int N> __global__ void __launch_bounds__(256) h
     T* out = static_cast<T*>(a.out) + offset_of(g, query, a.out_stride) + ch;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     float own_lse = -INFINITY;
-    uint2 old[N];
+    float4 old[N];
 #pragma unroll
-    for (int k = 0; k < N; ++k) old[k] = make_uint2(0, 0);
+    for (int k = 0; k < N; ++k) old[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (g.own_lse && part == 0) {
         own_lse = g.own_lse[query];
 #pragma unroll
-        for (int k = 0; k < N; ++k) old[k] = *reinterpret_cast<const uint2*>(out + 128 * k);
+        for (int k = 0; k < N; ++k) old[k] = *reinterpret_cast<const float4*>(g.own_out + query * HS_LATENT_DIM + ch + 128 * k);
     }
     Joined<N> j;
     j.top = -INFINITY, j.sum = 0.f;
@@ -747,10 +751,9 @@ template <typename T, int WARPS, int N> __global__ void __launch_bounds__(256) h
     const Mix m = mix(j.top, j.sum, own_lse);
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        const float2 h0 = unpack2<T>(old[k].x), h1 = unpack2<T>(old[k].y);
         auto joined = [&](float sum, float own) { return (j.sum == 0.f ? 0.f : sum * m.prefix) + (m.own != 0.f ? own * m.own : 0.f); };
-        *reinterpret_cast<uint2*>(out + 128 * k) = make_uint2(pack2<T>(joined(j.acc[k].x, h0.x), joined(j.acc[k].y, h0.y)),
-                                                             pack2<T>(joined(j.acc[k].z, h1.x), joined(j.acc[k].w, h1.y)));
+        *reinterpret_cast<uint2*>(out + 128 * k) = make_uint2(pack2<T>(joined(j.acc[k].x, old[k].x), joined(j.acc[k].y, old[k].y)),
+                                                             pack2<T>(joined(j.acc[k].z, old[k].z), joined(j.acc[k].w, old[k].w)));
     }
     if (a.lse && ch == 0) a.lse[query] = m.lse;
 }
@@ -849,15 +852,17 @@ int64_t padded_rows(int64_t n) { return (n + kRows - 1) / kRows * kRows; }
 // part is done, where a pair of SMs takes 6 us for a unit.  More have not the place (0.26 MB a unit), and not the need.
 constexpr int64_t kJoinUnits = 2 * kMaxPairs;
 
-// Workspace: hs_latent_attend's for the own rows (its error word is the call's), then their lse, the partial results,
+// Workspace: hs_latent_attend's for the own rows (its error word is the call's), then their lse and outputs (in 32 bits:
+// they are rounded once, in the join; twice, outputs of mostly own rows were off by 0.0027, once by 0.0021, in bf16), the partial results,
 // where the pairs' pieces start, the prefix's rows in 16 bits, scales and their logarithms.
 struct Layout {
-    size_t lse, parts, starts, rows, scales, logs, end;
+    size_t lse, own, parts, starts, rows, scales, logs, end;
     Layout(int batch, int positions, int heads, int64_t own_rows, int64_t prefix_rows)
     {
         auto after = [](size_t at, size_t bytes) { return (at + bytes + 255) / 256 * 256; };
         lse = after(0, hs_attend_workspace_bytes(batch, positions, heads, own_rows));
-        parts = after(lse, sizeof(float) * batch * positions * (size_t)heads);
+        own = after(lse, sizeof(float) * batch * positions * (size_t)heads);
+        parts = after(own, own_rows > 0 ? sizeof(float) * HS_LATENT_DIM * batch * positions * (size_t)heads : 0);
         const int64_t units = ((int64_t)batch * positions * heads + 127) / 128;
         starts = after(parts, sizeof(Sums) * (2 * kMaxPairs + (units <= kJoinUnits ? units : 0)));
         rows = after(starts, sizeof(Start) * kMaxPairs);
@@ -984,7 +989,8 @@ cudaError_t hs_launch_attend_shared(const hs_attend_t& a, const hs_prefix_t& p, 
         hs_attend_t own = a;
         own.lse = reinterpret_cast<float*>(ws + at.lse);
         g.own_lse = own.lse;
-        e = hs_launch_attend(own, s, widened, own_pairs);
+        g.own_out = reinterpret_cast<float*>(ws + at.own);
+        e = hs_launch_attend(own, s, widened, own_pairs, reinterpret_cast<float*>(ws + at.own));
         if (e != cudaSuccess) return e;
     }
     g.cut(pairs, p.n_rows, 5, kUnitCost, kRows);

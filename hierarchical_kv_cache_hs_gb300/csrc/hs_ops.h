@@ -19,8 +19,8 @@ inline int hs_norm_group(int dim, int carry, int group) { return group >= dim + 
 // hs_ops.cpp has checked the arguments; these launch.
 // after: the call's kernels may begin while the one before them in the stream runs, which has to come from the same call
 // and let them; what is launched behind them with launch_after begins when that one is done.  pairs: of SMs that it may
-// take (0: all).
-cudaError_t hs_launch_attend(const hs_attend_t& a, cudaStream_t s, bool after = false, int pairs = 0);
+// take (0: all).  wide: where outputs go instead of a.out, [batch][positions][heads][512], unrounded.
+cudaError_t hs_launch_attend(const hs_attend_t& a, cudaStream_t s, bool after = false, int pairs = 0, float* wide = nullptr);
 cudaError_t hs_launch_prefill(const hs_prefill_t& a, cudaStream_t s);
 cudaError_t hs_launch_norm(const hs_norm_t& a, cudaStream_t s);
 cudaError_t hs_launch_write(const hs_write_t& a, cudaStream_t s);

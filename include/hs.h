@@ -930,13 +930,13 @@ int hs_norm_rotate(const hs_rotate_t* args, hs_stream_t stream);
  * A prefix row that a request does not see has no part in its outputs, whatever it
  * holds; one with a value that is not finite makes the output NaN of every request
  * that sees it.
- * Roundings as in hs_latent_attend, and the own rows' part is rounded to `dtype`
- * before it is joined.  out and lse are of the whole; with no row at all out is 0 and
- * lse -inf.  batch * positions * heads stays below 2^31.
+ * Roundings as in hs_latent_attend: both parts are joined in fp32 and rounded once.
+ * out and lse are of the whole; with no row at all out is 0 and lse -inf.  batch * positions * heads stays below 2^31.
  * The workspace call takes what hs_latent_attend's does, and the prefix's rows
  * and form.  8-bit prefixes, and prefixes with lengths, are copied into the
  * workspace in 16 bits at every call (1152 bytes a row, and 8 for their scales);
- * partial results take 0.26 MB for each of up to 304 pieces and units.
+ * partial results take 0.26 MB for each of up to 304 pieces and units, the own
+ * rows' part 2 KB a query where there are own rows.
  * Source: no passage (as hs_latent_attend).
  */
 typedef struct {

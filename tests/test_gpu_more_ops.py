@@ -670,6 +670,24 @@ def test_shared_strides_with_lengths(hs, e4m3):
     _check_shared(*got, _shared_ref(every, prefix, seen, rows, picked, e4m3, SCALE), BF)
 
 
+@pytest.mark.parametrize("dtype", [BF, HALF])
+@pytest.mark.parametrize("size", [(20, 2, 128, 54, 842), (16, 1, 16, 1, 700), (90, 1, 32, 30, 500), (5, 1, 16, 64, 2000)])
+def test_shared_mostly_own_rows_are_rounded_once(hs, size, dtype):
+    """The own rows' part comes unrounded into the join."""
+    B, P, H, M, N = size
+    g = _gen(sum(size))
+    q, prefix, rows = (_randn(g, *s, dtype=dtype) for s in ((B, P, H, 576), (M, 576), (B, N, 576)))
+    lengths = _ints([N] * B)
+    out, _ = _shared(hs, q, prefix, rows, lengths=lengths)
+    picked = [[torch.arange(N - P + 1 + p, device="cuda") for p in range(P)] for _ in range(B)]
+    o = _shared_ref(q, prefix, [M] * B, rows, picked, False, SCALE)[0]
+    # A rounding is off by at most half a step, u of the power of two below the value; evenly spread and over a
+    # mantissa m whose logarithm is evenly spread, its 2-norm is u sqrt(E[1 / m^2] / 3) = u sqrt(3 / (8 ln 2) / 3) =
+    # 0.425 u of the value's.  The weights (their errors independent, and values of no common sign) and the output:
+    # 0.425 sqrt 2 = 0.601 u; the part rounded in between would make it 0.736.
+    assert (out.double() - o).norm() <= 0.64 * _half(dtype) * o.norm()
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("std,scale", [(0.0, SCALE), (30.0, SCALE), (1.0, -0.05), (1.0, 0.0)])
 def test_shared_flat_and_peaked(hs, std, scale, e4m3):
