@@ -99,6 +99,14 @@ __device__ __forceinline__ float warp_top(float v)  // likewise
     return d;
 }
 
+__device__ __forceinline__ void product2(float& a0, float& a1, float b, float rest)  // with b + rest, rounded once
+{
+    asm("{\n\t.reg .b64 a, b, r;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\tmov.b64 r, {%3, %3};\n\t"
+        "mul.rn.f32x2 r, a, r;\n\tfma.rn.f32x2 a, a, b, r;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(a0), "+f"(a1)
+        : "f"(b), "f"(rest));
+}
+
 __device__ __noinline__ float rare_quotient(float y, float scale) { return divided(y, scale, 0.f); }
 
 template <typename T, bool E4M3>
@@ -166,6 +174,7 @@ __global__ void __launch_bounds__(kWarps * 32, kWriteBlocks) hs_write_kernel(con
                               : make_float2(ox * s0 + r.x * c0, oy * s1 + r.y * c1);
             }
         }
+        float f = 1.f;
         if (a.weight) {
             float sum = 0.f, odd = 0.f;
 #pragma unroll
@@ -174,14 +183,14 @@ __global__ void __launch_bounds__(kWarps * 32, kWriteBlocks) hs_write_kernel(con
                 for (int k = 0; k < 8; k += 2) square2(sum, odd, h[v][k], h[v][k + 1]);
             sum += odd;
             for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-            const float f = rsqrtf(sum / HS_LATENT_DIM + a.eps);
+            f = rsqrtf(sum / HS_LATENT_DIM + a.eps);
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
                 float w[8];
                 Piece<T>::unpack(weight[v], w);
 #pragma unroll
                 for (int k = 0; k < 8; k += 2) {
-                    mul2(h[v][k], h[v][k + 1], f, f);
+                    if constexpr (!E4M3) mul2(h[v][k], h[v][k + 1], f, f);
                     mul2(h[v][k], h[v][k + 1], w[k], w[k + 1]);
                 }
             }
@@ -191,23 +200,30 @@ __global__ void __launch_bounds__(kWarps * 32, kWriteBlocks) hs_write_kernel(con
             for (int v = 0; v < 2; ++v) reinterpret_cast<uint4*>(out)[v * 32 + lane] = Piece<T>::pack(h[v]);
             reinterpret_cast<uint32_t*>(out + 2 * HS_LATENT_DIM)[lane] = pack2<T>(r.x, r.y);
         } else {
-            float top = nan_max(fabsf(r.x), fabsf(r.y));
+            // h: x w, exact products of 16-bit values, to be multiplied by f.  The quotients by max |y| / 448 are products
+            // with 448 f / max |y| (of the rotary channels 448 / max |y|) in two floats each, so that only one rounding
+            // is left in them: fewer values beside a border of e4m3 fall to its other side.
+            float tops[2] = {0.f, nan_max(fabsf(r.x), fabsf(r.y))};
 #pragma unroll
             for (int v = 0; v < 2; ++v)
 #pragma unroll
-                for (int k = 0; k < 8; k += 2) top = top3(top, h[v][k], h[v][k + 1]);
-            const float scale = warp_top(top) / HS_E4M3_MAX, inv = inverse(scale);
-            if (inv != 0.f) {
+                for (int k = 0; k < 8; k += 2) tops[0] = top3(tops[0], h[v][k], h[v][k + 1]);
+            tops[0] = warp_top(tops[0]), tops[1] = warp_top(tops[1]);
+            const float y = tops[0] * f, top = nan_max(y, tops[1]), rest = y > tops[1] ? fmaf(tops[0], f, -y) : 0.f;
+            const float scale = top / HS_E4M3_MAX, inv = 1.f / top;
+            const float by = HS_E4M3_MAX * inv, by_rest = (fmaf(-by, top, HS_E4M3_MAX) - by * rest) * inv;
+            const float by_f = by * f, by_f_rest = fmaf(by, f, -by_f) + by_rest * f;
+            if (inverse(scale) != 0.f && by_f > 1e-30f && by_f < 1e30f) {
 #pragma unroll
                 for (int v = 0; v < 2; ++v)
 #pragma unroll
-                    for (int k = 0; k < 8; k += 2) quotients(h[v][k], h[v][k + 1], scale, inv);
-                quotients(r.x, r.y, scale, inv);
+                    for (int k = 0; k < 8; k += 2) product2(h[v][k], h[v][k + 1], by_f, by_f_rest);
+                product2(r.x, r.y, by, by_rest);
             } else {  // zeros, or beyond what a reciprocal serves
 #pragma unroll
                 for (int v = 0; v < 2; ++v)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) h[v][k] = rare_quotient(h[v][k], scale);
+                    for (int k = 0; k < 8; ++k) h[v][k] = rare_quotient(h[v][k] * f, scale);
                 r = make_float2(rare_quotient(r.x, scale), rare_quotient(r.y, scale));
             }
             auto two = [](float y0, float y1) -> uint32_t { return __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3); };

@@ -797,8 +797,8 @@ int hs_rms_norm(const hs_norm_t* args, hs_stream_t stream);
  * rotary channels),
  *   y = [x[:512] / sqrt(mean(x[:512]^2) + eps) * weight ; rotated x[512:]]
  * as a row in the form `row_format` (HS_ROWS_E4M3: scale = max|y| / 448, values
- * e4m3(y / scale) with the quotient in fp32; all zeros: scale 0; a NaN makes the
- * scale NaN).  Without weight (NULL) the latent channels stay as they are.
+ * e4m3(448 y / max|y|) of the quotient rounded once to fp32; x * weight stays
+ * within fp32's range; all zeros: scale 0; a NaN makes the scale NaN).  Without weight (NULL) the latent channels stay as they are.
  * Each row is written once and whole (the 12 last bytes of an 8-bit row as zeros);
  * what lies between rows is left as it was.  Where it goes:
  *   start NULL  row t of `rows` (batch is ignored; n_rows >= tokens): the rows
