@@ -327,6 +327,28 @@ def test_write_contexts(hs, new, lengths, e4m3):
         assert (hold[touched][:, 580:592] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, HALF])
+@pytest.mark.parametrize("norm", [True, False])
+def test_write_values_beside_borders(hs, dtype, norm):
+    """8-bit values are those of the exact quotients, but for quotients that lie on a border of e4m3 within what the
+    rotation, the norm's root and one rounding leave: 2^-20 of them (the rotary channels': of their pair)."""
+    g = _gen(40)
+    n = 3000
+    x, w = _randn(g, n, 576, dtype=dtype), _randn(g, 512, dtype=dtype) if norm else None
+    positions = torch.randint(0, 9999, (n,), generator=g, device="cuda", dtype=torch.int32)
+    rows = torch.zeros((n, 592), dtype=torch.uint8, device="cuda")
+    hs.hs_latent_write(x, rows, weight=w, eps=EPS, positions=positions, inv_freq=_freq(64), row_format=hs.HS_ROWS_E4M3)
+    y, _ = _write_ref(x, w, positions, _freq(64), True)
+    q = 448 * y / y.abs().amax(-1, keepdim=True)
+    got = rows[:, :576].contiguous().view(torch.float8_e4m3fn).double()
+    want = q.float().to(torch.float8_e4m3fn).double()
+    near = 2.0 ** -20 * q.abs()
+    pair = q[:, 512:].abs().view(n, 32, 2).sum(-1, keepdim=True).expand(n, 32, 2).reshape(n, 64)
+    near[:, 512:] = 2.0 ** -20 * pair
+    off = (q - (got + want) / 2).abs()
+    assert bool(((got == want) | (off <= near)).all())
+
+
 def test_write_start_that_lies_outside(hs):
     """start and lengths of any value write nothing outside the rows."""
     x = _randn(_gen(2), 6, 576)
