@@ -927,9 +927,10 @@ cudaError_t widen_prefix(SharedArgs& g, const hs_prefix_t& p, uint8_t* ws, const
 // Pairs of SMs for the own rows' part: all, so that the prefix's kernel follows it, or some, beside which that runs.  By
 // an estimate in ns, fitted to both kernels' times over 1 to 128 heads, 1 to 16 tiles a unit and 6 to 60 pairs; 5 % less
 // are asked for.  (64 requests x 16 heads, 16,384 shared rows, 1 to 512 own: 50.9 us one after the other, 44.7 with 26
-// pairs, 54.9 with 18, 56.6 with 44; 128 x 8 heads, 1000 shared rows, 64 own: 31.4, and 25.5 with 52; 200 x 128 heads,
-// 4096 shared rows, 64 own: 182, and 216 at best.)  Contexts of more than 512 rows may be far shorter than that, so they
-// are taken one after the other.
+// pairs, 54.9 with 18, 56.6 with 44; 128 x 8 heads, 1000 shared rows, 64 own: 31.4, and 25.5 with 52; but 64 x 128 heads,
+// 16,384 shared 8-bit rows, 256 own: 206.3, and 207.3 with 6, 242 with 18; 64 x 16 heads, 2048 shared rows, 1 to 512 own:
+// 31.9, and 33.4 with the 32 that the estimate takes.)  Contexts of more than 512 rows may be far shorter than that, so
+// they are taken one after the other.
 int pairs_beside(const hs_attend_t& a, bool ragged, int units, int tiles, int all)
 {
     const int64_t rows = a.slots ? a.entries : a.n_rows, own_tiles = rows <= kTile ? 1 : (rows + kTile - 1) / kTile;
