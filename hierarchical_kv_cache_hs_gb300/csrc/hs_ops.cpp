@@ -232,13 +232,14 @@ int hs_norm_rotate(const hs_rotate_t* args, hs_stream_t stream)
     if (!args) return HS_ERR_ARG;
     const hs_rotate_t& a = *args;
     if (!is_16bit(a.dtype) && a.dtype != HS_TYPE_FP32) return HS_ERR_ARG;
-    if (a.dim <= 0 || a.tokens < 0 || a.heads[0] <= 0 || (a.x[1] ? a.heads[1] <= 0 : a.heads[1] != 0)) return HS_ERR_ARG;
+    if (a.dim <= 0 || a.tokens < 0 || a.heads[0] <= 0 || a.heads[1] < 0) return HS_ERR_ARG;
     if (a.rope < 0 || a.rope_at < 0 || (a.rotation == HS_ROTATE_NONE && a.rope)) return HS_ERR_ARG;
     if (!(a.eps >= 0.0f) || !std::isfinite(a.eps)) return HS_ERR_ARG;
     if (a.dim > HS_MAX_HEAD_CHANNELS || a.heads[0] > HS_MAX_HEADS || a.heads[1] > HS_MAX_HEADS || a.tokens > HS_MAX_TOKENS)
         return HS_ERR_LIMIT;
     if (a.rope > a.dim || a.rope_at > a.dim - a.rope) return HS_ERR_ARG;
-    if (a.tokens == 0) return HS_OK;
+    if (a.tokens == 0) return HS_OK;  // arrays of no tokens have no address, the keys' neither
+    if ((a.x[1] != nullptr) != (a.heads[1] > 0)) return HS_ERR_ARG;
     if (const int rc = check_rotation(a.rotation, a.rope, a.positions, a.inv_freq)) return rc;
     const uintptr_t el = a.dtype == HS_TYPE_FP32 ? 4 : 2;
     for (int k = 0; k < 2; ++k) {

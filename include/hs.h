@@ -892,7 +892,8 @@ int hs_latent_read(const hs_read_t* args, hs_stream_t stream);
  *           two must not overlap.  Any alignment of the element; 16-byte aligned
  *           rows (and rope_at, and half of rope for HS_ROTATE_HALVES) go faster.
  *   weight  [dim] of `dtype`
- * x[1] NULL: one array.  rope: even, 0 without a rotation.
+ * x[1] NULL, heads[1] 0: one array (with no tokens, x is not looked at).  Queries'
+ * and keys' arrays do not overlap one another.  rope: even, 0 without a rotation.
  * Source: no passage (the producer of the queries that hs_latent_prefill and
  * hs_latent_attend take).
  */

@@ -199,3 +199,11 @@ def test_binding_checks_tensors(hs):
         dict(prefix=good["prefix"].half()), dict(prefix=good["prefix"][None]), dict(prefix=good["prefix"][:, :512]),
         dict(row_format=hs.HS_ROWS_E4M3), dict(prefix_lengths=lengths.long()), dict(prefix_lengths=lengths[:1]),
         dict(lengths=None), dict(q=good["q"][0]), dict(lse=torch.zeros(2, 1, 4))])
+
+
+def test_rotate_no_tokens_with_keys(hs):
+    """Arrays of no tokens have no address; the heads are given all the same."""
+    nowhere = dict(tokens=0, x=(0, 0), out=(0, 0), weight=(0, 0), positions=None, inv_freq=None)
+    assert _rotate(hs, **nowhere) == hs.HS_OK
+    assert _rotate(hs, heads=(16, 0), **nowhere) == hs.HS_OK
+    assert _rotate(hs, heads=(16, -1), **nowhere) == hs.HS_ERR_ARG
