@@ -58,7 +58,7 @@ int check_rows(const void* rows, int64_t n_rows, int64_t row_stride, int64_t req
     return n_rows > INT32_MAX ? HS_ERR_LIMIT : HS_OK;
 }
 
-// An output of [n0][n1] rows of `channels`: one axis inside the other, and no two rows on one another.
+// An output of [n0][n1] rows of `channels` (strides in the same unit): one axis inside the other, and no two rows on one another.
 bool apart(const int64_t* stride, int64_t n0, int64_t n1, int channels)
 {
     if (n0 <= 1 || n1 <= 1) return (n0 <= 1 || stride[0] >= channels) && (n1 <= 1 || stride[1] >= channels);
@@ -205,8 +205,8 @@ int hs_latent_write(const hs_write_t* args, hs_stream_t stream)
     if (const int rc = check_rows(a.rows, a.n_rows, a.row_stride, a.request_stride, a.row_format, batch)) return rc;
     if (!a.start && a.n_rows < a.tokens) return HS_ERR_ARG;
     // rows of two requests on one another would be written twice
-    const int64_t apart = a.request_stride - row_bytes(a.row_format);
-    if (batch > 1 && a.n_rows > 0 && (apart < 0 || (a.n_rows > 1 && apart / (a.n_rows - 1) < a.row_stride))) return HS_ERR_ARG;
+    const int64_t strides[2] = {a.request_stride, a.row_stride};
+    if (a.n_rows > 0 && !apart(strides, batch, a.n_rows, row_bytes(a.row_format))) return HS_ERR_ARG;
     return result(hs_launch_write(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -809,8 +809,8 @@ int hs_rms_norm(const hs_norm_t* args, hs_stream_t stream);
  *               hs_latent_attend): the i-th of n goes to row lengths[b] - n + i of
  *               request b.  Not written: tokens of no request, and rows outside
  *               [0, n_rows).  (start is clamped to [0, tokens].)
- * So no two tokens go to one row; with batch > 1, request_stride has to keep the
- * requests' rows apart.  `rows` is device memory, or pinned host memory mapped
+ * So no two tokens go to one row; with batch > 1, the strides have to keep all
+ * rows apart (requests behind one another, or row by row in turn).  `rows` is device memory, or pinned host memory mapped
  * into the device address space (a handle's hs_host_pool: n_rows = H, row_stride
  * = R, request_stride = H * R; a prompt's rows then cross the host link once, as
  * they are written).

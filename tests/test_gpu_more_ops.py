@@ -380,6 +380,27 @@ def test_write_special_values(hs, dtype):
     _check_rows(rows[keep], y[keep], slack[keep], True, dtype)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_write_requests_in_turn(hs, e4m3):
+    """Row i of every request side by side, then row i + 1 of every request: no two rows on one another."""
+    B, N = 5, 12
+    g = _gen(31)
+    new, lengths = [3, 1, 0, 12, 2], [7, 1, 4, 12, 9]
+    n, width = sum(new), 592 if e4m3 else 1152
+    x, start = _randn(g, n, 576), _ints(np.concatenate([[0], np.cumsum(new)]).tolist())
+    kw = dict(start=start, lengths=_ints(lengths), row_format=hs.HS_ROWS_E4M3 if e4m3 else hs.HS_ROWS_16BIT)
+    turns = torch.full((N, B, width), 0xA5, dtype=torch.uint8, device="cuda")
+    apart = torch.full((B, N, width), 0xA5, dtype=torch.uint8, device="cuda")
+    hs.hs_latent_write(x, turns.transpose(0, 1), **kw)
+    hs.hs_latent_write(x, apart, **kw)
+    assert torch.equal(turns.transpose(0, 1), apart)
+    one_row = torch.full((1, B, width), 0xA5, dtype=torch.uint8, device="cuda")  # a stride that no row uses
+    hs.hs_latent_write(x, one_row.transpose(0, 1), **kw)
+    assert torch.equal(one_row[0], apart[:, 0])
+    with pytest.raises(hs.HsError):
+        hs.hs_latent_write(x, turns.transpose(0, 1)[:, :1].expand(B, N, width), **kw)
+
+
 def test_write_into_the_host_pool(hs):
     """A prompt's rows go to a handle's pinned pool as they are written, and come back from it."""
     B, S, R = 3, 64, 592
