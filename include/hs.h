@@ -929,8 +929,11 @@ int hs_norm_rotate(const hs_rotate_t* args, hs_stream_t stream);
  *   lengths         device int32 [batch], clamped to [0, n_rows]; NULL: all rows
  *                   for every request
  * A prefix row that a request does not see has no part in its outputs, whatever it
- * holds; one with a value that is not finite makes the output NaN of every request
- * that sees it.
+ * holds.  A value that is not finite, in a row that a request does see: 8-bit rows,
+ * and rows of a prefix with lengths, make that request's outputs NaN.  16-bit rows
+ * of a prefix without lengths are taken as they are: a NaN, and an infinity whose
+ * score is +inf (or NaN), makes the output of that position and head NaN; one whose
+ * score is -inf has weight 0, and only the channel of a latent infinity may be NaN.
  * Roundings as in hs_latent_attend: both parts are joined in fp32 and rounded once.
  * out and lse are of the whole; with no row at all out is 0 and lse -inf.  batch * positions * heads stays below 2^31.
  * The workspace call takes what hs_latent_attend's does, and the prefix's rows

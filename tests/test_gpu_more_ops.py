@@ -656,6 +656,38 @@ def test_shared_prefix_rows_that_are_not_finite(hs, value, e4m3):
     assert torch.equal(out[rest], want[rest]) and torch.equal(lse[rest], want_lse[rest])
 
 
+@pytest.mark.parametrize("dtype", [BF, HALF])
+@pytest.mark.parametrize("channel", [100, 540])
+@pytest.mark.parametrize("size", [(6, 16), (3, 128)])
+@pytest.mark.parametrize("value", [NAN, math.inf, -math.inf])
+def test_shared_prefix_values_that_are_not_finite_without_lengths(hs, value, size, channel, dtype):
+    """16-bit rows that all see, taken as they are: a NaN, or a score of +inf, makes a head's output NaN; a score of
+    -inf is a weight of 0, and leaves all but an infinite latent channel (0 times it).  With lengths that cover the
+    prefix such a row makes all of them NaN."""
+    B, H = size
+    g = _gen(B + channel)
+    M = 300
+    q, prefix, rows = _randn(g, B, 1, H, 576, dtype=dtype), _randn(g, M, 576, dtype=dtype), _randn(g, B, 20, 576, dtype=dtype)
+    q[..., channel] = torch.where(q[..., channel] == 0, 1.0, q[..., channel])  # no 0 times infinity
+    lengths, every = _ints([20] * B), [[torch.arange(20, device="cuda")] for _ in range(B)]
+    prefix[200, channel] = value
+    out, _ = _shared(hs, q, prefix, rows, lengths=lengths)
+    score = q[:, 0, :, channel].double() * value
+    below = score == -math.inf  # the others are +inf or NaN
+    assert out[:, 0][~below].isnan().all() and (value != value or bool(below.any()) and bool((~below).any()))
+    off = torch.zeros(512, dtype=torch.bool, device="cuda")
+    off[channel:channel + 1] = True
+    # without the row: a weight of 0 adds nothing, and the rows' order and tiles are those of zeros in its place
+    without = torch.cat([prefix[:200], prefix[201:]])
+    o, _, mean_abs, reach = _shared_ref(q, without, [M - 1] * B, rows, every, False, SCALE)
+    half, score = _half(dtype), 576 * 2.0 ** -23 * reach + 2.0 ** -17
+    tol = half * o.abs() + (2 * half + 2 * score) * mean_abs + _least(dtype) + 1e-30  # as in _check_shared
+    err = (out.double() - o).abs()[:, 0][below][:, ~off]
+    assert bool((err <= tol[:, 0][below][:, ~off]).all())
+    out, _ = _shared(hs, q, prefix, rows, lengths=lengths, prefix_lengths=_ints([M] * B))
+    assert out.isnan().all()
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 def test_shared_without_own_rows_or_prefix(hs, e4m3):
     g = _gen(13)
