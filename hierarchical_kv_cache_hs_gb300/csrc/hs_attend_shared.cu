@@ -863,7 +863,8 @@ constexpr int64_t kJoinUnits = 2 * kMaxPairs;
 
 // Workspace: hs_latent_attend's for the own rows (its error word is the call's), then their lse and outputs (in 32 bits:
 // they are rounded once, in the join; twice, outputs of mostly own rows were off by 0.0027, once by 0.0021, in bf16), the partial results,
-// where the pairs' pieces start, the prefix's rows in 16 bits, scales and their logarithms.
+// where the pairs' pieces start, the prefix's rows in 16 bits, scales and their logarithms.  More requests never need
+// less, so that a workspace for a loop's largest batch serves its smaller ones: units above kJoinUnits have its sums, too.
 struct Layout {
     size_t lse, own, parts, starts, rows, scales, logs, end;
     Layout(int batch, int positions, int heads, int64_t own_rows, int64_t prefix_rows)
@@ -873,7 +874,7 @@ struct Layout {
         own = after(lse, sizeof(float) * batch * positions * (size_t)heads);
         parts = after(own, own_rows > 0 ? sizeof(float) * HS_LATENT_DIM * batch * positions * (size_t)heads : 0);
         const int64_t units = ((int64_t)batch * positions * heads + 127) / 128;
-        starts = after(parts, sizeof(Sums) * (2 * kMaxPairs + (units <= kJoinUnits ? units : 0)));
+        starts = after(parts, sizeof(Sums) * (2 * kMaxPairs + (units < kJoinUnits ? units : kJoinUnits)));
         rows = after(starts, sizeof(Start) * kMaxPairs);
         scales = after(rows, 2 * HS_ROW_DIM * (size_t)prefix_rows);
         logs = after(scales, sizeof(float) * padded_rows(prefix_rows));

@@ -940,7 +940,8 @@ int hs_norm_rotate(const hs_rotate_t* args, hs_stream_t stream);
  * and form.  8-bit prefixes, and prefixes with lengths, are copied into the
  * workspace in 16 bits at every call (1152 bytes a row, and 8 for their scales);
  * partial results take 0.26 MB for each of up to 304 pieces and units, the own
- * rows' part 2 KB a query where there are own rows.
+ * rows' part 2 KB a query where there are own rows.  No size gives less when it
+ * grows: a workspace of the largest sizes serves all smaller ones.
  * Source: no passage (as hs_latent_attend).
  */
 typedef struct {

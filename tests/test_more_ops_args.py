@@ -207,3 +207,20 @@ def test_rotate_no_tokens_with_keys(hs):
     assert _rotate(hs, **nowhere) == hs.HS_OK
     assert _rotate(hs, heads=(16, 0), **nowhere) == hs.HS_OK
     assert _rotate(hs, heads=(16, -1), **nowhere) == hs.HS_ERR_ARG
+
+
+@pytest.mark.parametrize("positions,heads", [(1, 128), (1, 16), (3, 20), (2, 200)])
+@pytest.mark.parametrize("rows,prefix", [(0, 16384), (512, 16384), (5, 1), (2048, 3001)])
+def test_shared_workspace_of_more_requests_is_no_smaller(hs, positions, heads, rows, prefix):
+    """A workspace for the largest batch serves every smaller one; 152 and 304 units of 128 queries among them."""
+    sizes = [hs.hs_latent_attend_shared_workspace(b, positions, heads, rows, prefix) for b in range(1, 2600)]
+    assert sizes == sorted(sizes)
+
+
+def test_shared_workspace_grows_with_each_size(hs):
+    size = hs.hs_latent_attend_shared_workspace
+    for axis, values in enumerate(([1, 7, 152, 153, 256, 4096], [1, 2, 3, 64], [1, 16, 32, 33, 48, 128, 129, 512],
+                                   [0, 1, 64, 65, 512, 4096], [0, 1, 128, 129, 65536])):
+        for base in ((1, 1, 16, 0, 1000), (5, 3, 20, 300, 3001), (150, 1, 128, 512, 16384), (20, 1, 32, 2048, 100)):
+            got = [size(*base[:axis], v, *base[axis + 1:]) for v in values]
+            assert got == sorted(got), (axis, base, got)
