@@ -24,7 +24,8 @@ SOURCES = ["hs_api.cpp", "hs_resolve.cu", "hs_copy.cu", "hs_noalloc.cu",
            "hs_rows.cu", "hs_rotate.cu"]
 HEADERS = [os.path.join(CSRC, "hs_internal.h"), os.path.join(CSRC, "hs_gather_pool.h"),
            os.path.join(CSRC, "hs_ops.h"), os.path.join(CSRC, "hs_tc.h"),
-           os.path.join(CSRC, "hs_attend.h"), os.path.join(CSRC, "hs_pieces.h"), os.path.join(CSRC, "hs_rotation.h"),
+           os.path.join(CSRC, "hs_attend.h"), os.path.join(CSRC, "hs_cut.h"),
+           os.path.join(CSRC, "hs_pieces.h"), os.path.join(CSRC, "hs_rotation.h"),
            os.path.join(INCLUDE, "hs.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -31,11 +31,6 @@ namespace hs_attn {
 namespace {
 
 constexpr int kThreads = 14 * 32;
-// Tiles' time that a unit's queries, first scores and output take.  Without it pieces of several short
-// units end last: contexts of 32768, 1, 20001 and 777 rows 43 -> 34 us, 24 ragged ones of up to 16,384
-// rows 56 -> 35, 90 requests x 2048 rows x 128 heads 91 -> 86 (4: 35, 38, 87; 12: 34, 35, 83, but 8-bit
-// rows of 24 ragged contexts 43 -> 45).
-constexpr int kUnitCost = 7;
 
 // Shared memory of a CTA.
 constexpr int kQTmem = 6;                        // of Q's 9 blocks of 64 channels, those in tensor memory; the others here:
@@ -771,8 +766,7 @@ cudaError_t launch_pair(const hs_attend_t& a, int sms, cudaStream_t s, bool afte
     g.wide = wide;
     g.head_blocks = (a.heads + 127) / 128;
     g.units = a.batch * a.positions * g.head_blocks;
-    // Pieces also write and join up to two partial results a pair: about 10 us, 10 tiles' time.
-    g.cut(sms / 2 < kMaxPairs ? (sms > 1 ? sms / 2 : 1) : kMaxPairs, a.slots ? a.entries : a.n_rows, 10, kUnitCost);
+    g.cut(sms / 2 < kMaxPairs ? (sms > 1 ? sms / 2 : 1) : kMaxPairs, a.slots ? a.entries : a.n_rows, kPairJoin, kPairUnitCost);
     const bool e4m3 = a.row_format == HS_ROWS_E4M3;
     if (a.dtype == HS_TYPE_BF16)
         return e4m3 ? launch<__nv_bfloat16, true>(g, s) : launch<__nv_bfloat16, false>(g, s);

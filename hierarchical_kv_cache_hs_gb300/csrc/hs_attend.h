@@ -1,9 +1,10 @@
-// What the kernels of hs_latent_attend and hs_latent_attend_shared share: how the work is
-// cut, which rows a tile holds, and how 8-bit rows become operands.
+// What the kernels of hs_latent_attend and hs_latent_attend_shared share: a worker's piece of
+// the work, which rows a tile holds, and how 8-bit rows become operands.
 #pragma once
 
 #include <type_traits>
 
+#include "hs_cut.h"
 #include "hs_ops.h"
 #include "hs_tc.h"
 
@@ -11,41 +12,6 @@ namespace hs_attn {
 
 using tc::wait;
 
-constexpr int kTile = 64;  // rows a tile
-
-// A unit is a request, a position and a block of heads; its rows come in tiles, one at
-// least.  The tiles of all units form one line, which the workers (an SM, or a pair of
-// SMs) cut into equal pieces (flat), or whole units go to each.  A unit's own time (its
-// queries, its sums' way out) counts as `cost` tiles before its first one, but for the
-// line's first unit: every piece has that once.  A cut inside it is a cut at the unit's
-// start, so a worker may get no piece; the one before a piece that starts inside a unit
-// always has one.
-struct Cut {
-    int flat;
-    int units;         // at most HS_MAX_BATCH x HS_MAX_POSITIONS x HS_MAX_HEADS / 128, below 2^31
-    int unit_tiles;    // tiles of a unit; with lengths, the most that one has
-    int workers;
-    int cost;
-    int64_t share;     // slots: tiles (and cost) a worker, and how many workers have one more
-    int extra;
-    int unit_share, unit_extra;  // units a worker, likewise
-
-    // Fill in the cut: whole units, or pieces where those are `join` tiles' time shorter.
-    void cut(int most, int64_t rows, int join, int unit_cost, int tile = kTile)
-    {
-        cost = unit_cost;
-        unit_tiles = rows <= tile ? 1 : (int)((rows + tile - 1) / tile);
-        const int64_t total = (int64_t)units * unit_tiles;
-        workers = (int)(total < most ? total : most);
-        flat = (int64_t)((units + workers - 1) / workers) * unit_tiles > (total + workers - 1) / workers + join;
-        if (!flat && workers > units) workers = units;
-        const int64_t line = (int64_t)units * (unit_tiles + cost) - cost;
-        share = line / workers;
-        extra = (int)(line % workers);
-        unit_share = units / workers;
-        unit_extra = units % workers;
-    }
-};
 struct Args : Cut {
     hs_attend_t a;
     int head_blocks;
@@ -326,13 +292,7 @@ __device__ __forceinline__ bool find_cut(const Start* start, int workers, int x,
     return true;
 }
 
-constexpr int kMaxPairs = 76;  // pairs of SMs
-
-// The kernels: a pair of SMs for up to 128 heads; and one SM for up to 32 heads and 8-bit
-// rows, whose conversion, done twice by a pair, bounds them there (256 requests x 2048
-// rows: 102 against 204 us with 16 heads, 128 against 206 with 32; a form for 48 heads took
-// 262 where the pair takes 209, one for 16-bit rows 154 where it takes 140 with 16).
-constexpr int kNarrowHeads = 32;
+// The kernels, for a pair of SMs and for one.
 cudaError_t launch_pair(const hs_attend_t& a, int sms, cudaStream_t s, bool after, float* wide);  // sms: that it may take
 cudaError_t launch_narrow(const hs_attend_t& a, int sms, cudaStream_t s, bool after, float* wide);
 size_t pair_workspace(int64_t units, int64_t tiles);

@@ -19,10 +19,6 @@ namespace hs_attn {
 namespace {
 
 constexpr int kThreads = 14 * 32;
-// Tiles' time that a unit's queries, first scores and output take: 24 ragged contexts of up to 16,384
-// rows 47 -> 35 us, 200 requests x 1000 rows x 32 heads 76 -> 72, 256 x 2048 x 16 102 (7: 34, 73, 105).
-constexpr int kUnitCost = 3;
-constexpr int kMaxCtas = 152;
 constexpr int kStageBytes = 9 * 64 * 128;  // 9 blocks of 64 channels, [64 rows][128 B]
 constexpr int kBlock = 64 * 128;
 
@@ -563,8 +559,7 @@ cudaError_t launch_narrow(const hs_attend_t& a, int sms, cudaStream_t s, bool af
     g.wide = wide;
     g.head_blocks = 1;
     g.units = a.batch * a.positions;
-    // Pieces also write and join up to two partial results an SM: about 8 us, 6 tiles' time.
-    g.cut(sms < kMaxCtas ? sms : kMaxCtas, a.slots ? a.entries : a.n_rows, 6, kUnitCost);
+    g.cut(sms < kMaxCtas ? sms : kMaxCtas, a.slots ? a.entries : a.n_rows, kNarrowJoin, kNarrowUnitCost);
     if (a.dtype == HS_TYPE_BF16) return a.heads <= 16 ? launch<__nv_bfloat16, 16>(g, s) : launch<__nv_bfloat16, 32>(g, s);
     return a.heads <= 16 ? launch<__half, 16>(g, s) : launch<__half, 32>(g, s);
 }

@@ -43,9 +43,6 @@ namespace {
 
 constexpr int kThreads = 7 * 32;
 constexpr int kRows = 128;  // rows a tile
-// Tiles' time that a unit's queries and output take: with the own rows' part first, 2 instead of 4 cost 3 us (16 requests
-// x 3 x 32 heads, 4096 rows: 42 against 39.5; 64 x 32 heads, 16,384 rows: 70 against 68), 7 changed nothing.
-constexpr int kUnitCost = 4;
 
 constexpr int kQTmem = 6;
 constexpr int kBlock = 64 * 128;                   // bytes of 64 rows x 64 channels
@@ -925,36 +922,6 @@ cudaError_t widen_prefix(SharedArgs& g, const hs_prefix_t& p, uint8_t* ws, const
     return cudaGetLastError();
 }
 
-// Pairs of SMs for the own rows' part: all, so that the prefix's kernel follows it, or some, beside which that runs.  By
-// an estimate in ns, fitted to both kernels' times over 1 to 128 heads, 1 to 16 tiles a unit and 6 to 60 pairs; 5 % less
-// are asked for.  (64 requests x 16 heads, 16,384 shared rows, 1 to 512 own: 50.9 us one after the other, 44.7 with 26
-// pairs, 54.9 with 18, 56.6 with 44; 128 x 8 heads, 1000 shared rows, 64 own: 31.4, and 25.5 with 52; but 64 x 128 heads,
-// 16,384 shared 8-bit rows, 256 own: 206.3, and 207.3 with 6, 242 with 18; 64 x 16 heads, 2048 shared rows, 1 to 512 own:
-// 31.9, and 33.4 with the 32 that the estimate takes.)  Contexts of more than 512 rows may be far shorter than that, so
-// they are taken one after the other.
-int pairs_beside(const hs_attend_t& a, bool ragged, int units, int tiles, int all)
-{
-    const int64_t rows = a.slots ? a.entries : a.n_rows, own_tiles = rows <= kTile ? 1 : (rows + kTile - 1) / kTile;
-    if (!a.slots && own_tiles > 8) return all;
-    const bool e4m3 = a.row_format == HS_ROWS_E4M3, narrow = e4m3 && a.heads <= kNarrowHeads;  // narrow: an SM a unit
-    const int heads = a.heads < 128 ? a.heads : 128;
-    const int64_t own_units = (int64_t)a.batch * a.positions * ((a.heads + 127) / 128);
-    const int64_t own_unit = narrow ? 1200 + 200 * heads + 1350 * own_tiles : 4200 + 30 * heads + (e4m3 ? 1700 : 1050) * own_tiles;
-    const int64_t unit = (ragged ? (3 * (int64_t)tiles + 3) / 4 : tiles) + kUnitCost;
-    auto own = [&](int64_t n) { return 7000 + (own_units + (narrow ? 2 : 1) * n - 1) / ((narrow ? 2 : 1) * n) * own_unit; };
-    auto prefix = [&](int64_t n) {
-        const int64_t whole = (units + n - 1) / n * unit, pieces = (units * unit + n - 1) / n + 2;
-        return 13000 + (e4m3 ? 1600 : 1450) * (whole < pieces ? whole : pieces);
-    };
-    int best = all;
-    int64_t time = (own(all) + prefix(all) - 2000) * 95 / 100 * 17;
-    for (int n = 1; n < all; ++n) {
-        const int64_t x = own(n), y = prefix(all - n), t = 16 * (x > y ? x : y) + (x < y ? x : y);  // the longer of both counts
-        if (t < time) time = t, best = n;
-    }
-    return best;
-}
-
 }  // namespace
 }  // namespace hs_attn
 
@@ -1005,15 +972,15 @@ cudaError_t hs_launch_attend_shared(const hs_attend_t& a, const hs_prefix_t& p, 
         e = hs_launch_attend(own, s, widened, own_pairs, reinterpret_cast<float*>(ws + at.own));
         if (e != cudaSuccess) return e;
     }
-    g.cut(pairs, p.n_rows, 5, kUnitCost, kRows);
+    g.cut(pairs, p.n_rows, 5, kSharedUnitCost, kRows);
     if (g.flat) {
         // Each pair's partial results go out and come back, 1.2 us for ten pairs where a tile takes 1.4: few tiles take
         // fewer pairs.
-        auto time = [&](int64_t n) { return ((int64_t)g.units * (g.unit_tiles + kUnitCost) + n - 1) / n * 1400 + n * 120; };
+        auto time = [&](int64_t n) { return ((int64_t)g.units * (g.unit_tiles + kSharedUnitCost) + n - 1) / n * 1400 + n * 120; };
         int best = pairs;
         for (int n = pairs - 1; n > 0 && n > g.units; --n)
             if (time(n) < time(best)) best = n;
-        g.cut(best, p.n_rows, 5, kUnitCost, kRows);
+        g.cut(best, p.n_rows, 5, kSharedUnitCost, kRows);
     }
     if (p.lengths && !g.flat) {  // the device cuts the line
         const int64_t tiles = (int64_t)g.units * g.unit_tiles;

@@ -656,6 +656,50 @@ def test_shared_prefix_rows_that_are_not_finite(hs, value, e4m3):
     assert torch.equal(out[rest], want[rest]) and torch.equal(lse[rest], want_lse[rest])
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("size", [(1, 1, 16, 3001, 2048), (8, 1, 16, 2000, 2048), (5, 3, 20, 900, 1100), (1, 1, 128, 3001, 2048),
+                                  (8, 1, 128, 5000, 1500), (40, 1, 16, 4000, 1030), (3, 1, 200, 300, 4096)])
+def test_shared_long_lists(hs, size, e4m3):
+    """Own rows by lists of more than 16 tiles: the own rows' part in pieces before the prefix's kernel, or in whole
+    units beside it."""
+    B, P, H, M, K = size
+    g = _gen(sum(size))
+    N = K + 37
+    q, prefix, rows = _randn(g, B, P, H, 576), _form(_randn(g, M, 576), e4m3), _form(_randn(g, B, N, 576), e4m3)
+    slots = torch.rand((B, P, N), generator=g, device="cuda").topk(K, -1).indices.int()
+    slots = slots.masked_fill(torch.rand(slots.shape, generator=g, device="cuda") < 0.1, -1)
+    picked = [[s[s >= 0].long() for s in req] for req in slots]
+    out, lse = _shared(hs, q, prefix, rows, e4m3=e4m3, slots=slots)
+    _check_shared(out, lse, _shared_ref(q, prefix, [M] * B, rows, picked, e4m3, SCALE), BF)
+    seen = torch.randint(0, M + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+    out, lse = _shared(hs, q, prefix, rows, e4m3=e4m3, slots=slots, prefix_lengths=seen)
+    _check_shared(out, lse, _shared_ref(q, prefix, seen.tolist(), rows, picked, e4m3, SCALE), BF)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("B,H,M", [(1, 16, 3001), (6, 16, 700), (2, 128, 1000)])
+def test_shared_over_what_a_resolve_step_returned(hs, B, H, M, e4m3):
+    """The own rows lie in a handle's device buffer, at the slots that its resolve steps return."""
+    K, C, S = 1200, 3000, 1500
+    g = _gen(B + H)
+    q, prefix, rows = _randn(g, B, 1, H, 576), _form(_randn(g, M, 576), e4m3), _form(_randn(g, B, C, 576), e4m3)
+    form, raw = hs.HS_ROWS_E4M3 if e4m3 else hs.HS_ROWS_16BIT, rows.view(torch.uint8)
+    stream = torch.cuda.current_stream()
+    out, lse = torch.empty((B, 1, H, 512), dtype=BF, device="cuda"), torch.empty((B, 1, H), device="cuda")
+    ws = torch.empty(hs.hs_latent_attend_shared_workspace(B, 1, H, K, M, form), dtype=torch.uint8, device="cuda")
+    hs.hs_workspace_clear(ws)
+    with hs.Handle(B, C, raw.shape[-1], S, 2) as h:
+        h.host_pool()[:, :C] = raw.cpu().numpy()
+        for step in range(2):  # the second evicts
+            topk = torch.stack([torch.randperm(C, generator=g, device="cuda")[:K] for _ in range(B)]).int()
+            slots = torch.full((B, 1, K), -5, dtype=torch.int32, device="cuda")
+            h.resolve(topk, K, slots, stream)
+            hs.hs_latent_attend_shared(q, prefix, h, out, SCALE, slots=slots, lse=lse, workspace=ws, row_format=form, stream=stream)
+            picked = [[t.long()] for t in topk]
+            _check_shared(out, lse, _shared_ref(q, prefix, [M] * B, rows, picked, e4m3, SCALE), BF)
+        assert h.stats()["err_bits"] == 0 and hs.hs_workspace_error(ws) == 0
+
+
 @pytest.mark.parametrize("dtype", [BF, HALF])
 @pytest.mark.parametrize("channel", [100, 540])
 @pytest.mark.parametrize("size", [(6, 16), (3, 128)])
