@@ -389,7 +389,7 @@ template <typename T> cudaError_t launch(const hs_rotate_t& a, cudaStream_t s)
     // not with several units a lane for many (8192 x 36 of 96: 40.0 against 34.1; of 80 40.0 against 33.1).
     const int units = a.dim / (2 * H);
     int nv = 1, best = 1 << 30;
-    for (int n : {1, 2, 3, 4, 8})
+    for (int n : {1, 2, 3, 4, 8})  // 8 of 32-bit types: 1024 channels of 16 bits are 128 units, 4 a lane
         for (int team = 4; team <= 32; team *= 2)
             if (n * team >= units && n * team < best && (team > 4 || n == 1 || a.heads[0] + a.heads[1] <= kFew)) best = n * team, nv = n, g.team = team;
     const int ahead = nv == 1 ? 4 : nv == 2 ? 2 : 1, once = ahead * (32 / g.team);  // heads of a warp at once
@@ -425,7 +425,7 @@ template <typename T> cudaError_t launch(const hs_rotate_t& a, cudaStream_t s)
         hs_rotate_kernel<T, 3, 1><<<grid, kThreads, smem, s>>>(g);
     else if (nv == 4)
         hs_rotate_kernel<T, 4, 1><<<grid, kThreads, smem, s>>>(g);
-    else
+    else if constexpr (sizeof(T) == 4)
         hs_rotate_kernel<T, 8, 1><<<grid, kThreads, smem, s>>>(g);
     return cudaGetLastError();
 }

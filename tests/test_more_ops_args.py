@@ -1,6 +1,8 @@
 """Rows written and read back, heads' norm and rotation, and attention over a shared
 prefix without a GPU: what the library and the binding refuse, before any CUDA call."""
 import ctypes
+import shutil
+import subprocess
 
 import pytest
 
@@ -224,3 +226,11 @@ def test_shared_workspace_grows_with_each_size(hs):
         for base in ((1, 1, 16, 0, 1000), (5, 3, 20, 300, 3001), (150, 1, 128, 512, 16384), (20, 1, 32, 2048, 100)):
             got = [size(*base[:axis], v, *base[axis + 1:]) for v in values]
             assert got == sorted(got), (axis, base, got)
+
+
+@pytest.mark.skipif(shutil.which("nm") is None, reason="needs nm")
+def test_no_rotation_kernel_that_nothing_reaches(hs):
+    """Heads of 16-bit types have at most 1024 / 8 units, 4 a lane of 32; the form of 8 is fp32's."""
+    names = subprocess.run(["nm", "-C", hs.LIB_PATH], capture_output=True, text=True, check=True).stdout
+    wide = [line for line in names.splitlines() if "hs_rotate_kernel<" in line and ", 8, 1>" in line]
+    assert not [line for line in wide if "hs_rotate_kernel<float" not in line], wide
