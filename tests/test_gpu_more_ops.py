@@ -151,6 +151,30 @@ def test_rotate_strides_and_in_place(hs, dim, rope, at, pairs):
     assert torch.equal(hold[..., :8], before[..., :8]) and torch.equal(hold[..., 8 + dim:], before[..., 8 + dim:])
 
 
+@pytest.mark.parametrize("pairs", [True, False])
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("where", ["x", "out", "both"])
+@pytest.mark.parametrize("dtype", [BF, HALF, F32])
+@pytest.mark.parametrize("dim,rope,at,heads", [(128, 128, 0, 6), (192, 64, 128, 6), (192, 64, 128, 1), (62, 30, 3, 6), (1024, 512, 256, 2)])
+def test_rotate_odd_alignment(hs, dim, rope, at, heads, dtype, where, norm, pairs):
+    """Inputs, outputs or both an element off every border: heads that would go in units go element by element."""
+    g = _gen(dim + rope + heads)
+    n = 13
+    x = torch.full((n, heads, dim + 3), NAN, dtype=dtype, device="cuda")[..., 1:1 + dim] if where != "out" else \
+        torch.empty((n, heads, dim), dtype=dtype, device="cuda")
+    x.copy_(_randn(g, n, heads, dim, dtype=dtype))
+    hold = torch.full((n, heads, dim + 3), 5.0, dtype=dtype, device="cuda")
+    out = hold[..., 1:1 + dim] if where != "x" else torch.full((n, heads, dim), NAN, dtype=dtype, device="cuda")
+    w = _randn(g, dim, dtype=dtype) if norm else None
+    positions = torch.randint(0, 5000, (n,), generator=g, device="cuda", dtype=torch.int32)
+    freq = _freq(rope)
+    hs.hs_norm_rotate(x, out, q_weight=w, eps=EPS, positions=positions, inv_freq=freq, rope_at=at,
+                      rotation=hs.HS_ROTATE_PAIRS if pairs else hs.HS_ROTATE_HALVES)
+    _close(out, *_rotate_ref(x, w, positions, freq, at, pairs), dtype)
+    if where != "x":
+        assert (hold[..., 0] == 5).all() and (hold[..., 1 + dim:] == 5).all()
+
+
 @pytest.mark.parametrize("heads,keys", [(8, 2), (1, 1), (2, 1), (40, 4)])
 def test_rotate_packed_in_place(hs, heads, keys):
     """Queries, keys and values side by side in one array, as a projection leaves them; rotated where they lie."""
