@@ -348,7 +348,8 @@ int hs_create(int batch, int ctx_len, int row_bytes, int buffer_slots, int host_
         ok = alloc_pool(h, h->pool_bytes);
         if (ok) {
             void* dp = nullptr;
-            ok = cudaHostGetDevicePointer(&dp, h->h_pool, 0) == cudaSuccess;
+            // one address for both sides: what hs_host_pool returns is also given to kernels
+            ok = cudaHostGetDevicePointer(&dp, h->h_pool, 0) == cudaSuccess && dp == h->h_pool;
             h->d_pool = static_cast<uint8_t*>(dp);
         }
     }

@@ -252,6 +252,8 @@ int hs_resolve_ce(hs_handle* h, const int32_t* topk_idx, int K, int32_t* out_slo
 int hs_stats(hs_handle* h, hs_stats_t* out, int32_t* last_miss);
 
 /* Host pointer of the pinned, device-mapped host pool [B][H][R]; its size in bytes.
+ * It is the pool's device address, too, in either placement (hs_create fails where
+ * it would not be).
  * Source: HiSparse blog, "HiSparseの設計" (inactive KV entries are offloaded to
  * host memory); vLLM Hybrid HiSparse post, "Mixed Residency" (pinned host memory). */
 uint8_t* hs_host_pool(hs_handle* h);

@@ -451,6 +451,47 @@ def test_write_into_the_host_pool(hs):
         assert torch.equal(out, _wide(staged, True).float().to(BF))
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("pages", ["base", "huge"])
+def test_pool_in_either_placement(hs, pages, e4m3):
+    """Contexts written into a pool of ordinary or of huge pages, read back from it, and resolved into the buffer."""
+    if pages == "huge" and hs.hs_huge_page_bytes() == 0:
+        pytest.skip("the host offers no transparent huge pages")
+    B, S, C = 2, 128, 256
+    new, lengths = [200, 31], [250, 31]
+    g = _gen(32)
+    n, R = sum(new), 592 if e4m3 else 1152
+    form = hs.HS_ROWS_E4M3 if e4m3 else hs.HS_ROWS_16BIT
+    x, start, ends = _randn(g, n, 576), _ints([0, 200, 231]), _ints(lengths)
+    staged, stream = torch.zeros((n, R), dtype=torch.uint8, device="cuda"), torch.cuda.current_stream()
+    hs.hs_latent_write(x, staged, row_format=form)
+    mode = hs.HS_POOL_PAGES_HUGE if pages == "huge" else hs.HS_POOL_PAGES_BASE
+    hs.hs_set_host_pool_pages(mode)
+    try:
+        h = hs.Handle(B, C, R, S, 2)
+    finally:
+        hs.hs_set_host_pool_pages(hs.HS_POOL_PAGES_AUTO)
+    with h:
+        assert hs.hs_host_pool_pages(h.h) == mode
+        pool = h.host_pool()
+        pool[:] = 0xA5
+        hs.hs_latent_write(x, h, start=start, lengths=ends, row_format=form, stream=stream)
+        out = torch.full((n, 576), NAN, dtype=BF, device="cuda")
+        hs.hs_latent_read(h, out, start=start, lengths=ends, row_format=form, stream=stream)
+        torch.cuda.synchronize()
+        want = np.full_like(pool, 0xA5)
+        want[0, 50:250], want[1, :31] = staged[:200].cpu().numpy(), staged[200:].cpu().numpy()
+        assert (pool == want).all()
+        values = _wide(staged if e4m3 else staged.view(BF), e4m3).float().to(BF)
+        assert torch.equal(out, values)
+        topk = torch.stack([50 + torch.randperm(200, generator=g, device="cuda")[:20],
+                            torch.randperm(31, generator=g, device="cuda")[:20]]).int()
+        slots, picked = torch.empty((B, 20), dtype=torch.int32, device="cuda"), torch.empty((B, 20, 576), dtype=BF, device="cuda")
+        h.resolve(topk, 20, slots, stream)
+        hs.hs_latent_read(h, picked, slots=slots, row_format=form, dtype=BF, stream=stream)
+        assert torch.equal(picked[0], values[topk[0].long() - 50]) and torch.equal(picked[1], values[200 + topk[1].long()])
+
+
 # ---- read ------------------------------------------------------------------------------
 
 def _check_read(out, want):
