@@ -863,6 +863,7 @@ int hs_host_pool_pages(hs_handle* h)
 }
 
 size_t hs_huge_page_bytes(void) { return huge_page_bytes(); }
+int hs_device(hs_handle* h) { return valid(h) ? h->device : HS_ERR_ARG; }
 uint8_t* hs_device_buffer(hs_handle* h) { return valid(h) ? h->d_buf : nullptr; }
 size_t hs_device_buffer_bytes(hs_handle* h) { return valid(h) ? h->buf_bytes : 0; }
 

@@ -266,6 +266,7 @@ def _load():
         "hs_set_host_pool_pages": ([I], I),
         "hs_host_pool_pages": ([P], I),
         "hs_huge_page_bytes": ([], Z),
+        "hs_device": ([P], I),
         "hs_device_buffer": ([P], P),
         "hs_device_buffer_bytes": ([P], Z),
         "hs_set_lengths": ([P, P], I),
@@ -447,6 +448,14 @@ def hs_host_pool_pages(h: int) -> int:
 
 def hs_huge_page_bytes() -> int:
     return int(lib.hs_huge_page_bytes())
+
+
+def hs_device(h: int) -> int:
+    """The index of the CUDA device that holds a handle's buffers."""
+    r = lib.hs_device(h)
+    if r < 0:
+        raise HsError(r, "hs_device")
+    return r
 
 
 def hs_device_buffer(h: int) -> int:
@@ -704,6 +713,8 @@ def _rows_of(rows, row_format, dtype, device, lead):
     if isinstance(rows, Handle):
         if (rows.B,) != lead or rows.R < width:
             raise ValueError("the handle has %d requests of %d-byte rows" % (rows.B, rows.R))
+        if hs_device(rows.h) != device.index:
+            raise ValueError("the handle is on device %d, the tensors on %s" % (hs_device(rows.h), device))
         n = rows.S + rows.T
         return hs_device_buffer(rows.h), n, rows.R, n * rows.R
     shape = rows.shape
@@ -947,10 +958,12 @@ def _places_of(start, lengths, device, B):
             0 if lengths is None else _vector(lengths, "lengths", B, _INT32, device))
 
 
-def _pool_of(h, row_format):
+def _pool_of(h, row_format, device):
     """(address, rows a request, row stride, request stride) of a handle's host pool."""
     if h.R < _ROW_WIDTH.get(row_format, 1 << 30):
         raise ValueError("the handle has rows of %d bytes" % h.R)
+    if hs_device(h.h) != device.index:  # whose pool that device has mapped
+        raise ValueError("the handle is on device %d, the tensors on %s" % (hs_device(h.h), device))
     return hs_host_pool(h.h), h.H, h.R, h.H * h.R
 
 
@@ -986,7 +999,7 @@ def hs_latent_write(x, rows, weight=None, eps: float = 0.0, positions=None, inv_
         if isinstance(rows, Handle):
             if rows.B != batch:
                 raise ValueError("the handle has %d requests" % rows.B)
-            address, n_rows, row_stride, request_stride = _pool_of(rows, row_format)
+            address, n_rows, row_stride, request_stride = _pool_of(rows, row_format, device)
         else:
             address, n_rows, row_stride, request_stride = _rows_of(rows, row_format, dtype, device, (batch,))
     _on_current_device(device)
@@ -1043,7 +1056,7 @@ def hs_latent_read(rows, out, slots=None, start=None, lengths=None, row_format: 
     if isinstance(rows, Handle) and start is not None:
         if rows.B != B:
             raise ValueError("the handle has %d requests" % rows.B)
-        address, n_rows, row_stride, request_stride = _pool_of(rows, row_format)
+        address, n_rows, row_stride, request_stride = _pool_of(rows, row_format, device)
     else:
         address, n_rows, row_stride, request_stride = _rows_of(rows, row_format, dtype, device, (B,))
     _on_current_device(device)

@@ -297,6 +297,10 @@ int hs_set_host_pool_pages(int mode);
 int hs_host_pool_pages(hs_handle* h);
 size_t hs_huge_page_bytes(void);
 
+/* The CUDA device that was current when the handle was created, on which its buffers lie.
+ * Source: no passage (the pages name one GPU). */
+int hs_device(hs_handle* h);
+
 /* Device pointer of the buffer [B][S+T][R] that out_slot indexes; its size in bytes.
  * Source: HiSparse blog, "HiSparseの設計" (the hot device buffer in HBM);
  * vLLM Hybrid HiSparse post, "Mixed Residency" (the tail stays on the GPU). */

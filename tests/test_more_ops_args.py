@@ -234,3 +234,19 @@ def test_no_rotation_kernel_that_nothing_reaches(hs):
     names = subprocess.run(["nm", "-C", hs.LIB_PATH], capture_output=True, text=True, check=True).stdout
     wide = [line for line in names.splitlines() if "hs_rotate_kernel<" in line and ", 8, 1>" in line]
     assert not [line for line in wide if "hs_rotate_kernel<float" not in line], wide
+
+
+def test_handles_of_another_device_are_refused(hs, monkeypatch):
+    """A handle's buffer and pool belong to the device it was created on; the tensors' may be another."""
+    h = object.__new__(hs.Handle)  # of 2 requests, never created
+    h.B, h.R, h.S, h.T, h.H, h.h = 2, 1152, 8, 0, 16, None
+    here, there = torch.device("cuda", 0), torch.device("cuda", 1)
+    monkeypatch.setattr(hs, "hs_device", lambda handle: 1)
+    monkeypatch.setattr(hs, "hs_device_buffer", lambda handle: 1 << 20)
+    monkeypatch.setattr(hs, "hs_host_pool", lambda handle: 1 << 21)
+    for refused in (lambda: hs._rows_of(h, hs.HS_ROWS_16BIT, torch.bfloat16, here, (2,)), lambda: hs._pool_of(h, hs.HS_ROWS_16BIT, here)):
+        with pytest.raises(ValueError, match="on device 1"):
+            refused()
+    assert hs._rows_of(h, hs.HS_ROWS_16BIT, torch.bfloat16, there, (2,)) == (1 << 20, 8, 1152, 8 * 1152)
+    assert hs._pool_of(h, hs.HS_ROWS_16BIT, there) == (1 << 21, 16, 1152, 16 * 1152)
+    assert hs.lib.hs_device(None) == hs.HS_ERR_ARG
