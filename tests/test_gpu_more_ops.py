@@ -14,7 +14,8 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
-from test_gpu_ops import BF, HALF, NAN, SCALE, _gen, _pack8, _randn, _softmax_ref, _wide  # noqa: E402
+from test_gpu_ops import (BF, HALF, NAN, SCALE, _check_prefill, _gen, _pack8, _prefill, _prompt_case, _randn,  # noqa: E402
+                          _softmax_ref, _wide)
 
 F32 = torch.float32
 EPS = 1e-6
@@ -572,6 +573,25 @@ def test_read_special_values(hs):
     hs.hs_latent_read(rows, out, slots=_ints([[0, 1, 2, 3]]), row_format=hs.HS_ROWS_E4M3, dtype=BF)
     assert torch.isfinite(out[0, [0, 3]]).all() and out[0, 1].isnan().sum() == 1
     assert (~torch.isfinite(out[0, 2])).all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("nq,nk", [([30, 1, 200], [300, 500, 200]), ([5, 0, 129], [5, 0, 700])])
+def test_read_contexts_for_a_prompt(hs, nq, nk, e4m3):
+    """A prompt's next chunk: the cached rows of its contexts are read back, the chunk's own among them, and the
+    prompt's attention takes them as its rows."""
+    g = _gen(sum(nq))
+    q, rows, w_uk, w_uv = _prompt_case(nq, nk, 2, BF, False, sum(nk))
+    N, start = 720, _ints(np.concatenate([[0], np.cumsum(nk)]).tolist())
+    form = hs.HS_ROWS_E4M3 if e4m3 else hs.HS_ROWS_16BIT
+    cache = torch.full((len(nk), N, 592 if e4m3 else 1152), 0xFF, dtype=torch.uint8, device="cuda")  # NaN
+    positions, freq, w = torch.randint(0, 9999, (sum(nk),), generator=g, device="cuda", dtype=torch.int32), _freq(64), _randn(g, 512)
+    hs.hs_latent_write(rows, cache, weight=w, eps=EPS, positions=positions, inv_freq=freq, start=start, lengths=_ints(nk), row_format=form)
+    back = torch.full((sum(nk), 576), NAN, dtype=BF, device="cuda")
+    hs.hs_latent_read(cache, back, start=start, lengths=_ints(nk), row_format=form)
+    held = torch.cat([cache[b, :m] for b, m in enumerate(nk)])
+    assert torch.equal(back, _wide(held if e4m3 else held.view(BF), e4m3).float().to(BF))
+    _check_prefill(*_prefill(hs, q, back, w_uk, w_uv, nq, nk), q, back, w_uk, w_uv, nq, nk, False)
 
 
 def test_read_handle_slots(hs):
