@@ -4,8 +4,10 @@
 //   y = x w / sqrt(mean x^2 + eps);  a pair (a, b) of y becomes (a cos - b sin, a sin + b cos)
 //
 // Each element is read once and written once, so the floor is memory's: 8192 tokens x (32 + 8) heads of 128 bf16
-// channels take 35.4 us, 4.7 TB/s, 0.70 of a copy's rate; the issue slots are 64 % taken (80 registers, 24 warps an SM),
-// and what a warp does between its loads is not hidden whole.  64 x 128 heads: 3.3 us; one token: 3.2, a launch.
+// channels take 35.3 us, 4.8 TB/s, 0.70 of a copy's rate; the issue slots are 64 % taken (80 registers, 24 warps an SM),
+// and what a warp does between its loads is not hidden whole.  The last 64 channels of 8192 x 32 queries of 192, in
+// place: 16.6 us, 0.60.  64 x 128 heads: 3.3 us; one token: 3.2, a launch.  (Replayed from a graph, inputs larger than
+// L2.  Times at choices further on are of the step that took them.)
 // A ring of bulk copies through shared memory instead of loads to registers took 49 us for the 36, and values kept
 // unpacked between the norm and the rotation 39 to 43: registers.
 //

@@ -8,10 +8,13 @@
 //
 // Each input is read once and each output written once (1156 + 592 bytes a token written as an 8-bit row), so the
 // floor is memory's.  Inputs larger than L2, on one GB300:
-//   writing 65,536 rows of 8 bits   24.3 us, 4.7 TB/s, 0.69 of a copy's rate: some 250 instructions a row, which
-//                                   take 63 % of the issue slots, and what a warp does between its loads
+//   writing 65,536 rows of 8 bits   23.6 us, 4.8 TB/s, 0.71 of a copy's rate: some 275 instructions a row, which
+//                                   take 67 % of the issue slots, and what a warp does between its loads
 //   reading 64 x 2048 8-bit rows by slots   37.0 us, 6.2 TB/s, 0.91 of a copy's rate: memory
-//   64 rows written, 3 x 77 read    2.2 and 2.7 us: a launch and the latency of two loads in a row
+//   64 rows written, 3 x 77 read    2.4 and 2.8 us: a launch and the latency of two loads in a row
+//   65,536 rows into a handle's host pool   395 us of 16 bits, 191 GB/s (a copy to the host 193); 262 of 8 bits, 148
+//   65,536 rows read from it        364 us of 16 bits, 208 GB/s (a copy from the host 210); 204 of 8 bits, 186
+// (Times at choices further on are of the step that took them.)
 #include "hs_pieces.h"
 #include "hs_rotation.h"
 #include "hs_tc.h"
