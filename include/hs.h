@@ -628,12 +628,12 @@ int hs_resolve_noalloc(int batch, int ctx_len, int row_bytes, int buffer_slots, 
 #define HS_ROW8_BYTES  592
 #define HS_TYPE_BF16   0
 #define HS_TYPE_FP16   1
-#define HS_TYPE_FP32   2    /* hs_rms_norm only */
+#define HS_TYPE_FP32   2    /* hs_rms_norm, hs_norm_rotate, and what hs_latent_read writes */
 #define HS_ROWS_16BIT  0
 #define HS_ROWS_E4M3   1
 #define HS_MAX_HEADS   1024
 #define HS_MAX_POSITIONS 1024
-#define HS_MAX_TOKENS  (1 << 24)  /* tokens of one hs_latent_prefill or hs_rms_norm call */
+#define HS_MAX_TOKENS  (1 << 24)  /* tokens of one call (hs_latent_attend, ..._shared: HS_MAX_BATCH x HS_MAX_POSITIONS) */
 #define HS_MAX_NORM_DIM 16384     /* channels of one normed row, the carried ones included */
 
 /*
@@ -816,10 +816,10 @@ int hs_rms_norm(const hs_norm_t* args, hs_stream_t stream);
  *               request b.  Not written: tokens of no request, and rows outside
  *               [0, n_rows).  (start is clamped to [0, tokens].)
  * So no two tokens go to one row; with batch > 1, the strides have to keep all
- * rows apart (requests behind one another, or row by row in turn).  `rows` is device memory, or pinned host memory mapped
- * into the device address space (a handle's hs_host_pool: n_rows = H, row_stride
- * = R, request_stride = H * R; a prompt's rows then cross the host link once, as
- * they are written).
+ * rows apart (requests behind one another, or row by row in turn).  `rows` is
+ * device memory, or pinned host memory mapped into the device address space (a
+ * handle's hs_host_pool: n_rows = H, row_stride = R, request_stride = H * R; a
+ * prompt's rows then cross the host link once, as they are written).
  *   x       [tokens][576] of `dtype` (bf16 or fp16, also the type of 16-bit
  *           rows), channels contiguous, x_stride elements between tokens, a
  *           multiple of 8; x, rows and weight 16-byte aligned, row_stride and
@@ -898,8 +898,9 @@ int hs_latent_read(const hs_read_t* args, hs_stream_t stream);
  *           two must not overlap.  Any alignment of the element; 16-byte aligned
  *           rows (and rope_at, and half of rope for HS_ROTATE_HALVES) go faster.
  *   weight  [dim] of `dtype`
- * x[1] NULL, heads[1] 0: one array (with no tokens, x is not looked at).  Queries'
- * and keys' arrays do not overlap one another.  rope: even, 0 without a rotation.
+ * x[1] NULL, heads[1] 0: one array (with no tokens, x is not looked at).  Neither
+ * array's outputs may lie on the other's inputs or outputs.  rope: even, 0 without a
+ * rotation.
  * Source: no passage (the producer of the queries that hs_latent_prefill and
  * hs_latent_attend take).
  */

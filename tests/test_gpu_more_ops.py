@@ -1045,6 +1045,20 @@ assert all(torch.equal(a, b) for a, b in zip(found, (rows, back, turned, out)))
 """
 
 
+def test_no_tokens(hs):
+    """Calls of no tokens change nothing, keys or not."""
+    x, q, k = (torch.zeros(s, dtype=BF, device="cuda") for s in ((0, 576), (0, 16, 192), (0, 2, 192)))
+    rows, out = torch.full((2, 3, 576), 7.0, dtype=BF, device="cuda"), torch.full((5, 576), 7.0, dtype=BF, device="cuda")
+    start, lengths, none, freq, w = _ints([0, 0, 0]), _ints([1, 3]), _ints([]), _freq(64), torch.ones(192, dtype=BF, device="cuda")
+    hs.hs_latent_write(x, rows, positions=none, inv_freq=freq, start=start, lengths=lengths)
+    hs.hs_latent_write(x, rows[0], positions=none, inv_freq=freq)
+    hs.hs_latent_read(rows, out[:0], start=start, lengths=lengths)
+    hs.hs_latent_read(rows, out, start=start)
+    hs.hs_norm_rotate(q, q, positions=none, inv_freq=freq)
+    hs.hs_norm_rotate(q, q, k=k, k_out=k, q_weight=w, k_weight=w, eps=EPS, positions=none, inv_freq=freq)
+    assert (rows == 7).all() and (out == 7).all()
+
+
 def test_first_calls_in_a_graph():
     """A program whose first calls are captured."""
     import os
